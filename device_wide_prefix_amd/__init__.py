@@ -14,6 +14,9 @@ fallback; if the library is not built, importing the binding's functions raises.
     scan_debug(x, out, tile_elems, ...)    -> descriptor words (numpy uint64)
     watchdog_trips()                       -> int
     selftest_wave(x)                       -> (incl, shift)
+    delta_rule(q, k, v, g, beta, ...)      -> out or (out, final_state)
+    delta_rule_backward(d_out, q, ...)     -> (dq, dk, dv, dg, dbeta, d_initial_state)
+    delta_rule_step(q, k, v, g, beta, state, slots=None, ...) -> out (state updated)
 The C entry points take raw device pointers; the *_ptr functions expose them.
 """
 from __future__ import annotations
@@ -27,7 +30,7 @@ LIB_PATH = os.path.join(PKG_DIR, "libdws_scan.so")
 # dws_status
 OK, ERR_INVALID_ARG, ERR_UNSUPPORTED, ERR_OVERLAP, ERR_HIP, ERR_OOM, ERR_MISALIGNED = range(7)
 # dws_dtype
-INT32, UINT32, FLOAT32, PAIR_I32_F32, PAIR_U32 = 0, 1, 2, 3, 4
+INT32, UINT32, FLOAT32, PAIR_I32_F32, PAIR_U32, FLOAT16, BFLOAT16 = 0, 1, 2, 3, 4, 5, 6
 # dws_op
 OP_SUM, OP_MAX, OP_MIN, OP_AFFINE, OP_SEGMENTED_SUM = 0, 1, 2, 3, 4
 # dws_variant
@@ -48,6 +51,7 @@ EXPORTED_SYMBOLS = (
     "dws_scan_profiled", "dws_select_flagged", "dws_scan_op", "dws_partition_flagged", "dws_reduce_by_key",
     "dws_run_length_encode", "dws_device_memory_info", "dws_scan_noalloc", "dws_scan_plan", "dws_scan_seeded",
     "dws_reduce", "dws_scan_op_seeded", "dws_reduce_op", "dws_select_if", "dws_partition_if",
+    "dws_delta_rule_workspace", "dws_delta_rule", "dws_delta_rule_backward", "dws_delta_rule_step",
 )
 
 
@@ -67,6 +71,23 @@ class LaunchPlan(ctypes.Structure):
     """dws_launch_plan: what a single-pass or chained call would launch."""
     _fields_ = [("threads", ctypes.c_uint), ("tile_elems", ctypes.c_uint), ("num_tiles", ctypes.c_uint),
                 ("tile_index", ctypes.c_int), ("nontemporal", ctypes.c_int), ("pause_units", ctypes.c_int)]
+
+
+class Rows(ctypes.Structure):
+    """dws_rows: a (tokens, heads, dim) array."""
+    _fields_ = [("data", ctypes.c_void_p), ("token_stride", ctypes.c_longlong), ("head_stride", ctypes.c_longlong)]
+
+
+class DeltaRuleArgs(ctypes.Structure):
+    """dws_delta_rule_args."""
+    _fields_ = ([(x, ctypes.c_longlong) for x in ("tokens", "n_seqs")] + [("d_offsets", ctypes.c_void_p)] +
+                [(x, ctypes.c_int) for x in ("heads_qk", "heads_v", "dim_k", "dim_v", "dtype", "g_dtype", "beta_dtype")] +
+                [("scale", ctypes.c_float)] + [(x, Rows) for x in ("q", "k", "v", "g", "beta", "out")] +
+                [(x, ctypes.c_void_p) for x in ("d_initial_state", "d_final_state", "d_slots")] +
+                [("n_states", ctypes.c_longlong), ("out_grad", Rows), ("d_final_grad", ctypes.c_void_p)] +
+                [(x, Rows) for x in ("q_grad", "k_grad", "v_grad", "g_grad", "beta_grad")] +
+                [("d_initial_grad", ctypes.c_void_p), ("zero_tail", ctypes.c_int), ("d_workspace", ctypes.c_void_p),
+                 ("workspace_bytes", ctypes.c_size_t)])
 
 
 _lib = None
@@ -140,6 +161,12 @@ def load_library():
     lib.dws_run_length_encode.restype = ci
     lib.dws_select_flagged.argtypes = [vp, vp, vp, sz, ci, vp, vp]
     lib.dws_select_flagged.restype = ci
+    lib.dws_delta_rule_workspace.argtypes = [ctypes.POINTER(DeltaRuleArgs), ci, ctypes.POINTER(sz)]
+    lib.dws_delta_rule_workspace.restype = ci
+    for name in ("dws_delta_rule", "dws_delta_rule_backward", "dws_delta_rule_step"):
+        f = getattr(lib, name)
+        f.argtypes = [ctypes.POINTER(DeltaRuleArgs), vp]
+        f.restype = ci
     lib.dws_selftest_wave.argtypes = [vp, vp, vp, sz, ci, vp]
     lib.dws_selftest_wave.restype = ci
     _lib = lib
@@ -534,6 +561,212 @@ def run_length_encode(keys, unique_keys=None, lengths=None, count=None, stream=N
                                                     keys.numel(), count.data_ptr(), _stream(keys, stream)),
                "dws_run_length_encode")
     return unique_keys, lengths, count
+
+
+# ---- the gated delta rule ---------------------------------------------------
+
+def _float_code(t, what) -> int:
+    import torch
+    codes = {torch.float32: FLOAT32, torch.float16: FLOAT16, torch.bfloat16: BFLOAT16}
+    if t.dtype not in codes:
+        raise TypeError(f"{what} must be float32, float16 or bfloat16, got {t.dtype}")
+    return codes[t.dtype]
+
+
+def _rows(t, what, tokens, heads, dim, like=None, device=None) -> Rows:
+    """The dws_rows of t, (tokens, heads, dim) or, for dim 0, (tokens, heads)."""
+    import torch
+    shape = (tokens, heads, dim) if dim else (tokens, heads)
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{what} must be a GPU tensor (there is no CPU path)")
+    if tuple(t.shape) != shape or t.device != device or (like is not None and t.dtype != like):
+        raise ValueError(f"{what} must have shape {shape}" + (f", dtype {like}" if like is not None else "") +
+                         f" and be on {device}, got {tuple(t.shape)}, {t.dtype} on {t.device}")
+    if dim > 1 and t.stride(2) != 1 and t.numel():
+        raise ValueError(f"{what} must be contiguous in its last dimension")
+    return Rows(t.data_ptr(), t.stride(0), t.stride(1))
+
+
+def _device_ints(t, what, dtype, n, device):
+    import torch
+    if not isinstance(t, torch.Tensor) or t.dtype != dtype or t.device != device or not t.is_contiguous() or \
+            (n is not None and t.numel() != n) or t.dim() != 1:
+        raise ValueError(f"{what} must be a contiguous one-dimensional {dtype} tensor on {device}" +
+                         (f" of {n} elements" if n is not None else ""))
+    return t.data_ptr()
+
+
+def _state_ptr(t, what, count, heads, dim_k, dim_v, device):
+    import torch
+    if not isinstance(t, torch.Tensor) or t.dtype != torch.float32 or t.device != device or not t.is_contiguous() or \
+            t.dim() != 4 or tuple(t.shape[1:]) != (heads, dim_k, dim_v) or (count is not None and t.shape[0] != count):
+        raise ValueError(f"{what} must be a contiguous float32 tensor ({'count' if count is None else count}, {heads}, "
+                         f"{dim_k}, {dim_v}) on {device}")
+    return t.data_ptr()
+
+
+def _delta_args(q, k, v, g, beta, offsets, n_seqs, scale):
+    """The members that all three delta-rule calls share; checks shapes, types and devices."""
+    import torch
+    for x, what in ((q, "q"), (k, "k"), (v, "v"), (beta, "beta")):
+        if not isinstance(x, torch.Tensor) or not x.is_cuda:
+            raise TypeError(f"{what} must be a GPU tensor (there is no CPU path)")
+    if q.dim() != 3 or v.dim() != 3:
+        raise ValueError("q, k and v must be (tokens, heads, dim)")
+    a = DeltaRuleArgs()
+    a.tokens, a.heads_qk, a.dim_k = q.shape
+    a.heads_v, a.dim_v = v.shape[1:]
+    a.dtype = _float_code(q, "q")
+    a.q = _rows(q, "q", a.tokens, a.heads_qk, a.dim_k, q.dtype, q.device)
+    a.k = _rows(k, "k", a.tokens, a.heads_qk, a.dim_k, q.dtype, q.device)
+    a.v = _rows(v, "v", a.tokens, a.heads_v, a.dim_v, q.dtype, q.device)
+    if g is not None:
+        a.g = _rows(g, "g", a.tokens, a.heads_v, 0, None, q.device)
+        a.g_dtype = _float_code(g, "g")
+    a.beta = _rows(beta, "beta", a.tokens, a.heads_v, 0, None, q.device)
+    a.beta_dtype = _float_code(beta, "beta")
+    if offsets is not None:
+        a.d_offsets = _device_ints(offsets, "offsets", torch.int64, None, q.device)
+        n_seqs = offsets.numel() - 1
+    a.n_seqs = n_seqs
+    a.scale = a.dim_k ** -0.5 if scale is None else float(scale)
+    return a
+
+
+class _on_stream:
+    """Allocate on the stream that the call runs on: memory that is freed when
+    the binding returns is then reused in that stream's order only."""
+
+    def __init__(self, x, stream):
+        import torch
+        self.device = torch.cuda.device(x.device)
+        current = torch.cuda.current_stream(x.device)
+        self.stream = int(current.cuda_stream) if stream is None else int(stream)
+        other = None
+        if self.stream != int(current.cuda_stream):
+            other = torch.cuda.default_stream(x.device) if self.stream == 0 else \
+                torch.cuda.ExternalStream(self.stream, device=x.device)
+        self.other = torch.cuda.stream(other)
+
+    def __enter__(self):
+        self.device.__enter__()
+        self.other.__enter__()
+        return self.stream
+
+    def __exit__(self, *exc):
+        self.other.__exit__(*exc)
+        self.device.__exit__(*exc)
+        return False
+
+
+def _delta_workspace(a, backward, device):
+    import torch
+    need = ctypes.c_size_t(0)
+    _check(load_library().dws_delta_rule_workspace(ctypes.byref(a), int(backward), ctypes.byref(need)),
+           "dws_delta_rule_workspace")
+    work = torch.empty(need.value, dtype=torch.uint8, device=device)
+    a.d_workspace, a.workspace_bytes = work.data_ptr(), need.value
+    return work
+
+
+def delta_rule(q, k, v, g, beta, offsets=None, initial_state=None, final_state=None, slots=None, scale=None, out=None,
+               stream=None):
+    """The gated delta rule over whole sequences (dws_delta_rule).
+
+    q, k: (tokens, heads_qk, dim_k); v: (tokens, heads_v, dim_v), all float32, float16 or bfloat16, any strides with a
+    contiguous last dimension. g (log decays, or None) and beta: (tokens, heads_v), each any of the three types.
+    offsets: int64 GPU tensor of n + 1 ascending row numbers (None: one sequence). initial_state: float32
+    (n, heads_v, dim_k, dim_v) or None for zero. final_state: None, a tensor like it to write (may be initial_state),
+    or True for a new one. slots: int32 GPU tensor of n places when the states are a pool (count, heads_v, dim_k,
+    dim_v); sequences with a place below 0, outside the pool or named before are left out. scale: dim_k^-0.5 by
+    default. Rows of ``out`` behind the last sequence stay as they were, and are 0 in a new one.
+    Returns out, or (out, final_state) when the final state is asked for."""
+    import torch
+    a = _delta_args(q, k, v, g, beta, offsets, 1, scale)
+    count = a.n_seqs
+    if slots is not None:
+        a.d_slots = _device_ints(slots, "slots", torch.int32, a.n_seqs, q.device)
+        count = None
+        if final_state is True or (initial_state is None and final_state is None):
+            raise ValueError("slots name places of a given state tensor")
+    with _on_stream(q, stream) as s:
+        if out is None:
+            # a sequence that is left out keeps its rows: 0 in a new tensor
+            out = torch.empty(v.shape, dtype=q.dtype, device=q.device) if slots is None else \
+                torch.zeros(v.shape, dtype=q.dtype, device=q.device)
+            a.zero_tail = int(offsets is not None)
+        a.out = _rows(out, "out", a.tokens, a.heads_v, a.dim_v, q.dtype, q.device)
+        if final_state is True:
+            final_state = torch.empty((a.n_seqs, a.heads_v, a.dim_k, a.dim_v), dtype=torch.float32, device=q.device)
+        for t, what in ((initial_state, "initial_state"), (final_state, "final_state")):
+            if t is not None:
+                setattr(a, "d_" + what, _state_ptr(t, what, count, a.heads_v, a.dim_k, a.dim_v, q.device))
+                if slots is not None:
+                    if count is not None and t.shape[0] != count:
+                        raise ValueError("initial_state and final_state must have the same number of states")
+                    count = a.n_states = t.shape[0]
+        work = _delta_workspace(a, False, q.device)
+        _check(load_library().dws_delta_rule(ctypes.byref(a), s), "dws_delta_rule")
+        del work
+    return out if final_state is None else (out, final_state)
+
+
+def delta_rule_backward(d_out, q, k, v, g, beta, offsets=None, initial_state=None, d_final_state=None, scale=None,
+                        stream=None):
+    """Gradients of delta_rule (dws_delta_rule_backward): the arguments of the forward call and the gradient(s) of its
+    result(s). Returns (dq, dk, dv, dg, dbeta, d_initial_state) in the type of q, dg None without g and
+    d_initial_state None without initial_state; rows behind the last sequence are 0."""
+    import torch
+    a = _delta_args(q, k, v, g, beta, offsets, 1, scale)
+    a.out_grad = _rows(d_out, "d_out", a.tokens, a.heads_v, a.dim_v, q.dtype, q.device)
+    for t, what, name in ((initial_state, "initial_state", "d_initial_state"), (d_final_state, "d_final_state", "d_final_grad")):
+        if t is not None:
+            setattr(a, name, _state_ptr(t, what, a.n_seqs, a.heads_v, a.dim_k, a.dim_v, q.device))
+    with _on_stream(q, stream) as s:
+        def new(*shape):
+            return torch.empty(shape, dtype=q.dtype, device=q.device)
+
+        dq, dk, dv = new(*q.shape), new(*k.shape), new(*v.shape)
+        dg = new(*g.shape) if g is not None else None
+        dbeta = new(*beta.shape)
+        d_initial = new(*initial_state.shape) if initial_state is not None else None
+        a.q_grad, a.k_grad, a.v_grad = (Rows(t.data_ptr(), t.stride(0), t.stride(1)) for t in (dq, dk, dv))
+        if dg is not None:
+            a.g_grad = Rows(dg.data_ptr(), dg.stride(0), dg.stride(1))
+        a.beta_grad = Rows(dbeta.data_ptr(), dbeta.stride(0), dbeta.stride(1))
+        if d_initial is not None:
+            a.d_initial_grad = d_initial.data_ptr()
+        a.zero_tail = int(offsets is not None)
+        work = _delta_workspace(a, True, q.device)
+        _check(load_library().dws_delta_rule_backward(ctypes.byref(a), s), "dws_delta_rule_backward")
+        del work
+    return dq, dk, dv, dg, dbeta, d_initial
+
+
+def delta_rule_step(q, k, v, g, beta, state, slots=None, offsets=None, scale=None, out=None, stream=None):
+    """A few more tokens for each sequence (dws_delta_rule_step), fp32 arithmetic, ``state`` updated in place.
+
+    state: float32 (count, heads_v, dim_k, dim_v); sequence i uses state i, or slots[i] (int32 GPU tensor; places below
+    0, outside the pool or named before are left out: their rows of ``out`` and the states stay, and the rows are 0 in
+    a new ``out``). The tokens are shared out evenly over the sequences, or by offsets (int64 GPU tensor, n + 1).
+    Other arguments as delta_rule. Returns out."""
+    import torch
+    if not isinstance(state, torch.Tensor) or state.dim() != 4:
+        raise ValueError("state must be a (count, heads_v, dim_k, dim_v) tensor")
+    n = slots.numel() if isinstance(slots, torch.Tensor) else state.shape[0]
+    a = _delta_args(q, k, v, g, beta, offsets, n, scale)
+    if a.n_seqs != n or n < 1 or (offsets is None and a.tokens % n):
+        raise ValueError(f"{n} sequences do not fit {a.tokens} tokens or {a.n_seqs + 1} offsets")
+    a.d_final_state = a.d_initial_state = _state_ptr(state, "state", None, a.heads_v, a.dim_k, a.dim_v, q.device)
+    if slots is not None:
+        a.d_slots = _device_ints(slots, "slots", torch.int32, n, q.device)
+        a.n_states = state.shape[0]
+    with _on_stream(q, stream) as s:
+        if out is None:
+            out = torch.zeros(v.shape, dtype=q.dtype, device=q.device)
+        a.out = _rows(out, "out", a.tokens, a.heads_v, a.dim_v, q.dtype, q.device)
+        _check(load_library().dws_delta_rule_step(ctypes.byref(a), s), "dws_delta_rule_step")
+    return out
 
 
 def device_memory_info() -> dict:

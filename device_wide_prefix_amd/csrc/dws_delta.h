@@ -1,0 +1,83 @@
+// Host-side interface between the delta rule's C entry points
+// (dws_delta_abi.cpp) and its kernels. Not installed; not part of the public ABI.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "dws_scan.h"
+
+namespace dws {
+
+// Tokens of a chunk: 64 for the 16-bit types, 32 for fp32, whose tiles take
+// twice the LDS (two (chunk x 256) tiles and two (chunk x chunk) ones fit).
+constexpr int delta_chunk(int dtype) { return dtype == DWS_FLOAT32 ? 32 : 64; }
+// Head dimensions the chunk kernels are built for; others run zero-padded.
+constexpr int delta_padded_k(int dim_k) { return dim_k <= 64 ? 64 : (dim_k <= 128 ? 128 : 256); }
+// Columns of a value head are laid out in the workspace in whole 32s.
+constexpr int delta_padded_v(int dim_v) { return (dim_v + 31) / 32 * 32; }
+
+// Parts (numbers of the input type whose sum is the value) of the operands
+// computed in fp32: those of a chunk's size, and all that a final state depends on.
+constexpr int delta_fine_parts(int dtype) { return dtype == DWS_FLOAT32 ? 1 : 2; }
+constexpr int delta_precise_parts(int dtype) { return dtype == DWS_BFLOAT16 ? 3 : delta_fine_parts(dtype); }
+
+// One (tokens, heads, dim) operand: strides in elements, dim contiguous.
+struct DeltaRows {
+    void* data;
+    int64_t ts, hs;
+};
+
+// What every delta-rule kernel is given (by value).
+struct DeltaParams {
+    int64_t tokens, n_seqs;
+    const int64_t* offsets;      // n_seqs + 1, or null: tokens / n_seqs each
+    int heads_qk, heads_v, dim_k, dim_v, dv_pad;
+    float scale;
+    int g_dtype, beta_dtype;
+    int vec;                     // q, k (and d_out) rows can be read in 16-byte units
+    DeltaRows q, k, v, g, beta, out;
+    const float* initial;        // (n_seqs or n_states, heads_v, dim_k, dim_v)
+    float* final_state;
+    const int* slots;
+    int64_t n_states;
+    // backward
+    DeltaRows d_out, dq, dk, dv, dg, dbeta;
+    const float* d_final;
+    void* d_initial;
+    int zero_tail;               // zero the output rows behind the last sequence
+    // workspace
+    int64_t n_slots;             // chunk slots: tokens / chunk + n_seqs + 1 (the last ones empty)
+    float* w_gate;               // [slot][head][3][chunk]: e^G, e^(G_C - G), beta
+    void* w_t;                   // [slot][head][parts][chunk][chunk]: (I + L diag(beta))^-1
+    void* w_p;                   // [slot][head][fine][chunk][chunk]: P (forward), its transpose (backward)
+    void* w_tt;                  // [slot][head][fine][chunk][chunk]: transpose of (I + diag(beta) L)^-1 (backward)
+    void* w_s;                   // [slot][head][padded dim_k][dv_pad]: states at the chunks' starts
+    void* w_u;                   // [slot][head][fine][chunk][dv_pad]: U'
+    void* w_z;                   // [slot][head][fine][chunk][dv_pad]: Z
+    void* w_ds;                  // [slot][head][padded dim_k][dv_pad]: state gradients at the chunks' ends
+};
+
+// Per-type launchers (dws_delta_{bf16,f16,f32}.hip). `precise`: the final
+// state is wanted, with fp32 accuracy.
+hipError_t launch_delta_forward_bf16(const DeltaParams& p, bool precise, hipStream_t stream);
+hipError_t launch_delta_forward_f16(const DeltaParams& p, bool precise, hipStream_t stream);
+hipError_t launch_delta_forward_f32(const DeltaParams& p, bool precise, hipStream_t stream);
+hipError_t launch_delta_backward_bf16(const DeltaParams& p, hipStream_t stream);
+hipError_t launch_delta_backward_f16(const DeltaParams& p, hipStream_t stream);
+hipError_t launch_delta_backward_f32(const DeltaParams& p, hipStream_t stream);
+
+struct DeltaStepParams {
+    int64_t tokens, n_seqs;
+    const int64_t* offsets;
+    int heads_qk, heads_v, dim_k, dim_v;
+    float scale;
+    int dtype, g_dtype, beta_dtype;
+    DeltaRows q, k, v, g, beta, out;
+    float* state;
+    const int* slots;
+    int64_t n_states;
+};
+hipError_t launch_delta_step(const DeltaStepParams& p, bool vec4, hipStream_t stream);
+
+}  // namespace dws

@@ -1,0 +1,297 @@
+// Device pieces the delta-rule kernels share: matrix fragments, their products
+// and loads, and the map from chunk slots to sequences.
+//
+// Fragment layouts (16 x 16 tiles, 64 lanes, gq = lane / 16, lr = lane % 16):
+//   operand   lane holds 8 elements of row (or column) lr along the contraction
+//   acc       lane holds column lr, rows 4 gq + r, r = 0..3
+// A contraction may run over its 32 indices in any order that both operands
+// share. In "natural" order element j of lane group gq is index 8 gq + j: one
+// 16-byte read of a row. In "acc" order it is 4 gq + j for j < 4 and
+// 16 + 4 gq + (j - 4) above: exactly the rows that two stacked acc tiles hold, so
+// a product's result is the next product's operand without leaving its lane.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "dws_delta.h"
+
+namespace dws {
+
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x8 __attribute__((ext_vector_type(8)));
+typedef __bf16 bf16_t;
+typedef _Float16 f16_t;
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+
+template <class T>
+using Vec8 = T __attribute__((ext_vector_type(8)));
+template <class T>
+using Vec4 = T __attribute__((ext_vector_type(4)));
+
+__device__ __forceinline__ f32x4 mma(Vec8<bf16_t> a, Vec8<bf16_t> b, f32x4 c)
+{
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
+}
+__device__ __forceinline__ f32x4 mma(Vec8<f16_t> a, Vec8<f16_t> b, f32x4 c)
+{
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
+}
+// fp32: eight products of depth 4. Step j contracts element j of every lane
+// group, so the 32 indices are covered in whichever order the elements are in.
+__device__ __forceinline__ f32x4 mma(Vec8<float> a, Vec8<float> b, f32x4 c)
+{
+#pragma unroll
+    for (int j = 0; j < 8; ++j) c = __builtin_amdgcn_mfma_f32_16x16x4f32(a[j], b[j], c, 0, 0, 0);
+    return c;
+}
+
+// An operand computed in fp32 as NP parts of type T: the rounded value and the
+// rounded rests. One bf16 part is off by at most 2^-8 of the value, two by
+// 2^-16, three hold all of fp32 (fp16: 2^-11, then 2^-22); fp32 is one part.
+template <class T, int NP>
+struct Parts {
+    Vec8<T> p[NP];
+};
+template <class T, int NP>
+__device__ __forceinline__ Parts<T, NP> parts_of(f32x8 x)
+{
+    Parts<T, NP> r;
+#pragma unroll
+    for (int n = 0; n < NP; ++n) {
+        r.p[n] = __builtin_convertvector(x, Vec8<T>);
+        if (n + 1 < NP) x -= __builtin_convertvector(r.p[n], f32x8);
+    }
+    return r;
+}
+template <class T, int NP>
+__device__ __forceinline__ Parts<T, NP> parts_of(f32x4 lo, f32x4 hi)
+{
+    return parts_of<T, NP>(__builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+}
+// Product of two operands in parts, smallest terms first. Terms whose parts'
+// numbers sum to more than the longer one's last part are below its rounding
+// and are left out.
+template <class T, int NA, int NB>
+__device__ __forceinline__ f32x4 mma(const Parts<T, NA>& a, const Parts<T, NB>& b, f32x4 c)
+{
+    constexpr int LAST = (NA > NB ? NA : NB) - 1;
+#pragma unroll
+    for (int s = LAST; s >= 0; --s)
+#pragma unroll
+        for (int i = 0; i < NA; ++i)
+            if (s - i >= 0 && s - i < NB) c = mma(a.p[i], b.p[s - i], c);
+    return c;
+}
+template <class T, int NP>
+__device__ __forceinline__ f32x4 mma(Vec8<T> a, const Parts<T, NP>& b, f32x4 c)
+{
+#pragma unroll
+    for (int n = NP - 1; n >= 0; --n) c = mma(a, b.p[n], c);
+    return c;
+}
+
+// ---- LDS tiles: rows of `stride` elements --------------------------------
+
+// LDS row length: 16 bytes more than the row, so that the 16 rows a fragment
+// read touches start in different banks.
+template <class T>
+constexpr int lds_stride(int cols) { return cols + 16 / (int)sizeof(T); }
+
+// Operand rows r0..r0+15, contraction columns c0..c0+31, natural order.
+template <class T>
+__device__ __forceinline__ Vec8<T> frag_nat(const T* tile, int stride, int r0, int c0, int lane)
+{
+    const T* p = tile + (r0 + (lane & 15)) * stride + c0 + (lane >> 4) * 8;
+    if constexpr (sizeof(T) == 2) {
+        return *reinterpret_cast<const Vec8<T>*>(p);
+    } else {
+        const Vec4<T> a = *reinterpret_cast<const Vec4<T>*>(p), b = *reinterpret_cast<const Vec4<T>*>(p + 4);
+        return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
+    }
+}
+// The same in acc order.
+template <class T>
+__device__ __forceinline__ Vec8<T> frag_acc(const T* tile, int stride, int r0, int c0, int lane)
+{
+    const T* p = tile + (r0 + (lane & 15)) * stride + c0 + (lane >> 4) * 4;
+    const Vec4<T> a = *reinterpret_cast<const Vec4<T>*>(p), b = *reinterpret_cast<const Vec4<T>*>(p + 16);
+    return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
+}
+// The parts of an operand in as many tiles, one behind the other.
+template <int NP, class T>
+__device__ __forceinline__ Parts<T, NP> parts_acc(const T* tile, int tile_elems, int stride, int r0, int c0, int lane)
+{
+    Parts<T, NP> a;
+#pragma unroll
+    for (int n = 0; n < NP; ++n) a.p[n] = frag_acc(tile + n * tile_elems, stride, r0, c0, lane);
+    return a;
+}
+// Four elements of column c0 + lr in rows r0 + 4 gq + (0..3): what an acc tile
+// of these rows and columns holds. The 16-bit types use the transposing LDS
+// read: within 16 lanes, lane i points at 4 elements of row i / 4 and receives
+// column i of the 4 x 16 block.
+template <class T>
+__device__ __forceinline__ Vec4<T> quad_tr(const T* tile, int stride, int r0, int c0, int lane)
+{
+    if constexpr (sizeof(T) == 2) {
+        const T* p = tile + (r0 + (lane >> 4) * 4 + ((lane >> 2) & 3)) * stride + c0 + (lane & 3) * 4;
+        const s16x4 v = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+            (__attribute__((address_space(3))) s16x4*)(reinterpret_cast<uintptr_t>(p)));
+        return __builtin_bit_cast(Vec4<T>, v);
+    } else {
+        const T* p = tile + (r0 + (lane >> 4) * 4) * stride + c0 + (lane & 15);
+        return Vec4<T>{p[0], p[stride], p[2 * stride], p[3 * stride]};
+    }
+}
+// Operand of the transposed tile: its rows are the tile's columns c0..c0+15,
+// the contraction the tile's rows r0..r0+31 in acc order.
+template <class T>
+__device__ __forceinline__ Vec8<T> frag_tr(const T* tile, int stride, int r0, int c0, int lane)
+{
+    const Vec4<T> a = quad_tr(tile, stride, r0, c0, lane), b = quad_tr(tile, stride, r0 + 16, c0, lane);
+    return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
+}
+
+template <int NP, class T>
+__device__ __forceinline__ Parts<T, NP> parts_tr(const T* tile, int tile_elems, int stride, int r0, int c0, int lane)
+{
+    Parts<T, NP> a;
+#pragma unroll
+    for (int n = 0; n < NP; ++n) a.p[n] = frag_tr(tile + n * tile_elems, stride, r0, c0, lane);
+    return a;
+}
+// x as NP parts, `step` elements apart.
+template <int NP, class T>
+__device__ __forceinline__ void store_parts(T* at, int64_t step, float x)
+{
+#pragma unroll
+    for (int n = 0; n < NP; ++n) {
+        const T y = (T)x;
+        at[n * step] = y;
+        x -= (float)y;
+    }
+}
+
+// ---- global memory --------------------------------------------------------
+
+__device__ __forceinline__ float load_gate(const DeltaRows& r, int64_t token, int head, int dtype)
+{
+    const int64_t at = token * r.ts + head * r.hs;
+    if (dtype == DWS_FLOAT32) return static_cast<const float*>(r.data)[at];
+    if (dtype == DWS_BFLOAT16) return (float)static_cast<const bf16_t*>(r.data)[at];
+    return (float)static_cast<const f16_t*>(r.data)[at];
+}
+
+// A log decay below -104 gives a factor below the least fp32 number whatever
+// it is multiplied with, so it is taken as -104: sums of a chunk's decays and
+// their differences then stay finite for -infinity too. NaN stays NaN.
+__device__ __forceinline__ float clamp_decay(float g) { return g < -104.f ? -104.f : g; }
+
+// rows x cols elements at `src` (row stride `ld`) into an LDS tile, zero in
+// the columns up to `padded` and in the rows up to `all_rows`.
+template <class T, int THREADS>
+__device__ __forceinline__ void stage_tile(T* tile, int stride, const T* src, int64_t ld, int rows, int cols,
+                                           int all_rows, int padded, bool vec, int tid)
+{
+    constexpr int V = 16 / (int)sizeof(T);
+    typedef T VecT __attribute__((ext_vector_type(V)));
+    const int units = padded / V;
+    for (int i = tid; i < all_rows * units; i += THREADS) {
+        const int r = i / units, c = (i - r * units) * V;
+        VecT x = {};
+        if (r < rows) {
+            if (vec && c + V <= cols) {
+                x = *reinterpret_cast<const VecT*>(src + r * ld + c);
+            } else {
+#pragma unroll
+                for (int j = 0; j < V; ++j)
+                    if (c + j < cols) x[j] = src[r * ld + c + j];
+            }
+        }
+        *reinterpret_cast<VecT*>(tile + r * stride + c) = x;
+    }
+}
+
+// ---- sequences ------------------------------------------------------------
+
+// First row and length of sequence i; whatever the offsets hold, the rows lie
+// in [0, tokens).
+__device__ __forceinline__ int64_t seq_begin(const int64_t* offsets, int64_t tokens, int64_t n_seqs, int64_t i)
+{
+    if (offsets == nullptr) return i * (tokens / n_seqs);
+    const int64_t b = offsets[i];
+    return b < 0 ? 0 : (b > tokens ? tokens : b);
+}
+__device__ __forceinline__ int64_t seq_length(const int64_t* offsets, int64_t tokens, int64_t n_seqs, int64_t i,
+                                              int64_t begin)
+{
+    if (offsets == nullptr) return tokens / n_seqs;
+    const int64_t e = offsets[i + 1];
+    const int64_t end = e < begin ? begin : (e > tokens ? tokens : e);
+    return end - begin;
+}
+
+// Chunk c of sequence i is chunk slot begin_i / C + i + c. Its ceil(len / C)
+// chunks end before the next sequence's first slot, since
+// ceil((b + C x - a) / C) <= x + 1 + floor(b / C) - floor(a / C), and the last
+// one before tokens / C + n_seqs.
+__device__ __forceinline__ int64_t first_slot(int64_t begin, int64_t i, int chunk) { return begin / chunk + i; }
+
+struct SlotInfo {
+    int64_t seq;
+    int64_t row;       // first row of the chunk
+    int rows;          // its tokens, 0 for a slot without any
+    int64_t beyond;    // for a slot behind the last sequence's: how far, else -1
+};
+template <int C>
+__device__ __forceinline__ SlotInfo slot_info(const int64_t* offsets, int64_t tokens, int64_t n_seqs, int64_t slot)
+{
+    int64_t lo = 0, hi = n_seqs - 1;      // last sequence whose first slot is not behind `slot`
+    while (lo < hi) {
+        const int64_t mid = (lo + hi + 1) / 2;
+        if (first_slot(seq_begin(offsets, tokens, n_seqs, mid), mid, C) <= slot)
+            lo = mid;
+        else
+            hi = mid - 1;
+    }
+    SlotInfo s;
+    s.seq = lo;
+    const int64_t begin = seq_begin(offsets, tokens, n_seqs, lo);
+    const int64_t len = seq_length(offsets, tokens, n_seqs, lo, begin);
+    const int64_t c = slot - first_slot(begin, lo, C);
+    const int64_t left = len - c * C;
+    s.row = begin + c * C;
+    s.rows = c < 0 || left <= 0 ? 0 : (left < C ? (int)left : C);
+    s.beyond = lo == n_seqs - 1 && c >= 0 && left <= 0 ? c - (len + C - 1) / C : -1;
+    return s;
+}
+
+// Whether sequence i takes part: its slot is in the pool and no earlier
+// sequence of the call names it. Every thread of the workgroup calls it.
+template <int THREADS>
+__device__ __forceinline__ bool slot_taken(const int* slots, int64_t n_states, int64_t i, int64_t* state, int tid)
+{
+    if (slots == nullptr) {
+        *state = i;
+        return true;
+    }
+    const int mine = slots[i];
+    bool again = false;
+    for (int64_t j = tid; j < i; j += THREADS) again |= slots[j] == mine;
+    *state = mine;
+    const bool dup = __syncthreads_or(again);
+    return mine >= 0 && mine < n_states && !dup;
+}
+
+// Workgroup index -> (group, part of `parts`) such that the parts of a group
+// are dealt to one XCD (workgroups go to the 8 XCDs in turn): they read the same
+// rows, which that XCD's L2 then holds once. `blocks` is a multiple of 8 parts.
+__device__ __forceinline__ void xcd_split(uint32_t block, uint32_t parts, uint32_t* group, uint32_t* part)
+{
+    const uint32_t eight = block / (8 * parts), rest = block - eight * 8 * parts;
+    *part = rest / 8;
+    *group = eight * 8 + rest % 8;
+}
+
+}  // namespace dws

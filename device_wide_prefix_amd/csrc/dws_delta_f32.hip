@@ -1,0 +1,14 @@
+// The chunked gated delta rule for f32 inputs.
+#include "dws_delta_kernel.hpp"
+
+namespace dws {
+
+hipError_t launch_delta_forward_f32(const DeltaParams& p, bool precise, hipStream_t stream)
+{
+    (void)precise;      // fp32 operands are exact
+    return forward_type<float, 1>(p, stream);
+}
+
+hipError_t launch_delta_backward_f32(const DeltaParams& p, hipStream_t stream) { return backward_type<float>(p, stream); }
+
+}  // namespace dws

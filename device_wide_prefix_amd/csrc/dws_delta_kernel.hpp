@@ -1,0 +1,893 @@
+// The chunked gated delta rule: kernels over chunks of C tokens.
+//
+// With G_i the sum of a chunk's first i log decays, D_ij = e^(G_i - G_j) for
+// i >= j, S the state at the chunk's start and B = diag(beta):
+//   L = tril(D o K K^T, -1)          X = V - diag(e^G) K S
+//   U' = (I + L B)^-1 X              u = B U'       (what each token writes)
+//   O = scale diag(e^G) Q S + P u    P = scale tril(D o Q K^T)
+//   S <- e^(G_C) S + K^T diag(e^(G_C - G)) u
+// k_delta_prep does for every chunk at once what does not depend on S (P and
+// the inverse); k_delta_scan then goes through a sequence's chunks. The columns
+// of S never meet: each wave owns 16 of them for the whole sequence, S in its
+// registers, and passes products on as operands without a transfer.
+#pragma once
+
+#include "dws_delta_device.hpp"
+
+namespace dws {
+
+template <class T>
+constexpr int kChunk = sizeof(T) == 4 ? 32 : 64;
+
+// Parts of the 16-bit operands that are computed in fp32. With one part for
+// all, bf16 outputs and gradients are off by 3.3e-3 to 4.9e-3 (2-norm), twice
+// what rounding the result itself gives (1.7e-3). The arrays of a chunk's size,
+// P, X, U', Z, dU, scale e^G dO, W1 and W2, make up nearly all of that; in two
+// parts they leave at most 1.4 times the result's own rounding. So does the
+// inverse: where keys repeat, its rows subtract neighbouring tokens from each
+// other, and what is left is far smaller than its entries' rounding. S and dS,
+// which are larger and cost the most products and bytes, add 0.5 times at most
+// and keep one part.
+template <class T>
+constexpr int kFine = sizeof(T) == 4 ? 1 : 2;
+// Parts of everything that a final state depends on, for fp32 accuracy.
+template <class T>
+constexpr int kPrecise = __is_same(T, bf16_t) ? 3 : kFine<T>;
+
+// ---- the inverse of a unit lower triangular matrix -----------------------
+
+// inv = (I + M)^-1, M strictly lower triangular, with M_ij = l[i][j] *
+// (BY_ROW ? beta[i] : beta[j]); both fp32 in LDS, rows of C + 1. Diagonal
+// 16 x 16 blocks by substitution (one wave each, a column a lane), then block
+// row i from the rows above: inv_ij = -inv_ii sum_k M_ik inv_kj. Substitution
+// keeps the error at the size of the result's entries; a product of powers
+// (I - M)(I + M^2)... would not, since the powers of M can be far larger.
+template <int C, bool BY_ROW>
+__device__ __forceinline__ void invert_unit_lower(const float (*l)[C + 1], const float* beta, float (*inv)[C + 1],
+                                                  int wave, int lane)
+{
+    constexpr int NB = C / 16;
+    const int col = lane & 15, gq = lane >> 4;
+    auto m = [&](int i, int j) { return l[i][j] * (BY_ROW ? beta[i] : beta[j]); };
+    {
+        const int b0 = wave * 16;
+        float x[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            float s = i == col ? 1.f : 0.f;
+#pragma unroll
+            for (int j = 0; j < i; ++j) s -= m(b0 + i, b0 + j) * x[j];
+            x[i] = s;
+        }
+        if (gq == 0) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) inv[b0 + i][b0 + col] = x[i];
+        }
+        // the blocks above the diagonal
+        for (int jb = wave + 1; jb < NB; ++jb)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) inv[b0 + gq * 4 + r][jb * 16 + col] = 0.f;
+    }
+    __syncthreads();
+    for (int ib = 1; ib < NB; ++ib) {
+        float acc[4] = {};
+        if (wave < ib) {
+            for (int k = wave * 16; k < ib * 16; ++k) {
+                const float y = inv[k][wave * 16 + col];
+#pragma unroll
+                for (int r = 0; r < 4; ++r) acc[r] += m(ib * 16 + gq * 4 + r, k) * y;
+            }
+#pragma unroll
+            for (int r = 0; r < 4; ++r) inv[ib * 16 + gq * 4 + r][wave * 16 + col] = acc[r];
+        }
+        __syncthreads();
+        if (wave < ib) {
+            float y[4] = {};
+            for (int k = 0; k < 16; ++k) {
+                const float a = inv[ib * 16 + k][wave * 16 + col];
+#pragma unroll
+                for (int r = 0; r < 4; ++r) y[r] -= inv[ib * 16 + gq * 4 + r][ib * 16 + k] * a;
+            }
+#pragma unroll
+            for (int r = 0; r < 4; ++r) acc[r] = y[r];
+        }
+        __syncthreads();
+        if (wave < ib) {
+#pragma unroll
+            for (int r = 0; r < 4; ++r) inv[ib * 16 + gq * 4 + r][wave * 16 + col] = acc[r];
+        }
+        __syncthreads();
+    }
+}
+
+template <class T, int C>
+struct PrepShared {
+    float l[C][C + 1];
+    float inv[C][C + 1];
+    double total[C];
+    float beta[C];
+};
+template <class T, int DK>
+constexpr size_t prep_lds_bytes()
+{
+    constexpr int C = kChunk<T>;
+    return sizeof(PrepShared<T, C>) + 2 * (size_t)C * lds_stride<T>(DK) * sizeof(T);
+}
+
+// Sums of the chunk's log decays, in double: the differences of two sums of 64
+// then keep fp32 accuracy however large the sums are.
+template <int C>
+__device__ __forceinline__ double scan_decays(double g, int lane)
+{
+#pragma unroll
+    for (int d = 1; d < C; d *= 2) {
+        const double o = __shfl_up(g, d, 64);
+        if (lane >= d) g += o;
+    }
+    return g;
+}
+
+template <class T>
+__device__ __forceinline__ void zero_rows(const DeltaRows& r, int64_t first, int64_t last, int64_t step, int chunk,
+                                          int heads, int dim, int tid, int threads)
+{
+    if (r.data == nullptr) return;
+    T* p = static_cast<T*>(r.data);
+    for (int64_t base = first; base < last; base += step)
+        for (int i = tid; i < chunk * heads * dim; i += threads) {
+            const int64_t row = base + i / (heads * dim);
+            const int h = i / dim % heads, d = i % dim;
+            if (row < last) p[row * r.ts + h * r.hs + d] = (T)0.f;
+        }
+}
+
+// One workgroup for each (chunk slot, value head): gate factors, P and the
+// inverse(s) to the workspace. Products over dim_k on the matrix cores, wave w
+// owning the tokens 16 w .. 16 w + 15.
+template <class T, int DK, int NP, bool BWD>
+__global__ __launch_bounds__(kChunk<T> * 4) void k_delta_prep(DeltaParams p)
+{
+    constexpr int C = kChunk<T>, THREADS = C * 4, NB = C / 16, LK = lds_stride<T>(DK);
+    extern __shared__ __attribute__((aligned(16))) char smem[];
+    auto& sh = *reinterpret_cast<PrepShared<T, C>*>(smem);
+    T* ks = reinterpret_cast<T*>(smem + sizeof(PrepShared<T, C>));
+    T* qs = ks + C * LK;
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, gq = lane >> 4, lr = lane & 15;
+    const int64_t slot = blockIdx.x / p.heads_v;
+    const int h = blockIdx.x % p.heads_v, hk = h / (p.heads_v / p.heads_qk);
+    const SlotInfo info = slot_info<C>(p.offsets, p.tokens, p.n_seqs, slot);
+    if (info.rows == 0) {
+        if (p.zero_tail && info.beyond >= 0 && h == 0) {
+            const int64_t begin = seq_begin(p.offsets, p.tokens, p.n_seqs, info.seq);
+            const int64_t len = seq_length(p.offsets, p.tokens, p.n_seqs, info.seq, begin);
+            const int64_t spare = p.n_slots - first_slot(begin, info.seq, C) - (len + C - 1) / C;
+            const int64_t first = begin + len + info.beyond * C, step = spare * C;
+            if constexpr (BWD) {
+                zero_rows<T>(p.dq, first, p.tokens, step, C, p.heads_qk, p.dim_k, tid, THREADS);
+                zero_rows<T>(p.dk, first, p.tokens, step, C, p.heads_qk, p.dim_k, tid, THREADS);
+                zero_rows<T>(p.dv, first, p.tokens, step, C, p.heads_v, p.dim_v, tid, THREADS);
+                zero_rows<T>(p.dg, first, p.tokens, step, C, p.heads_v, 1, tid, THREADS);
+                zero_rows<T>(p.dbeta, first, p.tokens, step, C, p.heads_v, 1, tid, THREADS);
+            } else {
+                zero_rows<T>(p.out, first, p.tokens, step, C, p.heads_v, p.dim_v, tid, THREADS);
+            }
+        }
+        return;
+    }
+    const T* k0 = static_cast<const T*>(p.k.data) + info.row * p.k.ts + hk * p.k.hs;
+    const T* q0 = static_cast<const T*>(p.q.data) + info.row * p.q.ts + hk * p.q.hs;
+    stage_tile<T, THREADS>(ks, LK, k0, p.k.ts, info.rows, p.dim_k, C, DK, p.vec, tid);
+    stage_tile<T, THREADS>(qs, LK, q0, p.q.ts, info.rows, p.dim_k, C, DK, p.vec, tid);
+    const int64_t at = slot * p.heads_v + h;
+    if (wave == 0) {
+        const bool in = lane < info.rows;
+        const float g = in && p.g.data ? clamp_decay(load_gate(p.g, info.row + lane, h, p.g_dtype)) : 0.f;
+        const float b = in ? load_gate(p.beta, info.row + lane, h, p.beta_dtype) : 0.f;
+        const double total = scan_decays<C>((double)g, lane);
+        const double last = __shfl(total, C - 1, 64);
+        if (lane < C) {
+            sh.total[lane] = total;
+            sh.beta[lane] = b;
+            float* w = p.w_gate + at * 3 * C;
+            w[lane] = expf((float)total);
+            w[C + lane] = expf((float)(last - total));
+            w[2 * C + lane] = b;
+        }
+    }
+    __syncthreads();
+
+    // row tile `wave` of K K^T and Q K^T, up to the diagonal
+    constexpr int NF = kFine<T>;
+    T* wp = static_cast<T*>(p.w_p) + at * NF * C * C;
+#pragma unroll
+    for (int nt = 0; nt < NB; ++nt) {
+        f32x4 kk = {}, qk = {};
+        if (nt <= wave) {
+#pragma unroll
+            for (int kb = 0; kb < DK; kb += 32) {
+                const Vec8<T> b = frag_nat(ks, LK, nt * 16, kb, lane);
+                kk = mma(frag_nat(ks, LK, wave * 16, kb, lane), b, kk);
+                qk = mma(frag_nat(qs, LK, wave * 16, kb, lane), b, qk);
+            }
+        }
+        const int j = nt * 16 + lr;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            const int i = wave * 16 + gq * 4 + r;
+            const float d = i >= j ? expf((float)(sh.total[i] - sh.total[j])) : 0.f;
+            sh.l[i][j] = i > j ? d * kk[r] : 0.f;
+            const float pij = i >= j ? p.scale * d * qk[r] : 0.f;
+            store_parts<NF>(wp + (BWD ? j * C + i : i * C + j), C * C, pij);
+        }
+    }
+    __syncthreads();
+
+    invert_unit_lower<C, false>(sh.l, sh.beta, sh.inv, wave, lane);
+    constexpr int NX = NP > NF ? NP : NF;
+    T* wt = static_cast<T*>(p.w_t) + at * NX * C * C;
+    for (int i = tid; i < C * C; i += THREADS) store_parts<NX>(wt + i, C * C, sh.inv[i / C][i % C]);
+    if constexpr (BWD) {
+        __syncthreads();
+        invert_unit_lower<C, true>(sh.l, sh.beta, sh.inv, wave, lane);
+        T* wtt = static_cast<T*>(p.w_tt) + at * NF * C * C;
+        for (int i = tid; i < C * C; i += THREADS) store_parts<NF>(wtt + i, C * C, sh.inv[i % C][i / C]);
+    }
+}
+
+// ---- the forward scan ------------------------------------------------------
+
+template <class T, int DK, int NP, bool STORE>
+constexpr size_t scan_lds_bytes()
+{
+    constexpr int C = kChunk<T>;
+    const size_t qk = (size_t)C * lds_stride<T>(DK) * sizeof(T), cc = (size_t)C * lds_stride<T>(C) * sizeof(T);
+    constexpr int NX = NP > kFine<T> ? NP : kFine<T>;
+    return (STORE ? 1 : 2) * qk + (STORE ? NX : NX + kFine<T>) * cc + 3 * C * sizeof(float);
+}
+
+// STORE: instead of the outputs, the states at the chunks' starts and U' go to
+// the workspace (for the backward pass). NP: parts of the operands the state
+// depends on. NW waves, 16 columns of the value head each.
+template <class T, int DK, int NP, bool STORE, int NW>
+__global__ __launch_bounds__(NW * 64) void k_delta_scan(DeltaParams p)
+{
+    constexpr int C = kChunk<T>, THREADS = NW * 64, NB = C / 16, LK = lds_stride<T>(DK), LC = lds_stride<T>(C);
+    constexpr int NF = kFine<T>, NX = NP > NF ? NP : NF;
+    extern __shared__ __attribute__((aligned(16))) char smem[];
+    T* ks = reinterpret_cast<T*>(smem);
+    T* qs = ks + C * LK;                       // not with STORE
+    T* ts = STORE ? qs : qs + C * LK;          // NX tiles
+    T* ps = ts + NX * C * LC;                  // NF tiles, not with STORE
+    float* gate = reinterpret_cast<float*>(STORE ? ps : ps + NF * C * LC);
+
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, gq = lane >> 4, lr = lane & 15;
+    const uint32_t parts = (uint32_t)((p.dim_v + NW * 16 - 1) / (NW * 16));
+    uint32_t group, part;
+    xcd_split(blockIdx.x, parts, &group, &part);
+    if (group >= (uint64_t)p.n_seqs * p.heads_v) return;
+    const int64_t seq = group / p.heads_v;
+    const int h = group % p.heads_v, hk = h / (p.heads_v / p.heads_qk);
+    const int col = (part * NW + wave) * 16 + lr;
+    const bool mine = col < p.dim_v;
+    int64_t st;
+    if (!slot_taken<THREADS>(p.slots, p.n_states, seq, &st, tid)) return;
+    const int64_t begin = seq_begin(p.offsets, p.tokens, p.n_seqs, seq);
+    const int64_t len = seq_length(p.offsets, p.tokens, p.n_seqs, seq, begin);
+    const int64_t slot0 = first_slot(begin, seq, C);
+    const int64_t state_at = (st * p.heads_v + h) * p.dim_k * p.dim_v + col;
+
+    f32x4 s[DK / 16];
+#pragma unroll
+    for (int t = 0; t < DK / 16; ++t)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            const int row = t * 16 + gq * 4 + r;
+            s[t][r] = p.initial && mine && row < p.dim_k ? p.initial[state_at + (int64_t)row * p.dim_v] : 0.f;
+        }
+
+    for (int64_t c0 = 0, slot = slot0; c0 < len; c0 += C, ++slot) {
+        const int rows = len - c0 < C ? (int)(len - c0) : C;
+        const int64_t row0 = begin + c0, at = slot * p.heads_v + h;
+        stage_tile<T, THREADS>(ks, LK, static_cast<const T*>(p.k.data) + row0 * p.k.ts + hk * p.k.hs, p.k.ts, rows,
+                               p.dim_k, C, DK, p.vec, tid);
+        if constexpr (!STORE) {
+            stage_tile<T, THREADS>(qs, LK, static_cast<const T*>(p.q.data) + row0 * p.q.ts + hk * p.q.hs, p.q.ts, rows,
+                                   p.dim_k, C, DK, p.vec, tid);
+            stage_tile<T, THREADS>(ps, LC, static_cast<const T*>(p.w_p) + at * NF * C * C, C, NF * C, C, NF * C, C, true,
+                                   tid);
+        }
+        stage_tile<T, THREADS>(ts, LC, static_cast<const T*>(p.w_t) + at * NX * C * C, C, NX * C, C, NX * C, C, true, tid);
+        for (int i = tid; i < 3 * C; i += THREADS) gate[i] = p.w_gate[at * 3 * C + i];
+        // this wave's columns of V, laid out as the products' results
+        f32x4 x[NB];
+        const T* v0 = static_cast<const T*>(p.v.data) + row0 * p.v.ts + h * p.v.hs + col;
+#pragma unroll
+        for (int mt = 0; mt < NB; ++mt)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const int row = mt * 16 + gq * 4 + r;
+                x[mt][r] = mine && row < rows ? (float)v0[row * p.v.ts] : 0.f;
+            }
+        __syncthreads();
+
+        if constexpr (STORE) {
+            T* ws = static_cast<T*>(p.w_s) + at * DK * p.dv_pad + col;
+            if (col < p.dv_pad)
+#pragma unroll
+                for (int t = 0; t < DK / 16; ++t)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) ws[(t * 16 + gq * 4 + r) * p.dv_pad] = (T)s[t][r];
+        }
+        Parts<T, NP> sb[DK / 32];
+#pragma unroll
+        for (int kb = 0; kb < DK / 32; ++kb) sb[kb] = parts_of<T, NP>(s[2 * kb], s[2 * kb + 1]);
+        // X = V - diag(e^G) K S
+#pragma unroll
+        for (int mt = 0; mt < NB; ++mt) {
+            f32x4 acc = {};
+#pragma unroll
+            for (int kb = 0; kb < DK / 32; ++kb) acc = mma(frag_acc(ks, LK, mt * 16, kb * 32, lane), sb[kb], acc);
+#pragma unroll
+            for (int r = 0; r < 4; ++r) x[mt][r] -= gate[mt * 16 + gq * 4 + r] * acc[r];
+        }
+        Parts<T, NX> xb[C / 32];
+#pragma unroll
+        for (int kb = 0; kb < C / 32; ++kb) xb[kb] = parts_of<T, NX>(x[2 * kb], x[2 * kb + 1]);
+        // U' = (I + L B)^-1 X; u = B U'
+        f32x4 u[NB];
+#pragma unroll
+        for (int mt = 0; mt < NB; ++mt) {
+            f32x4 acc = {};
+#pragma unroll
+            for (int kb = 0; kb <= mt / 2; ++kb)
+                acc = mma(parts_acc<NX>(ts, C * LC, LC, mt * 16, kb * 32, lane), xb[kb], acc);
+            if constexpr (STORE) {
+                T* wu = static_cast<T*>(p.w_u) + at * NF * C * p.dv_pad + col;
+                if (col < p.dv_pad)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r)
+                        store_parts<NF>(wu + (mt * 16 + gq * 4 + r) * p.dv_pad, C * p.dv_pad, acc[r]);
+            }
+#pragma unroll
+            for (int r = 0; r < 4; ++r) u[mt][r] = gate[2 * C + mt * 16 + gq * 4 + r] * acc[r];
+        }
+        if constexpr (!STORE) {
+            Parts<T, NF> ub[C / 32];
+#pragma unroll
+            for (int kb = 0; kb < C / 32; ++kb) ub[kb] = parts_of<T, NF>(u[2 * kb], u[2 * kb + 1]);
+            T* o0 = static_cast<T*>(p.out.data) + row0 * p.out.ts + h * p.out.hs + col;
+#pragma unroll
+            for (int mt = 0; mt < NB; ++mt) {
+                f32x4 acc = {};
+#pragma unroll
+                for (int kb = 0; kb < DK / 32; ++kb)
+                    acc = mma(frag_acc(qs, LK, mt * 16, kb * 32, lane), sb[kb].p[0], acc);
+#pragma unroll
+                for (int r = 0; r < 4; ++r) acc[r] *= p.scale * gate[mt * 16 + gq * 4 + r];
+#pragma unroll
+                for (int kb = 0; kb <= mt / 2; ++kb)
+                    acc = mma(parts_acc<NF>(ps, C * LC, LC, mt * 16, kb * 32, lane), ub[kb], acc);
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const int row = mt * 16 + gq * 4 + r;
+                    if (mine && row < rows) o0[row * p.out.ts] = (T)acc[r];
+                }
+            }
+        }
+        // S <- e^(G_C) S + K^T diag(e^(G_C - G)) u
+#pragma unroll
+        for (int mt = 0; mt < NB; ++mt)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) u[mt][r] *= gate[C + mt * 16 + gq * 4 + r];
+        Parts<T, NX> ub[C / 32];
+#pragma unroll
+        for (int kb = 0; kb < C / 32; ++kb) ub[kb] = parts_of<T, NX>(u[2 * kb], u[2 * kb + 1]);
+        const float keep = gate[C - 1];
+#pragma unroll
+        for (int t = 0; t < DK / 16; ++t) {
+#pragma unroll
+            for (int r = 0; r < 4; ++r) s[t][r] *= keep;
+#pragma unroll
+            for (int kb = 0; kb < C / 32; ++kb) s[t] = mma(frag_tr(ks, LK, kb * 32, t * 16, lane), ub[kb], s[t]);
+        }
+        __syncthreads();
+    }
+    if (!STORE && p.final_state != nullptr && mine) {
+#pragma unroll
+        for (int t = 0; t < DK / 16; ++t)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const int row = t * 16 + gq * 4 + r;
+                if (row < p.dim_k) p.final_state[state_at + (int64_t)row * p.dim_v] = s[t][r];
+            }
+    }
+}
+
+// ---- the backward scan -----------------------------------------------------
+//
+// With dS' the gradient at the chunk's end and dO given:
+//   dU = P^T dO + diag(e^(G_C - G)) K dS'     Z = (I + B L)^-T dU     dX = B Z = dV
+//   dS = e^(G_C) dS' + Q^T diag(scale e^G) dO - K^T diag(e^G) dX
+// The same shape as the forward scan, from a sequence's last chunk to its
+// first. Z and dS' go to the workspace, dV to its place.
+
+template <class T, int DK>
+constexpr size_t scan_back_lds_bytes()
+{
+    constexpr int C = kChunk<T>;
+    return 2 * (size_t)C * lds_stride<T>(DK) * sizeof(T) + 2 * kFine<T> * (size_t)C * lds_stride<T>(C) * sizeof(T) +
+           3 * C * sizeof(float);
+}
+
+template <class T, int DK, int NW>
+__global__ __launch_bounds__(NW * 64) void k_delta_scan_back(DeltaParams p)
+{
+    constexpr int C = kChunk<T>, THREADS = NW * 64, NB = C / 16, LK = lds_stride<T>(DK), LC = lds_stride<T>(C);
+    constexpr int NF = kFine<T>;
+    extern __shared__ __attribute__((aligned(16))) char smem[];
+    T* ks = reinterpret_cast<T*>(smem);
+    T* qs = ks + C * LK;
+    T* ts = qs + C * LK;
+    T* ps = ts + NF * C * LC;
+    float* gate = reinterpret_cast<float*>(ps + NF * C * LC);
+
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, gq = lane >> 4, lr = lane & 15;
+    const uint32_t parts = (uint32_t)((p.dim_v + NW * 16 - 1) / (NW * 16));
+    uint32_t group, part;
+    xcd_split(blockIdx.x, parts, &group, &part);
+    if (group >= (uint64_t)p.n_seqs * p.heads_v) return;
+    const int64_t seq = group / p.heads_v;
+    const int h = group % p.heads_v, hk = h / (p.heads_v / p.heads_qk);
+    const int col = (part * NW + wave) * 16 + lr;
+    const bool mine = col < p.dim_v, held = col < p.dv_pad;
+    const int64_t begin = seq_begin(p.offsets, p.tokens, p.n_seqs, seq);
+    const int64_t len = seq_length(p.offsets, p.tokens, p.n_seqs, seq, begin);
+    const int64_t chunks = (len + C - 1) / C, slot0 = first_slot(begin, seq, C);
+    const int64_t state_at = (seq * p.heads_v + h) * p.dim_k * p.dim_v + col;
+
+    f32x4 ds[DK / 16];
+#pragma unroll
+    for (int t = 0; t < DK / 16; ++t)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            const int row = t * 16 + gq * 4 + r;
+            ds[t][r] = p.d_final && mine && row < p.dim_k ? p.d_final[state_at + (int64_t)row * p.dim_v] : 0.f;
+        }
+
+    for (int64_t c = chunks - 1; c >= 0; --c) {
+        const int64_t c0 = c * C, row0 = begin + c0, at = (slot0 + c) * p.heads_v + h;
+        const int rows = len - c0 < C ? (int)(len - c0) : C;
+        stage_tile<T, THREADS>(ks, LK, static_cast<const T*>(p.k.data) + row0 * p.k.ts + hk * p.k.hs, p.k.ts, rows,
+                               p.dim_k, C, DK, p.vec, tid);
+        stage_tile<T, THREADS>(qs, LK, static_cast<const T*>(p.q.data) + row0 * p.q.ts + hk * p.q.hs, p.q.ts, rows,
+                               p.dim_k, C, DK, p.vec, tid);
+        stage_tile<T, THREADS>(ps, LC, static_cast<const T*>(p.w_p) + at * NF * C * C, C, NF * C, C, NF * C, C, true, tid);
+        stage_tile<T, THREADS>(ts, LC, static_cast<const T*>(p.w_tt) + at * NF * C * C, C, NF * C, C, NF * C, C, true, tid);
+        for (int i = tid; i < 3 * C; i += THREADS) gate[i] = p.w_gate[at * 3 * C + i];
+        f32x4 d_o[NB];
+        const T* o0 = static_cast<const T*>(p.d_out.data) + row0 * p.d_out.ts + h * p.d_out.hs + col;
+#pragma unroll
+        for (int mt = 0; mt < NB; ++mt)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const int row = mt * 16 + gq * 4 + r;
+                d_o[mt][r] = mine && row < rows ? (float)o0[row * p.d_out.ts] : 0.f;
+            }
+        __syncthreads();
+
+        T* wds = static_cast<T*>(p.w_ds) + at * DK * p.dv_pad + col;
+        if (held)
+#pragma unroll
+            for (int t = 0; t < DK / 16; ++t)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) wds[(t * 16 + gq * 4 + r) * p.dv_pad] = (T)ds[t][r];
+        Parts<T, 1> db[DK / 32], ob[C / 32];     // dO is exact in T
+#pragma unroll
+        for (int kb = 0; kb < DK / 32; ++kb) db[kb] = parts_of<T, 1>(ds[2 * kb], ds[2 * kb + 1]);
+#pragma unroll
+        for (int kb = 0; kb < C / 32; ++kb) ob[kb] = parts_of<T, 1>(d_o[2 * kb], d_o[2 * kb + 1]);
+        f32x4 z[NB];
+#pragma unroll
+        for (int mt = 0; mt < NB; ++mt) {
+            f32x4 acc = {};
+#pragma unroll
+            for (int kb = 0; kb < DK / 32; ++kb) acc = mma(frag_acc(ks, LK, mt * 16, kb * 32, lane), db[kb], acc);
+#pragma unroll
+            for (int r = 0; r < 4; ++r) acc[r] *= gate[C + mt * 16 + gq * 4 + r];
+#pragma unroll
+            for (int kb = mt / 2; kb < C / 32; ++kb) acc = mma(parts_acc<NF>(ps, C * LC, LC, mt * 16, kb * 32, lane), ob[kb], acc);
+            z[mt] = acc;
+        }
+        Parts<T, NF> ub[C / 32];
+#pragma unroll
+        for (int kb = 0; kb < C / 32; ++kb) ub[kb] = parts_of<T, NF>(z[2 * kb], z[2 * kb + 1]);
+        T* wz = static_cast<T*>(p.w_z) + at * NF * C * p.dv_pad + col;
+        T* dv0 = static_cast<T*>(p.dv.data) + row0 * p.dv.ts + h * p.dv.hs + col;
+#pragma unroll
+        for (int mt = 0; mt < NB; ++mt) {
+            f32x4 acc = {};
+#pragma unroll
+            for (int kb = mt / 2; kb < C / 32; ++kb) acc = mma(parts_acc<NF>(ts, C * LC, LC, mt * 16, kb * 32, lane), ub[kb], acc);
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const int row = mt * 16 + gq * 4 + r;
+                if (held) store_parts<NF>(wz + row * p.dv_pad, C * p.dv_pad, acc[r]);
+                const float dx = gate[2 * C + row] * acc[r];
+                if (mine && row < rows) dv0[row * p.dv.ts] = (T)dx;
+                z[mt][r] = -gate[row] * dx;
+                d_o[mt][r] *= p.scale * gate[row];
+            }
+        }
+        Parts<T, 1> xb[C / 32];
+        Parts<T, NF> eb[C / 32];
+#pragma unroll
+        for (int kb = 0; kb < C / 32; ++kb) {
+            xb[kb] = parts_of<T, 1>(z[2 * kb], z[2 * kb + 1]);
+            eb[kb] = parts_of<T, NF>(d_o[2 * kb], d_o[2 * kb + 1]);
+        }
+        const float keep = gate[C - 1];
+#pragma unroll
+        for (int t = 0; t < DK / 16; ++t) {
+#pragma unroll
+            for (int r = 0; r < 4; ++r) ds[t][r] *= keep;
+#pragma unroll
+            for (int kb = 0; kb < C / 32; ++kb) {
+                ds[t] = mma(frag_tr(qs, LK, kb * 32, t * 16, lane), eb[kb], ds[t]);
+                ds[t] = mma(frag_tr(ks, LK, kb * 32, t * 16, lane), xb[kb], ds[t]);
+            }
+        }
+        __syncthreads();
+    }
+    if (p.d_initial != nullptr && mine) {
+        T* di = static_cast<T*>(p.d_initial);
+#pragma unroll
+        for (int t = 0; t < DK / 16; ++t)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const int row = t * 16 + gq * 4 + r;
+                if (row < p.dim_k) di[state_at + (int64_t)row * p.dim_v] = (T)ds[t][r];
+            }
+    }
+}
+
+// ---- the gradients of q, k and the gates ------------------------------------
+//
+// Every chunk by itself, from the states, U', Z and dS' of the two scans:
+//   dP = tril(dO U'^T) B                      M = -tril(Z U'^T, -1) B
+//   W1 = scale D o dP                         W2 = B (D o M)
+//   dQ = W1 K + scale diag(e^G) dO S^T
+//   dK = W1^T Q + (W2 + W2^T) K + diag(e^(G_C - G)) B U' dS'^T - diag(e^G) B Z S^T
+//   dbeta_i = Z_i . U'_i
+//   N = W1 o Q K^T + W2 o K K^T
+//   dG_i = sum_j (N_ij - N_ji) + (scale e^G dO S^T)_i . q_i - (e^G B Z S^T)_i . k_i - w_i,
+//          w_i = (e^(G_C - G) B U' dS'^T)_i . k_i;   dG_C also gets sum w + e^(G_C) <S, dS'>
+//   dg_t = sum of dG_i from t to the chunk's end
+// One workgroup for each (chunk slot, query/key head), wave w the tokens
+// 16 w .. 16 w + 15; the value heads that share the key head in turn, so that
+// their sums need no atomics and have one order.
+
+template <class T, int DK>
+constexpr size_t grad_lds_bytes()
+{
+    constexpr int C = kChunk<T>;
+    return 2 * (size_t)C * lds_stride<T>(DK) * sizeof(T) + 2 * kFine<T> * (size_t)C * lds_stride<T>(C) * sizeof(T) +
+           (size_t)C * sizeof(double) + (6 * C + C / 16 * C + 16) * sizeof(float);
+}
+
+template <class T>
+__device__ __forceinline__ Vec8<T> frag_global(const T* base, int64_t ld, int r0, int c0, int lane)
+{
+    const T* p = base + (int64_t)(r0 + (lane & 15)) * ld + c0 + (lane >> 4) * 8;
+    if constexpr (sizeof(T) == 2) {
+        return *reinterpret_cast<const Vec8<T>*>(p);
+    } else {
+        const Vec4<T> a = *reinterpret_cast<const Vec4<T>*>(p), b = *reinterpret_cast<const Vec4<T>*>(p + 4);
+        return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
+    }
+}
+template <int NP, class T>
+__device__ __forceinline__ Parts<T, NP> parts_global(const T* base, int64_t step, int64_t ld, int r0, int c0, int lane)
+{
+    Parts<T, NP> a;
+#pragma unroll
+    for (int n = 0; n < NP; ++n) a.p[n] = frag_global(base + n * step, ld, r0, c0, lane);
+    return a;
+}
+// The same from a caller's array: zero outside rows x cols, and element by
+// element where 16-byte reads are not possible.
+template <class T>
+__device__ __forceinline__ Vec8<T> frag_user(const T* base, int64_t ld, int r0, int c0, int rows, int cols, bool vec,
+                                             int lane)
+{
+    const int r = r0 + (lane & 15), c = c0 + (lane >> 4) * 8;
+    Vec8<T> x = {};
+    if (r < rows) {
+        if (vec && c + 8 <= cols) return frag_global(base, ld, r0, c0, lane);
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            if (c + j < cols) x[j] = base[(int64_t)r * ld + c + j];
+    }
+    return x;
+}
+
+__device__ __forceinline__ float sum16(float x)      // over the 16 lanes of a group
+{
+#pragma unroll
+    for (int d = 1; d < 16; d *= 2) x += __shfl_xor(x, d, 64);
+    return x;
+}
+__device__ __forceinline__ float sum_groups(float x) // over the 4 groups
+{
+    x += __shfl_xor(x, 16, 64);
+    return x + __shfl_xor(x, 32, 64);
+}
+
+template <class T, int DK>
+__global__ __launch_bounds__(kChunk<T> * 4) void k_delta_grad(DeltaParams p)
+{
+    constexpr int C = kChunk<T>, THREADS = C * 4, NB = C / 16, NW = THREADS / 64, LK = lds_stride<T>(DK),
+                  LC = lds_stride<T>(C), NK = DK / 16, NF = kFine<T>;
+    extern __shared__ __attribute__((aligned(16))) char smem[];
+    double* total = reinterpret_cast<double*>(smem);
+    T* ks = reinterpret_cast<T*>(total + C);
+    T* qs = ks + C * LK;
+    T* w1 = qs + C * LK;
+    T* w2 = w1 + NF * C * LC;
+    float* gate = reinterpret_cast<float*>(w2 + NF * C * LC);     // e^G, e^(G_C - G), beta
+    float* row_part = gate + 3 * C;                          // dG without column sums and w
+    float* row_w = row_part + C;                             // w
+    float* d_beta = row_w + C;
+    float* col_part = d_beta + C;                            // [NW][C] column sums of N
+    float* inner = col_part + NB * C;                        // [NW] parts of <S, dS'>
+
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, gq = lane >> 4, lr = lane & 15;
+    const int64_t slot = blockIdx.x / p.heads_qk;
+    const int hk = blockIdx.x % p.heads_qk, share = p.heads_v / p.heads_qk;
+    const SlotInfo info = slot_info<C>(p.offsets, p.tokens, p.n_seqs, slot);
+    if (info.rows == 0) return;
+    const int rows = info.rows;
+    stage_tile<T, THREADS>(ks, LK, static_cast<const T*>(p.k.data) + info.row * p.k.ts + hk * p.k.hs, p.k.ts, rows,
+                           p.dim_k, C, DK, p.vec, tid);
+    stage_tile<T, THREADS>(qs, LK, static_cast<const T*>(p.q.data) + info.row * p.q.ts + hk * p.q.hs, p.q.ts, rows,
+                           p.dim_k, C, DK, p.vec, tid);
+    __syncthreads();
+    f32x4 dq[NK] = {}, dk[NK] = {};
+
+    for (int m = 0; m < share; ++m) {
+        const int h = hk * share + m;
+        const int64_t at = slot * p.heads_v + h;
+        for (int i = tid; i < 3 * C; i += THREADS) gate[i] = p.w_gate[at * 3 * C + i];
+        if (wave == 0) {
+            const float g = lane < rows && p.g.data ? clamp_decay(load_gate(p.g, info.row + lane, h, p.g_dtype)) : 0.f;
+            const double t = scan_decays<C>((double)g, lane);
+            if (lane < C) total[lane] = t;
+        }
+        __syncthreads();
+
+        const T* d_o = static_cast<const T*>(p.d_out.data) + info.row * p.d_out.ts + h * p.d_out.hs;
+        const T* ws = static_cast<const T*>(p.w_s) + at * DK * p.dv_pad;
+        const T* wds = static_cast<const T*>(p.w_ds) + at * DK * p.dv_pad;
+        const T* wu = static_cast<const T*>(p.w_u) + at * NF * C * p.dv_pad;
+        const T* wz = static_cast<const T*>(p.w_z) + at * NF * C * p.dv_pad;
+        f32x4 dp[NB] = {}, zu[NB] = {}, os[NK] = {}, zs[NK] = {}, us[NK] = {};
+        float zdotu = 0.f, sds = 0.f;
+        for (int c = 0; c < p.dv_pad; c += 32) {
+            const Vec8<T> ao = frag_user(d_o, p.d_out.ts, wave * 16, c, rows, p.dim_v, p.vec, lane);
+            const Parts<T, NF> az = parts_global<NF>(wz, C * p.dv_pad, p.dv_pad, wave * 16, c, lane);
+            const Parts<T, NF> au = parts_global<NF>(wu, C * p.dv_pad, p.dv_pad, wave * 16, c, lane);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                float z = 0.f, u = 0.f;
+#pragma unroll
+                for (int n = NF - 1; n >= 0; --n) {
+                    z += (float)az.p[n][j];
+                    u += (float)au.p[n][j];
+                }
+                zdotu += z * u;
+            }
+#pragma unroll
+            for (int nt = 0; nt < NB; ++nt)
+                if (nt <= wave) {
+                    const Parts<T, NF> b = parts_global<NF>(wu, C * p.dv_pad, p.dv_pad, nt * 16, c, lane);
+                    dp[nt] = mma(ao, b, dp[nt]);
+                    zu[nt] = mma(az, b, zu[nt]);
+                }
+#pragma unroll
+            for (int t = 0; t < NK; ++t) {
+                const Vec8<T> b = frag_global(ws, p.dv_pad, t * 16, c, lane);
+                const Vec8<T> d = frag_global(wds, p.dv_pad, t * 16, c, lane);
+                os[t] = mma(ao, b, os[t]);
+                zs[t] = mma(az.p[0], b, zs[t]);
+                us[t] = mma(au, Parts<T, 1>{{d}}, us[t]);
+                if (t % NW == wave)
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) sds += (float)b[j] * (float)d[j];
+            }
+        }
+        zdotu = sum_groups(zdotu);               // lane: row lr of the wave's 16
+        if (gq == 0) d_beta[wave * 16 + lr] = zdotu;
+        sds = sum_groups(sum16(sds));
+        if (lane == 0) inner[wave] = sds;
+
+        // W1, W2 and N; Q K^T and K K^T once more
+        float nrow[4] = {};
+#pragma unroll
+        for (int nt = 0; nt < NB; ++nt) {
+            const int j = nt * 16 + lr;
+            float ncol = 0.f;
+            f32x4 kk = {}, qk = {};
+            if (nt <= wave) {
+#pragma unroll
+                for (int kb = 0; kb < DK; kb += 32) {
+                    const Vec8<T> b = frag_nat(ks, LK, nt * 16, kb, lane);
+                    kk = mma(frag_nat(ks, LK, wave * 16, kb, lane), b, kk);
+                    qk = mma(frag_nat(qs, LK, wave * 16, kb, lane), b, qk);
+                }
+            }
+            const float bj = gate[2 * C + j];
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const int i = wave * 16 + gq * 4 + r;
+                const float d = i >= j ? expf((float)(total[i] - total[j])) : 0.f;
+                const float a = i >= j ? p.scale * d * bj * dp[nt][r] : 0.f;
+                const float b = i > j ? -gate[2 * C + i] * d * bj * zu[nt][r] : 0.f;
+                store_parts<NF>(w1 + i * LC + j, C * LC, a);
+                store_parts<NF>(w2 + i * LC + j, C * LC, b);
+                const float n = i > j ? a * qk[r] + b * kk[r] : 0.f;     // N_ii cancels in dG
+                nrow[r] += n;
+                ncol += n;
+            }
+            ncol = sum_groups(ncol);
+            if (gq == 0) col_part[wave * C + j] = ncol;
+        }
+        __syncthreads();
+
+        // the products with S, and their shares of dG
+        float grow[4] = {}, gw[4] = {};
+#pragma unroll
+        for (int t = 0; t < NK; ++t)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const int i = wave * 16 + gq * 4 + r;
+                const float qv = (float)qs[i * LK + t * 16 + lr], kv = (float)ks[i * LK + t * 16 + lr];
+                const float b = gate[2 * C + i];
+                const float a1 = p.scale * gate[i] * os[t][r], a2 = gate[i] * b * zs[t][r];
+                const float a3 = gate[C + i] * b * us[t][r];
+                dq[t][r] += a1;
+                dk[t][r] += a3 - a2;
+                grow[r] += a1 * qv - a2 * kv;
+                gw[r] += a3 * kv;
+            }
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            const float a = sum16(grow[r] + nrow[r]), b = sum16(gw[r]);
+            if (lr == 0) {
+                row_part[wave * 16 + gq * 4 + r] = a;
+                row_w[wave * 16 + gq * 4 + r] = b;
+            }
+        }
+        // the products with K and Q: rows i of W1 and W2 for dQ and dK, columns for dK
+#pragma unroll
+        for (int kb = 0; kb < C / 32; ++kb) {
+            const Parts<T, NF> a1 = parts_acc<NF>(w1, C * LC, LC, wave * 16, kb * 32, lane);
+            const Parts<T, NF> a2 = parts_acc<NF>(w2, C * LC, LC, wave * 16, kb * 32, lane);
+            const Parts<T, NF> b1 = parts_tr<NF>(w1, C * LC, LC, kb * 32, wave * 16, lane);
+            const Parts<T, NF> b2 = parts_tr<NF>(w2, C * LC, LC, kb * 32, wave * 16, lane);
+#pragma unroll
+            for (int t = 0; t < NK; ++t) {
+                const Parts<T, 1> kt = {{frag_tr(ks, LK, kb * 32, t * 16, lane)}};
+                const Parts<T, 1> qt = {{frag_tr(qs, LK, kb * 32, t * 16, lane)}};
+                dq[t] = mma(a1, kt, dq[t]);
+                dk[t] = mma(b1, qt, dk[t]);
+                dk[t] = mma(a2, kt, dk[t]);
+                dk[t] = mma(b2, kt, dk[t]);
+            }
+        }
+        __syncthreads();
+        if (wave == 0) {
+            float x = 0.f, w = 0.f;
+            if (lane < C) {
+                w = row_w[lane];
+                x = row_part[lane] - w;
+#pragma unroll
+                for (int i = 0; i < NW; ++i) x -= col_part[i * C + lane];
+            }
+            float wsum = sum_groups(sum16(w)), in = 0.f;
+#pragma unroll
+            for (int i = 0; i < NW; ++i) in += inner[i];
+            if (lane == C - 1) x += wsum + gate[C - 1] * in;
+            // sums from each token to the chunk's end
+#pragma unroll
+            for (int d = 1; d < C; d *= 2) {
+                const float o = __shfl_down(x, d, 64);
+                if (lane + d < C) x += o;
+            }
+            if (lane < rows) {
+                if (p.dg.data)
+                    static_cast<T*>(p.dg.data)[(info.row + lane) * p.dg.ts + h * p.dg.hs] = (T)x;
+                static_cast<T*>(p.dbeta.data)[(info.row + lane) * p.dbeta.ts + h * p.dbeta.hs] = (T)d_beta[lane];
+            }
+        }
+        __syncthreads();
+    }
+    T* q0 = static_cast<T*>(p.dq.data) + info.row * p.dq.ts + hk * p.dq.hs;
+    T* k0 = static_cast<T*>(p.dk.data) + info.row * p.dk.ts + hk * p.dk.hs;
+#pragma unroll
+    for (int t = 0; t < NK; ++t)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            const int i = wave * 16 + gq * 4 + r, c = t * 16 + lr;
+            if (i < rows && c < p.dim_k) {
+                q0[i * p.dq.ts + c] = (T)dq[t][r];
+                k0[i * p.dk.ts + c] = (T)dk[t][r];
+            }
+        }
+}
+
+// ---- launches --------------------------------------------------------------
+
+template <class K>
+hipError_t launch_lds(K kernel, uint64_t blocks, int threads, size_t lds, const DeltaParams& p, hipStream_t stream)
+{
+    // more than 64 KiB of LDS has to be asked for, on the current device
+    if (lds > 64 * 1024) {
+        const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(kernel),
+                                                 hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
+        if (e != hipSuccess) return e;
+    }
+    kernel<<<dim3((uint32_t)blocks), dim3((uint32_t)threads), lds, stream>>>(p);
+    return hipGetLastError();
+}
+
+inline uint64_t scan_blocks(const DeltaParams& p, int waves)
+{
+    const uint64_t parts = ((uint64_t)p.dim_v + waves * 16 - 1) / (waves * 16);
+    const uint64_t groups = ((uint64_t)p.n_seqs * p.heads_v + 7) / 8 * 8;
+    return groups * parts;
+}
+
+template <class T, int DK, int NP>
+hipError_t forward_dk(const DeltaParams& p, hipStream_t stream)
+{
+    constexpr int C = kChunk<T>, NW = 4;
+    hipError_t e = launch_lds(k_delta_prep<T, DK, NP, false>, (uint64_t)p.n_slots * p.heads_v, C * 4,
+                              prep_lds_bytes<T, DK>(), p, stream);
+    if (e != hipSuccess) return e;
+    return launch_lds(k_delta_scan<T, DK, NP, false, NW>, scan_blocks(p, NW), NW * 64, scan_lds_bytes<T, DK, NP, false>(),
+                      p, stream);
+}
+template <class T, int NP>
+hipError_t forward_type(const DeltaParams& p, hipStream_t stream)
+{
+    switch (delta_padded_k(p.dim_k)) {
+    case 64: return forward_dk<T, 64, NP>(p, stream);
+    case 128: return forward_dk<T, 128, NP>(p, stream);
+    default: return forward_dk<T, 256, NP>(p, stream);
+    }
+}
+
+template <class T, int DK>
+hipError_t backward_dk(const DeltaParams& p, hipStream_t stream)
+{
+    constexpr int C = kChunk<T>, NW = 4;
+    hipError_t e = launch_lds(k_delta_prep<T, DK, 1, true>, (uint64_t)p.n_slots * p.heads_v, C * 4,
+                              prep_lds_bytes<T, DK>(), p, stream);
+    if (e != hipSuccess) return e;
+    e = launch_lds(k_delta_scan<T, DK, 1, true, NW>, scan_blocks(p, NW), NW * 64, scan_lds_bytes<T, DK, 1, true>(), p,
+                   stream);
+    if (e != hipSuccess) return e;
+    e = launch_lds(k_delta_scan_back<T, DK, NW>, scan_blocks(p, NW), NW * 64, scan_back_lds_bytes<T, DK>(), p, stream);
+    if (e != hipSuccess) return e;
+    return launch_lds(k_delta_grad<T, DK>, (uint64_t)p.n_slots * p.heads_qk, C * 4, grad_lds_bytes<T, DK>(), p, stream);
+}
+template <class T>
+hipError_t backward_type(const DeltaParams& p, hipStream_t stream)
+{
+    switch (delta_padded_k(p.dim_k)) {
+    case 64: return backward_dk<T, 64>(p, stream);
+    case 128: return backward_dk<T, 128>(p, stream);
+    default: return backward_dk<T, 256>(p, stream);
+    }
+}
+
+}  // namespace dws

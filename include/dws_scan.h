@@ -96,7 +96,10 @@ typedef enum dws_dtype {
      * section A4, data types) and {uint32, uint32}; first component at the
      * lower address */
     DWS_PAIR_I32_F32 = 3,
-    DWS_PAIR_U32 = 4
+    DWS_PAIR_U32 = 4,
+    /* 16-bit floats: the delta rule only */
+    DWS_FLOAT16 = 5,
+    DWS_BFLOAT16 = 6
 } dws_dtype;
 
 /* Largest supported element count (2^35). */
@@ -507,6 +510,121 @@ dws_status dws_scan_op_seeded(const void* d_in, void* d_out, size_t n, dws_dtype
  */
 dws_status dws_reduce_op(const void* d_in, size_t n, dws_dtype dtype, dws_op op, void* d_total,
                          hipStream_t stream);
+
+/* ---- the gated delta rule: a scan of matrix-valued affine maps ------------
+ *
+ * For each sequence and value head, with S the (dim_k x dim_v) fp32 state, k_t,
+ * q_t of the query/key head that the value head shares, and t the tokens in
+ * order:
+ *   S'  = exp(g_t) S
+ *   u_t = beta_t (v_t - S'^T k_t)
+ *   S   = S' + k_t u_t^T
+ *   o_t = scale S^T q_t
+ * S -> exp(g)(I - beta k k^T) S + beta k v^T is an affine map of S, so this is
+ * the inclusive scan of such maps applied to a first state, as DWS_OP_AFFINE is
+ * for scalars; dws_delta_rule cuts the sequence into chunks and carries the
+ * state from chunk to chunk, dws_delta_rule_step goes token by token.
+ */
+
+/* A (tokens, heads, dim) array on the device: element (t, h, d) is at
+ * t * token_stride + h * head_stride + d (strides in elements, not negative,
+ * below 2^40). Inputs may repeat elements (a stride of 0); outputs may not. */
+typedef struct dws_rows {
+    void* data;
+    long long token_stride;
+    long long head_stride;
+} dws_rows;
+
+/*
+ * Arguments of the delta-rule calls; set unused members to 0.
+ *
+ * Sequences: the rows (tokens) of all arrays hold n_seqs sequences one after
+ * another. d_offsets (DEVICE, n_seqs + 1 int64, 8-byte aligned) gives sequence
+ * i the rows d_offsets[i] .. d_offsets[i+1] - 1; NULL means tokens / n_seqs rows
+ * each. Rows in no sequence are not read. Offsets must not decrease; whatever
+ * they hold, nothing outside the arrays is touched.
+ *
+ * dtype (DWS_FLOAT32, DWS_FLOAT16 or DWS_BFLOAT16) is that of q, k, v, out and
+ * of every gradient. g (the natural logarithm of the decay; -infinity forgets
+ * the state; data == NULL for no decay) and beta have dtypes of their own among
+ * the three. dim_k and dim_v are at most 256; heads_v is a multiple of heads_qk,
+ * and value head h uses query/key head h / (heads_v / heads_qk).
+ *
+ * States are fp32, (count, heads_v, dim_k, dim_v), contiguous. Without d_slots
+ * count is n_seqs; with it (DEVICE, n_seqs int32) count is n_states and sequence
+ * i uses state d_slots[i]. A sequence whose slot is negative, n_states or more,
+ * or named by an earlier sequence of the call is left out: its rows of out and
+ * the states stay as they were.
+ *
+ * With DWS_FLOAT16 the operands of the matrix products, states among them, are
+ * rounded to fp16 and must stay below 65504.
+ */
+typedef struct dws_delta_rule_args {
+    long long tokens, n_seqs;
+    const long long* d_offsets;
+    int heads_qk, heads_v, dim_k, dim_v;
+    int dtype, g_dtype, beta_dtype;     /* dws_dtype */
+    float scale;
+    dws_rows q, k, v;                   /* dim: dim_k, dim_k, dim_v */
+    dws_rows g, beta;                   /* dim: 1 */
+    dws_rows out;                       /* dim: dim_v */
+    const float* d_initial_state;       /* NULL: zero */
+    float* d_final_state;               /* NULL: not wanted; may be d_initial_state */
+    const int* d_slots;
+    long long n_states;
+    /* dws_delta_rule_backward only */
+    dws_rows out_grad;                  /* in */
+    const float* d_final_grad;          /* in; NULL: zero */
+    dws_rows q_grad, k_grad, v_grad, g_grad, beta_grad;   /* out; g_grad.data may be NULL */
+    void* d_initial_grad;               /* out, dtype; NULL: not wanted */
+    /* != 0: rows of out (of the gradients) behind the last sequence become 0
+     * instead of staying as they were */
+    int zero_tail;
+    void* d_workspace;                  /* DEVICE, 256-byte aligned */
+    size_t workspace_bytes;
+} dws_delta_rule_args;
+
+/* Bytes of workspace that dws_delta_rule (backward == 0) or
+ * dws_delta_rule_backward needs for these sizes, types and this choice of
+ * d_final_state (host only, no HIP call). The workspace is the caller's, not the
+ * stream's, since it grows with the tokens; it holds nothing between calls, and
+ * calls that may run at the same time, replays of captured graphs among them,
+ * need one each. */
+dws_status dws_delta_rule_workspace(const dws_delta_rule_args* args, int backward, size_t* bytes);
+
+/*
+ * Whole sequences, in chunks on the matrix cores. With 16-bit inputs the fp32
+ * operands of the products are split into 16-bit parts: where the state is
+ * wanted (d_final_state) as many as give it fp32 accuracy, else as many as keep
+ * an output's error near that of rounding it to dtype. Errors,
+ * checked before any HIP call: NULL args, a required pointer that is NULL, sizes,
+ * strides or types out of range, heads_v not a multiple of heads_qk, tokens not
+ * a multiple of n_seqs without d_offsets, a workspace that is too small, or an
+ * output that names an element twice give DWS_ERR_INVALID_ARG; a dimension above
+ * 256 or more chunks and heads than a launch holds, DWS_ERR_UNSUPPORTED; a
+ * pointer not aligned to its element, DWS_ERR_MISALIGNED; an output or the
+ * workspace whose range meets another operand's, DWS_ERR_OVERLAP. Asynchronous on
+ * `stream`, allocates nothing, may be captured.
+ */
+dws_status dws_delta_rule(const dws_delta_rule_args* args, hipStream_t stream);
+
+/*
+ * Gradients of a sum of out . out_grad + final_state . d_final_grad with respect
+ * to q, k, v, g, beta and the initial state (d_slots must be NULL, else
+ * DWS_ERR_UNSUPPORTED; out and d_final_state are not used). The states of the
+ * forward pass are computed again. Query and key gradients are summed over the
+ * value heads that share them in one fixed order. Sums are fp32; each gradient is
+ * rounded once, to dtype. Errors as dws_delta_rule.
+ */
+dws_status dws_delta_rule_backward(const dws_delta_rule_args* args, hipStream_t stream);
+
+/*
+ * A few more tokens for each sequence, token by token, in fp32 arithmetic: reads
+ * each state at d_final_state once, writes it back once, and writes out.
+ * d_initial_state must equal d_final_state. No workspace; sequences without
+ * tokens leave their state. Errors as dws_delta_rule.
+ */
+dws_status dws_delta_rule_step(const dws_delta_rule_args* args, hipStream_t stream);
 
 /* Human-readable name of a status code (static string, never NULL). */
 const char* dws_status_string(dws_status status);

@@ -1,0 +1,428 @@
+"""The gated delta rule on the GPU against its token-by-token definition in 64 bits."""
+import pytest
+import torch
+
+import device_wide_prefix_amd as dws
+from delta_reference import close, inputs, reference, tolerance
+from gpu_util import note
+
+pytestmark = pytest.mark.gpu
+BF16, FP16, FP32 = torch.bfloat16, torch.float16, torch.float32
+NAMES = ("q", "k", "v", "g", "beta")
+
+
+def forward(x, offsets, initial, scale=None, **more):
+    out = dws.delta_rule(*(x[a] for a in NAMES), offsets=offsets, initial_state=initial, scale=scale, **more)
+    torch.cuda.synchronize()
+    return out
+
+
+def gradients(x, offsets, initial, scale, d_out, d_final):
+    """The reference's gradients, by differentiating it."""
+    leaves = {a: x[a].double().cpu().requires_grad_() for a in NAMES if x[a] is not None}
+    s = None if initial is None else initial.double().cpu().requires_grad_()
+    o, f = reference(leaves["q"], leaves["k"], leaves["v"], leaves.get("g"), leaves["beta"], offsets.tolist(), s, scale)
+    loss = (o * d_out.double().cpu()).sum()
+    if d_final is not None:
+        loss = loss + (f * d_final.double().cpu()).sum()
+    wanted = [leaves[a] for a in NAMES if a in leaves] + ([s] if s is not None else [])
+    got = list(torch.autograd.grad(loss, wanted, allow_unused=True))
+    got = [torch.zeros_like(w) if y is None else y for y, w in zip(got, wanted)]
+    if "g" not in leaves:
+        got.insert(3, None)
+    return got + ([None] if s is None else [])
+
+
+# lens, heads_qk, heads_v, dim_k, dim_v, initial state
+SHAPES = [
+    ([1], 1, 1, 1, 1, True),
+    ([31], 1, 1, 64, 64, False),
+    ([32], 1, 2, 64, 16, True),
+    ([33, 1, 0, 2], 1, 1, 8, 8, True),
+    ([63, 64, 65], 2, 2, 64, 64, False),
+    ([0, 129, 0], 2, 6, 40, 24, True),
+    ([127, 128], 1, 1, 65, 17, True),
+    ([200], 1, 1, 128, 128, True),
+    ([97, 70], 3, 3, 100, 130, False),
+    ([130], 1, 2, 256, 256, True),
+    ([70, 3], 1, 1, 129, 255, True),
+]
+
+
+@pytest.mark.parametrize("dtype", [FP32, BF16, FP16])
+@pytest.mark.parametrize("lens,hk,hv,dk,dv,init", SHAPES)
+def test_forward(gpu, lens, hk, hv, dk, dv, init, dtype):
+    note(f"delta forward {lens} {hk} {hv} {dk} {dv} {init} {dtype}")
+    x, offsets, initial = inputs(1, lens, hk, hv, dk, dv, dtype, init=init)
+    want, final = reference(*(x[a] for a in NAMES), offsets.tolist(), None if initial is None else initial.double().cpu(), dk ** -0.5)
+    close(forward(x, offsets, initial), want, dtype, "out")
+    out, state = forward(x, offsets, initial, final_state=True)
+    close(out, want, dtype, "out")
+    close(state, final, dtype, "state")
+
+
+@pytest.mark.parametrize("dtype", [FP32, BF16, FP16])
+@pytest.mark.parametrize("lens,hk,hv,dk,dv,init", SHAPES)
+def test_backward(gpu, lens, hk, hv, dk, dv, init, dtype):
+    note(f"delta backward {lens} {hk} {hv} {dk} {dv} {init} {dtype}")
+    x, offsets, initial = inputs(2, lens, hk, hv, dk, dv, dtype, init=init)
+    gen = torch.Generator().manual_seed(3)
+    d_out = torch.randn(x["v"].shape, generator=gen).to(dtype).cuda()
+    d_final = 0.3 * torch.randn(len(lens), hv, dk, dv, generator=gen).cuda() if init else None
+    got = dws.delta_rule_backward(d_out, *(x[a] for a in NAMES), offsets=offsets, initial_state=initial, d_final_state=d_final)
+    torch.cuda.synchronize()
+    want = gradients(x, offsets, initial, dk ** -0.5, d_out, d_final)
+    for what, a, b in zip(("dq", "dk", "dv", "dg", "dbeta", "d_initial"), got, want):
+        assert (a is None) == (b is None)
+        if a is not None:
+            assert a.dtype == dtype
+            close(a, b, dtype, what)
+
+
+@pytest.mark.parametrize("gates", [(FP32, FP32), (BF16, BF16), (FP16, FP32), (FP32, FP16)])
+def test_gate_types(gpu, gates):
+    x, offsets, initial = inputs(4, [70, 40], 1, 2, 64, 32, BF16, gates=gates)
+    want, final = reference(*(x[a] for a in NAMES), offsets.tolist(), initial.double().cpu(), 0.5)
+    out, state = forward(x, offsets, initial, scale=0.5, final_state=True)
+    close(out, want, BF16, "out")
+    close(state, final, BF16, "state")
+    pool = initial.clone()
+    close(dws.delta_rule_step(*(x[a] for a in NAMES), pool, offsets=offsets, scale=0.5), want, BF16, "out")
+    close(pool, final, FP32, "state")
+
+
+@pytest.mark.parametrize("dtype", [FP32, BF16])
+def test_no_decay(gpu, dtype):
+    x, offsets, initial = inputs(5, [150], 1, 1, 64, 48, dtype)
+    x["g"] = None
+    want, final = reference(*(x[a] for a in NAMES), offsets.tolist(), initial.double().cpu(), 0.125)
+    out, state = forward(x, offsets, initial, final_state=True)
+    close(out, want, dtype, "out")
+    close(state, final, dtype, "state")
+    d_out = torch.ones_like(x["v"])
+    got = dws.delta_rule_backward(d_out, *(x[a] for a in NAMES), offsets=offsets, initial_state=initial)
+    want = gradients(x, offsets, initial, 0.125, d_out, None)
+    assert got[3] is None
+    for what, a, b in zip(("dq", "dk", "dv", "dg", "dbeta", "d_initial"), got, want):
+        if a is not None:
+            close(a, b, dtype, what)
+
+
+def special(kind, dtype, n=140, hv=2, dk=64, dv=32):
+    x, offsets, initial = inputs(6, [n], 1, hv, dk, dv, dtype)
+    if kind == "forget":                 # -infinity, and more than any sum of 64 decays
+        x["g"][5] = -float("inf")
+        x["g"][70:75] = -float("inf")
+        x["g"][20, 0] = -200.0
+        x["g"][100:, 1] = -1e30
+        x["g"][n - 1] = torch.finfo(FP32).min
+    elif kind == "long_decay":           # sums of hundreds whose differences are small
+        x["g"][:] = -60.0
+        x["g"][::3] = -1e-3
+    elif kind == "beta_zero":            # tokens that change nothing
+        x["beta"][::2] = 0
+        x["beta"][64:128] = 0
+    elif kind == "same_keys":            # every key alike: the system's powers grow, its inverse does not
+        x["k"][:] = x["k"][:1]
+        x["beta"][:] = 1
+        x["g"][:] = 0
+    elif kind == "growth":
+        x["g"][:] = 0.01
+    return x, offsets, initial
+
+
+@pytest.mark.parametrize("dtype", [FP32, BF16, FP16])
+@pytest.mark.parametrize("kind", ["forget", "long_decay", "beta_zero", "same_keys", "growth"])
+def test_special_gates(gpu, kind, dtype):
+    note(f"delta special {kind} {dtype}")
+    x, offsets, initial = special(kind, dtype)
+    want, final = reference(*(x[a] for a in NAMES), offsets.tolist(), initial.double().cpu(), 0.125)
+    out, state = forward(x, offsets, initial, final_state=True)
+    close(out, want, dtype, "out", kind)
+    close(state, final, dtype, "state", kind)
+    pool = initial.clone()
+    close(dws.delta_rule_step(*(x[a] for a in NAMES), pool, scale=0.125), want, dtype, "out", kind)
+    close(pool, final, FP32, "state", kind)
+    d_out = torch.randn(x["v"].shape, generator=torch.Generator().manual_seed(1)).to(dtype).cuda()
+    got = dws.delta_rule_backward(d_out, *(x[a] for a in NAMES), initial_state=initial, scale=0.125)
+    if kind == "forget":                 # exp's derivative at -infinity is 0, which autograd's 0 * inf is not
+        x["g"] = x["g"].clamp(min=-1e4)
+    want = gradients(x, offsets, initial, 0.125, d_out, None)
+    for what, a, b in zip(("dq", "dk", "dv", "dg", "dbeta", "d_initial"), got, want):
+        close(a, b, dtype, what, kind)
+
+
+@pytest.mark.parametrize("dtype", [FP32, BF16])
+def test_gradient_against_differences(gpu, dtype):
+    """The kernel's gradients along a direction against a central difference of the 64-bit definition. The difference's
+    own error is h^2 / 6 of the third derivative: below 1e-6 of it for h = 1e-3 at these sizes."""
+    x, offsets, initial = inputs(7, [75, 30], 1, 2, 32, 16, dtype)
+    gen = torch.Generator().manual_seed(8)
+    d_out = torch.randn(x["v"].shape, generator=gen).to(dtype).cuda()
+    d_final = torch.randn(initial.shape, generator=gen).cuda()
+    got = dws.delta_rule_backward(d_out, *(x[a] for a in NAMES), offsets=offsets, initial_state=initial, d_final_state=d_final)
+    base = {a: x[a].double().cpu() for a in NAMES}
+    base["s"] = initial.double().cpu()
+
+    def loss(y):
+        o, f = reference(*(y[a] for a in NAMES), offsets.tolist(), y["s"], 32 ** -0.5)
+        return ((o * d_out.double().cpu()).sum() + (f * d_final.double().cpu()).sum()).item()
+
+    h = 1e-3
+    for a, d in zip(NAMES + ("s",), got):
+        way = torch.randn(base[a].shape, generator=gen, dtype=torch.float64)
+        slope = (loss({**base, a: base[a] + h * way}) - loss({**base, a: base[a] - h * way})) / (2 * h)
+        mine = (d.double().cpu() * way).sum().item()
+        # an error of tolerance() of the gradient's norm, along a direction of norm sqrt(n) that knows nothing of it,
+        # five deviations far
+        allowed = 5 * tolerance(dtype, "d" + a) * d.double().norm().item() + 1e-5 * abs(slope) + 1e-6
+        assert abs(mine - slope) <= allowed, (a, mine, slope, allowed)
+
+
+@pytest.mark.parametrize("dtype", [FP32, BF16])
+def test_strides(gpu, dtype):
+    """Parts of one buffer, one element off 16-byte alignment, heads outermost, and repeated rows and heads."""
+    lens, hk, hv, dk, dv = [70, 33], 2, 4, 48, 40
+    x, offsets, initial = inputs(9, lens, hk, hv, dk, dv, dtype)
+    n = sum(lens)
+    plain = forward(x, offsets, initial)
+    d_out = torch.randn(n, hv, dv, generator=torch.Generator().manual_seed(2)).to(dtype).cuda()
+    plain_grads = dws.delta_rule_backward(d_out, *(x[a] for a in NAMES), offsets=offsets, initial_state=initial)
+    for shift in (0, 1):
+        fused = torch.zeros(n, 2 * hk * dk + hv * dv + 16 + shift, dtype=dtype, device="cuda")
+        y = dict(x)
+        at = shift
+        for a, h, d in (("q", hk, dk), ("k", hk, dk), ("v", hv, dv)):
+            y[a] = fused[:, at: at + h * d].unflatten(1, (h, d))
+            y[a].copy_(x[a])
+            at += h * d
+        for a in ("g", "beta"):
+            y[a] = x[a].t().contiguous().t()
+        assert torch.equal(forward(y, offsets, initial), plain)
+        d_view = torch.zeros(hv, n, dv + 3, dtype=dtype, device="cuda")[:, :, shift: shift + dv].transpose(0, 1)
+        d_view.copy_(d_out)
+        got = dws.delta_rule_backward(d_view, *(y[a] for a in NAMES), offsets=offsets, initial_state=initial)
+        for a, b in zip(got, plain_grads):
+            assert torch.equal(a, b)
+    y = {a: (x[a].transpose(0, 1).contiguous().transpose(0, 1) if x[a].dim() == 3 else x[a]) for a in NAMES}
+    out = torch.full((hv, n, dv), 7.0, dtype=dtype, device="cuda").transpose(0, 1)
+    assert forward(y, offsets, initial, out=out) is out
+    assert torch.equal(out, plain)
+    pool = initial.clone()
+    dws.delta_rule_step(*(y[a] for a in NAMES), pool, offsets=offsets, out=out)
+    close(out, plain, dtype, "dg")      # two results of the type, each off by its own tolerance
+    # one query and key for all heads and one v for all tokens, by strides of 0
+    y = dict(x)
+    y["q"], y["k"] = x["q"][:, :1].expand(n, hk, dk), x["k"][:, :1].expand(n, hk, dk)
+    y["v"] = x["v"][:1].expand(n, hv, dv)
+    whole = {a: b.contiguous() for a, b in y.items()}
+    assert torch.equal(forward(y, offsets, initial), forward(whole, offsets, initial))
+
+
+@pytest.mark.parametrize("dtype", [FP32, BF16])
+@pytest.mark.parametrize("tail", [1, 53, 130])
+def test_rows_behind_the_last_sequence(gpu, dtype, tail):
+    """They are not read, and stay as they were in a given output; in a new one, and in gradients, they are 0."""
+    x, offsets, initial = inputs(10, [10], 1, 2, 32, 24, dtype, tail=tail)
+    for a in NAMES:
+        x[a][10:] = float("nan")
+    want, final = reference(*(x[a][:10] for a in NAMES), [0, 10], initial.double().cpu(), 32 ** -0.5)
+    out = torch.full(x["v"].shape, 5.0, dtype=dtype, device="cuda")
+    _, state = forward(x, offsets, initial, out=out, final_state=True)
+    close(out[:10], want, dtype, "out")
+    close(state, final, dtype, "state")
+    assert (out[10:] == 5).all()
+    assert (forward(x, offsets, initial)[10:] == 0).all()
+    d_out = torch.full(x["v"].shape, float("nan"), dtype=dtype, device="cuda")
+    d_out[:10] = 1
+    got = dws.delta_rule_backward(d_out, *(x[a] for a in NAMES), offsets=offsets, initial_state=initial)
+    for a in got[:5]:
+        assert torch.isfinite(a).all() and (a[10:] == 0).all()
+    out.fill_(5)
+    pool = initial.clone()
+    dws.delta_rule_step(*(x[a] for a in NAMES), pool, offsets=offsets, out=out)
+    close(out[:10], want, dtype, "out")
+    assert (out[10:] == 5).all()
+
+
+def test_empty_calls(gpu):
+    x, offsets, initial = inputs(11, [0, 0], 1, 2, 32, 24, BF16)
+    out, state = forward(x, offsets, initial, final_state=True)
+    assert out.shape == (0, 2, 24) and torch.equal(state, initial)
+    got = dws.delta_rule_backward(torch.empty_like(x["v"]), *(x[a] for a in NAMES), offsets=offsets, initial_state=initial,
+                                  d_final_state=initial)
+    assert torch.equal(got[5], initial.to(BF16)) and got[0].numel() == 0
+    pool = initial.clone()
+    dws.delta_rule_step(*(x[a] for a in NAMES), pool)
+    assert torch.equal(pool, initial)
+
+
+def test_offsets_that_decrease_touch_nothing_outside(gpu):
+    """Wrong offsets give unspecified values, inside the arrays."""
+    x, _, initial = inputs(12, [200], 1, 2, 32, 24, BF16, init=False)
+    for bad in ([0, 300, 100, 200], [-50, 20, 10, 1 << 40], [200, 0, 200, 0]):
+        offsets = torch.tensor(bad, dtype=torch.int64, device="cuda")
+        guard = torch.full((600, 2, 24), 5.0, dtype=BF16, device="cuda")
+        out, state = forward(x, offsets, None, out=guard[200:400], final_state=True)
+        assert state.shape[0] == 3 and (guard[:200] == 5).all() and (guard[400:] == 5).all()
+        dws.delta_rule_backward(out.contiguous(), *(x[a] for a in NAMES), offsets=offsets)
+        torch.cuda.synchronize()
+
+
+STEPS = [(1, 1, 1, 1, 1, 1), (3, 1, 2, 4, 64, 64), (5, 2, 1, 3, 128, 128), (2, 7, 1, 1, 256, 255), (4, 3, 2, 2, 40, 100)]
+
+
+@pytest.mark.parametrize("dtype", [FP32, BF16, FP16])
+@pytest.mark.parametrize("n,tokens,hk,hv,dk,dv", [(n, t, hk, hk * r, dk, dv) for n, t, hk, r, dk, dv in STEPS])
+def test_step(gpu, n, tokens, hk, hv, dk, dv, dtype):
+    note(f"delta step {n} {tokens} {hk} {hv} {dk} {dv} {dtype}")
+    x, offsets, initial = inputs(13, [tokens] * n, hk, hv, dk, dv, dtype)
+    want, final = reference(*(x[a] for a in NAMES), offsets.tolist(), initial.double().cpu(), dk ** -0.5)
+    pool = torch.full((n + 3, hv, dk, dv), 9.0, device="cuda")
+    slots = torch.randperm(n + 3, generator=torch.Generator().manual_seed(1))[:n].to(torch.int32).cuda()
+    pool[slots.long()] = initial
+    out = dws.delta_rule_step(*(x[a] for a in NAMES), pool, slots=slots)
+    close(out, want, dtype, "out")
+    close(pool[slots.long()], final, FP32, "state")
+    rest = torch.ones(n + 3, dtype=torch.bool)
+    rest[slots.long().cpu()] = False
+    assert (pool[rest.cuda()] == 9).all()
+    again = initial.clone()
+    assert torch.equal(dws.delta_rule_step(*(x[a] for a in NAMES), again), out)
+    assert torch.equal(again, pool[slots.long()])
+
+
+@pytest.mark.parametrize("whole", [False, True])
+def test_slots_that_leave_sequences_out(gpu, whole):
+    """A slot below 0, outside the pool or named before: the sequence's rows and the states stay as they were."""
+    lens = [3, 2, 4, 1, 3, 2]
+    x, offsets, _ = inputs(14, lens, 1, 2, 32, 16, FP32)
+    slots = torch.tensor([4, -1, 2, 4, 7, 0], dtype=torch.int32, device="cuda")
+    pool = 0.3 * torch.randn(7, 2, 32, 16, device="cuda")
+    before = pool.clone()
+    out = torch.full(x["v"].shape, 3.0, device="cuda")
+    if whole:
+        dws.delta_rule(*(x[a] for a in NAMES), offsets=offsets, initial_state=pool, final_state=pool, slots=slots, out=out)
+    else:
+        dws.delta_rule_step(*(x[a] for a in NAMES), pool, slots=slots, offsets=offsets, out=out)
+    first = torch.zeros(6, 2, 32, 16, dtype=torch.float64)
+    taken = {0: 4, 2: 2, 5: 0}
+    for i, s in taken.items():
+        first[i] = before[s].double().cpu()
+    want, final = reference(*(x[a] for a in NAMES), offsets.tolist(), first, 32 ** -0.5)
+    ends = offsets.tolist()
+    for i in range(6):
+        rows = slice(ends[i], ends[i + 1])
+        if i in taken:
+            close(out[rows], want[rows], FP32, "out")
+            close(pool[taken[i]], final[i], FP32, "state")
+        else:
+            assert (out[rows] == 3).all()
+    for s in (1, 3, 5, 6):
+        assert torch.equal(pool[s], before[s])
+
+
+def test_prefill_then_steps(gpu):
+    """A prompt in two calls and tokens one by one, states in a pool, are the sequence in one."""
+    lens = [150, 97]
+    x, offsets, _ = inputs(15, lens, 2, 4, 64, 48, BF16, init=False)
+    want, final = reference(*(x[a] for a in NAMES), offsets.tolist(), None, 64 ** -0.5)
+    pool = torch.randn(5, 4, 64, 48, device="cuda")
+    slots = torch.tensor([3, 1], dtype=torch.int32, device="cuda")
+    cuts = [(0, 70), (70, 90)]
+    outs = [[], []]
+
+    def part(a, b):
+        rows = torch.cat([torch.arange(s + a, s + b) for s in (0, 150)]).cuda()
+        return {y: x[y][rows] for y in NAMES}, torch.tensor([0, b - a, 2 * (b - a)], device="cuda")
+
+    for i, (a, b) in enumerate(cuts):
+        y, off = part(a, b)
+        o, _ = dws.delta_rule(*(y[z] for z in NAMES), offsets=off, initial_state=pool if i else None, final_state=pool,
+                              slots=slots)
+        for s in range(2):
+            outs[s].append(o[s * (b - a):(s + 1) * (b - a)])
+    for t in range(90, 97):
+        y, off = part(t, t + 1)
+        o = dws.delta_rule_step(*(y[z] for z in NAMES), pool, slots=slots)
+        for s in range(2):
+            outs[s].append(o[s: s + 1])
+    for s, start in enumerate((0, 150)):
+        close(torch.cat(outs[s]), want[start: start + 97], BF16, "out")
+    _, final = reference(*(x[a] for a in NAMES), [0, 97], None, 64 ** -0.5)
+    close(pool[3], final[0], BF16, "state")
+
+
+def test_far_states(gpu):
+    """States whose place in the pool is beyond 2^32 bytes and 2^31 elements."""
+    hv, dk, dv = 1, 256, 256
+    count = (1 << 31) // (dk * dv) + 5
+    pool = torch.empty(count, hv, dk, dv, device="cuda")
+    x, offsets, initial = inputs(16, [3, 2], 1, hv, dk, dv, FP32)
+    slots = torch.tensor([count - 1, 2], dtype=torch.int32, device="cuda")
+    pool[slots.long()] = initial
+    want, final = reference(*(x[a] for a in NAMES), offsets.tolist(), initial.double().cpu(), 1 / 16)
+    close(dws.delta_rule_step(*(x[a] for a in NAMES), pool, slots=slots, offsets=offsets), want, FP32, "out")
+    close(pool[slots.long()], final, FP32, "state")
+    pool[slots.long()] = initial
+    out, _ = dws.delta_rule(*(x[a] for a in NAMES), offsets=offsets, initial_state=pool, final_state=pool, slots=slots)
+    close(out, want, FP32, "out")
+    close(pool[slots.long()], final, FP32, "state")
+
+
+def test_repeats_bit_for_bit(gpu):
+    x, offsets, initial = inputs(17, [500, 129], 2, 6, 64, 64, BF16)
+    d_out = torch.randn(x["v"].shape, generator=torch.Generator().manual_seed(2)).to(BF16).cuda()
+    first = None
+    for _ in range(4):
+        got = forward(x, offsets, initial, final_state=True)
+        got += dws.delta_rule_backward(d_out, *(x[a] for a in NAMES), offsets=offsets, initial_state=initial)
+        first = first or got
+        assert all(torch.equal(a, b) for a, b in zip(got, first))
+
+
+def test_graphs_and_streams(gpu):
+    """Each call captured once and replayed between eager calls and on its own beside them; two graphs and a stream at
+    once do not share memory."""
+    x, offsets, initial = inputs(18, [200, 65], 2, 4, 64, 64, BF16)
+    d_out = torch.randn(x["v"].shape, generator=torch.Generator().manual_seed(2)).to(BF16).cuda()
+    args = [x[a] for a in NAMES]
+
+    def everything(pool):
+        out, final = dws.delta_rule(*args, offsets=offsets, initial_state=initial, final_state=True)
+        grads = dws.delta_rule_backward(d_out, *args, offsets=offsets, initial_state=initial)
+        stepped = dws.delta_rule_step(*(y[:2] for y in args), pool)
+        return [out, final, *grads, stepped, pool]
+
+    want = [t.clone() for t in everything(initial.clone())]
+    torch.cuda.synchronize()
+    graphs = []
+    for _ in range(2):
+        pool = initial.clone()
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            got = everything(pool)
+        graphs.append((graph, got, pool))
+    side = torch.cuda.Stream()
+    for _ in range(3):
+        for _, got, pool in graphs:
+            for t in got:
+                t.zero_()
+            pool.copy_(initial)
+        torch.cuda.synchronize()
+        with torch.cuda.stream(side):
+            aside = everything(initial.clone())
+        for graph, _, _ in graphs:
+            graph.replay()
+        eager = everything(initial.clone())
+        torch.cuda.synchronize()
+        for got in (aside, eager, graphs[0][1], graphs[1][1]):
+            assert all(torch.equal(a, b) for a, b in zip(got, want))
+    # another stream by its handle: what the binding allocates belongs to that stream
+    for _ in range(3):
+        out, final = dws.delta_rule(*args, offsets=offsets, initial_state=initial, final_state=True,
+                                    stream=side.cuda_stream)
+        junk = [torch.full_like(out, 3.0) for _ in range(4)]
+        side.synchronize()
+        assert torch.equal(out, want[0]) and torch.equal(final, want[1]) and len(junk) == 4
