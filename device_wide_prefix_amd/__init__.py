@@ -14,6 +14,11 @@ fallback; if the library is not built, importing the binding's functions raises.
     scan_debug(x, out, tile_elems, ...)    -> descriptor words (numpy uint64)
     watchdog_trips()                       -> int
     selftest_wave(x)                       -> (incl, shift)
+    pages_grow(refs, table, lengths, rows, new_lengths, page_tokens) -> granted
+    pages_fork(refs, table, lengths, parents, children, page_tokens) -> (granted, src, dst, count)
+    pages_free(refs, table, lengths, rows, page_tokens) -> freed
+    pages_compact(refs, table)             -> (count, remap, src, dst, moves)
+    pages_copy(pool, src, dst, count=None, page_dim=0) -> pool
     delta_rule(q, k, v, g, beta, ...)      -> out or (out, final_state)
     delta_rule_backward(d_out, q, ...)     -> (dq, dk, dv, dg, dbeta, d_initial_state)
     delta_rule_step(q, k, v, g, beta, state, slots=None, ...) -> out (state updated)
@@ -52,6 +57,7 @@ EXPORTED_SYMBOLS = (
     "dws_run_length_encode", "dws_device_memory_info", "dws_scan_noalloc", "dws_scan_plan", "dws_scan_seeded",
     "dws_reduce", "dws_scan_op_seeded", "dws_reduce_op", "dws_select_if", "dws_partition_if",
     "dws_delta_rule_workspace", "dws_delta_rule", "dws_delta_rule_backward", "dws_delta_rule_step",
+    "dws_pages_workspace", "dws_pages_grow", "dws_pages_fork", "dws_pages_free", "dws_pages_compact", "dws_pages_copy",
 )
 
 
@@ -88,6 +94,13 @@ class DeltaRuleArgs(ctypes.Structure):
                 [(x, Rows) for x in ("q_grad", "k_grad", "v_grad", "g_grad", "beta_grad")] +
                 [("d_initial_grad", ctypes.c_void_p), ("zero_tail", ctypes.c_int), ("d_workspace", ctypes.c_void_p),
                  ("workspace_bytes", ctypes.c_size_t)])
+
+
+class PageCache(ctypes.Structure):
+    """dws_page_cache."""
+    _fields_ = [("d_refs", ctypes.c_void_p), ("n_pages", ctypes.c_longlong), ("d_table", ctypes.c_void_p),
+                ("n_rows", ctypes.c_longlong), ("max_pages", ctypes.c_longlong), ("d_lengths", ctypes.c_void_p),
+                ("page_tokens", ctypes.c_longlong)]
 
 
 _lib = None
@@ -166,6 +179,14 @@ def load_library():
     for name in ("dws_delta_rule", "dws_delta_rule_backward", "dws_delta_rule_step"):
         f = getattr(lib, name)
         f.argtypes = [ctypes.POINTER(DeltaRuleArgs), vp]
+        f.restype = ci
+    pc, ll = ctypes.POINTER(PageCache), ctypes.c_longlong
+    for name, args in (("workspace", [pc, ll, ctypes.POINTER(sz)]), ("grow", [pc, vp, vp, ll, vp, vp, sz, vp]),
+                       ("fork", [pc, vp, vp, ll, vp, vp, vp, vp, vp, sz, vp]), ("free", [pc, vp, ll, vp, vp, sz, vp]),
+                       ("compact", [pc, vp, vp, vp, vp, vp, vp, sz, vp]),
+                       ("copy", [vp, ll, ll, ll, ll, vp, vp, ll, vp, vp])):
+        f = getattr(lib, "dws_pages_" + name)
+        f.argtypes = args
         f.restype = ci
     lib.dws_selftest_wave.argtypes = [vp, vp, vp, sz, ci, vp]
     lib.dws_selftest_wave.restype = ci
@@ -767,6 +788,115 @@ def delta_rule_step(q, k, v, g, beta, state, slots=None, offsets=None, scale=Non
         a.out = _rows(out, "out", a.tokens, a.heads_v, a.dim_v, q.dtype, q.device)
         _check(load_library().dws_delta_rule_step(ctypes.byref(a), s), "dws_delta_rule_step")
     return out
+
+
+# ---- pages of a cache --------------------------------------------------------
+
+def _page_cache(refs, table, lengths=None, page_tokens=0) -> PageCache:
+    import torch
+    if not isinstance(refs, torch.Tensor) or not refs.is_cuda:
+        raise TypeError("refs must be a GPU tensor (there is no CPU path)")
+    c = PageCache(d_refs=_device_ints(refs, "refs", torch.int32, None, refs.device), n_pages=refs.numel(),
+                  page_tokens=int(page_tokens))
+    if not isinstance(table, torch.Tensor) or table.dtype != torch.int32 or table.dim() != 2 or \
+            table.device != refs.device or not table.is_contiguous():
+        raise ValueError(f"table must be a contiguous int32 tensor (rows, pages) on {refs.device}")
+    c.d_table, (c.n_rows, c.max_pages) = table.data_ptr(), table.shape
+    if lengths is not None:
+        c.d_lengths = _device_ints(lengths, "lengths", torch.int32, table.shape[0], refs.device)
+    return c
+
+
+def _page_workspace(c, n, device):
+    import torch
+    need = ctypes.c_size_t(0)
+    _check(load_library().dws_pages_workspace(ctypes.byref(c), n, ctypes.byref(need)), "dws_pages_workspace")
+    return torch.empty(need.value, dtype=torch.uint8, device=device)
+
+
+def _new_ints(n, like, dtype=None):
+    import torch
+    return torch.empty(n, dtype=dtype or torch.int32, device=like.device)
+
+
+def pages_grow(refs, table, lengths, rows, new_lengths, page_tokens, stream=None):
+    """Pages for ``rows`` to hold ``new_lengths`` tokens, lowest free page first (dws_pages_grow). refs (pages,), table
+    (rows, max_pages) and lengths (rows,) are int32 GPU tensors, updated in place. Returns an int32 tensor: 1 where
+    granted, 0 where the row stays as it was."""
+    import torch
+    c = _page_cache(refs, table, lengths, page_tokens)
+    n = rows.numel() if isinstance(rows, torch.Tensor) else 0
+    a, b = (_device_ints(t, w, torch.int32, n, refs.device) for t, w in ((rows, "rows"), (new_lengths, "new_lengths")))
+    with _on_stream(refs, stream) as s:
+        granted, work = _new_ints(n, refs), _page_workspace(c, n, refs.device)
+        _check(load_library().dws_pages_grow(ctypes.byref(c), a, b, n, granted.data_ptr(), work.data_ptr(), work.numel(), s),
+               "dws_pages_grow")
+    return granted
+
+
+def pages_fork(refs, table, lengths, parents, children, page_tokens, stream=None):
+    """Rows ``children`` (empty) with the tokens of rows ``parents``: whole pages shared, an unfinished last page new
+    (dws_pages_fork). Returns (granted, src, dst, count): the pages to copy are src[:count] to dst[:count], count an
+    int64 GPU tensor, for pages_copy on each pool."""
+    import torch
+    c = _page_cache(refs, table, lengths, page_tokens)
+    n = parents.numel() if isinstance(parents, torch.Tensor) else 0
+    a, b = (_device_ints(t, w, torch.int32, n, refs.device) for t, w in ((parents, "parents"), (children, "children")))
+    with _on_stream(refs, stream) as s:
+        granted, src, dst = (_new_ints(n, refs) for _ in range(3))
+        count, work = _new_ints(1, refs, torch.int64), _page_workspace(c, n, refs.device)
+        _check(load_library().dws_pages_fork(ctypes.byref(c), a, b, n, granted.data_ptr(), src.data_ptr(), dst.data_ptr(),
+                                             count.data_ptr(), work.data_ptr(), work.numel(), s), "dws_pages_fork")
+    return granted, src, dst, count
+
+
+def pages_free(refs, table, lengths, rows, page_tokens, stream=None):
+    """Empties ``rows`` (dws_pages_free). Returns the number of pages that became free, a one-element int64 GPU tensor."""
+    import torch
+    c = _page_cache(refs, table, lengths, page_tokens)
+    a = _device_ints(rows, "rows", torch.int32, None, refs.device)
+    n = rows.numel()
+    with _on_stream(refs, stream) as s:
+        freed, work = _new_ints(1, refs, torch.int64), _page_workspace(c, n, refs.device)
+        _check(load_library().dws_pages_free(ctypes.byref(c), a, n, freed.data_ptr(), work.data_ptr(), work.numel(), s),
+               "dws_pages_free")
+    return freed
+
+
+def pages_compact(refs, table, stream=None):
+    """Pages in use renumbered to the front, with the fewest moves (dws_pages_compact); refs and table are updated.
+    Returns (count, remap, src, dst, moves): pages in use, new number of each page (-1: free), and the pages to copy,
+    src[:moves] to dst[:moves], for pages_copy on each pool. count and moves are int64 GPU tensors."""
+    import torch
+    c = _page_cache(refs, table)
+    with _on_stream(refs, stream) as s:
+        remap, src, dst = (_new_ints(n, refs) for n in (c.n_pages, c.n_pages // 2, c.n_pages // 2))
+        moves, count = (_new_ints(1, refs, torch.int64) for _ in range(2))
+        work = _page_workspace(c, 0, refs.device)
+        _check(load_library().dws_pages_compact(ctypes.byref(c), remap.data_ptr(), src.data_ptr(), dst.data_ptr(),
+                                                moves.data_ptr(), count.data_ptr(), work.data_ptr(), work.numel(), s),
+               "dws_pages_compact")
+    return count, remap, src, dst, moves
+
+
+def pages_copy(pool, src, dst, count=None, page_dim=0, stream=None):
+    """pool[dst[i]] = pool[src[i]] for the pairs (the first ``count``, an int64 GPU tensor, of them) whose pages are in
+    the pool (dws_pages_copy). pool: contiguous, of any type; page_dim 1: (layers, pages, ...). A written page must be
+    in one pair only. Returns pool."""
+    import torch
+    if not isinstance(pool, torch.Tensor) or not pool.is_cuda:
+        raise TypeError("pool must be a GPU tensor (there is no CPU path)")
+    if page_dim not in (0, 1) or pool.dim() <= page_dim or not pool.is_contiguous():
+        raise ValueError("pool must be contiguous, its pages in dimension 0 or 1")
+    n = src.numel() if isinstance(src, torch.Tensor) else 0
+    a, b = (_device_ints(t, w, torch.int32, n, pool.device) for t, w in ((src, "src"), (dst, "dst")))
+    k = None if count is None else _device_ints(count, "count", torch.int64, 1, pool.device)
+    layers, pages = (1 if page_dim == 0 else pool.shape[0]), pool.shape[page_dim]
+    layer_bytes = pool[0].numel() * pool.element_size() if page_dim and layers else pool.numel() * pool.element_size()
+    with _on_stream(pool, stream) as s:
+        _check(load_library().dws_pages_copy(pool.data_ptr(), pages, layer_bytes // pages if pages else 0, layers,
+                                             layer_bytes, a, b, n, k, s), "dws_pages_copy")
+    return pool
 
 
 def device_memory_info() -> dict:

@@ -626,6 +626,97 @@ dws_status dws_delta_rule_backward(const dws_delta_rule_args* args, hipStream_t 
  */
 dws_status dws_delta_rule_step(const dws_delta_rule_args* args, hipStream_t stream);
 
+/* ---- pages of a cache -------------------------------------------------------
+ *
+ * A cache (keys and values, or the states of dws_delta_rule_step) kept in pages
+ * of a pool. d_refs[p] counts the rows that hold page p; 0 (or less) is free.
+ * d_table[row * max_pages + i] is page i of a row and d_lengths[row] its tokens:
+ * a row of n tokens has ceil(n / page_tokens) pages, and -1 in its other
+ * entries. All arrays are DEVICE int32. Everything is stream compaction of the
+ * counts: pages are given out lowest first, and compaction moves the pages in
+ * use to the front. Results do not depend on scheduling. No call touches
+ * anything outside the arrays, whatever they hold: requests for rows outside
+ * the table (-1, say, in a batch of fixed size) do nothing, and entries outside
+ * the pool are skipped.
+ */
+typedef struct dws_page_cache {
+    int* d_refs;
+    long long n_pages;        /* 1 .. 2^24 */
+    int* d_table;
+    long long n_rows, max_pages;
+    int* d_lengths;           /* not used by dws_pages_compact */
+    long long page_tokens;    /* not used by dws_pages_compact */
+} dws_page_cache;
+
+/* Bytes of workspace (DEVICE, 256-byte aligned) for any of the calls below on
+ * this cache with n requests; only n_pages and n_rows are read. Host only. Calls
+ * that may run at the same time, replays of captured graphs among them, need a
+ * workspace each. */
+dws_status dws_pages_workspace(const dws_page_cache* cache, long long n, size_t* bytes);
+
+/*
+ * Gives row d_rows[i] the pages for d_new_lengths[i] tokens, for n requests in
+ * order: d_granted[i] becomes 1 and the row's length the new one, or, for a row
+ * outside the table or named by an earlier request, a length below the row's or
+ * beyond max_pages pages, or when fewer pages are free than it and the requests
+ * before it need, 0 and the row stays as it was. (After the first request
+ * without enough pages no later one that needs any is granted.) New pages count
+ * 1. All page calls: checks precede any HIP call; a NULL or wrapped array, a
+ * negative count, n_pages or page_tokens below 1 or too small a workspace give
+ * DWS_ERR_INVALID_ARG, sizes beyond the limits (2^24 pages, 2^31 - 1 rows,
+ * entries, tokens and requests) DWS_ERR_UNSUPPORTED, misaligned arrays
+ * DWS_ERR_MISALIGNED, arrays that overlap DWS_ERR_OVERLAP. Asynchronous,
+ * allocates nothing, may be captured.
+ */
+dws_status dws_pages_grow(const dws_page_cache* cache, const int* d_rows, const int* d_new_lengths, long long n,
+                          int* d_granted, void* d_workspace, size_t workspace_bytes, hipStream_t stream);
+
+/*
+ * Makes row d_children[i], which must be empty (length 0), a row with the tokens
+ * of row d_parents[i], for n requests in order: whole pages are shared (their
+ * counts go up), an unfinished last page gets a new page of its own. The pages
+ * to copy, at most n, are d_src[0 .. *d_count) and d_dst[..), -1 behind them,
+ * for dws_pages_copy. d_granted[i] is 0, and nothing is changed, for rows
+ * outside the table, a child that is not empty or named by an earlier request,
+ * or without a free page for it. A parent that is also a child of the call
+ * counts as it was before it (empty).
+ */
+dws_status dws_pages_fork(const dws_page_cache* cache, const int* d_parents, const int* d_children, long long n,
+                          int* d_granted, int* d_src, int* d_dst, long long* d_count, void* d_workspace,
+                          size_t workspace_bytes, hipStream_t stream);
+
+/*
+ * Empties n rows: takes one from the counts of their pages, sets those entries
+ * to -1 and the lengths to 0. A row named twice is emptied once. *d_freed is the
+ * number of pages that became free.
+ */
+dws_status dws_pages_free(const dws_page_cache* cache, const int* d_rows, long long n, long long* d_freed,
+                          void* d_workspace, size_t workspace_bytes, hipStream_t stream);
+
+/*
+ * Renumbers the *d_count pages in use to 0 .. *d_count - 1 with the fewest moves:
+ * the k-th free page among those places takes the k-th page in use behind them.
+ * Counts and table entries follow; d_remap[p] (n_pages) is the new number of page
+ * p, -1 if it was free. The *d_moves pages to copy are d_src[i] to d_dst[i]
+ * (n_pages / 2 entries each, -1 behind them), for dws_pages_copy; no page is in
+ * both.
+ */
+dws_status dws_pages_compact(const dws_page_cache* cache, int* d_remap, int* d_src, int* d_dst, long long* d_moves,
+                             long long* d_count, void* d_workspace, size_t workspace_bytes, hipStream_t stream);
+
+/*
+ * Copies page d_src[i] over page d_dst[i] in every layer, for n pairs, or the
+ * first *d_count of them where d_count is not NULL. Layer l of the pool has its
+ * n_pages pages of page_bytes bytes at d_pool + l * layer_stride (bytes). Pairs
+ * with a page outside the pool, or equal ones, are skipped. A page that is
+ * written must not be named by another pair, as source or destination: what it
+ * and its copies hold is unspecified then. Any size and alignment; multiples of
+ * 16 bytes are copied in 16-byte units, of 4 in 4-byte units.
+ */
+dws_status dws_pages_copy(void* d_pool, long long n_pages, long long page_bytes, long long n_layers,
+                          long long layer_stride, const int* d_src, const int* d_dst, long long n,
+                          const long long* d_count, hipStream_t stream);
+
 /* Human-readable name of a status code (static string, never NULL). */
 const char* dws_status_string(dws_status status);
 
