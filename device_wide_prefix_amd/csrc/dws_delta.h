@@ -9,11 +9,10 @@
 
 namespace dws {
 
-// Tokens of a chunk: 64 for the 16-bit types, 32 for fp32, whose tiles take
-// twice the LDS (two (chunk x 256) tiles and two (chunk x chunk) ones fit).
-constexpr int delta_chunk(int dtype) { return dtype == DWS_FLOAT32 ? 32 : 64; }
 // Head dimensions the chunk kernels are built for; others run zero-padded.
 constexpr int delta_padded_k(int dim_k) { return dim_k <= 64 ? 64 : (dim_k <= 128 ? 128 : 256); }
+// Tokens of a chunk (kChunk of the kernels, which says why).
+constexpr int delta_chunk(int dtype, int dim_k) { return dtype == DWS_FLOAT32 || dim_k > 128 ? 32 : 64; }
 // Columns of a value head are laid out in the workspace in whole 32s.
 constexpr int delta_padded_v(int dim_v) { return (dim_v + 31) / 32 * 32; }
 
@@ -35,7 +34,8 @@ struct DeltaParams {
     int heads_qk, heads_v, dim_k, dim_v, dv_pad;
     float scale;
     int g_dtype, beta_dtype;
-    int vec;                     // q, k (and d_out) rows can be read in 16-byte units
+    int vec;                     // q and k rows (and d_out's) are whole, aligned 16-byte units
+    int out4;                    // out's rows are whole, aligned units of four elements
     DeltaRows q, k, v, g, beta, out;
     const float* initial;        // (n_seqs or n_states, heads_v, dim_k, dim_v)
     float* final_state;

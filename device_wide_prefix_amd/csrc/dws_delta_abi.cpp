@@ -79,10 +79,11 @@ dws_status add_rows(Ranges* ranges, const dws_rows& a, int64_t tokens, int heads
     return ranges->add(a.data, span * size_of(dtype), written, size_of(dtype));
 }
 
-bool vec16(const DeltaRows& a, int dtype)
+// Whether the rows are whole, aligned units of `bytes` bytes.
+bool whole_units(const DeltaRows& a, int dim, int dtype, int bytes)
 {
-    const int64_t v = 16 / (int64_t)size_of(dtype);
-    return (reinterpret_cast<uintptr_t>(a.data) & 15u) == 0 && a.ts % v == 0 && a.hs % v == 0;
+    const int64_t v = bytes / (int64_t)size_of(dtype);
+    return reinterpret_cast<uintptr_t>(a.data) % bytes == 0 && dim % v == 0 && a.ts % v == 0 && a.hs % v == 0;
 }
 
 struct Sizes {
@@ -102,7 +103,7 @@ dws_status check_shape(const dws_delta_rule_args* a)
     if (a->tokens > kMaxTokens || a->n_seqs > kMaxTokens) return DWS_ERR_UNSUPPORTED;
     // one workgroup of at most 256 threads for each chunk slot and value head,
     // and scan workgroups of 16 columns at least
-    const uint64_t slots = (uint64_t)a->tokens / delta_chunk(a->dtype) + (uint64_t)a->n_seqs + 1;
+    const uint64_t slots = (uint64_t)a->tokens / delta_chunk(a->dtype, a->dim_k) + (uint64_t)a->n_seqs + 1;
     if (slots * (uint64_t)a->heads_v > kMaxThreads / 256) return DWS_ERR_UNSUPPORTED;
     if (((uint64_t)a->n_seqs * a->heads_v + 8) * 16 > kMaxThreads / 512) return DWS_ERR_UNSUPPORTED;
     return DWS_OK;
@@ -113,7 +114,7 @@ dws_status check_shape(const dws_delta_rule_args* a)
 Sizes workspace_of(const dws_delta_rule_args* a, bool backward, bool precise)
 {
     Sizes z{};
-    const size_t c = (size_t)delta_chunk(a->dtype), e = size_of(a->dtype);
+    const size_t c = (size_t)delta_chunk(a->dtype, a->dim_k), e = size_of(a->dtype);
     const size_t dk = (size_t)delta_padded_k(a->dim_k), dv = (size_t)delta_padded_v(a->dim_v);
     z.n_slots = a->tokens / (int64_t)c + a->n_seqs + 1;
     const size_t fine = (size_t)delta_fine_parts(a->dtype);
@@ -200,7 +201,8 @@ dws_status forward_entry(const dws_delta_rule_args* a, hipStream_t stream)
     if (a->d_workspace == nullptr || a->workspace_bytes < z.bytes) return DWS_ERR_INVALID_ARG;
     if ((st = r.add(a->d_workspace, z.bytes, true, 256)) != DWS_OK) return st;
     if (r.overlap()) return DWS_ERR_OVERLAP;
-    p.vec = vec16(p.q, a->dtype) && vec16(p.k, a->dtype);
+    p.vec = whole_units(p.q, a->dim_k, a->dtype, 16) && whole_units(p.k, a->dim_k, a->dtype, 16);
+    p.out4 = whole_units(p.out, a->dim_v, a->dtype, 4 * (int)size_of(a->dtype));
     p.initial = a->d_initial_state;
     p.final_state = a->d_final_state;
     p.slots = a->d_slots;
@@ -244,7 +246,8 @@ dws_status backward_entry(const dws_delta_rule_args* a, hipStream_t stream)
     if (a->d_workspace == nullptr || a->workspace_bytes < z.bytes) return DWS_ERR_INVALID_ARG;
     if ((st = r.add(a->d_workspace, z.bytes, true, 256)) != DWS_OK) return st;
     if (r.overlap()) return DWS_ERR_OVERLAP;
-    p.vec = vec16(p.q, a->dtype) && vec16(p.k, a->dtype) && vec16(p.d_out, a->dtype);
+    p.vec = whole_units(p.q, a->dim_k, a->dtype, 16) && whole_units(p.k, a->dim_k, a->dtype, 16) &&
+            whole_units(p.d_out, a->dim_v, a->dtype, 16);
     p.initial = a->d_initial_state;
     p.d_final = a->d_final_grad;
     p.d_initial = a->d_initial_grad;

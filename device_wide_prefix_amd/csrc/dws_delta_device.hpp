@@ -161,6 +161,17 @@ __device__ __forceinline__ Parts<T, NP> parts_tr(const T* tile, int tile_elems, 
     for (int n = 0; n < NP; ++n) a.p[n] = frag_tr(tile + n * tile_elems, stride, r0, c0, lane);
     return a;
 }
+// Four values as NP parts of four, `step` elements apart.
+template <int NP, class T>
+__device__ __forceinline__ void store_parts4(T* at, int64_t step, f32x4 x)
+{
+#pragma unroll
+    for (int n = 0; n < NP; ++n) {
+        const Vec4<T> y = __builtin_convertvector(x, Vec4<T>);
+        *reinterpret_cast<Vec4<T>*>(at + n * step) = y;
+        if (n + 1 < NP) x -= __builtin_convertvector(y, f32x4);
+    }
+}
 // x as NP parts, `step` elements apart.
 template <int NP, class T>
 __device__ __forceinline__ void store_parts(T* at, int64_t step, float x)
@@ -188,28 +199,58 @@ __device__ __forceinline__ float load_gate(const DeltaRows& r, int64_t token, in
 // their differences then stay finite for -infinity too. NaN stays NaN.
 __device__ __forceinline__ float clamp_decay(float g) { return g < -104.f ? -104.f : g; }
 
-// rows x cols elements at `src` (row stride `ld`) into an LDS tile, zero in
-// the columns up to `padded` and in the rows up to `all_rows`.
-template <class T, int THREADS>
-__device__ __forceinline__ void stage_tile(T* tile, int stride, const T* src, int64_t ld, int rows, int cols,
-                                           int all_rows, int padded, bool vec, int tid)
-{
-    constexpr int V = 16 / (int)sizeof(T);
+// A tile of ROWS x COLS elements on its way from global memory to LDS through
+// registers, 16 bytes at a time: load() for the next chunk is issued before a
+// chunk's products and store() after them, so that the loads are in flight
+// meanwhile. Rows from `rows` and columns from `cols` on become 0; their loads
+// go to the tile's first element instead of behind it.
+template <class T, int ROWS, int COLS, int THREADS>
+struct TileRegs {
+    static constexpr int V = 16 / (int)sizeof(T), UNITS = COLS / V, ALL = ROWS * UNITS;
+    static constexpr int N = (ALL + THREADS - 1) / THREADS;
     typedef T VecT __attribute__((ext_vector_type(V)));
-    const int units = padded / V;
-    for (int i = tid; i < all_rows * units; i += THREADS) {
-        const int r = i / units, c = (i - r * units) * V;
-        VecT x = {};
-        if (r < rows) {
-            if (vec && c + V <= cols) {
-                x = *reinterpret_cast<const VecT*>(src + r * ld + c);
-            } else {
+    VecT x[N];
+
+    __device__ __forceinline__ void load(const T* src, int64_t ld, int rows, int cols, int tid)
+    {
 #pragma unroll
-                for (int j = 0; j < V; ++j)
-                    if (c + j < cols) x[j] = src[r * ld + c + j];
-            }
+        for (int i = 0; i < N; ++i) {
+            const int u = tid + i * THREADS, r = u / UNITS, c = u % UNITS * V;
+            const bool in = r < rows && c < cols && (ALL % THREADS == 0 || u < ALL);
+            x[i] = *reinterpret_cast<const VecT*>(src + (in ? r * ld + c : 0));
         }
-        *reinterpret_cast<VecT*>(tile + r * stride + c) = x;
+    }
+    __device__ __forceinline__ void store(T* tile, int stride, int rows, int cols, int tid) const
+    {
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const int u = tid + i * THREADS, r = u / UNITS, c = u % UNITS * V;
+            const bool in = r < rows && c < cols;
+            if (ALL % THREADS == 0 || u < ALL) *reinterpret_cast<VecT*>(tile + r * stride + c) = in ? x[i] : VecT{};
+        }
+    }
+};
+// The same straight from global memory, element by element: rows that are not
+// whole 16-byte units.
+template <class T, int ROWS, int COLS, int THREADS>
+__device__ __forceinline__ void stage_elements(T* tile, int stride, const T* src, int64_t ld, int rows, int cols, int tid)
+{
+    for (int i = tid; i < ROWS * COLS; i += THREADS) {
+        const int r = i / COLS, c = i % COLS;
+        tile[r * stride + c] = r < rows && c < cols ? src[r * ld + c] : (T)0.f;
+    }
+}
+// A caller's tile, in either way.
+template <class T, int ROWS, int COLS, int THREADS>
+__device__ __forceinline__ void stage_tile(T* tile, int stride, const T* src, int64_t ld, int rows, int cols, bool vec,
+                                           int tid)
+{
+    if (vec) {
+        TileRegs<T, ROWS, COLS, THREADS> x;
+        x.load(src, ld, rows, cols, tid);
+        x.store(tile, stride, rows, cols, tid);
+    } else {
+        stage_elements<T, ROWS, COLS, THREADS>(tile, stride, src, ld, rows, cols, tid);
     }
 }
 

@@ -16,8 +16,10 @@
 
 namespace dws {
 
-template <class T>
-constexpr int kChunk = sizeof(T) == 4 ? 32 : 64;
+// Tokens of a chunk: 64, and 32 where a chunk's tiles twice over (the next
+// chunk's arrive while this one is worked on) would not fit 160 KB of LDS.
+template <class T, int DK>
+constexpr int kChunk = sizeof(T) == 4 || DK > 128 ? 32 : 64;
 
 // Parts of the 16-bit operands that are computed in fp32. With one part for
 // all, bf16 outputs and gradients are off by 3.3e-3 to 4.9e-3 (2-norm), twice
@@ -36,82 +38,71 @@ constexpr int kPrecise = __is_same(T, bf16_t) ? 3 : kFine<T>;
 
 // ---- the inverse of a unit lower triangular matrix -----------------------
 
-// inv = (I + M)^-1, M strictly lower triangular, with M_ij = l[i][j] *
-// (BY_ROW ? beta[i] : beta[j]); both fp32 in LDS, rows of C + 1. Diagonal
-// 16 x 16 blocks by substitution (one wave each, a column a lane), then block
-// row i from the rows above: inv_ij = -inv_ii sum_k M_ik inv_kj. Substitution
-// keeps the error at the size of the result's entries; a product of powers
-// (I - M)(I + M^2)... would not, since the powers of M can be far larger.
-template <int C, bool BY_ROW>
-__device__ __forceinline__ void invert_unit_lower(const float (*l)[C + 1], const float* beta, float (*inv)[C + 1],
-                                                  int wave, int lane)
+// fp32 product of two 16-row, 16-column blocks of LDS matrices (rows of LD):
+// acc + a[.., 0 .. K) b[0 .. K, ..), on the matrix cores.
+template <int LD, int K>
+__device__ __forceinline__ f32x4 block_product(const float* a, const float* b, f32x4 acc, int lane)
 {
-    constexpr int NB = C / 16;
+    const int lr = lane & 15, gq = lane >> 4;
+#pragma unroll
+    for (int k = 0; k < K; k += 4)
+        acc = __builtin_amdgcn_mfma_f32_16x16x4f32(a[lr * LD + k + gq], b[(k + gq) * LD + lr], acc, 0, 0, 0);
+    return acc;
+}
+template <int LD>
+__device__ __forceinline__ void store_block(float* at, f32x4 x, int lane)
+{
+#pragma unroll
+    for (int r = 0; r < 4; ++r) at[((lane >> 4) * 4 + r) * LD + (lane & 15)] = x[r];
+}
+
+// inv = (I + m)^-1, m strictly lower triangular, both fp32 in LDS with rows of
+// C + 1. The diagonal 16 x 16 blocks by substitution (one wave each, a column a
+// lane), then twice as large blocks from two: [[A, 0], [M, B]]^-1 has
+// -B^-1 M A^-1 in its corner. Substitution keeps the error at the size of the
+// result's entries; a product of powers (I - m)(I + m^2).. would not, since the
+// powers of m can be far larger than its inverse. `tmp`: C x (C + 1).
+template <int C>
+__device__ __forceinline__ void invert_unit_lower(const float* m, float* inv, float* tmp, int wave, int lane)
+{
+    constexpr int NB = C / 16, LD = C + 1;
     const int col = lane & 15, gq = lane >> 4;
-    auto m = [&](int i, int j) { return l[i][j] * (BY_ROW ? beta[i] : beta[j]); };
     {
-        const int b0 = wave * 16;
+        const float* d = m + wave * 16 * (LD + 1);
         float x[16];
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
             float s = i == col ? 1.f : 0.f;
 #pragma unroll
-            for (int j = 0; j < i; ++j) s -= m(b0 + i, b0 + j) * x[j];
+            for (int j = 0; j < i; ++j) s -= d[i * LD + j] * x[j];
             x[i] = s;
         }
-        if (gq == 0) {
+        // four lanes have the same column: each stores a quarter of it
 #pragma unroll
-            for (int i = 0; i < 16; ++i) inv[b0 + i][b0 + col] = x[i];
-        }
-        // the blocks above the diagonal
-        for (int jb = wave + 1; jb < NB; ++jb)
-#pragma unroll
-            for (int r = 0; r < 4; ++r) inv[b0 + gq * 4 + r][jb * 16 + col] = 0.f;
+        for (int i = 0; i < 16; ++i)
+            if (i / 4 == gq) inv[(wave * 16 + i) * LD + wave * 16 + col] = x[i];
+        for (int jb = wave + 1; jb < NB; ++jb) store_block<LD>(inv + wave * 16 * LD + jb * 16, f32x4{}, lane);
     }
     __syncthreads();
-    for (int ib = 1; ib < NB; ++ib) {
-        float acc[4] = {};
-        if (wave < ib) {
-            for (int k = wave * 16; k < ib * 16; ++k) {
-                const float y = inv[k][wave * 16 + col];
-#pragma unroll
-                for (int r = 0; r < 4; ++r) acc[r] += m(ib * 16 + gq * 4 + r, k) * y;
-            }
-#pragma unroll
-            for (int r = 0; r < 4; ++r) inv[ib * 16 + gq * 4 + r][wave * 16 + col] = acc[r];
-        }
+    // 16 -> 32: wave w < NB / 2 makes block (2 w + 1, 2 w)
+    const int a = wave * 2;
+    if (wave < NB / 2)
+        store_block<LD>(tmp + a * 16 * LD, block_product<LD, 16>(m + (a + 1) * 16 * LD + a * 16, inv + a * 16 * (LD + 1), f32x4{}, lane), lane);
+    __syncthreads();
+    if (wave < NB / 2)
+        store_block<LD>(inv + (a + 1) * 16 * LD + a * 16,
+                        -block_product<LD, 16>(inv + (a + 1) * 16 * (LD + 1), tmp + a * 16 * LD, f32x4{}, lane), lane);
+    __syncthreads();
+    if constexpr (NB == 4) {
+        // 32 -> 64: four blocks, one a wave
+        const int bi = wave >> 1, bj = wave & 1;
+        store_block<LD>(tmp + bi * 16 * LD + bj * 16,
+                        block_product<LD, 32>(m + (32 + bi * 16) * LD, inv + bj * 16, f32x4{}, lane), lane);
         __syncthreads();
-        if (wave < ib) {
-            float y[4] = {};
-            for (int k = 0; k < 16; ++k) {
-                const float a = inv[ib * 16 + k][wave * 16 + col];
-#pragma unroll
-                for (int r = 0; r < 4; ++r) y[r] -= inv[ib * 16 + gq * 4 + r][ib * 16 + k] * a;
-            }
-#pragma unroll
-            for (int r = 0; r < 4; ++r) acc[r] = y[r];
-        }
-        __syncthreads();
-        if (wave < ib) {
-#pragma unroll
-            for (int r = 0; r < 4; ++r) inv[ib * 16 + gq * 4 + r][wave * 16 + col] = acc[r];
-        }
+        store_block<LD>(inv + (32 + bi * 16) * LD + bj * 16,
+                        -block_product<LD, 32>(inv + (32 + bi * 16) * LD + 32, tmp + bj * 16, f32x4{}, lane), lane);
         __syncthreads();
     }
-}
-
-template <class T, int C>
-struct PrepShared {
-    float l[C][C + 1];
-    float inv[C][C + 1];
-    double total[C];
-    float beta[C];
-};
-template <class T, int DK>
-constexpr size_t prep_lds_bytes()
-{
-    constexpr int C = kChunk<T>;
-    return sizeof(PrepShared<T, C>) + 2 * (size_t)C * lds_stride<T>(DK) * sizeof(T);
 }
 
 // Sums of the chunk's log decays, in double: the differences of two sums of 64
@@ -141,17 +132,34 @@ __device__ __forceinline__ void zero_rows(const DeltaRows& r, int64_t first, int
         }
 }
 
+// LDS of the preparation: the matrices of the inversion share their place with
+// the K and Q tiles, which are done with before.
+template <class T, int DK>
+struct PrepLds {
+    static constexpr int C = kChunk<T, DK>, LK = lds_stride<T>(DK), LD = C + 1;
+    static constexpr size_t tiles = 2 * (size_t)C * LK * sizeof(T), inverse = 2 * (size_t)C * LD * sizeof(float);
+    static constexpr size_t shared = tiles > inverse ? tiles : inverse;
+    static constexpr size_t total = shared, beta = total + C * sizeof(double), m = beta + C * sizeof(float);
+    static constexpr size_t bytes = m + (size_t)C * LD * sizeof(float);
+};
+
 // One workgroup for each (chunk slot, value head): gate factors, P and the
 // inverse(s) to the workspace. Products over dim_k on the matrix cores, wave w
 // owning the tokens 16 w .. 16 w + 15.
 template <class T, int DK, int NP, bool BWD>
-__global__ __launch_bounds__(kChunk<T> * 4) void k_delta_prep(DeltaParams p)
+__global__ __launch_bounds__((kChunk<T, DK> * 4)) void k_delta_prep(DeltaParams p)
 {
-    constexpr int C = kChunk<T>, THREADS = C * 4, NB = C / 16, LK = lds_stride<T>(DK);
+    using S = PrepLds<T, DK>;
+    constexpr int C = S::C, THREADS = C * 4, NB = C / 16, LK = S::LK, LD = S::LD, NF = kFine<T>;
+    constexpr int NX = NP > NF ? NP : NF;
     extern __shared__ __attribute__((aligned(16))) char smem[];
-    auto& sh = *reinterpret_cast<PrepShared<T, C>*>(smem);
-    T* ks = reinterpret_cast<T*>(smem + sizeof(PrepShared<T, C>));
+    T* ks = reinterpret_cast<T*>(smem);
     T* qs = ks + C * LK;
+    float* inv = reinterpret_cast<float*>(smem);
+    float* tmp = inv + C * LD;
+    double* total = reinterpret_cast<double*>(smem + S::total);
+    float* beta = reinterpret_cast<float*>(smem + S::beta);
+    float* m = reinterpret_cast<float*>(smem + S::m);
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, gq = lane >> 4, lr = lane & 15;
     const int64_t slot = blockIdx.x / p.heads_v;
     const int h = blockIdx.x % p.heads_v, hk = h / (p.heads_v / p.heads_qk);
@@ -176,89 +184,108 @@ __global__ __launch_bounds__(kChunk<T> * 4) void k_delta_prep(DeltaParams p)
     }
     const T* k0 = static_cast<const T*>(p.k.data) + info.row * p.k.ts + hk * p.k.hs;
     const T* q0 = static_cast<const T*>(p.q.data) + info.row * p.q.ts + hk * p.q.hs;
-    stage_tile<T, THREADS>(ks, LK, k0, p.k.ts, info.rows, p.dim_k, C, DK, p.vec, tid);
-    stage_tile<T, THREADS>(qs, LK, q0, p.q.ts, info.rows, p.dim_k, C, DK, p.vec, tid);
     const int64_t at = slot * p.heads_v + h;
+    float g = 0.f, b = 0.f;
+    if (wave == 0 && lane < info.rows) {
+        if (p.g.data) g = clamp_decay(load_gate(p.g, info.row + lane, h, p.g_dtype));
+        b = load_gate(p.beta, info.row + lane, h, p.beta_dtype);
+    }
+    stage_tile<T, C, DK, THREADS>(ks, LK, k0, p.k.ts, info.rows, p.dim_k, p.vec, tid);
+    stage_tile<T, C, DK, THREADS>(qs, LK, q0, p.q.ts, info.rows, p.dim_k, p.vec, tid);
     if (wave == 0) {
-        const bool in = lane < info.rows;
-        const float g = in && p.g.data ? clamp_decay(load_gate(p.g, info.row + lane, h, p.g_dtype)) : 0.f;
-        const float b = in ? load_gate(p.beta, info.row + lane, h, p.beta_dtype) : 0.f;
-        const double total = scan_decays<C>((double)g, lane);
-        const double last = __shfl(total, C - 1, 64);
+        const double sum = scan_decays<C>((double)g, lane);
+        const double last = __shfl(sum, C - 1, 64);
         if (lane < C) {
-            sh.total[lane] = total;
-            sh.beta[lane] = b;
+            total[lane] = sum;
+            beta[lane] = b;
             float* w = p.w_gate + at * 3 * C;
-            w[lane] = expf((float)total);
-            w[C + lane] = expf((float)(last - total));
+            w[lane] = expf((float)sum);
+            w[C + lane] = expf((float)(last - sum));
             w[2 * C + lane] = b;
         }
     }
     __syncthreads();
 
-    // row tile `wave` of K K^T and Q K^T, up to the diagonal
-    constexpr int NF = kFine<T>;
+    // row tile `wave` of K K^T and Q K^T, up to the diagonal. m = L B.
     T* wp = static_cast<T*>(p.w_p) + at * NF * C * C;
+    f32x4 low[BWD ? NB : 1];      // B L
 #pragma unroll
     for (int nt = 0; nt < NB; ++nt) {
+        // P goes out four elements of a row a lane: its rows are tokens i
+        // forward, j (P transposed) backward, the other token being the one
+        // that runs along a lane's four results
         f32x4 kk = {}, qk = {};
         if (nt <= wave) {
 #pragma unroll
             for (int kb = 0; kb < DK; kb += 32) {
-                const Vec8<T> b = frag_nat(ks, LK, nt * 16, kb, lane);
-                kk = mma(frag_nat(ks, LK, wave * 16, kb, lane), b, kk);
-                qk = mma(frag_nat(qs, LK, wave * 16, kb, lane), b, qk);
+                const Vec8<T> ki = frag_nat(ks, LK, wave * 16, kb, lane), kj = frag_nat(ks, LK, nt * 16, kb, lane);
+                const Vec8<T> qi = frag_nat(qs, LK, wave * 16, kb, lane);
+                kk = mma(ki, kj, kk);
+                qk = BWD ? mma(qi, kj, qk) : mma(kj, qi, qk);
             }
         }
-        const int j = nt * 16 + lr;
+        f32x4 pij;
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-            const int i = wave * 16 + gq * 4 + r;
-            const float d = i >= j ? expf((float)(sh.total[i] - sh.total[j])) : 0.f;
-            sh.l[i][j] = i > j ? d * kk[r] : 0.f;
-            const float pij = i >= j ? p.scale * d * qk[r] : 0.f;
-            store_parts<NF>(wp + (BWD ? j * C + i : i * C + j), C * C, pij);
+            const int i = wave * 16 + gq * 4 + r, j = nt * 16 + lr;
+            const float d = i > j ? expf((float)(total[i] - total[j])) : 0.f;
+            m[i * LD + j] = i > j ? d * beta[j] * kk[r] : 0.f;
+            if constexpr (BWD) low[nt][r] = i > j ? d * beta[i] * kk[r] : 0.f;
+            const int pi = BWD ? i : wave * 16 + lr, pj = BWD ? j : nt * 16 + gq * 4 + r;
+            const float e = BWD ? d : (pi > pj ? expf((float)(total[pi] - total[pj])) : 0.f);
+            pij[r] = pi > pj ? p.scale * e * qk[r] : (pi == pj ? p.scale * qk[r] : 0.f);
         }
+        T* to = BWD ? wp + (nt * 16 + lr) * C + wave * 16 + gq * 4 : wp + (wave * 16 + lr) * C + nt * 16 + gq * 4;
+        store_parts4<NF>(to, C * C, pij);
     }
     __syncthreads();
 
-    invert_unit_lower<C, false>(sh.l, sh.beta, sh.inv, wave, lane);
-    constexpr int NX = NP > NF ? NP : NF;
+    invert_unit_lower<C>(m, inv, tmp, wave, lane);
     T* wt = static_cast<T*>(p.w_t) + at * NX * C * C;
-    for (int i = tid; i < C * C; i += THREADS) store_parts<NX>(wt + i, C * C, sh.inv[i / C][i % C]);
+    for (int i = tid; i < C * C / 4; i += THREADS) {
+        const float* x = inv + i / (C / 4) * LD + i % (C / 4) * 4;
+        store_parts4<NX>(wt + i * 4, C * C, f32x4{x[0], x[1], x[2], x[3]});
+    }
     if constexpr (BWD) {
+        // the other inverse, of I + B L
         __syncthreads();
-        invert_unit_lower<C, true>(sh.l, sh.beta, sh.inv, wave, lane);
+#pragma unroll
+        for (int nt = 0; nt < NB; ++nt)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) m[(wave * 16 + gq * 4 + r) * LD + nt * 16 + lr] = low[nt][r];
+        __syncthreads();
+        invert_unit_lower<C>(m, inv, tmp, wave, lane);
         T* wtt = static_cast<T*>(p.w_tt) + at * NF * C * C;
-        for (int i = tid; i < C * C; i += THREADS) store_parts<NF>(wtt + i, C * C, sh.inv[i % C][i / C]);
+        for (int i = tid; i < C * C / 4; i += THREADS) {
+            const float* x = inv + i % (C / 4) * 4 * LD + i / (C / 4);
+            store_parts4<NF>(wtt + i * 4, C * C, f32x4{x[0], x[LD], x[2 * LD], x[3 * LD]});
+        }
     }
 }
 
 // ---- the forward scan ------------------------------------------------------
 
-template <class T, int DK, int NP, bool STORE>
-constexpr size_t scan_lds_bytes()
-{
-    constexpr int C = kChunk<T>;
-    const size_t qk = (size_t)C * lds_stride<T>(DK) * sizeof(T), cc = (size_t)C * lds_stride<T>(C) * sizeof(T);
-    constexpr int NX = NP > kFine<T> ? NP : kFine<T>;
-    return (STORE ? 1 : 2) * qk + (STORE ? NX : NX + kFine<T>) * cc + 3 * C * sizeof(float);
-}
+// LDS of a scan workgroup, two of each but for the tiles of a caller's arrays
+// that cannot be read 16 bytes at a time.
+template <class T, int DK, int KQ, int TP>
+struct ScanLds {
+    static constexpr int C = kChunk<T, DK>, LK = lds_stride<T>(DK), LC = lds_stride<T>(C);
+    static constexpr size_t kq = KQ * (size_t)C * LK * sizeof(T), tp = TP * (size_t)C * LC * sizeof(T);
+    static constexpr size_t buffer = kq + tp + 3 * C * sizeof(float), bytes = 2 * buffer;
+};
 
 // STORE: instead of the outputs, the states at the chunks' starts and U' go to
 // the workspace (for the backward pass). NP: parts of the operands the state
-// depends on. NW waves, 16 columns of the value head each.
+// depends on. NW waves, 16 columns of the value head each. Two LDS buffers: the
+// next chunk's tiles are written to one while the other is read, so a chunk
+// needs one barrier, and the loads of the one after that are in flight.
 template <class T, int DK, int NP, bool STORE, int NW>
 __global__ __launch_bounds__(NW * 64) void k_delta_scan(DeltaParams p)
 {
-    constexpr int C = kChunk<T>, THREADS = NW * 64, NB = C / 16, LK = lds_stride<T>(DK), LC = lds_stride<T>(C);
     constexpr int NF = kFine<T>, NX = NP > NF ? NP : NF;
+    using L = ScanLds<T, DK, STORE ? 1 : 2, STORE ? NX : NX + NF>;
+    constexpr int C = L::C, THREADS = NW * 64, NB = C / 16, LK = L::LK, LC = L::LC;
     extern __shared__ __attribute__((aligned(16))) char smem[];
-    T* ks = reinterpret_cast<T*>(smem);
-    T* qs = ks + C * LK;                       // not with STORE
-    T* ts = STORE ? qs : qs + C * LK;          // NX tiles
-    T* ps = ts + NX * C * LC;                  // NF tiles, not with STORE
-    float* gate = reinterpret_cast<float*>(STORE ? ps : ps + NF * C * LC);
 
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, gq = lane >> 4, lr = lane & 15;
     const uint32_t parts = (uint32_t)((p.dim_v + NW * 16 - 1) / (NW * 16));
@@ -267,7 +294,7 @@ __global__ __launch_bounds__(NW * 64) void k_delta_scan(DeltaParams p)
     if (group >= (uint64_t)p.n_seqs * p.heads_v) return;
     const int64_t seq = group / p.heads_v;
     const int h = group % p.heads_v, hk = h / (p.heads_v / p.heads_qk);
-    const int col = (part * NW + wave) * 16 + lr;
+    const int col0 = (part * NW + wave) * 16, col = col0 + lr;
     const bool mine = col < p.dim_v;
     int64_t st;
     if (!slot_taken<THREADS>(p.slots, p.n_states, seq, &st, tid)) return;
@@ -275,6 +302,58 @@ __global__ __launch_bounds__(NW * 64) void k_delta_scan(DeltaParams p)
     const int64_t len = seq_length(p.offsets, p.tokens, p.n_seqs, seq, begin);
     const int64_t slot0 = first_slot(begin, seq, C);
     const int64_t state_at = (st * p.heads_v + h) * p.dim_k * p.dim_v + col;
+    const T* k0 = static_cast<const T*>(p.k.data) + hk * p.k.hs;
+    const T* q0 = static_cast<const T*>(p.q.data) + hk * p.q.hs;
+    const T* v0 = static_cast<const T*>(p.v.data) + h * p.v.hs + (mine ? col : 0);
+
+    TileRegs<T, C, DK, THREADS> kr, qr;
+    TileRegs<T, NX * C, C, THREADS> tr;
+    TileRegs<T, NF * C, C, THREADS> pr;
+    float gr[(3 * C + THREADS - 1) / THREADS];
+    T vr[NB * 4], vn[NB * 4];
+    auto rows_at = [&](int64_t c0) { return len - c0 < C ? (int)(len - c0) : C; };
+    // chunk c0 / C from global memory to registers
+    auto load = [&](int64_t c0) {
+        const int rows = rows_at(c0);
+        const int64_t row0 = begin + c0, at = (slot0 + c0 / C) * p.heads_v + h;
+        if (p.vec) {
+            kr.load(k0 + row0 * p.k.ts, p.k.ts, rows, p.dim_k, tid);
+            if constexpr (!STORE) qr.load(q0 + row0 * p.q.ts, p.q.ts, rows, p.dim_k, tid);
+        }
+        tr.load(static_cast<const T*>(p.w_t) + at * NX * C * C, C, NX * C, C, tid);
+        if constexpr (!STORE) pr.load(static_cast<const T*>(p.w_p) + at * NF * C * C, C, NF * C, C, tid);
+#pragma unroll
+        for (int i = 0; i * THREADS < 3 * C; ++i)
+            gr[i] = p.w_gate[at * 3 * C + (tid + i * THREADS < 3 * C ? tid + i * THREADS : 0)];
+#pragma unroll
+        for (int mt = 0; mt < NB; ++mt)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const int row = mt * 16 + gq * 4 + r;
+                vn[mt * 4 + r] = v0[(row0 + (row < rows ? row : 0)) * p.v.ts];
+            }
+    };
+    // and from there to an LDS buffer
+    auto store = [&](int64_t c0, char* buffer) {
+        const int rows = rows_at(c0);
+        const int64_t row0 = begin + c0;
+        T* ks = reinterpret_cast<T*>(buffer);
+        T* ts = reinterpret_cast<T*>(buffer + L::kq);
+        float* gate = reinterpret_cast<float*>(buffer + L::kq + L::tp);
+        if (p.vec) {
+            kr.store(ks, LK, rows, p.dim_k, tid);
+            if constexpr (!STORE) qr.store(ks + C * LK, LK, rows, p.dim_k, tid);
+        } else {
+            stage_elements<T, C, DK, THREADS>(ks, LK, k0 + row0 * p.k.ts, p.k.ts, rows, p.dim_k, tid);
+            if constexpr (!STORE)
+                stage_elements<T, C, DK, THREADS>(ks + C * LK, LK, q0 + row0 * p.q.ts, p.q.ts, rows, p.dim_k, tid);
+        }
+        tr.store(ts, LC, NX * C, C, tid);
+        if constexpr (!STORE) pr.store(ts + NX * C * LC, LC, NF * C, C, tid);
+#pragma unroll
+        for (int i = 0; i * THREADS < 3 * C; ++i)
+            if (tid + i * THREADS < 3 * C) gate[tid + i * THREADS] = gr[i];
+    };
 
     f32x4 s[DK / 16];
 #pragma unroll
@@ -284,31 +363,25 @@ __global__ __launch_bounds__(NW * 64) void k_delta_scan(DeltaParams p)
             const int row = t * 16 + gq * 4 + r;
             s[t][r] = p.initial && mine && row < p.dim_k ? p.initial[state_at + (int64_t)row * p.dim_v] : 0.f;
         }
-
-    for (int64_t c0 = 0, slot = slot0; c0 < len; c0 += C, ++slot) {
-        const int rows = len - c0 < C ? (int)(len - c0) : C;
-        const int64_t row0 = begin + c0, at = slot * p.heads_v + h;
-        stage_tile<T, THREADS>(ks, LK, static_cast<const T*>(p.k.data) + row0 * p.k.ts + hk * p.k.hs, p.k.ts, rows,
-                               p.dim_k, C, DK, p.vec, tid);
-        if constexpr (!STORE) {
-            stage_tile<T, THREADS>(qs, LK, static_cast<const T*>(p.q.data) + row0 * p.q.ts + hk * p.q.hs, p.q.ts, rows,
-                                   p.dim_k, C, DK, p.vec, tid);
-            stage_tile<T, THREADS>(ps, LC, static_cast<const T*>(p.w_p) + at * NF * C * C, C, NF * C, C, NF * C, C, true,
-                                   tid);
-        }
-        stage_tile<T, THREADS>(ts, LC, static_cast<const T*>(p.w_t) + at * NX * C * C, C, NX * C, C, NX * C, C, true, tid);
-        for (int i = tid; i < 3 * C; i += THREADS) gate[i] = p.w_gate[at * 3 * C + i];
-        // this wave's columns of V, laid out as the products' results
-        f32x4 x[NB];
-        const T* v0 = static_cast<const T*>(p.v.data) + row0 * p.v.ts + h * p.v.hs + col;
+    if (len > 0) {
+        load(0);
+        store(0, smem);
+    }
+    int which = 0;
+    for (int64_t c0 = 0; c0 < len; c0 += C, which ^= 1) {
+        const int rows = rows_at(c0);
+        const int64_t row0 = begin + c0, at = (slot0 + c0 / C) * p.heads_v + h;
+        char* buffer = smem + which * L::buffer;
+        const T* ks = reinterpret_cast<const T*>(buffer);
+        const T* qs = ks + C * LK;
+        const T* ts = reinterpret_cast<const T*>(buffer + L::kq);
+        const T* ps = ts + NX * C * LC;
+        const float* gate = reinterpret_cast<const float*>(buffer + L::kq + L::tp);
 #pragma unroll
-        for (int mt = 0; mt < NB; ++mt)
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const int row = mt * 16 + gq * 4 + r;
-                x[mt][r] = mine && row < rows ? (float)v0[row * p.v.ts] : 0.f;
-            }
+        for (int i = 0; i < NB * 4; ++i) vr[i] = vn[i];
         __syncthreads();
+        const bool more = c0 + C < len;
+        if (more) load(c0 + C);
 
         if constexpr (STORE) {
             T* ws = static_cast<T*>(p.w_s) + at * DK * p.dv_pad + col;
@@ -322,13 +395,17 @@ __global__ __launch_bounds__(NW * 64) void k_delta_scan(DeltaParams p)
 #pragma unroll
         for (int kb = 0; kb < DK / 32; ++kb) sb[kb] = parts_of<T, NP>(s[2 * kb], s[2 * kb + 1]);
         // X = V - diag(e^G) K S
+        f32x4 x[NB];
 #pragma unroll
         for (int mt = 0; mt < NB; ++mt) {
             f32x4 acc = {};
 #pragma unroll
             for (int kb = 0; kb < DK / 32; ++kb) acc = mma(frag_acc(ks, LK, mt * 16, kb * 32, lane), sb[kb], acc);
 #pragma unroll
-            for (int r = 0; r < 4; ++r) x[mt][r] -= gate[mt * 16 + gq * 4 + r] * acc[r];
+            for (int r = 0; r < 4; ++r) {
+                const int row = mt * 16 + gq * 4 + r;
+                x[mt][r] = (mine && row < rows ? (float)vr[mt * 4 + r] : 0.f) - gate[row] * acc[r];
+            }
         }
         Parts<T, NX> xb[C / 32];
 #pragma unroll
@@ -352,25 +429,31 @@ __global__ __launch_bounds__(NW * 64) void k_delta_scan(DeltaParams p)
             for (int r = 0; r < 4; ++r) u[mt][r] = gate[2 * C + mt * 16 + gq * 4 + r] * acc[r];
         }
         if constexpr (!STORE) {
+            // O transposed, so that a lane has four columns of one token: the
+            // state and u in the place of the left operand
             Parts<T, NF> ub[C / 32];
 #pragma unroll
             for (int kb = 0; kb < C / 32; ++kb) ub[kb] = parts_of<T, NF>(u[2 * kb], u[2 * kb + 1]);
-            T* o0 = static_cast<T*>(p.out.data) + row0 * p.out.ts + h * p.out.hs + col;
 #pragma unroll
             for (int mt = 0; mt < NB; ++mt) {
                 f32x4 acc = {};
 #pragma unroll
                 for (int kb = 0; kb < DK / 32; ++kb)
-                    acc = mma(frag_acc(qs, LK, mt * 16, kb * 32, lane), sb[kb].p[0], acc);
-#pragma unroll
-                for (int r = 0; r < 4; ++r) acc[r] *= p.scale * gate[mt * 16 + gq * 4 + r];
+                    acc = mma(sb[kb].p[0], frag_acc(qs, LK, mt * 16, kb * 32, lane), acc);
+                const int row = mt * 16 + lr, c = col0 + gq * 4;
+                acc *= p.scale * gate[row];
 #pragma unroll
                 for (int kb = 0; kb <= mt / 2; ++kb)
-                    acc = mma(parts_acc<NF>(ps, C * LC, LC, mt * 16, kb * 32, lane), ub[kb], acc);
+                    acc = mma(ub[kb], parts_acc<NF>(ps, C * LC, LC, mt * 16, kb * 32, lane), acc);
+                T* o = static_cast<T*>(p.out.data) + (row0 + row) * p.out.ts + h * p.out.hs + c;
+                if (row < rows) {
+                    if (p.out4) {
+                        if (c < p.dim_v) *reinterpret_cast<Vec4<T>*>(o) = __builtin_convertvector(acc, Vec4<T>);
+                    } else {
 #pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    const int row = mt * 16 + gq * 4 + r;
-                    if (mine && row < rows) o0[row * p.out.ts] = (T)acc[r];
+                        for (int r = 0; r < 4; ++r)
+                            if (c + r < p.dim_v) o[r] = (T)acc[r];
+                    }
                 }
             }
         }
@@ -390,7 +473,7 @@ __global__ __launch_bounds__(NW * 64) void k_delta_scan(DeltaParams p)
 #pragma unroll
             for (int kb = 0; kb < C / 32; ++kb) s[t] = mma(frag_tr(ks, LK, kb * 32, t * 16, lane), ub[kb], s[t]);
         }
-        __syncthreads();
+        if (more) store(c0 + C, smem + (which ^ 1) * L::buffer);
     }
     if (!STORE && p.final_state != nullptr && mine) {
 #pragma unroll
@@ -414,7 +497,7 @@ __global__ __launch_bounds__(NW * 64) void k_delta_scan(DeltaParams p)
 template <class T, int DK>
 constexpr size_t scan_back_lds_bytes()
 {
-    constexpr int C = kChunk<T>;
+    constexpr int C = kChunk<T, DK>;
     return 2 * (size_t)C * lds_stride<T>(DK) * sizeof(T) + 2 * kFine<T> * (size_t)C * lds_stride<T>(C) * sizeof(T) +
            3 * C * sizeof(float);
 }
@@ -422,7 +505,7 @@ constexpr size_t scan_back_lds_bytes()
 template <class T, int DK, int NW>
 __global__ __launch_bounds__(NW * 64) void k_delta_scan_back(DeltaParams p)
 {
-    constexpr int C = kChunk<T>, THREADS = NW * 64, NB = C / 16, LK = lds_stride<T>(DK), LC = lds_stride<T>(C);
+    constexpr int C = kChunk<T, DK>, THREADS = NW * 64, NB = C / 16, LK = lds_stride<T>(DK), LC = lds_stride<T>(C);
     constexpr int NF = kFine<T>;
     extern __shared__ __attribute__((aligned(16))) char smem[];
     T* ks = reinterpret_cast<T*>(smem);
@@ -457,12 +540,12 @@ __global__ __launch_bounds__(NW * 64) void k_delta_scan_back(DeltaParams p)
     for (int64_t c = chunks - 1; c >= 0; --c) {
         const int64_t c0 = c * C, row0 = begin + c0, at = (slot0 + c) * p.heads_v + h;
         const int rows = len - c0 < C ? (int)(len - c0) : C;
-        stage_tile<T, THREADS>(ks, LK, static_cast<const T*>(p.k.data) + row0 * p.k.ts + hk * p.k.hs, p.k.ts, rows,
-                               p.dim_k, C, DK, p.vec, tid);
-        stage_tile<T, THREADS>(qs, LK, static_cast<const T*>(p.q.data) + row0 * p.q.ts + hk * p.q.hs, p.q.ts, rows,
-                               p.dim_k, C, DK, p.vec, tid);
-        stage_tile<T, THREADS>(ps, LC, static_cast<const T*>(p.w_p) + at * NF * C * C, C, NF * C, C, NF * C, C, true, tid);
-        stage_tile<T, THREADS>(ts, LC, static_cast<const T*>(p.w_tt) + at * NF * C * C, C, NF * C, C, NF * C, C, true, tid);
+        stage_tile<T, C, DK, THREADS>(ks, LK, static_cast<const T*>(p.k.data) + row0 * p.k.ts + hk * p.k.hs, p.k.ts, rows,
+                                      p.dim_k, p.vec, tid);
+        stage_tile<T, C, DK, THREADS>(qs, LK, static_cast<const T*>(p.q.data) + row0 * p.q.ts + hk * p.q.hs, p.q.ts, rows,
+                                      p.dim_k, p.vec, tid);
+        stage_tile<T, NF * C, C, THREADS>(ps, LC, static_cast<const T*>(p.w_p) + at * NF * C * C, C, NF * C, C, true, tid);
+        stage_tile<T, NF * C, C, THREADS>(ts, LC, static_cast<const T*>(p.w_tt) + at * NF * C * C, C, NF * C, C, true, tid);
         for (int i = tid; i < 3 * C; i += THREADS) gate[i] = p.w_gate[at * 3 * C + i];
         f32x4 d_o[NB];
         const T* o0 = static_cast<const T*>(p.d_out.data) + row0 * p.d_out.ts + h * p.d_out.hs + col;
@@ -569,7 +652,7 @@ __global__ __launch_bounds__(NW * 64) void k_delta_scan_back(DeltaParams p)
 template <class T, int DK>
 constexpr size_t grad_lds_bytes()
 {
-    constexpr int C = kChunk<T>;
+    constexpr int C = kChunk<T, DK>;
     return 2 * (size_t)C * lds_stride<T>(DK) * sizeof(T) + 2 * kFine<T> * (size_t)C * lds_stride<T>(C) * sizeof(T) +
            (size_t)C * sizeof(double) + (6 * C + C / 16 * C + 16) * sizeof(float);
 }
@@ -623,9 +706,9 @@ __device__ __forceinline__ float sum_groups(float x) // over the 4 groups
 }
 
 template <class T, int DK>
-__global__ __launch_bounds__(kChunk<T> * 4) void k_delta_grad(DeltaParams p)
+__global__ __launch_bounds__((kChunk<T, DK> * 4)) void k_delta_grad(DeltaParams p)
 {
-    constexpr int C = kChunk<T>, THREADS = C * 4, NB = C / 16, NW = THREADS / 64, LK = lds_stride<T>(DK),
+    constexpr int C = kChunk<T, DK>, THREADS = C * 4, NB = C / 16, NW = THREADS / 64, LK = lds_stride<T>(DK),
                   LC = lds_stride<T>(C), NK = DK / 16, NF = kFine<T>;
     extern __shared__ __attribute__((aligned(16))) char smem[];
     double* total = reinterpret_cast<double*>(smem);
@@ -646,10 +729,10 @@ __global__ __launch_bounds__(kChunk<T> * 4) void k_delta_grad(DeltaParams p)
     const SlotInfo info = slot_info<C>(p.offsets, p.tokens, p.n_seqs, slot);
     if (info.rows == 0) return;
     const int rows = info.rows;
-    stage_tile<T, THREADS>(ks, LK, static_cast<const T*>(p.k.data) + info.row * p.k.ts + hk * p.k.hs, p.k.ts, rows,
-                           p.dim_k, C, DK, p.vec, tid);
-    stage_tile<T, THREADS>(qs, LK, static_cast<const T*>(p.q.data) + info.row * p.q.ts + hk * p.q.hs, p.q.ts, rows,
-                           p.dim_k, C, DK, p.vec, tid);
+    stage_tile<T, C, DK, THREADS>(ks, LK, static_cast<const T*>(p.k.data) + info.row * p.k.ts + hk * p.k.hs, p.k.ts, rows,
+                                  p.dim_k, p.vec, tid);
+    stage_tile<T, C, DK, THREADS>(qs, LK, static_cast<const T*>(p.q.data) + info.row * p.q.ts + hk * p.q.hs, p.q.ts, rows,
+                                  p.dim_k, p.vec, tid);
     __syncthreads();
     f32x4 dq[NK] = {}, dk[NK] = {};
 
@@ -849,11 +932,11 @@ inline uint64_t scan_blocks(const DeltaParams& p, int waves)
 template <class T, int DK, int NP>
 hipError_t forward_dk(const DeltaParams& p, hipStream_t stream)
 {
-    constexpr int C = kChunk<T>, NW = 4;
+    constexpr int C = kChunk<T, DK>, NW = 4, NF = kFine<T>, NX = NP > NF ? NP : NF;
     hipError_t e = launch_lds(k_delta_prep<T, DK, NP, false>, (uint64_t)p.n_slots * p.heads_v, C * 4,
-                              prep_lds_bytes<T, DK>(), p, stream);
+                              PrepLds<T, DK>::bytes, p, stream);
     if (e != hipSuccess) return e;
-    return launch_lds(k_delta_scan<T, DK, NP, false, NW>, scan_blocks(p, NW), NW * 64, scan_lds_bytes<T, DK, NP, false>(),
+    return launch_lds(k_delta_scan<T, DK, NP, false, NW>, scan_blocks(p, NW), NW * 64, ScanLds<T, DK, 2, NX + NF>::bytes,
                       p, stream);
 }
 template <class T, int NP>
@@ -869,11 +952,11 @@ hipError_t forward_type(const DeltaParams& p, hipStream_t stream)
 template <class T, int DK>
 hipError_t backward_dk(const DeltaParams& p, hipStream_t stream)
 {
-    constexpr int C = kChunk<T>, NW = 4;
+    constexpr int C = kChunk<T, DK>, NW = 4;
     hipError_t e = launch_lds(k_delta_prep<T, DK, 1, true>, (uint64_t)p.n_slots * p.heads_v, C * 4,
-                              prep_lds_bytes<T, DK>(), p, stream);
+                              PrepLds<T, DK>::bytes, p, stream);
     if (e != hipSuccess) return e;
-    e = launch_lds(k_delta_scan<T, DK, 1, true, NW>, scan_blocks(p, NW), NW * 64, scan_lds_bytes<T, DK, 1, true>(), p,
+    e = launch_lds(k_delta_scan<T, DK, 1, true, NW>, scan_blocks(p, NW), NW * 64, ScanLds<T, DK, 1, kFine<T>>::bytes, p,
                    stream);
     if (e != hipSuccess) return e;
     e = launch_lds(k_delta_scan_back<T, DK, NW>, scan_blocks(p, NW), NW * 64, scan_back_lds_bytes<T, DK>(), p, stream);
