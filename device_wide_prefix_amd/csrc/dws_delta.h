@@ -52,10 +52,10 @@ struct DeltaParams {
     void* w_t;                   // [slot][head][parts][chunk][chunk]: (I + L diag(beta))^-1
     void* w_p;                   // [slot][head][fine][chunk][chunk]: P (forward), its transpose (backward)
     void* w_tt;                  // [slot][head][fine][chunk][chunk]: transpose of (I + diag(beta) L)^-1 (backward)
-    void* w_s;                   // [slot][head][padded dim_k][dv_pad]: states at the chunks' starts
-    void* w_u;                   // [slot][head][fine][chunk][dv_pad]: U'
-    void* w_z;                   // [slot][head][fine][chunk][dv_pad]: Z
-    void* w_ds;                  // [slot][head][padded dim_k][dv_pad]: state gradients at the chunks' ends
+    void* w_s;                   // [slot][head][dv_pad][padded dim_k]: states at the chunks' starts
+    void* w_u;                   // [slot][head][fine][dv_pad][chunk]: U'
+    void* w_z;                   // [slot][head][fine][dv_pad][chunk]: Z
+    void* w_ds;                  // [slot][head][dv_pad][padded dim_k]: state gradients at the chunks' ends
 };
 
 // Per-type launchers (dws_delta_{bf16,f16,f32}.hip). `precise`: the final

@@ -17,6 +17,8 @@ constexpr int kMaxDim = 256;
 constexpr int kMaxHeads = 65535;
 constexpr int64_t kMaxTokens = ((int64_t)1 << 31) - 1;
 constexpr int64_t kMaxStride = (int64_t)1 << 40;
+// a chunk of 64 rows spans less than 2^30 bytes, for 32-bit offsets
+constexpr int64_t kMaxTokenStride = (int64_t)1 << 22;
 // a launch holds fewer than 2^32 threads
 constexpr uint64_t kMaxThreads = ((uint64_t)1 << 32) - 1;
 
@@ -68,6 +70,7 @@ dws_status add_rows(Ranges* ranges, const dws_rows& a, int64_t tokens, int heads
     if (tokens == 0) return DWS_OK;
     const int64_t ts = a.token_stride, hs = a.head_stride;
     if (ts < 0 || hs < 0 || ts > kMaxStride || hs > kMaxStride) return DWS_ERR_INVALID_ARG;
+    if (tokens > 1 && ts >= kMaxTokenStride) return DWS_ERR_UNSUPPORTED;
     if (written) {
         const __int128 heads_span = (__int128)(heads - 1) * hs + dim, token_span = (__int128)(tokens - 1) * ts + dim;
         const bool by_token = (heads == 1 || hs >= dim) && (tokens == 1 || ts >= heads_span);

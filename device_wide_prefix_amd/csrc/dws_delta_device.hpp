@@ -23,6 +23,8 @@ typedef float f32x8 __attribute__((ext_vector_type(8)));
 typedef __bf16 bf16_t;
 typedef _Float16 f16_t;
 typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x2_t __attribute__((ext_vector_type(2)));
+typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
 
 template <class T>
 using Vec8 = T __attribute__((ext_vector_type(8)));
@@ -89,6 +91,24 @@ __device__ __forceinline__ f32x4 mma(Vec8<T> a, const Parts<T, NP>& b, f32x4 c)
 #pragma unroll
     for (int n = NP - 1; n >= 0; --n) c = mma(a, b.p[n], c);
     return c;
+}
+
+// c[m] += a[m] b for M independent results: consecutive products never wait
+// for each other. LEFT: c[m] += b a[m], the transposed results.
+template <bool LEFT = false, class T, int NA, int NB, int M>
+__device__ __forceinline__ void mma_each(const Parts<T, NA> (&a)[M], const Parts<T, NB>& b, f32x4 (&c)[M], int from = 0,
+                                         int to = M)
+{
+    constexpr int LAST = (NA > NB ? NA : NB) - 1;
+#pragma unroll
+    for (int s = LAST; s >= 0; --s)
+#pragma unroll
+        for (int i = 0; i < NA; ++i)
+            if (s - i >= 0 && s - i < NB)
+#pragma unroll
+                for (int m = 0; m < M; ++m)
+                    if (m >= from && m < to)
+                        c[m] = LEFT ? mma(b.p[s - i], a[m].p[i], c[m]) : mma(a[m].p[i], b.p[s - i], c[m]);
 }
 
 // ---- LDS tiles: rows of `stride` elements --------------------------------
@@ -199,11 +219,39 @@ __device__ __forceinline__ float load_gate(const DeltaRows& r, int64_t token, in
 // their differences then stay finite for -infinity too. NaN stays NaN.
 __device__ __forceinline__ float clamp_decay(float g) { return g < -104.f ? -104.f : g; }
 
+// Buffer access: a resource over the rows of a chunk (32-bit offsets, and one
+// compare in hardware instead of 64-bit addresses and branches): reads outside
+// give 0, writes outside are dropped. kOutside is outside of every resource:
+// rows of a chunk span less than 2^30 bytes, which the C entry points check.
+constexpr int kOutside = (int)0x80000000u;
+constexpr int kRsrcFlags = 0x00020000;      // untyped dwords, as the scan kernels' resources
+
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t rows_rsrc(const void* first, int64_t row_bytes, int rows, int bytes)
+{
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(first), (short)0,
+                                             (int)((rows - 1) * row_bytes) + bytes, kRsrcFlags);
+}
+template <class T>
+__device__ __forceinline__ T buffer_load(__amdgpu_buffer_rsrc_t r, int at)
+{
+    if constexpr (sizeof(T) == 16) return __builtin_bit_cast(T, __builtin_amdgcn_raw_buffer_load_b128(r, at, 0, 0));
+    if constexpr (sizeof(T) == 8) return __builtin_bit_cast(T, __builtin_amdgcn_raw_buffer_load_b64(r, at, 0, 0));
+    if constexpr (sizeof(T) == 4) return __builtin_bit_cast(T, __builtin_amdgcn_raw_buffer_load_b32(r, at, 0, 0));
+    if constexpr (sizeof(T) == 2) return __builtin_bit_cast(T, __builtin_amdgcn_raw_buffer_load_b16(r, at, 0, 0));
+}
+template <class T>
+__device__ __forceinline__ void buffer_store(__amdgpu_buffer_rsrc_t r, int at, T x)
+{
+    if constexpr (sizeof(T) == 16) __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4_t, x), r, at, 0, 0);
+    if constexpr (sizeof(T) == 8) __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(u32x2_t, x), r, at, 0, 0);
+    if constexpr (sizeof(T) == 4) __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(uint32_t, x), r, at, 0, 0);
+    if constexpr (sizeof(T) == 2) __builtin_amdgcn_raw_buffer_store_b16(__builtin_bit_cast(uint16_t, x), r, at, 0, 0);
+}
+
 // A tile of ROWS x COLS elements on its way from global memory to LDS through
 // registers, 16 bytes at a time: load() for the next chunk is issued before a
 // chunk's products and store() after them, so that the loads are in flight
-// meanwhile. Rows from `rows` and columns from `cols` on become 0; their loads
-// go to the tile's first element instead of behind it.
+// meanwhile. Rows from `rows` and columns from `cols` on become 0.
 template <class T, int ROWS, int COLS, int THREADS>
 struct TileRegs {
     static constexpr int V = 16 / (int)sizeof(T), UNITS = COLS / V, ALL = ROWS * UNITS;
@@ -213,20 +261,20 @@ struct TileRegs {
 
     __device__ __forceinline__ void load(const T* src, int64_t ld, int rows, int cols, int tid)
     {
+        const auto rsrc = rows_rsrc(src, ld * (int)sizeof(T), rows, cols * (int)sizeof(T));
+        const int step = (int)ld * (int)sizeof(T);
 #pragma unroll
         for (int i = 0; i < N; ++i) {
             const int u = tid + i * THREADS, r = u / UNITS, c = u % UNITS * V;
-            const bool in = r < rows && c < cols && (ALL % THREADS == 0 || u < ALL);
-            x[i] = *reinterpret_cast<const VecT*>(src + (in ? r * ld + c : 0));
+            x[i] = buffer_load<VecT>(rsrc, r < rows && c < cols ? r * step + c * (int)sizeof(T) : kOutside);
         }
     }
-    __device__ __forceinline__ void store(T* tile, int stride, int rows, int cols, int tid) const
+    __device__ __forceinline__ void store(T* tile, int stride, int tid) const
     {
 #pragma unroll
         for (int i = 0; i < N; ++i) {
             const int u = tid + i * THREADS, r = u / UNITS, c = u % UNITS * V;
-            const bool in = r < rows && c < cols;
-            if (ALL % THREADS == 0 || u < ALL) *reinterpret_cast<VecT*>(tile + r * stride + c) = in ? x[i] : VecT{};
+            if (ALL % THREADS == 0 || u < ALL) *reinterpret_cast<VecT*>(tile + r * stride + c) = x[i];
         }
     }
 };
@@ -248,7 +296,7 @@ __device__ __forceinline__ void stage_tile(T* tile, int stride, const T* src, in
     if (vec) {
         TileRegs<T, ROWS, COLS, THREADS> x;
         x.load(src, ld, rows, cols, tid);
-        x.store(tile, stride, rows, cols, tid);
+        x.store(tile, stride, tid);
     } else {
         stage_elements<T, ROWS, COLS, THREADS>(tile, stride, src, ld, rows, cols, tid);
     }

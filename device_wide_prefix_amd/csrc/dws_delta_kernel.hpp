@@ -274,6 +274,84 @@ struct ScanLds {
     static constexpr size_t buffer = kq + tp + 3 * C * sizeof(float), bytes = 2 * buffer;
 };
 
+// What the two scans share: which columns of which sequence and head a wave
+// owns, and the state's transfer.
+template <int NW>
+struct ScanPlace {
+    int64_t seq, begin, len, slot0;
+    int h, hk, col0, col;
+    bool mine;
+};
+template <int C, int NW>
+__device__ __forceinline__ bool scan_place(const DeltaParams& p, int lane, int wave, ScanPlace<NW>* w)
+{
+    const uint32_t parts = (uint32_t)((p.dim_v + NW * 16 - 1) / (NW * 16));
+    uint32_t group, part;
+    xcd_split(blockIdx.x, parts, &group, &part);
+    if (group >= (uint64_t)p.n_seqs * p.heads_v) return false;
+    w->seq = group / p.heads_v;
+    w->h = group % p.heads_v;
+    w->hk = w->h / (p.heads_v / p.heads_qk);
+    w->col0 = (part * NW + wave) * 16;
+    w->col = w->col0 + (lane & 15);
+    w->mine = w->col < p.dim_v;
+    w->begin = seq_begin(p.offsets, p.tokens, p.n_seqs, w->seq);
+    w->len = seq_length(p.offsets, p.tokens, p.n_seqs, w->seq, w->begin);
+    w->slot0 = first_slot(w->begin, w->seq, C);
+    return true;
+}
+// A (dim_k x dim_v) state's 16 columns, laid out as results: element [t][r] of
+// a lane is row 16 t + 4 gq + r.
+template <int DK>
+__device__ __forceinline__ void load_state(f32x4 (&s)[DK / 16], const float* state, int dim_k, int dim_v, int col, int gq)
+{
+    const bool some = state != nullptr && col < dim_v;
+#pragma unroll
+    for (int t = 0; t < DK / 16; ++t)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            const int row = t * 16 + gq * 4 + r;
+            s[t][r] = some && row < dim_k ? state[(int64_t)row * dim_v + col] : 0.f;
+        }
+}
+// 16 columns of a chunk of a (tokens, dim) array, laid out as results.
+template <class T, int NB>
+struct ColumnRegs {
+    T x[NB * 4];
+
+    __device__ __forceinline__ void load(const T* first, int64_t ts, int rows, int dim, int col, int gq)
+    {
+        const auto rsrc = rows_rsrc(first, ts * (int)sizeof(T), rows, dim * (int)sizeof(T));
+        const int step = (int)ts * (int)sizeof(T);
+#pragma unroll
+        for (int i = 0; i < NB * 4; ++i) {
+            const int row = i / 4 * 16 + gq * 4 + i % 4;
+            x[i] = buffer_load<T>(rsrc, col < dim && row < rows ? row * step + col * (int)sizeof(T) : kOutside);
+        }
+    }
+    __device__ __forceinline__ f32x4 tile(int mt) const
+    {
+        return f32x4{(float)x[mt * 4], (float)x[mt * 4 + 1], (float)x[mt * 4 + 2], (float)x[mt * 4 + 3]};
+    }
+};
+// A state for the workspace, transposed: rows of DK, one a column of the value head.
+template <class T, int DK>
+__device__ __forceinline__ void store_columns(T* at, const f32x4 (&s)[DK / 16], int col, int dv_pad, int gq)
+{
+    if (col >= dv_pad) return;
+    T* to = at + col * DK + gq * 4;
+#pragma unroll
+    for (int t = 0; t < DK / 16; ++t) *reinterpret_cast<Vec4<T>*>(to + t * 16) = __builtin_convertvector(s[t], Vec4<T>);
+}
+template <class T, int NF, int C>
+__device__ __forceinline__ void store_columns(T* at, const f32x4 (&u)[C / 16], int col, int dv_pad, int gq)
+{
+    if (col >= dv_pad) return;
+#pragma unroll
+    for (int mt = 0; mt < C / 16; ++mt) store_parts4<NF>(at + col * C + mt * 16 + gq * 4, (int64_t)C * dv_pad, u[mt]);
+}
+__device__ __forceinline__ f32x4 gate4(const float* gate, int row) { return *reinterpret_cast<const f32x4*>(gate + row); }
+
 // STORE: instead of the outputs, the states at the chunks' starts and U' go to
 // the workspace (for the backward pass). NP: parts of the operands the state
 // depends on. NW waves, 16 columns of the value head each. Two LDS buffers: the
@@ -284,204 +362,169 @@ __global__ __launch_bounds__(NW * 64) void k_delta_scan(DeltaParams p)
 {
     constexpr int NF = kFine<T>, NX = NP > NF ? NP : NF;
     using L = ScanLds<T, DK, STORE ? 1 : 2, STORE ? NX : NX + NF>;
-    constexpr int C = L::C, THREADS = NW * 64, NB = C / 16, LK = L::LK, LC = L::LC;
+    constexpr int C = L::C, THREADS = NW * 64, NB = C / 16, LK = L::LK, LC = L::LC, NK = DK / 16;
     extern __shared__ __attribute__((aligned(16))) char smem[];
 
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, gq = lane >> 4, lr = lane & 15;
-    const uint32_t parts = (uint32_t)((p.dim_v + NW * 16 - 1) / (NW * 16));
-    uint32_t group, part;
-    xcd_split(blockIdx.x, parts, &group, &part);
-    if (group >= (uint64_t)p.n_seqs * p.heads_v) return;
-    const int64_t seq = group / p.heads_v;
-    const int h = group % p.heads_v, hk = h / (p.heads_v / p.heads_qk);
-    const int col0 = (part * NW + wave) * 16, col = col0 + lr;
-    const bool mine = col < p.dim_v;
+    ScanPlace<NW> w;
+    if (!scan_place<C, NW>(p, lane, wave, &w)) return;
     int64_t st;
-    if (!slot_taken<THREADS>(p.slots, p.n_states, seq, &st, tid)) return;
-    const int64_t begin = seq_begin(p.offsets, p.tokens, p.n_seqs, seq);
-    const int64_t len = seq_length(p.offsets, p.tokens, p.n_seqs, seq, begin);
-    const int64_t slot0 = first_slot(begin, seq, C);
-    const int64_t state_at = (st * p.heads_v + h) * p.dim_k * p.dim_v + col;
-    const T* k0 = static_cast<const T*>(p.k.data) + hk * p.k.hs;
-    const T* q0 = static_cast<const T*>(p.q.data) + hk * p.q.hs;
-    const T* v0 = static_cast<const T*>(p.v.data) + h * p.v.hs + (mine ? col : 0);
+    if (!slot_taken<THREADS>(p.slots, p.n_states, w.seq, &st, tid)) return;
+    const int64_t state_at = (st * p.heads_v + w.h) * p.dim_k * p.dim_v;
+    const T* k0 = static_cast<const T*>(p.k.data) + w.begin * p.k.ts + w.hk * p.k.hs;
+    const T* q0 = static_cast<const T*>(p.q.data) + w.begin * p.q.ts + w.hk * p.q.hs;
+    const T* v0 = static_cast<const T*>(p.v.data) + w.begin * p.v.ts + w.h * p.v.hs;
 
     TileRegs<T, C, DK, THREADS> kr, qr;
     TileRegs<T, NX * C, C, THREADS> tr;
     TileRegs<T, NF * C, C, THREADS> pr;
-    float gr[(3 * C + THREADS - 1) / THREADS];
-    T vr[NB * 4], vn[NB * 4];
-    auto rows_at = [&](int64_t c0) { return len - c0 < C ? (int)(len - c0) : C; };
-    // chunk c0 / C from global memory to registers
+    TileRegs<float, 3, C, THREADS> gr;
+    ColumnRegs<T, NB> vr;
+    auto rows_at = [&](int64_t c0) { return w.len - c0 < C ? (int)(w.len - c0) : C; };
+    // the chunk at c0, from global memory to registers
     auto load = [&](int64_t c0) {
         const int rows = rows_at(c0);
-        const int64_t row0 = begin + c0, at = (slot0 + c0 / C) * p.heads_v + h;
+        const int64_t at = (w.slot0 + c0 / C) * p.heads_v + w.h;
         if (p.vec) {
-            kr.load(k0 + row0 * p.k.ts, p.k.ts, rows, p.dim_k, tid);
-            if constexpr (!STORE) qr.load(q0 + row0 * p.q.ts, p.q.ts, rows, p.dim_k, tid);
+            kr.load(k0 + c0 * p.k.ts, p.k.ts, rows, p.dim_k, tid);
+            if constexpr (!STORE) qr.load(q0 + c0 * p.q.ts, p.q.ts, rows, p.dim_k, tid);
         }
         tr.load(static_cast<const T*>(p.w_t) + at * NX * C * C, C, NX * C, C, tid);
         if constexpr (!STORE) pr.load(static_cast<const T*>(p.w_p) + at * NF * C * C, C, NF * C, C, tid);
-#pragma unroll
-        for (int i = 0; i * THREADS < 3 * C; ++i)
-            gr[i] = p.w_gate[at * 3 * C + (tid + i * THREADS < 3 * C ? tid + i * THREADS : 0)];
-#pragma unroll
-        for (int mt = 0; mt < NB; ++mt)
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const int row = mt * 16 + gq * 4 + r;
-                vn[mt * 4 + r] = v0[(row0 + (row < rows ? row : 0)) * p.v.ts];
-            }
+        gr.load(p.w_gate + at * 3 * C, C, 3, C, tid);
+        vr.load(v0 + c0 * p.v.ts, p.v.ts, rows, p.dim_v, w.col, gq);
     };
     // and from there to an LDS buffer
     auto store = [&](int64_t c0, char* buffer) {
-        const int rows = rows_at(c0);
-        const int64_t row0 = begin + c0;
         T* ks = reinterpret_cast<T*>(buffer);
         T* ts = reinterpret_cast<T*>(buffer + L::kq);
-        float* gate = reinterpret_cast<float*>(buffer + L::kq + L::tp);
         if (p.vec) {
-            kr.store(ks, LK, rows, p.dim_k, tid);
-            if constexpr (!STORE) qr.store(ks + C * LK, LK, rows, p.dim_k, tid);
+            kr.store(ks, LK, tid);
+            if constexpr (!STORE) qr.store(ks + C * LK, LK, tid);
         } else {
-            stage_elements<T, C, DK, THREADS>(ks, LK, k0 + row0 * p.k.ts, p.k.ts, rows, p.dim_k, tid);
+            const int rows = rows_at(c0);
+            stage_elements<T, C, DK, THREADS>(ks, LK, k0 + c0 * p.k.ts, p.k.ts, rows, p.dim_k, tid);
             if constexpr (!STORE)
-                stage_elements<T, C, DK, THREADS>(ks + C * LK, LK, q0 + row0 * p.q.ts, p.q.ts, rows, p.dim_k, tid);
+                stage_elements<T, C, DK, THREADS>(ks + C * LK, LK, q0 + c0 * p.q.ts, p.q.ts, rows, p.dim_k, tid);
         }
-        tr.store(ts, LC, NX * C, C, tid);
-        if constexpr (!STORE) pr.store(ts + NX * C * LC, LC, NF * C, C, tid);
-#pragma unroll
-        for (int i = 0; i * THREADS < 3 * C; ++i)
-            if (tid + i * THREADS < 3 * C) gate[tid + i * THREADS] = gr[i];
+        tr.store(ts, LC, tid);
+        if constexpr (!STORE) pr.store(ts + NX * C * LC, LC, tid);
+        gr.store(reinterpret_cast<float*>(buffer + L::kq + L::tp), C, tid);
     };
 
-    f32x4 s[DK / 16];
-#pragma unroll
-    for (int t = 0; t < DK / 16; ++t)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-            const int row = t * 16 + gq * 4 + r;
-            s[t][r] = p.initial && mine && row < p.dim_k ? p.initial[state_at + (int64_t)row * p.dim_v] : 0.f;
-        }
-    if (len > 0) {
+    f32x4 s[NK];
+    load_state<DK>(s, p.initial ? p.initial + state_at : nullptr, p.dim_k, p.dim_v, w.col, gq);
+    if (w.len > 0) {
         load(0);
         store(0, smem);
     }
     int which = 0;
-    for (int64_t c0 = 0; c0 < len; c0 += C, which ^= 1) {
-        const int rows = rows_at(c0);
-        const int64_t row0 = begin + c0, at = (slot0 + c0 / C) * p.heads_v + h;
+    for (int64_t c0 = 0; c0 < w.len; c0 += C, which ^= 1) {
         char* buffer = smem + which * L::buffer;
         const T* ks = reinterpret_cast<const T*>(buffer);
         const T* qs = ks + C * LK;
         const T* ts = reinterpret_cast<const T*>(buffer + L::kq);
         const T* ps = ts + NX * C * LC;
         const float* gate = reinterpret_cast<const float*>(buffer + L::kq + L::tp);
+        f32x4 x[NB];
 #pragma unroll
-        for (int i = 0; i < NB * 4; ++i) vr[i] = vn[i];
+        for (int mt = 0; mt < NB; ++mt) x[mt] = vr.tile(mt);
         __syncthreads();
-        const bool more = c0 + C < len;
+        const bool more = c0 + C < w.len;
         if (more) load(c0 + C);
 
-        if constexpr (STORE) {
-            T* ws = static_cast<T*>(p.w_s) + at * DK * p.dv_pad + col;
-            if (col < p.dv_pad)
-#pragma unroll
-                for (int t = 0; t < DK / 16; ++t)
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) ws[(t * 16 + gq * 4 + r) * p.dv_pad] = (T)s[t][r];
-        }
+        const int64_t at = (w.slot0 + c0 / C) * p.heads_v + w.h;
+        if constexpr (STORE)
+            store_columns<T, DK>(static_cast<T*>(p.w_s) + at * DK * p.dv_pad, s, w.col, p.dv_pad, gq);
         Parts<T, NP> sb[DK / 32];
 #pragma unroll
         for (int kb = 0; kb < DK / 32; ++kb) sb[kb] = parts_of<T, NP>(s[2 * kb], s[2 * kb + 1]);
         // X = V - diag(e^G) K S
-        f32x4 x[NB];
+        {
+            f32x4 acc[NB] = {};
 #pragma unroll
-        for (int mt = 0; mt < NB; ++mt) {
-            f32x4 acc = {};
+            for (int kb = 0; kb < DK / 32; ++kb) {
+                Parts<T, 1> a[NB];
 #pragma unroll
-            for (int kb = 0; kb < DK / 32; ++kb) acc = mma(frag_acc(ks, LK, mt * 16, kb * 32, lane), sb[kb], acc);
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const int row = mt * 16 + gq * 4 + r;
-                x[mt][r] = (mine && row < rows ? (float)vr[mt * 4 + r] : 0.f) - gate[row] * acc[r];
+                for (int mt = 0; mt < NB; ++mt) a[mt].p[0] = frag_acc(ks, LK, mt * 16, kb * 32, lane);
+                mma_each(a, sb[kb], acc);
             }
-        }
-        Parts<T, NX> xb[C / 32];
 #pragma unroll
-        for (int kb = 0; kb < C / 32; ++kb) xb[kb] = parts_of<T, NX>(x[2 * kb], x[2 * kb + 1]);
+            for (int mt = 0; mt < NB; ++mt) x[mt] -= gate4(gate, mt * 16 + gq * 4) * acc[mt];
+        }
         // U' = (I + L B)^-1 X; u = B U'
-        f32x4 u[NB];
+        f32x4 u[NB] = {};
 #pragma unroll
-        for (int mt = 0; mt < NB; ++mt) {
-            f32x4 acc = {};
+        for (int kb = 0; kb < C / 32; ++kb) {
+            Parts<T, NX> a[NB];
 #pragma unroll
-            for (int kb = 0; kb <= mt / 2; ++kb)
-                acc = mma(parts_acc<NX>(ts, C * LC, LC, mt * 16, kb * 32, lane), xb[kb], acc);
-            if constexpr (STORE) {
-                T* wu = static_cast<T*>(p.w_u) + at * NF * C * p.dv_pad + col;
-                if (col < p.dv_pad)
-#pragma unroll
-                    for (int r = 0; r < 4; ++r)
-                        store_parts<NF>(wu + (mt * 16 + gq * 4 + r) * p.dv_pad, C * p.dv_pad, acc[r]);
-            }
-#pragma unroll
-            for (int r = 0; r < 4; ++r) u[mt][r] = gate[2 * C + mt * 16 + gq * 4 + r] * acc[r];
+            for (int mt = 2 * kb; mt < NB; ++mt) a[mt] = parts_acc<NX>(ts, C * LC, LC, mt * 16, kb * 32, lane);
+            mma_each(a, parts_of<T, NX>(x[2 * kb], x[2 * kb + 1]), u, 2 * kb);
         }
+        if constexpr (STORE)
+            store_columns<T, NF, C>(static_cast<T*>(p.w_u) + at * NF * C * p.dv_pad, u, w.col, p.dv_pad, gq);
+#pragma unroll
+        for (int mt = 0; mt < NB; ++mt) u[mt] *= gate4(gate, 2 * C + mt * 16 + gq * 4);
         if constexpr (!STORE) {
             // O transposed, so that a lane has four columns of one token: the
             // state and u in the place of the left operand
-            Parts<T, NF> ub[C / 32];
+            f32x4 o[NB] = {};
 #pragma unroll
-            for (int kb = 0; kb < C / 32; ++kb) ub[kb] = parts_of<T, NF>(u[2 * kb], u[2 * kb + 1]);
+            for (int kb = 0; kb < DK / 32; ++kb) {
+                Parts<T, 1> a[NB];
+#pragma unroll
+                for (int mt = 0; mt < NB; ++mt) a[mt].p[0] = frag_acc(qs, LK, mt * 16, kb * 32, lane);
+                mma_each<true>(a, Parts<T, 1>{{sb[kb].p[0]}}, o);
+            }
+#pragma unroll
+            for (int mt = 0; mt < NB; ++mt) o[mt] *= p.scale * gate[mt * 16 + lr];
+#pragma unroll
+            for (int kb = 0; kb < C / 32; ++kb) {
+                Parts<T, NF> a[NB];
+#pragma unroll
+                for (int mt = 2 * kb; mt < NB; ++mt) a[mt] = parts_acc<NF>(ps, C * LC, LC, mt * 16, kb * 32, lane);
+                mma_each<true>(a, parts_of<T, NF>(u[2 * kb], u[2 * kb + 1]), o, 2 * kb);
+            }
+            const int rows = rows_at(c0), c = w.col0 + gq * 4;
+            T* o0 = static_cast<T*>(p.out.data) + (w.begin + c0) * p.out.ts + w.h * p.out.hs;
+            const auto rsrc = rows_rsrc(o0, p.out.ts * (int)sizeof(T), rows, p.dim_v * (int)sizeof(T));
+            const int step = (int)p.out.ts * (int)sizeof(T);
 #pragma unroll
             for (int mt = 0; mt < NB; ++mt) {
-                f32x4 acc = {};
+                const int row = mt * 16 + lr, to = row < rows && c < p.dim_v ? row * step + c * (int)sizeof(T) : kOutside;
+                const Vec4<T> y = __builtin_convertvector(o[mt], Vec4<T>);
+                if (p.out4) {
+                    buffer_store(rsrc, to, y);
+                } else {
 #pragma unroll
-                for (int kb = 0; kb < DK / 32; ++kb)
-                    acc = mma(sb[kb].p[0], frag_acc(qs, LK, mt * 16, kb * 32, lane), acc);
-                const int row = mt * 16 + lr, c = col0 + gq * 4;
-                acc *= p.scale * gate[row];
-#pragma unroll
-                for (int kb = 0; kb <= mt / 2; ++kb)
-                    acc = mma(ub[kb], parts_acc<NF>(ps, C * LC, LC, mt * 16, kb * 32, lane), acc);
-                T* o = static_cast<T*>(p.out.data) + (row0 + row) * p.out.ts + h * p.out.hs + c;
-                if (row < rows) {
-                    if (p.out4) {
-                        if (c < p.dim_v) *reinterpret_cast<Vec4<T>*>(o) = __builtin_convertvector(acc, Vec4<T>);
-                    } else {
-#pragma unroll
-                        for (int r = 0; r < 4; ++r)
-                            if (c + r < p.dim_v) o[r] = (T)acc[r];
-                    }
+                    for (int r = 0; r < 4; ++r)
+                        buffer_store<T>(rsrc, c + r < p.dim_v ? to + r * (int)sizeof(T) : kOutside, y[r]);
                 }
             }
         }
         // S <- e^(G_C) S + K^T diag(e^(G_C - G)) u
 #pragma unroll
-        for (int mt = 0; mt < NB; ++mt)
-#pragma unroll
-            for (int r = 0; r < 4; ++r) u[mt][r] *= gate[C + mt * 16 + gq * 4 + r];
-        Parts<T, NX> ub[C / 32];
-#pragma unroll
-        for (int kb = 0; kb < C / 32; ++kb) ub[kb] = parts_of<T, NX>(u[2 * kb], u[2 * kb + 1]);
+        for (int mt = 0; mt < NB; ++mt) u[mt] *= gate4(gate, C + mt * 16 + gq * 4);
         const float keep = gate[C - 1];
 #pragma unroll
-        for (int t = 0; t < DK / 16; ++t) {
+        for (int t = 0; t < NK; ++t) s[t] *= keep;
 #pragma unroll
-            for (int r = 0; r < 4; ++r) s[t][r] *= keep;
+        for (int kb = 0; kb < C / 32; ++kb) {
+            const Parts<T, NX> ub = parts_of<T, NX>(u[2 * kb], u[2 * kb + 1]);
+            Parts<T, 1> a[NK];
 #pragma unroll
-            for (int kb = 0; kb < C / 32; ++kb) s[t] = mma(frag_tr(ks, LK, kb * 32, t * 16, lane), ub[kb], s[t]);
+            for (int t = 0; t < NK; ++t) a[t].p[0] = frag_tr(ks, LK, kb * 32, t * 16, lane);
+            mma_each(a, ub, s);
         }
         if (more) store(c0 + C, smem + (which ^ 1) * L::buffer);
     }
-    if (!STORE && p.final_state != nullptr && mine) {
+    if (!STORE && p.final_state != nullptr && w.mine) {
 #pragma unroll
-        for (int t = 0; t < DK / 16; ++t)
+        for (int t = 0; t < NK; ++t)
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
                 const int row = t * 16 + gq * 4 + r;
-                if (row < p.dim_k) p.final_state[state_at + (int64_t)row * p.dim_v] = s[t][r];
+                if (row < p.dim_k) p.final_state[state_at + (int64_t)row * p.dim_v + w.col] = s[t][r];
             }
     }
 }
@@ -494,141 +537,144 @@ __global__ __launch_bounds__(NW * 64) void k_delta_scan(DeltaParams p)
 // The same shape as the forward scan, from a sequence's last chunk to its
 // first. Z and dS' go to the workspace, dV to its place.
 
-template <class T, int DK>
-constexpr size_t scan_back_lds_bytes()
-{
-    constexpr int C = kChunk<T, DK>;
-    return 2 * (size_t)C * lds_stride<T>(DK) * sizeof(T) + 2 * kFine<T> * (size_t)C * lds_stride<T>(C) * sizeof(T) +
-           3 * C * sizeof(float);
-}
-
 template <class T, int DK, int NW>
 __global__ __launch_bounds__(NW * 64) void k_delta_scan_back(DeltaParams p)
 {
-    constexpr int C = kChunk<T, DK>, THREADS = NW * 64, NB = C / 16, LK = lds_stride<T>(DK), LC = lds_stride<T>(C);
     constexpr int NF = kFine<T>;
+    using L = ScanLds<T, DK, 2, 2 * NF>;
+    constexpr int C = L::C, THREADS = NW * 64, NB = C / 16, LK = L::LK, LC = L::LC, NK = DK / 16;
     extern __shared__ __attribute__((aligned(16))) char smem[];
-    T* ks = reinterpret_cast<T*>(smem);
-    T* qs = ks + C * LK;
-    T* ts = qs + C * LK;
-    T* ps = ts + NF * C * LC;
-    float* gate = reinterpret_cast<float*>(ps + NF * C * LC);
 
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, gq = lane >> 4, lr = lane & 15;
-    const uint32_t parts = (uint32_t)((p.dim_v + NW * 16 - 1) / (NW * 16));
-    uint32_t group, part;
-    xcd_split(blockIdx.x, parts, &group, &part);
-    if (group >= (uint64_t)p.n_seqs * p.heads_v) return;
-    const int64_t seq = group / p.heads_v;
-    const int h = group % p.heads_v, hk = h / (p.heads_v / p.heads_qk);
-    const int col = (part * NW + wave) * 16 + lr;
-    const bool mine = col < p.dim_v, held = col < p.dv_pad;
-    const int64_t begin = seq_begin(p.offsets, p.tokens, p.n_seqs, seq);
-    const int64_t len = seq_length(p.offsets, p.tokens, p.n_seqs, seq, begin);
-    const int64_t chunks = (len + C - 1) / C, slot0 = first_slot(begin, seq, C);
-    const int64_t state_at = (seq * p.heads_v + h) * p.dim_k * p.dim_v + col;
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, gq = lane >> 4;
+    ScanPlace<NW> w;
+    if (!scan_place<C, NW>(p, lane, wave, &w)) return;
+    const int64_t state_at = (w.seq * p.heads_v + w.h) * p.dim_k * p.dim_v;
+    const T* k0 = static_cast<const T*>(p.k.data) + w.begin * p.k.ts + w.hk * p.k.hs;
+    const T* q0 = static_cast<const T*>(p.q.data) + w.begin * p.q.ts + w.hk * p.q.hs;
+    const T* o0 = static_cast<const T*>(p.d_out.data) + w.begin * p.d_out.ts + w.h * p.d_out.hs;
 
-    f32x4 ds[DK / 16];
-#pragma unroll
-    for (int t = 0; t < DK / 16; ++t)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-            const int row = t * 16 + gq * 4 + r;
-            ds[t][r] = p.d_final && mine && row < p.dim_k ? p.d_final[state_at + (int64_t)row * p.dim_v] : 0.f;
+    TileRegs<T, C, DK, THREADS> kr, qr;
+    TileRegs<T, NF * C, C, THREADS> tr, pr;
+    TileRegs<float, 3, C, THREADS> gr;
+    ColumnRegs<T, NB> orr;
+    auto rows_at = [&](int64_t c0) { return w.len - c0 < C ? (int)(w.len - c0) : C; };
+    auto load = [&](int64_t c0) {
+        const int rows = rows_at(c0);
+        const int64_t at = (w.slot0 + c0 / C) * p.heads_v + w.h;
+        if (p.vec) {
+            kr.load(k0 + c0 * p.k.ts, p.k.ts, rows, p.dim_k, tid);
+            qr.load(q0 + c0 * p.q.ts, p.q.ts, rows, p.dim_k, tid);
         }
+        tr.load(static_cast<const T*>(p.w_tt) + at * NF * C * C, C, NF * C, C, tid);
+        pr.load(static_cast<const T*>(p.w_p) + at * NF * C * C, C, NF * C, C, tid);
+        gr.load(p.w_gate + at * 3 * C, C, 3, C, tid);
+        orr.load(o0 + c0 * p.d_out.ts, p.d_out.ts, rows, p.dim_v, w.col, gq);
+    };
+    auto store = [&](int64_t c0, char* buffer) {
+        T* ks = reinterpret_cast<T*>(buffer);
+        T* ts = reinterpret_cast<T*>(buffer + L::kq);
+        if (p.vec) {
+            kr.store(ks, LK, tid);
+            qr.store(ks + C * LK, LK, tid);
+        } else {
+            const int rows = rows_at(c0);
+            stage_elements<T, C, DK, THREADS>(ks, LK, k0 + c0 * p.k.ts, p.k.ts, rows, p.dim_k, tid);
+            stage_elements<T, C, DK, THREADS>(ks + C * LK, LK, q0 + c0 * p.q.ts, p.q.ts, rows, p.dim_k, tid);
+        }
+        tr.store(ts, LC, tid);
+        pr.store(ts + NF * C * LC, LC, tid);
+        gr.store(reinterpret_cast<float*>(buffer + L::kq + L::tp), C, tid);
+    };
 
-    for (int64_t c = chunks - 1; c >= 0; --c) {
-        const int64_t c0 = c * C, row0 = begin + c0, at = (slot0 + c) * p.heads_v + h;
-        const int rows = len - c0 < C ? (int)(len - c0) : C;
-        stage_tile<T, C, DK, THREADS>(ks, LK, static_cast<const T*>(p.k.data) + row0 * p.k.ts + hk * p.k.hs, p.k.ts, rows,
-                                      p.dim_k, p.vec, tid);
-        stage_tile<T, C, DK, THREADS>(qs, LK, static_cast<const T*>(p.q.data) + row0 * p.q.ts + hk * p.q.hs, p.q.ts, rows,
-                                      p.dim_k, p.vec, tid);
-        stage_tile<T, NF * C, C, THREADS>(ps, LC, static_cast<const T*>(p.w_p) + at * NF * C * C, C, NF * C, C, true, tid);
-        stage_tile<T, NF * C, C, THREADS>(ts, LC, static_cast<const T*>(p.w_tt) + at * NF * C * C, C, NF * C, C, true, tid);
-        for (int i = tid; i < 3 * C; i += THREADS) gate[i] = p.w_gate[at * 3 * C + i];
+    f32x4 ds[NK];
+    load_state<DK>(ds, p.d_final ? p.d_final + state_at : nullptr, p.dim_k, p.dim_v, w.col, gq);
+    const int64_t last = w.len > 0 ? (w.len - 1) / C * C : 0;
+    if (w.len > 0) {
+        load(last);
+        store(last, smem);
+    }
+    int which = 0;
+    for (int64_t c0 = last; c0 >= 0 && w.len > 0; c0 -= C, which ^= 1) {
+        char* buffer = smem + which * L::buffer;
+        const T* ks = reinterpret_cast<const T*>(buffer);
+        const T* qs = ks + C * LK;
+        const T* ts = reinterpret_cast<const T*>(buffer + L::kq);
+        const T* ps = ts + NF * C * LC;
+        const float* gate = reinterpret_cast<const float*>(buffer + L::kq + L::tp);
         f32x4 d_o[NB];
-        const T* o0 = static_cast<const T*>(p.d_out.data) + row0 * p.d_out.ts + h * p.d_out.hs + col;
 #pragma unroll
-        for (int mt = 0; mt < NB; ++mt)
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const int row = mt * 16 + gq * 4 + r;
-                d_o[mt][r] = mine && row < rows ? (float)o0[row * p.d_out.ts] : 0.f;
-            }
+        for (int mt = 0; mt < NB; ++mt) d_o[mt] = orr.tile(mt);
         __syncthreads();
+        if (c0 > 0) load(c0 - C);
 
-        T* wds = static_cast<T*>(p.w_ds) + at * DK * p.dv_pad + col;
-        if (held)
+        const int64_t at = (w.slot0 + c0 / C) * p.heads_v + w.h;
+        store_columns<T, DK>(static_cast<T*>(p.w_ds) + at * DK * p.dv_pad, ds, w.col, p.dv_pad, gq);
+        // dU
+        f32x4 z[NB] = {};
 #pragma unroll
-            for (int t = 0; t < DK / 16; ++t)
+        for (int kb = 0; kb < DK / 32; ++kb) {
+            Parts<T, 1> a[NB];
 #pragma unroll
-                for (int r = 0; r < 4; ++r) wds[(t * 16 + gq * 4 + r) * p.dv_pad] = (T)ds[t][r];
-        Parts<T, 1> db[DK / 32], ob[C / 32];     // dO is exact in T
-#pragma unroll
-        for (int kb = 0; kb < DK / 32; ++kb) db[kb] = parts_of<T, 1>(ds[2 * kb], ds[2 * kb + 1]);
-#pragma unroll
-        for (int kb = 0; kb < C / 32; ++kb) ob[kb] = parts_of<T, 1>(d_o[2 * kb], d_o[2 * kb + 1]);
-        f32x4 z[NB];
-#pragma unroll
-        for (int mt = 0; mt < NB; ++mt) {
-            f32x4 acc = {};
-#pragma unroll
-            for (int kb = 0; kb < DK / 32; ++kb) acc = mma(frag_acc(ks, LK, mt * 16, kb * 32, lane), db[kb], acc);
-#pragma unroll
-            for (int r = 0; r < 4; ++r) acc[r] *= gate[C + mt * 16 + gq * 4 + r];
-#pragma unroll
-            for (int kb = mt / 2; kb < C / 32; ++kb) acc = mma(parts_acc<NF>(ps, C * LC, LC, mt * 16, kb * 32, lane), ob[kb], acc);
-            z[mt] = acc;
+            for (int mt = 0; mt < NB; ++mt) a[mt].p[0] = frag_acc(ks, LK, mt * 16, kb * 32, lane);
+            mma_each(a, parts_of<T, 1>(ds[2 * kb], ds[2 * kb + 1]), z);
         }
-        Parts<T, NF> ub[C / 32];
 #pragma unroll
-        for (int kb = 0; kb < C / 32; ++kb) ub[kb] = parts_of<T, NF>(z[2 * kb], z[2 * kb + 1]);
-        T* wz = static_cast<T*>(p.w_z) + at * NF * C * p.dv_pad + col;
-        T* dv0 = static_cast<T*>(p.dv.data) + row0 * p.dv.ts + h * p.dv.hs + col;
-#pragma unroll
-        for (int mt = 0; mt < NB; ++mt) {
-            f32x4 acc = {};
-#pragma unroll
-            for (int kb = mt / 2; kb < C / 32; ++kb) acc = mma(parts_acc<NF>(ts, C * LC, LC, mt * 16, kb * 32, lane), ub[kb], acc);
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const int row = mt * 16 + gq * 4 + r;
-                if (held) store_parts<NF>(wz + row * p.dv_pad, C * p.dv_pad, acc[r]);
-                const float dx = gate[2 * C + row] * acc[r];
-                if (mine && row < rows) dv0[row * p.dv.ts] = (T)dx;
-                z[mt][r] = -gate[row] * dx;
-                d_o[mt][r] *= p.scale * gate[row];
-            }
-        }
-        Parts<T, 1> xb[C / 32];
-        Parts<T, NF> eb[C / 32];
+        for (int mt = 0; mt < NB; ++mt) z[mt] *= gate4(gate, C + mt * 16 + gq * 4);
 #pragma unroll
         for (int kb = 0; kb < C / 32; ++kb) {
-            xb[kb] = parts_of<T, 1>(z[2 * kb], z[2 * kb + 1]);
-            eb[kb] = parts_of<T, NF>(d_o[2 * kb], d_o[2 * kb + 1]);
+            Parts<T, NF> a[NB];
+#pragma unroll
+            for (int mt = 0; mt < 2 * kb + 2; ++mt) a[mt] = parts_acc<NF>(ps, C * LC, LC, mt * 16, kb * 32, lane);
+            mma_each(a, parts_of<T, 1>(d_o[2 * kb], d_o[2 * kb + 1]), z, 0, 2 * kb + 2);      // dO is exact in T
+        }
+        f32x4 y[NB] = {};
+#pragma unroll
+        for (int kb = 0; kb < C / 32; ++kb) {
+            Parts<T, NF> a[NB];
+#pragma unroll
+            for (int mt = 0; mt < 2 * kb + 2; ++mt) a[mt] = parts_acc<NF>(ts, C * LC, LC, mt * 16, kb * 32, lane);
+            mma_each(a, parts_of<T, NF>(z[2 * kb], z[2 * kb + 1]), y, 0, 2 * kb + 2);
+        }
+        store_columns<T, NF, C>(static_cast<T*>(p.w_z) + at * NF * C * p.dv_pad, y, w.col, p.dv_pad, gq);
+        const int rows = rows_at(c0);
+        T* dv0 = static_cast<T*>(p.dv.data) + (w.begin + c0) * p.dv.ts + w.h * p.dv.hs;
+        const auto rsrc = rows_rsrc(dv0, p.dv.ts * (int)sizeof(T), rows, p.dim_v * (int)sizeof(T));
+        const int step = (int)p.dv.ts * (int)sizeof(T);
+#pragma unroll
+        for (int mt = 0; mt < NB; ++mt) {
+            const int row = mt * 16 + gq * 4;
+            y[mt] *= gate4(gate, 2 * C + row);
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+                buffer_store<T>(rsrc, w.mine && row + r < rows ? (row + r) * step + w.col * (int)sizeof(T) : kOutside,
+                                (T)y[mt][r]);
+            const f32x4 eg = gate4(gate, row);
+            y[mt] *= -eg;
+            d_o[mt] *= p.scale * eg;
         }
         const float keep = gate[C - 1];
 #pragma unroll
-        for (int t = 0; t < DK / 16; ++t) {
+        for (int t = 0; t < NK; ++t) ds[t] *= keep;
 #pragma unroll
-            for (int r = 0; r < 4; ++r) ds[t][r] *= keep;
+        for (int kb = 0; kb < C / 32; ++kb) {
+            Parts<T, 1> a[NK];
 #pragma unroll
-            for (int kb = 0; kb < C / 32; ++kb) {
-                ds[t] = mma(frag_tr(qs, LK, kb * 32, t * 16, lane), eb[kb], ds[t]);
-                ds[t] = mma(frag_tr(ks, LK, kb * 32, t * 16, lane), xb[kb], ds[t]);
-            }
+            for (int t = 0; t < NK; ++t) a[t].p[0] = frag_tr(qs, LK, kb * 32, t * 16, lane);
+            mma_each(a, parts_of<T, NF>(d_o[2 * kb], d_o[2 * kb + 1]), ds);
+#pragma unroll
+            for (int t = 0; t < NK; ++t) a[t].p[0] = frag_tr(ks, LK, kb * 32, t * 16, lane);
+            mma_each(a, parts_of<T, 1>(y[2 * kb], y[2 * kb + 1]), ds);
         }
-        __syncthreads();
+        if (c0 > 0) store(c0 - C, smem + (which ^ 1) * L::buffer);
     }
-    if (p.d_initial != nullptr && mine) {
-        T* di = static_cast<T*>(p.d_initial);
+    if (p.d_initial != nullptr && w.mine) {
+        T* di = static_cast<T*>(p.d_initial) + state_at + w.col;
 #pragma unroll
-        for (int t = 0; t < DK / 16; ++t)
+        for (int t = 0; t < NK; ++t)
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
                 const int row = t * 16 + gq * 4 + r;
-                if (row < p.dim_k) di[state_at + (int64_t)row * p.dim_v] = (T)ds[t][r];
+                if (row < p.dim_k) di[(int64_t)row * p.dim_v] = (T)ds[t][r];
             }
     }
 }
@@ -645,53 +691,24 @@ __global__ __launch_bounds__(NW * 64) void k_delta_scan_back(DeltaParams p)
 //   dG_i = sum_j (N_ij - N_ji) + (scale e^G dO S^T)_i . q_i - (e^G B Z S^T)_i . k_i - w_i,
 //          w_i = (e^(G_C - G) B U' dS'^T)_i . k_i;   dG_C also gets sum w + e^(G_C) <S, dS'>
 //   dg_t = sum of dG_i from t to the chunk's end
-// One workgroup for each (chunk slot, query/key head), wave w the tokens
-// 16 w .. 16 w + 15; the value heads that share the key head in turn, so that
-// their sums need no atomics and have one order.
+// One workgroup for each (chunk slot, query/key head). A wave owns a row tile
+// of 16 tokens and 128 of the key columns (all, or half of 256); the value heads
+// that share the key head come in turn, so that their sums need no atomics and
+// have one order. The workspace's arrays have a row a value column: blocks of 32
+// go through LDS, where the transposing reads make operands of them.
 
 template <class T, int DK>
-constexpr size_t grad_lds_bytes()
-{
-    constexpr int C = kChunk<T, DK>;
-    return 2 * (size_t)C * lds_stride<T>(DK) * sizeof(T) + 2 * kFine<T> * (size_t)C * lds_stride<T>(C) * sizeof(T) +
-           (size_t)C * sizeof(double) + (6 * C + C / 16 * C + 16) * sizeof(float);
-}
-
-template <class T>
-__device__ __forceinline__ Vec8<T> frag_global(const T* base, int64_t ld, int r0, int c0, int lane)
-{
-    const T* p = base + (int64_t)(r0 + (lane & 15)) * ld + c0 + (lane >> 4) * 8;
-    if constexpr (sizeof(T) == 2) {
-        return *reinterpret_cast<const Vec8<T>*>(p);
-    } else {
-        const Vec4<T> a = *reinterpret_cast<const Vec4<T>*>(p), b = *reinterpret_cast<const Vec4<T>*>(p + 4);
-        return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
-    }
-}
-template <int NP, class T>
-__device__ __forceinline__ Parts<T, NP> parts_global(const T* base, int64_t step, int64_t ld, int r0, int c0, int lane)
-{
-    Parts<T, NP> a;
-#pragma unroll
-    for (int n = 0; n < NP; ++n) a.p[n] = frag_global(base + n * step, ld, r0, c0, lane);
-    return a;
-}
-// The same from a caller's array: zero outside rows x cols, and element by
-// element where 16-byte reads are not possible.
-template <class T>
-__device__ __forceinline__ Vec8<T> frag_user(const T* base, int64_t ld, int r0, int c0, int rows, int cols, bool vec,
-                                             int lane)
-{
-    const int r = r0 + (lane & 15), c = c0 + (lane >> 4) * 8;
-    Vec8<T> x = {};
-    if (r < rows) {
-        if (vec && c + 8 <= cols) return frag_global(base, ld, r0, c0, lane);
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-            if (c + j < cols) x[j] = base[(int64_t)r * ld + c + j];
-    }
-    return x;
-}
+struct GradLds {
+    static constexpr int C = kChunk<T, DK>, NB = C / 16, GROUPS = DK > 128 ? DK / 128 : 1, THREADS = NB * GROUPS * 64;
+    static constexpr int LK = lds_stride<T>(DK), LC = lds_stride<T>(C), NF = kFine<T>;
+    static constexpr size_t total = 0, ks = C * sizeof(double), qs = ks + (size_t)C * LK * sizeof(T);
+    static constexpr size_t w1 = qs + (size_t)C * LK * sizeof(T), w2 = w1 + (size_t)NF * C * LC * sizeof(T);
+    static constexpr size_t st = w2 + (size_t)NF * C * LC * sizeof(T), dst = st + (size_t)32 * LK * sizeof(T);
+    static constexpr size_t ut = dst + (size_t)32 * LK * sizeof(T), zt = ut + (size_t)NF * 32 * LC * sizeof(T);
+    static constexpr size_t gate = zt + (size_t)NF * 32 * LC * sizeof(T);
+    // floats behind: gate[3 C], row_part[GROUPS C], row_w[GROUPS C], d_beta[C], col_part[NB C], inner[THREADS / 64]
+    static constexpr size_t bytes = gate + ((4 + 2 * GROUPS + NB) * C + 16) * sizeof(float);
+};
 
 __device__ __forceinline__ float sum16(float x)      // over the 16 lanes of a group
 {
@@ -706,34 +723,52 @@ __device__ __forceinline__ float sum_groups(float x) // over the 4 groups
 }
 
 template <class T, int DK>
-__global__ __launch_bounds__((kChunk<T, DK> * 4)) void k_delta_grad(DeltaParams p)
+__global__ __launch_bounds__((GradLds<T, DK>::THREADS)) void k_delta_grad(DeltaParams p)
 {
-    constexpr int C = kChunk<T, DK>, THREADS = C * 4, NB = C / 16, NW = THREADS / 64, LK = lds_stride<T>(DK),
-                  LC = lds_stride<T>(C), NK = DK / 16, NF = kFine<T>;
+    using L = GradLds<T, DK>;
+    constexpr int C = L::C, THREADS = L::THREADS, NB = L::NB, GROUPS = L::GROUPS, LK = L::LK, LC = L::LC, NF = L::NF;
+    constexpr int NK = DK / 16 / GROUPS;             // key column tiles of a wave
     extern __shared__ __attribute__((aligned(16))) char smem[];
     double* total = reinterpret_cast<double*>(smem);
-    T* ks = reinterpret_cast<T*>(total + C);
-    T* qs = ks + C * LK;
-    T* w1 = qs + C * LK;
-    T* w2 = w1 + NF * C * LC;
-    float* gate = reinterpret_cast<float*>(w2 + NF * C * LC);     // e^G, e^(G_C - G), beta
-    float* row_part = gate + 3 * C;                          // dG without column sums and w
-    float* row_w = row_part + C;                             // w
-    float* d_beta = row_w + C;
-    float* col_part = d_beta + C;                            // [NW][C] column sums of N
-    float* inner = col_part + NB * C;                        // [NW] parts of <S, dS'>
+    T* ks = reinterpret_cast<T*>(smem + L::ks);
+    T* qs = reinterpret_cast<T*>(smem + L::qs);
+    T* w1 = reinterpret_cast<T*>(smem + L::w1);
+    T* w2 = reinterpret_cast<T*>(smem + L::w2);
+    T* st = reinterpret_cast<T*>(smem + L::st);
+    T* dst = reinterpret_cast<T*>(smem + L::dst);
+    T* ut = reinterpret_cast<T*>(smem + L::ut);
+    T* zt = reinterpret_cast<T*>(smem + L::zt);
+    float* gate = reinterpret_cast<float*>(smem + L::gate);      // e^G, e^(G_C - G), beta
+    float* row_part = gate + 3 * C;                              // dG without column sums and w
+    float* row_w = row_part + GROUPS * C;                        // w
+    float* d_beta = row_w + GROUPS * C;
+    float* col_part = d_beta + C;                                // [NB][C] column sums of N
+    float* inner = col_part + NB * C;                            // parts of <S, dS'>
 
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, gq = lane >> 4, lr = lane & 15;
+    const int tile = wave % NB, grp = wave / NB, row0 = tile * 16, key0 = grp * 128;
     const int64_t slot = blockIdx.x / p.heads_qk;
     const int hk = blockIdx.x % p.heads_qk, share = p.heads_v / p.heads_qk;
     const SlotInfo info = slot_info<C>(p.offsets, p.tokens, p.n_seqs, slot);
     if (info.rows == 0) return;
     const int rows = info.rows;
+
+    TileRegs<T, 32, DK, THREADS> sr, dsr;
+    TileRegs<T, 32, C, THREADS> ur[NF], zr[NF];
+    auto load = [&](int64_t at, int c) {
+        sr.load(static_cast<const T*>(p.w_s) + (at * p.dv_pad + c) * DK, DK, 32, DK, tid);
+        dsr.load(static_cast<const T*>(p.w_ds) + (at * p.dv_pad + c) * DK, DK, 32, DK, tid);
+#pragma unroll
+        for (int n = 0; n < NF; ++n) {
+            ur[n].load(static_cast<const T*>(p.w_u) + ((at * NF + n) * p.dv_pad + c) * C, C, 32, C, tid);
+            zr[n].load(static_cast<const T*>(p.w_z) + ((at * NF + n) * p.dv_pad + c) * C, C, 32, C, tid);
+        }
+    };
+    load(slot * p.heads_v + hk * share, 0);
     stage_tile<T, C, DK, THREADS>(ks, LK, static_cast<const T*>(p.k.data) + info.row * p.k.ts + hk * p.k.hs, p.k.ts, rows,
                                   p.dim_k, p.vec, tid);
     stage_tile<T, C, DK, THREADS>(qs, LK, static_cast<const T*>(p.q.data) + info.row * p.q.ts + hk * p.q.hs, p.q.ts, rows,
                                   p.dim_k, p.vec, tid);
-    __syncthreads();
     f32x4 dq[NK] = {}, dk[NK] = {};
 
     for (int m = 0; m < share; ++m) {
@@ -745,50 +780,75 @@ __global__ __launch_bounds__((kChunk<T, DK> * 4)) void k_delta_grad(DeltaParams 
             const double t = scan_decays<C>((double)g, lane);
             if (lane < C) total[lane] = t;
         }
-        __syncthreads();
 
         const T* d_o = static_cast<const T*>(p.d_out.data) + info.row * p.d_out.ts + h * p.d_out.hs;
-        const T* ws = static_cast<const T*>(p.w_s) + at * DK * p.dv_pad;
-        const T* wds = static_cast<const T*>(p.w_ds) + at * DK * p.dv_pad;
-        const T* wu = static_cast<const T*>(p.w_u) + at * NF * C * p.dv_pad;
-        const T* wz = static_cast<const T*>(p.w_z) + at * NF * C * p.dv_pad;
+        const auto o_rsrc = rows_rsrc(d_o, p.d_out.ts * (int)sizeof(T), rows, p.dim_v * (int)sizeof(T));
+        const int o_at = (row0 + lr) * (int)p.d_out.ts;
         f32x4 dp[NB] = {}, zu[NB] = {}, os[NK] = {}, zs[NK] = {}, us[NK] = {};
         float zdotu = 0.f, sds = 0.f;
         for (int c = 0; c < p.dv_pad; c += 32) {
-            const Vec8<T> ao = frag_user(d_o, p.d_out.ts, wave * 16, c, rows, p.dim_v, p.vec, lane);
-            const Parts<T, NF> az = parts_global<NF>(wz, C * p.dv_pad, p.dv_pad, wave * 16, c, lane);
-            const Parts<T, NF> au = parts_global<NF>(wu, C * p.dv_pad, p.dv_pad, wave * 16, c, lane);
+            // dO's rows of this wave, 32 columns in acc order
+            Parts<T, 1> ao;
+            if (p.vec) {
+                const int o0 = c + gq * 4, o1 = o0 + 16;
+                const bool in = row0 + lr < rows;
+                const Vec4<T> a = buffer_load<Vec4<T>>(o_rsrc, in && o0 < p.dim_v ? (o_at + o0) * (int)sizeof(T) : kOutside);
+                const Vec4<T> b = buffer_load<Vec4<T>>(o_rsrc, in && o1 < p.dim_v ? (o_at + o1) * (int)sizeof(T) : kOutside);
+                ao.p[0] = __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
+            } else {
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                float z = 0.f, u = 0.f;
-#pragma unroll
-                for (int n = NF - 1; n >= 0; --n) {
-                    z += (float)az.p[n][j];
-                    u += (float)au.p[n][j];
+                for (int j = 0; j < 8; ++j) {
+                    const int o = c + gq * 4 + j % 4 + j / 4 * 16;
+                    ao.p[0][j] = buffer_load<T>(o_rsrc, row0 + lr < rows && o < p.dim_v ? (o_at + o) * (int)sizeof(T) : kOutside);
                 }
-                zdotu += z * u;
             }
+            sr.store(st, LK, tid);
+            dsr.store(dst, LK, tid);
+#pragma unroll
+            for (int n = 0; n < NF; ++n) {
+                ur[n].store(ut + n * 32 * LC, LC, tid);
+                zr[n].store(zt + n * 32 * LC, LC, tid);
+            }
+            __syncthreads();
+            if (c + 32 < p.dv_pad)
+                load(at, c + 32);
+            else if (m + 1 < share)
+                load(at + 1, 0);
+            const Parts<T, NF> az = parts_tr<NF>(zt, 32 * LC, LC, 0, row0, lane);
+            const Parts<T, NF> au = parts_tr<NF>(ut, 32 * LC, LC, 0, row0, lane);
+            if (grp == 0)
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    float z = 0.f, u = 0.f;
+#pragma unroll
+                    for (int n = NF - 1; n >= 0; --n) {
+                        z += (float)az.p[n][j];
+                        u += (float)au.p[n][j];
+                    }
+                    zdotu += z * u;
+                }
 #pragma unroll
             for (int nt = 0; nt < NB; ++nt)
-                if (nt <= wave) {
-                    const Parts<T, NF> b = parts_global<NF>(wu, C * p.dv_pad, p.dv_pad, nt * 16, c, lane);
+                if (nt <= tile && nt % GROUPS == grp) {
+                    const Parts<T, NF> b = parts_tr<NF>(ut, 32 * LC, LC, 0, nt * 16, lane);
                     dp[nt] = mma(ao, b, dp[nt]);
                     zu[nt] = mma(az, b, zu[nt]);
                 }
 #pragma unroll
             for (int t = 0; t < NK; ++t) {
-                const Vec8<T> b = frag_global(ws, p.dv_pad, t * 16, c, lane);
-                const Vec8<T> d = frag_global(wds, p.dv_pad, t * 16, c, lane);
+                const Parts<T, 1> b = {{frag_tr(st, LK, 0, key0 + t * 16, lane)}};
+                const Parts<T, 1> d = {{frag_tr(dst, LK, 0, key0 + t * 16, lane)}};
                 os[t] = mma(ao, b, os[t]);
                 zs[t] = mma(az.p[0], b, zs[t]);
-                us[t] = mma(au, Parts<T, 1>{{d}}, us[t]);
-                if (t % NW == wave)
+                us[t] = mma(au, d, us[t]);
+                if (t % NB == tile)
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) sds += (float)b[j] * (float)d[j];
+                    for (int j = 0; j < 8; ++j) sds += (float)b.p[0][j] * (float)d.p[0][j];
             }
+            __syncthreads();
         }
-        zdotu = sum_groups(zdotu);               // lane: row lr of the wave's 16
-        if (gq == 0) d_beta[wave * 16 + lr] = zdotu;
+        zdotu = sum_groups(zdotu);               // lane: row lr of the tile
+        if (gq == 0 && grp == 0) d_beta[row0 + lr] = zdotu;
         sds = sum_groups(sum16(sds));
         if (lane == 0) inner[wave] = sds;
 
@@ -796,22 +856,23 @@ __global__ __launch_bounds__((kChunk<T, DK> * 4)) void k_delta_grad(DeltaParams 
         float nrow[4] = {};
 #pragma unroll
         for (int nt = 0; nt < NB; ++nt) {
+            if (nt % GROUPS != grp) continue;
             const int j = nt * 16 + lr;
             float ncol = 0.f;
             f32x4 kk = {}, qk = {};
-            if (nt <= wave) {
+            if (nt <= tile) {
 #pragma unroll
                 for (int kb = 0; kb < DK; kb += 32) {
                     const Vec8<T> b = frag_nat(ks, LK, nt * 16, kb, lane);
-                    kk = mma(frag_nat(ks, LK, wave * 16, kb, lane), b, kk);
-                    qk = mma(frag_nat(qs, LK, wave * 16, kb, lane), b, qk);
+                    kk = mma(frag_nat(ks, LK, row0, kb, lane), b, kk);
+                    qk = mma(frag_nat(qs, LK, row0, kb, lane), b, qk);
                 }
             }
             const float bj = gate[2 * C + j];
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
-                const int i = wave * 16 + gq * 4 + r;
-                const float d = i >= j ? expf((float)(total[i] - total[j])) : 0.f;
+                const int i = row0 + gq * 4 + r;
+                const float d = i > j ? expf((float)(total[i] - total[j])) : (i == j ? 1.f : 0.f);
                 const float a = i >= j ? p.scale * d * bj * dp[nt][r] : 0.f;
                 const float b = i > j ? -gate[2 * C + i] * d * bj * zu[nt][r] : 0.f;
                 store_parts<NF>(w1 + i * LC + j, C * LC, a);
@@ -821,7 +882,7 @@ __global__ __launch_bounds__((kChunk<T, DK> * 4)) void k_delta_grad(DeltaParams 
                 ncol += n;
             }
             ncol = sum_groups(ncol);
-            if (gq == 0) col_part[wave * C + j] = ncol;
+            if (gq == 0) col_part[tile * C + j] = ncol;
         }
         __syncthreads();
 
@@ -831,8 +892,8 @@ __global__ __launch_bounds__((kChunk<T, DK> * 4)) void k_delta_grad(DeltaParams 
         for (int t = 0; t < NK; ++t)
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
-                const int i = wave * 16 + gq * 4 + r;
-                const float qv = (float)qs[i * LK + t * 16 + lr], kv = (float)ks[i * LK + t * 16 + lr];
+                const int i = row0 + gq * 4 + r, c = key0 + t * 16 + lr;
+                const float qv = (float)qs[i * LK + c], kv = (float)ks[i * LK + c];
                 const float b = gate[2 * C + i];
                 const float a1 = p.scale * gate[i] * os[t][r], a2 = gate[i] * b * zs[t][r];
                 const float a3 = gate[C + i] * b * us[t][r];
@@ -845,21 +906,21 @@ __global__ __launch_bounds__((kChunk<T, DK> * 4)) void k_delta_grad(DeltaParams 
         for (int r = 0; r < 4; ++r) {
             const float a = sum16(grow[r] + nrow[r]), b = sum16(gw[r]);
             if (lr == 0) {
-                row_part[wave * 16 + gq * 4 + r] = a;
-                row_w[wave * 16 + gq * 4 + r] = b;
+                row_part[grp * C + row0 + gq * 4 + r] = a;
+                row_w[grp * C + row0 + gq * 4 + r] = b;
             }
         }
         // the products with K and Q: rows i of W1 and W2 for dQ and dK, columns for dK
 #pragma unroll
         for (int kb = 0; kb < C / 32; ++kb) {
-            const Parts<T, NF> a1 = parts_acc<NF>(w1, C * LC, LC, wave * 16, kb * 32, lane);
-            const Parts<T, NF> a2 = parts_acc<NF>(w2, C * LC, LC, wave * 16, kb * 32, lane);
-            const Parts<T, NF> b1 = parts_tr<NF>(w1, C * LC, LC, kb * 32, wave * 16, lane);
-            const Parts<T, NF> b2 = parts_tr<NF>(w2, C * LC, LC, kb * 32, wave * 16, lane);
+            const Parts<T, NF> a1 = parts_acc<NF>(w1, C * LC, LC, row0, kb * 32, lane);
+            const Parts<T, NF> a2 = parts_acc<NF>(w2, C * LC, LC, row0, kb * 32, lane);
+            const Parts<T, NF> b1 = parts_tr<NF>(w1, C * LC, LC, kb * 32, row0, lane);
+            const Parts<T, NF> b2 = parts_tr<NF>(w2, C * LC, LC, kb * 32, row0, lane);
 #pragma unroll
             for (int t = 0; t < NK; ++t) {
-                const Parts<T, 1> kt = {{frag_tr(ks, LK, kb * 32, t * 16, lane)}};
-                const Parts<T, 1> qt = {{frag_tr(qs, LK, kb * 32, t * 16, lane)}};
+                const Parts<T, 1> kt = {{frag_tr(ks, LK, kb * 32, key0 + t * 16, lane)}};
+                const Parts<T, 1> qt = {{frag_tr(qs, LK, kb * 32, key0 + t * 16, lane)}};
                 dq[t] = mma(a1, kt, dq[t]);
                 dk[t] = mma(b1, qt, dk[t]);
                 dk[t] = mma(a2, kt, dk[t]);
@@ -870,14 +931,18 @@ __global__ __launch_bounds__((kChunk<T, DK> * 4)) void k_delta_grad(DeltaParams 
         if (wave == 0) {
             float x = 0.f, w = 0.f;
             if (lane < C) {
-                w = row_w[lane];
-                x = row_part[lane] - w;
 #pragma unroll
-                for (int i = 0; i < NW; ++i) x -= col_part[i * C + lane];
+                for (int i = 0; i < GROUPS; ++i) {
+                    w += row_w[i * C + lane];
+                    x += row_part[i * C + lane];
+                }
+                x -= w;
+#pragma unroll
+                for (int i = 0; i < NB; ++i) x -= col_part[i * C + lane];
             }
             float wsum = sum_groups(sum16(w)), in = 0.f;
 #pragma unroll
-            for (int i = 0; i < NW; ++i) in += inner[i];
+            for (int i = 0; i < NB * GROUPS; ++i) in += inner[i];
             if (lane == C - 1) x += wsum + gate[C - 1] * in;
             // sums from each token to the chunk's end
 #pragma unroll
@@ -895,15 +960,16 @@ __global__ __launch_bounds__((kChunk<T, DK> * 4)) void k_delta_grad(DeltaParams 
     }
     T* q0 = static_cast<T*>(p.dq.data) + info.row * p.dq.ts + hk * p.dq.hs;
     T* k0 = static_cast<T*>(p.dk.data) + info.row * p.dk.ts + hk * p.dk.hs;
+    const auto q_rsrc = rows_rsrc(q0, p.dq.ts * (int)sizeof(T), rows, p.dim_k * (int)sizeof(T));
+    const auto k_rsrc = rows_rsrc(k0, p.dk.ts * (int)sizeof(T), rows, p.dim_k * (int)sizeof(T));
 #pragma unroll
     for (int t = 0; t < NK; ++t)
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-            const int i = wave * 16 + gq * 4 + r, c = t * 16 + lr;
-            if (i < rows && c < p.dim_k) {
-                q0[i * p.dq.ts + c] = (T)dq[t][r];
-                k0[i * p.dk.ts + c] = (T)dk[t][r];
-            }
+            const int i = row0 + gq * 4 + r, c = key0 + t * 16 + lr;
+            const bool in = i < rows && c < p.dim_k;
+            buffer_store<T>(q_rsrc, in ? (i * (int)p.dq.ts + c) * (int)sizeof(T) : kOutside, (T)dq[t][r]);
+            buffer_store<T>(k_rsrc, in ? (i * (int)p.dk.ts + c) * (int)sizeof(T) : kOutside, (T)dk[t][r]);
         }
 }
 
@@ -959,9 +1025,10 @@ hipError_t backward_dk(const DeltaParams& p, hipStream_t stream)
     e = launch_lds(k_delta_scan<T, DK, 1, true, NW>, scan_blocks(p, NW), NW * 64, ScanLds<T, DK, 1, kFine<T>>::bytes, p,
                    stream);
     if (e != hipSuccess) return e;
-    e = launch_lds(k_delta_scan_back<T, DK, NW>, scan_blocks(p, NW), NW * 64, scan_back_lds_bytes<T, DK>(), p, stream);
+    e = launch_lds(k_delta_scan_back<T, DK, NW>, scan_blocks(p, NW), NW * 64, ScanLds<T, DK, 2, 2 * kFine<T>>::bytes, p, stream);
     if (e != hipSuccess) return e;
-    return launch_lds(k_delta_grad<T, DK>, (uint64_t)p.n_slots * p.heads_qk, C * 4, grad_lds_bytes<T, DK>(), p, stream);
+    return launch_lds(k_delta_grad<T, DK>, (uint64_t)p.n_slots * p.heads_qk, GradLds<T, DK>::THREADS,
+                      GradLds<T, DK>::bytes, p, stream);
 }
 template <class T>
 hipError_t backward_type(const DeltaParams& p, hipStream_t stream)

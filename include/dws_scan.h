@@ -527,8 +527,8 @@ dws_status dws_reduce_op(const void* d_in, size_t n, dws_dtype dtype, dws_op op,
  */
 
 /* A (tokens, heads, dim) array on the device: element (t, h, d) is at
- * t * token_stride + h * head_stride + d (strides in elements, not negative,
- * below 2^40). Inputs may repeat elements (a stride of 0); outputs may not. */
+ * t * token_stride + h * head_stride + d (strides in elements, not negative;
+ * below 2^22 between tokens and 2^40 between heads). Inputs may repeat elements (a stride of 0); outputs may not. */
 typedef struct dws_rows {
     void* data;
     long long token_stride;
@@ -601,7 +601,8 @@ dws_status dws_delta_rule_workspace(const dws_delta_rule_args* args, int backwar
  * strides or types out of range, heads_v not a multiple of heads_qk, tokens not
  * a multiple of n_seqs without d_offsets, a workspace that is too small, or an
  * output that names an element twice give DWS_ERR_INVALID_ARG; a dimension above
- * 256 or more chunks and heads than a launch holds, DWS_ERR_UNSUPPORTED; a
+ * 256, a token stride of 2^22 or more chunks and heads than a launch holds,
+ * DWS_ERR_UNSUPPORTED; a
  * pointer not aligned to its element, DWS_ERR_MISALIGNED; an output or the
  * workspace whose range meets another operand's, DWS_ERR_OVERLAP. Asynchronous on
  * `stream`, allocates nothing, may be captured.
