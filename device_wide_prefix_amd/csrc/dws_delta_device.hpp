@@ -18,6 +18,10 @@
 
 namespace dws {
 
+// One wave a SIMD: the kernel's LDS allows no more workgroups, so the compiler
+// may as well use all 512 registers to have reads in flight.
+#define DWS_ONE_WAVE __attribute__((amdgpu_waves_per_eu(1, 1)))
+
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef float f32x8 __attribute__((ext_vector_type(8)));
 typedef __bf16 bf16_t;
@@ -231,6 +235,14 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t rows_rsrc(const void* first, i
     return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(first), (short)0,
                                              (int)((rows - 1) * row_bytes) + bytes, kRsrcFlags);
 }
+template <int BYTES>
+struct Bits {
+    typedef uint32_t type;
+};
+template <>
+struct Bits<2> {
+    typedef uint16_t type;
+};
 template <class T>
 __device__ __forceinline__ T buffer_load(__amdgpu_buffer_rsrc_t r, int at)
 {

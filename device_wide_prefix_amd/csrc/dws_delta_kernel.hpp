@@ -305,19 +305,35 @@ __device__ __forceinline__ bool scan_place(const DeltaParams& p, int lane, int w
 template <int DK>
 __device__ __forceinline__ void load_state(f32x4 (&s)[DK / 16], const float* state, int dim_k, int dim_v, int col, int gq)
 {
-    const bool some = state != nullptr && col < dim_v;
+    // a resource over dim_k rows of the state, or over none
+    const auto rsrc = rows_rsrc(state, (int64_t)dim_v * 4, state != nullptr ? dim_k : 1, state != nullptr ? dim_v * 4 : 0);
 #pragma unroll
     for (int t = 0; t < DK / 16; ++t)
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
             const int row = t * 16 + gq * 4 + r;
-            s[t][r] = some && row < dim_k ? state[(int64_t)row * dim_v + col] : 0.f;
+            s[t][r] = buffer_load<float>(rsrc, col < dim_v && row < dim_k ? (row * dim_v + col) * 4 : kOutside);
+        }
+}
+template <int DK, class T>
+__device__ __forceinline__ void store_state(const f32x4 (&s)[DK / 16], T* state, int dim_k, int dim_v, int col, int gq)
+{
+    const auto rsrc = rows_rsrc(state, (int64_t)dim_v * (int)sizeof(T), dim_k, dim_v * (int)sizeof(T));
+#pragma unroll
+    for (int t = 0; t < DK / 16; ++t)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            const int row = t * 16 + gq * 4 + r;
+            buffer_store<T>(rsrc, col < dim_v && row < dim_k ? (row * dim_v + col) * (int)sizeof(T) : kOutside, (T)s[t][r]);
         }
 }
 // 16 columns of a chunk of a (tokens, dim) array, laid out as results.
 template <class T, int NB>
 struct ColumnRegs {
-    T x[NB * 4];
+    // one element a register: two 16-bit ones in one would have to be put
+    // together, and waited for, where they are loaded
+    typedef typename Bits<sizeof(T)>::type BitsT;
+    uint32_t x[NB * 4];
 
     __device__ __forceinline__ void load(const T* first, int64_t ts, int rows, int dim, int col, int gq)
     {
@@ -326,12 +342,15 @@ struct ColumnRegs {
 #pragma unroll
         for (int i = 0; i < NB * 4; ++i) {
             const int row = i / 4 * 16 + gq * 4 + i % 4;
-            x[i] = buffer_load<T>(rsrc, col < dim && row < rows ? row * step + col * (int)sizeof(T) : kOutside);
+            x[i] = buffer_load<BitsT>(rsrc, col < dim && row < rows ? row * step + col * (int)sizeof(T) : kOutside);
         }
     }
     __device__ __forceinline__ f32x4 tile(int mt) const
     {
-        return f32x4{(float)x[mt * 4], (float)x[mt * 4 + 1], (float)x[mt * 4 + 2], (float)x[mt * 4 + 3]};
+        f32x4 y;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) y[r] = (float)__builtin_bit_cast(T, (BitsT)x[mt * 4 + r]);
+        return y;
     }
 };
 // A state for the workspace, transposed: rows of DK, one a column of the value head.
@@ -358,7 +377,7 @@ __device__ __forceinline__ f32x4 gate4(const float* gate, int row) { return *rei
 // next chunk's tiles are written to one while the other is read, so a chunk
 // needs one barrier, and the loads of the one after that are in flight.
 template <class T, int DK, int NP, bool STORE, int NW>
-__global__ __launch_bounds__(NW * 64) void k_delta_scan(DeltaParams p)
+__global__ __launch_bounds__(NW * 64) DWS_ONE_WAVE void k_delta_scan(DeltaParams p)
 {
     constexpr int NF = kFine<T>, NX = NP > NF ? NP : NF;
     using L = ScanLds<T, DK, STORE ? 1 : 2, STORE ? NX : NX + NF>;
@@ -518,15 +537,7 @@ __global__ __launch_bounds__(NW * 64) void k_delta_scan(DeltaParams p)
         }
         if (more) store(c0 + C, smem + (which ^ 1) * L::buffer);
     }
-    if (!STORE && p.final_state != nullptr && w.mine) {
-#pragma unroll
-        for (int t = 0; t < NK; ++t)
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const int row = t * 16 + gq * 4 + r;
-                if (row < p.dim_k) p.final_state[state_at + (int64_t)row * p.dim_v + w.col] = s[t][r];
-            }
-    }
+    if (!STORE && p.final_state != nullptr) store_state<DK>(s, p.final_state + state_at, p.dim_k, p.dim_v, w.col, gq);
 }
 
 // ---- the backward scan -----------------------------------------------------
@@ -538,7 +549,7 @@ __global__ __launch_bounds__(NW * 64) void k_delta_scan(DeltaParams p)
 // first. Z and dS' go to the workspace, dV to its place.
 
 template <class T, int DK, int NW>
-__global__ __launch_bounds__(NW * 64) void k_delta_scan_back(DeltaParams p)
+__global__ __launch_bounds__(NW * 64) DWS_ONE_WAVE void k_delta_scan_back(DeltaParams p)
 {
     constexpr int NF = kFine<T>;
     using L = ScanLds<T, DK, 2, 2 * NF>;
@@ -667,16 +678,8 @@ __global__ __launch_bounds__(NW * 64) void k_delta_scan_back(DeltaParams p)
         }
         if (c0 > 0) store(c0 - C, smem + (which ^ 1) * L::buffer);
     }
-    if (p.d_initial != nullptr && w.mine) {
-        T* di = static_cast<T*>(p.d_initial) + state_at + w.col;
-#pragma unroll
-        for (int t = 0; t < NK; ++t)
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const int row = t * 16 + gq * 4 + r;
-                if (row < p.dim_k) di[(int64_t)row * p.dim_v] = (T)ds[t][r];
-            }
-    }
+    if (p.d_initial != nullptr)
+        store_state<DK>(ds, static_cast<T*>(p.d_initial) + state_at, p.dim_k, p.dim_v, w.col, gq);
 }
 
 // ---- the gradients of q, k and the gates ------------------------------------
@@ -723,7 +726,7 @@ __device__ __forceinline__ float sum_groups(float x) // over the 4 groups
 }
 
 template <class T, int DK>
-__global__ __launch_bounds__((GradLds<T, DK>::THREADS)) void k_delta_grad(DeltaParams p)
+__global__ __launch_bounds__((GradLds<T, DK>::THREADS)) DWS_ONE_WAVE void k_delta_grad(DeltaParams p)
 {
     using L = GradLds<T, DK>;
     constexpr int C = L::C, THREADS = L::THREADS, NB = L::NB, GROUPS = L::GROUPS, LK = L::LK, LC = L::LC, NF = L::NF;
