@@ -15,6 +15,8 @@ constexpr int delta_padded_k(int dim_k) { return dim_k <= 64 ? 64 : (dim_k <= 12
 constexpr int delta_chunk(int dtype, int dim_k) { return dtype == DWS_FLOAT32 || dim_k > 128 ? 32 : 64; }
 // Columns of a value head are laid out in the workspace in whole 32s.
 constexpr int delta_padded_v(int dim_v) { return (dim_v + 31) / 32 * 32; }
+// Elements of a triangular matrix's fragments (Triangle in the kernels).
+constexpr int delta_triangle(int chunk) { return (chunk == 64 ? 6 : 2) * 512; }
 
 // Parts (numbers of the input type whose sum is the value) of the operands
 // computed in fp32: those of a chunk's size, and all that a final state depends on.
@@ -34,7 +36,6 @@ struct DeltaParams {
     int heads_qk, heads_v, dim_k, dim_v, dv_pad;
     float scale;
     int g_dtype, beta_dtype;
-    int vec;                     // q and k rows (and d_out's) are whole, aligned 16-byte units
     int out4;                    // out's rows are whole, aligned units of four elements
     DeltaRows q, k, v, g, beta, out;
     const float* initial;        // (n_seqs or n_states, heads_v, dim_k, dim_v)
@@ -49,23 +50,35 @@ struct DeltaParams {
     // workspace
     int64_t n_slots;             // chunk slots: tokens / chunk + n_seqs + 1 (the last ones empty)
     float* w_gate;               // [slot][head][3][chunk]: e^G, e^(G_C - G), beta
-    void* w_t;                   // [slot][head][parts][chunk][chunk]: (I + L diag(beta))^-1
-    void* w_p;                   // [slot][head][fine][chunk][chunk]: P (forward), its transpose (backward)
-    void* w_tt;                  // [slot][head][fine][chunk][chunk]: transpose of (I + diag(beta) L)^-1 (backward)
+    // triangular matrices as operand fragments (Triangle in the kernels)
+    void* w_t;                   // [slot][head][parts][frags]: (I + L diag(beta))^-1
+    void* w_p;                   // [slot][head][fine][frags]: P (forward), its transpose (backward)
+    void* w_tt;                  // [slot][head][fine][frags]: transpose of (I + diag(beta) L)^-1 (backward)
     void* w_s;                   // [slot][head][dv_pad][padded dim_k]: states at the chunks' starts
     void* w_u;                   // [slot][head][fine][dv_pad][chunk]: U'
     void* w_z;                   // [slot][head][fine][dv_pad][chunk]: Z
     void* w_ds;                  // [slot][head][dv_pad][padded dim_k]: state gradients at the chunks' ends
 };
 
+// Arrays that are copied to the workspace first, since their rows are not whole
+// 16-byte units; the parameters name the copies.
+struct DeltaPack {
+    struct {
+        DeltaRows src;
+        void* dst;
+        int heads, dim, padded;
+    } rows[4];
+    int n;
+};
+
 // Per-type launchers (dws_delta_{bf16,f16,f32}.hip). `precise`: the final
 // state is wanted, with fp32 accuracy.
-hipError_t launch_delta_forward_bf16(const DeltaParams& p, bool precise, hipStream_t stream);
-hipError_t launch_delta_forward_f16(const DeltaParams& p, bool precise, hipStream_t stream);
-hipError_t launch_delta_forward_f32(const DeltaParams& p, bool precise, hipStream_t stream);
-hipError_t launch_delta_backward_bf16(const DeltaParams& p, hipStream_t stream);
-hipError_t launch_delta_backward_f16(const DeltaParams& p, hipStream_t stream);
-hipError_t launch_delta_backward_f32(const DeltaParams& p, hipStream_t stream);
+hipError_t launch_delta_forward_bf16(const DeltaParams& p, const DeltaPack& k, bool precise, hipStream_t stream);
+hipError_t launch_delta_forward_f16(const DeltaParams& p, const DeltaPack& k, bool precise, hipStream_t stream);
+hipError_t launch_delta_forward_f32(const DeltaParams& p, const DeltaPack& k, bool precise, hipStream_t stream);
+hipError_t launch_delta_backward_bf16(const DeltaParams& p, const DeltaPack& k, hipStream_t stream);
+hipError_t launch_delta_backward_f16(const DeltaParams& p, const DeltaPack& k, hipStream_t stream);
+hipError_t launch_delta_backward_f32(const DeltaParams& p, const DeltaPack& k, hipStream_t stream);
 
 struct DeltaStepParams {
     int64_t tokens, n_seqs;

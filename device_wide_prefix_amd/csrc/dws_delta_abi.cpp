@@ -89,8 +89,22 @@ bool whole_units(const DeltaRows& a, int dim, int dtype, int bytes)
     return reinterpret_cast<uintptr_t>(a.data) % bytes == 0 && dim % v == 0 && a.ts % v == 0 && a.hs % v == 0;
 }
 
+// Operand i of q, k, v, d_out: whether its rows have to be copied, and the
+// copy's row length, whole 16-byte units.
+struct Packed {
+    bool needed;
+    int heads, dim, padded;
+};
+Packed packed_of(const dws_delta_rule_args* a, int i)
+{
+    const dws_rows& r = i == 0 ? a->q : (i == 1 ? a->k : (i == 2 ? a->v : a->out_grad));
+    const int dim = i < 2 ? a->dim_k : a->dim_v, unit = 16 / (int)size_of(a->dtype);
+    const bool whole = whole_units({r.data, r.token_stride, r.head_stride}, dim, a->dtype, 16);
+    return {a->tokens > 0 && !whole, i < 2 ? a->heads_qk : a->heads_v, dim, (dim + unit - 1) / unit * unit};
+}
+
 struct Sizes {
-    size_t gate, t, p, tt, s, u, z, ds;    // offsets
+    size_t gate, t, p, tt, s, u, z, ds, pack[4];    // offsets
     size_t bytes;
     int64_t n_slots;
 };
@@ -129,17 +143,37 @@ Sizes workspace_of(const dws_delta_rule_args* a, bool backward, bool precise)
         return was;
     };
     z.gate = take(n * 3 * c * sizeof(float));
-    z.t = take(n * c * c * e * (precise ? (size_t)delta_precise_parts(a->dtype) : fine));
-    z.p = take(n * c * c * e * fine);
+    const size_t tri = (size_t)delta_triangle((int)c) * e;
+    z.t = take(n * tri * (precise ? (size_t)delta_precise_parts(a->dtype) : fine));
+    z.p = take(n * tri * fine);
     if (backward) {
-        z.tt = take(n * c * c * e * fine);
+        z.tt = take(n * tri * fine);
         z.s = take(n * dk * dv * e);
         z.u = take(n * c * dv * e * fine);
         z.z = take(n * c * dv * e * fine);
         z.ds = take(n * dk * dv * e);
     }
+    const int kinds = backward ? 4 : 3;
+    for (int i = 0; i < kinds; ++i) {
+        const Packed k = packed_of(a, i);
+        z.pack[i] = at;
+        if (k.needed) take((size_t)a->tokens * k.heads * k.padded * e);
+    }
     z.bytes = at;
     return z;
+}
+
+// Points the parameters at the copies of rows that are not whole 16-byte units.
+void pack(const dws_delta_rule_args* a, const Sizes& z, bool backward, DeltaParams* p, DeltaPack* k)
+{
+    DeltaRows* rows[] = {&p->q, &p->k, &p->v, &p->d_out};
+    for (int i = 0; i < (backward ? 4 : 3); ++i) {
+        const Packed of = packed_of(a, i);
+        if (!of.needed) continue;
+        auto& r = k->rows[k->n++];
+        r = {*rows[i], static_cast<char*>(a->d_workspace) + z.pack[i], of.heads, of.dim, of.padded};
+        *rows[i] = {r.dst, (int64_t)of.heads * of.padded, of.padded};
+    }
 }
 
 bool is_precise(const dws_delta_rule_args* a) { return a->d_final_state != nullptr && a->dtype != DWS_FLOAT32; }
@@ -204,7 +238,6 @@ dws_status forward_entry(const dws_delta_rule_args* a, hipStream_t stream)
     if (a->d_workspace == nullptr || a->workspace_bytes < z.bytes) return DWS_ERR_INVALID_ARG;
     if ((st = r.add(a->d_workspace, z.bytes, true, 256)) != DWS_OK) return st;
     if (r.overlap()) return DWS_ERR_OVERLAP;
-    p.vec = whole_units(p.q, a->dim_k, a->dtype, 16) && whole_units(p.k, a->dim_k, a->dtype, 16);
     p.out4 = whole_units(p.out, a->dim_v, a->dtype, 4 * (int)size_of(a->dtype));
     p.initial = a->d_initial_state;
     p.final_state = a->d_final_state;
@@ -216,10 +249,12 @@ dws_status forward_entry(const dws_delta_rule_args* a, hipStream_t stream)
     p.w_gate = reinterpret_cast<float*>(w + z.gate);
     p.w_t = w + z.t;
     p.w_p = w + z.p;
+    DeltaPack k{};
+    pack(a, z, false, &p, &k);
     switch (a->dtype) {
-    case DWS_BFLOAT16: return status_of(launch_delta_forward_bf16(p, precise, stream));
-    case DWS_FLOAT16: return status_of(launch_delta_forward_f16(p, precise, stream));
-    default: return status_of(launch_delta_forward_f32(p, precise, stream));
+    case DWS_BFLOAT16: return status_of(launch_delta_forward_bf16(p, k, precise, stream));
+    case DWS_FLOAT16: return status_of(launch_delta_forward_f16(p, k, precise, stream));
+    default: return status_of(launch_delta_forward_f32(p, k, precise, stream));
     }
 }
 
@@ -249,8 +284,6 @@ dws_status backward_entry(const dws_delta_rule_args* a, hipStream_t stream)
     if (a->d_workspace == nullptr || a->workspace_bytes < z.bytes) return DWS_ERR_INVALID_ARG;
     if ((st = r.add(a->d_workspace, z.bytes, true, 256)) != DWS_OK) return st;
     if (r.overlap()) return DWS_ERR_OVERLAP;
-    p.vec = whole_units(p.q, a->dim_k, a->dtype, 16) && whole_units(p.k, a->dim_k, a->dtype, 16) &&
-            whole_units(p.d_out, a->dim_v, a->dtype, 16);
     p.initial = a->d_initial_state;
     p.d_final = a->d_final_grad;
     p.d_initial = a->d_initial_grad;
@@ -265,10 +298,12 @@ dws_status backward_entry(const dws_delta_rule_args* a, hipStream_t stream)
     p.w_u = w + z.u;
     p.w_z = w + z.z;
     p.w_ds = w + z.ds;
+    DeltaPack k{};
+    pack(a, z, true, &p, &k);
     switch (a->dtype) {
-    case DWS_BFLOAT16: return status_of(launch_delta_backward_bf16(p, stream));
-    case DWS_FLOAT16: return status_of(launch_delta_backward_f16(p, stream));
-    default: return status_of(launch_delta_backward_f32(p, stream));
+    case DWS_BFLOAT16: return status_of(launch_delta_backward_bf16(p, k, stream));
+    case DWS_FLOAT16: return status_of(launch_delta_backward_f16(p, k, stream));
+    default: return status_of(launch_delta_backward_f32(p, k, stream));
     }
 }
 

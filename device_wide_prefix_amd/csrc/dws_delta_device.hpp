@@ -18,9 +18,10 @@
 
 namespace dws {
 
-// One wave a SIMD: the kernel's LDS allows no more workgroups, so the compiler
-// may as well use all 512 registers to have reads in flight.
+// Waves a SIMD: the kernels' LDS allows no more workgroups, so the compiler may
+// as well use all 512 (or 256) registers to have reads in flight.
 #define DWS_ONE_WAVE __attribute__((amdgpu_waves_per_eu(1, 1)))
+#define DWS_TWO_WAVES __attribute__((amdgpu_waves_per_eu(2, 2)))
 
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef float f32x8 __attribute__((ext_vector_type(8)));
@@ -235,14 +236,11 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t rows_rsrc(const void* first, i
     return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(first), (short)0,
                                              (int)((rows - 1) * row_bytes) + bytes, kRsrcFlags);
 }
-template <int BYTES>
-struct Bits {
-    typedef uint32_t type;
-};
-template <>
-struct Bits<2> {
-    typedef uint16_t type;
-};
+// Bytes of a row's elements in whole 16-byte units: the units are there (copied
+// rows are padded), and a unit's last dwords are checked by themselves.
+template <class T>
+__device__ __forceinline__ int whole_bytes(int elems) { return (elems * (int)sizeof(T) + 15) & ~15; }
+
 template <class T>
 __device__ __forceinline__ T buffer_load(__amdgpu_buffer_rsrc_t r, int at)
 {
@@ -273,7 +271,7 @@ struct TileRegs {
 
     __device__ __forceinline__ void load(const T* src, int64_t ld, int rows, int cols, int tid)
     {
-        const auto rsrc = rows_rsrc(src, ld * (int)sizeof(T), rows, cols * (int)sizeof(T));
+        const auto rsrc = rows_rsrc(src, ld * (int)sizeof(T), rows, whole_bytes<T>(cols));
         const int step = (int)ld * (int)sizeof(T);
 #pragma unroll
         for (int i = 0; i < N; ++i) {
@@ -290,27 +288,15 @@ struct TileRegs {
         }
     }
 };
-// The same straight from global memory, element by element: rows that are not
-// whole 16-byte units.
-template <class T, int ROWS, int COLS, int THREADS>
-__device__ __forceinline__ void stage_elements(T* tile, int stride, const T* src, int64_t ld, int rows, int cols, int tid)
+// 8 elements as an operand.
+template <class T>
+__device__ __forceinline__ Vec8<T> buffer_frag(__amdgpu_buffer_rsrc_t r, int at)
 {
-    for (int i = tid; i < ROWS * COLS; i += THREADS) {
-        const int r = i / COLS, c = i % COLS;
-        tile[r * stride + c] = r < rows && c < cols ? src[r * ld + c] : (T)0.f;
-    }
-}
-// A caller's tile, in either way.
-template <class T, int ROWS, int COLS, int THREADS>
-__device__ __forceinline__ void stage_tile(T* tile, int stride, const T* src, int64_t ld, int rows, int cols, bool vec,
-                                           int tid)
-{
-    if (vec) {
-        TileRegs<T, ROWS, COLS, THREADS> x;
-        x.load(src, ld, rows, cols, tid);
-        x.store(tile, stride, tid);
+    if constexpr (sizeof(T) == 2) {
+        return buffer_load<Vec8<T>>(r, at);
     } else {
-        stage_elements<T, ROWS, COLS, THREADS>(tile, stride, src, ld, rows, cols, tid);
+        const Vec4<T> a = buffer_load<Vec4<T>>(r, at), b = buffer_load<Vec4<T>>(r, at == kOutside ? at : at + 16);
+        return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
     }
 }
 

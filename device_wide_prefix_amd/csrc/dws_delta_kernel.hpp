@@ -36,6 +36,37 @@ constexpr int kFine = sizeof(T) == 4 ? 1 : 2;
 template <class T>
 constexpr int kPrecise = __is_same(T, bf16_t) ? 3 : kFine<T>;
 
+// ---- triangular chunk x chunk matrices as operands -------------------------
+
+// Where four consecutive elements (row, col .. col + 3) of a lower (upper)
+// triangular C x C matrix are when it is kept as operand fragments of 16 rows
+// and 32 columns, 64 lanes x 8 elements each: only the fragments that are not
+// all zero, each read with one 16-byte access a lane (two for fp32). `acc` and
+// `nat`: the order of the contraction.
+template <int C>
+struct Triangle {
+    static constexpr int frags = C == 64 ? 6 : 2, elems = frags * 512;
+    static __device__ constexpr bool in_lower(int row, int col) { return col / 32 <= row / 32; }
+    static __device__ constexpr bool in_upper(int row, int col) { return col / 32 >= row / 32; }
+    // fragment (row tile mt, column block kb)
+    static __device__ constexpr int lower(int mt, int kb) { return kb == 0 ? mt : 2 + mt; }
+    static __device__ constexpr int upper(int mt, int kb) { return kb == 0 ? mt : 2 + mt; }
+    static __device__ constexpr int acc(int row, int col) { return ((col % 16 / 4) * 16 + row % 16) * 8 + col % 32 / 16 * 4; }
+    static __device__ constexpr int nat(int row, int col) { return ((col % 32 / 8) * 16 + row % 16) * 8 + col % 8; }
+    static __device__ constexpr int lower_acc(int row, int col) { return lower(row / 16, col / 32) * 512 + acc(row, col); }
+    static __device__ constexpr int lower_nat(int row, int col) { return lower(row / 16, col / 32) * 512 + nat(row, col); }
+    static __device__ constexpr int upper_acc(int row, int col) { return upper(row / 16, col / 32) * 512 + acc(row, col); }
+};
+// The parts of fragment f.
+template <int NP, class T>
+__device__ __forceinline__ Parts<T, NP> parts_at(const T* frags, int elems, int f, int lane)
+{
+    Parts<T, NP> a;
+#pragma unroll
+    for (int n = 0; n < NP; ++n) a.p[n] = frag_nat(frags + n * elems + f * 512 + lane * 8, 0, 0, 0, 0);
+    return a;
+}
+
 // ---- the inverse of a unit lower triangular matrix -----------------------
 
 // fp32 product of two 16-row, 16-column blocks of LDS matrices (rows of LD):
@@ -190,8 +221,11 @@ __global__ __launch_bounds__((kChunk<T, DK> * 4)) void k_delta_prep(DeltaParams 
         if (p.g.data) g = clamp_decay(load_gate(p.g, info.row + lane, h, p.g_dtype));
         b = load_gate(p.beta, info.row + lane, h, p.beta_dtype);
     }
-    stage_tile<T, C, DK, THREADS>(ks, LK, k0, p.k.ts, info.rows, p.dim_k, p.vec, tid);
-    stage_tile<T, C, DK, THREADS>(qs, LK, q0, p.q.ts, info.rows, p.dim_k, p.vec, tid);
+    TileRegs<T, C, DK, THREADS> kr, qr;
+    kr.load(k0, p.k.ts, info.rows, p.dim_k, tid);
+    qr.load(q0, p.q.ts, info.rows, p.dim_k, tid);
+    kr.store(ks, LK, tid);
+    qr.store(qs, LK, tid);
     if (wave == 0) {
         const double sum = scan_decays<C>((double)g, lane);
         const double last = __shfl(sum, C - 1, 64);
@@ -207,7 +241,8 @@ __global__ __launch_bounds__((kChunk<T, DK> * 4)) void k_delta_prep(DeltaParams 
     __syncthreads();
 
     // row tile `wave` of K K^T and Q K^T, up to the diagonal. m = L B.
-    T* wp = static_cast<T*>(p.w_p) + at * NF * C * C;
+    using F = Triangle<C>;
+    T* wp = static_cast<T*>(p.w_p) + at * NF * F::elems;
     f32x4 low[BWD ? NB : 1];      // B L
 #pragma unroll
     for (int nt = 0; nt < NB; ++nt) {
@@ -235,16 +270,19 @@ __global__ __launch_bounds__((kChunk<T, DK> * 4)) void k_delta_prep(DeltaParams 
             const float e = BWD ? d : (pi > pj ? expf((float)(total[pi] - total[pj])) : 0.f);
             pij[r] = pi > pj ? p.scale * e * qk[r] : (pi == pj ? p.scale * qk[r] : 0.f);
         }
-        T* to = BWD ? wp + (nt * 16 + lr) * C + wave * 16 + gq * 4 : wp + (wave * 16 + lr) * C + nt * 16 + gq * 4;
-        store_parts4<NF>(to, C * C, pij);
+        if (BWD ? F::in_upper(nt * 16, wave * 16) : F::in_lower(wave * 16, nt * 16))
+            store_parts4<NF>(wp + (BWD ? F::upper_acc(nt * 16 + lr, wave * 16 + gq * 4)
+                                       : F::lower_nat(wave * 16 + lr, nt * 16 + gq * 4)),
+                             F::elems, pij);
     }
     __syncthreads();
 
     invert_unit_lower<C>(m, inv, tmp, wave, lane);
-    T* wt = static_cast<T*>(p.w_t) + at * NX * C * C;
+    T* wt = static_cast<T*>(p.w_t) + at * NX * F::elems;
     for (int i = tid; i < C * C / 4; i += THREADS) {
-        const float* x = inv + i / (C / 4) * LD + i % (C / 4) * 4;
-        store_parts4<NX>(wt + i * 4, C * C, f32x4{x[0], x[1], x[2], x[3]});
+        const int row = i / (C / 4), c = i % (C / 4) * 4;
+        const float* x = inv + row * LD + c;
+        if (F::in_lower(row, c)) store_parts4<NX>(wt + F::lower_acc(row, c), F::elems, f32x4{x[0], x[1], x[2], x[3]});
     }
     if constexpr (BWD) {
         // the other inverse, of I + B L
@@ -255,35 +293,45 @@ __global__ __launch_bounds__((kChunk<T, DK> * 4)) void k_delta_prep(DeltaParams 
             for (int r = 0; r < 4; ++r) m[(wave * 16 + gq * 4 + r) * LD + nt * 16 + lr] = low[nt][r];
         __syncthreads();
         invert_unit_lower<C>(m, inv, tmp, wave, lane);
-        T* wtt = static_cast<T*>(p.w_tt) + at * NF * C * C;
+        T* wtt = static_cast<T*>(p.w_tt) + at * NF * F::elems;
         for (int i = tid; i < C * C / 4; i += THREADS) {
-            const float* x = inv + i % (C / 4) * 4 * LD + i / (C / 4);
-            store_parts4<NF>(wtt + i * 4, C * C, f32x4{x[0], x[LD], x[2 * LD], x[3 * LD]});
+            const int row = i / (C / 4), c = i % (C / 4) * 4;       // of the transposed
+            const float* x = inv + c * LD + row;
+            if (F::in_upper(row, c))
+                store_parts4<NF>(wtt + F::upper_acc(row, c), F::elems, f32x4{x[0], x[LD], x[2 * LD], x[3 * LD]});
         }
     }
 }
 
-// ---- the forward scan ------------------------------------------------------
+// ---- the scans --------------------------------------------------------------
+//
+// A workgroup goes through one sequence's chunks for NW x 16 columns of a value
+// head. Its first NW waves carry the states, 16 columns each: what they do from
+// chunk to chunk is the time that no parallelism takes away, so they do nothing
+// else. NW more waves, one on each of the same SIMDs, bring the next chunk's
+// tiles to LDS and work out the outputs of the last one from the states and u
+// that were left in LDS. Two LDS buffers and one barrier a chunk.
 
-// LDS of a scan workgroup, two of each but for the tiles of a caller's arrays
-// that cannot be read 16 bytes at a time.
-template <class T, int DK, int KQ, int TP>
+// LDS of a scan workgroup: KQ tiles of keys or queries, TP triangular matrices,
+// the columns of V or dO and the gate factors; with OUT, the states and u on
+// their way to the outputs.
+template <class T, int DK, int NW, int KQ, int TP, bool OUT>
 struct ScanLds {
-    static constexpr int C = kChunk<T, DK>, LK = lds_stride<T>(DK), LC = lds_stride<T>(C);
-    static constexpr size_t kq = KQ * (size_t)C * LK * sizeof(T), tp = TP * (size_t)C * LC * sizeof(T);
-    static constexpr size_t buffer = kq + tp + 3 * C * sizeof(float), bytes = 2 * buffer;
+    static constexpr int C = kChunk<T, DK>, LK = lds_stride<T>(DK), LC = lds_stride<T>(C), LV = lds_stride<T>(NW * 16);
+    static constexpr size_t ks = 0, ts = ks + KQ * (size_t)C * LK * sizeof(T);
+    static constexpr size_t vs = ts + TP * (size_t)Triangle<C>::elems * sizeof(T);
+    static constexpr size_t gate = vs + (size_t)C * LV * sizeof(T), sx = gate + 3 * C * sizeof(float);
+    static constexpr size_t ux = sx + (OUT ? (size_t)NW * 16 * LK * sizeof(T) : 0);
+    static constexpr size_t buffer = ux + (OUT ? kFine<T> * (size_t)NW * 16 * LC * sizeof(T) : 0), bytes = 2 * buffer;
 };
 
-// What the two scans share: which columns of which sequence and head a wave
-// owns, and the state's transfer.
-template <int NW>
+// Which columns of which sequence and head a workgroup goes through.
 struct ScanPlace {
     int64_t seq, begin, len, slot0;
-    int h, hk, col0, col;
-    bool mine;
+    int h, hk, first;       // first column of the workgroup
 };
 template <int C, int NW>
-__device__ __forceinline__ bool scan_place(const DeltaParams& p, int lane, int wave, ScanPlace<NW>* w)
+__device__ __forceinline__ bool scan_place(const DeltaParams& p, ScanPlace* w)
 {
     const uint32_t parts = (uint32_t)((p.dim_v + NW * 16 - 1) / (NW * 16));
     uint32_t group, part;
@@ -292,9 +340,7 @@ __device__ __forceinline__ bool scan_place(const DeltaParams& p, int lane, int w
     w->seq = group / p.heads_v;
     w->h = group % p.heads_v;
     w->hk = w->h / (p.heads_v / p.heads_qk);
-    w->col0 = (part * NW + wave) * 16;
-    w->col = w->col0 + (lane & 15);
-    w->mine = w->col < p.dim_v;
+    w->first = part * NW * 16;
     w->begin = seq_begin(p.offsets, p.tokens, p.n_seqs, w->seq);
     w->len = seq_length(p.offsets, p.tokens, p.n_seqs, w->seq, w->begin);
     w->slot0 = first_slot(w->begin, w->seq, C);
@@ -327,32 +373,6 @@ __device__ __forceinline__ void store_state(const f32x4 (&s)[DK / 16], T* state,
             buffer_store<T>(rsrc, col < dim_v && row < dim_k ? (row * dim_v + col) * (int)sizeof(T) : kOutside, (T)s[t][r]);
         }
 }
-// 16 columns of a chunk of a (tokens, dim) array, laid out as results.
-template <class T, int NB>
-struct ColumnRegs {
-    // one element a register: two 16-bit ones in one would have to be put
-    // together, and waited for, where they are loaded
-    typedef typename Bits<sizeof(T)>::type BitsT;
-    uint32_t x[NB * 4];
-
-    __device__ __forceinline__ void load(const T* first, int64_t ts, int rows, int dim, int col, int gq)
-    {
-        const auto rsrc = rows_rsrc(first, ts * (int)sizeof(T), rows, dim * (int)sizeof(T));
-        const int step = (int)ts * (int)sizeof(T);
-#pragma unroll
-        for (int i = 0; i < NB * 4; ++i) {
-            const int row = i / 4 * 16 + gq * 4 + i % 4;
-            x[i] = buffer_load<BitsT>(rsrc, col < dim && row < rows ? row * step + col * (int)sizeof(T) : kOutside);
-        }
-    }
-    __device__ __forceinline__ f32x4 tile(int mt) const
-    {
-        f32x4 y;
-#pragma unroll
-        for (int r = 0; r < 4; ++r) y[r] = (float)__builtin_bit_cast(T, (BitsT)x[mt * 4 + r]);
-        return y;
-    }
-};
 // A state for the workspace, transposed: rows of DK, one a column of the value head.
 template <class T, int DK>
 __device__ __forceinline__ void store_columns(T* at, const f32x4 (&s)[DK / 16], int col, int dv_pad, int gq)
@@ -371,105 +391,168 @@ __device__ __forceinline__ void store_columns(T* at, const f32x4 (&u)[C / 16], i
 }
 __device__ __forceinline__ f32x4 gate4(const float* gate, int row) { return *reinterpret_cast<const f32x4*>(gate + row); }
 
+
 // STORE: instead of the outputs, the states at the chunks' starts and U' go to
 // the workspace (for the backward pass). NP: parts of the operands the state
-// depends on. NW waves, 16 columns of the value head each. Two LDS buffers: the
-// next chunk's tiles are written to one while the other is read, so a chunk
-// needs one barrier, and the loads of the one after that are in flight.
+// depends on.
 template <class T, int DK, int NP, bool STORE, int NW>
-__global__ __launch_bounds__(NW * 64) DWS_ONE_WAVE void k_delta_scan(DeltaParams p)
+__global__ __launch_bounds__(NW * 128) DWS_TWO_WAVES void k_delta_scan(DeltaParams p)
 {
     constexpr int NF = kFine<T>, NX = NP > NF ? NP : NF;
-    using L = ScanLds<T, DK, STORE ? 1 : 2, STORE ? NX : NX + NF>;
-    constexpr int C = L::C, THREADS = NW * 64, NB = C / 16, LK = L::LK, LC = L::LC, NK = DK / 16;
+    using L = ScanLds<T, DK, NW, 1, NX, !STORE>;
+    constexpr int C = L::C, THREADS = NW * 64, NB = C / 16, LK = L::LK, LC = L::LC, LV = L::LV, NK = DK / 16;
+    using F = Triangle<C>;
     extern __shared__ __attribute__((aligned(16))) char smem[];
 
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, gq = lane >> 4, lr = lane & 15;
-    ScanPlace<NW> w;
-    if (!scan_place<C, NW>(p, lane, wave, &w)) return;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) % NW;
+    const int gq = lane >> 4, lr = lane & 15;
+    ScanPlace w;
+    if (!scan_place<C, NW>(p, &w)) return;
     int64_t st;
-    if (!slot_taken<THREADS>(p.slots, p.n_states, w.seq, &st, tid)) return;
+    if (!slot_taken<2 * THREADS>(p.slots, p.n_states, w.seq, &st, threadIdx.x)) return;
     const int64_t state_at = (st * p.heads_v + w.h) * p.dim_k * p.dim_v;
-    const T* k0 = static_cast<const T*>(p.k.data) + w.begin * p.k.ts + w.hk * p.k.hs;
-    const T* q0 = static_cast<const T*>(p.q.data) + w.begin * p.q.ts + w.hk * p.q.hs;
-    const T* v0 = static_cast<const T*>(p.v.data) + w.begin * p.v.ts + w.h * p.v.hs;
+    const int chunks = (int)((w.len + C - 1) / C);
+    const int col0 = w.first + wave * 16, col = col0 + lr;
+    auto rows_at = [&](int c) { return w.len - (int64_t)c * C < C ? (int)(w.len - (int64_t)c * C) : C; };
+    auto place_at = [&](int c) { return (w.slot0 + c) * p.heads_v + w.h; };
 
-    TileRegs<T, C, DK, THREADS> kr, qr;
-    TileRegs<T, NX * C, C, THREADS> tr;
-    TileRegs<T, NF * C, C, THREADS> pr;
-    TileRegs<float, 3, C, THREADS> gr;
-    ColumnRegs<T, NB> vr;
-    auto rows_at = [&](int64_t c0) { return w.len - c0 < C ? (int)(w.len - c0) : C; };
-    // the chunk at c0, from global memory to registers
-    auto load = [&](int64_t c0) {
-        const int rows = rows_at(c0);
-        const int64_t at = (w.slot0 + c0 / C) * p.heads_v + w.h;
-        if (p.vec) {
-            kr.load(k0 + c0 * p.k.ts, p.k.ts, rows, p.dim_k, tid);
-            if constexpr (!STORE) qr.load(q0 + c0 * p.q.ts, p.q.ts, rows, p.dim_k, tid);
+    if (__builtin_amdgcn_readfirstlane(threadIdx.x) >= THREADS) {
+        // tiles and outputs
+        const int tid = threadIdx.x - THREADS;
+        const T* k0 = static_cast<const T*>(p.k.data) + w.begin * p.k.ts + w.hk * p.k.hs;
+        const T* q0 = static_cast<const T*>(p.q.data) + w.begin * p.q.ts + w.hk * p.q.hs;
+        const T* v0 = static_cast<const T*>(p.v.data) + w.begin * p.v.ts + w.h * p.v.hs + w.first;
+        const int cols = p.dim_v - w.first < NW * 16 ? p.dim_v - w.first : NW * 16;
+        TileRegs<T, C, DK, THREADS> kr;
+        TileRegs<T, 1, NX * F::elems, THREADS> tr;
+        TileRegs<T, C, NW * 16, THREADS> vr;
+        TileRegs<float, 1, 3 * C, THREADS> gr;
+        auto load = [&](int c) {
+            const int rows = rows_at(c);
+            kr.load(k0 + (int64_t)c * C * p.k.ts, p.k.ts, rows, p.dim_k, tid);
+            tr.load(static_cast<const T*>(p.w_t) + place_at(c) * NX * F::elems, 0, 1, NX * F::elems, tid);
+            vr.load(v0 + (int64_t)c * C * p.v.ts, p.v.ts, rows, cols, tid);
+            gr.load(p.w_gate + place_at(c) * 3 * C, 0, 1, 3 * C, tid);
+        };
+        auto store = [&](int c) {
+            char* buffer = smem + (c & 1) * L::buffer;
+            kr.store(reinterpret_cast<T*>(buffer + L::ks), LK, tid);
+            tr.store(reinterpret_cast<T*>(buffer + L::ts), 0, tid);
+            vr.store(reinterpret_cast<T*>(buffer + L::vs), LV, tid);
+            gr.store(reinterpret_cast<float*>(buffer + L::gate), 0, tid);
+        };
+        if (chunks > 0) {
+            load(0);
+            store(0);
         }
-        tr.load(static_cast<const T*>(p.w_t) + at * NX * C * C, C, NX * C, C, tid);
-        if constexpr (!STORE) pr.load(static_cast<const T*>(p.w_p) + at * NF * C * C, C, NF * C, C, tid);
-        gr.load(p.w_gate + at * 3 * C, C, 3, C, tid);
-        vr.load(v0 + c0 * p.v.ts, p.v.ts, rows, p.dim_v, w.col, gq);
-    };
-    // and from there to an LDS buffer
-    auto store = [&](int64_t c0, char* buffer) {
-        T* ks = reinterpret_cast<T*>(buffer);
-        T* ts = reinterpret_cast<T*>(buffer + L::kq);
-        if (p.vec) {
-            kr.store(ks, LK, tid);
-            if constexpr (!STORE) qr.store(ks + C * LK, LK, tid);
-        } else {
-            const int rows = rows_at(c0);
-            stage_elements<T, C, DK, THREADS>(ks, LK, k0 + c0 * p.k.ts, p.k.ts, rows, p.dim_k, tid);
-            if constexpr (!STORE)
-                stage_elements<T, C, DK, THREADS>(ks + C * LK, LK, q0 + c0 * p.q.ts, p.q.ts, rows, p.dim_k, tid);
+        if (chunks > 1) load(1);
+        Parts<T, 1> qf[DK / 32][NB];
+        Parts<T, NF> pf[C / 32][NB];
+        float eg[NB];
+        for (int c = 0; c < chunks + (STORE ? 0 : 1); ++c) {
+            __syncthreads();
+            if (c + 1 < chunks) store(c + 1);
+            if (c + 2 < chunks) load(c + 2);
+            if constexpr (!STORE) {
+                if (c > 0) {
+                    // O transposed, so that a lane has four columns of one
+                    // token: the state and u in the place of the left operand
+                    const char* buffer = smem + ((c - 1) & 1) * L::buffer;
+                    const T* sx = reinterpret_cast<const T*>(buffer + L::sx);
+                    const T* ux = reinterpret_cast<const T*>(buffer + L::ux);
+                    f32x4 o[NB] = {};
+#pragma unroll
+                    for (int kb = 0; kb < DK / 32; ++kb)
+                        mma_each<true>(qf[kb], Parts<T, 1>{{frag_nat(sx, LK, wave * 16, kb * 32, lane)}}, o);
+#pragma unroll
+                    for (int mt = 0; mt < NB; ++mt) o[mt] *= p.scale * eg[mt];
+#pragma unroll
+                    for (int kb = 0; kb < C / 32; ++kb) {
+                        Parts<T, NF> ub;
+#pragma unroll
+                        for (int n = 0; n < NF; ++n)
+                            ub.p[n] = frag_nat(ux + n * NW * 16 * LC, LC, wave * 16, kb * 32, lane);
+                        mma_each<true>(pf[kb], ub, o, 2 * kb);
+                    }
+                    const int rows = rows_at(c - 1), oc = col0 + gq * 4;
+                    T* o0 = static_cast<T*>(p.out.data) + (w.begin + (int64_t)(c - 1) * C) * p.out.ts + w.h * p.out.hs;
+                    const auto rsrc = rows_rsrc(o0, p.out.ts * (int)sizeof(T), rows, p.dim_v * (int)sizeof(T));
+                    const int step = (int)p.out.ts * (int)sizeof(T);
+#pragma unroll
+                    for (int mt = 0; mt < NB; ++mt) {
+                        const int row = mt * 16 + lr;
+                        const int to = row < rows && oc < p.dim_v ? row * step + oc * (int)sizeof(T) : kOutside;
+                        const Vec4<T> y = __builtin_convertvector(o[mt], Vec4<T>);
+                        if (p.out4) {
+                            buffer_store(rsrc, to, y);
+                        } else {
+#pragma unroll
+                            for (int r = 0; r < 4; ++r)
+                                buffer_store<T>(rsrc, oc + r < p.dim_v ? to + r * (int)sizeof(T) : kOutside, y[r]);
+                        }
+                    }
+                }
+                if (c < chunks) {
+                    const int rows = rows_at(c);
+                    const auto rsrc = rows_rsrc(q0 + (int64_t)c * C * p.q.ts, p.q.ts * (int)sizeof(T), rows,
+                                                whole_bytes<T>(p.dim_k));
+                    const T* wp = static_cast<const T*>(p.w_p) + place_at(c) * NF * F::elems;
+#pragma unroll
+                    for (int mt = 0; mt < NB; ++mt) {
+                        const int row = mt * 16 + lr;
+#pragma unroll
+                        for (int kb = 0; kb < DK / 32; ++kb) {
+                            const int k = kb * 32 + gq * 8;
+                            qf[kb][mt].p[0] = buffer_frag<T>(
+                                rsrc, row < rows && k < p.dim_k ? (row * (int)p.q.ts + k) * (int)sizeof(T) : kOutside);
+                        }
+                        eg[mt] = p.w_gate[place_at(c) * 3 * C + row];
+                    }
+#pragma unroll
+                    for (int kb = 0; kb < C / 32; ++kb)
+#pragma unroll
+                        for (int mt = 2 * kb; mt < NB; ++mt) pf[kb][mt] = parts_at<NF>(wp, F::elems, F::lower(mt, kb), lane);
+                }
+            }
         }
-        tr.store(ts, LC, tid);
-        if constexpr (!STORE) pr.store(ts + NX * C * LC, LC, tid);
-        gr.store(reinterpret_cast<float*>(buffer + L::kq + L::tp), C, tid);
-    };
+        return;
+    }
 
     f32x4 s[NK];
-    load_state<DK>(s, p.initial ? p.initial + state_at : nullptr, p.dim_k, p.dim_v, w.col, gq);
-    if (w.len > 0) {
-        load(0);
-        store(0, smem);
-    }
-    int which = 0;
-    for (int64_t c0 = 0; c0 < w.len; c0 += C, which ^= 1) {
-        char* buffer = smem + which * L::buffer;
-        const T* ks = reinterpret_cast<const T*>(buffer);
-        const T* qs = ks + C * LK;
-        const T* ts = reinterpret_cast<const T*>(buffer + L::kq);
-        const T* ps = ts + NX * C * LC;
-        const float* gate = reinterpret_cast<const float*>(buffer + L::kq + L::tp);
-        f32x4 x[NB];
-#pragma unroll
-        for (int mt = 0; mt < NB; ++mt) x[mt] = vr.tile(mt);
-        __syncthreads();
-        const bool more = c0 + C < w.len;
-        if (more) load(c0 + C);
-
-        const int64_t at = (w.slot0 + c0 / C) * p.heads_v + w.h;
-        if constexpr (STORE)
-            store_columns<T, DK>(static_cast<T*>(p.w_s) + at * DK * p.dv_pad, s, w.col, p.dv_pad, gq);
+    load_state<DK>(s, p.initial ? p.initial + state_at : nullptr, p.dim_k, p.dim_v, col, gq);
+    for (int c = 0; c < chunks; ++c) {
+        char* buffer = smem + (c & 1) * L::buffer;
+        const T* ks = reinterpret_cast<const T*>(buffer + L::ks);
+        const T* ts = reinterpret_cast<const T*>(buffer + L::ts);
+        const T* vs = reinterpret_cast<const T*>(buffer + L::vs);
+        const float* gate = reinterpret_cast<const float*>(buffer + L::gate);
         Parts<T, NP> sb[DK / 32];
 #pragma unroll
         for (int kb = 0; kb < DK / 32; ++kb) sb[kb] = parts_of<T, NP>(s[2 * kb], s[2 * kb + 1]);
-        // X = V - diag(e^G) K S
-        {
-            f32x4 acc[NB] = {};
+        if constexpr (STORE)
+            store_columns<T, DK>(static_cast<T*>(p.w_s) + place_at(c) * DK * p.dv_pad, s, col, p.dv_pad, gq);
+        __syncthreads();
+        if constexpr (!STORE) {
+            T* sx = reinterpret_cast<T*>(buffer + L::sx) + (wave * 16 + lr) * LK + gq * 4;
 #pragma unroll
             for (int kb = 0; kb < DK / 32; ++kb) {
-                Parts<T, 1> a[NB];
-#pragma unroll
-                for (int mt = 0; mt < NB; ++mt) a[mt].p[0] = frag_acc(ks, LK, mt * 16, kb * 32, lane);
-                mma_each(a, sb[kb], acc);
+                *reinterpret_cast<Vec4<T>*>(sx + kb * 32) = __builtin_shufflevector(sb[kb].p[0], sb[kb].p[0], 0, 1, 2, 3);
+                *reinterpret_cast<Vec4<T>*>(sx + kb * 32 + 16) = __builtin_shufflevector(sb[kb].p[0], sb[kb].p[0], 4, 5, 6, 7);
             }
+        }
+        // X = V - diag(e^G) K S
+        f32x4 x[NB] = {};
 #pragma unroll
-            for (int mt = 0; mt < NB; ++mt) x[mt] -= gate4(gate, mt * 16 + gq * 4) * acc[mt];
+        for (int kb = 0; kb < DK / 32; ++kb) {
+            Parts<T, 1> a[NB];
+#pragma unroll
+            for (int mt = 0; mt < NB; ++mt) a[mt].p[0] = frag_acc(ks, LK, mt * 16, kb * 32, lane);
+            mma_each(a, sb[kb], x);
+        }
+#pragma unroll
+        for (int mt = 0; mt < NB; ++mt) {
+            const Vec4<T> v = quad_tr(vs, LV, mt * 16, wave * 16, lane);
+            x[mt] = __builtin_convertvector(v, f32x4) - gate4(gate, mt * 16 + gq * 4) * x[mt];
         }
         // U' = (I + L B)^-1 X; u = B U'
         f32x4 u[NB] = {};
@@ -477,49 +560,17 @@ __global__ __launch_bounds__(NW * 64) DWS_ONE_WAVE void k_delta_scan(DeltaParams
         for (int kb = 0; kb < C / 32; ++kb) {
             Parts<T, NX> a[NB];
 #pragma unroll
-            for (int mt = 2 * kb; mt < NB; ++mt) a[mt] = parts_acc<NX>(ts, C * LC, LC, mt * 16, kb * 32, lane);
+            for (int mt = 2 * kb; mt < NB; ++mt) a[mt] = parts_at<NX>(ts, F::elems, F::lower(mt, kb), lane);
             mma_each(a, parts_of<T, NX>(x[2 * kb], x[2 * kb + 1]), u, 2 * kb);
         }
         if constexpr (STORE)
-            store_columns<T, NF, C>(static_cast<T*>(p.w_u) + at * NF * C * p.dv_pad, u, w.col, p.dv_pad, gq);
+            store_columns<T, NF, C>(static_cast<T*>(p.w_u) + place_at(c) * NF * C * p.dv_pad, u, col, p.dv_pad, gq);
 #pragma unroll
         for (int mt = 0; mt < NB; ++mt) u[mt] *= gate4(gate, 2 * C + mt * 16 + gq * 4);
         if constexpr (!STORE) {
-            // O transposed, so that a lane has four columns of one token: the
-            // state and u in the place of the left operand
-            f32x4 o[NB] = {};
+            T* ux = reinterpret_cast<T*>(buffer + L::ux) + (wave * 16 + lr) * LC + gq * 4;
 #pragma unroll
-            for (int kb = 0; kb < DK / 32; ++kb) {
-                Parts<T, 1> a[NB];
-#pragma unroll
-                for (int mt = 0; mt < NB; ++mt) a[mt].p[0] = frag_acc(qs, LK, mt * 16, kb * 32, lane);
-                mma_each<true>(a, Parts<T, 1>{{sb[kb].p[0]}}, o);
-            }
-#pragma unroll
-            for (int mt = 0; mt < NB; ++mt) o[mt] *= p.scale * gate[mt * 16 + lr];
-#pragma unroll
-            for (int kb = 0; kb < C / 32; ++kb) {
-                Parts<T, NF> a[NB];
-#pragma unroll
-                for (int mt = 2 * kb; mt < NB; ++mt) a[mt] = parts_acc<NF>(ps, C * LC, LC, mt * 16, kb * 32, lane);
-                mma_each<true>(a, parts_of<T, NF>(u[2 * kb], u[2 * kb + 1]), o, 2 * kb);
-            }
-            const int rows = rows_at(c0), c = w.col0 + gq * 4;
-            T* o0 = static_cast<T*>(p.out.data) + (w.begin + c0) * p.out.ts + w.h * p.out.hs;
-            const auto rsrc = rows_rsrc(o0, p.out.ts * (int)sizeof(T), rows, p.dim_v * (int)sizeof(T));
-            const int step = (int)p.out.ts * (int)sizeof(T);
-#pragma unroll
-            for (int mt = 0; mt < NB; ++mt) {
-                const int row = mt * 16 + lr, to = row < rows && c < p.dim_v ? row * step + c * (int)sizeof(T) : kOutside;
-                const Vec4<T> y = __builtin_convertvector(o[mt], Vec4<T>);
-                if (p.out4) {
-                    buffer_store(rsrc, to, y);
-                } else {
-#pragma unroll
-                    for (int r = 0; r < 4; ++r)
-                        buffer_store<T>(rsrc, c + r < p.dim_v ? to + r * (int)sizeof(T) : kOutside, y[r]);
-                }
-            }
+            for (int mt = 0; mt < NB; ++mt) store_parts4<NF>(ux + mt * 16, NW * 16 * LC, u[mt]);
         }
         // S <- e^(G_C) S + K^T diag(e^(G_C - G)) u
 #pragma unroll
@@ -530,14 +581,25 @@ __global__ __launch_bounds__(NW * 64) DWS_ONE_WAVE void k_delta_scan(DeltaParams
 #pragma unroll
         for (int kb = 0; kb < C / 32; ++kb) {
             const Parts<T, NX> ub = parts_of<T, NX>(u[2 * kb], u[2 * kb + 1]);
-            Parts<T, 1> a[NK];
 #pragma unroll
-            for (int t = 0; t < NK; ++t) a[t].p[0] = frag_tr(ks, LK, kb * 32, t * 16, lane);
-            mma_each(a, ub, s);
+            for (int t0 = 0; t0 < NK; t0 += 4) {
+                Parts<T, 1> a[4];
+                f32x4 acc[4];
+#pragma unroll
+                for (int t = 0; t < 4; ++t) {
+                    a[t].p[0] = frag_tr(ks, LK, kb * 32, (t0 + t) * 16, lane);
+                    acc[t] = s[t0 + t];
+                }
+                mma_each(a, ub, acc);
+#pragma unroll
+                for (int t = 0; t < 4; ++t) s[t0 + t] = acc[t];
+            }
         }
-        if (more) store(c0 + C, smem + (which ^ 1) * L::buffer);
     }
-    if (!STORE && p.final_state != nullptr) store_state<DK>(s, p.final_state + state_at, p.dim_k, p.dim_v, w.col, gq);
+    if constexpr (!STORE) {
+        __syncthreads();      // the other waves' last chunk
+        if (p.final_state != nullptr) store_state<DK>(s, p.final_state + state_at, p.dim_k, p.dim_v, col, gq);
+    }
 }
 
 // ---- the backward scan -----------------------------------------------------
@@ -549,85 +611,92 @@ __global__ __launch_bounds__(NW * 64) DWS_ONE_WAVE void k_delta_scan(DeltaParams
 // first. Z and dS' go to the workspace, dV to its place.
 
 template <class T, int DK, int NW>
-__global__ __launch_bounds__(NW * 64) DWS_ONE_WAVE void k_delta_scan_back(DeltaParams p)
+__global__ __launch_bounds__(NW * 128) DWS_TWO_WAVES void k_delta_scan_back(DeltaParams p)
 {
     constexpr int NF = kFine<T>;
-    using L = ScanLds<T, DK, 2, 2 * NF>;
-    constexpr int C = L::C, THREADS = NW * 64, NB = C / 16, LK = L::LK, LC = L::LC, NK = DK / 16;
+    using L = ScanLds<T, DK, NW, 2, 2 * NF, false>;
+    constexpr int C = L::C, THREADS = NW * 64, NB = C / 16, LK = L::LK, LV = L::LV, NK = DK / 16;
+    using F = Triangle<C>;
     extern __shared__ __attribute__((aligned(16))) char smem[];
 
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, gq = lane >> 4;
-    ScanPlace<NW> w;
-    if (!scan_place<C, NW>(p, lane, wave, &w)) return;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) % NW;
+    const int gq = lane >> 4, lr = lane & 15;
+    ScanPlace w;
+    if (!scan_place<C, NW>(p, &w)) return;
     const int64_t state_at = (w.seq * p.heads_v + w.h) * p.dim_k * p.dim_v;
-    const T* k0 = static_cast<const T*>(p.k.data) + w.begin * p.k.ts + w.hk * p.k.hs;
-    const T* q0 = static_cast<const T*>(p.q.data) + w.begin * p.q.ts + w.hk * p.q.hs;
-    const T* o0 = static_cast<const T*>(p.d_out.data) + w.begin * p.d_out.ts + w.h * p.d_out.hs;
+    const int chunks = (int)((w.len + C - 1) / C);
+    const int col = w.first + wave * 16 + lr;
+    auto rows_at = [&](int c) { return w.len - (int64_t)c * C < C ? (int)(w.len - (int64_t)c * C) : C; };
+    auto place_at = [&](int c) { return (w.slot0 + c) * p.heads_v + w.h; };
 
-    TileRegs<T, C, DK, THREADS> kr, qr;
-    TileRegs<T, NF * C, C, THREADS> tr, pr;
-    TileRegs<float, 3, C, THREADS> gr;
-    ColumnRegs<T, NB> orr;
-    auto rows_at = [&](int64_t c0) { return w.len - c0 < C ? (int)(w.len - c0) : C; };
-    auto load = [&](int64_t c0) {
-        const int rows = rows_at(c0);
-        const int64_t at = (w.slot0 + c0 / C) * p.heads_v + w.h;
-        if (p.vec) {
-            kr.load(k0 + c0 * p.k.ts, p.k.ts, rows, p.dim_k, tid);
-            qr.load(q0 + c0 * p.q.ts, p.q.ts, rows, p.dim_k, tid);
+    if (__builtin_amdgcn_readfirstlane(threadIdx.x) >= THREADS) {
+        const int tid = threadIdx.x - THREADS;
+        const T* k0 = static_cast<const T*>(p.k.data) + w.begin * p.k.ts + w.hk * p.k.hs;
+        const T* q0 = static_cast<const T*>(p.q.data) + w.begin * p.q.ts + w.hk * p.q.hs;
+        const T* o0 = static_cast<const T*>(p.d_out.data) + w.begin * p.d_out.ts + w.h * p.d_out.hs + w.first;
+        const int cols = p.dim_v - w.first < NW * 16 ? p.dim_v - w.first : NW * 16;
+        TileRegs<T, C, DK, THREADS> kr, qr;
+        TileRegs<T, 1, NF * F::elems, THREADS> tr, pr;
+        TileRegs<T, C, NW * 16, THREADS> orr;
+        TileRegs<float, 1, 3 * C, THREADS> gr;
+        auto load = [&](int c) {
+            const int rows = rows_at(c);
+            kr.load(k0 + (int64_t)c * C * p.k.ts, p.k.ts, rows, p.dim_k, tid);
+            qr.load(q0 + (int64_t)c * C * p.q.ts, p.q.ts, rows, p.dim_k, tid);
+            tr.load(static_cast<const T*>(p.w_tt) + place_at(c) * NF * F::elems, 0, 1, NF * F::elems, tid);
+            pr.load(static_cast<const T*>(p.w_p) + place_at(c) * NF * F::elems, 0, 1, NF * F::elems, tid);
+            orr.load(o0 + (int64_t)c * C * p.d_out.ts, p.d_out.ts, rows, cols, tid);
+            gr.load(p.w_gate + place_at(c) * 3 * C, 0, 1, 3 * C, tid);
+        };
+        auto store = [&](int c) {
+            char* buffer = smem + (c & 1) * L::buffer;
+            kr.store(reinterpret_cast<T*>(buffer + L::ks), LK, tid);
+            qr.store(reinterpret_cast<T*>(buffer + L::ks) + C * LK, LK, tid);
+            tr.store(reinterpret_cast<T*>(buffer + L::ts), 0, tid);
+            pr.store(reinterpret_cast<T*>(buffer + L::ts) + NF * F::elems, 0, tid);
+            orr.store(reinterpret_cast<T*>(buffer + L::vs), LV, tid);
+            gr.store(reinterpret_cast<float*>(buffer + L::gate), 0, tid);
+        };
+        if (chunks > 0) {
+            load(chunks - 1);
+            store(chunks - 1);
         }
-        tr.load(static_cast<const T*>(p.w_tt) + at * NF * C * C, C, NF * C, C, tid);
-        pr.load(static_cast<const T*>(p.w_p) + at * NF * C * C, C, NF * C, C, tid);
-        gr.load(p.w_gate + at * 3 * C, C, 3, C, tid);
-        orr.load(o0 + c0 * p.d_out.ts, p.d_out.ts, rows, p.dim_v, w.col, gq);
-    };
-    auto store = [&](int64_t c0, char* buffer) {
-        T* ks = reinterpret_cast<T*>(buffer);
-        T* ts = reinterpret_cast<T*>(buffer + L::kq);
-        if (p.vec) {
-            kr.store(ks, LK, tid);
-            qr.store(ks + C * LK, LK, tid);
-        } else {
-            const int rows = rows_at(c0);
-            stage_elements<T, C, DK, THREADS>(ks, LK, k0 + c0 * p.k.ts, p.k.ts, rows, p.dim_k, tid);
-            stage_elements<T, C, DK, THREADS>(ks + C * LK, LK, q0 + c0 * p.q.ts, p.q.ts, rows, p.dim_k, tid);
+        if (chunks > 1) load(chunks - 2);
+        for (int c = chunks - 1; c >= 0; --c) {
+            __syncthreads();
+            if (c > 0) store(c - 1);
+            if (c > 1) load(c - 2);
         }
-        tr.store(ts, LC, tid);
-        pr.store(ts + NF * C * LC, LC, tid);
-        gr.store(reinterpret_cast<float*>(buffer + L::kq + L::tp), C, tid);
-    };
+        return;
+    }
 
     f32x4 ds[NK];
-    load_state<DK>(ds, p.d_final ? p.d_final + state_at : nullptr, p.dim_k, p.dim_v, w.col, gq);
-    const int64_t last = w.len > 0 ? (w.len - 1) / C * C : 0;
-    if (w.len > 0) {
-        load(last);
-        store(last, smem);
-    }
-    int which = 0;
-    for (int64_t c0 = last; c0 >= 0 && w.len > 0; c0 -= C, which ^= 1) {
-        char* buffer = smem + which * L::buffer;
-        const T* ks = reinterpret_cast<const T*>(buffer);
+    load_state<DK>(ds, p.d_final ? p.d_final + state_at : nullptr, p.dim_k, p.dim_v, col, gq);
+    for (int c = chunks - 1; c >= 0; --c) {
+        char* buffer = smem + (c & 1) * L::buffer;
+        const T* ks = reinterpret_cast<const T*>(buffer + L::ks);
         const T* qs = ks + C * LK;
-        const T* ts = reinterpret_cast<const T*>(buffer + L::kq);
-        const T* ps = ts + NF * C * LC;
-        const float* gate = reinterpret_cast<const float*>(buffer + L::kq + L::tp);
-        f32x4 d_o[NB];
+        const T* ts = reinterpret_cast<const T*>(buffer + L::ts);
+        const T* ps = ts + NF * F::elems;
+        const T* os = reinterpret_cast<const T*>(buffer + L::vs);
+        const float* gate = reinterpret_cast<const float*>(buffer + L::gate);
+        const int64_t at = place_at(c);
+        store_columns<T, DK>(static_cast<T*>(p.w_ds) + at * DK * p.dv_pad, ds, col, p.dv_pad, gq);
+        Parts<T, 1> db[DK / 32];
 #pragma unroll
-        for (int mt = 0; mt < NB; ++mt) d_o[mt] = orr.tile(mt);
+        for (int kb = 0; kb < DK / 32; ++kb) db[kb] = parts_of<T, 1>(ds[2 * kb], ds[2 * kb + 1]);
         __syncthreads();
-        if (c0 > 0) load(c0 - C);
-
-        const int64_t at = (w.slot0 + c0 / C) * p.heads_v + w.h;
-        store_columns<T, DK>(static_cast<T*>(p.w_ds) + at * DK * p.dv_pad, ds, w.col, p.dv_pad, gq);
-        // dU
+        // dU; dO is exact in T
+        Vec4<T> d_o[NB];
+#pragma unroll
+        for (int mt = 0; mt < NB; ++mt) d_o[mt] = quad_tr(os, LV, mt * 16, wave * 16, lane);
         f32x4 z[NB] = {};
 #pragma unroll
         for (int kb = 0; kb < DK / 32; ++kb) {
             Parts<T, 1> a[NB];
 #pragma unroll
             for (int mt = 0; mt < NB; ++mt) a[mt].p[0] = frag_acc(ks, LK, mt * 16, kb * 32, lane);
-            mma_each(a, parts_of<T, 1>(ds[2 * kb], ds[2 * kb + 1]), z);
+            mma_each(a, db[kb], z);
         }
 #pragma unroll
         for (int mt = 0; mt < NB; ++mt) z[mt] *= gate4(gate, C + mt * 16 + gq * 4);
@@ -635,51 +704,62 @@ __global__ __launch_bounds__(NW * 64) DWS_ONE_WAVE void k_delta_scan_back(DeltaP
         for (int kb = 0; kb < C / 32; ++kb) {
             Parts<T, NF> a[NB];
 #pragma unroll
-            for (int mt = 0; mt < 2 * kb + 2; ++mt) a[mt] = parts_acc<NF>(ps, C * LC, LC, mt * 16, kb * 32, lane);
-            mma_each(a, parts_of<T, 1>(d_o[2 * kb], d_o[2 * kb + 1]), z, 0, 2 * kb + 2);      // dO is exact in T
+            for (int mt = 0; mt < 2 * kb + 2; ++mt) a[mt] = parts_at<NF>(ps, F::elems, F::upper(mt, kb), lane);
+            mma_each(a, Parts<T, 1>{{__builtin_shufflevector(d_o[2 * kb], d_o[2 * kb + 1], 0, 1, 2, 3, 4, 5, 6, 7)}}, z, 0,
+                     2 * kb + 2);
         }
         f32x4 y[NB] = {};
 #pragma unroll
         for (int kb = 0; kb < C / 32; ++kb) {
             Parts<T, NF> a[NB];
 #pragma unroll
-            for (int mt = 0; mt < 2 * kb + 2; ++mt) a[mt] = parts_acc<NF>(ts, C * LC, LC, mt * 16, kb * 32, lane);
+            for (int mt = 0; mt < 2 * kb + 2; ++mt) a[mt] = parts_at<NF>(ts, F::elems, F::upper(mt, kb), lane);
             mma_each(a, parts_of<T, NF>(z[2 * kb], z[2 * kb + 1]), y, 0, 2 * kb + 2);
         }
-        store_columns<T, NF, C>(static_cast<T*>(p.w_z) + at * NF * C * p.dv_pad, y, w.col, p.dv_pad, gq);
-        const int rows = rows_at(c0);
-        T* dv0 = static_cast<T*>(p.dv.data) + (w.begin + c0) * p.dv.ts + w.h * p.dv.hs;
+        store_columns<T, NF, C>(static_cast<T*>(p.w_z) + at * NF * C * p.dv_pad, y, col, p.dv_pad, gq);
+        const int rows = rows_at(c);
+        T* dv0 = static_cast<T*>(p.dv.data) + (w.begin + (int64_t)c * C) * p.dv.ts + w.h * p.dv.hs;
         const auto rsrc = rows_rsrc(dv0, p.dv.ts * (int)sizeof(T), rows, p.dim_v * (int)sizeof(T));
         const int step = (int)p.dv.ts * (int)sizeof(T);
+        f32x4 e[NB];
 #pragma unroll
         for (int mt = 0; mt < NB; ++mt) {
             const int row = mt * 16 + gq * 4;
             y[mt] *= gate4(gate, 2 * C + row);
 #pragma unroll
             for (int r = 0; r < 4; ++r)
-                buffer_store<T>(rsrc, w.mine && row + r < rows ? (row + r) * step + w.col * (int)sizeof(T) : kOutside,
+                buffer_store<T>(rsrc, col < p.dim_v && row + r < rows ? (row + r) * step + col * (int)sizeof(T) : kOutside,
                                 (T)y[mt][r]);
             const f32x4 eg = gate4(gate, row);
             y[mt] *= -eg;
-            d_o[mt] *= p.scale * eg;
+            e[mt] = __builtin_convertvector(d_o[mt], f32x4) * (p.scale * eg);
         }
         const float keep = gate[C - 1];
 #pragma unroll
         for (int t = 0; t < NK; ++t) ds[t] *= keep;
 #pragma unroll
         for (int kb = 0; kb < C / 32; ++kb) {
-            Parts<T, 1> a[NK];
+            const Parts<T, NF> eb = parts_of<T, NF>(e[2 * kb], e[2 * kb + 1]);
+            const Parts<T, 1> yb = parts_of<T, 1>(y[2 * kb], y[2 * kb + 1]);
 #pragma unroll
-            for (int t = 0; t < NK; ++t) a[t].p[0] = frag_tr(qs, LK, kb * 32, t * 16, lane);
-            mma_each(a, parts_of<T, NF>(d_o[2 * kb], d_o[2 * kb + 1]), ds);
+            for (int t0 = 0; t0 < NK; t0 += 4) {
+                Parts<T, 1> a[4], b[4];
+                f32x4 acc[4];
 #pragma unroll
-            for (int t = 0; t < NK; ++t) a[t].p[0] = frag_tr(ks, LK, kb * 32, t * 16, lane);
-            mma_each(a, parts_of<T, 1>(y[2 * kb], y[2 * kb + 1]), ds);
+                for (int t = 0; t < 4; ++t) {
+                    a[t].p[0] = frag_tr(qs, LK, kb * 32, (t0 + t) * 16, lane);
+                    b[t].p[0] = frag_tr(ks, LK, kb * 32, (t0 + t) * 16, lane);
+                    acc[t] = ds[t0 + t];
+                }
+                mma_each(a, eb, acc);
+                mma_each(b, yb, acc);
+#pragma unroll
+                for (int t = 0; t < 4; ++t) ds[t0 + t] = acc[t];
+            }
         }
-        if (c0 > 0) store(c0 - C, smem + (which ^ 1) * L::buffer);
     }
     if (p.d_initial != nullptr)
-        store_state<DK>(ds, static_cast<T*>(p.d_initial) + state_at, p.dim_k, p.dim_v, w.col, gq);
+        store_state<DK>(ds, static_cast<T*>(p.d_initial) + state_at, p.dim_k, p.dim_v, col, gq);
 }
 
 // ---- the gradients of q, k and the gates ------------------------------------
@@ -768,10 +848,13 @@ __global__ __launch_bounds__((GradLds<T, DK>::THREADS)) DWS_ONE_WAVE void k_delt
         }
     };
     load(slot * p.heads_v + hk * share, 0);
-    stage_tile<T, C, DK, THREADS>(ks, LK, static_cast<const T*>(p.k.data) + info.row * p.k.ts + hk * p.k.hs, p.k.ts, rows,
-                                  p.dim_k, p.vec, tid);
-    stage_tile<T, C, DK, THREADS>(qs, LK, static_cast<const T*>(p.q.data) + info.row * p.q.ts + hk * p.q.hs, p.q.ts, rows,
-                                  p.dim_k, p.vec, tid);
+    {
+        TileRegs<T, C, DK, THREADS> kr, qr;
+        kr.load(static_cast<const T*>(p.k.data) + info.row * p.k.ts + hk * p.k.hs, p.k.ts, rows, p.dim_k, tid);
+        qr.load(static_cast<const T*>(p.q.data) + info.row * p.q.ts + hk * p.q.hs, p.q.ts, rows, p.dim_k, tid);
+        kr.store(ks, LK, tid);
+        qr.store(qs, LK, tid);
+    }
     f32x4 dq[NK] = {}, dk[NK] = {};
 
     for (int m = 0; m < share; ++m) {
@@ -785,26 +868,18 @@ __global__ __launch_bounds__((GradLds<T, DK>::THREADS)) DWS_ONE_WAVE void k_delt
         }
 
         const T* d_o = static_cast<const T*>(p.d_out.data) + info.row * p.d_out.ts + h * p.d_out.hs;
-        const auto o_rsrc = rows_rsrc(d_o, p.d_out.ts * (int)sizeof(T), rows, p.dim_v * (int)sizeof(T));
+        const auto o_rsrc = rows_rsrc(d_o, p.d_out.ts * (int)sizeof(T), rows, whole_bytes<T>(p.dim_v));
         const int o_at = (row0 + lr) * (int)p.d_out.ts;
         f32x4 dp[NB] = {}, zu[NB] = {}, os[NK] = {}, zs[NK] = {}, us[NK] = {};
         float zdotu = 0.f, sds = 0.f;
         for (int c = 0; c < p.dv_pad; c += 32) {
             // dO's rows of this wave, 32 columns in acc order
             Parts<T, 1> ao;
-            if (p.vec) {
-                const int o0 = c + gq * 4, o1 = o0 + 16;
-                const bool in = row0 + lr < rows;
-                const Vec4<T> a = buffer_load<Vec4<T>>(o_rsrc, in && o0 < p.dim_v ? (o_at + o0) * (int)sizeof(T) : kOutside);
-                const Vec4<T> b = buffer_load<Vec4<T>>(o_rsrc, in && o1 < p.dim_v ? (o_at + o1) * (int)sizeof(T) : kOutside);
-                ao.p[0] = __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
-            } else {
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const int o = c + gq * 4 + j % 4 + j / 4 * 16;
-                    ao.p[0][j] = buffer_load<T>(o_rsrc, row0 + lr < rows && o < p.dim_v ? (o_at + o) * (int)sizeof(T) : kOutside);
-                }
-            }
+            const int o0 = c + gq * 4, o1 = o0 + 16;
+            const bool in = row0 + lr < rows;
+            const Vec4<T> oa = buffer_load<Vec4<T>>(o_rsrc, in && o0 < p.dim_v ? (o_at + o0) * (int)sizeof(T) : kOutside);
+            const Vec4<T> ob = buffer_load<Vec4<T>>(o_rsrc, in && o1 < p.dim_v ? (o_at + o1) * (int)sizeof(T) : kOutside);
+            ao.p[0] = __builtin_shufflevector(oa, ob, 0, 1, 2, 3, 4, 5, 6, 7);
             sr.store(st, LK, tid);
             dsr.store(dst, LK, tid);
 #pragma unroll
@@ -991,26 +1066,74 @@ hipError_t launch_lds(K kernel, uint64_t blocks, int threads, size_t lds, const 
     return hipGetLastError();
 }
 
+// Rows that cannot be read 16 bytes at a time, copied to ones that can: padded
+// to whole units, zero behind dim.
+template <class T>
+__global__ __launch_bounds__(256) void k_delta_pack(DeltaRows src, T* dst, int64_t tokens, int heads, int dim, int padded)
+{
+    const int64_t n = tokens * heads * padded;
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {
+        const int64_t row = i / padded, t = row / heads;
+        const int d = (int)(i - row * padded), h = (int)(row - t * heads);
+        dst[i] = d < dim ? static_cast<const T*>(src.data)[t * src.ts + h * src.hs + d] : (T)0.f;
+    }
+}
+template <class T>
+hipError_t pack_rows(const DeltaPack& k, int64_t tokens, hipStream_t stream)
+{
+    if (k.n == 0 || tokens == 0) return hipSuccess;
+    for (int i = 0; i < k.n; ++i) {
+        const auto& r = k.rows[i];
+        const int64_t blocks = (tokens * r.heads * r.padded + 255) / 256;
+        k_delta_pack<T><<<dim3((uint32_t)(blocks < 4096 ? blocks : 4096)), dim3(256), 0, stream>>>(
+            r.src, static_cast<T*>(r.dst), tokens, r.heads, r.dim, r.padded);
+    }
+    return hipGetLastError();
+}
+
 inline uint64_t scan_blocks(const DeltaParams& p, int waves)
 {
     const uint64_t parts = ((uint64_t)p.dim_v + waves * 16 - 1) / (waves * 16);
     const uint64_t groups = ((uint64_t)p.n_seqs * p.heads_v + 7) / 8 * 8;
     return groups * parts;
 }
+// 16-column waves of a scan workgroup: four share a chunk's tiles. Two where
+// four would leave compute units without a workgroup, and for fp32 heads above
+// 128, whose tiles and states leave LDS for no more.
+template <class T, int DK>
+constexpr int kMostWaves = sizeof(T) == 4 && DK > 128 ? 2 : 4;
+constexpr uint64_t kComputeUnits = 256;
+
+template <class T, int DK, int NP, bool STORE, int NW>
+hipError_t launch_scan(const DeltaParams& p, hipStream_t stream)
+{
+    constexpr int NF = kFine<T>, NX = NP > NF ? NP : NF;
+    return launch_lds(k_delta_scan<T, DK, NP, STORE, NW>, scan_blocks(p, NW), NW * 128,
+                      ScanLds<T, DK, NW, 1, NX, !STORE>::bytes, p, stream);
+}
+template <class T, int DK, int NW>
+hipError_t launch_back(const DeltaParams& p, hipStream_t stream)
+{
+    return launch_lds(k_delta_scan_back<T, DK, NW>, scan_blocks(p, NW), NW * 128,
+                      ScanLds<T, DK, NW, 2, 2 * kFine<T>, false>::bytes, p, stream);
+}
+inline bool few_groups(const DeltaParams& p) { return scan_blocks(p, 4) < kComputeUnits; }
 
 template <class T, int DK, int NP>
 hipError_t forward_dk(const DeltaParams& p, hipStream_t stream)
 {
-    constexpr int C = kChunk<T, DK>, NW = 4, NF = kFine<T>, NX = NP > NF ? NP : NF;
-    hipError_t e = launch_lds(k_delta_prep<T, DK, NP, false>, (uint64_t)p.n_slots * p.heads_v, C * 4,
-                              PrepLds<T, DK>::bytes, p, stream);
+    constexpr int C = kChunk<T, DK>;
+    const hipError_t e = launch_lds(k_delta_prep<T, DK, NP, false>, (uint64_t)p.n_slots * p.heads_v, C * 4,
+                                    PrepLds<T, DK>::bytes, p, stream);
     if (e != hipSuccess) return e;
-    return launch_lds(k_delta_scan<T, DK, NP, false, NW>, scan_blocks(p, NW), NW * 64, ScanLds<T, DK, 2, NX + NF>::bytes,
-                      p, stream);
+    if (few_groups(p)) return launch_scan<T, DK, NP, false, 2>(p, stream);
+    return launch_scan<T, DK, NP, false, kMostWaves<T, DK>>(p, stream);
 }
 template <class T, int NP>
-hipError_t forward_type(const DeltaParams& p, hipStream_t stream)
+hipError_t forward_type(const DeltaParams& p, const DeltaPack& k, hipStream_t stream)
 {
+    const hipError_t e = pack_rows<T>(k, p.tokens, stream);
+    if (e != hipSuccess) return e;
     switch (delta_padded_k(p.dim_k)) {
     case 64: return forward_dk<T, 64, NP>(p, stream);
     case 128: return forward_dk<T, 128, NP>(p, stream);
@@ -1021,21 +1144,22 @@ hipError_t forward_type(const DeltaParams& p, hipStream_t stream)
 template <class T, int DK>
 hipError_t backward_dk(const DeltaParams& p, hipStream_t stream)
 {
-    constexpr int C = kChunk<T, DK>, NW = 4;
+    constexpr int C = kChunk<T, DK>;
     hipError_t e = launch_lds(k_delta_prep<T, DK, 1, true>, (uint64_t)p.n_slots * p.heads_v, C * 4,
                               PrepLds<T, DK>::bytes, p, stream);
     if (e != hipSuccess) return e;
-    e = launch_lds(k_delta_scan<T, DK, 1, true, NW>, scan_blocks(p, NW), NW * 64, ScanLds<T, DK, 1, kFine<T>>::bytes, p,
-                   stream);
+    e = few_groups(p) ? launch_scan<T, DK, 1, true, 2>(p, stream) : launch_scan<T, DK, 1, true, kMostWaves<T, DK>>(p, stream);
     if (e != hipSuccess) return e;
-    e = launch_lds(k_delta_scan_back<T, DK, NW>, scan_blocks(p, NW), NW * 64, ScanLds<T, DK, 2, 2 * kFine<T>>::bytes, p, stream);
+    e = few_groups(p) ? launch_back<T, DK, 2>(p, stream) : launch_back<T, DK, kMostWaves<T, DK>>(p, stream);
     if (e != hipSuccess) return e;
     return launch_lds(k_delta_grad<T, DK>, (uint64_t)p.n_slots * p.heads_qk, GradLds<T, DK>::THREADS,
                       GradLds<T, DK>::bytes, p, stream);
 }
 template <class T>
-hipError_t backward_type(const DeltaParams& p, hipStream_t stream)
+hipError_t backward_type(const DeltaParams& p, const DeltaPack& k, hipStream_t stream)
 {
+    const hipError_t e = pack_rows<T>(k, p.tokens, stream);
+    if (e != hipSuccess) return e;
     switch (delta_padded_k(p.dim_k)) {
     case 64: return backward_dk<T, 64>(p, stream);
     case 128: return backward_dk<T, 128>(p, stream);

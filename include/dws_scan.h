@@ -585,8 +585,10 @@ typedef struct dws_delta_rule_args {
 } dws_delta_rule_args;
 
 /* Bytes of workspace that dws_delta_rule (backward == 0) or
- * dws_delta_rule_backward needs for these sizes, types and this choice of
- * d_final_state (host only, no HIP call). The workspace is the caller's, not the
+ * dws_delta_rule_backward needs with these arguments, their pointers, strides
+ * and choice of d_final_state included (host only, no HIP call): rows of q, k, v
+ * and out_grad that are not whole, aligned 16-byte units are copied there first.
+ * The workspace is the caller's, not the
  * stream's, since it grows with the tokens; it holds nothing between calls, and
  * calls that may run at the same time, replays of captured graphs among them,
  * need one each. */
