@@ -446,13 +446,15 @@ __global__ __launch_bounds__(NW * 128) DWS_TWO_WAVES void k_delta_scan(DeltaPara
             store(0);
         }
         if (chunks > 1) load(1);
-        Parts<T, 1> qf[DK / 32][NB];
-        Parts<T, NF> pf[C / 32][NB];
-        float eg[NB];
+        // Outputs are shared out by token tiles, so that each of Q's and P's
+        // rows is read once: MT token tiles, CT column tiles a wave
+        constexpr int MT = NB > NW ? NB / NW : 1, CT = NB / MT;
+        const int mt0 = wave * MT % NB, ct0 = wave * MT / NB * CT;
+        Parts<T, 1> qf[DK / 32][MT];
+        Parts<T, NF> pf[C / 32][MT];
+        float eg[MT];
         for (int c = 0; c < chunks + (STORE ? 0 : 1); ++c) {
             __syncthreads();
-            if (c + 1 < chunks) store(c + 1);
-            if (c + 2 < chunks) load(c + 2);
             if constexpr (!STORE) {
                 if (c > 0) {
                     // O transposed, so that a lane has four columns of one
@@ -460,37 +462,47 @@ __global__ __launch_bounds__(NW * 128) DWS_TWO_WAVES void k_delta_scan(DeltaPara
                     const char* buffer = smem + ((c - 1) & 1) * L::buffer;
                     const T* sx = reinterpret_cast<const T*>(buffer + L::sx);
                     const T* ux = reinterpret_cast<const T*>(buffer + L::ux);
-                    f32x4 o[NB] = {};
+                    f32x4 o[CT][MT] = {};
 #pragma unroll
                     for (int kb = 0; kb < DK / 32; ++kb)
-                        mma_each<true>(qf[kb], Parts<T, 1>{{frag_nat(sx, LK, wave * 16, kb * 32, lane)}}, o);
 #pragma unroll
-                    for (int mt = 0; mt < NB; ++mt) o[mt] *= p.scale * eg[mt];
+                        for (int ct = 0; ct < CT; ++ct)
+                            mma_each<true>(qf[kb], Parts<T, 1>{{frag_nat(sx, LK, (ct0 + ct) * 16, kb * 32, lane)}}, o[ct]);
+#pragma unroll
+                    for (int ct = 0; ct < CT; ++ct)
+#pragma unroll
+                        for (int m = 0; m < MT; ++m) o[ct][m] *= p.scale * eg[m];
 #pragma unroll
                     for (int kb = 0; kb < C / 32; ++kb) {
-                        Parts<T, NF> ub;
+                        if (2 * kb > mt0 + MT - 1) continue;       // P is lower triangular
 #pragma unroll
-                        for (int n = 0; n < NF; ++n)
-                            ub.p[n] = frag_nat(ux + n * NW * 16 * LC, LC, wave * 16, kb * 32, lane);
-                        mma_each<true>(pf[kb], ub, o, 2 * kb);
+                        for (int ct = 0; ct < CT; ++ct) {
+                            Parts<T, NF> ub;
+#pragma unroll
+                            for (int n = 0; n < NF; ++n)
+                                ub.p[n] = frag_nat(ux + n * NW * 16 * LC, LC, (ct0 + ct) * 16, kb * 32, lane);
+                            mma_each<true>(pf[kb], ub, o[ct]);
+                        }
                     }
-                    const int rows = rows_at(c - 1), oc = col0 + gq * 4;
+                    const int rows = rows_at(c - 1);
                     T* o0 = static_cast<T*>(p.out.data) + (w.begin + (int64_t)(c - 1) * C) * p.out.ts + w.h * p.out.hs;
                     const auto rsrc = rows_rsrc(o0, p.out.ts * (int)sizeof(T), rows, p.dim_v * (int)sizeof(T));
                     const int step = (int)p.out.ts * (int)sizeof(T);
 #pragma unroll
-                    for (int mt = 0; mt < NB; ++mt) {
-                        const int row = mt * 16 + lr;
-                        const int to = row < rows && oc < p.dim_v ? row * step + oc * (int)sizeof(T) : kOutside;
-                        const Vec4<T> y = __builtin_convertvector(o[mt], Vec4<T>);
-                        if (p.out4) {
-                            buffer_store(rsrc, to, y);
-                        } else {
+                    for (int ct = 0; ct < CT; ++ct)
 #pragma unroll
-                            for (int r = 0; r < 4; ++r)
-                                buffer_store<T>(rsrc, oc + r < p.dim_v ? to + r * (int)sizeof(T) : kOutside, y[r]);
+                        for (int m = 0; m < MT; ++m) {
+                            const int row = (mt0 + m) * 16 + lr, oc = w.first + (ct0 + ct) * 16 + gq * 4;
+                            const int to = row < rows && oc < p.dim_v ? row * step + oc * (int)sizeof(T) : kOutside;
+                            const Vec4<T> y = __builtin_convertvector(o[ct][m], Vec4<T>);
+                            if (p.out4) {
+                                buffer_store(rsrc, to, y);
+                            } else {
+#pragma unroll
+                                for (int r = 0; r < 4; ++r)
+                                    buffer_store<T>(rsrc, oc + r < p.dim_v ? to + r * (int)sizeof(T) : kOutside, y[r]);
+                            }
                         }
-                    }
                 }
                 if (c < chunks) {
                     const int rows = rows_at(c);
@@ -498,22 +510,27 @@ __global__ __launch_bounds__(NW * 128) DWS_TWO_WAVES void k_delta_scan(DeltaPara
                                                 whole_bytes<T>(p.dim_k));
                     const T* wp = static_cast<const T*>(p.w_p) + place_at(c) * NF * F::elems;
 #pragma unroll
-                    for (int mt = 0; mt < NB; ++mt) {
-                        const int row = mt * 16 + lr;
+                    for (int m = 0; m < MT; ++m) {
+                        const int row = (mt0 + m) * 16 + lr;
 #pragma unroll
                         for (int kb = 0; kb < DK / 32; ++kb) {
                             const int k = kb * 32 + gq * 8;
-                            qf[kb][mt].p[0] = buffer_frag<T>(
+                            qf[kb][m].p[0] = buffer_frag<T>(
                                 rsrc, row < rows && k < p.dim_k ? (row * (int)p.q.ts + k) * (int)sizeof(T) : kOutside);
                         }
-                        eg[mt] = p.w_gate[place_at(c) * 3 * C + row];
+                        eg[m] = p.w_gate[place_at(c) * 3 * C + row];
+                        // (above the diagonal: not kept, and 0)
+#pragma unroll
+                        for (int kb = 0; kb < C / 32; ++kb)
+                            if (2 * kb <= mt0 + m)
+                                pf[kb][m] = parts_at<NF>(wp, F::elems, F::lower(mt0 + m, kb), lane);
+                            else
+                                pf[kb][m] = Parts<T, NF>{};
                     }
-#pragma unroll
-                    for (int kb = 0; kb < C / 32; ++kb)
-#pragma unroll
-                        for (int mt = 2 * kb; mt < NB; ++mt) pf[kb][mt] = parts_at<NF>(wp, F::elems, F::lower(mt, kb), lane);
                 }
             }
+            if (c + 1 < chunks) store(c + 1);
+            if (c + 2 < chunks) load(c + 2);
         }
         return;
     }
