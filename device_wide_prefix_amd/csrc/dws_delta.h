@@ -49,7 +49,7 @@ struct DeltaParams {
     int zero_tail;               // zero the output rows behind the last sequence
     // workspace
     int64_t n_slots;             // chunk slots: tokens / chunk + n_seqs + 1 (the last ones empty)
-    float* w_gate;               // [slot][head][3][chunk]: e^G, e^(G_C - G), beta
+    float* w_gate;               // [slot][head][5][chunk]: gate factors (kGateArrays in the kernels)
     // triangular matrices as operand fragments (Triangle in the kernels)
     void* w_t;                   // [slot][head][parts][frags]: (I + L diag(beta))^-1
     void* w_p;                   // [slot][head][fine][frags]: P (forward), its transpose (backward)

@@ -142,7 +142,7 @@ Sizes workspace_of(const dws_delta_rule_args* a, bool backward, bool precise)
         at += (bytes + 255) / 256 * 256;
         return was;
     };
-    z.gate = take(n * 3 * c * sizeof(float));
+    z.gate = take(n * 5 * c * sizeof(float));
     const size_t tri = (size_t)delta_triangle((int)c) * e;
     z.t = take(n * tri * (precise ? (size_t)delta_precise_parts(a->dtype) : fine));
     z.p = take(n * tri * fine);

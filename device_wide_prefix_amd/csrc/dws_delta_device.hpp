@@ -331,16 +331,19 @@ struct SlotInfo {
     int rows;          // its tokens, 0 for a slot without any
     int64_t beyond;    // for a slot behind the last sequence's: how far, else -1
 };
+// Every lane of the wave calls it. The last sequence whose first slot is not
+// behind `slot`, 64 candidates a round: a round is one trip to memory, and a
+// binary search's six would be most of a small kernel's time.
 template <int C>
-__device__ __forceinline__ SlotInfo slot_info(const int64_t* offsets, int64_t tokens, int64_t n_seqs, int64_t slot)
+__device__ __forceinline__ SlotInfo slot_info(const int64_t* offsets, int64_t tokens, int64_t n_seqs, int64_t slot, int lane)
 {
-    int64_t lo = 0, hi = n_seqs - 1;      // last sequence whose first slot is not behind `slot`
+    int64_t lo = 0, hi = n_seqs - 1;
     while (lo < hi) {
-        const int64_t mid = (lo + hi + 1) / 2;
-        if (first_slot(seq_begin(offsets, tokens, n_seqs, mid), mid, C) <= slot)
-            lo = mid;
-        else
-            hi = mid - 1;
+        const int64_t step = (hi - lo) / 64 + 1, at = lo + lane * step;
+        const bool in = at <= hi && first_slot(seq_begin(offsets, tokens, n_seqs, at <= hi ? at : hi), at, C) <= slot;
+        const uint64_t found = __ballot(in);
+        lo += found == 0 ? 0 : (63 - __builtin_clzll(found)) * step;
+        if (lo + step - 1 < hi) hi = lo + step - 1;
     }
     SlotInfo s;
     s.seq = lo;

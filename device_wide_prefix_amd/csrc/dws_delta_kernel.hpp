@@ -87,26 +87,35 @@ __device__ __forceinline__ void store_block(float* at, f32x4 x, int lane)
     for (int r = 0; r < 4; ++r) at[((lane >> 4) * 4 + r) * LD + (lane & 15)] = x[r];
 }
 
+// Row length of the inversion's matrices: rows start at 16 bytes, and 16 rows
+// in different banks.
+constexpr int inverse_stride(int c) { return c + 4; }
+
 // inv = (I + m)^-1, m strictly lower triangular, both fp32 in LDS with rows of
-// C + 1. The diagonal 16 x 16 blocks by substitution (one wave each, a column a
+// inverse_stride(C); of m only the entries below the diagonal are read. The diagonal 16 x 16 blocks by substitution (one wave each, a column a
 // lane), then twice as large blocks from two: [[A, 0], [M, B]]^-1 has
 // -B^-1 M A^-1 in its corner. Substitution keeps the error at the size of the
 // result's entries; a product of powers (I - m)(I + m^2).. would not, since the
-// powers of m can be far larger than its inverse. `tmp`: C x (C + 1).
+// powers of m can be far larger than its inverse. `tmp` is as large.
 template <int C>
 __device__ __forceinline__ void invert_unit_lower(const float* m, float* inv, float* tmp, int wave, int lane)
 {
-    constexpr int NB = C / 16, LD = C + 1;
+    constexpr int NB = C / 16, LD = inverse_stride(C);
     const int col = lane & 15, gq = lane >> 4;
     {
         const float* d = m + wave * 16 * (LD + 1);
         float x[16];
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
-            float s = i == col ? 1.f : 0.f;
+            f32x4 s = {i == col ? 1.f : 0.f, 0.f, 0.f, 0.f};      // four sums: a shorter chain
 #pragma unroll
-            for (int j = 0; j < i; ++j) s -= d[i * LD + j] * x[j];
-            x[i] = s;
+            for (int j = 0; j < i; j += 4) {
+                const f32x4 v = *reinterpret_cast<const f32x4*>(d + i * LD + j);
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (j + e < i) s[e] -= v[e] * x[j + e];
+            }
+            x[i] = (s[0] + s[1]) + (s[2] + s[3]);
         }
         // four lanes have the same column: each stores a quarter of it
 #pragma unroll
@@ -136,8 +145,12 @@ __device__ __forceinline__ void invert_unit_lower(const float* m, float* inv, fl
     }
 }
 
-// Sums of the chunk's log decays, in double: the differences of two sums of 64
-// then keep fp32 accuracy however large the sums are.
+// Gate factors of a chunk in the workspace: e^G, e^(G_C - G), beta, and the sums
+// of the decays (as logarithms to base 2) in two fp32 parts, C of each.
+constexpr int kGateArrays = 5;
+
+// Sums over a chunk in double, then split in two: the difference of two sums
+// keeps fp32 accuracy however large they are.
 template <int C>
 __device__ __forceinline__ double scan_decays(double g, int lane)
 {
@@ -147,6 +160,12 @@ __device__ __forceinline__ double scan_decays(double g, int lane)
         if (lane >= d) g += o;
     }
     return g;
+}
+__device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
+// e^(G_i - G_j)
+__device__ __forceinline__ float decay(float hi_i, float lo_i, float hi_j, float lo_j)
+{
+    return exp2_fast((hi_i - hi_j) + (lo_i - lo_j));
 }
 
 template <class T>
@@ -163,20 +182,24 @@ __device__ __forceinline__ void zero_rows(const DeltaRows& r, int64_t first, int
         }
 }
 
+__device__ __forceinline__ f32x4 gate4(const float* gate, int row) { return *reinterpret_cast<const f32x4*>(gate + row); }
+// Row of tile t of a lower triangle's tiles in order: 0; 1, 1; 2, 2, 2; ...
+__device__ __forceinline__ int tile_row(int t) { return t < 1 ? 0 : (t < 3 ? 1 : (t < 6 ? 2 : 3)); }
+
 // LDS of the preparation: the matrices of the inversion share their place with
 // the K and Q tiles, which are done with before.
 template <class T, int DK>
 struct PrepLds {
-    static constexpr int C = kChunk<T, DK>, LK = lds_stride<T>(DK), LD = C + 1;
+    static constexpr int C = kChunk<T, DK>, LK = lds_stride<T>(DK), LD = inverse_stride(C);
     static constexpr size_t tiles = 2 * (size_t)C * LK * sizeof(T), inverse = 2 * (size_t)C * LD * sizeof(float);
     static constexpr size_t shared = tiles > inverse ? tiles : inverse;
-    static constexpr size_t total = shared, beta = total + C * sizeof(double), m = beta + C * sizeof(float);
+    static constexpr size_t gate = shared, m = gate + 3 * C * sizeof(float);      // gate: beta, sums
     static constexpr size_t bytes = m + (size_t)C * LD * sizeof(float);
 };
 
 // One workgroup for each (chunk slot, value head): gate factors, P and the
-// inverse(s) to the workspace. Products over dim_k on the matrix cores, wave w
-// owning the tokens 16 w .. 16 w + 15.
+// inverse(s) to the workspace. The 16 x 16 tiles of K K^T and Q K^T up to the
+// diagonal, row by row, go to the waves in turn.
 template <class T, int DK, int NP, bool BWD>
 __global__ __launch_bounds__((kChunk<T, DK> * 4)) void k_delta_prep(DeltaParams p)
 {
@@ -188,13 +211,14 @@ __global__ __launch_bounds__((kChunk<T, DK> * 4)) void k_delta_prep(DeltaParams 
     T* qs = ks + C * LK;
     float* inv = reinterpret_cast<float*>(smem);
     float* tmp = inv + C * LD;
-    double* total = reinterpret_cast<double*>(smem + S::total);
-    float* beta = reinterpret_cast<float*>(smem + S::beta);
+    float* beta = reinterpret_cast<float*>(smem + S::gate);
+    float* sum_hi = beta + C;
+    float* sum_lo = sum_hi + C;
     float* m = reinterpret_cast<float*>(smem + S::m);
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, gq = lane >> 4, lr = lane & 15;
     const int64_t slot = blockIdx.x / p.heads_v;
     const int h = blockIdx.x % p.heads_v, hk = h / (p.heads_v / p.heads_qk);
-    const SlotInfo info = slot_info<C>(p.offsets, p.tokens, p.n_seqs, slot);
+    const SlotInfo info = slot_info<C>(p.offsets, p.tokens, p.n_seqs, slot, lane);
     if (info.rows == 0) {
         if (p.zero_tail && info.beyond >= 0 && h == 0) {
             const int64_t begin = seq_begin(p.offsets, p.tokens, p.n_seqs, info.seq);
@@ -224,56 +248,71 @@ __global__ __launch_bounds__((kChunk<T, DK> * 4)) void k_delta_prep(DeltaParams 
     TileRegs<T, C, DK, THREADS> kr, qr;
     kr.load(k0, p.k.ts, info.rows, p.dim_k, tid);
     qr.load(q0, p.q.ts, info.rows, p.dim_k, tid);
-    kr.store(ks, LK, tid);
-    qr.store(qs, LK, tid);
     if (wave == 0) {
-        const double sum = scan_decays<C>((double)g, lane);
+        const double sum = scan_decays<C>((double)g * 1.4426950408889634, lane);
         const double last = __shfl(sum, C - 1, 64);
         if (lane < C) {
-            total[lane] = sum;
+            const float hi = (float)sum, lo = (float)(sum - (double)hi);
             beta[lane] = b;
-            float* w = p.w_gate + at * 3 * C;
-            w[lane] = expf((float)sum);
-            w[C + lane] = expf((float)(last - sum));
+            sum_hi[lane] = hi;
+            sum_lo[lane] = lo;
+            float* w = p.w_gate + at * kGateArrays * C;
+            w[lane] = exp2_fast(hi);
+            w[C + lane] = exp2_fast((float)(last - sum));
             w[2 * C + lane] = b;
+            w[3 * C + lane] = hi;
+            w[4 * C + lane] = lo;
         }
     }
+    kr.store(ks, LK, tid);
+    qr.store(qs, LK, tid);
     __syncthreads();
 
-    // row tile `wave` of K K^T and Q K^T, up to the diagonal. m = L B.
+    // A tile's results run along i for the forward pass and along j for the
+    // backward one, whichever makes a lane's four neighbours in P or its
+    // transpose. m = L B.
     using F = Triangle<C>;
+    constexpr int TILES = NB * (NB + 1) / 2, EACH = (TILES + NB - 1) / NB;
     T* wp = static_cast<T*>(p.w_p) + at * NF * F::elems;
-    f32x4 low[BWD ? NB : 1];      // B L
+    f32x4 low[BWD ? EACH : 1];      // B L
 #pragma unroll
-    for (int nt = 0; nt < NB; ++nt) {
-        // P goes out four elements of a row a lane: its rows are tokens i
-        // forward, j (P transposed) backward, the other token being the one
-        // that runs along a lane's four results
+    for (int e = 0; e < EACH; ++e) {
+        const int tile = e * NB + wave;
+        if (tile >= TILES) break;
+        const int it = tile_row(tile), jt = tile - it * (it + 1) / 2;
         f32x4 kk = {}, qk = {};
-        if (nt <= wave) {
 #pragma unroll
-            for (int kb = 0; kb < DK; kb += 32) {
-                const Vec8<T> ki = frag_nat(ks, LK, wave * 16, kb, lane), kj = frag_nat(ks, LK, nt * 16, kb, lane);
-                const Vec8<T> qi = frag_nat(qs, LK, wave * 16, kb, lane);
-                kk = mma(ki, kj, kk);
-                qk = BWD ? mma(qi, kj, qk) : mma(kj, qi, qk);
-            }
+        for (int kb = 0; kb < DK; kb += 32) {
+            const Vec8<T> ki = frag_nat(ks, LK, it * 16, kb, lane), kj = frag_nat(ks, LK, jt * 16, kb, lane);
+            const Vec8<T> qi = frag_nat(qs, LK, it * 16, kb, lane);
+            kk = BWD ? mma(ki, kj, kk) : mma(kj, ki, kk);
+            qk = BWD ? mma(qi, kj, qk) : mma(kj, qi, qk);
         }
-        f32x4 pij;
+        const int one = (BWD ? jt : it) * 16 + lr, four = (BWD ? it : jt) * 16 + gq * 4;
+        const float hi = sum_hi[one], lo = sum_lo[one], b1 = beta[one];
+        const f32x4 hi4 = gate4(sum_hi, four), lo4 = gate4(sum_lo, four), b4 = gate4(beta, four);
+        f32x4 pij, mij;
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-            const int i = wave * 16 + gq * 4 + r, j = nt * 16 + lr;
-            const float d = i > j ? expf((float)(total[i] - total[j])) : 0.f;
-            m[i * LD + j] = i > j ? d * beta[j] * kk[r] : 0.f;
-            if constexpr (BWD) low[nt][r] = i > j ? d * beta[i] * kk[r] : 0.f;
-            const int pi = BWD ? i : wave * 16 + lr, pj = BWD ? j : nt * 16 + gq * 4 + r;
-            const float e = BWD ? d : (pi > pj ? expf((float)(total[pi] - total[pj])) : 0.f);
-            pij[r] = pi > pj ? p.scale * e * qk[r] : (pi == pj ? p.scale * qk[r] : 0.f);
+            const int i = BWD ? four + r : one, j = BWD ? one : four + r;
+            const float d = BWD ? decay(hi4[r], lo4[r], hi, lo) : decay(hi, lo, hi4[r], lo4[r]);
+            pij[r] = i > j ? p.scale * d * qk[r] : (i == j ? p.scale * qk[r] : 0.f);
+            mij[r] = i > j ? d * kk[r] : 0.f;
         }
-        if (BWD ? F::in_upper(nt * 16, wave * 16) : F::in_lower(wave * 16, nt * 16))
-            store_parts4<NF>(wp + (BWD ? F::upper_acc(nt * 16 + lr, wave * 16 + gq * 4)
-                                       : F::lower_nat(wave * 16 + lr, nt * 16 + gq * 4)),
-                             F::elems, pij);
+        if constexpr (BWD) {
+            low[e] = mij * b4;
+#pragma unroll
+            for (int r = 0; r < 4; ++r) m[(four + r) * LD + one] = mij[r] * b1;
+            store_parts4<NF>(wp + F::upper_acc(one, four), F::elems, pij);
+        } else {
+            *reinterpret_cast<f32x4*>(m + one * LD + four) = mij * b4;
+            store_parts4<NF>(wp + F::lower_nat(one, four), F::elems, pij);
+        }
+    }
+    // the zero tile beside each even diagonal tile, which its fragment holds
+    if (wave % 2 == 0) {
+        const int row = (BWD ? wave + 1 : wave) * 16 + lr, c = (BWD ? wave : wave + 1) * 16 + gq * 4;
+        store_parts4<NF>(wp + (BWD ? F::upper_acc(row, c) : F::lower_nat(row, c)), F::elems, f32x4{});
     }
     __syncthreads();
 
@@ -288,9 +327,12 @@ __global__ __launch_bounds__((kChunk<T, DK> * 4)) void k_delta_prep(DeltaParams 
         // the other inverse, of I + B L
         __syncthreads();
 #pragma unroll
-        for (int nt = 0; nt < NB; ++nt)
-#pragma unroll
-            for (int r = 0; r < 4; ++r) m[(wave * 16 + gq * 4 + r) * LD + nt * 16 + lr] = low[nt][r];
+        for (int e = 0; e < EACH; ++e) {
+            const int tile = e * NB + wave;
+            if (tile >= TILES) break;
+            const int it = tile_row(tile), jt = tile - it * (it + 1) / 2;
+            store_block<LD>(m + it * 16 * LD + jt * 16, low[e], lane);
+        }
         __syncthreads();
         invert_unit_lower<C>(m, inv, tmp, wave, lane);
         T* wtt = static_cast<T*>(p.w_tt) + at * NF * F::elems;
@@ -389,7 +431,6 @@ __device__ __forceinline__ void store_columns(T* at, const f32x4 (&u)[C / 16], i
 #pragma unroll
     for (int mt = 0; mt < C / 16; ++mt) store_parts4<NF>(at + col * C + mt * 16 + gq * 4, (int64_t)C * dv_pad, u[mt]);
 }
-__device__ __forceinline__ f32x4 gate4(const float* gate, int row) { return *reinterpret_cast<const f32x4*>(gate + row); }
 
 
 // STORE: instead of the outputs, the states at the chunks' starts and U' go to
@@ -432,7 +473,7 @@ __global__ __launch_bounds__(NW * 128) DWS_TWO_WAVES void k_delta_scan(DeltaPara
             kr.load(k0 + (int64_t)c * C * p.k.ts, p.k.ts, rows, p.dim_k, tid);
             tr.load(static_cast<const T*>(p.w_t) + place_at(c) * NX * F::elems, 0, 1, NX * F::elems, tid);
             vr.load(v0 + (int64_t)c * C * p.v.ts, p.v.ts, rows, cols, tid);
-            gr.load(p.w_gate + place_at(c) * 3 * C, 0, 1, 3 * C, tid);
+            gr.load(p.w_gate + place_at(c) * kGateArrays * C, 0, 1, 3 * C, tid);
         };
         auto store = [&](int c) {
             char* buffer = smem + (c & 1) * L::buffer;
@@ -518,7 +559,7 @@ __global__ __launch_bounds__(NW * 128) DWS_TWO_WAVES void k_delta_scan(DeltaPara
                             qf[kb][m].p[0] = buffer_frag<T>(
                                 rsrc, row < rows && k < p.dim_k ? (row * (int)p.q.ts + k) * (int)sizeof(T) : kOutside);
                         }
-                        eg[m] = p.w_gate[place_at(c) * 3 * C + row];
+                        eg[m] = p.w_gate[place_at(c) * kGateArrays * C + row];
                         // (above the diagonal: not kept, and 0)
 #pragma unroll
                         for (int kb = 0; kb < C / 32; ++kb)
@@ -663,7 +704,7 @@ __global__ __launch_bounds__(NW * 128) DWS_TWO_WAVES void k_delta_scan_back(Delt
             tr.load(static_cast<const T*>(p.w_tt) + place_at(c) * NF * F::elems, 0, 1, NF * F::elems, tid);
             pr.load(static_cast<const T*>(p.w_p) + place_at(c) * NF * F::elems, 0, 1, NF * F::elems, tid);
             orr.load(o0 + (int64_t)c * C * p.d_out.ts, p.d_out.ts, rows, cols, tid);
-            gr.load(p.w_gate + place_at(c) * 3 * C, 0, 1, 3 * C, tid);
+            gr.load(p.w_gate + place_at(c) * kGateArrays * C, 0, 1, 3 * C, tid);
         };
         auto store = [&](int c) {
             char* buffer = smem + (c & 1) * L::buffer;
@@ -792,22 +833,23 @@ __global__ __launch_bounds__(NW * 128) DWS_TWO_WAVES void k_delta_scan_back(Delt
 //          w_i = (e^(G_C - G) B U' dS'^T)_i . k_i;   dG_C also gets sum w + e^(G_C) <S, dS'>
 //   dg_t = sum of dG_i from t to the chunk's end
 // One workgroup for each (chunk slot, query/key head). A wave owns a row tile
-// of 16 tokens and 128 of the key columns (all, or half of 256); the value heads
+// of 16 tokens and 64 of the key columns; the value heads
 // that share the key head come in turn, so that their sums need no atomics and
 // have one order. The workspace's arrays have a row a value column: blocks of 32
 // go through LDS, where the transposing reads make operands of them.
 
 template <class T, int DK>
 struct GradLds {
-    static constexpr int C = kChunk<T, DK>, NB = C / 16, GROUPS = DK > 128 ? DK / 128 : 1, THREADS = NB * GROUPS * 64;
+    static constexpr int C = kChunk<T, DK>, NB = C / 16, GROUPS = DK / 64, THREADS = NB * GROUPS * 64;
     static constexpr int LK = lds_stride<T>(DK), LC = lds_stride<T>(C), NF = kFine<T>;
-    static constexpr size_t total = 0, ks = C * sizeof(double), qs = ks + (size_t)C * LK * sizeof(T);
-    static constexpr size_t w1 = qs + (size_t)C * LK * sizeof(T), w2 = w1 + (size_t)NF * C * LC * sizeof(T);
-    static constexpr size_t st = w2 + (size_t)NF * C * LC * sizeof(T), dst = st + (size_t)32 * LK * sizeof(T);
-    static constexpr size_t ut = dst + (size_t)32 * LK * sizeof(T), zt = ut + (size_t)NF * 32 * LC * sizeof(T);
-    static constexpr size_t gate = zt + (size_t)NF * 32 * LC * sizeof(T);
-    // floats behind: gate[3 C], row_part[GROUPS C], row_w[GROUPS C], d_beta[C], col_part[NB C], inner[THREADS / 64]
-    static constexpr size_t bytes = gate + ((4 + 2 * GROUPS + NB) * C + 16) * sizeof(float);
+    static constexpr size_t ks = 0, qs = ks + (size_t)C * LK * sizeof(T), w1 = qs + (size_t)C * LK * sizeof(T);
+    static constexpr size_t w2 = w1 + (size_t)NF * C * LC * sizeof(T), w_end = w2 + (size_t)NF * C * LC * sizeof(T);
+    // the blocks of 32 value columns are done with before W1 and W2 are written
+    static constexpr size_t st = w1, dst = st + (size_t)32 * LK * sizeof(T), ut = dst + (size_t)32 * LK * sizeof(T);
+    static constexpr size_t zt = ut + (size_t)NF * 32 * LC * sizeof(T), z_end = zt + (size_t)NF * 32 * LC * sizeof(T);
+    static constexpr size_t gate = w_end > z_end ? w_end : z_end;
+    // floats behind: gate[5 C], row_part[GROUPS C], row_w[GROUPS C], d_beta[C], col_part[NB C], inner[THREADS / 64]
+    static constexpr size_t bytes = gate + ((kGateArrays + 1 + 2 * GROUPS + NB) * C + 16) * sizeof(float);
 };
 
 __device__ __forceinline__ float sum16(float x)      // over the 16 lanes of a group
@@ -823,13 +865,12 @@ __device__ __forceinline__ float sum_groups(float x) // over the 4 groups
 }
 
 template <class T, int DK>
-__global__ __launch_bounds__((GradLds<T, DK>::THREADS)) DWS_ONE_WAVE void k_delta_grad(DeltaParams p)
+__global__ __launch_bounds__((GradLds<T, DK>::THREADS)) DWS_TWO_WAVES void k_delta_grad(DeltaParams p)
 {
     using L = GradLds<T, DK>;
     constexpr int C = L::C, THREADS = L::THREADS, NB = L::NB, GROUPS = L::GROUPS, LK = L::LK, LC = L::LC, NF = L::NF;
     constexpr int NK = DK / 16 / GROUPS;             // key column tiles of a wave
     extern __shared__ __attribute__((aligned(16))) char smem[];
-    double* total = reinterpret_cast<double*>(smem);
     T* ks = reinterpret_cast<T*>(smem + L::ks);
     T* qs = reinterpret_cast<T*>(smem + L::qs);
     T* w1 = reinterpret_cast<T*>(smem + L::w1);
@@ -838,18 +879,18 @@ __global__ __launch_bounds__((GradLds<T, DK>::THREADS)) DWS_ONE_WAVE void k_delt
     T* dst = reinterpret_cast<T*>(smem + L::dst);
     T* ut = reinterpret_cast<T*>(smem + L::ut);
     T* zt = reinterpret_cast<T*>(smem + L::zt);
-    float* gate = reinterpret_cast<float*>(smem + L::gate);      // e^G, e^(G_C - G), beta
-    float* row_part = gate + 3 * C;                              // dG without column sums and w
+    float* gate = reinterpret_cast<float*>(smem + L::gate);      // the workspace's factors
+    float* row_part = gate + kGateArrays * C;                    // dG without column sums and w
     float* row_w = row_part + GROUPS * C;                        // w
     float* d_beta = row_w + GROUPS * C;
     float* col_part = d_beta + C;                                // [NB][C] column sums of N
     float* inner = col_part + NB * C;                            // parts of <S, dS'>
 
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, gq = lane >> 4, lr = lane & 15;
-    const int tile = wave % NB, grp = wave / NB, row0 = tile * 16, key0 = grp * 128;
+    const int tile = wave % NB, grp = wave / NB, row0 = tile * 16, key0 = grp * 64;
     const int64_t slot = blockIdx.x / p.heads_qk;
     const int hk = blockIdx.x % p.heads_qk, share = p.heads_v / p.heads_qk;
-    const SlotInfo info = slot_info<C>(p.offsets, p.tokens, p.n_seqs, slot);
+    const SlotInfo info = slot_info<C>(p.offsets, p.tokens, p.n_seqs, slot, lane);
     if (info.rows == 0) return;
     const int rows = info.rows;
 
@@ -877,12 +918,7 @@ __global__ __launch_bounds__((GradLds<T, DK>::THREADS)) DWS_ONE_WAVE void k_delt
     for (int m = 0; m < share; ++m) {
         const int h = hk * share + m;
         const int64_t at = slot * p.heads_v + h;
-        for (int i = tid; i < 3 * C; i += THREADS) gate[i] = p.w_gate[at * 3 * C + i];
-        if (wave == 0) {
-            const float g = lane < rows && p.g.data ? clamp_decay(load_gate(p.g, info.row + lane, h, p.g_dtype)) : 0.f;
-            const double t = scan_decays<C>((double)g, lane);
-            if (lane < C) total[lane] = t;
-        }
+        for (int i = tid; i < kGateArrays * C; i += THREADS) gate[i] = p.w_gate[at * kGateArrays * C + i];
 
         const T* d_o = static_cast<const T*>(p.d_out.data) + info.row * p.d_out.ts + h * p.d_out.hs;
         const auto o_rsrc = rows_rsrc(d_o, p.d_out.ts * (int)sizeof(T), rows, whole_bytes<T>(p.dim_v));
@@ -963,11 +999,11 @@ __global__ __launch_bounds__((GradLds<T, DK>::THREADS)) DWS_ONE_WAVE void k_delt
                     qk = mma(frag_nat(qs, LK, row0, kb, lane), b, qk);
                 }
             }
-            const float bj = gate[2 * C + j];
+            const float bj = gate[2 * C + j], hj = gate[3 * C + j], lj = gate[4 * C + j];
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
                 const int i = row0 + gq * 4 + r;
-                const float d = i > j ? expf((float)(total[i] - total[j])) : (i == j ? 1.f : 0.f);
+                const float d = i > j ? decay(gate[3 * C + i], gate[4 * C + i], hj, lj) : (i == j ? 1.f : 0.f);
                 const float a = i >= j ? p.scale * d * bj * dp[nt][r] : 0.f;
                 const float b = i > j ? -gate[2 * C + i] * d * bj * zu[nt][r] : 0.f;
                 store_parts<NF>(w1 + i * LC + j, C * LC, a);
