@@ -870,6 +870,7 @@ __global__ __launch_bounds__((GradLds<T, DK>::THREADS)) DWS_TWO_WAVES void k_del
     using L = GradLds<T, DK>;
     constexpr int C = L::C, THREADS = L::THREADS, NB = L::NB, GROUPS = L::GROUPS, LK = L::LK, LC = L::LC, NF = L::NF;
     constexpr int NK = DK / 16 / GROUPS;             // key column tiles of a wave
+    constexpr int NT = NB > GROUPS ? NB / GROUPS : 1;      // its column tiles of W1 and W2: grp, grp + GROUPS, ..
     extern __shared__ __attribute__((aligned(16))) char smem[];
     T* ks = reinterpret_cast<T*>(smem + L::ks);
     T* qs = reinterpret_cast<T*>(smem + L::qs);
@@ -923,7 +924,7 @@ __global__ __launch_bounds__((GradLds<T, DK>::THREADS)) DWS_TWO_WAVES void k_del
         const T* d_o = static_cast<const T*>(p.d_out.data) + info.row * p.d_out.ts + h * p.d_out.hs;
         const auto o_rsrc = rows_rsrc(d_o, p.d_out.ts * (int)sizeof(T), rows, whole_bytes<T>(p.dim_v));
         const int o_at = (row0 + lr) * (int)p.d_out.ts;
-        f32x4 dp[NB] = {}, zu[NB] = {}, os[NK] = {}, zs[NK] = {}, us[NK] = {};
+        f32x4 dp[NT] = {}, zu[NT] = {}, os[NK] = {}, zs[NK] = {}, us[NK] = {};
         float zdotu = 0.f, sds = 0.f;
         for (int c = 0; c < p.dv_pad; c += 32) {
             // dO's rows of this wave, 32 columns in acc order
@@ -959,11 +960,11 @@ __global__ __launch_bounds__((GradLds<T, DK>::THREADS)) DWS_TWO_WAVES void k_del
                     zdotu += z * u;
                 }
 #pragma unroll
-            for (int nt = 0; nt < NB; ++nt)
-                if (nt <= tile && nt % GROUPS == grp) {
-                    const Parts<T, NF> b = parts_tr<NF>(ut, 32 * LC, LC, 0, nt * 16, lane);
-                    dp[nt] = mma(ao, b, dp[nt]);
-                    zu[nt] = mma(az, b, zu[nt]);
+            for (int i = 0; i < NT; ++i)
+                if (grp + i * GROUPS <= tile) {
+                    const Parts<T, NF> b = parts_tr<NF>(ut, 32 * LC, LC, 0, (grp + i * GROUPS) * 16, lane);
+                    dp[i] = mma(ao, b, dp[i]);
+                    zu[i] = mma(az, b, zu[i]);
                 }
 #pragma unroll
             for (int t = 0; t < NK; ++t) {
@@ -986,9 +987,9 @@ __global__ __launch_bounds__((GradLds<T, DK>::THREADS)) DWS_TWO_WAVES void k_del
         // W1, W2 and N; Q K^T and K K^T once more
         float nrow[4] = {};
 #pragma unroll
-        for (int nt = 0; nt < NB; ++nt) {
-            if (nt % GROUPS != grp) continue;
-            const int j = nt * 16 + lr;
+        for (int e = 0; e < NT; ++e) {
+            const int nt = grp + e * GROUPS, j = nt * 16 + lr;
+            if (nt >= NB) break;
             float ncol = 0.f;
             f32x4 kk = {}, qk = {};
             if (nt <= tile) {
@@ -1004,8 +1005,8 @@ __global__ __launch_bounds__((GradLds<T, DK>::THREADS)) DWS_TWO_WAVES void k_del
             for (int r = 0; r < 4; ++r) {
                 const int i = row0 + gq * 4 + r;
                 const float d = i > j ? decay(gate[3 * C + i], gate[4 * C + i], hj, lj) : (i == j ? 1.f : 0.f);
-                const float a = i >= j ? p.scale * d * bj * dp[nt][r] : 0.f;
-                const float b = i > j ? -gate[2 * C + i] * d * bj * zu[nt][r] : 0.f;
+                const float a = i >= j ? p.scale * d * bj * dp[e][r] : 0.f;
+                const float b = i > j ? -gate[2 * C + i] * d * bj * zu[e][r] : 0.f;
                 store_parts<NF>(w1 + i * LC + j, C * LC, a);
                 store_parts<NF>(w2 + i * LC + j, C * LC, b);
                 const float n = i > j ? a * qk[r] + b * kk[r] : 0.f;     // N_ii cancels in dG
@@ -1042,7 +1043,7 @@ __global__ __launch_bounds__((GradLds<T, DK>::THREADS)) DWS_TWO_WAVES void k_del
             }
         }
         // the products with K and Q: rows i of W1 and W2 for dQ and dK, columns for dK
-#pragma unroll
+#pragma unroll 1
         for (int kb = 0; kb < C / 32; ++kb) {
             const Parts<T, NF> a1 = parts_acc<NF>(w1, C * LC, LC, row0, kb * 32, lane);
             const Parts<T, NF> a2 = parts_acc<NF>(w2, C * LC, LC, row0, kb * 32, lane);
