@@ -338,17 +338,22 @@ template <int C>
 __device__ __forceinline__ SlotInfo slot_info(const int64_t* offsets, int64_t tokens, int64_t n_seqs, int64_t slot, int lane)
 {
     int64_t lo = 0, hi = n_seqs - 1;
-    while (lo < hi) {
+    while (hi - lo >= 64) {
         const int64_t step = (hi - lo) / 64 + 1, at = lo + lane * step;
         const bool in = at <= hi && first_slot(seq_begin(offsets, tokens, n_seqs, at <= hi ? at : hi), at, C) <= slot;
         const uint64_t found = __ballot(in);
         lo += found == 0 ? 0 : (63 - __builtin_clzll(found)) * step;
         if (lo + step - 1 < hi) hi = lo + step - 1;
     }
+    // the last round brings the sequence's rows along
+    const int64_t at = lo + lane <= hi ? lo + lane : hi;
+    const int64_t b = seq_begin(offsets, tokens, n_seqs, at), n = seq_length(offsets, tokens, n_seqs, at, b);
+    const uint64_t found = __ballot(lo + lane <= hi && first_slot(b, at, C) <= slot);
+    const int k = found == 0 ? 0 : 63 - __builtin_clzll(found);
+    lo += k;
     SlotInfo s;
     s.seq = lo;
-    const int64_t begin = seq_begin(offsets, tokens, n_seqs, lo);
-    const int64_t len = seq_length(offsets, tokens, n_seqs, lo, begin);
+    const int64_t begin = __shfl(b, k, 64), len = __shfl(n, k, 64);
     const int64_t c = slot - first_slot(begin, lo, C);
     const int64_t left = len - c * C;
     s.row = begin + c * C;

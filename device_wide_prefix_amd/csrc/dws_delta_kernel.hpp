@@ -92,11 +92,12 @@ __device__ __forceinline__ void store_block(float* at, f32x4 x, int lane)
 constexpr int inverse_stride(int c) { return c + 4; }
 
 // inv = (I + m)^-1, m strictly lower triangular, both fp32 in LDS with rows of
-// inverse_stride(C); of m only the entries below the diagonal are read. The diagonal 16 x 16 blocks by substitution (one wave each, a column a
+// inverse_stride(C); of m only the entries below the diagonal are read, and the
+// inverse's upper right quarter is not written. The diagonal 16 x 16 blocks by substitution (one wave each, a column a
 // lane), then twice as large blocks from two: [[A, 0], [M, B]]^-1 has
 // -B^-1 M A^-1 in its corner. Substitution keeps the error at the size of the
 // result's entries; a product of powers (I - m)(I + m^2).. would not, since the
-// powers of m can be far larger than its inverse. `tmp` is as large.
+// powers of m can be far larger than its inverse. `tmp`: 32 x 32, the same rows.
 template <int C>
 __device__ __forceinline__ void invert_unit_lower(const float* m, float* inv, float* tmp, int wave, int lane)
 {
@@ -121,17 +122,18 @@ __device__ __forceinline__ void invert_unit_lower(const float* m, float* inv, fl
 #pragma unroll
         for (int i = 0; i < 16; ++i)
             if (i / 4 == gq) inv[(wave * 16 + i) * LD + wave * 16 + col] = x[i];
-        for (int jb = wave + 1; jb < NB; ++jb) store_block<LD>(inv + wave * 16 * LD + jb * 16, f32x4{}, lane);
+        if (wave % 2 == 0) store_block<LD>(inv + wave * 16 * LD + (wave + 1) * 16, f32x4{}, lane);
     }
     __syncthreads();
     // 16 -> 32: wave w < NB / 2 makes block (2 w + 1, 2 w)
     const int a = wave * 2;
     if (wave < NB / 2)
-        store_block<LD>(tmp + a * 16 * LD, block_product<LD, 16>(m + (a + 1) * 16 * LD + a * 16, inv + a * 16 * (LD + 1), f32x4{}, lane), lane);
+        store_block<LD>(tmp + wave * 16 * LD,
+                        block_product<LD, 16>(m + (a + 1) * 16 * LD + a * 16, inv + a * 16 * (LD + 1), f32x4{}, lane), lane);
     __syncthreads();
     if (wave < NB / 2)
         store_block<LD>(inv + (a + 1) * 16 * LD + a * 16,
-                        -block_product<LD, 16>(inv + (a + 1) * 16 * (LD + 1), tmp + a * 16 * LD, f32x4{}, lane), lane);
+                        -block_product<LD, 16>(inv + (a + 1) * 16 * (LD + 1), tmp + wave * 16 * LD, f32x4{}, lane), lane);
     __syncthreads();
     if constexpr (NB == 4) {
         // 32 -> 64: four blocks, one a wave
@@ -191,10 +193,11 @@ __device__ __forceinline__ int tile_row(int t) { return t < 1 ? 0 : (t < 3 ? 1 :
 template <class T, int DK>
 struct PrepLds {
     static constexpr int C = kChunk<T, DK>, LK = lds_stride<T>(DK), LD = inverse_stride(C);
-    static constexpr size_t tiles = 2 * (size_t)C * LK * sizeof(T), inverse = 2 * (size_t)C * LD * sizeof(float);
-    static constexpr size_t shared = tiles > inverse ? tiles : inverse;
-    static constexpr size_t gate = shared, m = gate + 3 * C * sizeof(float);      // gate: beta, sums
-    static constexpr size_t bytes = m + (size_t)C * LD * sizeof(float);
+    static constexpr size_t tiles = 2 * (size_t)C * LK * sizeof(T), matrix = (size_t)C * LD * sizeof(float);
+    // m and the inverse; a chunk of 64 keeps block products in the inverse's
+    // upper right quarter, one of 32 behind it
+    static constexpr size_t inverse = (C == 64 ? 2 : 3) * matrix;
+    static constexpr size_t gate = tiles > inverse ? tiles : inverse, bytes = gate + 3 * C * sizeof(float);
 };
 
 // One workgroup for each (chunk slot, value head): gate factors, P and the
@@ -209,12 +212,12 @@ __global__ __launch_bounds__((kChunk<T, DK> * 4)) void k_delta_prep(DeltaParams 
     extern __shared__ __attribute__((aligned(16))) char smem[];
     T* ks = reinterpret_cast<T*>(smem);
     T* qs = ks + C * LK;
-    float* inv = reinterpret_cast<float*>(smem);
-    float* tmp = inv + C * LD;
+    float* m = reinterpret_cast<float*>(smem);
+    float* inv = m + C * LD;
+    float* tmp = C == 64 ? inv + 32 : inv + C * LD;
     float* beta = reinterpret_cast<float*>(smem + S::gate);
     float* sum_hi = beta + C;
     float* sum_lo = sum_hi + C;
-    float* m = reinterpret_cast<float*>(smem + S::m);
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, gq = lane >> 4, lr = lane & 15;
     const int64_t slot = blockIdx.x / p.heads_v;
     const int h = blockIdx.x % p.heads_v, hk = h / (p.heads_v / p.heads_qk);
@@ -275,6 +278,7 @@ __global__ __launch_bounds__((kChunk<T, DK> * 4)) void k_delta_prep(DeltaParams 
     constexpr int TILES = NB * (NB + 1) / 2, EACH = (TILES + NB - 1) / NB;
     T* wp = static_cast<T*>(p.w_p) + at * NF * F::elems;
     f32x4 low[BWD ? EACH : 1];      // B L
+    f32x4 lb[EACH];                 // L B, for m once K and Q are done with
 #pragma unroll
     for (int e = 0; e < EACH; ++e) {
         const int tile = e * NB + wave;
@@ -301,11 +305,10 @@ __global__ __launch_bounds__((kChunk<T, DK> * 4)) void k_delta_prep(DeltaParams 
         }
         if constexpr (BWD) {
             low[e] = mij * b4;
-#pragma unroll
-            for (int r = 0; r < 4; ++r) m[(four + r) * LD + one] = mij[r] * b1;
+            lb[e] = mij * b1;
             store_parts4<NF>(wp + F::upper_acc(one, four), F::elems, pij);
         } else {
-            *reinterpret_cast<f32x4*>(m + one * LD + four) = mij * b4;
+            lb[e] = mij * b4;
             store_parts4<NF>(wp + F::lower_nat(one, four), F::elems, pij);
         }
     }
@@ -313,6 +316,17 @@ __global__ __launch_bounds__((kChunk<T, DK> * 4)) void k_delta_prep(DeltaParams 
     if (wave % 2 == 0) {
         const int row = (BWD ? wave + 1 : wave) * 16 + lr, c = (BWD ? wave : wave + 1) * 16 + gq * 4;
         store_parts4<NF>(wp + (BWD ? F::upper_acc(row, c) : F::lower_nat(row, c)), F::elems, f32x4{});
+    }
+    __syncthreads();
+#pragma unroll
+    for (int e = 0; e < EACH; ++e) {
+        const int tile = e * NB + wave;
+        if (tile >= TILES) break;
+        const int it = tile_row(tile), jt = tile - it * (it + 1) / 2;
+        if constexpr (BWD)
+            store_block<LD>(m + it * 16 * LD + jt * 16, lb[e], lane);
+        else
+            *reinterpret_cast<f32x4*>(m + (it * 16 + lr) * LD + jt * 16 + gq * 4) = lb[e];
     }
     __syncthreads();
 
@@ -845,11 +859,14 @@ struct GradLds {
     static constexpr size_t ks = 0, qs = ks + (size_t)C * LK * sizeof(T), w1 = qs + (size_t)C * LK * sizeof(T);
     static constexpr size_t w2 = w1 + (size_t)NF * C * LC * sizeof(T), w_end = w2 + (size_t)NF * C * LC * sizeof(T);
     // the blocks of 32 value columns are done with before W1 and W2 are written
-    static constexpr size_t st = w1, dst = st + (size_t)32 * LK * sizeof(T), ut = dst + (size_t)32 * LK * sizeof(T);
+    // (read transposed only: rows 32 bytes longer lie in different banks)
+    static constexpr int LS = DK + 32 / (int)sizeof(T);
+    static constexpr size_t st = w1, dst = st + (size_t)32 * LS * sizeof(T), ut = dst + (size_t)32 * LS * sizeof(T);
     static constexpr size_t zt = ut + (size_t)NF * 32 * LC * sizeof(T), z_end = zt + (size_t)NF * 32 * LC * sizeof(T);
     static constexpr size_t gate = w_end > z_end ? w_end : z_end;
-    // floats behind: gate[5 C], row_part[GROUPS C], row_w[GROUPS C], d_beta[C], col_part[NB C], inner[THREADS / 64]
-    static constexpr size_t bytes = gate + ((kGateArrays + 1 + 2 * GROUPS + NB) * C + 16) * sizeof(float);
+    // floats behind: gate[5 C], row_part[GROUPS C], row_w[GROUPS C], d_beta[C], col_part[NB C], n_part[GROUPS C],
+    // inner[THREADS / 64]
+    static constexpr size_t bytes = gate + ((kGateArrays + 1 + 3 * GROUPS + NB) * C + 16) * sizeof(float);
 };
 
 __device__ __forceinline__ float sum16(float x)      // over the 16 lanes of a group
@@ -868,7 +885,7 @@ template <class T, int DK>
 __global__ __launch_bounds__((GradLds<T, DK>::THREADS)) DWS_TWO_WAVES void k_delta_grad(DeltaParams p)
 {
     using L = GradLds<T, DK>;
-    constexpr int C = L::C, THREADS = L::THREADS, NB = L::NB, GROUPS = L::GROUPS, LK = L::LK, LC = L::LC, NF = L::NF;
+    constexpr int C = L::C, THREADS = L::THREADS, NB = L::NB, GROUPS = L::GROUPS, LK = L::LK, LC = L::LC, LS = L::LS, NF = L::NF;
     constexpr int NK = DK / 16 / GROUPS;             // key column tiles of a wave
     constexpr int NT = NB > GROUPS ? NB / GROUPS : 1;      // its column tiles of W1 and W2: grp, grp + GROUPS, ..
     extern __shared__ __attribute__((aligned(16))) char smem[];
@@ -885,7 +902,8 @@ __global__ __launch_bounds__((GradLds<T, DK>::THREADS)) DWS_TWO_WAVES void k_del
     float* row_w = row_part + GROUPS * C;                        // w
     float* d_beta = row_w + GROUPS * C;
     float* col_part = d_beta + C;                                // [NB][C] column sums of N
-    float* inner = col_part + NB * C;                            // parts of <S, dS'>
+    float* n_part = col_part + NB * C;                           // [GROUPS][C] row sums of N
+    float* inner = n_part + GROUPS * C;                          // parts of <S, dS'>
 
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, gq = lane >> 4, lr = lane & 15;
     const int tile = wave % NB, grp = wave / NB, row0 = tile * 16, key0 = grp * 64;
@@ -897,7 +915,15 @@ __global__ __launch_bounds__((GradLds<T, DK>::THREADS)) DWS_TWO_WAVES void k_del
 
     TileRegs<T, 32, DK, THREADS> sr, dsr;
     TileRegs<T, 32, C, THREADS> ur[NF], zr[NF];
-    auto load = [&](int64_t at, int c) {
+    Vec4<T> oa, ob;        // dO's row lr of this wave, 32 columns in acc order
+    auto load = [&](int h, int c) {
+        const int64_t at = slot * p.heads_v + h;
+        const T* d_o = static_cast<const T*>(p.d_out.data) + info.row * p.d_out.ts + h * p.d_out.hs;
+        const auto rsrc = rows_rsrc(d_o, p.d_out.ts * (int)sizeof(T), rows, whole_bytes<T>(p.dim_v));
+        const int o0 = c + gq * 4, from = ((row0 + lr) * (int)p.d_out.ts + o0) * (int)sizeof(T);
+        const bool in = row0 + lr < rows;
+        oa = buffer_load<Vec4<T>>(rsrc, in && o0 < p.dim_v ? from : kOutside);
+        ob = buffer_load<Vec4<T>>(rsrc, in && o0 + 16 < p.dim_v ? from + 16 * (int)sizeof(T) : kOutside);
         sr.load(static_cast<const T*>(p.w_s) + (at * p.dv_pad + c) * DK, DK, 32, DK, tid);
         dsr.load(static_cast<const T*>(p.w_ds) + (at * p.dv_pad + c) * DK, DK, 32, DK, tid);
 #pragma unroll
@@ -906,7 +932,7 @@ __global__ __launch_bounds__((GradLds<T, DK>::THREADS)) DWS_TWO_WAVES void k_del
             zr[n].load(static_cast<const T*>(p.w_z) + ((at * NF + n) * p.dv_pad + c) * C, C, 32, C, tid);
         }
     };
-    load(slot * p.heads_v + hk * share, 0);
+    load(hk * share, 0);
     {
         TileRegs<T, C, DK, THREADS> kr, qr;
         kr.load(static_cast<const T*>(p.k.data) + info.row * p.k.ts + hk * p.k.hs, p.k.ts, rows, p.dim_k, tid);
@@ -921,21 +947,13 @@ __global__ __launch_bounds__((GradLds<T, DK>::THREADS)) DWS_TWO_WAVES void k_del
         const int64_t at = slot * p.heads_v + h;
         for (int i = tid; i < kGateArrays * C; i += THREADS) gate[i] = p.w_gate[at * kGateArrays * C + i];
 
-        const T* d_o = static_cast<const T*>(p.d_out.data) + info.row * p.d_out.ts + h * p.d_out.hs;
-        const auto o_rsrc = rows_rsrc(d_o, p.d_out.ts * (int)sizeof(T), rows, whole_bytes<T>(p.dim_v));
-        const int o_at = (row0 + lr) * (int)p.d_out.ts;
         f32x4 dp[NT] = {}, zu[NT] = {}, os[NK] = {}, zs[NK] = {}, us[NK] = {};
         float zdotu = 0.f, sds = 0.f;
         for (int c = 0; c < p.dv_pad; c += 32) {
-            // dO's rows of this wave, 32 columns in acc order
             Parts<T, 1> ao;
-            const int o0 = c + gq * 4, o1 = o0 + 16;
-            const bool in = row0 + lr < rows;
-            const Vec4<T> oa = buffer_load<Vec4<T>>(o_rsrc, in && o0 < p.dim_v ? (o_at + o0) * (int)sizeof(T) : kOutside);
-            const Vec4<T> ob = buffer_load<Vec4<T>>(o_rsrc, in && o1 < p.dim_v ? (o_at + o1) * (int)sizeof(T) : kOutside);
             ao.p[0] = __builtin_shufflevector(oa, ob, 0, 1, 2, 3, 4, 5, 6, 7);
-            sr.store(st, LK, tid);
-            dsr.store(dst, LK, tid);
+            sr.store(st, LS, tid);
+            dsr.store(dst, LS, tid);
 #pragma unroll
             for (int n = 0; n < NF; ++n) {
                 ur[n].store(ut + n * 32 * LC, LC, tid);
@@ -943,9 +961,9 @@ __global__ __launch_bounds__((GradLds<T, DK>::THREADS)) DWS_TWO_WAVES void k_del
             }
             __syncthreads();
             if (c + 32 < p.dv_pad)
-                load(at, c + 32);
+                load(h, c + 32);
             else if (m + 1 < share)
-                load(at + 1, 0);
+                load(h + 1, 0);
             const Parts<T, NF> az = parts_tr<NF>(zt, 32 * LC, LC, 0, row0, lane);
             const Parts<T, NF> au = parts_tr<NF>(ut, 32 * LC, LC, 0, row0, lane);
             if (grp == 0)
@@ -963,13 +981,13 @@ __global__ __launch_bounds__((GradLds<T, DK>::THREADS)) DWS_TWO_WAVES void k_del
             for (int i = 0; i < NT; ++i)
                 if (grp + i * GROUPS <= tile) {
                     const Parts<T, NF> b = parts_tr<NF>(ut, 32 * LC, LC, 0, (grp + i * GROUPS) * 16, lane);
-                    dp[i] = mma(ao, b, dp[i]);
-                    zu[i] = mma(az, b, zu[i]);
+                    dp[i] = mma(b, ao, dp[i]);
+                    zu[i] = mma(b, az, zu[i]);
                 }
 #pragma unroll
             for (int t = 0; t < NK; ++t) {
-                const Parts<T, 1> b = {{frag_tr(st, LK, 0, key0 + t * 16, lane)}};
-                const Parts<T, 1> d = {{frag_tr(dst, LK, 0, key0 + t * 16, lane)}};
+                const Parts<T, 1> b = {{frag_tr(st, LS, 0, key0 + t * 16, lane)}};
+                const Parts<T, 1> d = {{frag_tr(dst, LS, 0, key0 + t * 16, lane)}};
                 os[t] = mma(ao, b, os[t]);
                 zs[t] = mma(az.p[0], b, zs[t]);
                 us[t] = mma(au, d, us[t]);
@@ -984,59 +1002,64 @@ __global__ __launch_bounds__((GradLds<T, DK>::THREADS)) DWS_TWO_WAVES void k_del
         sds = sum_groups(sum16(sds));
         if (lane == 0) inner[wave] = sds;
 
-        // W1, W2 and N; Q K^T and K K^T once more
-        float nrow[4] = {};
+        // W1, W2 and N; Q K^T and K K^T once more. A lane has token i = lr of
+        // the row tile and four tokens j
+        float nrow = 0.f;
+        const int i = row0 + lr;
+        const float bi = gate[2 * C + i], hi = gate[3 * C + i], li = gate[4 * C + i];
 #pragma unroll
         for (int e = 0; e < NT; ++e) {
-            const int nt = grp + e * GROUPS, j = nt * 16 + lr;
+            const int nt = grp + e * GROUPS, j0 = nt * 16 + gq * 4;
             if (nt >= NB) break;
-            float ncol = 0.f;
-            f32x4 kk = {}, qk = {};
+            f32x4 a = {}, b = {}, ncol = {};
             if (nt <= tile) {
+                f32x4 kk = {}, qk = {};
 #pragma unroll
                 for (int kb = 0; kb < DK; kb += 32) {
-                    const Vec8<T> b = frag_nat(ks, LK, nt * 16, kb, lane);
-                    kk = mma(frag_nat(ks, LK, row0, kb, lane), b, kk);
-                    qk = mma(frag_nat(qs, LK, row0, kb, lane), b, qk);
+                    const Vec8<T> kj = frag_nat(ks, LK, nt * 16, kb, lane);
+                    kk = mma(kj, frag_nat(ks, LK, row0, kb, lane), kk);
+                    qk = mma(kj, frag_nat(qs, LK, row0, kb, lane), qk);
+                }
+                const f32x4 bj = gate4(gate, 2 * C + j0), hj = gate4(gate, 3 * C + j0), lj = gate4(gate, 4 * C + j0);
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const int j = j0 + r;
+                    const float d = decay(hi, li, hj[r], lj[r]) * bj[r];
+                    a[r] = i > j ? p.scale * d * dp[e][r] : (i == j ? p.scale * bj[r] * dp[e][r] : 0.f);
+                    b[r] = i > j ? -bi * d * zu[e][r] : 0.f;
+                    ncol[r] = i > j ? a[r] * qk[r] + b[r] * kk[r] : 0.f;     // N_ii cancels in dG
+                    nrow += ncol[r];
                 }
             }
-            const float bj = gate[2 * C + j], hj = gate[3 * C + j], lj = gate[4 * C + j];
+            store_parts4<NF>(w1 + i * LC + j0, C * LC, a);
+            store_parts4<NF>(w2 + i * LC + j0, C * LC, b);
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
-                const int i = row0 + gq * 4 + r;
-                const float d = i > j ? decay(gate[3 * C + i], gate[4 * C + i], hj, lj) : (i == j ? 1.f : 0.f);
-                const float a = i >= j ? p.scale * d * bj * dp[e][r] : 0.f;
-                const float b = i > j ? -gate[2 * C + i] * d * bj * zu[e][r] : 0.f;
-                store_parts<NF>(w1 + i * LC + j, C * LC, a);
-                store_parts<NF>(w2 + i * LC + j, C * LC, b);
-                const float n = i > j ? a * qk[r] + b * kk[r] : 0.f;     // N_ii cancels in dG
-                nrow[r] += n;
-                ncol += n;
+                const float n = sum16(ncol[r]);
+                if (lr == 0) col_part[tile * C + j0 + r] = n;
             }
-            ncol = sum_groups(ncol);
-            if (gq == 0) col_part[tile * C + j] = ncol;
         }
+        nrow = sum_groups(nrow);
+        if (gq == 0) n_part[grp * C + i] = nrow;
         __syncthreads();
 
         // the products with S, and their shares of dG
-        float grow[4] = {}, gw[4] = {};
+        f32x4 grow = {}, gw = {};
+        const f32x4 eg4 = gate4(gate, row0 + gq * 4), eo4 = gate4(gate, C + row0 + gq * 4);
+        const f32x4 b4 = gate4(gate, 2 * C + row0 + gq * 4);
 #pragma unroll
-        for (int t = 0; t < NK; ++t)
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const int i = row0 + gq * 4 + r, c = key0 + t * 16 + lr;
-                const float qv = (float)qs[i * LK + c], kv = (float)ks[i * LK + c];
-                const float b = gate[2 * C + i];
-                const float a1 = p.scale * gate[i] * os[t][r], a2 = gate[i] * b * zs[t][r];
-                const float a3 = gate[C + i] * b * us[t][r];
-                dq[t][r] += a1;
-                dk[t][r] += a3 - a2;
-                grow[r] += a1 * qv - a2 * kv;
-                gw[r] += a3 * kv;
-            }
+        for (int t = 0; t < NK; ++t) {
+            const f32x4 qv = __builtin_convertvector(quad_tr(qs, LK, row0, key0 + t * 16, lane), f32x4);
+            const f32x4 kv = __builtin_convertvector(quad_tr(ks, LK, row0, key0 + t * 16, lane), f32x4);
+            const f32x4 a1 = eg4 * p.scale * os[t], a2 = eg4 * b4 * zs[t], a3 = eo4 * b4 * us[t];
+            dq[t] += a1;
+            dk[t] += a3 - a2;
+            grow += a1 * qv - a2 * kv;
+            gw += a3 * kv;
+        }
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-            const float a = sum16(grow[r] + nrow[r]), b = sum16(gw[r]);
+            const float a = sum16(grow[r]), b = sum16(gw[r]);
             if (lr == 0) {
                 row_part[grp * C + row0 + gq * 4 + r] = a;
                 row_w[grp * C + row0 + gq * 4 + r] = b;
@@ -1066,7 +1089,7 @@ __global__ __launch_bounds__((GradLds<T, DK>::THREADS)) DWS_TWO_WAVES void k_del
 #pragma unroll
                 for (int i = 0; i < GROUPS; ++i) {
                     w += row_w[i * C + lane];
-                    x += row_part[i * C + lane];
+                    x += row_part[i * C + lane] + n_part[i * C + lane];
                 }
                 x -= w;
 #pragma unroll
