@@ -28,6 +28,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 PKG_DIR = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(PKG_DIR, "libdws_scan.so")
@@ -174,11 +175,12 @@ def load_library():
     lib.dws_run_length_encode.restype = ci
     lib.dws_select_flagged.argtypes = [vp, vp, vp, sz, ci, vp, vp]
     lib.dws_select_flagged.restype = ci
-    lib.dws_delta_rule_workspace.argtypes = [ctypes.POINTER(DeltaRuleArgs), ci, ctypes.POINTER(sz)]
+    # (dws_delta_rule_args by address: a DeltaRuleArgs or its bytes)
+    lib.dws_delta_rule_workspace.argtypes = [vp, ci, ctypes.POINTER(sz)]
     lib.dws_delta_rule_workspace.restype = ci
     for name in ("dws_delta_rule", "dws_delta_rule_backward", "dws_delta_rule_step"):
         f = getattr(lib, name)
-        f.argtypes = [ctypes.POINTER(DeltaRuleArgs), vp]
+        f.argtypes = [vp, vp]
         f.restype = ci
     pc, ll = ctypes.POINTER(PageCache), ctypes.c_longlong
     for name, args in (("workspace", [pc, ll, ctypes.POINTER(sz)]), ("grow", [pc, vp, vp, ll, vp, vp, sz, vp]),
@@ -586,107 +588,125 @@ def run_length_encode(keys, unique_keys=None, lengths=None, count=None, stream=N
 
 # ---- the gated delta rule ---------------------------------------------------
 
-def _float_code(t, what) -> int:
-    import torch
-    codes = {torch.float32: FLOAT32, torch.float16: FLOAT16, torch.bfloat16: BFLOAT16}
-    if t.dtype not in codes:
-        raise TypeError(f"{what} must be float32, float16 or bfloat16, got {t.dtype}")
-    return codes[t.dtype]
+# dws_delta_rule_args as a struct: packing one tuple takes a third of the time
+# of setting the members of a ctypes structure, and these calls are short. Where
+# each member starts in the list of values:
+_DELTA = struct.Struct("@qqPiiiiiiif" + 6 * "Pqq" + "PPPq" + "Pqq" + "P" + 5 * "Pqq" + "PiPQ")
+(_N_SEQS, _OFFSETS, _G_DTYPE, _Q, _K, _V, _G, _BETA, _OUT, _INITIAL, _FINAL, _SLOTS, _N_STATES, _OUT_GRAD, _FINAL_GRAD,
+ _Q_GRAD, _K_GRAD, _V_GRAD, _G_GRAD, _BETA_GRAD, _INITIAL_GRAD, _ZERO_TAIL, _WORKSPACE) = (
+    1, 2, 8, 11, 14, 17, 20, 23, 26, 29, 30, 31, 32, 33, 36, 37, 40, 43, 46, 49, 52, 53, 54)
+
+_float_codes = {}
 
 
-def _rows(t, what, tokens, heads, dim, like=None, device=None) -> Rows:
-    """The dws_rows of t, (tokens, heads, dim) or, for dim 0, (tokens, heads)."""
+def _float_code(dtype, what) -> int:
+    if not _float_codes:
+        import torch
+        _float_codes.update({torch.float32: FLOAT32, torch.float16: FLOAT16, torch.bfloat16: BFLOAT16})
+    code = _float_codes.get(dtype)
+    if code is None:
+        raise TypeError(f"{what} must be float32, float16 or bfloat16, got {dtype}")
+    return code
+
+
+def _gpu_tensor(t, what):
     import torch
-    shape = (tokens, heads, dim) if dim else (tokens, heads)
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{what} must be a GPU tensor (there is no CPU path)")
-    if tuple(t.shape) != shape or t.device != device or (like is not None and t.dtype != like):
-        raise ValueError(f"{what} must have shape {shape}" + (f", dtype {like}" if like is not None else "") +
+
+
+def _rows(t, what, shape, dtype, device):
+    """dws_rows of t: (tokens, heads, dim), or (tokens, heads) with dtype None."""
+    _gpu_tensor(t, what)
+    if t.shape != shape or t.device != device or (dtype is not None and t.dtype != dtype):
+        raise ValueError(f"{what} must have shape {tuple(shape)}" + (f", dtype {dtype}" if dtype is not None else "") +
                          f" and be on {device}, got {tuple(t.shape)}, {t.dtype} on {t.device}")
-    if dim > 1 and t.stride(2) != 1 and t.numel():
+    strides = t.stride()
+    if len(strides) == 3 and strides[2] != 1 and shape[2] > 1 and t.numel():
         raise ValueError(f"{what} must be contiguous in its last dimension")
-    return Rows(t.data_ptr(), t.stride(0), t.stride(1))
+    return t.data_ptr(), strides[0], strides[1]
 
 
 def _device_ints(t, what, dtype, n, device):
     import torch
     if not isinstance(t, torch.Tensor) or t.dtype != dtype or t.device != device or not t.is_contiguous() or \
-            (n is not None and t.numel() != n) or t.dim() != 1:
+            t.dim() != 1 or (n is not None and t.shape[0] != n):
         raise ValueError(f"{what} must be a contiguous one-dimensional {dtype} tensor on {device}" +
                          (f" of {n} elements" if n is not None else ""))
     return t.data_ptr()
 
 
-def _state_ptr(t, what, count, heads, dim_k, dim_v, device):
+def _state_ptr(t, what, count, shape, device):
     import torch
     if not isinstance(t, torch.Tensor) or t.dtype != torch.float32 or t.device != device or not t.is_contiguous() or \
-            t.dim() != 4 or tuple(t.shape[1:]) != (heads, dim_k, dim_v) or (count is not None and t.shape[0] != count):
-        raise ValueError(f"{what} must be a contiguous float32 tensor ({'count' if count is None else count}, {heads}, "
-                         f"{dim_k}, {dim_v}) on {device}")
+            t.dim() != 4 or t.shape[1:] != shape or (count is not None and t.shape[0] != count):
+        raise ValueError(f"{what} must be a contiguous float32 tensor {('count' if count is None else count, *shape)} on {device}")
     return t.data_ptr()
 
 
 def _delta_args(q, k, v, g, beta, offsets, n_seqs, scale):
-    """The members that all three delta-rule calls share; checks shapes, types and devices."""
+    """The values that all three delta-rule calls share; checks shapes, types and devices. Returns (values, device)."""
     import torch
-    for x, what in ((q, "q"), (k, "k"), (v, "v"), (beta, "beta")):
-        if not isinstance(x, torch.Tensor) or not x.is_cuda:
-            raise TypeError(f"{what} must be a GPU tensor (there is no CPU path)")
+    _gpu_tensor(q, "q")
+    _gpu_tensor(v, "v")
     if q.dim() != 3 or v.dim() != 3:
         raise ValueError("q, k and v must be (tokens, heads, dim)")
-    a = DeltaRuleArgs()
-    a.tokens, a.heads_qk, a.dim_k = q.shape
-    a.heads_v, a.dim_v = v.shape[1:]
-    a.dtype = _float_code(q, "q")
-    a.q = _rows(q, "q", a.tokens, a.heads_qk, a.dim_k, q.dtype, q.device)
-    a.k = _rows(k, "k", a.tokens, a.heads_qk, a.dim_k, q.dtype, q.device)
-    a.v = _rows(v, "v", a.tokens, a.heads_v, a.dim_v, q.dtype, q.device)
-    if g is not None:
-        a.g = _rows(g, "g", a.tokens, a.heads_v, 0, None, q.device)
-        a.g_dtype = _float_code(g, "g")
-    a.beta = _rows(beta, "beta", a.tokens, a.heads_v, 0, None, q.device)
-    a.beta_dtype = _float_code(beta, "beta")
+    device, dtype = q.device, q.dtype
+    tokens, heads_qk, dim_k = shape = q.shape
+    heads_v, dim_v = v.shape[1:]
+    code = _float_code(dtype, "q")
+    gates = (tokens, heads_v)
+    a = [0] * 56
     if offsets is not None:
-        a.d_offsets = _device_ints(offsets, "offsets", torch.int64, None, q.device)
-        n_seqs = offsets.numel() - 1
-    a.n_seqs = n_seqs
-    a.scale = a.dim_k ** -0.5 if scale is None else float(scale)
-    return a
+        a[_OFFSETS] = _device_ints(offsets, "offsets", torch.int64, None, device)
+        n_seqs = offsets.shape[0] - 1
+    if g is not None:
+        a[_G: _G + 3] = _rows(g, "g", gates, None, device)
+        a[_G_DTYPE] = _float_code(g.dtype, "g")
+    a[_BETA: _BETA + 3] = _rows(beta, "beta", gates, None, device)
+    a[:2] = tokens, n_seqs
+    a[3:8] = heads_qk, heads_v, dim_k, dim_v, code
+    a[9:11] = _float_code(beta.dtype, "beta"), dim_k ** -0.5 if scale is None else float(scale)
+    a[_Q: _Q + 9] = (*_rows(q, "q", shape, dtype, device), *_rows(k, "k", shape, dtype, device),
+                     *_rows(v, "v", (tokens, heads_v, dim_v), dtype, device))
+    return a, device
 
 
 class _on_stream:
-    """Allocate on the stream that the call runs on: memory that is freed when
-    the binding returns is then reused in that stream's order only."""
+    """Make x's device current, and allocate on the stream that the call runs on: memory that is freed when the binding
+    returns is then reused in that stream's order only. Gives the stream's handle."""
+    __slots__ = ("x", "given", "contexts")
 
     def __init__(self, x, stream):
-        import torch
-        self.device = torch.cuda.device(x.device)
-        current = torch.cuda.current_stream(x.device)
-        self.stream = int(current.cuda_stream) if stream is None else int(stream)
-        other = None
-        if self.stream != int(current.cuda_stream):
-            other = torch.cuda.default_stream(x.device) if self.stream == 0 else \
-                torch.cuda.ExternalStream(self.stream, device=x.device)
-        self.other = torch.cuda.stream(other)
+        self.x, self.given, self.contexts = x, stream, ()
 
     def __enter__(self):
-        self.device.__enter__()
-        self.other.__enter__()
-        return self.stream
+        import torch
+        device = self.x.device
+        if self.given is None and device.index == torch.cuda.current_device():
+            return torch.cuda.current_stream().cuda_stream
+        current = int(torch.cuda.current_stream(device).cuda_stream)
+        handle = current if self.given is None else int(self.given)
+        self.contexts = (torch.cuda.device(device),)
+        if handle != current:
+            self.contexts += (torch.cuda.stream(torch.cuda.default_stream(device) if handle == 0 else
+                                                torch.cuda.ExternalStream(handle, device=device)),)
+        for c in self.contexts:
+            c.__enter__()
+        return handle
 
     def __exit__(self, *exc):
-        self.other.__exit__(*exc)
-        self.device.__exit__(*exc)
+        for c in reversed(self.contexts):
+            c.__exit__(*exc)
         return False
 
 
 def _delta_workspace(a, backward, device):
     import torch
     need = ctypes.c_size_t(0)
-    _check(load_library().dws_delta_rule_workspace(ctypes.byref(a), int(backward), ctypes.byref(need)),
-           "dws_delta_rule_workspace")
+    _check(load_library().dws_delta_rule_workspace(_DELTA.pack(*a), backward, ctypes.byref(need)), "dws_delta_rule_workspace")
     work = torch.empty(need.value, dtype=torch.uint8, device=device)
-    a.d_workspace, a.workspace_bytes = work.data_ptr(), need.value
+    a[_WORKSPACE:] = work.data_ptr(), need.value
     return work
 
 
@@ -703,31 +723,29 @@ def delta_rule(q, k, v, g, beta, offsets=None, initial_state=None, final_state=N
     default. Rows of ``out`` behind the last sequence stay as they were, and are 0 in a new one.
     Returns out, or (out, final_state) when the final state is asked for."""
     import torch
-    a = _delta_args(q, k, v, g, beta, offsets, 1, scale)
-    count = a.n_seqs
+    a, device = _delta_args(q, k, v, g, beta, offsets, 1, scale)
+    n_seqs, state_shape = a[_N_SEQS], (v.shape[1], q.shape[2], v.shape[2])
+    count = n_seqs
     if slots is not None:
-        a.d_slots = _device_ints(slots, "slots", torch.int32, a.n_seqs, q.device)
+        a[_SLOTS] = _device_ints(slots, "slots", torch.int32, n_seqs, device)
         count = None
         if final_state is True or (initial_state is None and final_state is None):
             raise ValueError("slots name places of a given state tensor")
     with _on_stream(q, stream) as s:
         if out is None:
             # a sequence that is left out keeps its rows: 0 in a new tensor
-            out = torch.empty(v.shape, dtype=q.dtype, device=q.device) if slots is None else \
-                torch.zeros(v.shape, dtype=q.dtype, device=q.device)
-            a.zero_tail = int(offsets is not None)
-        a.out = _rows(out, "out", a.tokens, a.heads_v, a.dim_v, q.dtype, q.device)
+            out = (torch.empty if slots is None else torch.zeros)(v.shape, dtype=q.dtype, device=device)
+            a[_ZERO_TAIL] = int(offsets is not None)
+        a[_OUT: _OUT + 3] = _rows(out, "out", v.shape, q.dtype, device)
         if final_state is True:
-            final_state = torch.empty((a.n_seqs, a.heads_v, a.dim_k, a.dim_v), dtype=torch.float32, device=q.device)
-        for t, what in ((initial_state, "initial_state"), (final_state, "final_state")):
+            final_state = torch.empty((n_seqs, *state_shape), dtype=torch.float32, device=device)
+        for t, what, at in ((initial_state, "initial_state", _INITIAL), (final_state, "final_state", _FINAL)):
             if t is not None:
-                setattr(a, "d_" + what, _state_ptr(t, what, count, a.heads_v, a.dim_k, a.dim_v, q.device))
+                a[at] = _state_ptr(t, what, count, state_shape, device)
                 if slots is not None:
-                    if count is not None and t.shape[0] != count:
-                        raise ValueError("initial_state and final_state must have the same number of states")
-                    count = a.n_states = t.shape[0]
-        work = _delta_workspace(a, False, q.device)
-        _check(load_library().dws_delta_rule(ctypes.byref(a), s), "dws_delta_rule")
+                    count = a[_N_STATES] = t.shape[0]
+        work = _delta_workspace(a, 0, device)
+        _check(load_library().dws_delta_rule(_DELTA.pack(*a), s), "dws_delta_rule")
         del work
     return out if final_state is None else (out, final_state)
 
@@ -738,30 +756,27 @@ def delta_rule_backward(d_out, q, k, v, g, beta, offsets=None, initial_state=Non
     result(s). Returns (dq, dk, dv, dg, dbeta, d_initial_state) in the type of q, dg None without g and
     d_initial_state None without initial_state; rows behind the last sequence are 0."""
     import torch
-    a = _delta_args(q, k, v, g, beta, offsets, 1, scale)
-    a.out_grad = _rows(d_out, "d_out", a.tokens, a.heads_v, a.dim_v, q.dtype, q.device)
-    for t, what, name in ((initial_state, "initial_state", "d_initial_state"), (d_final_state, "d_final_state", "d_final_grad")):
+    a, device = _delta_args(q, k, v, g, beta, offsets, 1, scale)
+    a[_OUT_GRAD: _OUT_GRAD + 3] = _rows(d_out, "d_out", v.shape, q.dtype, device)
+    n_seqs, state_shape = a[_N_SEQS], (v.shape[1], q.shape[2], v.shape[2])
+    for t, what, at in ((initial_state, "initial_state", _INITIAL), (d_final_state, "d_final_state", _FINAL_GRAD)):
         if t is not None:
-            setattr(a, name, _state_ptr(t, what, a.n_seqs, a.heads_v, a.dim_k, a.dim_v, q.device))
+            a[at] = _state_ptr(t, what, n_seqs, state_shape, device)
     with _on_stream(q, stream) as s:
-        def new(*shape):
-            return torch.empty(shape, dtype=q.dtype, device=q.device)
-
-        dq, dk, dv = new(*q.shape), new(*k.shape), new(*v.shape)
-        dg = new(*g.shape) if g is not None else None
-        dbeta = new(*beta.shape)
-        d_initial = new(*initial_state.shape) if initial_state is not None else None
-        a.q_grad, a.k_grad, a.v_grad = (Rows(t.data_ptr(), t.stride(0), t.stride(1)) for t in (dq, dk, dv))
-        if dg is not None:
-            a.g_grad = Rows(dg.data_ptr(), dg.stride(0), dg.stride(1))
-        a.beta_grad = Rows(dbeta.data_ptr(), dbeta.stride(0), dbeta.stride(1))
+        grads = []
+        for like, at in ((q, _Q_GRAD), (k, _K_GRAD), (v, _V_GRAD), (g, _G_GRAD), (beta, _BETA_GRAD)):
+            t = None if like is None else torch.empty(like.shape, dtype=q.dtype, device=device)
+            if t is not None:
+                a[at: at + 3] = t.data_ptr(), t.stride(0), t.stride(1)
+            grads.append(t)
+        d_initial = None if initial_state is None else torch.empty(initial_state.shape, dtype=q.dtype, device=device)
         if d_initial is not None:
-            a.d_initial_grad = d_initial.data_ptr()
-        a.zero_tail = int(offsets is not None)
-        work = _delta_workspace(a, True, q.device)
-        _check(load_library().dws_delta_rule_backward(ctypes.byref(a), s), "dws_delta_rule_backward")
+            a[_INITIAL_GRAD] = d_initial.data_ptr()
+        a[_ZERO_TAIL] = int(offsets is not None)
+        work = _delta_workspace(a, 1, device)
+        _check(load_library().dws_delta_rule_backward(_DELTA.pack(*a), s), "dws_delta_rule_backward")
         del work
-    return dq, dk, dv, dg, dbeta, d_initial
+    return (*grads, d_initial)
 
 
 def delta_rule_step(q, k, v, g, beta, state, slots=None, offsets=None, scale=None, out=None, stream=None):
@@ -775,18 +790,18 @@ def delta_rule_step(q, k, v, g, beta, state, slots=None, offsets=None, scale=Non
     if not isinstance(state, torch.Tensor) or state.dim() != 4:
         raise ValueError("state must be a (count, heads_v, dim_k, dim_v) tensor")
     n = slots.numel() if isinstance(slots, torch.Tensor) else state.shape[0]
-    a = _delta_args(q, k, v, g, beta, offsets, n, scale)
-    if a.n_seqs != n or n < 1 or (offsets is None and a.tokens % n):
-        raise ValueError(f"{n} sequences do not fit {a.tokens} tokens or {a.n_seqs + 1} offsets")
-    a.d_final_state = a.d_initial_state = _state_ptr(state, "state", None, a.heads_v, a.dim_k, a.dim_v, q.device)
+    a, device = _delta_args(q, k, v, g, beta, offsets, n, scale)
+    if a[_N_SEQS] != n or n < 1 or (offsets is None and a[0] % n):
+        raise ValueError(f"{n} sequences do not fit {a[0]} tokens or {a[_N_SEQS] + 1} offsets")
+    a[_INITIAL] = a[_FINAL] = _state_ptr(state, "state", None, (v.shape[1], q.shape[2], v.shape[2]), device)
     if slots is not None:
-        a.d_slots = _device_ints(slots, "slots", torch.int32, n, q.device)
-        a.n_states = state.shape[0]
+        a[_SLOTS] = _device_ints(slots, "slots", torch.int32, n, device)
+        a[_N_STATES] = state.shape[0]
     with _on_stream(q, stream) as s:
         if out is None:
-            out = torch.zeros(v.shape, dtype=q.dtype, device=q.device)
-        a.out = _rows(out, "out", a.tokens, a.heads_v, a.dim_v, q.dtype, q.device)
-        _check(load_library().dws_delta_rule_step(ctypes.byref(a), s), "dws_delta_rule_step")
+            out = torch.zeros(v.shape, dtype=q.dtype, device=device)
+        a[_OUT: _OUT + 3] = _rows(out, "out", v.shape, q.dtype, device)
+        _check(load_library().dws_delta_rule_step(_DELTA.pack(*a), s), "dws_delta_rule_step")
     return out
 
 
@@ -794,8 +809,7 @@ def delta_rule_step(q, k, v, g, beta, state, slots=None, offsets=None, scale=Non
 
 def _page_cache(refs, table, lengths=None, page_tokens=0) -> PageCache:
     import torch
-    if not isinstance(refs, torch.Tensor) or not refs.is_cuda:
-        raise TypeError("refs must be a GPU tensor (there is no CPU path)")
+    _gpu_tensor(refs, "refs")
     c = PageCache(d_refs=_device_ints(refs, "refs", torch.int32, None, refs.device), n_pages=refs.numel(),
                   page_tokens=int(page_tokens))
     if not isinstance(table, torch.Tensor) or table.dtype != torch.int32 or table.dim() != 2 or \
@@ -843,7 +857,7 @@ def pages_fork(refs, table, lengths, parents, children, page_tokens, stream=None
     n = parents.numel() if isinstance(parents, torch.Tensor) else 0
     a, b = (_device_ints(t, w, torch.int32, n, refs.device) for t, w in ((parents, "parents"), (children, "children")))
     with _on_stream(refs, stream) as s:
-        granted, src, dst = (_new_ints(n, refs) for _ in range(3))
+        granted, src, dst = _new_ints((3, n), refs).unbind(0)
         count, work = _new_ints(1, refs, torch.int64), _page_workspace(c, n, refs.device)
         _check(load_library().dws_pages_fork(ctypes.byref(c), a, b, n, granted.data_ptr(), src.data_ptr(), dst.data_ptr(),
                                              count.data_ptr(), work.data_ptr(), work.numel(), s), "dws_pages_fork")
@@ -870,8 +884,10 @@ def pages_compact(refs, table, stream=None):
     import torch
     c = _page_cache(refs, table)
     with _on_stream(refs, stream) as s:
-        remap, src, dst = (_new_ints(n, refs) for n in (c.n_pages, c.n_pages // 2, c.n_pages // 2))
-        moves, count = (_new_ints(1, refs, torch.int64) for _ in range(2))
+        half = c.n_pages // 2
+        remap = _new_ints(c.n_pages, refs)
+        src, dst = _new_ints((2, half), refs).unbind(0)
+        moves, count = _new_ints(2, refs, torch.int64).split(1)
         work = _page_workspace(c, 0, refs.device)
         _check(load_library().dws_pages_compact(ctypes.byref(c), remap.data_ptr(), src.data_ptr(), dst.data_ptr(),
                                                 moves.data_ptr(), count.data_ptr(), work.data_ptr(), work.numel(), s),
@@ -884,8 +900,7 @@ def pages_copy(pool, src, dst, count=None, page_dim=0, stream=None):
     the pool (dws_pages_copy). pool: contiguous, of any type; page_dim 1: (layers, pages, ...). A written page must be
     in one pair only. Returns pool."""
     import torch
-    if not isinstance(pool, torch.Tensor) or not pool.is_cuda:
-        raise TypeError("pool must be a GPU tensor (there is no CPU path)")
+    _gpu_tensor(pool, "pool")
     if page_dim not in (0, 1) or pool.dim() <= page_dim or not pool.is_contiguous():
         raise ValueError("pool must be contiguous, its pages in dimension 0 or 1")
     n = src.numel() if isinstance(src, torch.Tensor) else 0

@@ -92,6 +92,54 @@ __global__ __launch_bounds__(kThreads) void k_pages_count(PageCache c, int* live
             claim[i] = INT32_MAX;
 }
 
+// What request i needs, if the row it names is its own: *length the tokens to
+// start from (-1: refused), and the pages.
+template <bool FORK>
+__device__ __forceinline__ long long pages_needed(const PageCache& c, const PageRequests& r, int64_t i, int row, int64_t* length)
+{
+    *length = -1;
+    if constexpr (FORK) {
+        const int parent = r.a[i];
+        if (parent < 0 || parent >= c.rows || c.lengths[row] != 0) return 0;
+        const int64_t n = c.lengths[parent];
+        if (n < 0 || n > c.max_pages * c.page_tokens) return 0;
+        *length = n;
+        return n % c.page_tokens != 0;
+    } else {
+        const int64_t old = c.lengths[row], now = r.b[i];
+        if (old < 0 || now < old || pages_of(now, c.page_tokens) > c.max_pages) return 0;
+        *length = old;
+        return pages_of(now, c.page_tokens) - pages_of(old, c.page_tokens);
+    }
+}
+// Entry k of the row of granted request i; `first`: its first new page in `fresh`.
+template <bool FORK>
+__device__ __forceinline__ void apply_entry(const PageCache& c, const PageRequests& r, int64_t i, int64_t k, int64_t length,
+                                            int rank, const int* fresh)
+{
+    if constexpr (FORK) {
+        const int* held = c.table + (int64_t)r.a[i] * c.max_pages;
+        const int64_t whole = length / c.page_tokens;
+        int page = -1;
+        if (k < whole) {
+            page = held[k];
+            if (page >= 0 && page < c.pages) atomicAdd(&c.refs[page], 1);
+        } else if (k == whole && rank >= 0) {
+            page = fresh[rank];
+            c.refs[page] = 1;
+            r.src[rank] = held[k];
+            r.dst[rank] = page;
+        }
+        c.table[(int64_t)r.b[i] * c.max_pages + k] = page;
+    } else {
+        const int64_t first = pages_of(length, c.page_tokens);
+        if (k < first || k >= pages_of(r.b[i], c.page_tokens)) return;
+        const int page = fresh[rank + (k - first)];
+        c.table[(int64_t)r.a[i] * c.max_pages + k] = page;
+        c.refs[page] = 1;
+    }
+}
+
 // Workgroup 0: which requests are granted, in order. The others: the free pages
 // of their tile, by rank, as far as `most` can be asked for.
 template <bool FORK>
@@ -139,20 +187,7 @@ __global__ __launch_bounds__(kPlanThreads) void k_pages_plan(PageCache c, PageRe
             const int row = FORK ? r.b[i] : r.a[i];
             if (row >= 0 && row < c.rows &&
                 __hip_atomic_load(&r.claim[row], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == (int)i) {
-                if constexpr (FORK) {
-                    const int parent = r.a[i];
-                    if (parent >= 0 && parent < c.rows && c.lengths[row] == 0) {
-                        length = c.lengths[parent];
-                        if (length > c.max_pages * c.page_tokens) length = -1;
-                        need = length > 0 && length % c.page_tokens != 0;
-                    }
-                } else {
-                    const int64_t old = c.lengths[row], now = r.b[i];
-                    if (old >= 0 && now >= old && pages_of(now, c.page_tokens) <= c.max_pages) {
-                        length = old;
-                        need = pages_of(now, c.page_tokens) - pages_of(old, c.page_tokens);
-                    }
-                }
+                need = pages_needed<FORK>(c, r, i, row, &length);
             }
         }
         const int64_t first = taken + block_exclusive<kPlanThreads>(need, wide, tid, &all);
@@ -172,46 +207,71 @@ __global__ __launch_bounds__(kPlanThreads) void k_pages_plan(PageCache c, PageRe
 constexpr int64_t kSplit = 2048;      // table entries of a row that one workgroup handles
 
 // Workgroup (i, split): entries split * kSplit .. of request i's row.
-__global__ __launch_bounds__(kThreads) void k_pages_grow(PageCache c, PageRequests r, uint32_t splits)
+template <bool FORK>
+__global__ __launch_bounds__(kThreads) void k_pages_apply(PageCache c, PageRequests r, uint32_t splits)
 {
     const int64_t i = blockIdx.x / splits, from = (int64_t)(blockIdx.x % splits) * kSplit;
-    const int64_t old = r.length[i];
-    if (old < 0) return;
-    const int64_t row = r.a[i], now = r.b[i];
-    const int64_t first = pages_of(old, c.page_tokens), last = pages_of(now, c.page_tokens);
-    const int64_t end = last < from + kSplit ? last : from + kSplit;
-    for (int64_t k = (from > first ? from : first) + threadIdx.x; k < end; k += kThreads) {
-        const int page = r.fresh[r.rank[i] + (k - first)];
-        c.table[row * c.max_pages + k] = page;
-        c.refs[page] = 1;
-    }
-    if (from == 0 && threadIdx.x == 0) c.lengths[row] = (int)now;
-}
-
-__global__ __launch_bounds__(kThreads) void k_pages_fork(PageCache c, PageRequests r, uint32_t splits)
-{
-    const int64_t i = blockIdx.x / splits, from = (int64_t)(blockIdx.x % splits) * kSplit;
-    if (from == 0 && threadIdx.x == 0 && i >= *r.count) r.src[i] = r.dst[i] = -1;
+    const bool one = from == 0 && threadIdx.x == 0;
+    if constexpr (FORK)
+        if (one && i >= *r.count) r.src[i] = r.dst[i] = -1;
     const int64_t length = r.length[i];
     if (length < 0) return;
-    const int* held = c.table + (int64_t)r.a[i] * c.max_pages;
-    int* row = c.table + (int64_t)r.b[i] * c.max_pages;
-    const int64_t whole = length / c.page_tokens;
     const int64_t end = c.max_pages < from + kSplit ? c.max_pages : from + kSplit;
-    for (int64_t k = from + threadIdx.x; k < end; k += kThreads) {
-        int page = -1;
-        if (k < whole) {
-            page = held[k];
-            if (page >= 0 && page < c.pages) atomicAdd(&c.refs[page], 1);
-        } else if (k == whole && r.rank[i] >= 0) {
-            page = r.fresh[r.rank[i]];
-            c.refs[page] = 1;
-            r.src[r.rank[i]] = held[k];
-            r.dst[r.rank[i]] = page;
-        }
-        row[k] = page;
+    const int rank = r.rank[i];
+    for (int64_t k = from + threadIdx.x; k < end; k += kThreads) apply_entry<FORK>(c, r, i, k, length, rank, r.fresh);
+    if (one) c.lengths[FORK ? r.b[i] : r.a[i]] = FORK ? (int)length : r.b[i];
+}
+
+// All three steps in one workgroup, with LDS in the place of the workspace: a
+// small cache's pass over the counts takes less than two more launches (a fork
+// of 4 rows over 509 pages: 57 us with three launches, %SMALL% us with one).
+constexpr int kSmallPages = 8192, kSmallRows = 4096;
+constexpr int64_t kSmallEntries = 65536;      // table entries
+template <bool FORK>
+__global__ __launch_bounds__(kPlanThreads) void k_pages_small(PageCache c, PageRequests r)
+{
+    __shared__ int part[kPlanThreads / 64];
+    __shared__ long long wide[kPlanThreads / 64];
+    __shared__ int claim[kSmallRows], fresh[kSmallPages], lengths[kPlanThreads], ranks[kPlanThreads];
+    const int tid = threadIdx.x, n = (int)r.n;
+    const int row = tid < n ? (FORK ? r.b[tid] : r.a[tid]) : -1;
+    const bool named = row >= 0 && row < c.rows;
+    if (named) claim[row] = INT32_MAX;
+    int free[kSmallPages / kPlanThreads], mine = 0, n_free;
+#pragma unroll
+    for (int i = 0; i < kSmallPages / kPlanThreads; ++i) {
+        const int64_t p = tid * (kSmallPages / kPlanThreads) + i;
+        free[i] = p < c.pages && c.refs[p] <= 0;
+        mine += free[i];
     }
-    if (from == 0 && threadIdx.x == 0) c.lengths[r.b[i]] = (int)length;
+    int at = block_exclusive<kPlanThreads>(mine, part, tid, &n_free);
+#pragma unroll
+    for (int i = 0; i < kSmallPages / kPlanThreads; ++i)
+        if (free[i]) fresh[at++] = tid * (kSmallPages / kPlanThreads) + i;
+    if (named) atomicMin(&claim[row], tid);
+    __syncthreads();
+    long long need = 0, all;
+    int64_t length = -1;
+    if (named && claim[row] == tid) need = pages_needed<FORK>(c, r, tid, row, &length);
+    const long long first = block_exclusive<kPlanThreads>(need, wide, tid, &all);
+    const bool ok = length >= 0 && (need == 0 || first + need <= n_free);
+    const int given = block_sum<kPlanThreads>(ok && need > 0, part, tid);
+    lengths[tid] = ok ? (int)length : -1;
+    ranks[tid] = ok && need > 0 ? (int)first : -1;
+    if (tid < n) {
+        r.granted[tid] = ok;
+        if constexpr (FORK)
+            if (tid >= given) r.src[tid] = r.dst[tid] = -1;
+    }
+    if constexpr (FORK)
+        if (tid == 0) *r.count = given;
+    __syncthreads();
+    const int most = (int)c.max_pages;
+    for (int e = tid; e < n * most; e += kPlanThreads) {
+        const int i = e / most;
+        if (lengths[i] >= 0) apply_entry<FORK>(c, r, i, e - i * most, lengths[i], ranks[i], fresh);
+    }
+    if (ok) c.lengths[row] = FORK ? (int)length : r.b[tid];
 }
 
 // Takes the rows' lengths: of requests for the same row one gets it, the others 0.
@@ -243,6 +303,30 @@ __global__ __launch_bounds__(kThreads) void k_pages_free(PageCache c, PageFree f
     }
     n = block_sum<kThreads>(n, part, threadIdx.x);
     if (threadIdx.x == 0 && n > 0) atomicAdd(reinterpret_cast<unsigned long long*>(f.freed), (unsigned long long)n);
+}
+
+// Both steps in one workgroup, for few entries.
+constexpr int64_t kSmallFree = 16384;
+__global__ __launch_bounds__(kPlanThreads) void k_pages_free_small(PageCache c, PageFree f)
+{
+    __shared__ int part[kPlanThreads / 64], lengths[kPlanThreads];
+    const int tid = threadIdx.x, n = (int)f.n, most = (int)c.max_pages;
+    if (tid < n) {
+        const int row = f.row[tid];
+        lengths[tid] = row >= 0 && row < c.rows ? atomicExch(&c.lengths[row], 0) : 0;
+    }
+    __syncthreads();
+    int freed = 0;
+    for (int e = tid; e < n * most; e += kPlanThreads) {
+        const int i = e / most, k = e - i * most;
+        if (lengths[i] <= 0 || k >= pages_of(lengths[i], c.page_tokens)) continue;
+        int* entry = c.table + (int64_t)f.row[i] * c.max_pages + k;
+        const int page = *entry;
+        if (page >= 0 && page < c.pages) freed += atomicSub(&c.refs[page], 1) == 1;
+        *entry = -1;
+    }
+    freed = block_sum<kPlanThreads>(freed, part, tid);
+    if (tid == 0) *f.freed = freed;
 }
 
 // With `live` pages in use: the k-th free page before place `live` (a hole) takes
@@ -317,6 +401,64 @@ __global__ __launch_bounds__(kThreads) void k_pages_renumber(PageCache c, PageCo
     }
 }
 
+// All of it in one workgroup, with the remap in LDS.
+__global__ __launch_bounds__(kPlanThreads) void k_pages_compact_small(PageCache c, PageCompact k)
+{
+    __shared__ int part[kPlanThreads / 64], remap[kSmallPages], hole[kSmallPages / 2], front;
+    const int tid = threadIdx.x, pages = (int)c.pages;
+    constexpr int EACH = kSmallPages / kPlanThreads;
+    int used[EACH], refs[EACH], n = 0, live;
+#pragma unroll
+    for (int i = 0; i < EACH; ++i) {
+        const int p = tid * EACH + i;
+        refs[i] = p < pages ? c.refs[p] : 0;
+        used[i] = refs[i] > 0;
+        n += used[i];
+    }
+    const int before = block_exclusive<kPlanThreads>(n, part, tid, &live);
+    int rank = before;
+    if (tid == 0) front = live;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < EACH; ++i) {
+        const int p = tid * EACH + i;
+        if (p == live) front = rank;           // pages in use among the first `live` places
+        if (p < live && p < pages && !used[i]) hole[p - rank] = p;
+        rank += used[i];
+    }
+    __syncthreads();
+    const int moves = live - front;
+    rank = before;
+#pragma unroll
+    for (int i = 0; i < EACH; ++i) {
+        const int p = tid * EACH + i;
+        if (p < pages) {
+            int to = used[i] ? p : -1;
+            if (used[i] && p >= live) {
+                const int t = rank - front;
+                to = hole[t];
+                k.src[t] = p;
+                k.dst[t] = to;
+                c.refs[to] = refs[i];
+                c.refs[p] = 0;
+            }
+            remap[p] = to;
+            k.remap[p] = to;
+        }
+        rank += used[i];
+    }
+    for (int t = moves + tid; t < (int)k.list; t += kPlanThreads) k.src[t] = k.dst[t] = -1;
+    if (tid == 0) {
+        *k.count = live;
+        *k.moves = moves;
+    }
+    __syncthreads();
+    for (int64_t e = tid; e < c.rows * c.max_pages; e += kPlanThreads) {
+        const int page = c.table[e];
+        if (page >= 0 && page < pages && remap[page] >= 0 && remap[page] != page) c.table[e] = remap[page];
+    }
+}
+
 // One workgroup copies kSlice bytes of one page in one layer at a time.
 constexpr int64_t kSlice = 16384;
 
@@ -355,15 +497,16 @@ uint32_t clamp_grid(int64_t blocks, int64_t most) { return (uint32_t)(blocks < 1
 template <bool FORK>
 hipError_t launch_requests(const PageCache& c, const PageRequests& r, hipStream_t stream)
 {
+    if (c.pages <= kSmallPages && c.rows <= kSmallRows && r.n <= kPlanThreads && r.n * c.max_pages <= kSmallEntries) {
+        k_pages_small<FORK><<<dim3(1), dim3(kPlanThreads), 0, stream>>>(c, r);
+        return hipGetLastError();
+    }
     const int64_t tiles = tiles_of(c.pages);
     const uint32_t splits = splits_of(c);
     k_pages_count<<<dim3((uint32_t)tiles), dim3(kThreads), 0, stream>>>(c, r.live, r.claim);
     k_pages_plan<FORK><<<dim3((uint32_t)tiles + 1), dim3(kPlanThreads), 0, stream>>>(c, r);
     if (r.n == 0) return hipGetLastError();
-    if constexpr (FORK)
-        k_pages_fork<<<dim3((uint32_t)r.n * splits), dim3(kThreads), 0, stream>>>(c, r, splits);
-    else
-        k_pages_grow<<<dim3((uint32_t)r.n * splits), dim3(kThreads), 0, stream>>>(c, r, splits);
+    k_pages_apply<FORK><<<dim3((uint32_t)r.n * splits), dim3(kThreads), 0, stream>>>(c, r, splits);
     return hipGetLastError();
 }
 
@@ -381,6 +524,10 @@ hipError_t launch_pages_fork(const PageCache& c, const PageRequests& r, hipStrea
 
 hipError_t launch_pages_free(const PageCache& c, const PageFree& f, hipStream_t stream)
 {
+    if (f.n <= kPlanThreads && f.n * c.max_pages <= kSmallFree) {
+        k_pages_free_small<<<dim3(1), dim3(kPlanThreads), 0, stream>>>(c, f);
+        return hipGetLastError();
+    }
     const uint32_t splits = splits_of(c);
     k_pages_take<<<dim3((uint32_t)(f.n / kThreads + 1)), dim3(kThreads), 0, stream>>>(c, f);
     if (f.n == 0) return hipGetLastError();
@@ -390,6 +537,10 @@ hipError_t launch_pages_free(const PageCache& c, const PageFree& f, hipStream_t 
 
 hipError_t launch_pages_compact(const PageCache& c, const PageCompact& k, hipStream_t stream)
 {
+    if (c.pages <= kSmallPages && c.rows * c.max_pages <= kSmallEntries) {
+        k_pages_compact_small<<<dim3(1), dim3(kPlanThreads), 0, stream>>>(c, k);
+        return hipGetLastError();
+    }
     const int64_t tiles = tiles_of(c.pages);
     k_pages_count<<<dim3((uint32_t)tiles), dim3(kThreads), 0, stream>>>(c, k.live, nullptr);
     k_pages_rank<<<dim3((uint32_t)tiles), dim3(kPlanThreads), 0, stream>>>(c, k);

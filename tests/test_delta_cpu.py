@@ -131,6 +131,28 @@ def test_workspace_grows_with_the_call(lib):
     assert need(tokens=1 << 20) > 1000 * need()
 
 
+def test_packed_arguments_are_the_structure():
+    """The binding packs dws_delta_rule_args: every member of the structure where the packed value goes."""
+    assert dws._DELTA.size == ctypes.sizeof(dws.DeltaRuleArgs)
+    a = [0] * 56
+    places = {"n_seqs": dws._N_SEQS, "d_offsets": dws._OFFSETS, "g_dtype": dws._G_DTYPE, "d_initial_state": dws._INITIAL,
+              "d_final_state": dws._FINAL, "d_slots": dws._SLOTS, "n_states": dws._N_STATES, "d_final_grad": dws._FINAL_GRAD,
+              "d_initial_grad": dws._INITIAL_GRAD, "zero_tail": dws._ZERO_TAIL, "d_workspace": dws._WORKSPACE,
+              "workspace_bytes": dws._WORKSPACE + 1, "tokens": 0, "heads_qk": 3, "heads_v": 4, "dim_k": 5, "dim_v": 6,
+              "dtype": 7, "beta_dtype": 9, "scale": 10}
+    rows = {"q": dws._Q, "k": dws._K, "v": dws._V, "g": dws._G, "beta": dws._BETA, "out": dws._OUT, "out_grad": dws._OUT_GRAD,
+            "q_grad": dws._Q_GRAD, "k_grad": dws._K_GRAD, "v_grad": dws._V_GRAD, "g_grad": dws._G_GRAD, "beta_grad": dws._BETA_GRAD}
+    for i in range(56):
+        a[i] = i + 1
+    s = dws.DeltaRuleArgs.from_buffer_copy(dws._DELTA.pack(*a))
+    assert len(places) + 3 * len(rows) == 56
+    for name, at in places.items():
+        assert getattr(s, name) == at + 1, name
+    for name, at in rows.items():
+        r = getattr(s, name)
+        assert (r.data, r.token_stride, r.head_stride) == (at + 1, at + 2, at + 3), name
+
+
 def test_binding_refuses_cpu_tensors():
     x, offsets, initial = inputs(1, [8], 1, 1, 16, 16, torch.float32, device="cpu")
     args = [x[a] for a in NAMES]
