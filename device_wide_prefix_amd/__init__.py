@@ -684,7 +684,9 @@ class _on_stream:
         import torch
         device = self.x.device
         if self.given is None and device.index == torch.cuda.current_device():
-            return torch.cuda.current_stream().cuda_stream
+            # the handle alone: current_stream() would make a Stream object, as much time as a launch takes
+            raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+            return raw(device.index) if raw is not None else torch.cuda.current_stream().cuda_stream
         current = int(torch.cuda.current_stream(device).cuda_stream)
         handle = current if self.given is None else int(self.given)
         self.contexts = (torch.cuda.device(device),)
@@ -887,7 +889,7 @@ def pages_compact(refs, table, stream=None):
         half = c.n_pages // 2
         remap = _new_ints(c.n_pages, refs)
         src, dst = _new_ints((2, half), refs).unbind(0)
-        moves, count = _new_ints(2, refs, torch.int64).split(1)
+        moves, count = _new_ints(1, refs, torch.int64), _new_ints(1, refs, torch.int64)
         work = _page_workspace(c, 0, refs.device)
         _check(load_library().dws_pages_compact(ctypes.byref(c), remap.data_ptr(), src.data_ptr(), dst.data_ptr(),
                                                 moves.data_ptr(), count.data_ptr(), work.data_ptr(), work.numel(), s),
@@ -907,7 +909,7 @@ def pages_copy(pool, src, dst, count=None, page_dim=0, stream=None):
     a, b = (_device_ints(t, w, torch.int32, n, pool.device) for t, w in ((src, "src"), (dst, "dst")))
     k = None if count is None else _device_ints(count, "count", torch.int64, 1, pool.device)
     layers, pages = (1 if page_dim == 0 else pool.shape[0]), pool.shape[page_dim]
-    layer_bytes = pool[0].numel() * pool.element_size() if page_dim and layers else pool.numel() * pool.element_size()
+    layer_bytes = pool.numel() * pool.element_size() // max(1, layers)
     with _on_stream(pool, stream) as s:
         _check(load_library().dws_pages_copy(pool.data_ptr(), pages, layer_bytes // pages if pages else 0, layers,
                                              layer_bytes, a, b, n, k, s), "dws_pages_copy")

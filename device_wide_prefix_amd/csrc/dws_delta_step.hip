@@ -153,9 +153,19 @@ hipError_t launch(const DeltaStepParams& p, hipStream_t stream)
 
 }  // namespace
 
+// A workgroup takes as many of a head's columns as it has, 128 at most: whole
+// rows of 512 bytes, and one sum over the rows for all of them (128 sequences of
+// 32 heads of 128 x 128: 91 us, 5.82 TB/s, against 109 us with 32 columns; four
+// tokens for 64 of them 68 against 109; 16 sequences 14.1 against 17.6; 64 x 64
+// heads with their 64 columns 17.5 against 25.2 with 32 and 40.5 with 128). With
+// fewer heads than compute units it takes 32, which spreads them over more (one
+// sequence of 32 heads 6.1 us against 8.6).
 hipError_t launch_delta_step(const DeltaStepParams& p, bool vec4, hipStream_t stream)
 {
-    return vec4 ? launch<4, 8>(p, stream) : launch<1, 32>(p, stream);
+    constexpr int64_t kComputeUnits = 256;
+    if (!vec4) return launch<1, 32>(p, stream);
+    if (p.dim_v <= 32 || p.n_seqs * p.heads_v < kComputeUnits) return launch<4, 8>(p, stream);
+    return p.dim_v <= 64 ? launch<4, 16>(p, stream) : launch<4, 32>(p, stream);
 }
 
 }  // namespace dws

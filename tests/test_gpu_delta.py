@@ -79,6 +79,38 @@ def test_backward(gpu, lens, hk, hv, dk, dv, init, dtype):
             close(a, b, dtype, what)
 
 
+# sequences and heads enough for workgroups of the widest kind on every compute unit
+MANY = [([0, 70, 33, 1, 64, 5] * 6, 8, 8, 64, 64), ([65, 2, 40, 129] * 9, 2, 8, 128, 70), ([33, 64, 31] * 9, 3, 12, 200, 40),
+        ([20, 90] * 17, 8, 8, 256, 17), ([30] * 65, 2, 4, 128, 128)]
+
+
+@pytest.mark.parametrize("dtype", [FP32, BF16, FP16])
+@pytest.mark.parametrize("lens,hk,hv,dk,dv", MANY)
+def test_many_sequences(gpu, lens, hk, hv, dk, dv, dtype):
+    note(f"delta many {len(lens)} {hk} {hv} {dk} {dv} {dtype}")
+    assert len(lens) * hv * -(-dv // 64) >= 256
+    x, offsets, initial = inputs(21, lens, hk, hv, dk, dv, dtype, tail=3)
+    ends = offsets.tolist()
+    some = sorted({0, 1, 2, 3, len(lens) // 2, len(lens) - 2, len(lens) - 1})
+    d_out = torch.randn(x["v"].shape, generator=torch.Generator().manual_seed(3)).to(dtype).cuda()
+    d_final = 0.3 * torch.randn(initial.shape, generator=torch.Generator().manual_seed(4)).cuda()
+    out, state = forward(x, offsets, initial, final_state=True)
+    plain = forward(x, offsets, initial)
+    got = dws.delta_rule_backward(d_out, *(x[a] for a in NAMES), offsets=offsets, initial_state=initial, d_final_state=d_final)
+    assert (out[ends[-1]:] == 0).all() and (got[0][ends[-1]:] == 0).all()
+    for i in some:
+        rows = slice(ends[i], ends[i + 1])
+        y = {a: x[a][rows] for a in NAMES}
+        at = torch.tensor([0, lens[i]])
+        want, final = reference(*(y[a] for a in NAMES), at.tolist(), initial[i: i + 1].double().cpu(), dk ** -0.5)
+        close(out[rows], want, dtype, "out")
+        close(plain[rows], want, dtype, "out")
+        close(state[i: i + 1], final, dtype, "state")
+        want = gradients(y, at, initial[i: i + 1], dk ** -0.5, d_out[rows], d_final[i: i + 1])
+        for what, a, b in zip(("dq", "dk", "dv", "dg", "dbeta", "d_initial"), got, want):
+            close(a[rows] if what != "d_initial" else a[i: i + 1], b, dtype, what, f"{i}")
+
+
 @pytest.mark.parametrize("gates", [(FP32, FP32), (BF16, BF16), (FP16, FP32), (FP32, FP16)])
 def test_gate_types(gpu, gates):
     x, offsets, initial = inputs(4, [70, 40], 1, 2, 64, 32, BF16, gates=gates)
@@ -269,7 +301,10 @@ def test_offsets_that_decrease_touch_nothing_outside(gpu):
         torch.cuda.synchronize()
 
 
-STEPS = [(1, 1, 1, 1, 1, 1), (3, 1, 2, 4, 64, 64), (5, 2, 1, 3, 128, 128), (2, 7, 1, 1, 256, 255), (4, 3, 2, 2, 40, 100)]
+# sequences, tokens of each, heads_qk, value heads a key head, dim_k, dim_v; the last ones have more heads than the
+# device has compute units
+STEPS = [(1, 1, 1, 1, 1, 1), (3, 1, 2, 4, 64, 64), (5, 2, 1, 3, 128, 128), (2, 7, 1, 1, 256, 255), (4, 3, 2, 2, 40, 100),
+         (130, 1, 1, 2, 64, 64), (43, 2, 2, 3, 72, 36), (150, 1, 2, 1, 128, 128), (70, 3, 4, 1, 256, 132), (300, 1, 1, 1, 24, 31)]
 
 
 @pytest.mark.parametrize("dtype", [FP32, BF16, FP16])
