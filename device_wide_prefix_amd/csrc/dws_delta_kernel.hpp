@@ -93,36 +93,49 @@ constexpr int inverse_stride(int c) { return c + 4; }
 
 // inv = (I + m)^-1, m strictly lower triangular, both fp32 in LDS with rows of
 // inverse_stride(C); of m only the entries below the diagonal are read, and the
-// inverse's upper right quarter is not written. The diagonal 16 x 16 blocks by substitution (one wave each, a column a
-// lane), then twice as large blocks from two: [[A, 0], [M, B]]^-1 has
-// -B^-1 M A^-1 in its corner. Substitution keeps the error at the size of the
-// result's entries; a product of powers (I - m)(I + m^2).. would not, since the
-// powers of m can be far larger than its inverse. `tmp`: 32 x 32, the same rows.
+// inverse's upper right quarter is not written. The diagonal 8 x 8 blocks by
+// substitution (a column of one of them a lane of the first wave), then thrice
+// twice as large blocks from two: [[A, 0], [M, B]]^-1 has -B^-1 M A^-1 in its
+// corner. Substitution keeps the error at the size of the result's entries; a
+// product of powers (I - m)(I + m^2).. would not, since the powers of m can be
+// far larger than its inverse. `tmp`: 32 x 32, the same rows. THREADS = 4 C.
 template <int C>
 __device__ __forceinline__ void invert_unit_lower(const float* m, float* inv, float* tmp, int wave, int lane)
 {
     constexpr int NB = C / 16, LD = inverse_stride(C);
-    const int col = lane & 15, gq = lane >> 4;
-    {
-        const float* d = m + wave * 16 * (LD + 1);
-        float x[16];
+    if (wave == 0 && lane < C) {
+        const int b0 = lane / 8 * 8, col = lane % 8;
+        const float* d = m + b0 * (LD + 1);
+        float x[8];
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            f32x4 s = {i == col ? 1.f : 0.f, 0.f, 0.f, 0.f};      // four sums: a shorter chain
+        for (int i = 0; i < 8; ++i) {
+            float s = i == col ? 1.f : 0.f;
 #pragma unroll
-            for (int j = 0; j < i; j += 4) {
-                const f32x4 v = *reinterpret_cast<const f32x4*>(d + i * LD + j);
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    if (j + e < i) s[e] -= v[e] * x[j + e];
-            }
-            x[i] = (s[0] + s[1]) + (s[2] + s[3]);
+            for (int j = 0; j < i; ++j) s -= d[i * LD + j] * x[j];
+            x[i] = s;
         }
-        // four lanes have the same column: each stores a quarter of it
 #pragma unroll
-        for (int i = 0; i < 16; ++i)
-            if (i / 4 == gq) inv[(wave * 16 + i) * LD + wave * 16 + col] = x[i];
+        for (int i = 0; i < 8; ++i) inv[(b0 + i) * LD + b0 + col] = x[i];
+    }
+    // zero above the diagonal within the 32 x 32 blocks
+    {
+        const int r = lane / 8, c = lane % 8;
+        inv[(wave * 16 + r) * LD + wave * 16 + 8 + c] = 0.f;
         if (wave % 2 == 0) store_block<LD>(inv + wave * 16 * LD + (wave + 1) * 16, f32x4{}, lane);
+    }
+    __syncthreads();
+    {
+        // 8 -> 16: wave w makes the corner of diagonal block w, an element a lane
+        const int r = lane / 8, c = lane % 8, b0 = wave * 16;
+        float y = 0.f;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) y += m[(b0 + 8 + r) * LD + b0 + k] * inv[(b0 + k) * LD + b0 + c];
+        tmp[(wave * 8 + r) * LD + c] = y;
+        __syncthreads();
+        y = 0.f;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) y -= inv[(b0 + 8 + r) * LD + b0 + 8 + k] * tmp[(wave * 8 + k) * LD + c];
+        inv[(b0 + 8 + r) * LD + b0 + c] = y;
     }
     __syncthreads();
     // 16 -> 32: wave w < NB / 2 makes block (2 w + 1, 2 w)
