@@ -36,7 +36,7 @@ struct DeltaParams {
     int heads_qk, heads_v, dim_k, dim_v, dv_pad;
     float scale;
     int g_dtype, beta_dtype;
-    int out4;                    // out's rows are whole, aligned units of four elements
+    int out4, dv4;               // out's (dv's) rows are whole, aligned units of four elements
     DeltaRows q, k, v, g, beta, out;
     const float* initial;        // (n_seqs or n_states, heads_v, dim_k, dim_v)
     float* final_state;

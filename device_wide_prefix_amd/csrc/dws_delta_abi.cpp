@@ -284,6 +284,7 @@ dws_status backward_entry(const dws_delta_rule_args* a, hipStream_t stream)
     if (a->d_workspace == nullptr || a->workspace_bytes < z.bytes) return DWS_ERR_INVALID_ARG;
     if ((st = r.add(a->d_workspace, z.bytes, true, 256)) != DWS_OK) return st;
     if (r.overlap()) return DWS_ERR_OVERLAP;
+    p.dv4 = whole_units(p.dv, a->dim_v, a->dtype, 4 * (int)size_of(a->dtype));
     p.initial = a->d_initial_state;
     p.d_final = a->d_final_grad;
     p.d_initial = a->d_initial_grad;

@@ -14,6 +14,8 @@
 
 #include "dws_delta_device.hpp"
 
+#include <type_traits>
+
 namespace dws {
 
 // Tokens of a chunk: 64, and 32 where a chunk's tiles twice over (the next
@@ -693,7 +695,8 @@ __global__ __launch_bounds__(NW * 128) DWS_TWO_WAVES void k_delta_scan(DeltaPara
 //   dU = P^T dO + diag(e^(G_C - G)) K dS'     Z = (I + B L)^-T dU     dX = B Z = dV
 //   dS = e^(G_C) dS' + Q^T diag(scale e^G) dO - K^T diag(e^G) dX
 // The same shape as the forward scan, from a sequence's last chunk to its
-// first. Z and dS' go to the workspace, dV to its place.
+// first. Z and dS' go to the workspace; the next kernel, which has Z by rows,
+// writes dV (16 two-byte stores a lane here were a third of a chunk's time).
 
 template <class T, int DK, int NW>
 __global__ __launch_bounds__(NW * 128) DWS_TWO_WAVES void k_delta_scan_back(DeltaParams p)
@@ -802,21 +805,12 @@ __global__ __launch_bounds__(NW * 128) DWS_TWO_WAVES void k_delta_scan_back(Delt
             mma_each(a, parts_of<T, NF>(z[2 * kb], z[2 * kb + 1]), y, 0, 2 * kb + 2);
         }
         store_columns<T, NF, C>(static_cast<T*>(p.w_z) + at * NF * C * p.dv_pad, y, col, p.dv_pad, gq);
-        const int rows = rows_at(c);
-        T* dv0 = static_cast<T*>(p.dv.data) + (w.begin + (int64_t)c * C) * p.dv.ts + w.h * p.dv.hs;
-        const auto rsrc = rows_rsrc(dv0, p.dv.ts * (int)sizeof(T), rows, p.dim_v * (int)sizeof(T));
-        const int step = (int)p.dv.ts * (int)sizeof(T);
         f32x4 e[NB];
 #pragma unroll
         for (int mt = 0; mt < NB; ++mt) {
             const int row = mt * 16 + gq * 4;
-            y[mt] *= gate4(gate, 2 * C + row);
-#pragma unroll
-            for (int r = 0; r < 4; ++r)
-                buffer_store<T>(rsrc, col < p.dim_v && row + r < rows ? (row + r) * step + col * (int)sizeof(T) : kOutside,
-                                (T)y[mt][r]);
             const f32x4 eg = gate4(gate, row);
-            y[mt] *= -eg;
+            y[mt] *= -(eg * gate4(gate, 2 * C + row));
             e[mt] = __builtin_convertvector(d_o[mt], f32x4) * (p.scale * eg);
         }
         const float keep = gate[C - 1];
@@ -854,7 +848,7 @@ __global__ __launch_bounds__(NW * 128) DWS_TWO_WAVES void k_delta_scan_back(Delt
 //   W1 = scale D o dP                         W2 = B (D o M)
 //   dQ = W1 K + scale diag(e^G) dO S^T
 //   dK = W1^T Q + (W2 + W2^T) K + diag(e^(G_C - G)) B U' dS'^T - diag(e^G) B Z S^T
-//   dbeta_i = Z_i . U'_i
+//   dV = B Z              dbeta_i = Z_i . U'_i
 //   N = W1 o Q K^T + W2 o K K^T
 //   dG_i = sum_j (N_ij - N_ji) + (scale e^G dO S^T)_i . q_i - (e^G B Z S^T)_i . k_i - w_i,
 //          w_i = (e^(G_C - G) B U' dS'^T)_i . k_i;   dG_C also gets sum w + e^(G_C) <S, dS'>
@@ -882,16 +876,40 @@ struct GradLds {
     static constexpr size_t bytes = gate + ((kGateArrays + 1 + 3 * GROUPS + NB) * C + 16) * sizeof(float);
 };
 
-__device__ __forceinline__ float sum16(float x)      // over the 16 lanes of a group
+// Over the 16 lanes of a group, by rotations within a row of lanes.
+__device__ __forceinline__ float sum16(float x)
 {
-#pragma unroll
-    for (int d = 1; d < 16; d *= 2) x += __shfl_xor(x, d, 64);
-    return x;
+    auto turned = [](float y, auto n) {
+        return __builtin_bit_cast(float, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, y), 0x120 + decltype(n)::value, 0xf,
+                                                                  0xf, true));
+    };
+    x += turned(x, std::integral_constant<int, 8>{});
+    x += turned(x, std::integral_constant<int, 4>{});
+    x += turned(x, std::integral_constant<int, 2>{});
+    return x + turned(x, std::integral_constant<int, 1>{});
 }
 __device__ __forceinline__ float sum_groups(float x) // over the 4 groups
 {
     x += __shfl_xor(x, 16, 64);
     return x + __shfl_xor(x, 32, 64);
+}
+// Eight elements of a row (at element `row` of the resource, -1: none), columns
+// c .. c + 3 and c + 16 .. c + 19.
+template <class T>
+__device__ __forceinline__ void store_quads(__amdgpu_buffer_rsrc_t rsrc, bool whole, int row, int c, int dim, Vec8<T> x)
+{
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+        const int o = c + q * 16;
+        const Vec4<T> y = q == 0 ? __builtin_shufflevector(x, x, 0, 1, 2, 3) : __builtin_shufflevector(x, x, 4, 5, 6, 7);
+        if (whole) {
+            buffer_store(rsrc, row >= 0 && o < dim ? (row + o) * (int)sizeof(T) : kOutside, y);
+        } else {
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+                buffer_store<T>(rsrc, row >= 0 && o + r < dim ? (row + o + r) * (int)sizeof(T) : kOutside, y[r]);
+        }
+    }
 }
 
 template <class T, int DK>
@@ -960,6 +978,8 @@ __global__ __launch_bounds__((GradLds<T, DK>::THREADS)) DWS_TWO_WAVES void k_del
         const int64_t at = slot * p.heads_v + h;
         for (int i = tid; i < kGateArrays * C; i += THREADS) gate[i] = p.w_gate[at * kGateArrays * C + i];
 
+        const auto dv_rsrc = rows_rsrc(static_cast<T*>(p.dv.data) + info.row * p.dv.ts + h * p.dv.hs, p.dv.ts * (int)sizeof(T),
+                                       rows, p.dim_v * (int)sizeof(T));
         f32x4 dp[NT] = {}, zu[NT] = {}, os[NK] = {}, zs[NK] = {}, us[NK] = {};
         float zdotu = 0.f, sds = 0.f;
         for (int c = 0; c < p.dv_pad; c += 32) {
@@ -979,7 +999,8 @@ __global__ __launch_bounds__((GradLds<T, DK>::THREADS)) DWS_TWO_WAVES void k_del
                 load(h + 1, 0);
             const Parts<T, NF> az = parts_tr<NF>(zt, 32 * LC, LC, 0, row0, lane);
             const Parts<T, NF> au = parts_tr<NF>(ut, 32 * LC, LC, 0, row0, lane);
-            if (grp == 0)
+            if (grp == 0) {
+                f32x8 dv = {};
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
                     float z = 0.f, u = 0.f;
@@ -989,7 +1010,11 @@ __global__ __launch_bounds__((GradLds<T, DK>::THREADS)) DWS_TWO_WAVES void k_del
                         u += (float)au.p[n][j];
                     }
                     zdotu += z * u;
+                    dv[j] = gate[2 * C + row0 + lr] * z;
                 }
+                store_quads(dv_rsrc, p.dv4, row0 + lr < rows ? (row0 + lr) * (int)p.dv.ts : -1, c + gq * 4, p.dim_v,
+                            __builtin_convertvector(dv, Vec8<T>));
+            }
 #pragma unroll
             for (int i = 0; i < NT; ++i)
                 if (grp + i * GROUPS <= tile) {
