@@ -325,6 +325,16 @@ __device__ __forceinline__ int64_t seq_length(const int64_t* offsets, int64_t to
 // one before tokens / C + n_seqs.
 __device__ __forceinline__ int64_t first_slot(int64_t begin, int64_t i, int chunk) { return begin / chunk + i; }
 
+// A value that all lanes have, for the compiler to know it: a buffer resource
+// made of one that it takes for different in each lane costs a loop over the
+// lanes at every access.
+__device__ __forceinline__ int uniform(int x) { return __builtin_amdgcn_readfirstlane(x); }
+__device__ __forceinline__ int64_t uniform(int64_t x)
+{
+    const uint32_t lo = (uint32_t)uniform((int)x), hi = (uint32_t)uniform((int)(x >> 32));
+    return (int64_t)((uint64_t)hi << 32 | lo);
+}
+
 struct SlotInfo {
     int64_t seq;
     int64_t row;       // first row of the chunk
@@ -350,10 +360,10 @@ __device__ __forceinline__ SlotInfo slot_info(const int64_t* offsets, int64_t to
     const int64_t b = seq_begin(offsets, tokens, n_seqs, at), n = seq_length(offsets, tokens, n_seqs, at, b);
     const uint64_t found = __ballot(lo + lane <= hi && first_slot(b, at, C) <= slot);
     const int k = found == 0 ? 0 : 63 - __builtin_clzll(found);
-    lo += k;
+    lo = uniform(lo + k);
     SlotInfo s;
     s.seq = lo;
-    const int64_t begin = __shfl(b, k, 64), len = __shfl(n, k, 64);
+    const int64_t begin = uniform(__shfl(b, k, 64)), len = uniform(__shfl(n, k, 64));
     const int64_t c = slot - first_slot(begin, lo, C);
     const int64_t left = len - c * C;
     s.row = begin + c * C;

@@ -233,7 +233,7 @@ __global__ __launch_bounds__((kChunk<T, DK> * 4)) void k_delta_prep(DeltaParams 
     float* beta = reinterpret_cast<float*>(smem + S::gate);
     float* sum_hi = beta + C;
     float* sum_lo = sum_hi + C;
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, gq = lane >> 4, lr = lane & 15;
+    const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6), gq = lane >> 4, lr = lane & 15;
     const int64_t slot = blockIdx.x / p.heads_v;
     const int h = blockIdx.x % p.heads_v, hk = h / (p.heads_v / p.heads_qk);
     const SlotInfo info = slot_info<C>(p.offsets, p.tokens, p.n_seqs, slot, lane);
@@ -936,7 +936,7 @@ __global__ __launch_bounds__((GradLds<T, DK>::THREADS)) DWS_TWO_WAVES void k_del
     float* n_part = col_part + NB * C;                           // [GROUPS][C] row sums of N
     float* inner = n_part + GROUPS * C;                          // parts of <S, dS'>
 
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, gq = lane >> 4, lr = lane & 15;
+    const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6), gq = lane >> 4, lr = lane & 15;
     const int tile = wave % NB, grp = wave / NB, row0 = tile * 16, key0 = grp * 64;
     const int64_t slot = blockIdx.x / p.heads_qk;
     const int hk = blockIdx.x % p.heads_qk, share = p.heads_v / p.heads_qk;
@@ -997,6 +997,7 @@ __global__ __launch_bounds__((GradLds<T, DK>::THREADS)) DWS_TWO_WAVES void k_del
                 load(h, c + 32);
             else if (m + 1 < share)
                 load(h + 1, 0);
+            __builtin_amdgcn_sched_barrier(0);
             const Parts<T, NF> az = parts_tr<NF>(zt, 32 * LC, LC, 0, row0, lane);
             const Parts<T, NF> au = parts_tr<NF>(ut, 32 * LC, LC, 0, row0, lane);
             if (grp == 0) {
@@ -1015,6 +1016,7 @@ __global__ __launch_bounds__((GradLds<T, DK>::THREADS)) DWS_TWO_WAVES void k_del
                 store_quads(dv_rsrc, p.dv4, row0 + lr < rows ? (row0 + lr) * (int)p.dv.ts : -1, c + gq * 4, p.dim_v,
                             __builtin_convertvector(dv, Vec8<T>));
             }
+            __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
             for (int i = 0; i < NT; ++i)
                 if (grp + i * GROUPS <= tile) {
@@ -1022,6 +1024,7 @@ __global__ __launch_bounds__((GradLds<T, DK>::THREADS)) DWS_TWO_WAVES void k_del
                     dp[i] = mma(b, ao, dp[i]);
                     zu[i] = mma(b, az, zu[i]);
                 }
+            __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
             for (int t = 0; t < NK; ++t) {
                 const Parts<T, 1> b = {{frag_tr(st, LS, 0, key0 + t * 16, lane)}};
@@ -1047,6 +1050,7 @@ __global__ __launch_bounds__((GradLds<T, DK>::THREADS)) DWS_TWO_WAVES void k_del
         const float bi = gate[2 * C + i], hi = gate[3 * C + i], li = gate[4 * C + i];
 #pragma unroll
         for (int e = 0; e < NT; ++e) {
+            __builtin_amdgcn_sched_barrier(0);
             const int nt = grp + e * GROUPS, j0 = nt * 16 + gq * 4;
             if (nt >= NB) break;
             f32x4 a = {}, b = {}, ncol = {};
