@@ -93,16 +93,17 @@ __device__ __forceinline__ void store_block(float* at, f32x4 x, int lane)
 // in different banks.
 constexpr int inverse_stride(int c) { return c + 4; }
 
-// inv = (I + m)^-1, m strictly lower triangular, both fp32 in LDS with rows of
-// inverse_stride(C); of m only the entries below the diagonal are read, and the
+// m <- (I + m)^-1, m strictly lower triangular, fp32 in LDS with rows of
+// inverse_stride(C). Of m only the entries below the diagonal are read, and the
 // inverse's upper right quarter is not written. The diagonal 8 x 8 blocks by
 // substitution (a column of one of them a lane of the first wave), then thrice
 // twice as large blocks from two: [[A, 0], [M, B]]^-1 has -B^-1 M A^-1 in its
 // corner. Substitution keeps the error at the size of the result's entries; a
 // product of powers (I - m)(I + m^2).. would not, since the powers of m can be
-// far larger than its inverse. `tmp`: 32 x 32, the same rows. THREADS = 4 C.
+// far larger than its inverse. Each block takes the place of the part of m that
+// it was made from. `tmp`: 32 x 32, the same rows. THREADS = 4 C.
 template <int C>
-__device__ __forceinline__ void invert_unit_lower(const float* m, float* inv, float* tmp, int wave, int lane)
+__device__ __forceinline__ void invert_unit_lower(float* m, float* tmp, int wave, int lane)
 {
     constexpr int NB = C / 16, LD = inverse_stride(C);
     if (wave == 0 && lane < C) {
@@ -117,13 +118,13 @@ __device__ __forceinline__ void invert_unit_lower(const float* m, float* inv, fl
             x[i] = s;
         }
 #pragma unroll
-        for (int i = 0; i < 8; ++i) inv[(b0 + i) * LD + b0 + col] = x[i];
+        for (int i = 0; i < 8; ++i) m[(b0 + i) * LD + b0 + col] = x[i];
     }
     // zero above the diagonal within the 32 x 32 blocks
     {
         const int r = lane / 8, c = lane % 8;
-        inv[(wave * 16 + r) * LD + wave * 16 + 8 + c] = 0.f;
-        if (wave % 2 == 0) store_block<LD>(inv + wave * 16 * LD + (wave + 1) * 16, f32x4{}, lane);
+        m[(wave * 16 + r) * LD + wave * 16 + 8 + c] = 0.f;
+        if (wave % 2 == 0) store_block<LD>(m + wave * 16 * LD + (wave + 1) * 16, f32x4{}, lane);
     }
     __syncthreads();
     {
@@ -131,33 +132,33 @@ __device__ __forceinline__ void invert_unit_lower(const float* m, float* inv, fl
         const int r = lane / 8, c = lane % 8, b0 = wave * 16;
         float y = 0.f;
 #pragma unroll
-        for (int k = 0; k < 8; ++k) y += m[(b0 + 8 + r) * LD + b0 + k] * inv[(b0 + k) * LD + b0 + c];
+        for (int k = 0; k < 8; ++k) y += m[(b0 + 8 + r) * LD + b0 + k] * m[(b0 + k) * LD + b0 + c];
         tmp[(wave * 8 + r) * LD + c] = y;
         __syncthreads();
         y = 0.f;
 #pragma unroll
-        for (int k = 0; k < 8; ++k) y -= inv[(b0 + 8 + r) * LD + b0 + 8 + k] * tmp[(wave * 8 + k) * LD + c];
-        inv[(b0 + 8 + r) * LD + b0 + c] = y;
+        for (int k = 0; k < 8; ++k) y -= m[(b0 + 8 + r) * LD + b0 + 8 + k] * tmp[(wave * 8 + k) * LD + c];
+        m[(b0 + 8 + r) * LD + b0 + c] = y;
     }
     __syncthreads();
     // 16 -> 32: wave w < NB / 2 makes block (2 w + 1, 2 w)
     const int a = wave * 2;
     if (wave < NB / 2)
         store_block<LD>(tmp + wave * 16 * LD,
-                        block_product<LD, 16>(m + (a + 1) * 16 * LD + a * 16, inv + a * 16 * (LD + 1), f32x4{}, lane), lane);
+                        block_product<LD, 16>(m + (a + 1) * 16 * LD + a * 16, m + a * 16 * (LD + 1), f32x4{}, lane), lane);
     __syncthreads();
     if (wave < NB / 2)
-        store_block<LD>(inv + (a + 1) * 16 * LD + a * 16,
-                        -block_product<LD, 16>(inv + (a + 1) * 16 * (LD + 1), tmp + wave * 16 * LD, f32x4{}, lane), lane);
+        store_block<LD>(m + (a + 1) * 16 * LD + a * 16,
+                        -block_product<LD, 16>(m + (a + 1) * 16 * (LD + 1), tmp + wave * 16 * LD, f32x4{}, lane), lane);
     __syncthreads();
     if constexpr (NB == 4) {
         // 32 -> 64: four blocks, one a wave
         const int bi = wave >> 1, bj = wave & 1;
         store_block<LD>(tmp + bi * 16 * LD + bj * 16,
-                        block_product<LD, 32>(m + (32 + bi * 16) * LD, inv + bj * 16, f32x4{}, lane), lane);
+                        block_product<LD, 32>(m + (32 + bi * 16) * LD, m + bj * 16, f32x4{}, lane), lane);
         __syncthreads();
-        store_block<LD>(inv + (32 + bi * 16) * LD + bj * 16,
-                        -block_product<LD, 32>(inv + (32 + bi * 16) * LD + 32, tmp + bj * 16, f32x4{}, lane), lane);
+        store_block<LD>(m + (32 + bi * 16) * LD + bj * 16,
+                        -block_product<LD, 32>(m + (32 + bi * 16) * LD + 32, tmp + bj * 16, f32x4{}, lane), lane);
         __syncthreads();
     }
 }
@@ -203,16 +204,18 @@ __device__ __forceinline__ f32x4 gate4(const float* gate, int row) { return *rei
 // Row of tile t of a lower triangle's tiles in order: 0; 1, 1; 2, 2, 2; ...
 __device__ __forceinline__ int tile_row(int t) { return t < 1 ? 0 : (t < 3 ? 1 : (t < 6 ? 2 : 3)); }
 
-// LDS of the preparation: the matrices of the inversion share their place with
-// the K and Q tiles, which are done with before.
+// LDS of the preparation: the matrix that is inverted takes the place of the K
+// tile, which is done with before (Q's fragments come straight from memory).
+// 18 KB for 128 key columns, eight workgroups a compute unit; four, with Q and
+// the inverse in LDS too, measured the same (121 to 125 us on 8,544 chunks and
+// heads): the vector instructions, 1,200 a wave, are what bounds it.
 template <class T, int DK>
 struct PrepLds {
     static constexpr int C = kChunk<T, DK>, LK = lds_stride<T>(DK), LD = inverse_stride(C);
-    static constexpr size_t tiles = 2 * (size_t)C * LK * sizeof(T), matrix = (size_t)C * LD * sizeof(float);
-    // m and the inverse; a chunk of 64 keeps block products in the inverse's
-    // upper right quarter, one of 32 behind it
-    static constexpr size_t inverse = (C == 64 ? 2 : 3) * matrix;
-    static constexpr size_t gate = tiles > inverse ? tiles : inverse, bytes = gate + 3 * C * sizeof(float);
+    static constexpr size_t tile = (size_t)C * LK * sizeof(T), matrix = (size_t)C * LD * sizeof(float);
+    // block products: in the upper right quarter of a 64 x 64 matrix, behind a smaller one
+    static constexpr size_t inverse = (C == 64 ? 1 : 2) * matrix;
+    static constexpr size_t gate = tile > inverse ? tile : inverse, bytes = gate + 3 * C * sizeof(float);
 };
 
 // One workgroup for each (chunk slot, value head): gate factors, P and the
@@ -226,10 +229,8 @@ __global__ __launch_bounds__((kChunk<T, DK> * 4)) void k_delta_prep(DeltaParams 
     constexpr int NX = NP > NF ? NP : NF;
     extern __shared__ __attribute__((aligned(16))) char smem[];
     T* ks = reinterpret_cast<T*>(smem);
-    T* qs = ks + C * LK;
     float* m = reinterpret_cast<float*>(smem);
-    float* inv = m + C * LD;
-    float* tmp = C == 64 ? inv + 32 : inv + C * LD;
+    float* tmp = C == 64 ? m + 32 : m + C * LD;
     float* beta = reinterpret_cast<float*>(smem + S::gate);
     float* sum_hi = beta + C;
     float* sum_lo = sum_hi + C;
@@ -263,9 +264,8 @@ __global__ __launch_bounds__((kChunk<T, DK> * 4)) void k_delta_prep(DeltaParams 
         if (p.g.data) g = clamp_decay(load_gate(p.g, info.row + lane, h, p.g_dtype));
         b = load_gate(p.beta, info.row + lane, h, p.beta_dtype);
     }
-    TileRegs<T, C, DK, THREADS> kr, qr;
+    TileRegs<T, C, DK, THREADS> kr;
     kr.load(k0, p.k.ts, info.rows, p.dim_k, tid);
-    qr.load(q0, p.q.ts, info.rows, p.dim_k, tid);
     if (wave == 0) {
         const double sum = scan_decays<C>((double)g * 1.4426950408889634, lane);
         const double last = __shfl(sum, C - 1, 64);
@@ -283,7 +283,6 @@ __global__ __launch_bounds__((kChunk<T, DK> * 4)) void k_delta_prep(DeltaParams 
         }
     }
     kr.store(ks, LK, tid);
-    qr.store(qs, LK, tid);
     __syncthreads();
 
     // A tile's results run along i for the forward pass and along j for the
@@ -293,19 +292,25 @@ __global__ __launch_bounds__((kChunk<T, DK> * 4)) void k_delta_prep(DeltaParams 
     constexpr int TILES = NB * (NB + 1) / 2, EACH = (TILES + NB - 1) / NB;
     T* wp = static_cast<T*>(p.w_p) + at * NF * F::elems;
     f32x4 low[BWD ? EACH : 1];      // B L
-    f32x4 lb[EACH];                 // L B, for m once K and Q are done with
+    f32x4 lb[EACH];                 // L B, for m once K is done with
+    const auto q_rsrc = rows_rsrc(q0, p.q.ts * (int)sizeof(T), info.rows, whole_bytes<T>(p.dim_k));
 #pragma unroll
     for (int e = 0; e < EACH; ++e) {
         const int tile = e * NB + wave;
         if (tile >= TILES) break;
         const int it = tile_row(tile), jt = tile - it * (it + 1) / 2;
         f32x4 kk = {}, qk = {};
+        Vec8<T> qf[DK / 32];
 #pragma unroll
-        for (int kb = 0; kb < DK; kb += 32) {
-            const Vec8<T> ki = frag_nat(ks, LK, it * 16, kb, lane), kj = frag_nat(ks, LK, jt * 16, kb, lane);
-            const Vec8<T> qi = frag_nat(qs, LK, it * 16, kb, lane);
+        for (int kb = 0; kb < DK / 32; ++kb) {
+            const int row = it * 16 + lr, c = kb * 32 + gq * 8;
+            qf[kb] = buffer_frag<T>(q_rsrc, row < info.rows && c < p.dim_k ? (row * (int)p.q.ts + c) * (int)sizeof(T) : kOutside);
+        }
+#pragma unroll
+        for (int kb = 0; kb < DK / 32; ++kb) {
+            const Vec8<T> ki = frag_nat(ks, LK, it * 16, kb * 32, lane), kj = frag_nat(ks, LK, jt * 16, kb * 32, lane);
             kk = BWD ? mma(ki, kj, kk) : mma(kj, ki, kk);
-            qk = BWD ? mma(qi, kj, qk) : mma(kj, qi, qk);
+            qk = BWD ? mma(qf[kb], kj, qk) : mma(kj, qf[kb], qk);
         }
         const int one = (BWD ? jt : it) * 16 + lr, four = (BWD ? it : jt) * 16 + gq * 4;
         const float hi = sum_hi[one], lo = sum_lo[one], b1 = beta[one];
@@ -345,11 +350,11 @@ __global__ __launch_bounds__((kChunk<T, DK> * 4)) void k_delta_prep(DeltaParams 
     }
     __syncthreads();
 
-    invert_unit_lower<C>(m, inv, tmp, wave, lane);
+    invert_unit_lower<C>(m, tmp, wave, lane);
     T* wt = static_cast<T*>(p.w_t) + at * NX * F::elems;
     for (int i = tid; i < C * C / 4; i += THREADS) {
         const int row = i / (C / 4), c = i % (C / 4) * 4;
-        const float* x = inv + row * LD + c;
+        const float* x = m + row * LD + c;
         if (F::in_lower(row, c)) store_parts4<NX>(wt + F::lower_acc(row, c), F::elems, f32x4{x[0], x[1], x[2], x[3]});
     }
     if constexpr (BWD) {
@@ -363,11 +368,11 @@ __global__ __launch_bounds__((kChunk<T, DK> * 4)) void k_delta_prep(DeltaParams 
             store_block<LD>(m + it * 16 * LD + jt * 16, low[e], lane);
         }
         __syncthreads();
-        invert_unit_lower<C>(m, inv, tmp, wave, lane);
+        invert_unit_lower<C>(m, tmp, wave, lane);
         T* wtt = static_cast<T*>(p.w_tt) + at * NF * F::elems;
         for (int i = tid; i < C * C / 4; i += THREADS) {
             const int row = i / (C / 4), c = i % (C / 4) * 4;       // of the transposed
-            const float* x = inv + c * LD + row;
+            const float* x = m + c * LD + row;
             if (F::in_upper(row, c))
                 store_parts4<NF>(wtt + F::upper_acc(row, c), F::elems, f32x4{x[0], x[LD], x[2 * LD], x[3 * LD]});
         }
@@ -402,11 +407,11 @@ struct ScanPlace {
     int h, hk, first;       // first column of the workgroup
 };
 template <int C, int NW>
-__device__ __forceinline__ bool scan_place(const DeltaParams& p, ScanPlace* w)
+__device__ __forceinline__ bool scan_place(const DeltaParams& p, uint32_t block, ScanPlace* w)
 {
     const uint32_t parts = (uint32_t)((p.dim_v + NW * 16 - 1) / (NW * 16));
     uint32_t group, part;
-    xcd_split(blockIdx.x, parts, &group, &part);
+    xcd_split(block, parts, &group, &part);
     if (group >= (uint64_t)p.n_seqs * p.heads_v) return false;
     w->seq = group / p.heads_v;
     w->h = group % p.heads_v;
@@ -466,18 +471,16 @@ __device__ __forceinline__ void store_columns(T* at, const f32x4 (&u)[C / 16], i
 // the workspace (for the backward pass). NP: parts of the operands the state
 // depends on.
 template <class T, int DK, int NP, bool STORE, int NW>
-__global__ __launch_bounds__(NW * 128) DWS_TWO_WAVES void k_delta_scan(DeltaParams p)
+__device__ __forceinline__ void delta_scan(const DeltaParams& p, uint32_t block, char* smem)
 {
     constexpr int NF = kFine<T>, NX = NP > NF ? NP : NF;
     using L = ScanLds<T, DK, NW, 1, NX, !STORE>;
     constexpr int C = L::C, THREADS = NW * 64, NB = C / 16, LK = L::LK, LC = L::LC, LV = L::LV, NK = DK / 16;
     using F = Triangle<C>;
-    extern __shared__ __attribute__((aligned(16))) char smem[];
-
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) % NW;
     const int gq = lane >> 4, lr = lane & 15;
     ScanPlace w;
-    if (!scan_place<C, NW>(p, &w)) return;
+    if (!scan_place<C, NW>(p, block, &w)) return;
     int64_t st;
     if (!slot_taken<2 * THREADS>(p.slots, p.n_states, w.seq, &st, threadIdx.x)) return;
     const int64_t state_at = (st * p.heads_v + w.h) * p.dim_k * p.dim_v;
@@ -699,18 +702,16 @@ __global__ __launch_bounds__(NW * 128) DWS_TWO_WAVES void k_delta_scan(DeltaPara
 // writes dV (16 two-byte stores a lane here were a third of a chunk's time).
 
 template <class T, int DK, int NW>
-__global__ __launch_bounds__(NW * 128) DWS_TWO_WAVES void k_delta_scan_back(DeltaParams p)
+__device__ __forceinline__ void delta_scan_back(const DeltaParams& p, uint32_t block, char* smem)
 {
     constexpr int NF = kFine<T>;
     using L = ScanLds<T, DK, NW, 2, 2 * NF, false>;
     constexpr int C = L::C, THREADS = NW * 64, NB = C / 16, LK = L::LK, LV = L::LV, NK = DK / 16;
     using F = Triangle<C>;
-    extern __shared__ __attribute__((aligned(16))) char smem[];
-
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) % NW;
     const int gq = lane >> 4, lr = lane & 15;
     ScanPlace w;
-    if (!scan_place<C, NW>(p, &w)) return;
+    if (!scan_place<C, NW>(p, block, &w)) return;
     const int64_t state_at = (w.seq * p.heads_v + w.h) * p.dim_k * p.dim_v;
     const int chunks = (int)((w.len + C - 1) / C);
     const int col = w.first + wave * 16 + lr;
@@ -839,6 +840,26 @@ __global__ __launch_bounds__(NW * 128) DWS_TWO_WAVES void k_delta_scan_back(Delt
     }
     if (p.d_initial != nullptr)
         store_state<DK>(ds, static_cast<T*>(p.d_initial) + state_at, p.dim_k, p.dim_v, col, gq);
+}
+
+template <class T, int DK, int NP, int NW>
+__global__ __launch_bounds__(NW * 128) DWS_TWO_WAVES void k_delta_scan(DeltaParams p)
+{
+    extern __shared__ __attribute__((aligned(16))) char smem[];
+    delta_scan<T, DK, NP, false, NW>(p, blockIdx.x, smem);
+}
+// The backward pass's two scans, which do not need each other: half of the
+// workgroups each, the longer ones first. Where there are fewer of them than
+// compute units both run at once.
+template <class T, int DK, int NW>
+__global__ __launch_bounds__(NW * 128) DWS_TWO_WAVES void k_delta_scan_both(DeltaParams p)
+{
+    extern __shared__ __attribute__((aligned(16))) char smem[];
+    const uint32_t half = gridDim.x / 2;
+    if (blockIdx.x < half)
+        delta_scan_back<T, DK, NW>(p, blockIdx.x, smem);
+    else
+        delta_scan<T, DK, 1, true, NW>(p, blockIdx.x - half, smem);
 }
 
 // ---- the gradients of q, k and the gates ------------------------------------
@@ -1223,20 +1244,20 @@ template <class T, int DK>
 constexpr int kMostWaves = sizeof(T) == 4 && DK > 128 ? 2 : 4;
 constexpr uint64_t kComputeUnits = 256;
 
-template <class T, int DK, int NP, bool STORE, int NW>
+template <class T, int DK, int NP, int NW>
 hipError_t launch_scan(const DeltaParams& p, hipStream_t stream)
 {
     constexpr int NF = kFine<T>, NX = NP > NF ? NP : NF;
-    return launch_lds(k_delta_scan<T, DK, NP, STORE, NW>, scan_blocks(p, NW), NW * 128,
-                      ScanLds<T, DK, NW, 1, NX, !STORE>::bytes, p, stream);
+    return launch_lds(k_delta_scan<T, DK, NP, NW>, scan_blocks(p, NW), NW * 128, ScanLds<T, DK, NW, 1, NX, true>::bytes, p,
+                      stream);
 }
 template <class T, int DK, int NW>
-hipError_t launch_back(const DeltaParams& p, hipStream_t stream)
+hipError_t launch_both(const DeltaParams& p, hipStream_t stream)
 {
-    return launch_lds(k_delta_scan_back<T, DK, NW>, scan_blocks(p, NW), NW * 128,
+    // the backward scan's LDS, the larger one
+    return launch_lds(k_delta_scan_both<T, DK, NW>, 2 * scan_blocks(p, NW), NW * 128,
                       ScanLds<T, DK, NW, 2, 2 * kFine<T>, false>::bytes, p, stream);
 }
-inline bool few_groups(const DeltaParams& p) { return scan_blocks(p, 4) < kComputeUnits; }
 
 template <class T, int DK, int NP>
 hipError_t forward_dk(const DeltaParams& p, hipStream_t stream)
@@ -1245,8 +1266,8 @@ hipError_t forward_dk(const DeltaParams& p, hipStream_t stream)
     const hipError_t e = launch_lds(k_delta_prep<T, DK, NP, false>, (uint64_t)p.n_slots * p.heads_v, C * 4,
                                     PrepLds<T, DK>::bytes, p, stream);
     if (e != hipSuccess) return e;
-    if (few_groups(p)) return launch_scan<T, DK, NP, false, 2>(p, stream);
-    return launch_scan<T, DK, NP, false, kMostWaves<T, DK>>(p, stream);
+    if (scan_blocks(p, 4) < kComputeUnits) return launch_scan<T, DK, NP, 2>(p, stream);
+    return launch_scan<T, DK, NP, kMostWaves<T, DK>>(p, stream);
 }
 template <class T, int NP>
 hipError_t forward_type(const DeltaParams& p, const DeltaPack& k, hipStream_t stream)
@@ -1267,9 +1288,8 @@ hipError_t backward_dk(const DeltaParams& p, hipStream_t stream)
     hipError_t e = launch_lds(k_delta_prep<T, DK, 1, true>, (uint64_t)p.n_slots * p.heads_v, C * 4,
                               PrepLds<T, DK>::bytes, p, stream);
     if (e != hipSuccess) return e;
-    e = few_groups(p) ? launch_scan<T, DK, 1, true, 2>(p, stream) : launch_scan<T, DK, 1, true, kMostWaves<T, DK>>(p, stream);
-    if (e != hipSuccess) return e;
-    e = few_groups(p) ? launch_back<T, DK, 2>(p, stream) : launch_back<T, DK, kMostWaves<T, DK>>(p, stream);
+    e = 2 * scan_blocks(p, 4) < kComputeUnits ? launch_both<T, DK, 2>(p, stream)
+                                              : launch_both<T, DK, kMostWaves<T, DK>>(p, stream);
     if (e != hipSuccess) return e;
     return launch_lds(k_delta_grad<T, DK>, (uint64_t)p.n_slots * p.heads_qk, GradLds<T, DK>::THREADS,
                       GradLds<T, DK>::bytes, p, stream);
