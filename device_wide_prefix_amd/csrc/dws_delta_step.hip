@@ -32,7 +32,7 @@ __device__ __forceinline__ void store_as(void* p, int64_t at, int dtype, float x
 // One workgroup: CBL * VW columns of one (sequence, value head). A row of the
 // block is read by CBL lanes, VW columns each; thread group rg holds rows
 // rg, rg + GROUPS, ... in registers for all of the sequence's tokens.
-template <int VW, int CBL, int RPT>
+template <int VW, int CBL, int RPT, bool NT>
 __global__ __launch_bounds__(kStepThreads) void k_delta_step(DeltaStepParams p)
 {
     constexpr int GROUPS = kStepThreads / CBL, CB = CBL * VW, WAVES = kStepThreads / 64;
@@ -61,7 +61,8 @@ __global__ __launch_bounds__(kStepThreads) void k_delta_step(DeltaStepParams p)
     for (int i = 0; i < RPT; ++i) {
         const int row = rg + i * GROUPS;
         s[i] = VecF{};
-        if (row < p.dim_k && c0 < p.dim_v) s[i] = *reinterpret_cast<const VecF*>(s0 + (int64_t)row * p.dim_v);
+        const VecF* at = reinterpret_cast<const VecF*>(s0 + (int64_t)row * p.dim_v);
+        if (row < p.dim_k && c0 < p.dim_v) s[i] = NT ? __builtin_nontemporal_load(at) : *at;
     }
     for (int64_t t = begin; t < begin + len; ++t) {
         for (int i = tid; i < kStepMaxK; i += kStepThreads) {
@@ -133,20 +134,26 @@ __global__ __launch_bounds__(kStepThreads) void k_delta_step(DeltaStepParams p)
 #pragma unroll
     for (int i = 0; i < RPT; ++i) {
         const int row = rg + i * GROUPS;
-        if (row < p.dim_k && c0 < p.dim_v) *reinterpret_cast<VecF*>(s0 + (int64_t)row * p.dim_v) = s[i];
+        VecF* at = reinterpret_cast<VecF*>(s0 + (int64_t)row * p.dim_v);
+        if (row < p.dim_k && c0 < p.dim_v) {
+            if (NT)
+                __builtin_nontemporal_store(s[i], at);
+            else
+                *at = s[i];
+        }
     }
 }
 
-template <int VW, int CBL>
+template <int VW, int CBL, bool NT = false>
 hipError_t launch(const DeltaStepParams& p, hipStream_t stream)
 {
     constexpr int GROUPS = kStepThreads / CBL, CB = CBL * VW;
     const uint64_t blocks = (uint64_t)p.n_seqs * p.heads_v * (((uint64_t)p.dim_v + CB - 1) / CB);
     const dim3 grid((uint32_t)blocks), threads(kStepThreads);
     switch (delta_padded_k(p.dim_k)) {
-    case 64: k_delta_step<VW, CBL, 64 / GROUPS><<<grid, threads, 0, stream>>>(p); break;
-    case 128: k_delta_step<VW, CBL, 128 / GROUPS><<<grid, threads, 0, stream>>>(p); break;
-    default: k_delta_step<VW, CBL, 256 / GROUPS><<<grid, threads, 0, stream>>>(p); break;
+    case 64: k_delta_step<VW, CBL, 64 / GROUPS, NT><<<grid, threads, 0, stream>>>(p); break;
+    case 128: k_delta_step<VW, CBL, 128 / GROUPS, NT><<<grid, threads, 0, stream>>>(p); break;
+    default: k_delta_step<VW, CBL, 256 / GROUPS, NT><<<grid, threads, 0, stream>>>(p); break;
     }
     return hipGetLastError();
 }
@@ -154,18 +161,23 @@ hipError_t launch(const DeltaStepParams& p, hipStream_t stream)
 }  // namespace
 
 // A workgroup takes as many of a head's columns as it has, 128 at most: whole
-// rows of 512 bytes, and one sum over the rows for all of them (128 sequences of
-// 32 heads of 128 x 128: 91 us, 5.82 TB/s, against 109 us with 32 columns; four
-// tokens for 64 of them 68 against 109; 16 sequences 14.1 against 17.6; 64 x 64
-// heads with their 64 columns 17.5 against 25.2 with 32 and 40.5 with 128). With
-// fewer heads than compute units it takes 32, which spreads them over more (one
-// sequence of 32 heads 6.1 us against 8.6).
+// rows of 512 bytes, and one sum over the rows for all of them (16 sequences of
+// 32 heads of 128 x 128: 14.1 us against 17.6 us with 32 columns; four tokens for
+// 64 of them 68 against 109; 64 x 64 heads with their 64 columns 17.5 against
+// 25.2 with 32 and 40.5 with 128). With fewer heads than compute units it takes
+// 32, which spreads them over more (one sequence of 32 heads 6.1 us against 8.6).
+// States of 128 MB and more, half of the last-level cache, will not be there at
+// the next step, with a model's other layers in between: they go past it (128
+// sequences, three pools in turn: 105 us, 5.0 TB/s, against 117 us).
 hipError_t launch_delta_step(const DeltaStepParams& p, bool vec4, hipStream_t stream)
 {
-    constexpr int64_t kComputeUnits = 256;
+    constexpr int64_t kComputeUnits = 256, kPast = (int64_t)128 << 20;
+    const int64_t heads = p.n_seqs * p.heads_v;
     if (!vec4) return launch<1, 32>(p, stream);
-    if (p.dim_v <= 32 || p.n_seqs * p.heads_v < kComputeUnits) return launch<4, 8>(p, stream);
-    return p.dim_v <= 64 ? launch<4, 16>(p, stream) : launch<4, 32>(p, stream);
+    if (p.dim_v <= 32 || heads < kComputeUnits) return launch<4, 8>(p, stream);
+    const bool past = heads * p.dim_k * p.dim_v * 4 >= kPast;
+    if (p.dim_v <= 64) return past ? launch<4, 16, true>(p, stream) : launch<4, 16>(p, stream);
+    return past ? launch<4, 32, true>(p, stream) : launch<4, 32>(p, stream);
 }
 
 }  // namespace dws

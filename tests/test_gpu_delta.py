@@ -327,6 +327,25 @@ def test_step(gpu, n, tokens, hk, hv, dk, dv, dtype):
     assert torch.equal(again, pool[slots.long()])
 
 
+@pytest.mark.parametrize("dv", [64, 128])
+def test_step_of_a_large_batch(gpu, dv):
+    """States of more than 128 MB, which are read and written past the caches."""
+    n, hv, dk = 1100 * 64 // dv, 2, 256
+    assert n * hv * dk * dv * 4 >= 128 << 20
+    x, offsets, _ = inputs(22, [2] * n, 1, hv, dk, dv, BF16, init=False)
+    gen = torch.Generator(device="cuda").manual_seed(5)
+    pool = 0.3 * torch.randn(n + 1, hv, dk, dv, device="cuda", generator=gen)
+    first = pool.clone()
+    slots = torch.arange(n, 0, -1, dtype=torch.int32, device="cuda")
+    out = dws.delta_rule_step(*(x[a] for a in NAMES), pool, slots=slots)
+    assert torch.equal(pool[0], first[0])
+    for i in (0, 1, n // 2, n - 1):
+        y = {a: x[a][2 * i: 2 * i + 2] for a in NAMES}
+        want, final = reference(*(y[a] for a in NAMES), [0, 2], first[n - i: n - i + 1].double().cpu(), 1 / 16)
+        close(out[2 * i: 2 * i + 2], want, BF16, "out")
+        close(pool[n - i: n - i + 1], final, FP32, "state")
+
+
 @pytest.mark.parametrize("whole", [False, True])
 def test_slots_that_leave_sequences_out(gpu, whole):
     """A slot below 0, outside the pool or named before: the sequence's rows and the states stay as they were."""
