@@ -93,7 +93,7 @@ class DeltaRuleArgs(ctypes.Structure):
                 [(x, ctypes.c_void_p) for x in ("d_initial_state", "d_final_state", "d_slots")] +
                 [("n_states", ctypes.c_longlong), ("out_grad", Rows), ("d_final_grad", ctypes.c_void_p)] +
                 [(x, Rows) for x in ("q_grad", "k_grad", "v_grad", "g_grad", "beta_grad")] +
-                [("d_initial_grad", ctypes.c_void_p), ("zero_tail", ctypes.c_int), ("d_workspace", ctypes.c_void_p),
+                [("d_initial_grad", ctypes.c_void_p), ("zero_rest", ctypes.c_int), ("d_workspace", ctypes.c_void_p),
                  ("workspace_bytes", ctypes.c_size_t)])
 
 
@@ -593,7 +593,7 @@ def run_length_encode(keys, unique_keys=None, lengths=None, count=None, stream=N
 # each member starts in the list of values:
 _DELTA = struct.Struct("@qqPiiiiiiif" + 6 * "Pqq" + "PPPq" + "Pqq" + "P" + 5 * "Pqq" + "PiPQ")
 (_N_SEQS, _OFFSETS, _G_DTYPE, _Q, _K, _V, _G, _BETA, _OUT, _INITIAL, _FINAL, _SLOTS, _N_STATES, _OUT_GRAD, _FINAL_GRAD,
- _Q_GRAD, _K_GRAD, _V_GRAD, _G_GRAD, _BETA_GRAD, _INITIAL_GRAD, _ZERO_TAIL, _WORKSPACE) = (
+ _Q_GRAD, _K_GRAD, _V_GRAD, _G_GRAD, _BETA_GRAD, _INITIAL_GRAD, _ZERO_REST, _WORKSPACE) = (
     1, 2, 8, 11, 14, 17, 20, 23, 26, 29, 30, 31, 32, 33, 36, 37, 40, 43, 46, 49, 52, 53, 54)
 
 _float_codes = {}
@@ -722,7 +722,7 @@ def delta_rule(q, k, v, g, beta, offsets=None, initial_state=None, final_state=N
     (n, heads_v, dim_k, dim_v) or None for zero. final_state: None, a tensor like it to write (may be initial_state),
     or True for a new one. slots: int32 GPU tensor of n places when the states are a pool (count, heads_v, dim_k,
     dim_v); sequences with a place below 0, outside the pool or named before are left out. scale: dim_k^-0.5 by
-    default. Rows of ``out`` behind the last sequence stay as they were, and are 0 in a new one.
+    default. Rows of ``out`` in no sequence stay as they were, and are 0 in a new one.
     Returns out, or (out, final_state) when the final state is asked for."""
     import torch
     a, device = _delta_args(q, k, v, g, beta, offsets, 1, scale)
@@ -737,7 +737,7 @@ def delta_rule(q, k, v, g, beta, offsets=None, initial_state=None, final_state=N
         if out is None:
             # a sequence that is left out keeps its rows: 0 in a new tensor
             out = (torch.empty if slots is None else torch.zeros)(v.shape, dtype=q.dtype, device=device)
-            a[_ZERO_TAIL] = int(offsets is not None)
+            a[_ZERO_REST] = int(offsets is not None)
         a[_OUT: _OUT + 3] = _rows(out, "out", v.shape, q.dtype, device)
         if final_state is True:
             final_state = torch.empty((n_seqs, *state_shape), dtype=torch.float32, device=device)
@@ -756,7 +756,7 @@ def delta_rule_backward(d_out, q, k, v, g, beta, offsets=None, initial_state=Non
                         stream=None):
     """Gradients of delta_rule (dws_delta_rule_backward): the arguments of the forward call and the gradient(s) of its
     result(s). Returns (dq, dk, dv, dg, dbeta, d_initial_state) in the type of q, dg None without g and
-    d_initial_state None without initial_state; rows behind the last sequence are 0."""
+    d_initial_state None without initial_state; rows in no sequence are 0."""
     import torch
     a, device = _delta_args(q, k, v, g, beta, offsets, 1, scale)
     a[_OUT_GRAD: _OUT_GRAD + 3] = _rows(d_out, "d_out", v.shape, q.dtype, device)
@@ -774,7 +774,7 @@ def delta_rule_backward(d_out, q, k, v, g, beta, offsets=None, initial_state=Non
         d_initial = None if initial_state is None else torch.empty(initial_state.shape, dtype=q.dtype, device=device)
         if d_initial is not None:
             a[_INITIAL_GRAD] = d_initial.data_ptr()
-        a[_ZERO_TAIL] = int(offsets is not None)
+        a[_ZERO_REST] = int(offsets is not None)
         work = _delta_workspace(a, 1, device)
         _check(load_library().dws_delta_rule_backward(_DELTA.pack(*a), s), "dws_delta_rule_backward")
         del work

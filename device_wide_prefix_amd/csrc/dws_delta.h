@@ -46,7 +46,7 @@ struct DeltaParams {
     DeltaRows d_out, dq, dk, dv, dg, dbeta;
     const float* d_final;
     void* d_initial;
-    int zero_tail;               // zero the output rows behind the last sequence
+    int zero_rest;               // zero the output rows in no sequence
     // workspace
     int64_t n_slots;             // chunk slots: tokens / chunk + n_seqs + 1 (the last ones empty)
     float* w_gate;               // [slot][head][5][chunk]: gate factors (kGateArrays in the kernels)

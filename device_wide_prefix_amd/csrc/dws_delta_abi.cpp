@@ -243,7 +243,7 @@ dws_status forward_entry(const dws_delta_rule_args* a, hipStream_t stream)
     p.final_state = a->d_final_state;
     p.slots = a->d_slots;
     p.n_states = states;
-    p.zero_tail = a->zero_tail;
+    p.zero_rest = a->zero_rest;
     p.n_slots = z.n_slots;
     char* w = static_cast<char*>(a->d_workspace);
     p.w_gate = reinterpret_cast<float*>(w + z.gate);
@@ -281,6 +281,8 @@ dws_status backward_entry(const dws_delta_rule_args* a, hipStream_t stream)
         st = r.add(a->d_initial_grad, state_bytes(a, a->n_seqs, e), true, e);
     if (st != DWS_OK) return st;
     const Sizes z = workspace_of(a, true, false);
+    // the gradients' workgroups have up to 512 threads
+    if ((uint64_t)z.n_slots * (uint64_t)a->heads_qk > kMaxThreads / 512) return DWS_ERR_UNSUPPORTED;
     if (a->d_workspace == nullptr || a->workspace_bytes < z.bytes) return DWS_ERR_INVALID_ARG;
     if ((st = r.add(a->d_workspace, z.bytes, true, 256)) != DWS_OK) return st;
     if (r.overlap()) return DWS_ERR_OVERLAP;
@@ -288,7 +290,7 @@ dws_status backward_entry(const dws_delta_rule_args* a, hipStream_t stream)
     p.initial = a->d_initial_state;
     p.d_final = a->d_final_grad;
     p.d_initial = a->d_initial_grad;
-    p.zero_tail = a->zero_tail;
+    p.zero_rest = a->zero_rest;
     p.n_slots = z.n_slots;
     char* w = static_cast<char*>(a->d_workspace);
     p.w_gate = reinterpret_cast<float*>(w + z.gate);

@@ -19,8 +19,7 @@
 namespace dws {
 
 // Waves a SIMD: the kernels' LDS allows no more workgroups, so the compiler may
-// as well use all 512 (or 256) registers to have reads in flight.
-#define DWS_ONE_WAVE __attribute__((amdgpu_waves_per_eu(1, 1)))
+// as well use all 256 registers to have reads in flight.
 #define DWS_TWO_WAVES __attribute__((amdgpu_waves_per_eu(2, 2)))
 
 typedef float f32x4 __attribute__((ext_vector_type(4)));
@@ -88,13 +87,6 @@ __device__ __forceinline__ f32x4 mma(const Parts<T, NA>& a, const Parts<T, NB>& 
 #pragma unroll
         for (int i = 0; i < NA; ++i)
             if (s - i >= 0 && s - i < NB) c = mma(a.p[i], b.p[s - i], c);
-    return c;
-}
-template <class T, int NP>
-__device__ __forceinline__ f32x4 mma(Vec8<T> a, const Parts<T, NP>& b, f32x4 c)
-{
-#pragma unroll
-    for (int n = NP - 1; n >= 0; --n) c = mma(a, b.p[n], c);
     return c;
 }
 
@@ -197,17 +189,6 @@ __device__ __forceinline__ void store_parts4(T* at, int64_t step, f32x4 x)
         if (n + 1 < NP) x -= __builtin_convertvector(y, f32x4);
     }
 }
-// x as NP parts, `step` elements apart.
-template <int NP, class T>
-__device__ __forceinline__ void store_parts(T* at, int64_t step, float x)
-{
-#pragma unroll
-    for (int n = 0; n < NP; ++n) {
-        const T y = (T)x;
-        at[n * step] = y;
-        x -= (float)y;
-    }
-}
 
 // ---- global memory --------------------------------------------------------
 
@@ -219,8 +200,8 @@ __device__ __forceinline__ float load_gate(const DeltaRows& r, int64_t token, in
     return (float)static_cast<const f16_t*>(r.data)[at];
 }
 
-// A log decay below -104 gives a factor below the least fp32 number whatever
-// it is multiplied with, so it is taken as -104: sums of a chunk's decays and
+// A log decay below -104 gives a factor that fp32 rounds to 0 (e^-104 is less
+// than half its least number), so it is taken as -104: sums of a chunk's decays and
 // their differences then stay finite for -infinity too. NaN stays NaN.
 __device__ __forceinline__ float clamp_decay(float g) { return g < -104.f ? -104.f : g; }
 

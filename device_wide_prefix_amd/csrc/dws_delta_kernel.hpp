@@ -239,19 +239,23 @@ __global__ __launch_bounds__((kChunk<T, DK> * 4)) void k_delta_prep(DeltaParams 
     const int h = blockIdx.x % p.heads_v, hk = h / (p.heads_v / p.heads_qk);
     const SlotInfo info = slot_info<C>(p.offsets, p.tokens, p.n_seqs, slot, lane);
     if (info.rows == 0) {
-        if (p.zero_tail && info.beyond >= 0 && h == 0) {
+        if (p.zero_rest && info.beyond >= 0 && h == 0) {
             const int64_t begin = seq_begin(p.offsets, p.tokens, p.n_seqs, info.seq);
             const int64_t len = seq_length(p.offsets, p.tokens, p.n_seqs, info.seq, begin);
             const int64_t spare = p.n_slots - first_slot(begin, info.seq, C) - (len + C - 1) / C;
-            const int64_t first = begin + len + info.beyond * C, step = spare * C;
+            const int64_t head = seq_begin(p.offsets, p.tokens, p.n_seqs, 0), at = info.beyond * C, step = spare * C;
+            auto zero = [&](const DeltaRows& r, int heads, int dim) {
+                zero_rows<T>(r, begin + len + at, p.tokens, step, C, heads, dim, tid, THREADS);
+                zero_rows<T>(r, at, head, step, C, heads, dim, tid, THREADS);
+            };
             if constexpr (BWD) {
-                zero_rows<T>(p.dq, first, p.tokens, step, C, p.heads_qk, p.dim_k, tid, THREADS);
-                zero_rows<T>(p.dk, first, p.tokens, step, C, p.heads_qk, p.dim_k, tid, THREADS);
-                zero_rows<T>(p.dv, first, p.tokens, step, C, p.heads_v, p.dim_v, tid, THREADS);
-                zero_rows<T>(p.dg, first, p.tokens, step, C, p.heads_v, 1, tid, THREADS);
-                zero_rows<T>(p.dbeta, first, p.tokens, step, C, p.heads_v, 1, tid, THREADS);
+                zero(p.dq, p.heads_qk, p.dim_k);
+                zero(p.dk, p.heads_qk, p.dim_k);
+                zero(p.dv, p.heads_v, p.dim_v);
+                zero(p.dg, p.heads_v, 1);
+                zero(p.dbeta, p.heads_v, 1);
             } else {
-                zero_rows<T>(p.out, first, p.tokens, step, C, p.heads_v, p.dim_v, tid, THREADS);
+                zero(p.out, p.heads_v, p.dim_v);
             }
         }
         return;
@@ -1051,7 +1055,7 @@ __global__ __launch_bounds__((GradLds<T, DK>::THREADS)) DWS_TWO_WAVES void k_del
                 const Parts<T, 1> b = {{frag_tr(st, LS, 0, key0 + t * 16, lane)}};
                 const Parts<T, 1> d = {{frag_tr(dst, LS, 0, key0 + t * 16, lane)}};
                 os[t] = mma(ao, b, os[t]);
-                zs[t] = mma(az.p[0], b, zs[t]);
+                zs[t] = mma(az.p[0], b.p[0], zs[t]);
                 us[t] = mma(au, d, us[t]);
                 if (t % NB == tile)
 #pragma unroll

@@ -528,7 +528,8 @@ dws_status dws_reduce_op(const void* d_in, size_t n, dws_dtype dtype, dws_op op,
 
 /* A (tokens, heads, dim) array on the device: element (t, h, d) is at
  * t * token_stride + h * head_stride + d (strides in elements, not negative;
- * below 2^22 between tokens and 2^40 between heads). Inputs may repeat elements (a stride of 0); outputs may not. */
+ * below 2^22 between tokens, at most 2^40 between heads). Inputs may repeat
+ * elements (a stride of 0); outputs may not. */
 typedef struct dws_rows {
     void* data;
     long long token_stride;
@@ -557,7 +558,8 @@ typedef struct dws_rows {
  * the states stay as they were.
  *
  * With DWS_FLOAT16 the operands of the matrix products, states among them, are
- * rounded to fp16 and must stay below 65504.
+ * rounded to fp16: they must stay below 65504, and below 2^-14 they lose digits
+ * (gradients of a sum that is far smaller than that want scaling up).
  */
 typedef struct dws_delta_rule_args {
     long long tokens, n_seqs;
@@ -577,9 +579,9 @@ typedef struct dws_delta_rule_args {
     const float* d_final_grad;          /* in; NULL: zero */
     dws_rows q_grad, k_grad, v_grad, g_grad, beta_grad;   /* out; g_grad.data may be NULL */
     void* d_initial_grad;               /* out, dtype; NULL: not wanted */
-    /* != 0: rows of out (of the gradients) behind the last sequence become 0
-     * instead of staying as they were */
-    int zero_tail;
+    /* != 0: rows of out (of the gradients) in no sequence, before the first or
+     * behind the last, become 0 instead of staying as they were */
+    int zero_rest;
     void* d_workspace;                  /* DEVICE, 256-byte aligned */
     size_t workspace_bytes;
 } dws_delta_rule_args;
@@ -603,9 +605,9 @@ dws_status dws_delta_rule_workspace(const dws_delta_rule_args* args, int backwar
  * strides or types out of range, heads_v not a multiple of heads_qk, tokens not
  * a multiple of n_seqs without d_offsets, a workspace that is too small, or an
  * output that names an element twice give DWS_ERR_INVALID_ARG; a dimension above
- * 256, a token stride of 2^22 or more chunks and heads than a launch holds,
- * DWS_ERR_UNSUPPORTED; a
- * pointer not aligned to its element, DWS_ERR_MISALIGNED; an output or the
+ * 256, a token stride of 2^22 or more, or more chunks and heads than a launch
+ * holds, DWS_ERR_UNSUPPORTED; a pointer not aligned to its element,
+ * DWS_ERR_MISALIGNED; an output or the
  * workspace whose range meets another operand's, DWS_ERR_OVERLAP. Asynchronous on
  * `stream`, allocates nothing, may be captured.
  */

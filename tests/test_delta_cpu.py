@@ -137,7 +137,7 @@ def test_packed_arguments_are_the_structure():
     a = [0] * 56
     places = {"n_seqs": dws._N_SEQS, "d_offsets": dws._OFFSETS, "g_dtype": dws._G_DTYPE, "d_initial_state": dws._INITIAL,
               "d_final_state": dws._FINAL, "d_slots": dws._SLOTS, "n_states": dws._N_STATES, "d_final_grad": dws._FINAL_GRAD,
-              "d_initial_grad": dws._INITIAL_GRAD, "zero_tail": dws._ZERO_TAIL, "d_workspace": dws._WORKSPACE,
+              "d_initial_grad": dws._INITIAL_GRAD, "zero_rest": dws._ZERO_REST, "d_workspace": dws._WORKSPACE,
               "workspace_bytes": dws._WORKSPACE + 1, "tokens": 0, "heads_qk": 3, "heads_v": 4, "dim_k": 5, "dim_v": 6,
               "dtype": 7, "beta_dtype": 9, "scale": 10}
     rows = {"q": dws._Q, "k": dws._K, "v": dws._V, "g": dws._G, "beta": dws._BETA, "out": dws._OUT, "out_grad": dws._OUT_GRAD,

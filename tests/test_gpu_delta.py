@@ -277,6 +277,36 @@ def test_rows_behind_the_last_sequence(gpu, dtype, tail):
     assert (out[10:] == 5).all()
 
 
+@pytest.mark.parametrize("dtype", [FP32, BF16])
+@pytest.mark.parametrize("head,lens,tail", [(1, [10], 0), (65, [10, 70], 3), (200, [0], 0), (130, [3, 0], 70)])
+def test_rows_before_the_first_sequence(gpu, dtype, head, lens, tail):
+    """As those behind the last one."""
+    x, offsets, initial = inputs(23, lens, 1, 2, 32, 24, dtype, tail=head + tail)
+    offsets += head
+    end = head + sum(lens)
+    for a in NAMES:
+        x[a][:head] = x[a][end:] = float("nan")
+    want, final = reference(*(x[a][head:end] for a in NAMES), [i - head for i in offsets.tolist()], initial.double().cpu(), 32 ** -0.5)
+    out = torch.full(x["v"].shape, 5.0, dtype=dtype, device="cuda")
+    _, state = forward(x, offsets, initial, out=out, final_state=True)
+    close(out[head:end], want, dtype, "out")
+    close(state, final, dtype, "state")
+    assert (out[:head] == 5).all() and (out[end:] == 5).all()
+
+    def rest_is_zero(a):
+        return torch.isfinite(a).all() and (a[:head] == 0).all() and (a[end:] == 0).all()
+
+    dirty = [torch.full_like(x[a], float("nan")) for a in NAMES]      # what new tensors find in their memory
+    del dirty
+    assert rest_is_zero(forward(x, offsets, initial))
+    d_out = torch.full(x["v"].shape, float("nan"), dtype=dtype, device="cuda")
+    d_out[head:end] = 1
+    dirty = [torch.full_like(x[a], float("nan")) for a in NAMES]
+    del dirty
+    got = dws.delta_rule_backward(d_out, *(x[a] for a in NAMES), offsets=offsets, initial_state=initial)
+    assert all(rest_is_zero(a) for a in got[:5])
+
+
 def test_empty_calls(gpu):
     x, offsets, initial = inputs(11, [0, 0], 1, 2, 32, 24, BF16)
     out, state = forward(x, offsets, initial, final_state=True)
