@@ -614,26 +614,18 @@ __device__ __forceinline__ void delta_scan(const DeltaParams& p, uint32_t block,
 
     f32x4 s[NK];
     load_state<DK>(s, p.initial ? p.initial + state_at : nullptr, p.dim_k, p.dim_v, col, gq);
+    Parts<T, NP> sb[DK / 32];
+#pragma unroll
+    for (int kb = 0; kb < DK / 32; ++kb) sb[kb] = parts_of<T, NP>(s[2 * kb], s[2 * kb + 1]);
     for (int c = 0; c < chunks; ++c) {
         char* buffer = smem + (c & 1) * L::buffer;
         const T* ks = reinterpret_cast<const T*>(buffer + L::ks);
         const T* ts = reinterpret_cast<const T*>(buffer + L::ts);
         const T* vs = reinterpret_cast<const T*>(buffer + L::vs);
         const float* gate = reinterpret_cast<const float*>(buffer + L::gate);
-        Parts<T, NP> sb[DK / 32];
-#pragma unroll
-        for (int kb = 0; kb < DK / 32; ++kb) sb[kb] = parts_of<T, NP>(s[2 * kb], s[2 * kb + 1]);
         if constexpr (STORE)
             store_columns<T, DK>(static_cast<T*>(p.w_s) + place_at(c) * DK * p.dv_pad, s, col, p.dv_pad, gq);
         __syncthreads();
-        if constexpr (!STORE) {
-            T* sx = reinterpret_cast<T*>(buffer + L::sx) + (wave * 16 + lr) * LK + gq * 4;
-#pragma unroll
-            for (int kb = 0; kb < DK / 32; ++kb) {
-                *reinterpret_cast<Vec4<T>*>(sx + kb * 32) = __builtin_shufflevector(sb[kb].p[0], sb[kb].p[0], 0, 1, 2, 3);
-                *reinterpret_cast<Vec4<T>*>(sx + kb * 32 + 16) = __builtin_shufflevector(sb[kb].p[0], sb[kb].p[0], 4, 5, 6, 7);
-            }
-        }
         // X = V - diag(e^G) K S
         f32x4 x[NB] = {};
 #pragma unroll
@@ -642,6 +634,14 @@ __device__ __forceinline__ void delta_scan(const DeltaParams& p, uint32_t block,
 #pragma unroll
             for (int mt = 0; mt < NB; ++mt) a[mt].p[0] = frag_acc(ks, LK, mt * 16, kb * 32, lane);
             mma_each(a, sb[kb], x);
+        }
+        if constexpr (!STORE) {
+            T* sx = reinterpret_cast<T*>(buffer + L::sx) + (wave * 16 + lr) * LK + gq * 4;
+#pragma unroll
+            for (int kb = 0; kb < DK / 32; ++kb) {
+                *reinterpret_cast<Vec4<T>*>(sx + kb * 32) = __builtin_shufflevector(sb[kb].p[0], sb[kb].p[0], 0, 1, 2, 3);
+                *reinterpret_cast<Vec4<T>*>(sx + kb * 32 + 16) = __builtin_shufflevector(sb[kb].p[0], sb[kb].p[0], 4, 5, 6, 7);
+            }
         }
 #pragma unroll
         for (int mt = 0; mt < NB; ++mt) {
@@ -687,6 +687,10 @@ __device__ __forceinline__ void delta_scan(const DeltaParams& p, uint32_t block,
                 mma_each(a, ub, acc);
 #pragma unroll
                 for (int t = 0; t < 4; ++t) s[t0 + t] = acc[t];
+                // the next chunk's operands, while the other tiles' products run
+                if (kb == C / 32 - 1)
+#pragma unroll
+                    for (int t = 0; t < 4; t += 2) sb[(t0 + t) / 2] = parts_of<T, NP>(s[t0 + t], s[t0 + t + 1]);
             }
         }
     }
