@@ -54,10 +54,11 @@ struct DeltaParams {
     void* w_t;                   // [slot][head][parts][frags]: (I + L diag(beta))^-1
     void* w_p;                   // [slot][head][fine][frags]: P (forward), its transpose (backward)
     void* w_tt;                  // [slot][head][fine][frags]: transpose of (I + diag(beta) L)^-1 (backward)
-    void* w_s;                   // [slot][head][dv_pad][padded dim_k]: states at the chunks' starts
-    void* w_u;                   // [slot][head][fine][dv_pad][chunk]: U'
-    void* w_z;                   // [slot][head][fine][dv_pad][chunk]: Z
-    void* w_ds;                  // [slot][head][dv_pad][padded dim_k]: state gradients at the chunks' ends
+    // 16 columns of the value head after the other (store_columns in the kernels)
+    void* w_s;                   // [slot][head][dv_pad / 16][16 x padded dim_k]: states at the chunks' starts
+    void* w_u;                   // [slot][head][fine][dv_pad / 16][16 x chunk]: U'
+    void* w_z;                   // [slot][head][fine][dv_pad / 16][16 x chunk]: Z
+    void* w_ds;                  // [slot][head][dv_pad / 16][16 x padded dim_k]: state gradients at the chunks' ends
 };
 
 // Arrays that are copied to the workspace first, since their rows are not whole

@@ -268,6 +268,24 @@ struct TileRegs {
             if (ALL % THREADS == 0 || u < ALL) *reinterpret_cast<VecT*>(tile + r * stride + c) = x[i];
         }
     }
+    // ROWS columns of COLS elements, 16 at a time as the lanes of a scan wave
+    // hold them, to a row for each
+    __device__ __forceinline__ void store_columns(T* tile, int stride, int tid) const
+    {
+        constexpr int EACH = COLS * 16 / (64 * V);       // units of a lane
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const int u = tid + i * THREADS, lane = u % 64, t = u / 64 % EACH, group = u / 64 / EACH;
+            if (ALL % THREADS != 0 && u >= ALL) break;
+            T* to = tile + (group * 16 + lane % 16) * stride + t * (V * 4) + lane / 16 * 4;
+            if constexpr (V == 8) {
+                *reinterpret_cast<Vec4<T>*>(to) = __builtin_shufflevector(x[i], x[i], 0, 1, 2, 3);
+                *reinterpret_cast<Vec4<T>*>(to + 16) = __builtin_shufflevector(x[i], x[i], 4, 5, 6, 7);
+            } else {
+                *reinterpret_cast<VecT*>(to) = x[i];
+            }
+        }
+    }
 };
 // 8 elements as an operand.
 template <class T>

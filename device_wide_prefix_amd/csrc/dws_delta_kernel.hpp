@@ -453,23 +453,27 @@ __device__ __forceinline__ void store_state(const f32x4 (&s)[DK / 16], T* state,
             buffer_store<T>(rsrc, col < dim_v && row < dim_k ? (row * dim_v + col) * (int)sizeof(T) : kOutside, (T)s[t][r]);
         }
 }
-// A state for the workspace, transposed: rows of DK, one a column of the value head.
-template <class T, int DK>
-__device__ __forceinline__ void store_columns(T* at, const f32x4 (&s)[DK / 16], int col, int dv_pad, int gq)
+// Sixteen columns of R rows, laid out as results, in the workspace: 16 bytes a
+// lane after the other, as the lanes hold them (TileRegs::store_columns puts
+// them in order), so that every store is of whole lines. With a row for each
+// column, 16 lines a store and a quarter of each, the stores were half of a
+// chunk's time in the backward scan.
+template <class T, int NP, int R>
+__device__ __forceinline__ void store_columns(T* at, int64_t part, const Parts<T, NP> (&x)[R / 32], int group, int lane)
 {
-    if (col >= dv_pad) return;
-    T* to = at + col * DK + gq * 4;
+    T* to = at + (int64_t)group * 16 * R + lane * (16 / (int)sizeof(T));
 #pragma unroll
-    for (int t = 0; t < DK / 16; ++t) *reinterpret_cast<Vec4<T>*>(to + t * 16) = __builtin_convertvector(s[t], Vec4<T>);
-}
-template <class T, int NF, int C>
-__device__ __forceinline__ void store_columns(T* at, const f32x4 (&u)[C / 16], int col, int dv_pad, int gq)
-{
-    if (col >= dv_pad) return;
+    for (int n = 0; n < NP; ++n)
 #pragma unroll
-    for (int mt = 0; mt < C / 16; ++mt) store_parts4<NF>(at + col * C + mt * 16 + gq * 4, (int64_t)C * dv_pad, u[mt]);
+        for (int t = 0; t < R / 32; ++t) {
+            if constexpr (sizeof(T) == 2) {
+                *reinterpret_cast<Vec8<T>*>(to + n * part + t * 512) = x[t].p[n];
+            } else {
+                *reinterpret_cast<Vec4<T>*>(to + t * 512) = __builtin_shufflevector(x[t].p[n], x[t].p[n], 0, 1, 2, 3);
+                *reinterpret_cast<Vec4<T>*>(to + t * 512 + 256) = __builtin_shufflevector(x[t].p[n], x[t].p[n], 4, 5, 6, 7);
+            }
+        }
 }
-
 
 // STORE: instead of the outputs, the states at the chunks' starts and U' go to
 // the workspace (for the backward pass). NP: parts of the operands the state
@@ -624,7 +628,8 @@ __device__ __forceinline__ void delta_scan(const DeltaParams& p, uint32_t block,
         const T* vs = reinterpret_cast<const T*>(buffer + L::vs);
         const float* gate = reinterpret_cast<const float*>(buffer + L::gate);
         if constexpr (STORE)
-            store_columns<T, DK>(static_cast<T*>(p.w_s) + place_at(c) * DK * p.dv_pad, s, col, p.dv_pad, gq);
+            if (col0 < p.dv_pad)
+                store_columns<T, NP, DK>(static_cast<T*>(p.w_s) + place_at(c) * DK * p.dv_pad, 0, sb, col0 / 16, lane);
         __syncthreads();
         // X = V - diag(e^G) K S
         f32x4 x[NB] = {};
@@ -658,7 +663,13 @@ __device__ __forceinline__ void delta_scan(const DeltaParams& p, uint32_t block,
             mma_each(a, parts_of<T, NX>(x[2 * kb], x[2 * kb + 1]), u, 2 * kb);
         }
         if constexpr (STORE)
-            store_columns<T, NF, C>(static_cast<T*>(p.w_u) + place_at(c) * NF * C * p.dv_pad, u, col, p.dv_pad, gq);
+            if (col0 < p.dv_pad) {
+                Parts<T, NF> up[C / 32];
+#pragma unroll
+                for (int kb = 0; kb < C / 32; ++kb) up[kb] = parts_of<T, NF>(u[2 * kb], u[2 * kb + 1]);
+                store_columns<T, NF, C>(static_cast<T*>(p.w_u) + place_at(c) * NF * C * p.dv_pad, (int64_t)C * p.dv_pad, up,
+                                        col0 / 16, lane);
+            }
 #pragma unroll
         for (int mt = 0; mt < NB; ++mt) u[mt] *= gate4(gate, 2 * C + mt * 16 + gq * 4);
         if constexpr (!STORE) {
@@ -722,7 +733,7 @@ __device__ __forceinline__ void delta_scan_back(const DeltaParams& p, uint32_t b
     if (!scan_place<C, NW>(p, block, &w)) return;
     const int64_t state_at = (w.seq * p.heads_v + w.h) * p.dim_k * p.dim_v;
     const int chunks = (int)((w.len + C - 1) / C);
-    const int col = w.first + wave * 16 + lr;
+    const int col0 = w.first + wave * 16, col = col0 + lr;
     auto rows_at = [&](int c) { return w.len - (int64_t)c * C < C ? (int)(w.len - (int64_t)c * C) : C; };
     auto place_at = [&](int c) { return (w.slot0 + c) * p.heads_v + w.h; };
 
@@ -778,10 +789,11 @@ __device__ __forceinline__ void delta_scan_back(const DeltaParams& p, uint32_t b
         const T* os = reinterpret_cast<const T*>(buffer + L::vs);
         const float* gate = reinterpret_cast<const float*>(buffer + L::gate);
         const int64_t at = place_at(c);
-        store_columns<T, DK>(static_cast<T*>(p.w_ds) + at * DK * p.dv_pad, ds, col, p.dv_pad, gq);
         Parts<T, 1> db[DK / 32];
 #pragma unroll
         for (int kb = 0; kb < DK / 32; ++kb) db[kb] = parts_of<T, 1>(ds[2 * kb], ds[2 * kb + 1]);
+        if (col0 < p.dv_pad)
+            store_columns<T, 1, DK>(static_cast<T*>(p.w_ds) + at * DK * p.dv_pad, 0, db, col0 / 16, lane);
         __syncthreads();
         // dU; dO is exact in T
         Vec4<T> d_o[NB];
@@ -813,7 +825,12 @@ __device__ __forceinline__ void delta_scan_back(const DeltaParams& p, uint32_t b
             for (int mt = 0; mt < 2 * kb + 2; ++mt) a[mt] = parts_at<NF>(ts, F::elems, F::upper(mt, kb), lane);
             mma_each(a, parts_of<T, NF>(z[2 * kb], z[2 * kb + 1]), y, 0, 2 * kb + 2);
         }
-        store_columns<T, NF, C>(static_cast<T*>(p.w_z) + at * NF * C * p.dv_pad, y, col, p.dv_pad, gq);
+        if (col0 < p.dv_pad) {
+            Parts<T, NF> zp[C / 32];
+#pragma unroll
+            for (int kb = 0; kb < C / 32; ++kb) zp[kb] = parts_of<T, NF>(y[2 * kb], y[2 * kb + 1]);
+            store_columns<T, NF, C>(static_cast<T*>(p.w_z) + at * NF * C * p.dv_pad, (int64_t)C * p.dv_pad, zp, col0 / 16, lane);
+        }
         f32x4 e[NB];
 #pragma unroll
         for (int mt = 0; mt < NB; ++mt) {
@@ -885,8 +902,8 @@ __global__ __launch_bounds__(NW * 128) DWS_TWO_WAVES void k_delta_scan_both(Delt
 // One workgroup for each (chunk slot, query/key head). A wave owns a row tile
 // of 16 tokens and 64 of the key columns; the value heads
 // that share the key head come in turn, so that their sums need no atomics and
-// have one order. The workspace's arrays have a row a value column: blocks of 32
-// go through LDS, where the transposing reads make operands of them.
+// have one order. Blocks of 32 value columns of the workspace's arrays go through
+// LDS, a row a column, where the transposing reads make operands of them.
 
 template <class T, int DK>
 struct GradLds {
@@ -1014,12 +1031,12 @@ __global__ __launch_bounds__((GradLds<T, DK>::THREADS)) DWS_TWO_WAVES void k_del
         for (int c = 0; c < p.dv_pad; c += 32) {
             Parts<T, 1> ao;
             ao.p[0] = __builtin_shufflevector(oa, ob, 0, 1, 2, 3, 4, 5, 6, 7);
-            sr.store(st, LS, tid);
-            dsr.store(dst, LS, tid);
+            sr.store_columns(st, LS, tid);
+            dsr.store_columns(dst, LS, tid);
 #pragma unroll
             for (int n = 0; n < NF; ++n) {
-                ur[n].store(ut + n * 32 * LC, LC, tid);
-                zr[n].store(zt + n * 32 * LC, LC, tid);
+                ur[n].store_columns(ut + n * 32 * LC, LC, tid);
+                zr[n].store_columns(zt + n * 32 * LC, LC, tid);
             }
             __syncthreads();
             if (c + 32 < p.dv_pad)
