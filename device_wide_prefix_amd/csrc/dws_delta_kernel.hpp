@@ -616,6 +616,7 @@ __device__ __forceinline__ void delta_scan(const DeltaParams& p, uint32_t block,
         return;
     }
 
+    __builtin_amdgcn_s_setprio(2);
     f32x4 s[NK];
     load_state<DK>(s, p.initial ? p.initial + state_at : nullptr, p.dim_k, p.dim_v, col, gq);
     Parts<T, NP> sb[DK / 32];
@@ -778,6 +779,7 @@ __device__ __forceinline__ void delta_scan_back(const DeltaParams& p, uint32_t b
         return;
     }
 
+    __builtin_amdgcn_s_setprio(2);
     f32x4 ds[NK];
     load_state<DK>(ds, p.d_final ? p.d_final + state_at : nullptr, p.dim_k, p.dim_v, col, gq);
     for (int c = chunks - 1; c >= 0; --c) {
