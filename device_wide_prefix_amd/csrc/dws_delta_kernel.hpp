@@ -544,26 +544,43 @@ __device__ __forceinline__ void delta_scan(const DeltaParams& p, uint32_t block,
                     const T* sx = reinterpret_cast<const T*>(buffer + L::sx);
                     const T* ux = reinterpret_cast<const T*>(buffer + L::ux);
                     f32x4 o[CT][MT] = {};
+                    // reads of the next products' operands ahead of the products
+                    Parts<T, 1> sa[2][CT];
+                    Parts<T, NF> ua[2][CT];
+                    auto read_s = [&](int kb) {
 #pragma unroll
-                    for (int kb = 0; kb < DK / 32; ++kb)
+                        for (int ct = 0; ct < CT; ++ct) sa[kb % 2][ct].p[0] = frag_nat(sx, LK, (ct0 + ct) * 16, kb * 32, lane);
+                    };
+                    auto read_u = [&](int kb) {
 #pragma unroll
                         for (int ct = 0; ct < CT; ++ct)
-                            mma_each<true>(qf[kb], Parts<T, 1>{{frag_nat(sx, LK, (ct0 + ct) * 16, kb * 32, lane)}}, o[ct]);
+#pragma unroll
+                            for (int n = 0; n < NF; ++n)
+                                ua[kb % 2][ct].p[n] = frag_nat(ux + n * NW * 16 * LC, LC, (ct0 + ct) * 16, kb * 32, lane);
+                    };
+                    read_s(0);
+#pragma unroll
+                    for (int kb = 0; kb < DK / 32; ++kb) {
+                        if (kb + 1 < DK / 32)
+                            read_s(kb + 1);
+                        else
+                            read_u(0);
+                        if constexpr (MT == 1) __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+                        for (int ct = 0; ct < CT; ++ct) mma_each<true>(qf[kb], sa[kb % 2][ct], o[ct]);
+                        if constexpr (MT == 1) __builtin_amdgcn_sched_barrier(0);
+                    }
 #pragma unroll
                     for (int ct = 0; ct < CT; ++ct)
 #pragma unroll
                         for (int m = 0; m < MT; ++m) o[ct][m] *= p.scale * eg[m];
 #pragma unroll
                     for (int kb = 0; kb < C / 32; ++kb) {
-                        if (2 * kb > mt0 + MT - 1) continue;       // P is lower triangular
+                        if (kb + 1 < C / 32) read_u(kb + 1);
+                        if constexpr (MT == 1) __builtin_amdgcn_sched_barrier(0);
+                        if (2 * kb <= mt0 + MT - 1)       // P is lower triangular
 #pragma unroll
-                        for (int ct = 0; ct < CT; ++ct) {
-                            Parts<T, NF> ub;
-#pragma unroll
-                            for (int n = 0; n < NF; ++n)
-                                ub.p[n] = frag_nat(ux + n * NW * 16 * LC, LC, (ct0 + ct) * 16, kb * 32, lane);
-                            mma_each<true>(pf[kb], ub, o[ct]);
-                        }
+                            for (int ct = 0; ct < CT; ++ct) mma_each<true>(pf[kb], ua[kb % 2][ct], o[ct]);
                     }
                     const int rows = rows_at(c - 1);
                     T* o0 = static_cast<T*>(p.out.data) + (w.begin + (int64_t)(c - 1) * C) * p.out.ts + w.h * p.out.hs;
