@@ -498,7 +498,10 @@ __device__ __forceinline__ void delta_scan(const DeltaParams& p, uint32_t block,
     auto place_at = [&](int c) { return (w.slot0 + c) * p.heads_v + w.h; };
 
     if (__builtin_amdgcn_readfirstlane(threadIdx.x) >= THREADS) {
-        // tiles and outputs
+        // tiles and outputs, which the other waves wait for at the barrier: first
+        // on their SIMDs (packed prompts 440 us without, 428 with; the other way
+        // round 460). The backward scan has no outputs here, and its states first.
+        __builtin_amdgcn_s_setprio(2);
         const int tid = threadIdx.x - THREADS;
         const T* k0 = static_cast<const T*>(p.k.data) + w.begin * p.k.ts + w.hk * p.k.hs;
         const T* q0 = static_cast<const T*>(p.q.data) + w.begin * p.q.ts + w.hk * p.q.hs;
@@ -633,7 +636,6 @@ __device__ __forceinline__ void delta_scan(const DeltaParams& p, uint32_t block,
         return;
     }
 
-    __builtin_amdgcn_s_setprio(2);
     f32x4 s[NK];
     load_state<DK>(s, p.initial ? p.initial + state_at : nullptr, p.dim_k, p.dim_v, col, gq);
     Parts<T, NP> sb[DK / 32];
@@ -651,12 +653,18 @@ __device__ __forceinline__ void delta_scan(const DeltaParams& p, uint32_t block,
         __syncthreads();
         // X = V - diag(e^G) K S
         f32x4 x[NB] = {};
+        Parts<T, 1> ka[2][NB];
+        auto read_k = [&](int kb) {
+#pragma unroll
+            for (int mt = 0; mt < NB; ++mt) ka[kb % 2][mt].p[0] = frag_acc(ks, LK, mt * 16, kb * 32, lane);
+        };
+        read_k(0);
 #pragma unroll
         for (int kb = 0; kb < DK / 32; ++kb) {
-            Parts<T, 1> a[NB];
-#pragma unroll
-            for (int mt = 0; mt < NB; ++mt) a[mt].p[0] = frag_acc(ks, LK, mt * 16, kb * 32, lane);
-            mma_each(a, sb[kb], x);
+            if (kb + 1 < DK / 32) read_k(kb + 1);
+            __builtin_amdgcn_sched_barrier(0);
+            mma_each(ka[kb % 2], sb[kb], x);
+            __builtin_amdgcn_sched_barrier(0);
         }
         if constexpr (!STORE) {
             T* sx = reinterpret_cast<T*>(buffer + L::sx) + (wave * 16 + lr) * LK + gq * 4;
@@ -1281,9 +1289,12 @@ inline uint64_t scan_blocks(const DeltaParams& p, int waves)
     const uint64_t groups = ((uint64_t)p.n_seqs * p.heads_v + 7) / 8 * 8;
     return groups * parts;
 }
-// 16-column waves of a scan workgroup: four share a chunk's tiles. Two where
-// four would leave compute units without a workgroup, and for fp32 heads above
-// 128, whose tiles and states leave LDS for no more.
+// 16-column waves of a scan workgroup: four share a chunk's tiles. Two, whose
+// chunks take less time, as long as every workgroup still has a compute unit to
+// itself: 8,192 tokens of 64 heads of 128 x 128 forward in 386 us with two and 440
+// with four, of 72 heads 651 and 474; backward 711 and 787 with 32 heads, 1,136 and
+// 1,020 with 48. And two for fp32 heads above 128, whose tiles and states leave
+// LDS for no more.
 template <class T, int DK>
 constexpr int kMostWaves = sizeof(T) == 4 && DK > 128 ? 2 : 4;
 constexpr uint64_t kComputeUnits = 256;
@@ -1310,7 +1321,7 @@ hipError_t forward_dk(const DeltaParams& p, hipStream_t stream)
     const hipError_t e = launch_lds(k_delta_prep<T, DK, NP, false>, (uint64_t)p.n_slots * p.heads_v, C * 4,
                                     PrepLds<T, DK>::bytes, p, stream);
     if (e != hipSuccess) return e;
-    if (scan_blocks(p, 4) < kComputeUnits) return launch_scan<T, DK, NP, 2>(p, stream);
+    if (scan_blocks(p, 2) <= kComputeUnits) return launch_scan<T, DK, NP, 2>(p, stream);
     return launch_scan<T, DK, NP, kMostWaves<T, DK>>(p, stream);
 }
 template <class T, int NP>
@@ -1332,7 +1343,7 @@ hipError_t backward_dk(const DeltaParams& p, hipStream_t stream)
     hipError_t e = launch_lds(k_delta_prep<T, DK, 1, true>, (uint64_t)p.n_slots * p.heads_v, C * 4,
                               PrepLds<T, DK>::bytes, p, stream);
     if (e != hipSuccess) return e;
-    e = 2 * scan_blocks(p, 4) < kComputeUnits ? launch_both<T, DK, 2>(p, stream)
+    e = 2 * scan_blocks(p, 2) <= kComputeUnits ? launch_both<T, DK, 2>(p, stream)
                                               : launch_both<T, DK, kMostWaves<T, DK>>(p, stream);
     if (e != hipSuccess) return e;
     return launch_lds(k_delta_grad<T, DK>, (uint64_t)p.n_slots * p.heads_qk, GradLds<T, DK>::THREADS,

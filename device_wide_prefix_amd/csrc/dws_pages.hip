@@ -223,10 +223,13 @@ __global__ __launch_bounds__(kThreads) void k_pages_apply(PageCache c, PageReque
 }
 
 // All three steps in one workgroup, with LDS in the place of the workspace: a
-// small cache's pass over the counts takes less than two more launches (a fork
-// of 4 rows over 509 pages: 57 us with three launches, %SMALL% us with one).
+// small cache's pass over the counts takes less than two more launches. Growing 4
+// rows of 64 entries over 512 pages 5.5 us against 11.6 us, 128 of 32 over 8,192
+// pages 9.4 against 13.5; but 32 of 1,024, which want more than one compute unit,
+// 23.3 against 14.2. (Compaction of the three caches: 4.1 and 9.1, 11.6 and 12.1,
+// 20.0 and 11.9 us.)
 constexpr int kSmallPages = 8192, kSmallRows = 4096;
-constexpr int64_t kSmallEntries = 65536;      // table entries
+constexpr int64_t kSmallEntries = 8192;       // table entries
 template <bool FORK>
 __global__ __launch_bounds__(kPlanThreads) void k_pages_small(PageCache c, PageRequests r)
 {
@@ -305,8 +308,9 @@ __global__ __launch_bounds__(kThreads) void k_pages_free(PageCache c, PageFree f
     if (threadIdx.x == 0 && n > 0) atomicAdd(reinterpret_cast<unsigned long long*>(f.freed), (unsigned long long)n);
 }
 
-// Both steps in one workgroup, for few entries.
-constexpr int64_t kSmallFree = 16384;
+// Both steps in one workgroup, for few entries (16 rows of 32: 2.1 us against
+// 3.8 us with two launches; 32 rows of 128: 6.8 against 4.3).
+constexpr int64_t kSmallFree = 1024;
 __global__ __launch_bounds__(kPlanThreads) void k_pages_free_small(PageCache c, PageFree f)
 {
     __shared__ int part[kPlanThreads / 64], lengths[kPlanThreads];
