@@ -557,6 +557,11 @@ typedef struct dws_rows {
  * or named by an earlier sequence of the call is left out: its rows of out and
  * the states stay as they were.
  *
+ * An input that is not finite stays in its sequence and in the heads that use it;
+ * there dws_delta_rule gives unspecified values from the first token of its chunk
+ * on, at most 63 tokens before it (a zero above a matrix's diagonal times infinity
+ * is not zero), and dws_delta_rule_step from its token on.
+ *
  * With DWS_FLOAT16 the operands of the matrix products, states among them, are
  * rounded to fp16: they must stay below 65504, and below 2^-14 they lose digits
  * (gradients of a sum that is far smaller than that want scaling up).

@@ -307,6 +307,34 @@ def test_rows_before_the_first_sequence(gpu, dtype, head, lens, tail):
     assert all(rest_is_zero(a) for a in got[:5])
 
 
+@pytest.mark.parametrize("dtype", [FP32, BF16])
+@pytest.mark.parametrize("what", ["q", "k", "v", "g", "beta"])
+@pytest.mark.parametrize("value", ["nan", "inf"])
+def test_what_is_not_finite_stays_in_its_sequence_and_head(gpu, dtype, what, value):
+    """One bad element of one head: other sequences, heads and earlier chunks give the same bits."""
+    lens, at = [200, 70, 130], 200 + 69          # the second sequence's last token but one
+    x, offsets, initial = inputs(24, lens + [64], 2, 2, 64, 48, dtype)
+    d_out = torch.randn(x["v"].shape, generator=torch.Generator().manual_seed(6)).to(dtype).cuda()
+
+    def run():
+        out, state = forward(x, offsets, initial, final_state=True)
+        grads = dws.delta_rule_backward(d_out, *(x[a] for a in NAMES), offsets=offsets, initial_state=initial)
+        torch.cuda.synchronize()
+        return out, state, grads
+    good = run()
+    x[what][(at, 1) if what in ("g", "beta") else (at, 1, 5)] = float(value)
+    bad = run()
+    keep = torch.ones(x["v"].shape[0], dtype=torch.bool, device="cuda")
+    keep[200:270] = False
+    for a, b in zip((good[0], *good[2][:5]), (bad[0], *bad[2][:5])):
+        assert torch.equal(a[keep], b[keep]) and torch.equal(a[:, 0], b[:, 0])
+    for a, b in ((good[1], bad[1]), (good[2][5], bad[2][5])):
+        assert torch.equal(a[[0, 2, 3]], b[[0, 2, 3]]) and torch.equal(a[1, 0], b[1, 0])
+    chunk = 32 if dtype == FP32 else 64
+    assert torch.equal(good[0][200: 200 + 69 // chunk * chunk], bad[0][200: 200 + 69 // chunk * chunk])
+    assert not torch.isfinite(bad[0][at, 1]).all() or (what in ("k", "g", "beta") and not torch.isfinite(bad[1][1, 1]).all())
+
+
 def test_empty_calls(gpu):
     x, offsets, initial = inputs(11, [0, 0], 1, 2, 32, 24, BF16)
     out, state = forward(x, offsets, initial, final_state=True)
