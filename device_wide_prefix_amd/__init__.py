@@ -182,7 +182,8 @@ def load_library():
         f = getattr(lib, name)
         f.argtypes = [vp, vp]
         f.restype = ci
-    pc, ll = ctypes.POINTER(PageCache), ctypes.c_longlong
+    # (dws_page_cache likewise: a PageCache or its bytes)
+    pc, ll = vp, ctypes.c_longlong
     for name, args in (("workspace", [pc, ll, ctypes.POINTER(sz)]), ("grow", [pc, vp, vp, ll, vp, vp, sz, vp]),
                        ("fork", [pc, vp, vp, ll, vp, vp, vp, vp, vp, sz, vp]), ("free", [pc, vp, ll, vp, vp, sz, vp]),
                        ("compact", [pc, vp, vp, vp, vp, vp, vp, sz, vp]),
@@ -599,6 +600,16 @@ _DELTA = struct.Struct("@qqPiiiiiiif" + 6 * "Pqq" + "PPPq" + "Pqq" + "P" + 5 * "
 _float_codes = {}
 
 
+def _int32():
+    import torch
+    return torch.int32
+
+
+def _int64():
+    import torch
+    return torch.int64
+
+
 def _float_code(dtype, what) -> int:
     if not _float_codes:
         import torch
@@ -617,36 +628,41 @@ def _gpu_tensor(t, what):
 
 def _rows(t, what, shape, dtype, device):
     """dws_rows of t: (tokens, heads, dim), or (tokens, heads) with dtype None."""
+    try:
+        if t.shape == shape and t.device == device and (dtype is None or t.dtype == dtype):
+            strides = t.stride()
+            if len(strides) == 2 or strides[2] == 1 or shape[2] <= 1 or not t.numel():
+                return t.data_ptr(), strides[0], strides[1]
+            raise ValueError(f"{what} must be contiguous in its last dimension")
+    except AttributeError:
+        pass
     _gpu_tensor(t, what)
-    if t.shape != shape or t.device != device or (dtype is not None and t.dtype != dtype):
-        raise ValueError(f"{what} must have shape {tuple(shape)}" + (f", dtype {dtype}" if dtype is not None else "") +
-                         f" and be on {device}, got {tuple(t.shape)}, {t.dtype} on {t.device}")
-    strides = t.stride()
-    if len(strides) == 3 and strides[2] != 1 and shape[2] > 1 and t.numel():
-        raise ValueError(f"{what} must be contiguous in its last dimension")
-    return t.data_ptr(), strides[0], strides[1]
+    raise ValueError(f"{what} must have shape {tuple(shape)}" + (f", dtype {dtype}" if dtype is not None else "") +
+                     f" and be on {device}, got {tuple(t.shape)}, {t.dtype} on {t.device}")
 
 
 def _device_ints(t, what, dtype, n, device):
-    import torch
-    if not isinstance(t, torch.Tensor) or t.dtype != dtype or t.device != device or not t.is_contiguous() or \
-            t.dim() != 1 or (n is not None and t.shape[0] != n):
-        raise ValueError(f"{what} must be a contiguous one-dimensional {dtype} tensor on {device}" +
-                         (f" of {n} elements" if n is not None else ""))
-    return t.data_ptr()
+    try:
+        if t.dtype == dtype and t.device == device and t.dim() == 1 and (n is None or t.shape[0] == n) and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    raise ValueError(f"{what} must be a contiguous one-dimensional {dtype} tensor on {device}" +
+                     (f" of {n} elements" if n is not None else ""))
 
 
 def _state_ptr(t, what, count, shape, device):
-    import torch
-    if not isinstance(t, torch.Tensor) or t.dtype != torch.float32 or t.device != device or not t.is_contiguous() or \
-            t.dim() != 4 or t.shape[1:] != shape or (count is not None and t.shape[0] != count):
-        raise ValueError(f"{what} must be a contiguous float32 tensor {('count' if count is None else count, *shape)} on {device}")
-    return t.data_ptr()
+    try:
+        if t.dim() == 4 and _float_code(t.dtype, what) == FLOAT32 and t.shape[1:] == shape and t.device == device and \
+                (count is None or t.shape[0] == count) and t.is_contiguous():
+            return t.data_ptr()
+    except (AttributeError, TypeError):
+        pass
+    raise ValueError(f"{what} must be a contiguous float32 tensor {('count' if count is None else count, *shape)} on {device}")
 
 
 def _delta_args(q, k, v, g, beta, offsets, n_seqs, scale):
     """The values that all three delta-rule calls share; checks shapes, types and devices. Returns (values, device)."""
-    import torch
     _gpu_tensor(q, "q")
     _gpu_tensor(v, "v")
     if q.dim() != 3 or v.dim() != 3:
@@ -658,7 +674,7 @@ def _delta_args(q, k, v, g, beta, offsets, n_seqs, scale):
     gates = (tokens, heads_v)
     a = [0] * 56
     if offsets is not None:
-        a[_OFFSETS] = _device_ints(offsets, "offsets", torch.int64, None, device)
+        a[_OFFSETS] = _device_ints(offsets, "offsets", _int64(), None, device)
         n_seqs = offsets.shape[0] - 1
     if g is not None:
         a[_G: _G + 3] = _rows(g, "g", gates, None, device)
@@ -683,10 +699,13 @@ class _on_stream:
     def __enter__(self):
         import torch
         device = self.x.device
-        if self.given is None and device.index == torch.cuda.current_device():
-            # the handle alone: current_stream() would make a Stream object, as much time as a launch takes
-            raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-            return raw(device.index) if raw is not None else torch.cuda.current_stream().cuda_stream
+        if self.given is None:
+            try:
+                # the handle alone: current_stream() would make a Stream object, as much time as a launch takes
+                if device.index == torch._C._cuda_getDevice():
+                    return torch._C._cuda_getCurrentRawStream(device.index)
+            except AttributeError:      # another version of torch
+                pass
         current = int(torch.cuda.current_stream(device).cuda_stream)
         handle = current if self.given is None else int(self.given)
         self.contexts = (torch.cuda.device(device),)
@@ -809,24 +828,29 @@ def delta_rule_step(q, k, v, g, beta, state, slots=None, offsets=None, scale=Non
 
 # ---- pages of a cache --------------------------------------------------------
 
-def _page_cache(refs, table, lengths=None, page_tokens=0) -> PageCache:
-    import torch
+_PAGES = struct.Struct("@PqPqqPq")      # dws_page_cache
+
+
+def _page_cache(refs, table, lengths=None, page_tokens=0):
+    """dws_page_cache, packed; and the number of pages."""
     _gpu_tensor(refs, "refs")
-    c = PageCache(d_refs=_device_ints(refs, "refs", torch.int32, None, refs.device), n_pages=refs.numel(),
-                  page_tokens=int(page_tokens))
-    if not isinstance(table, torch.Tensor) or table.dtype != torch.int32 or table.dim() != 2 or \
-            table.device != refs.device or not table.is_contiguous():
-        raise ValueError(f"table must be a contiguous int32 tensor (rows, pages) on {refs.device}")
-    c.d_table, (c.n_rows, c.max_pages) = table.data_ptr(), table.shape
-    if lengths is not None:
-        c.d_lengths = _device_ints(lengths, "lengths", torch.int32, table.shape[0], refs.device)
-    return c
+    device, int32 = refs.device, refs.dtype
+    pages, at = refs.shape[0] if refs.dim() else 0, _device_ints(refs, "refs", _int32(), None, device)
+    try:
+        ok = table.dtype == int32 and table.dim() == 2 and table.device == device and table.is_contiguous()
+    except AttributeError:
+        ok = False
+    if not ok:
+        raise ValueError(f"table must be a contiguous int32 tensor (rows, pages) on {device}")
+    rows, most = table.shape
+    held = 0 if lengths is None else _device_ints(lengths, "lengths", int32, rows, device)
+    return _PAGES.pack(at, pages, table.data_ptr(), rows, most, held, int(page_tokens)), pages
 
 
 def _page_workspace(c, n, device):
     import torch
     need = ctypes.c_size_t(0)
-    _check(load_library().dws_pages_workspace(ctypes.byref(c), n, ctypes.byref(need)), "dws_pages_workspace")
+    _check(load_library().dws_pages_workspace(c, n, ctypes.byref(need)), "dws_pages_workspace")
     return torch.empty(need.value, dtype=torch.uint8, device=device)
 
 
@@ -840,12 +864,12 @@ def pages_grow(refs, table, lengths, rows, new_lengths, page_tokens, stream=None
     (rows, max_pages) and lengths (rows,) are int32 GPU tensors, updated in place. Returns an int32 tensor: 1 where
     granted, 0 where the row stays as it was."""
     import torch
-    c = _page_cache(refs, table, lengths, page_tokens)
+    c, _ = _page_cache(refs, table, lengths, page_tokens)
     n = rows.numel() if isinstance(rows, torch.Tensor) else 0
-    a, b = (_device_ints(t, w, torch.int32, n, refs.device) for t, w in ((rows, "rows"), (new_lengths, "new_lengths")))
+    a, b = _device_ints(rows, "rows", torch.int32, n, refs.device), _device_ints(new_lengths, "new_lengths", torch.int32, n, refs.device)
     with _on_stream(refs, stream) as s:
         granted, work = _new_ints(n, refs), _page_workspace(c, n, refs.device)
-        _check(load_library().dws_pages_grow(ctypes.byref(c), a, b, n, granted.data_ptr(), work.data_ptr(), work.numel(), s),
+        _check(load_library().dws_pages_grow(c, a, b, n, granted.data_ptr(), work.data_ptr(), work.numel(), s),
                "dws_pages_grow")
     return granted
 
@@ -855,13 +879,13 @@ def pages_fork(refs, table, lengths, parents, children, page_tokens, stream=None
     (dws_pages_fork). Returns (granted, src, dst, count): the pages to copy are src[:count] to dst[:count], count an
     int64 GPU tensor, for pages_copy on each pool."""
     import torch
-    c = _page_cache(refs, table, lengths, page_tokens)
+    c, _ = _page_cache(refs, table, lengths, page_tokens)
     n = parents.numel() if isinstance(parents, torch.Tensor) else 0
-    a, b = (_device_ints(t, w, torch.int32, n, refs.device) for t, w in ((parents, "parents"), (children, "children")))
+    a, b = _device_ints(parents, "parents", torch.int32, n, refs.device), _device_ints(children, "children", torch.int32, n, refs.device)
     with _on_stream(refs, stream) as s:
         granted, src, dst = _new_ints((3, n), refs).unbind(0)
         count, work = _new_ints(1, refs, torch.int64), _page_workspace(c, n, refs.device)
-        _check(load_library().dws_pages_fork(ctypes.byref(c), a, b, n, granted.data_ptr(), src.data_ptr(), dst.data_ptr(),
+        _check(load_library().dws_pages_fork(c, a, b, n, granted.data_ptr(), src.data_ptr(), dst.data_ptr(),
                                              count.data_ptr(), work.data_ptr(), work.numel(), s), "dws_pages_fork")
     return granted, src, dst, count
 
@@ -869,12 +893,12 @@ def pages_fork(refs, table, lengths, parents, children, page_tokens, stream=None
 def pages_free(refs, table, lengths, rows, page_tokens, stream=None):
     """Empties ``rows`` (dws_pages_free). Returns the number of pages that became free, a one-element int64 GPU tensor."""
     import torch
-    c = _page_cache(refs, table, lengths, page_tokens)
+    c, _ = _page_cache(refs, table, lengths, page_tokens)
     a = _device_ints(rows, "rows", torch.int32, None, refs.device)
     n = rows.numel()
     with _on_stream(refs, stream) as s:
         freed, work = _new_ints(1, refs, torch.int64), _page_workspace(c, n, refs.device)
-        _check(load_library().dws_pages_free(ctypes.byref(c), a, n, freed.data_ptr(), work.data_ptr(), work.numel(), s),
+        _check(load_library().dws_pages_free(c, a, n, freed.data_ptr(), work.data_ptr(), work.numel(), s),
                "dws_pages_free")
     return freed
 
@@ -884,14 +908,14 @@ def pages_compact(refs, table, stream=None):
     Returns (count, remap, src, dst, moves): pages in use, new number of each page (-1: free), and the pages to copy,
     src[:moves] to dst[:moves], for pages_copy on each pool. count and moves are int64 GPU tensors."""
     import torch
-    c = _page_cache(refs, table)
+    c, pages = _page_cache(refs, table)
     with _on_stream(refs, stream) as s:
-        half = c.n_pages // 2
-        remap = _new_ints(c.n_pages, refs)
+        half = pages // 2
+        remap = _new_ints(pages, refs)
         src, dst = _new_ints((2, half), refs).unbind(0)
         moves, count = _new_ints(1, refs, torch.int64), _new_ints(1, refs, torch.int64)
         work = _page_workspace(c, 0, refs.device)
-        _check(load_library().dws_pages_compact(ctypes.byref(c), remap.data_ptr(), src.data_ptr(), dst.data_ptr(),
+        _check(load_library().dws_pages_compact(c, remap.data_ptr(), src.data_ptr(), dst.data_ptr(),
                                                 moves.data_ptr(), count.data_ptr(), work.data_ptr(), work.numel(), s),
                "dws_pages_compact")
     return count, remap, src, dst, moves
@@ -906,7 +930,8 @@ def pages_copy(pool, src, dst, count=None, page_dim=0, stream=None):
     if page_dim not in (0, 1) or pool.dim() <= page_dim or not pool.is_contiguous():
         raise ValueError("pool must be contiguous, its pages in dimension 0 or 1")
     n = src.numel() if isinstance(src, torch.Tensor) else 0
-    a, b = (_device_ints(t, w, torch.int32, n, pool.device) for t, w in ((src, "src"), (dst, "dst")))
+    device = pool.device
+    a, b = _device_ints(src, "src", torch.int32, n, device), _device_ints(dst, "dst", torch.int32, n, device)
     k = None if count is None else _device_ints(count, "count", torch.int64, 1, pool.device)
     layers, pages = (1 if page_dim == 0 else pool.shape[0]), pool.shape[page_dim]
     layer_bytes = pool.numel() * pool.element_size() // max(1, layers)

@@ -94,6 +94,12 @@ def test_refusals_of_copy(lib):
         assert call(**{"pool": None, "src": None, "dst": None, **more}) == dws.OK, more
 
 
+def test_packed_cache_is_the_structure():
+    values = [FAKE + 8 * i for i in range(7)]
+    c = dws.PageCache(*values)
+    assert dws._PAGES.size == ctypes.sizeof(c) and dws._PAGES.pack(*values) == bytes(c)
+
+
 def test_binding_refuses_cpu_tensors():
     x = torch.zeros(4, dtype=torch.int32)
     table = torch.zeros(2, 2, dtype=torch.int32)
