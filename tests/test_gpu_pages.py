@@ -298,16 +298,18 @@ def test_states_in_pages(gpu):
             assert all((o[0] == 0).all() for o in outs[10:])
 
 
-def test_graphs_and_streams(gpu):
-    """All five captured once and replayed between eager calls, from the same start each time."""
-    c = filled(13, 5000, 40, 150, 16)
+@pytest.mark.parametrize("pages,most", [(5000, 150), (9000, 300)])
+def test_graphs_and_streams(gpu, pages, most):
+    """All five captured once and replayed between eager calls, from the same start each time; in one launch each, and
+    in three."""
+    c = filled(13, pages, 40, most, 16)
     start = OnGpu(c)
     empty = [r for r in range(40) if not c.lengths[r]]
     full = [r for r in range(40) if c.lengths[r]]
     rows, new = ints(full[:8]), ints([min(2400, c.lengths[r] + 33) for r in full[:8]])
     parents, children, gone = ints(full[:len(empty)]), ints(empty), ints(full[-5:])
     gen = torch.Generator().manual_seed(1)
-    first = torch.randn(5000, 33, generator=gen).cuda()
+    first = torch.randn(pages, 33, generator=gen).cuda()
 
     def everything(work):
         refs, table, lengths, pool = work
