@@ -23,6 +23,14 @@ namespace dws {
 template <class T, int DK>
 constexpr int kChunk = sizeof(T) == 4 || DK > 128 ? 32 : 64;
 
+// Whether products with key columns behind dim_k, which are zeros, are left out:
+// for fp32, whose products take most of the time (heads of 72 x 40: 103 us with
+// them, 91 without). In 16 bits the branches cost more than they save (heads of
+// 96 x 96: 134 us with all products, 153 with branches), as they do with the
+// registers that fp32 heads above 128 take (160 x 128: 204 and 224 us).
+template <class T, int DK>
+constexpr bool kSkip = sizeof(T) == 4 && DK <= 128;
+
 // Parts of the 16-bit operands that are computed in fp32. With one part for
 // all, bf16 outputs and gradients are off by 3.3e-3 to 4.9e-3 (2-norm), twice
 // what rounding the result itself gives (1.7e-3). The arrays of a chunk's size,
@@ -312,6 +320,7 @@ __global__ __launch_bounds__((kChunk<T, DK> * 4)) void k_delta_prep(DeltaParams 
         }
 #pragma unroll
         for (int kb = 0; kb < DK / 32; ++kb) {
+            if (kSkip<T, DK> && kb * 32 >= p.dim_k) break;
             const Vec8<T> ki = frag_nat(ks, LK, it * 16, kb * 32, lane), kj = frag_nat(ks, LK, jt * 16, kb * 32, lane);
             kk = BWD ? mma(ki, kj, kk) : mma(kj, ki, kk);
             qk = BWD ? mma(qf[kb], kj, qk) : mma(kj, qf[kb], qk);
@@ -573,8 +582,9 @@ __device__ __forceinline__ void delta_scan(const DeltaParams& p, uint32_t block,
                         else
                             read_u(0);
                         if constexpr (MT == 1) __builtin_amdgcn_sched_barrier(0);
+                        if (!kSkip<T, DK> || kb * 32 < p.dim_k)
 #pragma unroll
-                        for (int ct = 0; ct < CT; ++ct) mma_each<true>(qf[kb], sa[kb % 2][ct], o[ct]);
+                            for (int ct = 0; ct < CT; ++ct) mma_each<true>(qf[kb], sa[kb % 2][ct], o[ct]);
                         if constexpr (MT == 1) __builtin_amdgcn_sched_barrier(0);
                     }
 #pragma unroll
@@ -667,7 +677,7 @@ __device__ __forceinline__ void delta_scan(const DeltaParams& p, uint32_t block,
         for (int kb = 0; kb < DK / 32; ++kb) {
             if (kb + 1 < DK / 32) read_k(kb + 1);
             __builtin_amdgcn_sched_barrier(0);
-            mma_each(ka[kb % 2], sb[kb], x);
+            if (!kSkip<T, DK> || kb * 32 < p.dim_k) mma_each(ka[kb % 2], sb[kb], x);
             __builtin_amdgcn_sched_barrier(0);
         }
         if constexpr (!STORE) {
@@ -718,6 +728,7 @@ __device__ __forceinline__ void delta_scan(const DeltaParams& p, uint32_t block,
             const Parts<T, NX> ub = parts_of<T, NX>(u[2 * kb], u[2 * kb + 1]);
 #pragma unroll
             for (int t0 = 0; t0 < NK; t0 += 4) {
+                if (kSkip<T, DK> && t0 * 16 >= p.dim_k) break;
                 Parts<T, 1> a[4];
                 f32x4 acc[4];
 #pragma unroll
@@ -838,7 +849,7 @@ __device__ __forceinline__ void delta_scan_back(const DeltaParams& p, uint32_t b
             Parts<T, 1> a[NB];
 #pragma unroll
             for (int mt = 0; mt < NB; ++mt) a[mt].p[0] = frag_acc(ks, LK, mt * 16, kb * 32, lane);
-            mma_each(a, db[kb], z);
+            if (!kSkip<T, DK> || kb * 32 < p.dim_k) mma_each(a, db[kb], z);
         }
 #pragma unroll
         for (int mt = 0; mt < NB; ++mt) z[mt] *= gate4(gate, C + mt * 16 + gq * 4);
@@ -881,6 +892,7 @@ __device__ __forceinline__ void delta_scan_back(const DeltaParams& p, uint32_t b
             const Parts<T, 1> yb = parts_of<T, 1>(y[2 * kb], y[2 * kb + 1]);
 #pragma unroll
             for (int t0 = 0; t0 < NK; t0 += 4) {
+                if (kSkip<T, DK> && t0 * 16 >= p.dim_k) break;
                 Parts<T, 1> a[4], b[4];
                 f32x4 acc[4];
 #pragma unroll
