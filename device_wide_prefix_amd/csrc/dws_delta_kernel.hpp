@@ -652,9 +652,21 @@ __device__ __forceinline__ void delta_scan(const DeltaParams& p, uint32_t block,
 
     f32x4 s[NK];
     load_state<DK>(s, p.initial ? p.initial + state_at : nullptr, p.dim_k, p.dim_v, col, gq);
-    Parts<T, NP> sb[DK / 32];
+    // Split ahead, while the last update's products run, or, where the parts would
+    // not fit the registers beside the state, when they are used.
+    constexpr bool AHEAD = NK * NP <= 32;
+    Parts<T, NP> sb[AHEAD ? DK / 32 : 1];
+    auto split = [&](int kb) {
+        if constexpr (AHEAD) sb[kb] = parts_of<T, NP>(s[2 * kb], s[2 * kb + 1]);
+    };
+    auto parts_of_state = [&](int kb) {
+        if constexpr (AHEAD)
+            return sb[kb];
+        else
+            return parts_of<T, NP>(s[2 * kb], s[2 * kb + 1]);
+    };
 #pragma unroll
-    for (int kb = 0; kb < DK / 32; ++kb) sb[kb] = parts_of<T, NP>(s[2 * kb], s[2 * kb + 1]);
+    for (int kb = 0; kb < DK / 32; ++kb) split(kb);
     for (int c = 0; c < chunks; ++c) {
         char* buffer = smem + (c & 1) * L::buffer;
         const T* ks = reinterpret_cast<const T*>(buffer + L::ks);
@@ -677,15 +689,16 @@ __device__ __forceinline__ void delta_scan(const DeltaParams& p, uint32_t block,
         for (int kb = 0; kb < DK / 32; ++kb) {
             if (kb + 1 < DK / 32) read_k(kb + 1);
             __builtin_amdgcn_sched_barrier(0);
-            if (!kSkip<T, DK> || kb * 32 < p.dim_k) mma_each(ka[kb % 2], sb[kb], x);
+            if (!kSkip<T, DK> || kb * 32 < p.dim_k) mma_each(ka[kb % 2], parts_of_state(kb), x);
             __builtin_amdgcn_sched_barrier(0);
         }
         if constexpr (!STORE) {
             T* sx = reinterpret_cast<T*>(buffer + L::sx) + (wave * 16 + lr) * LK + gq * 4;
 #pragma unroll
             for (int kb = 0; kb < DK / 32; ++kb) {
-                *reinterpret_cast<Vec4<T>*>(sx + kb * 32) = __builtin_shufflevector(sb[kb].p[0], sb[kb].p[0], 0, 1, 2, 3);
-                *reinterpret_cast<Vec4<T>*>(sx + kb * 32 + 16) = __builtin_shufflevector(sb[kb].p[0], sb[kb].p[0], 4, 5, 6, 7);
+                const Vec8<T> y = parts_of_state(kb).p[0];
+                *reinterpret_cast<Vec4<T>*>(sx + kb * 32) = __builtin_shufflevector(y, y, 0, 1, 2, 3);
+                *reinterpret_cast<Vec4<T>*>(sx + kb * 32 + 16) = __builtin_shufflevector(y, y, 4, 5, 6, 7);
             }
         }
 #pragma unroll
@@ -742,7 +755,7 @@ __device__ __forceinline__ void delta_scan(const DeltaParams& p, uint32_t block,
                 // the next chunk's operands, while the other tiles' products run
                 if (kb == C / 32 - 1)
 #pragma unroll
-                    for (int t = 0; t < 4; t += 2) sb[(t0 + t) / 2] = parts_of<T, NP>(s[t0 + t], s[t0 + t + 1]);
+                    for (int t = 0; t < 4; t += 2) split((t0 + t) / 2);
             }
         }
     }
