@@ -464,9 +464,12 @@ __global__ __launch_bounds__(kPlanThreads) void k_pages_compact_small(PageCache 
 }
 
 // One workgroup copies kSlice bytes of one page in one layer at a time, past
-// the caches: 6,000 pages of 32 KiB in two layers take 155.5 us (5.06 TB/s)
-// with non-temporal accesses, 162 us without; 8 loads in flight a thread, or
-// other grids from 1,024 workgroups up, stay within 1%.
+// the caches: 6,000 pages of 32 KiB in two layers take 155 us (5.05 TB/s), and 4%
+// more with accesses through the caches. 4,096 workgroups, a quarter as many, take
+// 1% more (again and again on the same pages, 147 us against 138), since their
+// last round leaves most compute units idle; far more than 16,384 cost where a
+// list is longer than its count (8,350 of 30,000 pairs: 103 us, 109 with 60,000).
+// 8 loads in flight a thread stay within 1%.
 constexpr int64_t kSlice = 16384;
 typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
 
@@ -560,7 +563,7 @@ hipError_t launch_pages_compact(const PageCache& c, const PageCompact& k, hipStr
 hipError_t launch_pages_copy(const PageCopy& c, hipStream_t stream)
 {
     const int64_t items = c.n * c.layers * ((c.page_bytes + kSlice - 1) / kSlice);
-    const dim3 grid(clamp_grid(items, 4096)), threads(kThreads);
+    const dim3 grid(clamp_grid(items, 16384)), threads(kThreads);
     if (c.unit == 16)
         k_pages_copy<u32x4_t><<<grid, threads, 0, stream>>>(c);
     else if (c.unit == 4)
