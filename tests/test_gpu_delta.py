@@ -434,6 +434,26 @@ def test_slots_that_leave_sequences_out(gpu, whole):
         assert torch.equal(pool[s], before[s])
 
 
+@pytest.mark.parametrize("n,most,hk,hv,dk,dv,dtype", [(50000, 4, 1, 2, 16, 16, BF16), (3000, 70, 2, 2, 96, 40, FP16),
+                                                      (1, 120000, 1, 1, 64, 64, BF16), (300, 200, 2, 4, 136, 64, FP32)])
+def test_chunks_and_steps_agree(gpu, n, most, hk, hv, dk, dv, dtype):
+    """The two forms against each other at sizes that the definition takes too long for: very many and very long
+    sequences. (As tolerance the one of two results of the type, each off by its own.)"""
+    note(f"delta chunks and steps {n} {most} {dtype}")
+    gen = torch.Generator().manual_seed(25)
+    lens = torch.randint(0, most + 1, (n,), generator=gen).tolist() if n > 1 else [most]
+    x, offsets, initial = inputs(26, lens, hk, hv, dk, dv, dtype)
+    out, final = forward(x, offsets, initial, final_state=True)
+    pool = initial.clone()
+    stepped = dws.delta_rule_step(*(x[a] for a in NAMES), pool, offsets=offsets)
+    torch.cuda.synchronize()
+    close(out, stepped, dtype, "dg")
+    close(forward(x, offsets, initial), stepped, dtype, "dg")
+    # both are off by the fp32 tolerance
+    off = (final - pool).double().norm() / pool.double().norm()
+    assert off <= 2 * tolerance(dtype, "state"), off
+
+
 def test_prefill_then_steps(gpu):
     """A prompt in two calls and tokens one by one, states in a pool, are the sequence in one."""
     lens = [150, 97]
