@@ -56,14 +56,11 @@ constexpr int kPrecise = __is_same(T, bf16_t) ? 3 : kFine<T>;
 template <int C>
 struct Triangle {
     static constexpr int frags = C == 64 ? 6 : 2, elems = frags * 512;
-    static __device__ constexpr bool in_lower(int row, int col) { return col / 32 <= row / 32; }
-    static __device__ constexpr bool in_upper(int row, int col) { return col / 32 >= row / 32; }
     // fragment (row tile mt, column block kb)
     static __device__ constexpr int lower(int mt, int kb) { return kb == 0 ? mt : 2 + mt; }
     static __device__ constexpr int upper(int mt, int kb) { return kb == 0 ? mt : 2 + mt; }
     static __device__ constexpr int acc(int row, int col) { return ((col % 16 / 4) * 16 + row % 16) * 8 + col % 32 / 16 * 4; }
     static __device__ constexpr int nat(int row, int col) { return ((col % 32 / 8) * 16 + row % 16) * 8 + col % 8; }
-    static __device__ constexpr int lower_acc(int row, int col) { return lower(row / 16, col / 32) * 512 + acc(row, col); }
     static __device__ constexpr int lower_nat(int row, int col) { return lower(row / 16, col / 32) * 512 + nat(row, col); }
     static __device__ constexpr int upper_acc(int row, int col) { return upper(row / 16, col / 32) * 512 + acc(row, col); }
 };
@@ -75,6 +72,15 @@ __device__ __forceinline__ Parts<T, NP> parts_at(const T* frags, int elems, int 
 #pragma unroll
     for (int n = 0; n < NP; ++n) a.p[n] = frag_nat(frags + n * elems + f * 512 + lane * 8, 0, 0, 0, 0);
     return a;
+}
+
+// Eight elements of a fragment as NP parts, `step` elements apart.
+template <int NP, class T>
+__device__ __forceinline__ void store_fragment(T* at, int64_t step, f32x4 lo, f32x4 hi)
+{
+    const Parts<T, NP> x = parts_of<T, NP>(lo, hi);
+#pragma unroll
+    for (int n = 0; n < NP; ++n) *reinterpret_cast<Vec8<T>*>(at + n * step) = x.p[n];
 }
 
 // ---- the inverse of a unit lower triangular matrix -----------------------
@@ -214,9 +220,10 @@ __device__ __forceinline__ int tile_row(int t) { return t < 1 ? 0 : (t < 3 ? 1 :
 
 // LDS of the preparation: the matrix that is inverted takes the place of the K
 // tile, which is done with before (Q's fragments come straight from memory).
-// 18 KB for 128 key columns, eight workgroups a compute unit; four, with Q and
-// the inverse in LDS too, measured the same, 121 to 125 us on 8,544 chunks and
-// heads with three parts of the inverse, whose 0.4 GB move at 3.3 TB/s then.
+// 18 KB for 128 key columns, seven workgroups a compute unit; four, with Q and
+// the inverse in LDS too, measured the same. 8,544 chunks and heads with three
+// parts of the inverse take 106 us: 565 MB, 5.3 TB/s (127 us when the inverse was
+// written in the order of its rows, 8 bytes to a line).
 template <class T, int DK>
 struct PrepLds {
     static constexpr int C = kChunk<T, DK>, LK = lds_stride<T>(DK), LD = inverse_stride(C);
@@ -365,10 +372,12 @@ __global__ __launch_bounds__((kChunk<T, DK> * 4)) void k_delta_prep(DeltaParams 
 
     invert_unit_lower<C>(m, tmp, wave, lane);
     T* wt = static_cast<T*>(p.w_t) + at * NX * F::elems;
-    for (int i = tid; i < C * C / 4; i += THREADS) {
-        const int row = i / (C / 4), c = i % (C / 4) * 4;
-        const float* x = m + row * LD + c;
-        if (F::in_lower(row, c)) store_parts4<NX>(wt + F::lower_acc(row, c), F::elems, f32x4{x[0], x[1], x[2], x[3]});
+    // fragment by fragment, so that a wave writes whole lines
+    for (int i = tid; i < F::frags * 64; i += THREADS) {
+        const int f = i / 64, kb = f >= NB, row = (kb ? f - 2 : f) * 16 + lr;
+        const float* x = m + row * LD + kb * 32 + gq * 4;
+        store_fragment<NX>(wt + f * 512 + lane * 8, F::elems, *reinterpret_cast<const f32x4*>(x),
+                           *reinterpret_cast<const f32x4*>(x + 16));
     }
     if constexpr (BWD) {
         // the other inverse, of I + B L
@@ -383,11 +392,11 @@ __global__ __launch_bounds__((kChunk<T, DK> * 4)) void k_delta_prep(DeltaParams 
         __syncthreads();
         invert_unit_lower<C>(m, tmp, wave, lane);
         T* wtt = static_cast<T*>(p.w_tt) + at * NF * F::elems;
-        for (int i = tid; i < C * C / 4; i += THREADS) {
-            const int row = i / (C / 4), c = i % (C / 4) * 4;       // of the transposed
-            const float* x = m + c * LD + row;
-            if (F::in_upper(row, c))
-                store_parts4<NF>(wtt + F::upper_acc(row, c), F::elems, f32x4{x[0], x[LD], x[2 * LD], x[3 * LD]});
+        for (int i = tid; i < F::frags * 64; i += THREADS) {
+            const int f = i / 64, kb = f >= 2, row = (kb ? f - 2 : f) * 16 + lr;       // of the transposed
+            const float* x = m + (kb * 32 + gq * 4) * LD + row;
+            store_fragment<NF>(wtt + f * 512 + lane * 8, F::elems, f32x4{x[0], x[LD], x[2 * LD], x[3 * LD]},
+                               f32x4{x[16 * LD], x[17 * LD], x[18 * LD], x[19 * LD]});
         }
     }
 }
