@@ -19,8 +19,11 @@ constexpr int delta_padded_v(int dim_v) { return (dim_v + 31) / 32 * 32; }
 constexpr int delta_triangle(int chunk) { return (chunk == 64 ? 6 : 2) * 512; }
 
 // Parts (numbers of the input type whose sum is the value) of the operands
-// computed in fp32: those of a chunk's size, and all that a final state depends on.
+// computed in fp32: those of a chunk's size, the states and the states' gradients
+// that the backward pass keeps, and all that a final state depends on.
 constexpr int delta_fine_parts(int dtype) { return dtype == DWS_FLOAT32 ? 1 : 2; }
+constexpr int delta_state_parts(int dtype) { return delta_fine_parts(dtype); }
+constexpr int delta_state_grad_parts(int dtype, int dim_k) { return dim_k > 128 ? delta_fine_parts(dtype) : 1; }
 constexpr int delta_precise_parts(int dtype) { return dtype == DWS_BFLOAT16 ? 3 : delta_fine_parts(dtype); }
 
 // One (tokens, heads, dim) operand: strides in elements, dim contiguous.
@@ -55,10 +58,10 @@ struct DeltaParams {
     void* w_p;                   // [slot][head][fine][frags]: P (forward), its transpose (backward)
     void* w_tt;                  // [slot][head][fine][frags]: transpose of (I + diag(beta) L)^-1 (backward)
     // 16 columns of the value head after the other (store_columns in the kernels)
-    void* w_s;                   // [slot][head][dv_pad / 16][16 x padded dim_k]: states at the chunks' starts
+    void* w_s;                   // [slot][head][state parts][dv_pad / 16][16 x padded dim_k]: states at the chunks' starts
     void* w_u;                   // [slot][head][fine][dv_pad / 16][16 x chunk]: U'
     void* w_z;                   // [slot][head][fine][dv_pad / 16][16 x chunk]: Z
-    void* w_ds;                  // [slot][head][dv_pad / 16][16 x padded dim_k]: state gradients at the chunks' ends
+    void* w_ds;                  // [slot][head][state grad parts][dv_pad / 16][16 x padded dim_k]: state gradients at the chunks' ends
 };
 
 // Arrays that are copied to the workspace first, since their rows are not whole

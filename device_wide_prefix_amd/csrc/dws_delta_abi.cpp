@@ -148,10 +148,10 @@ Sizes workspace_of(const dws_delta_rule_args* a, bool backward, bool precise)
     z.p = take(n * tri * fine);
     if (backward) {
         z.tt = take(n * tri * fine);
-        z.s = take(n * dk * dv * e);
+        z.s = take(n * dk * dv * e * (size_t)delta_state_parts(a->dtype));
         z.u = take(n * c * dv * e * fine);
         z.z = take(n * c * dv * e * fine);
-        z.ds = take(n * dk * dv * e);
+        z.ds = take(n * dk * dv * e * (size_t)delta_state_grad_parts(a->dtype, a->dim_k));
     }
     const int kinds = backward ? 4 : 3;
     for (int i = 0; i < kinds; ++i) {

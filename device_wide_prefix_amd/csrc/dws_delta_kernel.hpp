@@ -37,11 +37,22 @@ constexpr bool kSkip = sizeof(T) == 4 && DK <= 128;
 // P, X, U', Z, dU, scale e^G dO, W1 and W2, make up nearly all of that; in two
 // parts they leave at most 1.4 times the result's own rounding. So does the
 // inverse: where keys repeat, its rows subtract neighbouring tokens from each
-// other, and what is left is far smaller than its entries' rounding. S and dS,
-// which are larger and cost the most products and bytes, add 0.5 times at most
-// and keep one part.
+// other, and what is left is far smaller than its entries' rounding. S in the
+// outputs, which is larger and costs the most products, adds 0.35 times at most
+// and keeps one part.
 template <class T>
 constexpr int kFine = sizeof(T) == 4 ? 1 : 2;
+// Parts of the states (and of their gradients) in the backward pass. The decays'
+// gradients sum terms with both that cancel: in one part each, d_g was off by 1.3
+// times its own rounding at the median and 1.5 to 2.5 at the worst of 40 random
+// calls; with the states in two, at 10% of a training step's time, by 1.1 and 1.3
+// for heads up to 128. Chunks of wider heads are half as long, so that more comes
+// through the states: with both in two parts 1.03 instead of 1.6. (Both for all
+// heads: 540 us a training step against 477.)
+template <class T>
+constexpr int kStored = kFine<T>;
+template <class T, int DK>
+constexpr int kStoredGrad = DK > 128 ? kFine<T> : 1;
 // Parts of everything that a final state depends on, for fp32 accuracy.
 template <class T>
 constexpr int kPrecise = __is_same(T, bf16_t) ? 3 : kFine<T>;
@@ -480,8 +491,8 @@ __device__ __forceinline__ void store_state(const f32x4 (&s)[DK / 16], T* state,
 // them in order), so that every store is of whole lines. With a row for each
 // column, 16 lines a store and a quarter of each, the stores were half of a
 // chunk's time in the backward scan.
-template <class T, int NP, int R>
-__device__ __forceinline__ void store_columns(T* at, int64_t part, const Parts<T, NP> (&x)[R / 32], int group, int lane)
+template <class T, int NP, int R, int NX>
+__device__ __forceinline__ void store_columns(T* at, int64_t part, const Parts<T, NX> (&x)[R / 32], int group, int lane)
 {
     T* to = at + (int64_t)group * 16 * R + lane * (16 / (int)sizeof(T));
 #pragma unroll
@@ -684,7 +695,8 @@ __device__ __forceinline__ void delta_scan(const DeltaParams& p, uint32_t block,
         const float* gate = reinterpret_cast<const float*>(buffer + L::gate);
         if constexpr (STORE)
             if (col0 < p.dv_pad)
-                store_columns<T, NP, DK>(static_cast<T*>(p.w_s) + place_at(c) * DK * p.dv_pad, 0, sb, col0 / 16, lane);
+                store_columns<T, kStored<T>, DK>(static_cast<T*>(p.w_s) + place_at(c) * kStored<T> * DK * p.dv_pad,
+                                                 (int64_t)DK * p.dv_pad, sb, col0 / 16, lane);
         __syncthreads();
         // X = V - diag(e^G) K S
         f32x4 x[NB] = {};
@@ -782,8 +794,8 @@ __device__ __forceinline__ void delta_scan(const DeltaParams& p, uint32_t block,
 // The same shape as the forward scan, from a sequence's last chunk to its
 // first. Z and dS' go to the workspace; the next kernel, which has Z by rows,
 // writes dV (16 two-byte stores a lane here were a third of a chunk's time).
-// Both scans together move 513 MB for 2,096 chunks and heads of 128 x 128 in 132
-// us, 3.9 TB/s: the memory bounds them, most of it the states and Z and U'.
+// Both scans together move 581 MB for 2,096 chunks and heads of 128 x 128 in 140
+// us, 4.2 TB/s: the memory bounds them, most of it the states and Z and U'.
 
 template <class T, int DK, int NW>
 __device__ __forceinline__ void delta_scan_back(const DeltaParams& p, uint32_t block, char* smem)
@@ -855,11 +867,12 @@ __device__ __forceinline__ void delta_scan_back(const DeltaParams& p, uint32_t b
         const T* os = reinterpret_cast<const T*>(buffer + L::vs);
         const float* gate = reinterpret_cast<const float*>(buffer + L::gate);
         const int64_t at = place_at(c);
-        Parts<T, 1> db[DK / 32];
+        Parts<T, kStoredGrad<T, DK>> db[DK / 32];
 #pragma unroll
-        for (int kb = 0; kb < DK / 32; ++kb) db[kb] = parts_of<T, 1>(ds[2 * kb], ds[2 * kb + 1]);
+        for (int kb = 0; kb < DK / 32; ++kb) db[kb] = parts_of<T, kStoredGrad<T, DK>>(ds[2 * kb], ds[2 * kb + 1]);
         if (col0 < p.dv_pad)
-            store_columns<T, 1, DK>(static_cast<T*>(p.w_ds) + at * DK * p.dv_pad, 0, db, col0 / 16, lane);
+            store_columns<T, kStoredGrad<T, DK>, DK>(static_cast<T*>(p.w_ds) + at * kStoredGrad<T, DK> * DK * p.dv_pad,
+                                             (int64_t)DK * p.dv_pad, db, col0 / 16, lane);
         __syncthreads();
         // dU; dO is exact in T
         Vec4<T> d_o[NB];
@@ -951,7 +964,7 @@ __global__ __launch_bounds__(NW * 128) DWS_TWO_WAVES void k_delta_scan_both(Delt
     if (blockIdx.x < half)
         delta_scan_back<T, DK, NW>(p, blockIdx.x, smem);
     else
-        delta_scan<T, DK, 1, true, NW>(p, blockIdx.x - half, smem);
+        delta_scan<T, DK, kStored<T>, true, NW>(p, blockIdx.x - half, smem);
 }
 
 // ---- the gradients of q, k and the gates ------------------------------------
@@ -971,20 +984,20 @@ __global__ __launch_bounds__(NW * 128) DWS_TWO_WAVES void k_delta_scan_both(Delt
 // that share the key head come in turn, so that their sums need no atomics and
 // have one order. Blocks of 32 value columns of the workspace's arrays go through
 // LDS, a row a column, where the transposing reads make operands of them. 2,096
-// chunks and value heads of 128 x 128 take 152 us: 432 MB, which would take 90, but
+// chunks and value heads of 128 x 128 take 193 us: 555 MB, which would take 115, but
 // with all 256 registers of two waves a SIMD in use one block is in flight at a
 // time, and a third of the time goes to waiting for it.
 
 template <class T, int DK>
 struct GradLds {
     static constexpr int C = kChunk<T, DK>, NB = C / 16, GROUPS = DK / 64, THREADS = NB * GROUPS * 64;
-    static constexpr int LK = lds_stride<T>(DK), LC = lds_stride<T>(C), NF = kFine<T>;
+    static constexpr int LK = lds_stride<T>(DK), LC = lds_stride<T>(C), NF = kFine<T>, NS = kStored<T>, ND = kStoredGrad<T, DK>;
     static constexpr size_t ks = 0, qs = ks + (size_t)C * LK * sizeof(T), w1 = qs + (size_t)C * LK * sizeof(T);
     static constexpr size_t w2 = w1 + (size_t)NF * C * LC * sizeof(T), w_end = w2 + (size_t)NF * C * LC * sizeof(T);
     // the blocks of 32 value columns are done with before W1 and W2 are written
     // (read transposed only: rows 32 bytes longer lie in different banks)
     static constexpr int LS = DK + 32 / (int)sizeof(T);
-    static constexpr size_t st = w1, dst = st + (size_t)32 * LS * sizeof(T), ut = dst + (size_t)32 * LS * sizeof(T);
+    static constexpr size_t st = w1, dst = st + (size_t)NS * 32 * LS * sizeof(T), ut = dst + (size_t)ND * 32 * LS * sizeof(T);
     static constexpr size_t zt = ut + (size_t)NF * 32 * LC * sizeof(T), z_end = zt + (size_t)NF * 32 * LC * sizeof(T);
     static constexpr size_t gate = w_end > z_end ? w_end : z_end;
     // floats behind: gate[5 C], row_part[GROUPS C], row_w[GROUPS C], d_beta[C], col_part[NB C], n_part[GROUPS C],
@@ -1032,7 +1045,7 @@ template <class T, int DK>
 __global__ __launch_bounds__((GradLds<T, DK>::THREADS)) DWS_TWO_WAVES void k_delta_grad(DeltaParams p)
 {
     using L = GradLds<T, DK>;
-    constexpr int C = L::C, THREADS = L::THREADS, NB = L::NB, GROUPS = L::GROUPS, LK = L::LK, LC = L::LC, LS = L::LS, NF = L::NF;
+    constexpr int C = L::C, THREADS = L::THREADS, NB = L::NB, GROUPS = L::GROUPS, LK = L::LK, LC = L::LC, LS = L::LS, NF = L::NF, NS = L::NS, ND = L::ND;
     constexpr int NK = DK / 16 / GROUPS;             // key column tiles of a wave
     constexpr int NT = NB > GROUPS ? NB / GROUPS : 1;      // its column tiles of W1 and W2: grp, grp + GROUPS, ..
     extern __shared__ __attribute__((aligned(16))) char smem[];
@@ -1060,7 +1073,7 @@ __global__ __launch_bounds__((GradLds<T, DK>::THREADS)) DWS_TWO_WAVES void k_del
     if (info.rows == 0) return;
     const int rows = info.rows;
 
-    TileRegs<T, 32, DK, THREADS> sr, dsr;
+    TileRegs<T, 32, DK, THREADS> sr[NS], dsr[ND];
     TileRegs<T, 32, C, THREADS> ur[NF], zr[NF];
     Vec4<T> oa, ob;        // dO's row lr of this wave, 32 columns in acc order
     auto load = [&](int h, int c) {
@@ -1071,8 +1084,12 @@ __global__ __launch_bounds__((GradLds<T, DK>::THREADS)) DWS_TWO_WAVES void k_del
         const bool in = row0 + lr < rows;
         oa = buffer_load<Vec4<T>>(rsrc, in && o0 < p.dim_v ? from : kOutside);
         ob = buffer_load<Vec4<T>>(rsrc, in && o0 + 16 < p.dim_v ? from + 16 * (int)sizeof(T) : kOutside);
-        sr.load(static_cast<const T*>(p.w_s) + (at * p.dv_pad + c) * DK, DK, 32, DK, tid);
-        dsr.load(static_cast<const T*>(p.w_ds) + (at * p.dv_pad + c) * DK, DK, 32, DK, tid);
+#pragma unroll
+        for (int n = 0; n < NS; ++n)
+            sr[n].load(static_cast<const T*>(p.w_s) + ((at * NS + n) * p.dv_pad + c) * DK, DK, 32, DK, tid);
+#pragma unroll
+        for (int n = 0; n < ND; ++n)
+            dsr[n].load(static_cast<const T*>(p.w_ds) + ((at * ND + n) * p.dv_pad + c) * DK, DK, 32, DK, tid);
 #pragma unroll
         for (int n = 0; n < NF; ++n) {
             ur[n].load(static_cast<const T*>(p.w_u) + ((at * NF + n) * p.dv_pad + c) * C, C, 32, C, tid);
@@ -1101,8 +1118,10 @@ __global__ __launch_bounds__((GradLds<T, DK>::THREADS)) DWS_TWO_WAVES void k_del
         for (int c = 0; c < p.dv_pad; c += 32) {
             Parts<T, 1> ao;
             ao.p[0] = __builtin_shufflevector(oa, ob, 0, 1, 2, 3, 4, 5, 6, 7);
-            sr.store_columns(st, LS, tid);
-            dsr.store_columns(dst, LS, tid);
+#pragma unroll
+            for (int n = 0; n < NS; ++n) sr[n].store_columns(st + n * 32 * LS, LS, tid);
+#pragma unroll
+            for (int n = 0; n < ND; ++n) dsr[n].store_columns(dst + n * 32 * LS, LS, tid);
 #pragma unroll
             for (int n = 0; n < NF; ++n) {
                 ur[n].store_columns(ut + n * 32 * LC, LC, tid);
@@ -1143,14 +1162,21 @@ __global__ __launch_bounds__((GradLds<T, DK>::THREADS)) DWS_TWO_WAVES void k_del
             __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
             for (int t = 0; t < NK; ++t) {
-                const Parts<T, 1> b = {{frag_tr(st, LS, 0, key0 + t * 16, lane)}};
-                const Parts<T, 1> d = {{frag_tr(dst, LS, 0, key0 + t * 16, lane)}};
+                const Parts<T, NS> b = parts_tr<NS>(st, 32 * LS, LS, 0, key0 + t * 16, lane);
+                const Parts<T, ND> d = parts_tr<ND>(dst, 32 * LS, LS, 0, key0 + t * 16, lane);
                 os[t] = mma(ao, b, os[t]);
-                zs[t] = mma(az.p[0], b.p[0], zs[t]);
+                zs[t] = mma(az, b, zs[t]);
                 us[t] = mma(au, d, us[t]);
                 if (t % NB == tile)
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) sds += (float)b.p[0][j] * (float)d.p[0][j];
+                    for (int j = 0; j < 8; ++j) {
+                        float x = 0.f, y = 0.f;
+#pragma unroll
+                        for (int n = NS - 1; n >= 0; --n) x += (float)b.p[n][j];
+#pragma unroll
+                        for (int n = ND - 1; n >= 0; --n) y += (float)d.p[n][j];
+                        sds += x * y;
+                    }
             }
             __syncthreads();
         }

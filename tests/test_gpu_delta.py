@@ -184,6 +184,21 @@ def test_special_gates(gpu, kind, dtype):
         close(a, b, dtype, what, kind)
 
 
+@pytest.mark.parametrize("dtype", [BF16, FP16])
+@pytest.mark.parametrize("lens,dk,dv", [([42, 6, 21, 14, 28, 126, 54, 8, 2, 11, 130, 94], 256, 128), ([66, 111, 28, 27, 146], 128, 104),
+                                        ([47, 189], 200, 96)])
+def test_gradients_are_near_their_own_rounding(gpu, lens, dk, dv, dtype):
+    """Beside the result's rounding, at most one of the same size on the way (an operand in one part), independent of it:
+    sqrt(2) times it, and a fifth more for sums that cancel in part."""
+    x, offsets, initial = inputs(27, lens, 1, 2, dk, dv, dtype)
+    d_out = torch.randn(x["v"].shape, generator=torch.Generator().manual_seed(3)).to(dtype).cuda()
+    got = dws.delta_rule_backward(d_out, *(x[a] for a in NAMES), offsets=offsets, initial_state=initial)
+    want = gradients(x, offsets, initial, dk ** -0.5, d_out, None)
+    for what, a, b in zip(("dq", "dk", "dv", "dg", "dbeta", "d_initial"), got, want):
+        off, rounding = (a.double().cpu() - b).norm(), (b.to(dtype).double() - b).norm()
+        assert off <= 1.2 * 2 ** 0.5 * rounding, f"{what}: off by {off / rounding:.2f} times its rounding"
+
+
 @pytest.mark.parametrize("dtype", [FP32, BF16])
 def test_gradient_against_differences(gpu, dtype):
     """The kernel's gradients along a direction against a central difference of the 64-bit definition. The difference's
