@@ -984,7 +984,7 @@ __global__ __launch_bounds__(NW * 128) DWS_TWO_WAVES void k_delta_scan_both(Delt
 // that share the key head come in turn, so that their sums need no atomics and
 // have one order. Blocks of 32 value columns of the workspace's arrays go through
 // LDS, a row a column, where the transposing reads make operands of them. 2,096
-// chunks and value heads of 128 x 128 take 193 us: 555 MB, which would take 115, but
+// chunks and value heads of 128 x 128 take 186 us: 555 MB, which would take 115, but
 // with all 256 registers of two waves a SIMD in use one block is in flight at a
 // time, and a third of the time goes to waiting for it.
 
@@ -1116,16 +1116,22 @@ __global__ __launch_bounds__((GradLds<T, DK>::THREADS)) DWS_TWO_WAVES void k_del
         f32x4 dp[NT] = {}, zu[NT] = {}, os[NK] = {}, zs[NK] = {}, us[NK] = {};
         float zdotu = 0.f, sds = 0.f;
         for (int c = 0; c < p.dv_pad; c += 32) {
+            // (made unknown, so that the loop's addresses are worked out in each
+            // turn: kept over the turns they take registers and spill, 193 us
+            // instead of 186)
+            int here = tid;
+            asm volatile("" : "+v"(here));
+            const int lane = here & 63, gq = lane >> 4, lr = lane & 15;
             Parts<T, 1> ao;
             ao.p[0] = __builtin_shufflevector(oa, ob, 0, 1, 2, 3, 4, 5, 6, 7);
 #pragma unroll
-            for (int n = 0; n < NS; ++n) sr[n].store_columns(st + n * 32 * LS, LS, tid);
+            for (int n = 0; n < NS; ++n) sr[n].store_columns(st + n * 32 * LS, LS, here);
 #pragma unroll
-            for (int n = 0; n < ND; ++n) dsr[n].store_columns(dst + n * 32 * LS, LS, tid);
+            for (int n = 0; n < ND; ++n) dsr[n].store_columns(dst + n * 32 * LS, LS, here);
 #pragma unroll
             for (int n = 0; n < NF; ++n) {
-                ur[n].store_columns(ut + n * 32 * LC, LC, tid);
-                zr[n].store_columns(zt + n * 32 * LC, LC, tid);
+                ur[n].store_columns(ut + n * 32 * LC, LC, here);
+                zr[n].store_columns(zt + n * 32 * LC, LC, here);
             }
             __syncthreads();
             if (c + 32 < p.dv_pad)
