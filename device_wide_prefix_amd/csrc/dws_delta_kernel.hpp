@@ -984,7 +984,7 @@ __global__ __launch_bounds__(NW * 128) DWS_TWO_WAVES void k_delta_scan_both(Delt
 // that share the key head come in turn, so that their sums need no atomics and
 // have one order. Blocks of 32 value columns of the workspace's arrays go through
 // LDS, a row a column, where the transposing reads make operands of them. 2,096
-// chunks and value heads of 128 x 128 take 186 us: 555 MB, which would take 115, but
+// chunks and value heads of 128 x 128 take 191 us: 555 MB, which would take 115, but
 // with all 256 registers of two waves a SIMD in use one block is in flight at a
 // time, and a third of the time goes to waiting for it.
 
@@ -1117,8 +1117,8 @@ __global__ __launch_bounds__((GradLds<T, DK>::THREADS)) DWS_TWO_WAVES void k_del
         float zdotu = 0.f, sds = 0.f;
         for (int c = 0; c < p.dv_pad; c += 32) {
             // (made unknown, so that the loop's addresses are worked out in each
-            // turn: kept over the turns they take registers and spill, 193 us
-            // instead of 186)
+            // turn: kept over the turns they take registers and spill, 196 us
+            // instead of 191)
             int here = tid;
             asm volatile("" : "+v"(here));
             const int lane = here & 63, gq = lane >> 4, lr = lane & 15;
