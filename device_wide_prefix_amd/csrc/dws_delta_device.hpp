@@ -287,14 +287,17 @@ struct TileRegs {
         }
     }
 };
-// 8 elements as an operand.
+// 8 elements as an operand, of a row that has `left` more from there on. Rows are
+// whole 16-byte units, so an fp32 row may end between the two: what lies behind it,
+// another head's elements or a gap, is not read. It would meet zeros, but
+// infinity and NaN times 0 are NaN.
 template <class T>
-__device__ __forceinline__ Vec8<T> buffer_frag(__amdgpu_buffer_rsrc_t r, int at)
+__device__ __forceinline__ Vec8<T> buffer_frag(__amdgpu_buffer_rsrc_t r, int at, int left)
 {
     if constexpr (sizeof(T) == 2) {
         return buffer_load<Vec8<T>>(r, at);
     } else {
-        const Vec4<T> a = buffer_load<Vec4<T>>(r, at), b = buffer_load<Vec4<T>>(r, at == kOutside ? at : at + 16);
+        const Vec4<T> a = buffer_load<Vec4<T>>(r, at), b = buffer_load<Vec4<T>>(r, at == kOutside || left <= 4 ? kOutside : at + 16);
         return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
     }
 }

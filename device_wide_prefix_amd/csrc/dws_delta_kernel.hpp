@@ -334,7 +334,8 @@ __global__ __launch_bounds__((kChunk<T, DK> * 4)) void k_delta_prep(DeltaParams 
 #pragma unroll
         for (int kb = 0; kb < DK / 32; ++kb) {
             const int row = it * 16 + lr, c = kb * 32 + gq * 8;
-            qf[kb] = buffer_frag<T>(q_rsrc, row < info.rows && c < p.dim_k ? (row * (int)p.q.ts + c) * (int)sizeof(T) : kOutside);
+            qf[kb] = buffer_frag<T>(q_rsrc, row < info.rows && c < p.dim_k ? (row * (int)p.q.ts + c) * (int)sizeof(T) : kOutside,
+                                    p.dim_k - c);
         }
 #pragma unroll
         for (int kb = 0; kb < DK / 32; ++kb) {
@@ -651,7 +652,8 @@ __device__ __forceinline__ void delta_scan(const DeltaParams& p, uint32_t block,
                         for (int kb = 0; kb < DK / 32; ++kb) {
                             const int k = kb * 32 + gq * 8;
                             qf[kb][m].p[0] = buffer_frag<T>(
-                                rsrc, row < rows && k < p.dim_k ? (row * (int)p.q.ts + k) * (int)sizeof(T) : kOutside);
+                                rsrc, row < rows && k < p.dim_k ? (row * (int)p.q.ts + k) * (int)sizeof(T) : kOutside,
+                                p.dim_k - k);
                         }
                         eg[m] = p.w_gate[place_at(c) * kGateArrays * C + row];
                         // (above the diagonal: not kept, and 0)

@@ -573,3 +573,41 @@ def test_graphs_and_streams(gpu):
         junk = [torch.full_like(out, 3.0) for _ in range(4)]
         side.synchronize()
         assert torch.equal(out, want[0]) and torch.equal(final, want[1]) and len(junk) == 4
+
+
+@pytest.mark.parametrize("what", ["q", "k", "v"])
+@pytest.mark.parametrize("dtype,dk,dv", [(FP32, 65, 24), (FP32, 100, 36), (FP32, 12, 4), (FP32, 36, 17), (FP32, 130, 100),
+                                         (BF16, 12, 20), (BF16, 100, 65), (FP16, 65, 36)])
+def test_heads_do_not_meet_at_their_rows_ends(gpu, what, dtype, dk, dv):
+    """Rows that end inside a fragment: the next head's first elements, infinite here, change no bit of the head before."""
+    x, offsets, initial = inputs(31, [70, 40], 2, 2, dk, dv, dtype)
+    d_out = torch.randn(x["v"].shape, generator=torch.Generator().manual_seed(6)).to(dtype).cuda()
+
+    def run():
+        out, state = forward(x, offsets, initial, final_state=True)
+        return [out, state, *dws.delta_rule_backward(d_out, *(x[a] for a in NAMES), offsets=offsets, initial_state=initial)]
+    good = run()
+    x[what][50, 1, :4] = float("inf")
+    for a, b in zip(good, run()):
+        assert torch.equal(a[:, 0], b[:, 0])
+
+
+@pytest.mark.parametrize("dtype,dk,dv", [(FP32, 100, 36), (FP32, 36, 100), (FP32, 65, 17), (BF16, 40, 104), (FP16, 100, 36)])
+def test_what_lies_between_strided_rows_is_not_used(gpu, dtype, dk, dv):
+    """Parts of buffers that hold NaN everywhere else give the bits of the arrays alone."""
+    x, offsets, initial = inputs(32, [70, 33], 2, 4, dk, dv, dtype)
+    d_out = torch.randn(x["v"].shape, generator=torch.Generator().manual_seed(6)).to(dtype).cuda()
+
+    def run(y, d):
+        out, state = forward(y, offsets, initial, final_state=True)
+        return [out, state, *dws.delta_rule_backward(d, *(y[a] for a in NAMES), offsets=offsets, initial_state=initial)]
+
+    def inside(t, gap):
+        n, heads, dim = t.shape
+        part = torch.full((n + 2, heads + 1, dim + gap), float("nan"), dtype=t.dtype, device="cuda")[1: n + 1, :heads, :dim]
+        return part.copy_(t)
+    want = run(x, d_out)
+    for gap in (16, 12, 1):          # with 16-byte units kept, kept for fp32 only, and not
+        y = dict(x, **{a: inside(x[a], gap) for a in ("q", "k", "v")})
+        for a, b in zip(run(y, inside(d_out, gap)), want):
+            assert torch.equal(a, b)
