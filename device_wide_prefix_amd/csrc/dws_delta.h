@@ -94,6 +94,7 @@ struct DeltaStepParams {
     float* state;
     const int* slots;
     int64_t n_states;
+    int zero_rest;
 };
 hipError_t launch_delta_step(const DeltaStepParams& p, bool vec4, hipStream_t stream);
 

@@ -343,6 +343,7 @@ dws_status step_entry(const dws_delta_rule_args* a, hipStream_t stream)
     p.state = a->d_final_state;
     p.slots = a->d_slots;
     p.n_states = states;
+    p.zero_rest = a->zero_rest;
     const bool vec4 = a->dim_v % 4 == 0 && (reinterpret_cast<uintptr_t>(a->d_final_state) & 15u) == 0;
     return status_of(launch_delta_step(p, vec4, stream));
 }

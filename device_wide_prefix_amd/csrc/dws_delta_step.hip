@@ -144,6 +144,19 @@ __global__ __launch_bounds__(kStepThreads) void k_delta_step(DeltaStepParams p)
     }
 }
 
+// Zeros to the rows of out before the first sequence and behind the last.
+__global__ __launch_bounds__(kStepThreads) void k_delta_step_rest(DeltaStepParams p)
+{
+    const int64_t first = seq_begin(p.offsets, p.tokens, p.n_seqs, 0), last = seq_begin(p.offsets, p.tokens, p.n_seqs, p.n_seqs - 1);
+    const int64_t end = last + seq_length(p.offsets, p.tokens, p.n_seqs, p.n_seqs - 1, last);
+    const int64_t rest = first + p.tokens - end;
+    for (int64_t r = blockIdx.x; r < rest; r += gridDim.x) {
+        const int64_t row = r < first ? r : end + (r - first);
+        for (int i = threadIdx.x; i < p.heads_v * p.dim_v; i += kStepThreads)
+            store_as(p.out.data, row * p.out.ts + i / p.dim_v * p.out.hs + i % p.dim_v, p.dtype, 0.f);
+    }
+}
+
 template <int VW, int CBL, bool NT = false>
 hipError_t launch(const DeltaStepParams& p, hipStream_t stream)
 {
@@ -171,6 +184,10 @@ hipError_t launch(const DeltaStepParams& p, hipStream_t stream)
 // sequences, three pools in turn: 105 us, 5.0 TB/s, against 117 us).
 hipError_t launch_delta_step(const DeltaStepParams& p, bool vec4, hipStream_t stream)
 {
+    if (p.zero_rest && p.offsets != nullptr) {      // equal shares leave no rows
+        k_delta_step_rest<<<dim3((uint32_t)(p.tokens < 1024 ? p.tokens : 1024)), dim3(kStepThreads), 0, stream>>>(p);
+        if (const hipError_t e = hipGetLastError(); e != hipSuccess) return e;
+    }
     constexpr int64_t kComputeUnits = 256, kPast = (int64_t)128 << 20;
     const int64_t heads = p.n_seqs * p.heads_v;
     if (!vec4) return launch<1, 32>(p, stream);

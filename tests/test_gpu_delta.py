@@ -1,4 +1,6 @@
 """The gated delta rule on the GPU against its token-by-token definition in 64 bits."""
+import ctypes
+
 import pytest
 import torch
 
@@ -611,3 +613,59 @@ def test_what_lies_between_strided_rows_is_not_used(gpu, dtype, dk, dv):
         y = dict(x, **{a: inside(x[a], gap) for a in ("q", "k", "v")})
         for a, b in zip(run(y, inside(d_out, gap)), want):
             assert torch.equal(a, b)
+
+
+CODES = {FP32: dws.FLOAT32, FP16: dws.FLOAT16, BF16: dws.BFLOAT16}
+
+
+def rows_of(t):
+    return dws.Rows(t.data_ptr(), t.stride(0), t.stride(1))
+
+
+def c_arguments(x, n_seqs, **more):
+    """dws_delta_rule_args, for what the binding does not pass."""
+    a = dws.DeltaRuleArgs()
+    a.tokens, a.heads_qk, a.dim_k = x["q"].shape
+    a.n_seqs, a.heads_v, a.dim_v = n_seqs, x["v"].shape[1], x["v"].shape[2]
+    a.dtype, a.g_dtype, a.beta_dtype = (CODES[x[b].dtype] for b in ("q", "g", "beta"))
+    a.scale = a.dim_k ** -0.5
+    for name, value in {**{b: rows_of(x[b]) for b in NAMES}, **more}.items():
+        setattr(a, name, value)
+    return a
+
+
+def c_call(name, a, backward=None):
+    """The call by its name, with a workspace of its own where one is needed (`backward` 0 or 1)."""
+    lib = dws.load_library()
+    if backward is not None:
+        need = ctypes.c_size_t(0)
+        assert lib.dws_delta_rule_workspace(ctypes.byref(a), backward, ctypes.byref(need)) == dws.OK
+        work = torch.empty(need.value, dtype=torch.uint8, device="cuda")
+        a.d_workspace, a.workspace_bytes = work.data_ptr(), need.value
+    status = getattr(lib, name)(ctypes.byref(a), torch.cuda.current_stream().cuda_stream)
+    torch.cuda.synchronize()
+    return status
+
+
+@pytest.mark.parametrize("dtype", [FP32, BF16, FP16])
+@pytest.mark.parametrize("head,lens,tail", [(0, [2, 1], 0), (3, [2, 1], 0), (0, [2, 1], 1), (70, [1, 0, 4], 1500), (5, [0], 2)])
+def test_step_clears_the_rows_in_no_sequence(gpu, dtype, head, lens, tail):
+    """zero_rest: those before the first sequence and behind the last, and no others; without it they stay."""
+    x, offsets, initial = inputs(33, lens, 1, 2, 32, 23, dtype, tail=head + tail)
+    offsets += head
+    end = head + sum(lens)
+    for a in NAMES:
+        x[a][:head] = x[a][end:] = float("nan")
+    pool = initial.clone()
+    want = dws.delta_rule_step(*(x[a] for a in NAMES), pool, offsets=offsets)
+    for rest in (1, 0):
+        state = initial.clone()
+        wide = torch.full((x["v"].shape[0] + 2, 3, 23), 5.0, dtype=dtype, device="cuda")
+        out = wide[1:-1, :2]
+        a = c_arguments(x, len(lens), out=rows_of(out), d_offsets=offsets.data_ptr(), d_initial_state=state.data_ptr(),
+                        d_final_state=state.data_ptr(), zero_rest=rest)
+        assert c_call("dws_delta_rule_step", a) == dws.OK
+        assert torch.equal(out[head:end], want[head:end]) and torch.equal(state, pool)
+        left = 0 if rest else 5
+        assert (out[:head] == left).all() and (out[end:] == left).all()
+        assert (wide[:, 2] == 5).all() and (wide[0] == 5).all() and (wide[-1] == 5).all()
