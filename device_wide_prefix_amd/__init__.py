@@ -688,6 +688,18 @@ def _delta_args(q, k, v, g, beta, offsets, n_seqs, scale):
     return a, device
 
 
+def _records_no_graph(name, *tensors):
+    """Refuses tensors whose gradients the result would silently lack."""
+    import torch
+    if not torch.is_grad_enabled():
+        return
+    for t in tensors:
+        if getattr(t, "requires_grad", False):
+            raise RuntimeError(f"{name} records no graph: call it with detached tensors or under torch.no_grad(), as the "
+                               "forward and backward of a torch.autograd.Function are; delta_rule_backward gives "
+                               "delta_rule's gradients")
+
+
 class _on_stream:
     """Make x's device current, and allocate on the stream that the call runs on: memory that is freed when the binding
     returns is then reused in that stream's order only. Gives the stream's handle."""
@@ -742,8 +754,10 @@ def delta_rule(q, k, v, g, beta, offsets=None, initial_state=None, final_state=N
     or True for a new one. slots: int32 GPU tensor of n places when the states are a pool (count, heads_v, dim_k,
     dim_v); sequences with a place below 0, outside the pool or named before are left out. scale: dim_k^-0.5 by
     default. Rows of ``out`` in no sequence stay as they were, and are 0 in a new one.
+    Records no graph: tensors that require gradients are refused unless gradients are off (torch.no_grad()).
     Returns out, or (out, final_state) when the final state is asked for."""
     import torch
+    _records_no_graph("delta_rule", q, k, v, g, beta, initial_state, final_state, out)
     a, device = _delta_args(q, k, v, g, beta, offsets, 1, scale)
     n_seqs, state_shape = a[_N_SEQS], (v.shape[1], q.shape[2], v.shape[2])
     count = n_seqs
@@ -775,7 +789,8 @@ def delta_rule_backward(d_out, q, k, v, g, beta, offsets=None, initial_state=Non
                         stream=None):
     """Gradients of delta_rule (dws_delta_rule_backward): the arguments of the forward call and the gradient(s) of its
     result(s). Returns (dq, dk, dv, dg, dbeta, d_initial_state) in the type of q, dg None without g and
-    d_initial_state None without initial_state; rows in no sequence are 0."""
+    d_initial_state None without initial_state; rows in no sequence are 0. They have no graph of their own (no second
+    derivatives)."""
     import torch
     a, device = _delta_args(q, k, v, g, beta, offsets, 1, scale)
     a[_OUT_GRAD: _OUT_GRAD + 3] = _rows(d_out, "d_out", v.shape, q.dtype, device)
@@ -806,8 +821,9 @@ def delta_rule_step(q, k, v, g, beta, state, slots=None, offsets=None, scale=Non
     state: float32 (count, heads_v, dim_k, dim_v); sequence i uses state i, or slots[i] (int32 GPU tensor; places below
     0, outside the pool or named before are left out: their rows of ``out`` and the states stay, and the rows are 0 in
     a new ``out``). The tokens are shared out evenly over the sequences, or by offsets (int64 GPU tensor, n + 1).
-    Other arguments as delta_rule. Returns out."""
+    Other arguments, and tensors that require gradients, as delta_rule. Returns out."""
     import torch
+    _records_no_graph("delta_rule_step", q, k, v, g, beta, state, out)
     if not isinstance(state, torch.Tensor) or state.dim() != 4:
         raise ValueError("state must be a (count, heads_v, dim_k, dim_v) tensor")
     n = slots.numel() if isinstance(slots, torch.Tensor) else state.shape[0]

@@ -166,6 +166,24 @@ def test_binding_refuses_cpu_tensors():
         dws.delta_rule_step(*args, initial[0])
 
 
+@pytest.mark.parametrize("name", ["delta_rule", "delta_rule_step"])
+@pytest.mark.parametrize("which", NAMES + ("state", "out"))
+def test_tensors_that_require_gradients_are_refused(name, which):
+    """A result without a graph would train nothing and say nothing. (Without the refusal these fail as CPU tensors.)"""
+    x, _, initial = inputs(1, [8], 1, 1, 16, 16, torch.float32, device="cpu")
+    x.update(state=initial, out=torch.empty_like(x["v"]))
+    x[which].requires_grad_()
+
+    def call():
+        more = {"initial_state": x["state"]} if name == "delta_rule" else {"state": x["state"]}
+        return getattr(dws, name)(*(x[a] for a in NAMES), out=x["out"], **more)
+
+    with pytest.raises(RuntimeError, match="no graph"):
+        call()
+    with torch.no_grad(), pytest.raises(TypeError):
+        call()
+
+
 def test_tolerances_see_a_mistake():
     """The oracle with a mistake planted (a decay applied one token late) is far outside the tolerances."""
     x, offsets, initial = inputs(19, [100], 1, 2, 32, 16, torch.float32, device="cpu")

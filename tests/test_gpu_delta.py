@@ -669,3 +669,34 @@ def test_step_clears_the_rows_in_no_sequence(gpu, dtype, head, lens, tail):
         left = 0 if rest else 5
         assert (out[:head] == left).all() and (out[end:] == left).all()
         assert (wide[:, 2] == 5).all() and (wide[0] == 5).all() and (wide[-1] == 5).all()
+
+
+def test_in_an_autograd_function(gpu):
+    """The calls as a model's training step makes them, on tensors that require gradients: refused outside, and inside a
+    function's forward and backward the gradients of the definition."""
+    x, offsets, initial = inputs(34, [40, 25], 1, 2, 32, 16, FP32)
+
+    class Rule(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, *args):
+            ctx.save_for_backward(*args)
+            return dws.delta_rule(*args[:5], offsets=offsets, initial_state=args[5], final_state=True)
+
+        @staticmethod
+        def backward(ctx, d_out, d_final):
+            *args, s = ctx.saved_tensors
+            return dws.delta_rule_backward(d_out, *args, offsets=offsets, initial_state=s, d_final_state=d_final)
+
+    leaves = [x[a].requires_grad_() for a in NAMES] + [initial.requires_grad_()]
+    with pytest.raises(RuntimeError, match="no graph"):
+        dws.delta_rule(*leaves[:5], offsets=offsets)
+    with pytest.raises(RuntimeError, match="no graph"):
+        dws.delta_rule_step(*leaves[:5], initial.detach(), offsets=offsets)
+    out, state = Rule.apply(*leaves)
+    gen = torch.Generator().manual_seed(3)
+    d_out = torch.randn(out.shape, generator=gen).cuda()
+    d_final = torch.randn(state.shape, generator=gen).cuda()
+    got = torch.autograd.grad((out * d_out).sum() + (state * d_final).sum(), leaves)
+    want = gradients({a: x[a].detach() for a in NAMES}, offsets, initial.detach(), 32 ** -0.5, d_out, d_final)
+    for what, a, b in zip(("dq", "dk", "dv", "dg", "dbeta", "d_initial"), got, want):
+        close(a, b, FP32, what)
