@@ -93,7 +93,8 @@ class DeltaRuleArgs(ctypes.Structure):
                 [(x, ctypes.c_void_p) for x in ("d_initial_state", "d_final_state", "d_slots")] +
                 [("n_states", ctypes.c_longlong), ("out_grad", Rows), ("d_final_grad", ctypes.c_void_p)] +
                 [(x, Rows) for x in ("q_grad", "k_grad", "v_grad", "g_grad", "beta_grad")] +
-                [("d_initial_grad", ctypes.c_void_p), ("zero_rest", ctypes.c_int), ("d_workspace", ctypes.c_void_p),
+                [("d_initial_grad", ctypes.c_void_p), ("zero_rest", ctypes.c_int), ("options", ctypes.c_int),
+                 ("d_workspace", ctypes.c_void_p),
                  ("workspace_bytes", ctypes.c_size_t)])
 
 
@@ -593,6 +594,8 @@ def run_length_encode(keys, unique_keys=None, lengths=None, count=None, stream=N
 # of setting the members of a ctypes structure, and these calls are short. Where
 # each member starts in the list of values:
 _DELTA = struct.Struct("@qqPiiiiiiif" + 6 * "Pqq" + "PPPq" + "Pqq" + "P" + 5 * "Pqq" + "PiPQ")
+_DELTA_OPTIONS = struct.Struct(_DELTA.format[:-2] + "iPQ")      # with `options`, which is 0 in the other's padding
+DELTA_FP32_GRADS = 1
 (_N_SEQS, _OFFSETS, _G_DTYPE, _Q, _K, _V, _G, _BETA, _OUT, _INITIAL, _FINAL, _SLOTS, _N_STATES, _OUT_GRAD, _FINAL_GRAD,
  _Q_GRAD, _K_GRAD, _V_GRAD, _G_GRAD, _BETA_GRAD, _INITIAL_GRAD, _ZERO_REST, _WORKSPACE) = (
     1, 2, 8, 11, 14, 17, 20, 23, 26, 29, 30, 31, 32, 33, 36, 37, 40, 43, 46, 49, 52, 53, 54)
@@ -734,10 +737,17 @@ class _on_stream:
         return False
 
 
-def _delta_workspace(a, backward, device):
+def _delta_packed(a, options):
+    if not options:
+        return _DELTA.pack(*a)
+    return _DELTA_OPTIONS.pack(*a[:_ZERO_REST + 1], options, *a[_ZERO_REST + 1:])
+
+
+def _delta_workspace(a, options, backward, device):
     import torch
     need = ctypes.c_size_t(0)
-    _check(load_library().dws_delta_rule_workspace(_DELTA.pack(*a), backward, ctypes.byref(need)), "dws_delta_rule_workspace")
+    _check(load_library().dws_delta_rule_workspace(_delta_packed(a, options), backward, ctypes.byref(need)),
+           "dws_delta_rule_workspace")
     work = torch.empty(need.value, dtype=torch.uint8, device=device)
     a[_WORKSPACE:] = work.data_ptr(), need.value
     return work
@@ -779,17 +789,18 @@ def delta_rule(q, k, v, g, beta, offsets=None, initial_state=None, final_state=N
                 a[at] = _state_ptr(t, what, count, state_shape, device)
                 if slots is not None:
                     count = a[_N_STATES] = t.shape[0]
-        work = _delta_workspace(a, 0, device)
+        work = _delta_workspace(a, 0, 0, device)
         _check(load_library().dws_delta_rule(_DELTA.pack(*a), s), "dws_delta_rule")
         del work
     return out if final_state is None else (out, final_state)
 
 
 def delta_rule_backward(d_out, q, k, v, g, beta, offsets=None, initial_state=None, d_final_state=None, scale=None,
-                        stream=None):
+                        stream=None, fp32_grads=False):
     """Gradients of delta_rule (dws_delta_rule_backward): the arguments of the forward call and the gradient(s) of its
     result(s). Returns (dq, dk, dv, dg, dbeta, d_initial_state) in the type of q, dg None without g and
-    d_initial_state None without initial_state; rows in no sequence are 0. They have no graph of their own (no second
+    d_initial_state None without initial_state; rows in no sequence are 0. fp32_grads: dg, dbeta and d_initial_state in
+    float32, as g and the states may be; the last is then d_final_state for the sequence's part before. They have no graph of their own (no second
     derivatives)."""
     import torch
     a, device = _delta_args(q, k, v, g, beta, offsets, 1, scale)
@@ -799,18 +810,18 @@ def delta_rule_backward(d_out, q, k, v, g, beta, offsets=None, initial_state=Non
         if t is not None:
             a[at] = _state_ptr(t, what, n_seqs, state_shape, device)
     with _on_stream(q, stream) as s:
-        grads = []
+        grads, options, narrow = [], DELTA_FP32_GRADS if fp32_grads else 0, torch.float32 if fp32_grads else q.dtype
         for like, at in ((q, _Q_GRAD), (k, _K_GRAD), (v, _V_GRAD), (g, _G_GRAD), (beta, _BETA_GRAD)):
-            t = None if like is None else torch.empty(like.shape, dtype=q.dtype, device=device)
+            t = None if like is None else torch.empty(like.shape, dtype=q.dtype if like.dim() == 3 else narrow, device=device)
             if t is not None:
                 a[at: at + 3] = t.data_ptr(), t.stride(0), t.stride(1)
             grads.append(t)
-        d_initial = None if initial_state is None else torch.empty(initial_state.shape, dtype=q.dtype, device=device)
+        d_initial = None if initial_state is None else torch.empty(initial_state.shape, dtype=narrow, device=device)
         if d_initial is not None:
             a[_INITIAL_GRAD] = d_initial.data_ptr()
         a[_ZERO_REST] = int(offsets is not None)
-        work = _delta_workspace(a, 1, device)
-        _check(load_library().dws_delta_rule_backward(_DELTA.pack(*a), s), "dws_delta_rule_backward")
+        work = _delta_workspace(a, options, 1, device)
+        _check(load_library().dws_delta_rule_backward(_delta_packed(a, options), s), "dws_delta_rule_backward")
         del work
     return (*grads, d_initial)
 

@@ -49,6 +49,7 @@ struct DeltaParams {
     DeltaRows d_out, dq, dk, dv, dg, dbeta;
     const float* d_final;
     void* d_initial;
+    int fp32_grads;              // dg, dbeta and d_initial are fp32, else of the input type
     int zero_rest;               // zero the output rows in no sequence
     // workspace
     int64_t n_slots;             // chunk slots: tokens / chunk + n_seqs + 1 (the last ones empty)

@@ -113,6 +113,7 @@ dws_status check_shape(const dws_delta_rule_args* a)
 {
     if (a == nullptr) return DWS_ERR_INVALID_ARG;
     if (size_of(a->dtype) == 0 || a->tokens < 0 || a->n_seqs < 1) return DWS_ERR_INVALID_ARG;
+    if (a->options & ~DWS_DELTA_FP32_GRADS) return DWS_ERR_INVALID_ARG;
     if (a->heads_qk < 1 || a->heads_v < 1 || a->dim_k < 1 || a->dim_v < 1) return DWS_ERR_INVALID_ARG;
     if (a->heads_v % a->heads_qk != 0) return DWS_ERR_INVALID_ARG;
     if (a->d_offsets == nullptr && a->tokens % a->n_seqs != 0) return DWS_ERR_INVALID_ARG;
@@ -268,12 +269,15 @@ dws_status backward_entry(const dws_delta_rule_args* a, hipStream_t stream)
     if (st == DWS_OK) st = add_rows(&r, a->q_grad, a->tokens, a->heads_qk, a->dim_k, a->dtype, true, &p.dq);
     if (st == DWS_OK) st = add_rows(&r, a->k_grad, a->tokens, a->heads_qk, a->dim_k, a->dtype, true, &p.dk);
     if (st == DWS_OK) st = add_rows(&r, a->v_grad, a->tokens, a->heads_v, a->dim_v, a->dtype, true, &p.dv);
-    if (st == DWS_OK && a->g_grad.data != nullptr) {
+    if (st != DWS_OK) return st;
+    p.fp32_grads = a->options & DWS_DELTA_FP32_GRADS;
+    const int narrow = p.fp32_grads ? (int)DWS_FLOAT32 : a->dtype;      // of the gates' and the states' gradients
+    const size_t e = size_of(narrow);
+    if (a->g_grad.data != nullptr) {
         st = a->g.data == nullptr ? DWS_ERR_INVALID_ARG
-                                  : add_rows(&r, a->g_grad, a->tokens, a->heads_v, 1, a->dtype, true, &p.dg);
+                                  : add_rows(&r, a->g_grad, a->tokens, a->heads_v, 1, narrow, true, &p.dg);
     }
-    if (st == DWS_OK) st = add_rows(&r, a->beta_grad, a->tokens, a->heads_v, 1, a->dtype, true, &p.dbeta);
-    const size_t e = a != nullptr ? size_of(a->dtype) : 0;
+    if (st == DWS_OK) st = add_rows(&r, a->beta_grad, a->tokens, a->heads_v, 1, narrow, true, &p.dbeta);
     if (st == DWS_OK && a->d_initial_state != nullptr)
         st = r.add(a->d_initial_state, state_bytes(a, a->n_seqs, 4), false, 4);
     if (st == DWS_OK && a->d_final_grad != nullptr) st = r.add(a->d_final_grad, state_bytes(a, a->n_seqs, 4), false, 4);

@@ -274,12 +274,17 @@ __global__ __launch_bounds__((kChunk<T, DK> * 4)) void k_delta_prep(DeltaParams 
                 zero_rows<T>(r, begin + len + at, p.tokens, step, C, heads, dim, tid, THREADS);
                 zero_rows<T>(r, at, head, step, C, heads, dim, tid, THREADS);
             };
+            auto zero_gates = [&](const DeltaRows& r) {
+                if (!p.fp32_grads) return zero(r, p.heads_v, 1);
+                zero_rows<float>(r, begin + len + at, p.tokens, step, C, p.heads_v, 1, tid, THREADS);
+                zero_rows<float>(r, at, head, step, C, p.heads_v, 1, tid, THREADS);
+            };
             if constexpr (BWD) {
                 zero(p.dq, p.heads_qk, p.dim_k);
                 zero(p.dk, p.heads_qk, p.dim_k);
                 zero(p.dv, p.heads_v, p.dim_v);
-                zero(p.dg, p.heads_v, 1);
-                zero(p.dbeta, p.heads_v, 1);
+                zero_gates(p.dg);
+                zero_gates(p.dbeta);
             } else {
                 zero(p.out, p.heads_v, p.dim_v);
             }
@@ -945,8 +950,16 @@ __device__ __forceinline__ void delta_scan_back(const DeltaParams& p, uint32_t b
             }
         }
     }
-    if (p.d_initial != nullptr)
-        store_state<DK>(ds, static_cast<T*>(p.d_initial) + state_at, p.dim_k, p.dim_v, col, gq);
+    if (p.d_initial != nullptr) {
+        // (made unknown: else the places that load_state worked out are kept in
+        // registers until here, and heads above 128 spill 112 bytes a lane)
+        int here = col;
+        asm volatile("" : "+v"(here));
+        if (p.fp32_grads)
+            store_state<DK>(ds, static_cast<float*>(p.d_initial) + state_at, p.dim_k, p.dim_v, here, gq);
+        else
+            store_state<DK>(ds, static_cast<T*>(p.d_initial) + state_at, p.dim_k, p.dim_v, here, gq);
+    }
 }
 
 template <class T, int DK, int NP, int NW>
@@ -1298,9 +1311,15 @@ __global__ __launch_bounds__((GradLds<T, DK>::THREADS)) DWS_TWO_WAVES void k_del
                 if (lane + d < C) x += o;
             }
             if (lane < rows) {
-                if (p.dg.data)
-                    static_cast<T*>(p.dg.data)[(info.row + lane) * p.dg.ts + h * p.dg.hs] = (T)x;
-                static_cast<T*>(p.dbeta.data)[(info.row + lane) * p.dbeta.ts + h * p.dbeta.hs] = (T)d_beta[lane];
+                const int64_t g_at = (info.row + lane) * p.dg.ts + h * p.dg.hs;
+                const int64_t b_at = (info.row + lane) * p.dbeta.ts + h * p.dbeta.hs;
+                if (p.fp32_grads) {
+                    if (p.dg.data) static_cast<float*>(p.dg.data)[g_at] = x;
+                    static_cast<float*>(p.dbeta.data)[b_at] = d_beta[lane];
+                } else {
+                    if (p.dg.data) static_cast<T*>(p.dg.data)[g_at] = (T)x;
+                    static_cast<T*>(p.dbeta.data)[b_at] = (T)d_beta[lane];
+                }
             }
         }
         __syncthreads();

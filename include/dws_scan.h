@@ -536,6 +536,13 @@ typedef struct dws_rows {
     long long head_stride;
 } dws_rows;
 
+/* dws_delta_rule_args.options */
+enum {
+    /* g_grad, beta_grad and d_initial_grad are fp32 whatever dtype is: as g and the
+     * states may be, and as d_final_grad of the sequence's part before has to be */
+    DWS_DELTA_FP32_GRADS = 1
+};
+
 /*
  * Arguments of the delta-rule calls; set unused members to 0.
  *
@@ -546,7 +553,7 @@ typedef struct dws_rows {
  * they hold, nothing outside the arrays is touched.
  *
  * dtype (DWS_FLOAT32, DWS_FLOAT16 or DWS_BFLOAT16) is that of q, k, v, out and
- * of every gradient. g (the natural logarithm of the decay; -infinity forgets
+ * of every gradient (without DWS_DELTA_FP32_GRADS). g (the natural logarithm of the decay; -infinity forgets
  * the state; data == NULL for no decay) and beta have dtypes of their own among
  * the three. dim_k and dim_v are at most 256; heads_v is a multiple of heads_qk,
  * and value head h uses query/key head h / (heads_v / heads_qk).
@@ -583,10 +590,11 @@ typedef struct dws_delta_rule_args {
     dws_rows out_grad;                  /* in */
     const float* d_final_grad;          /* in; NULL: zero */
     dws_rows q_grad, k_grad, v_grad, g_grad, beta_grad;   /* out; g_grad.data may be NULL */
-    void* d_initial_grad;               /* out, dtype; NULL: not wanted */
+    void* d_initial_grad;               /* out; NULL: not wanted */
     /* != 0: rows of out (of the gradients) in no sequence, before the first or
      * behind the last, become 0 instead of staying as they were */
     int zero_rest;
+    int options;                        /* DWS_DELTA_..., or 0 */
     void* d_workspace;                  /* DEVICE, 256-byte aligned */
     size_t workspace_bytes;
 } dws_delta_rule_args;
@@ -607,7 +615,7 @@ dws_status dws_delta_rule_workspace(const dws_delta_rule_args* args, int backwar
  * wanted (d_final_state) as many as give it fp32 accuracy, else as many as keep
  * an output's error near that of rounding it to dtype. Errors,
  * checked before any HIP call: NULL args, a required pointer that is NULL, sizes,
- * strides or types out of range, heads_v not a multiple of heads_qk, tokens not
+ * strides, types or options out of range, heads_v not a multiple of heads_qk, tokens not
  * a multiple of n_seqs without d_offsets, a workspace that is too small, or an
  * output that names an element twice give DWS_ERR_INVALID_ARG; a dimension above
  * 256, a token stride of 2^22 or more, or more chunks and heads than a launch
@@ -624,7 +632,7 @@ dws_status dws_delta_rule(const dws_delta_rule_args* args, hipStream_t stream);
  * DWS_ERR_UNSUPPORTED; out and d_final_state are not used). The states of the
  * forward pass are computed again. Query and key gradients are summed over the
  * value heads that share them in one fixed order. Sums are fp32; each gradient is
- * rounded once, to dtype. Errors as dws_delta_rule.
+ * rounded once, to its type. Errors as dws_delta_rule.
  */
 dws_status dws_delta_rule_backward(const dws_delta_rule_args* args, hipStream_t stream);
 

@@ -153,6 +153,32 @@ def test_packed_arguments_are_the_structure():
         assert (r.data, r.token_stride, r.head_stride) == (at + 1, at + 2, at + 3), name
 
 
+def test_options(lib):
+    """Unknown ones are refused; fp32 gates' gradients take fp32's alignment and room."""
+    wide = dws.DELTA_FP32_GRADS
+    for name in CALLS:
+        for unknown in (1 << 30, -1, 1 << 8):
+            assert call(lib, name, arguments(options=unknown)) == dws.ERR_INVALID_ARG
+    need = ctypes.c_size_t(0)
+    assert lib.dws_delta_rule_workspace(ctypes.byref(arguments(options=1 << 30)), 1, ctypes.byref(need)) == dws.ERR_INVALID_ARG
+    assert lib.dws_delta_rule_workspace(ctypes.byref(arguments(options=wide)), 1, ctypes.byref(need)) == dws.OK
+    name, fits = "dws_delta_rule_backward", {"workspace_bytes": need.value, "d_workspace": 1 << 44}
+    for grad in ("g_grad", "beta_grad"):
+        assert call(lib, name, arguments(**fits, options=wide, **{grad: dws.Rows((1 << 40) + 2, 4, 1)})) == dws.ERR_MISALIGNED
+        # 512 elements that end where beta begins in 16 bits, and lie over it in 32
+        before = dws.Rows(arguments().beta.data - 128 * 4 * 2, 4, 1)
+        moved = dict(fits, g=dws.Rows(1 << 41, 4, 1), options=wide)
+        assert call(lib, name, arguments(**moved, **{grad: before})) == dws.ERR_OVERLAP
+    assert call(lib, name, arguments(**fits, options=wide, d_initial_grad=(1 << 42) + 2)) == dws.ERR_MISALIGNED
+
+
+def test_packed_options_are_the_structure():
+    s = dws.DeltaRuleArgs.from_buffer_copy(dws._delta_packed([i + 1 for i in range(56)], 77))
+    assert (s.options, s.zero_rest, s.d_workspace, s.workspace_bytes, s.tokens) == (77, 54, 55, 56, 1)
+    s = dws.DeltaRuleArgs.from_buffer_copy(dws._delta_packed([i + 1 for i in range(56)], 0))
+    assert (s.options, s.zero_rest, s.d_workspace) == (0, 54, 55)
+
+
 def test_binding_refuses_cpu_tensors():
     x, offsets, initial = inputs(1, [8], 1, 1, 16, 16, torch.float32, device="cpu")
     args = [x[a] for a in NAMES]

@@ -700,3 +700,52 @@ def test_in_an_autograd_function(gpu):
     want = gradients({a: x[a].detach() for a in NAMES}, offsets, initial.detach(), 32 ** -0.5, d_out, d_final)
     for what, a, b in zip(("dq", "dk", "dv", "dg", "dbeta", "d_initial"), got, want):
         close(a, b, FP32, what)
+
+
+@pytest.mark.parametrize("dtype", [FP32, BF16, FP16])
+@pytest.mark.parametrize("lens,hk,hv,dk,dv", [([70, 0, 33], 1, 2, 64, 40), ([129], 2, 2, 128, 128), ([65, 1], 1, 3, 136, 17)])
+def test_gradients_of_fp32_gates_and_states(gpu, lens, hk, hv, dk, dv, dtype):
+    """fp32_grads: the same values before their rounding, nearer to the definition; rows in no sequence 0 as well."""
+    x, offsets, initial = inputs(35, lens, hk, hv, dk, dv, dtype, tail=75)
+    offsets += 5
+    gen = torch.Generator().manual_seed(3)
+    d_out = torch.randn(x["v"].shape, generator=gen).to(dtype).cuda()
+    d_final = 0.3 * torch.randn(initial.shape, generator=gen).cuda()
+    args = (d_out, *(x[a] for a in NAMES))
+    more = {"offsets": offsets, "initial_state": initial, "d_final_state": d_final}
+    narrow = dws.delta_rule_backward(*args, **more)
+    dirty = [torch.full_like(x["g"], float("nan")) for _ in range(4)]      # what new tensors find in their memory
+    del dirty
+    wide = dws.delta_rule_backward(*args, **more, fp32_grads=True)
+    want = gradients(x, offsets, initial, dk ** -0.5, d_out, d_final)
+    for what, a, b, c in zip(("dq", "dk", "dv", "dg", "dbeta", "d_initial"), narrow, wide, want):
+        assert b.dtype == (dtype if what in ("dq", "dk", "dv") else FP32) and a.dtype == dtype
+        assert torch.equal(b.to(dtype), a), what
+        close(b, c, dtype, what)
+        if dtype != FP32 and b.dtype == FP32:
+            assert (b.double().cpu() - c).norm() < (a.double().cpu() - c).norm(), what
+        if what != "d_initial":
+            assert (b[:5] == 0).all() and (b[5 + sum(lens):] == 0).all(), what
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP16])
+def test_segments_pass_the_states_gradient_on(gpu, dtype):
+    """A sequence differentiated in three parts, each with the state's gradient of the one behind it, is the sequence in one."""
+    cuts = [0, 128, 320, 365]
+    x, offsets, initial = inputs(36, [cuts[-1]], 1, 2, 64, 48, dtype)
+    d_out = torch.randn(x["v"].shape, generator=torch.Generator().manual_seed(3)).to(dtype).cuda()
+    states = [initial]
+    parts = [{a: x[a][b:e] for a in NAMES} for b, e in zip(cuts, cuts[1:])]
+    for y in parts:
+        states.append(dws.delta_rule(*(y[a] for a in NAMES), initial_state=states[-1], final_state=True)[1])
+    with pytest.raises(ValueError):
+        dws.delta_rule_backward(d_out, *(x[a] for a in NAMES), initial_state=initial, d_final_state=initial.to(dtype))
+    got, ds = [], None
+    for i in (2, 1, 0):
+        *grads, ds = dws.delta_rule_backward(d_out[cuts[i]: cuts[i + 1]], *(parts[i][a] for a in NAMES),
+                                             initial_state=states[i], d_final_state=ds, fp32_grads=True)
+        got.insert(0, grads)
+    want = gradients(x, offsets, initial, 64 ** -0.5, d_out, None)
+    for i, what in enumerate(("dq", "dk", "dv", "dg", "dbeta")):
+        close(torch.cat([g[i] for g in got]), want[i], dtype, what)
+    close(ds, want[5], dtype, "d_initial")
