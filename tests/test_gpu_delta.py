@@ -749,3 +749,34 @@ def test_segments_pass_the_states_gradient_on(gpu, dtype):
     for i, what in enumerate(("dq", "dk", "dv", "dg", "dbeta")):
         close(torch.cat([g[i] for g in got]), want[i], dtype, what)
     close(ds, want[5], dtype, "d_initial")
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP16])
+@pytest.mark.parametrize("n,hk,hv,dk,dv", [(64, 2, 4, 64, 64), (41, 1, 2, 128, 96), (32, 1, 2, 200, 64)])
+def test_the_states_gradient_of_one_chunk(gpu, n, hk, hv, dk, dv, dtype):
+    """Nothing on its way is rounded to one 16-bit part: P, the inverse, dU and the two operands of the last products are
+    in two, each off by 2^-16 (fp16 2^-22), and the sums are fp32's, as tolerance() counts them.
+
+    An fp16 part below 2^-14 is off by up to 2^-25, however small it is, which the second parts of small operands are.
+    With all factors e^G and beta at most 1, and norms ||.|| of the matrices, the result is Q^T e - K^T y, with
+    y = T^T dU and dU = P^T dO scaled: e and y off by 2^-25 an element add 2^-25 sqrt(n dv) (||Q|| + ||K||), dU's
+    2^-25 sqrt(n dv) go through T and K, T's 2^-25 n (an n x n matrix) meet dU and K, and P's meet dO, T and K."""
+    x, offsets, initial = inputs(37, [n], hk, hv, dk, dv, dtype)
+    d_out = torch.randn(x["v"].shape, generator=torch.Generator().manual_seed(3)).to(dtype).cuda()
+    got = dws.delta_rule_backward(d_out, *(x[a] for a in NAMES), initial_state=initial, fp32_grads=True)[5].double().cpu()
+    want = gradients(x, offsets, initial, dk ** -0.5, d_out, None)[5]
+    tiny = 0.0
+    if dtype == FP16:
+        y = {a: x[a].double().cpu() for a in NAMES}
+        norm = torch.linalg.matrix_norm
+        for h in range(hv):
+            q, k, d_o = y["q"][:, h * hk // hv], y["k"][:, h * hk // hv], d_out[:, h].double().cpu()
+            total = y["g"][:, h].cumsum(0)
+            decay = (total[:, None] - total[None, :]).tril().exp().tril()
+            t = torch.linalg.inv(torch.eye(n) + (y["beta"][:, h, None] * decay * (k @ k.T)).tril(-1))
+            d_u = dk ** -0.5 * (decay * (q @ k.T)).T @ d_o
+            nq, nk, nt, nu, no = (norm(z, 2).item() for z in (q, k, t, d_u, d_o))
+            tiny += (2.0 ** -25 * ((n * dv) ** 0.5 * (nq + nk * (1 + nt)) + n * nk * (nu + nt * no))) ** 2
+    off, most = (got - want).norm().item(), 5 * (2.0 ** -16 if dtype == BF16 else 2.0 ** -22) + tolerance(FP32, "state")
+    print(f"off by {off / want.norm():.3g}, {most + tiny ** 0.5 / want.norm().item():.3g} allowed")
+    assert off <= most * want.norm().item() + tiny ** 0.5
