@@ -595,7 +595,7 @@ def run_length_encode(keys, unique_keys=None, lengths=None, count=None, stream=N
 # each member starts in the list of values:
 _DELTA = struct.Struct("@qqPiiiiiiif" + 6 * "Pqq" + "PPPq" + "Pqq" + "P" + 5 * "Pqq" + "PiPQ")
 _DELTA_OPTIONS = struct.Struct(_DELTA.format[:-2] + "iPQ")      # with `options`, which is 0 in the other's padding
-DELTA_FP32_GRADS = 1
+DELTA_FP32_GRADS, DELTA_PRECISE = 1, 2
 (_N_SEQS, _OFFSETS, _G_DTYPE, _Q, _K, _V, _G, _BETA, _OUT, _INITIAL, _FINAL, _SLOTS, _N_STATES, _OUT_GRAD, _FINAL_GRAD,
  _Q_GRAD, _K_GRAD, _V_GRAD, _G_GRAD, _BETA_GRAD, _INITIAL_GRAD, _ZERO_REST, _WORKSPACE) = (
     1, 2, 8, 11, 14, 17, 20, 23, 26, 29, 30, 31, 32, 33, 36, 37, 40, 43, 46, 49, 52, 53, 54)
@@ -754,7 +754,7 @@ def _delta_workspace(a, options, backward, device):
 
 
 def delta_rule(q, k, v, g, beta, offsets=None, initial_state=None, final_state=None, slots=None, scale=None, out=None,
-               stream=None):
+               stream=None, precise=False):
     """The gated delta rule over whole sequences (dws_delta_rule).
 
     q, k: (tokens, heads_qk, dim_k); v: (tokens, heads_v, dim_v), all float32, float16 or bfloat16, any strides with a
@@ -763,14 +763,15 @@ def delta_rule(q, k, v, g, beta, offsets=None, initial_state=None, final_state=N
     (n, heads_v, dim_k, dim_v) or None for zero. final_state: None, a tensor like it to write (may be initial_state),
     or True for a new one. slots: int32 GPU tensor of n places when the states are a pool (count, heads_v, dim_k,
     dim_v); sequences with a place below 0, outside the pool or named before are left out. scale: dim_k^-0.5 by
-    default. Rows of ``out`` in no sequence stay as they were, and are 0 in a new one.
+    default. Rows of ``out`` in no sequence stay as they were, and are 0 in a new one. precise: the states in 16-bit
+    products with fp32 accuracy also where no final one is asked for; ``out`` then has the same bits as where it is.
     Records no graph: tensors that require gradients are refused unless gradients are off (torch.no_grad()).
     Returns out, or (out, final_state) when the final state is asked for."""
     import torch
     _records_no_graph("delta_rule", q, k, v, g, beta, initial_state, final_state, out)
     a, device = _delta_args(q, k, v, g, beta, offsets, 1, scale)
     n_seqs, state_shape = a[_N_SEQS], (v.shape[1], q.shape[2], v.shape[2])
-    count = n_seqs
+    count, options = n_seqs, DELTA_PRECISE if precise else 0
     if slots is not None:
         a[_SLOTS] = _device_ints(slots, "slots", torch.int32, n_seqs, device)
         count = None
@@ -789,8 +790,8 @@ def delta_rule(q, k, v, g, beta, offsets=None, initial_state=None, final_state=N
                 a[at] = _state_ptr(t, what, count, state_shape, device)
                 if slots is not None:
                     count = a[_N_STATES] = t.shape[0]
-        work = _delta_workspace(a, 0, 0, device)
-        _check(load_library().dws_delta_rule(_DELTA.pack(*a), s), "dws_delta_rule")
+        work = _delta_workspace(a, options, 0, device)
+        _check(load_library().dws_delta_rule(_delta_packed(a, options), s), "dws_delta_rule")
         del work
     return out if final_state is None else (out, final_state)
 

@@ -76,8 +76,8 @@ struct DeltaPack {
     int n;
 };
 
-// Per-type launchers (dws_delta_{bf16,f16,f32}.hip). `precise`: the final
-// state is wanted, with fp32 accuracy.
+// Per-type launchers (dws_delta_{bf16,f16,f32}.hip). `precise`: the states have
+// fp32 accuracy, as a final one that is wanted has to.
 hipError_t launch_delta_forward_bf16(const DeltaParams& p, const DeltaPack& k, bool precise, hipStream_t stream);
 hipError_t launch_delta_forward_f16(const DeltaParams& p, const DeltaPack& k, bool precise, hipStream_t stream);
 hipError_t launch_delta_forward_f32(const DeltaParams& p, const DeltaPack& k, bool precise, hipStream_t stream);

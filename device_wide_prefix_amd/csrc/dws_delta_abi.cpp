@@ -113,7 +113,7 @@ dws_status check_shape(const dws_delta_rule_args* a)
 {
     if (a == nullptr) return DWS_ERR_INVALID_ARG;
     if (size_of(a->dtype) == 0 || a->tokens < 0 || a->n_seqs < 1) return DWS_ERR_INVALID_ARG;
-    if (a->options & ~DWS_DELTA_FP32_GRADS) return DWS_ERR_INVALID_ARG;
+    if (a->options & ~(DWS_DELTA_FP32_GRADS | DWS_DELTA_PRECISE)) return DWS_ERR_INVALID_ARG;
     if (a->heads_qk < 1 || a->heads_v < 1 || a->dim_k < 1 || a->dim_v < 1) return DWS_ERR_INVALID_ARG;
     if (a->heads_v % a->heads_qk != 0) return DWS_ERR_INVALID_ARG;
     if (a->d_offsets == nullptr && a->tokens % a->n_seqs != 0) return DWS_ERR_INVALID_ARG;
@@ -177,7 +177,10 @@ void pack(const dws_delta_rule_args* a, const Sizes& z, bool backward, DeltaPara
     }
 }
 
-bool is_precise(const dws_delta_rule_args* a) { return a->d_final_state != nullptr && a->dtype != DWS_FLOAT32; }
+bool is_precise(const dws_delta_rule_args* a)
+{
+    return a->dtype != DWS_FLOAT32 && (a->d_final_state != nullptr || (a->options & DWS_DELTA_PRECISE) != 0);
+}
 
 // The operands that both directions read, and the launch's parameters.
 dws_status common(const dws_delta_rule_args* a, Ranges* r, DeltaParams* p)

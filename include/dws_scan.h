@@ -540,7 +540,10 @@ typedef struct dws_rows {
 enum {
     /* g_grad, beta_grad and d_initial_grad are fp32 whatever dtype is: as g and the
      * states may be, and as d_final_grad of the sequence's part before has to be */
-    DWS_DELTA_FP32_GRADS = 1
+    DWS_DELTA_FP32_GRADS = 1,
+    /* dws_delta_rule: the products' operands as where d_final_state is wanted, so
+     * that out has the same bits with it and without */
+    DWS_DELTA_PRECISE = 2
 };
 
 /*
@@ -600,8 +603,8 @@ typedef struct dws_delta_rule_args {
 } dws_delta_rule_args;
 
 /* Bytes of workspace that dws_delta_rule (backward == 0) or
- * dws_delta_rule_backward needs with these arguments, their pointers, strides
- * and choice of d_final_state included (host only, no HIP call): rows of q, k, v
+ * dws_delta_rule_backward needs with these arguments, their pointers, strides,
+ * options and choice of d_final_state included (host only, no HIP call): rows of q, k, v
  * and out_grad that are not whole, aligned 16-byte units are copied there first.
  * The workspace is the caller's, not the
  * stream's, since it grows with the tokens; it holds nothing between calls, and
@@ -612,8 +615,9 @@ dws_status dws_delta_rule_workspace(const dws_delta_rule_args* args, int backwar
 /*
  * Whole sequences, in chunks on the matrix cores. With 16-bit inputs the fp32
  * operands of the products are split into 16-bit parts: where the state is
- * wanted (d_final_state) as many as give it fp32 accuracy, else as many as keep
- * an output's error near that of rounding it to dtype. Errors,
+ * wanted (d_final_state, or DWS_DELTA_PRECISE) as many as give it fp32 accuracy,
+ * else as many as keep an output's error near that of rounding it to dtype: out's
+ * last bits differ between the two. Errors,
  * checked before any HIP call: NULL args, a required pointer that is NULL, sizes,
  * strides, types or options out of range, heads_v not a multiple of heads_qk, tokens not
  * a multiple of n_seqs without d_offsets, a workspace that is too small, or an

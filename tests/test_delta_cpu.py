@@ -172,6 +172,19 @@ def test_options(lib):
     assert call(lib, name, arguments(**fits, options=wide, d_initial_grad=(1 << 42) + 2)) == dws.ERR_MISALIGNED
 
 
+def test_workspace_of_precise_outputs(lib):
+    """What a call with a final state needs, for the 16-bit types; nothing changes for fp32 and for gradients."""
+    def need(backward=0, **more):
+        n = ctypes.c_size_t(0)
+        assert lib.dws_delta_rule_workspace(ctypes.byref(arguments(**more)), backward, ctypes.byref(n)) == dws.OK
+        return n.value
+
+    assert need(d_final_state=None) < need(d_final_state=None, options=dws.DELTA_PRECISE) == need()
+    assert need(options=dws.DELTA_PRECISE) == need()
+    assert need(dtype=dws.FLOAT32, d_final_state=None, options=dws.DELTA_PRECISE) == need(dtype=dws.FLOAT32)
+    assert need(1, options=dws.DELTA_PRECISE) == need(1)
+
+
 def test_packed_options_are_the_structure():
     s = dws.DeltaRuleArgs.from_buffer_copy(dws._delta_packed([i + 1 for i in range(56)], 77))
     assert (s.options, s.zero_rest, s.d_workspace, s.workspace_bytes, s.tokens) == (77, 54, 55, 56, 1)

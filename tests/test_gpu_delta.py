@@ -780,3 +780,16 @@ def test_the_states_gradient_of_one_chunk(gpu, n, hk, hv, dk, dv, dtype):
     off, most = (got - want).norm().item(), 5 * (2.0 ** -16 if dtype == BF16 else 2.0 ** -22) + tolerance(FP32, "state")
     print(f"off by {off / want.norm():.3g}, {most + tiny ** 0.5 / want.norm().item():.3g} allowed")
     assert off <= most * want.norm().item() + tiny ** 0.5
+
+
+@pytest.mark.parametrize("dtype", [FP32, BF16, FP16])
+@pytest.mark.parametrize("lens,hk,hv,dk,dv", [([130, 1, 0, 64], 1, 2, 64, 48), ([200], 2, 2, 128, 128), ([70], 1, 1, 200, 40),
+                                              ([40] * 40, 4, 8, 96, 64)])
+def test_precise_outputs(gpu, lens, hk, hv, dk, dv, dtype):
+    """The same bits whether the final state is asked for or not."""
+    x, offsets, initial = inputs(38, lens, hk, hv, dk, dv, dtype, tail=3)
+    want, _ = forward(x, offsets, initial, final_state=True)
+    assert torch.equal(forward(x, offsets, initial, precise=True), want)
+    assert torch.equal(forward(x, offsets, initial, precise=True, final_state=True)[0], want)
+    if dtype == FP32:
+        assert torch.equal(forward(x, offsets, initial), want)
