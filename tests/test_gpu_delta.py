@@ -793,3 +793,70 @@ def test_precise_outputs(gpu, lens, hk, hv, dk, dv, dtype):
     assert torch.equal(forward(x, offsets, initial, precise=True, final_state=True)[0], want)
     if dtype == FP32:
         assert torch.equal(forward(x, offsets, initial), want)
+
+
+@pytest.mark.parametrize("n,each,hk,hv,dk,dv,dtype", [(3, 50, 1, 2, 40, 24, FP32), (70, 33, 1, 2, 64, 32, BF16),
+                                                      (200, 1, 2, 2, 32, 40, FP16), (5, 129, 2, 4, 136, 17, BF16),
+                                                      (4, 0, 1, 1, 16, 16, BF16), (300, 65, 1, 1, 64, 64, BF16)])
+def test_equal_shares_without_offsets(gpu, n, each, hk, hv, dk, dv, dtype):
+    """No offsets: tokens / n_seqs rows a sequence, with the bits of the offsets that say so."""
+    note(f"delta equal shares {n} {each} {dtype}")
+    x, offsets, initial = inputs(39, [each] * n, hk, hv, dk, dv, dtype)
+    d_out = torch.randn(x["v"].shape, generator=torch.Generator().manual_seed(6)).to(dtype).cuda()
+    d_final = 0.3 * torch.randn(initial.shape, generator=torch.Generator().manual_seed(7)).cuda()
+    pool = initial.clone()
+    more = {"offsets": offsets, "initial_state": initial}
+    want = [*forward(x, offsets, initial, final_state=True), dws.delta_rule_step(*(x[a] for a in NAMES), pool, offsets=offsets),
+            pool, *dws.delta_rule_backward(d_out, *(x[a] for a in NAMES), **more, d_final_state=d_final)]
+    out, final, stepped, state, *grads = [torch.full_like(t, 3.0) for t in want]
+    state.copy_(initial)
+    names = ("q_grad", "k_grad", "v_grad", "g_grad", "beta_grad")
+    for rest in (0, 1):
+        a = c_arguments(x, n, out=rows_of(out), d_initial_state=initial.data_ptr(), d_final_state=final.data_ptr(), zero_rest=rest,
+                        out_grad=rows_of(d_out), d_final_grad=d_final.data_ptr(), d_initial_grad=grads[5].data_ptr(),
+                        **{name: rows_of(t) for name, t in zip(names, grads)})
+        assert c_call("dws_delta_rule", a, 0) == dws.OK
+        assert c_call("dws_delta_rule_backward", a, 1) == dws.OK
+    a.out, a.d_initial_state, a.d_final_state = rows_of(stepped), state.data_ptr(), state.data_ptr()
+    assert c_call("dws_delta_rule_step", a) == dws.OK
+    for got, t in zip((out, final, stepped, state, *grads), want):
+        assert torch.equal(got, t)
+
+
+@pytest.mark.parametrize("whole", [False, True])
+def test_many_slots(gpu, whole):
+    """Tens of thousands of sequences on a pool: duplicates and places outside it among them, each found by a search of
+    the slots before its own."""
+    n, count, dk, dv = 40000, 30000, 16, 16
+    lens = [1] * n
+    x, offsets, _ = inputs(40, lens, 1, 1, dk, dv, BF16, init=False)
+    gen = torch.Generator().manual_seed(2)
+    slots = torch.randint(-5, count + 5, (n,), generator=gen).to(torch.int32)
+    pool = 0.3 * torch.randn(count, 1, dk, dv, generator=gen)
+    seen, first = {}, []
+    for i, s in enumerate(slots.tolist()):
+        first.append(0 <= s < count and s not in seen)
+        seen.setdefault(s, i)
+    first = torch.tensor(first)
+    assert 10000 < int(first.sum()) < 30000
+    out = torch.full(x["v"].shape, 3.0, dtype=BF16, device="cuda")
+    state, where = pool.cuda(), slots.cuda()
+    args = [x[a] for a in NAMES]
+    if whole:
+        dws.delta_rule(*args, offsets=offsets, initial_state=state, final_state=state, slots=where, out=out)
+    else:
+        dws.delta_rule_step(*args, state, slots=where, out=out)
+    assert (out[~first.cuda()] == 3).all()
+    # the sequences that take part, with states of their own and no slots
+    some = first.nonzero().reshape(-1)
+    alone = pool[slots[some].long()].cuda()
+    some_args = [t[some.cuda()] for t in args]
+    if whole:
+        want, final = dws.delta_rule(*some_args, offsets=torch.arange(len(some) + 1, device="cuda"), initial_state=alone,
+                                     final_state=True)
+    else:
+        want, final = dws.delta_rule_step(*some_args, alone), alone
+    assert torch.equal(out[first.cuda()], want)
+    wanted = pool.clone()
+    wanted[slots[some].long()] = final.cpu()
+    assert torch.equal(state.cpu(), wanted)
