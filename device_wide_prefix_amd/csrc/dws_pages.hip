@@ -514,7 +514,9 @@ hipError_t launch_requests(const PageCache& c, const PageRequests& r, hipStream_
     }
     const int64_t tiles = tiles_of(c.pages);
     const uint32_t splits = splits_of(c);
-    k_pages_count<<<dim3((uint32_t)tiles), dim3(kThreads), 0, stream>>>(c, r.live, r.claim);
+    // workgroups for the claims of many rows, too, which may be far more than pages
+    const int64_t clears = (c.rows + kPageTile - 1) / kPageTile;
+    k_pages_count<<<dim3(clamp_grid(tiles > clears ? tiles : clears, 1 << 16)), dim3(kThreads), 0, stream>>>(c, r.live, r.claim);
     k_pages_plan<FORK><<<dim3((uint32_t)tiles + 1), dim3(kPlanThreads), 0, stream>>>(c, r);
     if (r.n == 0) return hipGetLastError();
     k_pages_apply<FORK><<<dim3((uint32_t)r.n * splits), dim3(kThreads), 0, stream>>>(c, r, splits);

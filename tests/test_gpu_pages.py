@@ -349,3 +349,26 @@ def test_graphs_and_streams(gpu, pages, most):
         torch.cuda.synchronize()
         for got in (aside, eager, graphs[0][1], graphs[1][1]):
             assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+@pytest.mark.parametrize("rows", [4097, 200001])
+def test_far_more_rows_than_pages(gpu, rows):
+    """One tile of pages and many of rows, whose claims of the call before are all forgotten."""
+    note(f"pages rows {rows}")
+    pages, most, page_tokens, n = 300, 2, 4, 150
+    c = Cache(pages, rows, most, page_tokens)
+    rng = random.Random(11)
+    g = OnGpu(c)
+    for step in range(3):
+        named = [rng.choice([0, 1, rows - 1, rows, rng.randrange(rows)]) for _ in range(n)]
+        new = [rng.randint(0, most * page_tokens) for _ in range(n)]
+        granted = dws.pages_grow(*g.args(), ints(named), ints(new), page_tokens)
+        assert granted.tolist() == c.grow(named, new)
+        parents = [rng.choice(named) for _ in range(n)]
+        children = [rng.choice([rows - 2, rng.randrange(rows), rng.randrange(rows)]) for _ in range(n)]
+        granted, src, dst, count = dws.pages_fork(*g.args(), ints(parents), ints(children), page_tokens)
+        want, a, b = c.fork(parents, children)
+        assert granted.tolist() == want and count.tolist() == [len(a)] and src.tolist()[:len(a)] == a
+        some = named[::2]
+        assert dws.pages_free(*g.args(), ints(some), page_tokens).tolist() == [c.free(some)]
+    g.same(c)
