@@ -860,3 +860,70 @@ def test_many_slots(gpu, whole):
     wanted = pool.clone()
     wanted[slots[some].long()] = final.cpu()
     assert torch.equal(state.cpu(), wanted)
+
+
+def test_gradients_with_a_workspace_beyond_32_bits(gpu):
+    """A long sequence before a short one: the short one's gradients are those it has alone, and the long one's last part
+    has those it has as a sequence of its own behind the state before it."""
+    long, last, short, hk, hv, dk = 100032, 960, 70, 2, 16, 128
+    gen = torch.Generator(device="cuda").manual_seed(41)
+    n = long + short
+
+    def normal(*shape):
+        return torch.randn(*shape, generator=gen, device="cuda")
+
+    x = {a: torch.nn.functional.normalize(normal(n, hk, dk), dim=-1).to(BF16) for a in ("q", "k")}
+    x["v"], d_out = normal(n, hv, dk).to(BF16), normal(n, hv, dk).to(BF16)
+    x["g"], x["beta"] = -0.1 * torch.rand(n, hv, generator=gen, device="cuda"), torch.rand(n, hv, generator=gen, device="cuda").to(BF16)
+    offsets = torch.tensor([0, long, n], device="cuda")
+    a = c_arguments(x, 2, d_offsets=offsets.data_ptr())
+    need = ctypes.c_size_t(0)
+    assert dws.load_library().dws_delta_rule_workspace(ctypes.byref(a), 1, ctypes.byref(need)) == dws.OK
+    assert need.value > 1 << 32
+    got = dws.delta_rule_backward(d_out, *(x[a] for a in NAMES), offsets=offsets)[:5]
+    out = forward(x, offsets, None)
+
+    def part(rows):
+        return {a: x[a][rows] for a in NAMES}
+    rows = slice(long, n)
+    alone = dws.delta_rule_backward(d_out[rows], *part(rows).values())[:5]
+    assert torch.equal(out[rows], forward(part(rows), None, None))
+    for a, b in zip(got, alone):
+        assert torch.equal(a[rows], b)
+    before, rows = slice(0, long - last), slice(long - last, long)
+    state = dws.delta_rule(*part(before).values(), final_state=True)[1]
+    close(out[rows], forward(part(rows), None, state), BF16, "dg")
+    alone = dws.delta_rule_backward(d_out[rows], *part(rows).values(), initial_state=state)[:5]
+    for what, a, b in zip(("dq", "dk", "dv", "dg", "dbeta"), got, alone):
+        off = ((a[rows].double() - b.double()).norm() / b.double().norm()).item()
+        assert off <= 2 * tolerance(BF16, what), (what, off)          # both are off by the tolerance
+
+
+def test_rows_far_apart(gpu):
+    """Tokens whose rows are beyond 2^31 elements and 2^32 bytes of their first."""
+    n, hk, hv, dk, dv, stride = 1100, 1, 2, 64, 32, 1 << 21
+    x, offsets, initial = inputs(42, [700, n - 700], hk, hv, dk, dv, BF16)
+    d_out = torch.randn(x["v"].shape, generator=torch.Generator().manual_seed(3)).to(BF16).cuda()
+    far = torch.empty(n * stride, dtype=BF16, device="cuda")
+    y, at = dict(x), 0
+    for a in ("q", "k", "v"):
+        heads, dim = x[a].shape[1:]
+        y[a] = far.as_strided((n, heads, dim), (stride, dim, 1), at)
+        y[a].copy_(x[a])
+        at += heads * dim
+    d_far = far.as_strided((n, hv, dv), (stride, dv, 1), at)
+    d_far.copy_(d_out)
+    want, final = forward(x, offsets, initial, final_state=True)
+    got, state = forward(y, offsets, initial, final_state=True)
+    assert torch.equal(got, want) and torch.equal(state, final)
+    for a, b in zip(dws.delta_rule_backward(d_far, *(y[a] for a in NAMES), offsets=offsets, initial_state=initial),
+                    dws.delta_rule_backward(d_out, *(x[a] for a in NAMES), offsets=offsets, initial_state=initial)):
+        assert torch.equal(a, b)
+    pool, far_pool = initial.clone(), initial.clone()
+    assert torch.equal(dws.delta_rule_step(*(y[a] for a in NAMES), far_pool, offsets=offsets),
+                       dws.delta_rule_step(*(x[a] for a in NAMES), pool, offsets=offsets))
+    assert torch.equal(pool, far_pool)
+    # and a far output, in an array of its own
+    wide = torch.empty(n * stride, dtype=BF16, device="cuda").as_strided((n, hv, dv), (stride, dv, 1), 8)
+    forward(x, offsets, initial, out=wide, final_state=True)
+    assert torch.equal(wide, want)
