@@ -574,6 +574,11 @@ enum {
  * on, at most 63 tokens before it (a zero above a matrix's diagonal times infinity
  * is not zero), and dws_delta_rule_step from its token on.
  *
+ * A g below -104 counts as -104: fp32 rounds its factor to 0. With g above 0 states
+ * grow, and the sum over any run of 64 tokens must stay below 88 in
+ * dws_delta_rule and its gradients, which hold e to that sum in fp32 beside the
+ * states; dws_delta_rule_step holds the states only.
+ *
  * With DWS_FLOAT16 the operands of the matrix products, states among them, are
  * rounded to fp16: they must stay below 65504, and below 2^-14 they lose digits
  * (gradients of a sum that is far smaller than that want scaling up).
