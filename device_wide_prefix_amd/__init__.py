@@ -797,11 +797,12 @@ def delta_rule(q, k, v, g, beta, offsets=None, initial_state=None, final_state=N
 
 
 def delta_rule_backward(d_out, q, k, v, g, beta, offsets=None, initial_state=None, d_final_state=None, scale=None,
-                        stream=None, fp32_grads=False):
+                        stream=None, fp32_grads=False, precise=False):
     """Gradients of delta_rule (dws_delta_rule_backward): the arguments of the forward call and the gradient(s) of its
     result(s). Returns (dq, dk, dv, dg, dbeta, d_initial_state) in the type of q, dg None without g and
     d_initial_state None without initial_state; rows in no sequence are 0. fp32_grads: dg, dbeta and d_initial_state in
-    float32, as g and the states may be; the last is then d_final_state for the sequence's part before. They have no graph of their own (no second
+    float32, as g and the states may be; the last is then d_final_state for the sequence's part before. precise: the
+    states' gradients in 16-bit products in two parts, so that only each result's own rounding is left. They have no graph of their own (no second
     derivatives)."""
     import torch
     a, device = _delta_args(q, k, v, g, beta, offsets, 1, scale)
@@ -811,7 +812,8 @@ def delta_rule_backward(d_out, q, k, v, g, beta, offsets=None, initial_state=Non
         if t is not None:
             a[at] = _state_ptr(t, what, n_seqs, state_shape, device)
     with _on_stream(q, stream) as s:
-        grads, options, narrow = [], DELTA_FP32_GRADS if fp32_grads else 0, torch.float32 if fp32_grads else q.dtype
+        options = (DELTA_FP32_GRADS if fp32_grads else 0) | (DELTA_PRECISE if precise else 0)
+        grads, narrow = [], torch.float32 if fp32_grads else q.dtype
         for like, at in ((q, _Q_GRAD), (k, _K_GRAD), (v, _V_GRAD), (g, _G_GRAD), (beta, _BETA_GRAD)):
             t = None if like is None else torch.empty(like.shape, dtype=q.dtype if like.dim() == 3 else narrow, device=device)
             if t is not None:

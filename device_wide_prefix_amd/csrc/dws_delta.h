@@ -23,7 +23,10 @@ constexpr int delta_triangle(int chunk) { return (chunk == 64 ? 6 : 2) * 512; }
 // that the backward pass keeps, and all that a final state depends on.
 constexpr int delta_fine_parts(int dtype) { return dtype == DWS_FLOAT32 ? 1 : 2; }
 constexpr int delta_state_parts(int dtype) { return delta_fine_parts(dtype); }
-constexpr int delta_state_grad_parts(int dtype, int dim_k) { return dim_k > 128 ? delta_fine_parts(dtype) : 1; }
+constexpr int delta_state_grad_parts(int dtype, int dim_k, bool precise)
+{
+    return precise || dim_k > 128 ? delta_fine_parts(dtype) : 1;
+}
 constexpr int delta_precise_parts(int dtype) { return dtype == DWS_BFLOAT16 ? 3 : delta_fine_parts(dtype); }
 
 // One (tokens, heads, dim) operand: strides in elements, dim contiguous.
@@ -77,13 +80,14 @@ struct DeltaPack {
 };
 
 // Per-type launchers (dws_delta_{bf16,f16,f32}.hip). `precise`: the states have
-// fp32 accuracy, as a final one that is wanted has to.
+// fp32 accuracy, as a final one that is wanted has to; backward, the states'
+// gradients enter the products in as many parts as the states.
 hipError_t launch_delta_forward_bf16(const DeltaParams& p, const DeltaPack& k, bool precise, hipStream_t stream);
 hipError_t launch_delta_forward_f16(const DeltaParams& p, const DeltaPack& k, bool precise, hipStream_t stream);
 hipError_t launch_delta_forward_f32(const DeltaParams& p, const DeltaPack& k, bool precise, hipStream_t stream);
-hipError_t launch_delta_backward_bf16(const DeltaParams& p, const DeltaPack& k, hipStream_t stream);
-hipError_t launch_delta_backward_f16(const DeltaParams& p, const DeltaPack& k, hipStream_t stream);
-hipError_t launch_delta_backward_f32(const DeltaParams& p, const DeltaPack& k, hipStream_t stream);
+hipError_t launch_delta_backward_bf16(const DeltaParams& p, const DeltaPack& k, bool precise, hipStream_t stream);
+hipError_t launch_delta_backward_f16(const DeltaParams& p, const DeltaPack& k, bool precise, hipStream_t stream);
+hipError_t launch_delta_backward_f32(const DeltaParams& p, const DeltaPack& k, bool precise, hipStream_t stream);
 
 struct DeltaStepParams {
     int64_t tokens, n_seqs;

@@ -128,7 +128,8 @@ dws_status check_shape(const dws_delta_rule_args* a)
 }
 
 // Workspace arrays of a call, each at a multiple of 256 bytes. The caller's
-// sizes have passed check_shape. The counts of parts are the kernels'.
+// sizes have passed check_shape. The counts of parts are the kernels'. `precise`:
+// as the launchers'.
 Sizes workspace_of(const dws_delta_rule_args* a, bool backward, bool precise)
 {
     Sizes z{};
@@ -145,14 +146,14 @@ Sizes workspace_of(const dws_delta_rule_args* a, bool backward, bool precise)
     };
     z.gate = take(n * 5 * c * sizeof(float));
     const size_t tri = (size_t)delta_triangle((int)c) * e;
-    z.t = take(n * tri * (precise ? (size_t)delta_precise_parts(a->dtype) : fine));
+    z.t = take(n * tri * (precise && !backward ? (size_t)delta_precise_parts(a->dtype) : fine));
     z.p = take(n * tri * fine);
     if (backward) {
         z.tt = take(n * tri * fine);
         z.s = take(n * dk * dv * e * (size_t)delta_state_parts(a->dtype));
         z.u = take(n * c * dv * e * fine);
         z.z = take(n * c * dv * e * fine);
-        z.ds = take(n * dk * dv * e * (size_t)delta_state_grad_parts(a->dtype, a->dim_k));
+        z.ds = take(n * dk * dv * e * (size_t)delta_state_grad_parts(a->dtype, a->dim_k, precise));
     }
     const int kinds = backward ? 4 : 3;
     for (int i = 0; i < kinds; ++i) {
@@ -177,9 +178,9 @@ void pack(const dws_delta_rule_args* a, const Sizes& z, bool backward, DeltaPara
     }
 }
 
-bool is_precise(const dws_delta_rule_args* a)
+bool is_precise(const dws_delta_rule_args* a, bool backward)
 {
-    return a->dtype != DWS_FLOAT32 && (a->d_final_state != nullptr || (a->options & DWS_DELTA_PRECISE) != 0);
+    return a->dtype != DWS_FLOAT32 && ((!backward && a->d_final_state != nullptr) || (a->options & DWS_DELTA_PRECISE) != 0);
 }
 
 // The operands that both directions read, and the launch's parameters.
@@ -237,7 +238,7 @@ dws_status forward_entry(const dws_delta_rule_args* a, hipStream_t stream)
         st = r.add(a->d_initial_state, state_bytes(a, states, 4), false, 4);
     if (st == DWS_OK && a->d_final_state != nullptr) st = r.add(a->d_final_state, state_bytes(a, states, 4), true, 4);
     if (st != DWS_OK) return st;
-    const bool precise = is_precise(a);
+    const bool precise = is_precise(a, false);
     const Sizes z = workspace_of(a, false, precise);
     if (a->d_workspace == nullptr || a->workspace_bytes < z.bytes) return DWS_ERR_INVALID_ARG;
     if ((st = r.add(a->d_workspace, z.bytes, true, 256)) != DWS_OK) return st;
@@ -287,7 +288,8 @@ dws_status backward_entry(const dws_delta_rule_args* a, hipStream_t stream)
     if (st == DWS_OK && a->d_initial_grad != nullptr)
         st = r.add(a->d_initial_grad, state_bytes(a, a->n_seqs, e), true, e);
     if (st != DWS_OK) return st;
-    const Sizes z = workspace_of(a, true, false);
+    const bool precise = is_precise(a, true);
+    const Sizes z = workspace_of(a, true, precise);
     // the gradients' workgroups have up to 512 threads
     if ((uint64_t)z.n_slots * (uint64_t)a->heads_qk > kMaxThreads / 512) return DWS_ERR_UNSUPPORTED;
     if (a->d_workspace == nullptr || a->workspace_bytes < z.bytes) return DWS_ERR_INVALID_ARG;
@@ -311,9 +313,9 @@ dws_status backward_entry(const dws_delta_rule_args* a, hipStream_t stream)
     DeltaPack k{};
     pack(a, z, true, &p, &k);
     switch (a->dtype) {
-    case DWS_BFLOAT16: return status_of(launch_delta_backward_bf16(p, k, stream));
-    case DWS_FLOAT16: return status_of(launch_delta_backward_f16(p, k, stream));
-    default: return status_of(launch_delta_backward_f32(p, k, stream));
+    case DWS_BFLOAT16: return status_of(launch_delta_backward_bf16(p, k, precise, stream));
+    case DWS_FLOAT16: return status_of(launch_delta_backward_f16(p, k, precise, stream));
+    default: return status_of(launch_delta_backward_f32(p, k, precise, stream));
     }
 }
 
@@ -375,7 +377,7 @@ dws_status dws_delta_rule_workspace(const dws_delta_rule_args* args, int backwar
 {
     if (bytes == nullptr) return DWS_ERR_INVALID_ARG;
     if (dws_status st = check_shape(args); st != DWS_OK) return st;
-    *bytes = workspace_of(args, backward != 0, backward == 0 && is_precise(args)).bytes;
+    *bytes = workspace_of(args, backward != 0, is_precise(args, backward != 0)).bytes;
     return DWS_OK;
 }
 

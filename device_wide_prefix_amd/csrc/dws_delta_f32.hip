@@ -9,9 +9,9 @@ hipError_t launch_delta_forward_f32(const DeltaParams& p, const DeltaPack& k, bo
     return forward_type<float, 1>(p, k, stream);
 }
 
-hipError_t launch_delta_backward_f32(const DeltaParams& p, const DeltaPack& k, hipStream_t stream)
+hipError_t launch_delta_backward_f32(const DeltaParams& p, const DeltaPack& k, bool precise, hipStream_t stream)
 {
-    return backward_type<float>(p, k, stream);
+    return backward_type<float>(p, k, precise, stream);
 }
 
 }  // namespace dws

@@ -47,8 +47,9 @@ constexpr int kFine = sizeof(T) == 4 ? 1 : 2;
 // times its own rounding at the median and 1.5 to 2.5 at the worst of 40 random
 // calls; with the states in two, at 10% of a training step's time, by 1.1 and 1.3
 // for heads up to 128. Chunks of wider heads are half as long, so that more comes
-// through the states: with both in two parts 1.03 instead of 1.6. (Both for all
-// heads: 540 us a training step against 477.)
+// through the states: with both in two parts 1.03 instead of 1.6. Both for all
+// heads take 505 us a training step instead of 464, and leave each gradient's own
+// rounding alone (0.01 of it before); a caller can ask for that.
 template <class T>
 constexpr int kStored = kFine<T>;
 template <class T, int DK>
@@ -804,7 +805,7 @@ __device__ __forceinline__ void delta_scan(const DeltaParams& p, uint32_t block,
 // Both scans together move 581 MB for 2,096 chunks and heads of 128 x 128 in 140
 // us, 4.2 TB/s: the memory bounds them, most of it the states and Z and U'.
 
-template <class T, int DK, int NW>
+template <class T, int DK, int ND, int NW>
 __device__ __forceinline__ void delta_scan_back(const DeltaParams& p, uint32_t block, char* smem)
 {
     constexpr int NF = kFine<T>;
@@ -874,12 +875,12 @@ __device__ __forceinline__ void delta_scan_back(const DeltaParams& p, uint32_t b
         const T* os = reinterpret_cast<const T*>(buffer + L::vs);
         const float* gate = reinterpret_cast<const float*>(buffer + L::gate);
         const int64_t at = place_at(c);
-        Parts<T, kStoredGrad<T, DK>> db[DK / 32];
+        Parts<T, ND> db[DK / 32];
 #pragma unroll
-        for (int kb = 0; kb < DK / 32; ++kb) db[kb] = parts_of<T, kStoredGrad<T, DK>>(ds[2 * kb], ds[2 * kb + 1]);
+        for (int kb = 0; kb < DK / 32; ++kb) db[kb] = parts_of<T, ND>(ds[2 * kb], ds[2 * kb + 1]);
         if (col0 < p.dv_pad)
-            store_columns<T, kStoredGrad<T, DK>, DK>(static_cast<T*>(p.w_ds) + at * kStoredGrad<T, DK> * DK * p.dv_pad,
-                                             (int64_t)DK * p.dv_pad, db, col0 / 16, lane);
+            store_columns<T, ND, DK>(static_cast<T*>(p.w_ds) + at * ND * DK * p.dv_pad, (int64_t)DK * p.dv_pad, db,
+                                     col0 / 16, lane);
         __syncthreads();
         // dU; dO is exact in T
         Vec4<T> d_o[NB];
@@ -974,13 +975,13 @@ __global__ __launch_bounds__(NW * 128) DWS_TWO_WAVES void k_delta_scan(DeltaPara
 // The backward pass's two scans, which do not need each other: half of the
 // workgroups each, the longer ones first. Where there are fewer of them than
 // compute units both run at once.
-template <class T, int DK, int NW>
+template <class T, int DK, int ND, int NW>
 __global__ __launch_bounds__(NW * 128) DWS_TWO_WAVES void k_delta_scan_both(DeltaParams p)
 {
     extern __shared__ __attribute__((aligned(16))) char smem[];
     const uint32_t half = gridDim.x / 2;
     if (blockIdx.x < half)
-        delta_scan_back<T, DK, NW>(p, blockIdx.x, smem);
+        delta_scan_back<T, DK, ND, NW>(p, blockIdx.x, smem);
     else
         delta_scan<T, DK, kStored<T>, true, NW>(p, blockIdx.x - half, smem);
 }
@@ -1006,10 +1007,10 @@ __global__ __launch_bounds__(NW * 128) DWS_TWO_WAVES void k_delta_scan_both(Delt
 // with all 256 registers of two waves a SIMD in use one block is in flight at a
 // time, and a third of the time goes to waiting for it.
 
-template <class T, int DK>
+template <class T, int DK, int PARTS>
 struct GradLds {
     static constexpr int C = kChunk<T, DK>, NB = C / 16, GROUPS = DK / 64, THREADS = NB * GROUPS * 64;
-    static constexpr int LK = lds_stride<T>(DK), LC = lds_stride<T>(C), NF = kFine<T>, NS = kStored<T>, ND = kStoredGrad<T, DK>;
+    static constexpr int LK = lds_stride<T>(DK), LC = lds_stride<T>(C), NF = kFine<T>, NS = kStored<T>, ND = PARTS;
     static constexpr size_t ks = 0, qs = ks + (size_t)C * LK * sizeof(T), w1 = qs + (size_t)C * LK * sizeof(T);
     static constexpr size_t w2 = w1 + (size_t)NF * C * LC * sizeof(T), w_end = w2 + (size_t)NF * C * LC * sizeof(T);
     // the blocks of 32 value columns are done with before W1 and W2 are written
@@ -1059,10 +1060,10 @@ __device__ __forceinline__ void store_quads(__amdgpu_buffer_rsrc_t rsrc, bool wh
     }
 }
 
-template <class T, int DK>
-__global__ __launch_bounds__((GradLds<T, DK>::THREADS)) DWS_TWO_WAVES void k_delta_grad(DeltaParams p)
+template <class T, int DK, int PARTS>
+__global__ __launch_bounds__((GradLds<T, DK, PARTS>::THREADS)) DWS_TWO_WAVES void k_delta_grad(DeltaParams p)
 {
-    using L = GradLds<T, DK>;
+    using L = GradLds<T, DK, PARTS>;
     constexpr int C = L::C, THREADS = L::THREADS, NB = L::NB, GROUPS = L::GROUPS, LK = L::LK, LC = L::LC, LS = L::LS, NF = L::NF, NS = L::NS, ND = L::ND;
     constexpr int NK = DK / 16 / GROUPS;             // key column tiles of a wave
     constexpr int NT = NB > GROUPS ? NB / GROUPS : 1;      // its column tiles of W1 and W2: grp, grp + GROUPS, ..
@@ -1405,11 +1406,11 @@ hipError_t launch_scan(const DeltaParams& p, hipStream_t stream)
     return launch_lds(k_delta_scan<T, DK, NP, NW>, scan_blocks(p, NW), NW * 128, ScanLds<T, DK, NW, 1, NX, true>::bytes, p,
                       stream);
 }
-template <class T, int DK, int NW>
+template <class T, int DK, int ND, int NW>
 hipError_t launch_both(const DeltaParams& p, hipStream_t stream)
 {
     // the backward scan's LDS, the larger one
-    return launch_lds(k_delta_scan_both<T, DK, NW>, 2 * scan_blocks(p, NW), NW * 128,
+    return launch_lds(k_delta_scan_both<T, DK, ND, NW>, 2 * scan_blocks(p, NW), NW * 128,
                       ScanLds<T, DK, NW, 2, 2 * kFine<T>, false>::bytes, p, stream);
 }
 
@@ -1435,28 +1436,28 @@ hipError_t forward_type(const DeltaParams& p, const DeltaPack& k, hipStream_t st
     }
 }
 
-template <class T, int DK>
+template <class T, int DK, int ND>
 hipError_t backward_dk(const DeltaParams& p, hipStream_t stream)
 {
     constexpr int C = kChunk<T, DK>;
     hipError_t e = launch_lds(k_delta_prep<T, DK, 1, true>, (uint64_t)p.n_slots * p.heads_v, C * 4,
                               PrepLds<T, DK>::bytes, p, stream);
     if (e != hipSuccess) return e;
-    e = 2 * scan_blocks(p, 2) <= kComputeUnits ? launch_both<T, DK, 2>(p, stream)
-                                              : launch_both<T, DK, kMostWaves<T, DK>>(p, stream);
+    e = 2 * scan_blocks(p, 2) <= kComputeUnits ? launch_both<T, DK, ND, 2>(p, stream)
+                                              : launch_both<T, DK, ND, kMostWaves<T, DK>>(p, stream);
     if (e != hipSuccess) return e;
-    return launch_lds(k_delta_grad<T, DK>, (uint64_t)p.n_slots * p.heads_qk, GradLds<T, DK>::THREADS,
-                      GradLds<T, DK>::bytes, p, stream);
+    using L = GradLds<T, DK, ND>;
+    return launch_lds(k_delta_grad<T, DK, ND>, (uint64_t)p.n_slots * p.heads_qk, L::THREADS, L::bytes, p, stream);
 }
 template <class T>
-hipError_t backward_type(const DeltaParams& p, const DeltaPack& k, hipStream_t stream)
+hipError_t backward_type(const DeltaParams& p, const DeltaPack& k, bool precise, hipStream_t stream)
 {
     const hipError_t e = pack_rows<T>(k, p.tokens, stream);
     if (e != hipSuccess) return e;
     switch (delta_padded_k(p.dim_k)) {
-    case 64: return backward_dk<T, 64>(p, stream);
-    case 128: return backward_dk<T, 128>(p, stream);
-    default: return backward_dk<T, 256>(p, stream);
+    case 64: return precise ? backward_dk<T, 64, kFine<T>>(p, stream) : backward_dk<T, 64, kStoredGrad<T, 64>>(p, stream);
+    case 128: return precise ? backward_dk<T, 128, kFine<T>>(p, stream) : backward_dk<T, 128, kStoredGrad<T, 128>>(p, stream);
+    default: return backward_dk<T, 256, kStoredGrad<T, 256>>(p, stream);
     }
 }
 

@@ -542,7 +542,10 @@ enum {
      * states may be, and as d_final_grad of the sequence's part before has to be */
     DWS_DELTA_FP32_GRADS = 1,
     /* dws_delta_rule: the products' operands as where d_final_state is wanted, so
-     * that out has the same bits with it and without */
+     * that out has the same bits with it and without. dws_delta_rule_backward: the
+     * states' gradients in the products with the accuracy of the states, which
+     * leaves the error of each gradient's own rounding (without it that of one
+     * more operand of dtype for dim_k up to 128) */
     DWS_DELTA_PRECISE = 2
 };
 

@@ -173,7 +173,7 @@ def test_options(lib):
 
 
 def test_workspace_of_precise_outputs(lib):
-    """What a call with a final state needs, for the 16-bit types; nothing changes for fp32 and for gradients."""
+    """What a call with a final state needs, for the 16-bit types; more for gradients up to 128 key columns."""
     def need(backward=0, **more):
         n = ctypes.c_size_t(0)
         assert lib.dws_delta_rule_workspace(ctypes.byref(arguments(**more)), backward, ctypes.byref(n)) == dws.OK
@@ -182,7 +182,9 @@ def test_workspace_of_precise_outputs(lib):
     assert need(d_final_state=None) < need(d_final_state=None, options=dws.DELTA_PRECISE) == need()
     assert need(options=dws.DELTA_PRECISE) == need()
     assert need(dtype=dws.FLOAT32, d_final_state=None, options=dws.DELTA_PRECISE) == need(dtype=dws.FLOAT32)
-    assert need(1, options=dws.DELTA_PRECISE) == need(1)
+    assert need(1, options=dws.DELTA_PRECISE) > need(1)
+    for more in ({"dim_k": 200}, {"dtype": dws.FLOAT32}):
+        assert need(1, options=dws.DELTA_PRECISE, **more) == need(1, **more)
 
 
 def test_packed_options_are_the_structure():

@@ -927,3 +927,25 @@ def test_rows_far_apart(gpu):
     wide = torch.empty(n * stride, dtype=BF16, device="cuda").as_strided((n, hv, dv), (stride, dv, 1), 8)
     forward(x, offsets, initial, out=wide, final_state=True)
     assert torch.equal(wide, want)
+
+
+@pytest.mark.parametrize("dtype", [FP32, BF16, FP16])
+@pytest.mark.parametrize("lens,hk,hv,dk,dv", [([70, 0, 33], 1, 2, 64, 40), ([301], 2, 2, 128, 128), ([200, 65], 1, 2, 96, 64),
+                                              ([90], 1, 1, 200, 64), ([20, 45] * 20, 4, 8, 128, 64)])
+def test_precise_gradients(gpu, lens, hk, hv, dk, dv, dtype):
+    """No operand in one part: a rounded gradient is its rounding away from the definition, and one in fp32 at most six
+    two-part products deep (P, the inverse, dU, Z, S, dS'), off by 2^-16 each and double where sums cancel. (fp16's
+    second parts are below 2^-14, where they lose digits, but not more than bf16's have.)"""
+    x, offsets, initial = inputs(43, lens, hk, hv, dk, dv, dtype)
+    d_out = torch.randn(x["v"].shape, generator=torch.Generator().manual_seed(3)).to(dtype).cuda()
+    got = dws.delta_rule_backward(d_out, *(x[a] for a in NAMES), offsets=offsets, initial_state=initial, fp32_grads=True, precise=True)
+    want = gradients(x, offsets, initial, dk ** -0.5, d_out, None)
+    fine = 12 * 2.0 ** -16 if dtype != FP32 else 0.0
+    for what, a, b in zip(("dq", "dk", "dv", "dg", "dbeta", "d_initial"), got, want):
+        close(a, b, dtype, what)
+        off, rounding = (a.double().cpu() - b).norm().item(), (b.to(a.dtype).double() - b).norm().item()
+        most = rounding + (fine + tolerance(FP32, "state")) * b.norm().item()
+        assert off <= most, f"{what}: off by {off / rounding:.3f} times its rounding, {off / b.norm().item():.3g} of its norm"
+    if dk > 128 or dtype == FP32:        # as without
+        plain = dws.delta_rule_backward(d_out, *(x[a] for a in NAMES), offsets=offsets, initial_state=initial, fp32_grads=True)
+        assert all(torch.equal(a, b) for a, b in zip(got, plain))
