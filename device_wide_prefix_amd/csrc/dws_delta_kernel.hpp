@@ -427,8 +427,9 @@ __global__ __launch_bounds__((kChunk<T, DK> * 4)) void k_delta_prep(DeltaParams 
 // else. NW more waves, one on each of the same SIMDs, bring the next chunk's
 // tiles to LDS and work out the outputs of the last one from the states and u
 // that were left in LDS. Two LDS buffers and one barrier a chunk. A chunk of 64
-// tokens of a 128 x 128 head takes 2.0 us with two state-carrying waves and 3.3 us
-// with four and three parts (the same waves doing all of it: a third longer).
+// tokens of a 128 x 128 head takes 1.8 us with two state-carrying waves (2.5 us with
+// three parts) on half of the compute units, 2.3 us (3.2) on all of them, and 2.9 us
+// (5.0) with four. (The same waves doing all of it took a third longer.)
 // What bounds it is that chain of products, LDS reads and splittings; the matrix
 // cores are busy for a third of it.
 
@@ -802,8 +803,8 @@ __device__ __forceinline__ void delta_scan(const DeltaParams& p, uint32_t block,
 // The same shape as the forward scan, from a sequence's last chunk to its
 // first. Z and dS' go to the workspace; the next kernel, which has Z by rows,
 // writes dV (16 two-byte stores a lane here were a third of a chunk's time).
-// Both scans together move 581 MB for 2,096 chunks and heads of 128 x 128 in 140
-// us, 4.2 TB/s: the memory bounds them, most of it the states and Z and U'.
+// Both scans together move 580 MB for 2,096 chunks and heads of 128 x 128 in 146
+// us, 4.0 TB/s: the memory bounds them, most of it the states and Z and U'.
 
 template <class T, int DK, int ND, int NW>
 __device__ __forceinline__ void delta_scan_back(const DeltaParams& p, uint32_t block, char* smem)
@@ -1003,7 +1004,7 @@ __global__ __launch_bounds__(NW * 128) DWS_TWO_WAVES void k_delta_scan_both(Delt
 // that share the key head come in turn, so that their sums need no atomics and
 // have one order. Blocks of 32 value columns of the workspace's arrays go through
 // LDS, a row a column, where the transposing reads make operands of them. 2,096
-// chunks and value heads of 128 x 128 take 191 us: 555 MB, which would take 115, but
+// chunks and value heads of 128 x 128 take 177 us: 484 MB, which would take 90, but
 // with all 256 registers of two waves a SIMD in use one block is in flight at a
 // time, and a third of the time goes to waiting for it.
 
@@ -1136,8 +1137,8 @@ __global__ __launch_bounds__((GradLds<T, DK, PARTS>::THREADS)) DWS_TWO_WAVES voi
         float zdotu = 0.f, sds = 0.f;
         for (int c = 0; c < p.dv_pad; c += 32) {
             // (made unknown, so that the loop's addresses are worked out in each
-            // turn: kept over the turns they take registers and spill, 196 us
-            // instead of 191)
+            // turn: kept over the turns they take registers and spill, 190 us
+            // instead of 178)
             int here = tid;
             asm volatile("" : "+v"(here));
             const int lane = here & 63, gq = lane >> 4, lr = lane & 15;
@@ -1359,7 +1360,9 @@ hipError_t launch_lds(K kernel, uint64_t blocks, int threads, size_t lds, const 
 }
 
 // Rows that cannot be read 16 bytes at a time, copied to ones that can: padded
-// to whole units, zero behind dim.
+// to whole units, zero behind dim. 8,127 tokens of 8 key and 16 value heads of 128 x 128
+// in bf16, one element off: 168 us forward instead of 113, 463 backward instead of 356,
+// 18 us an array. It is for callers who cannot lay their rows out in whole units.
 template <class T>
 __global__ __launch_bounds__(256) void k_delta_pack(DeltaRows src, T* dst, int64_t tokens, int heads, int dim, int padded)
 {
@@ -1393,7 +1396,8 @@ inline uint64_t scan_blocks(const DeltaParams& p, int waves)
 // chunks take less time, as long as every workgroup still has a compute unit to
 // itself: 8,192 tokens of 64 heads of 128 x 128 forward in 386 us with two and 440
 // with four, of 72 heads 651 and 474; backward 711 and 787 with 32 heads, 1,136 and
-// 1,020 with 48. And two for fp32 heads above 128, whose tiles and states leave
+// 1,020 with 48. (Sequences are counted, an empty one like a long one: their lengths
+// are on the device.) And two for fp32 heads above 128, whose tiles and states leave
 // LDS for no more.
 template <class T, int DK>
 constexpr int kMostWaves = sizeof(T) == 4 && DK > 128 ? 2 : 4;

@@ -4,7 +4,8 @@
 // With a = e^g, and S the state before the token:
 //   u = beta (v - a S^T k);   S <- a S + k u^T;   o = scale S^T q = scale (a S^T q + (k . q) u)
 // so one pass over S gives both S^T k and S^T q, and only S itself is written.
-// Bound by the state's bytes: 8 dim_k dim_v for each head and token.
+// Bound by the state's bytes: 8 dim_k dim_v for each head and sequence, however many
+// tokens it has.
 #include "dws_delta_device.hpp"
 
 namespace dws {
