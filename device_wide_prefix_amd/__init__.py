@@ -802,8 +802,8 @@ def delta_rule_backward(d_out, q, k, v, g, beta, offsets=None, initial_state=Non
     result(s). Returns (dq, dk, dv, dg, dbeta, d_initial_state) in the type of q, dg None without g and
     d_initial_state None without initial_state; rows in no sequence are 0. fp32_grads: dg, dbeta and d_initial_state in
     float32, as g and the states may be; the last is then d_final_state for the sequence's part before. precise: the
-    states' gradients in 16-bit products in two parts, so that only each result's own rounding is left. They have no graph of their own (no second
-    derivatives)."""
+    states' gradients in 16-bit products in two parts, so that only each result's own rounding is left. They have no graph
+    of their own (no second derivatives)."""
     import torch
     a, device = _delta_args(q, k, v, g, beta, offsets, 1, scale)
     a[_OUT_GRAD: _OUT_GRAD + 3] = _rows(d_out, "d_out", v.shape, q.dtype, device)

@@ -559,9 +559,9 @@ enum {
  * they hold, nothing outside the arrays is touched.
  *
  * dtype (DWS_FLOAT32, DWS_FLOAT16 or DWS_BFLOAT16) is that of q, k, v, out and
- * of every gradient (without DWS_DELTA_FP32_GRADS). g (the natural logarithm of the decay; -infinity forgets
- * the state; data == NULL for no decay) and beta have dtypes of their own among
- * the three. dim_k and dim_v are at most 256; heads_v is a multiple of heads_qk,
+ * of every gradient (without DWS_DELTA_FP32_GRADS). g (the natural logarithm of
+ * the decay; -infinity forgets the state; data == NULL for no decay) and beta have
+ * dtypes of their own among the three. dim_k and dim_v are at most 256; heads_v is a multiple of heads_qk,
  * and value head h uses query/key head h / (heads_v / heads_qk).
  *
  * States are fp32, (count, heads_v, dim_k, dim_v), contiguous. Without d_slots
