@@ -59,6 +59,8 @@ EXPORTED_SYMBOLS = (
     "dws_reduce", "dws_scan_op_seeded", "dws_reduce_op", "dws_select_if", "dws_partition_if",
     "dws_delta_rule_workspace", "dws_delta_rule", "dws_delta_rule_backward", "dws_delta_rule_step",
     "dws_pages_workspace", "dws_pages_grow", "dws_pages_fork", "dws_pages_free", "dws_pages_compact", "dws_pages_copy",
+    "dws_pages_append", "dws_pages_attention_workspace", "dws_pages_attention", "dws_beam_select_workspace",
+    "dws_beam_select",
 )
 
 
@@ -103,6 +105,50 @@ class PageCache(ctypes.Structure):
     _fields_ = [("d_refs", ctypes.c_void_p), ("n_pages", ctypes.c_longlong), ("d_table", ctypes.c_void_p),
                 ("n_rows", ctypes.c_longlong), ("max_pages", ctypes.c_longlong), ("d_lengths", ctypes.c_void_p),
                 ("page_tokens", ctypes.c_longlong)]
+
+
+class PagePool(ctypes.Structure):
+    """dws_page_pool: the keys or values of a pool's pages."""
+    _fields_ = [("data", ctypes.c_void_p)] + [(x, ctypes.c_longlong) for x in ("page_stride", "token_stride", "head_stride")]
+
+
+class KvCache(ctypes.Structure):
+    """dws_kv_cache."""
+    _fields_ = ([("keys", PagePool), ("values", PagePool), ("d_table", ctypes.c_void_p), ("d_lengths", ctypes.c_void_p)] +
+                [(x, ctypes.c_longlong) for x in ("n_pages", "n_rows", "max_pages", "page_tokens")] +
+                [(x, ctypes.c_int) for x in ("heads", "dim_k", "dim_v", "dtype")])
+
+
+class PageSeqs(ctypes.Structure):
+    """dws_page_seqs."""
+    _fields_ = [("tokens", ctypes.c_longlong), ("n", ctypes.c_longlong), ("d_offsets", ctypes.c_void_p),
+                ("d_rows", ctypes.c_void_p)]
+
+
+class PagesAppendArgs(ctypes.Structure):
+    """dws_pages_append_args."""
+    _fields_ = ([("cache", KvCache), ("seqs", PageSeqs)] +
+                [(x, ctypes.c_void_p) for x in ("d_granted", "d_positions", "d_freqs")] +
+                [(x, ctypes.c_int) for x in ("pairs", "adjacent", "heads_q", "zero_rest")] +
+                [(x, Rows) for x in ("k", "v", "q", "q_out")])
+
+
+class PagesAttentionArgs(ctypes.Structure):
+    """dws_pages_attention_args."""
+    _fields_ = [("cache", KvCache), ("seqs", PageSeqs), ("heads_q", ctypes.c_int), ("scale", ctypes.c_float),
+                ("n_groups", ctypes.c_longlong), ("d_groups", ctypes.c_void_p), ("d_shared", ctypes.c_void_p),
+                ("zero_rest", ctypes.c_int), ("q", Rows), ("out", Rows), ("d_lse", ctypes.c_void_p),
+                ("d_workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t)]
+
+
+class BeamArgs(ctypes.Structure):
+    """dws_beam_args."""
+    _fields_ = ([("d_logits", ctypes.c_void_p)] +
+                [(x, ctypes.c_longlong) for x in ("batch", "beams", "vocab", "batch_stride", "beam_stride")] +
+                [("dtype", ctypes.c_int), ("k", ctypes.c_int), ("d_scores", ctypes.c_void_p), ("d_finished", ctypes.c_void_p),
+                 ("end_token", ctypes.c_longlong)] +
+                [(x, ctypes.c_void_p) for x in ("d_rows", "d_out_scores", "d_parents", "d_tokens", "d_out_rows", "d_src",
+                                                "d_dst", "d_workspace")] + [("workspace_bytes", ctypes.c_size_t)])
 
 
 _lib = None
@@ -191,6 +237,15 @@ def load_library():
                        ("copy", [vp, ll, ll, ll, ll, vp, vp, ll, vp, vp])):
         f = getattr(lib, "dws_pages_" + name)
         f.argtypes = args
+        f.restype = ci
+    # (and the arguments of the calls on cached keys and values and of the beam selection)
+    for name in ("dws_pages_append", "dws_pages_attention", "dws_beam_select"):
+        f = getattr(lib, name)
+        f.argtypes = [vp, vp]
+        f.restype = ci
+    for name in ("dws_pages_attention_workspace", "dws_beam_select_workspace"):
+        f = getattr(lib, name)
+        f.argtypes = [vp, ctypes.POINTER(sz)]
         f.restype = ci
     lib.dws_selftest_wave.argtypes = [vp, vp, vp, sz, ci, vp]
     lib.dws_selftest_wave.restype = ci
@@ -969,6 +1024,212 @@ def pages_copy(pool, src, dst, count=None, page_dim=0, stream=None):
         _check(load_library().dws_pages_copy(pool.data_ptr(), pages, layer_bytes // pages if pages else 0, layers,
                                              layer_bytes, a, b, n, k, s), "dws_pages_copy")
     return pool
+
+
+# ---- keys and values in pages ------------------------------------------------
+
+_KV = "PqqqPqqqPPqqqqiiii" + "qqPP"      # dws_kv_cache, dws_page_seqs
+_APPEND = struct.Struct("@" + _KV + "PPPiiii" + 4 * "Pqq")
+_ATTENTION = struct.Struct("@" + _KV + "ifqPPi" + 2 * "Pqq" + "PPQ")
+_BEAM = struct.Struct("@PqqqqqiiPPq" + 8 * "P" + "Q")
+
+
+def _pool(t, what, pages, page_tokens, heads, dtype, device):
+    """dws_page_pool of t (pages, page_tokens, heads, dim) and its dim."""
+    try:
+        ok = t.dim() == 4 and t.dtype == dtype and t.device == device and t.shape[:3] == (pages, page_tokens, heads) and \
+            (t.stride(3) == 1 or t.shape[3] <= 1)
+    except AttributeError:
+        ok = False
+    if not ok:
+        raise ValueError(f"{what} must have shape {(pages, page_tokens, heads)} + (dim,), dtype {dtype} and a contiguous "
+                         f"last dimension, and be on {device}")
+    return (t.data_ptr(), *t.stride()[:3]), t.shape[3]
+
+
+def _kv_args(keys, values, table, lengths, tokens, rows, offsets):
+    """The values of dws_kv_cache and dws_page_seqs; checks shapes, types and devices. Returns (values, device, n)."""
+    _gpu_tensor(keys, "keys")
+    if keys.dim() != 4:
+        raise ValueError("keys and values must be (pages, page_tokens, heads, dim)")
+    device, dtype = keys.device, keys.dtype
+    code = _float_code(dtype, "keys")
+    shape = keys.shape[:3]
+    k, dim_k = _pool(keys, "keys", *shape, dtype, device)
+    v, dim_v = _pool(values, "values", *shape, dtype, device)
+    int32 = _int32()
+    try:
+        ok = table.dtype == int32 and table.dim() == 2 and table.device == device and table.is_contiguous()
+    except AttributeError:
+        ok = False
+    if not ok:
+        raise ValueError(f"table must be a contiguous int32 tensor (rows, pages) on {device}")
+    n_rows, max_pages = table.shape
+    held = _device_ints(lengths, "lengths", int32, n_rows, device)
+    at = of = None
+    n = n_rows
+    if offsets is not None:
+        of = _device_ints(offsets, "offsets", _int64(), None, device)
+        n = offsets.shape[0] - 1
+        if n < 0:
+            raise ValueError("offsets holds one more than there are sequences")
+    if rows is not None:
+        at = _device_ints(rows, "rows", int32, n if offsets is not None else None, device)
+        n = rows.shape[0]
+    if rows is None and n > n_rows:
+        raise ValueError(f"{n} sequences, but the table has {n_rows} rows")
+    if offsets is None and (tokens % n if n else tokens):
+        raise ValueError(f"{tokens} tokens cannot be shared out to {n} sequences")
+    return (*k, *v, table.data_ptr(), held, shape[0], n_rows, max_pages, shape[1], shape[2], dim_k, dim_v, code,
+            tokens, n, of or 0, at or 0), device, n
+
+
+def pages_append(keys, values, table, lengths, k, v, rows=None, offsets=None, granted=None, positions=None, freqs=None,
+                 adjacent=False, q=None, q_out=None, stream=None):
+    """Keys and values of new tokens into the pages of a cache, turned by their positions on the way (dws_pages_append).
+
+    keys, values: (pages, page_tokens, heads, dim) views of one layer's pool, float32, float16 or bfloat16, any strides with
+    a contiguous last dimension; table (rows, max_pages) and lengths (rows,): int32 GPU tensors, as the other page calls
+    have them, the new tokens counted already (pages_grow). k: (tokens, heads, dim_k), v: (tokens, heads, dim_v): the last
+    tokens of rows ``rows`` (int32 GPU tensor; None: rows 0, 1, ...), shared out evenly or by offsets (int64 GPU tensor,
+    n + 1). granted (as pages_grow returns it): sequences with 0 are left out, as are rows outside the table, those that an
+    earlier sequence names, and sequences that have more tokens than their row.
+
+    freqs: float32 GPU tensor, the angle between neighbouring positions for each pair of the first 2 * len(freqs) dimensions
+    of k and q; pairs are (j, j + len(freqs)), or (2 j, 2 j + 1) with adjacent. positions (int32, one a token) replaces the
+    place in the row in the angles. q: (tokens, heads_q, dim_k) to be turned likewise, into q_out, which may be q (None: a new
+    tensor, 0 where the token is left out). Returns q_out, or None without q."""
+    import torch
+    _records_no_graph("pages_append", keys, values, k, v, q, q_out)
+    _gpu_tensor(k, "k")
+    tokens = k.shape[0] if k.dim() == 3 else -1
+    a, device, n = _kv_args(keys, values, table, lengths, max(tokens, 0), rows, offsets)
+    dtype, heads, dim_k, dim_v = keys.dtype, keys.shape[2], keys.shape[3], values.shape[3]
+    kr, vr = _rows(k, "k", (tokens, heads, dim_k), dtype, device), _rows(v, "v", (tokens, heads, dim_v), dtype, device)
+    ok = 0 if granted is None else _device_ints(granted, "granted", torch.int32, n, device)
+    at = 0 if positions is None else _device_ints(positions, "positions", torch.int32, tokens, device)
+    pairs = by = 0
+    if freqs is not None:
+        by, pairs = _device_ints(freqs, "freqs", torch.float32, None, device), freqs.shape[0]
+        if 2 * pairs > dim_k:
+            raise ValueError(f"{pairs} pairs do not fit {dim_k} dimensions")
+    if q is None and q_out is not None:
+        raise ValueError("q_out needs q")
+    with _on_stream(keys, stream) as s:
+        heads_q, zero, qr, to = 0, 0, (0, 0, 0), (0, 0, 0)
+        if q is not None:
+            _gpu_tensor(q, "q")
+            if q.dim() != 3:
+                raise ValueError("q must be (tokens, heads_q, dim_k)")
+            heads_q = q.shape[1]
+            qr = _rows(q, "q", (tokens, heads_q, dim_k), dtype, device)
+            if q_out is None:
+                q_out, zero = torch.empty(q.shape, dtype=dtype, device=device), 1
+            to = _rows(q_out, "q_out", q.shape, dtype, device)
+        _check(load_library().dws_pages_append(
+            _APPEND.pack(*a, ok, at, by, pairs, bool(adjacent), heads_q, zero, *kr, *vr, *qr, *to), s), "dws_pages_append")
+    return q_out
+
+
+def pages_attention(q, keys, values, table, lengths, rows=None, offsets=None, groups=None, shared=None, scale=None, out=None,
+                    lse=None, stream=None):
+    """Attention of each token's queries with the tokens of its row up to its own (dws_pages_attention).
+
+    q: (tokens, heads_q, dim_k); keys, values, table, lengths, rows and offsets as pages_append, whose tokens these are, one
+    a sequence or as many as a prompt has; heads_q is a multiple of the cache's heads. groups (int64 GPU tensor, groups + 1)
+    and shared (int32 GPU tensor): the first shared[g] tokens of sequences groups[g] .. groups[g + 1] - 1 are in the same
+    pages, as pages_fork leaves them, and are read once for all of these. scale: dim_k^-0.5 by default. Queries that see
+    nothing give 0. Rows of ``out`` in no sequence stay as they were, and are 0 in a new one. lse: None, True for a new
+    float32 (tokens, heads_q) tensor of the logarithms of the exponentials' sums, or one to write.
+    Returns out, or (out, lse)."""
+    import torch
+    _records_no_graph("pages_attention", q, keys, values, out, lse if lse is not True else None)
+    _gpu_tensor(q, "q")
+    if q.dim() != 3:
+        raise ValueError("q must be (tokens, heads_q, dim_k)")
+    tokens, heads_q = q.shape[:2]
+    a, device, n = _kv_args(keys, values, table, lengths, tokens, rows, offsets)
+    dtype, dim_k, dim_v = keys.dtype, keys.shape[3], values.shape[3]
+    if heads_q < 1 or heads_q % keys.shape[2]:
+        raise ValueError(f"{heads_q} query heads are no multiple of {keys.shape[2]}")
+    qr = _rows(q, "q", (tokens, heads_q, dim_k), dtype, device)
+    n_groups = gp = sh = 0
+    if (groups is None) != (shared is None):
+        raise ValueError("groups and shared go together")
+    if groups is not None:
+        gp, n_groups = _device_ints(groups, "groups", torch.int64, None, device), groups.shape[0] - 1
+        sh = _device_ints(shared, "shared", torch.int32, n_groups, device)
+    with _on_stream(q, stream) as s:
+        zero = 0
+        if out is None:
+            out, zero = torch.empty((tokens, heads_q, dim_v), dtype=dtype, device=device), int(offsets is not None)
+        elif lse is True and offsets is not None:
+            lse = torch.full((tokens, heads_q), float("-inf"), dtype=torch.float32, device=device)
+        to = _rows(out, "out", (tokens, heads_q, dim_v), dtype, device)
+        if lse is True:
+            lse = torch.empty((tokens, heads_q), dtype=torch.float32, device=device)
+        if lse is not None and not (isinstance(lse, torch.Tensor) and lse.dtype == torch.float32 and lse.device == device and
+                                    lse.shape == (tokens, heads_q) and lse.is_contiguous()):
+            raise ValueError(f"lse must be a contiguous float32 tensor {(tokens, heads_q)} on {device}")
+        to_lse = 0 if lse is None else lse.data_ptr()
+        rest = (heads_q, dim_k ** -0.5 if scale is None else float(scale), n_groups, gp, sh, zero, *qr, *to, to_lse)
+        need, lib = ctypes.c_size_t(0), load_library()
+        _check(lib.dws_pages_attention_workspace(_ATTENTION.pack(*a, *rest, 0, 0), ctypes.byref(need)),
+               "dws_pages_attention_workspace")
+        work = torch.empty(need.value, dtype=torch.uint8, device=device)
+        _check(lib.dws_pages_attention(_ATTENTION.pack(*a, *rest, work.data_ptr(), need.value), s), "dws_pages_attention")
+        del work
+    return out if lse is None else (out, lse)
+
+
+# ---- beam search ---------------------------------------------------------------
+
+def beam_select(logits, scores, k=None, finished=None, end_token=0, rows=None, stream=None):
+    """For each request the k (None: as many as beams) continuations of its beams with the largest
+    scores[beam] + log softmax(logits[beam])[token], in descending order, the lowest beam and token first among equal ones
+    (dws_beam_select).
+
+    logits: (batch, beams, vocab), float32, float16 or bfloat16, any strides with a contiguous last dimension; scores:
+    float32 (batch, beams). finished: bool or uint8 (batch, beams), beams that go on with end_token alone, at their score.
+    Returns (scores (batch, k) float32, parents (batch, k) int32, tokens (batch, k) int32).
+    With rows (int32 (batch, beams): cache rows or state slots of the beams; needs k == beams) also (rows, src, dst): the
+    continuations' rows, and which to copy where (batch * beams each, -1: none). States follow with
+    pages_copy(pool, src, dst), rows of pages with pages_free(.., dst, ..), pages_fork(.., src, dst, ..) and pages_copy."""
+    import torch
+    _records_no_graph("beam_select", logits, scores)
+    _gpu_tensor(logits, "logits")
+    if logits.dim() != 3 or (logits.stride(2) != 1 and logits.shape[2] > 1):
+        raise ValueError("logits must be (batch, beams, vocab), contiguous in the last dimension")
+    device, code = logits.device, _float_code(logits.dtype, "logits")
+    batch, beams, vocab = logits.shape
+    k = beams if k is None else int(k)
+
+    def plain(t, what, *dtypes):
+        if not (isinstance(t, torch.Tensor) and t.dtype in dtypes and t.shape == (batch, beams) and t.device == device and
+                t.is_contiguous()):
+            raise ValueError(f"{what} must be a contiguous {dtypes[0]} tensor {(batch, beams)} on {device}")
+        return t.data_ptr()
+
+    of = plain(scores, "scores", torch.float32)
+    over = 0 if finished is None else plain(finished, "finished", torch.bool, torch.uint8)
+    at = 0 if rows is None else plain(rows, "rows", torch.int32)
+    if rows is not None and k != beams:
+        raise ValueError("rows can be followed only with as many continuations as beams")
+    with _on_stream(logits, stream) as s:
+        best = torch.empty((batch, k), dtype=torch.float32, device=device)
+        parents, tokens = torch.empty((2, batch, k), dtype=torch.int32, device=device).unbind(0)
+        moves = (0, 0, 0)
+        if rows is not None:
+            new, src, dst = torch.empty((3, batch * beams), dtype=torch.int32, device=device).unbind(0)
+            moves = new.data_ptr(), src.data_ptr(), dst.data_ptr()
+        a = (logits.data_ptr(), batch, beams, vocab, logits.stride(0), logits.stride(1), code, k, of, over, int(end_token), at,
+             best.data_ptr(), parents.data_ptr(), tokens.data_ptr(), *moves)
+        need, lib = ctypes.c_size_t(0), load_library()
+        _check(lib.dws_beam_select_workspace(_BEAM.pack(*a, 0, 0), ctypes.byref(need)), "dws_beam_select_workspace")
+        work = torch.empty(need.value, dtype=torch.uint8, device=device)
+        _check(lib.dws_beam_select(_BEAM.pack(*a, work.data_ptr(), need.value), s), "dws_beam_select")
+        del work
+    return (best, parents, tokens) if rows is None else (best, parents, tokens, new.view(batch, beams), src, dst)
 
 
 def device_memory_info() -> dict:

@@ -22,7 +22,9 @@ ARCH = "gfx950"
 SOURCES = ["dws_sp_u32.hip", "dws_sp_f32.hip", "dws_aux.hip", "dws_stp.hip", "dws_select.hip", "dws_reduce.hip",
            "dws_op_minmax.hip", "dws_op_pairsum.hip", "dws_op_affine.hip", "dws_op_segsum.hip", "dws_rbk.hip",
            "dws_static.hip", "dws_delta_bf16.hip", "dws_delta_f16.hip", "dws_delta_f32.hip", "dws_delta_step.hip",
-           "dws_pages.hip", "dws_single_pass_host.cpp", "dws_delta_abi.cpp", "dws_pages_abi.cpp", "dws_abi.cpp"]
+           "dws_pages.hip", "dws_attention_bf16.hip", "dws_attention_f16.hip", "dws_attention_f32.hip",
+           "dws_attention_plan.hip", "dws_cache_append.hip", "dws_beam.hip", "dws_single_pass_host.cpp",
+           "dws_delta_abi.cpp", "dws_pages_abi.cpp", "dws_cache_abi.cpp", "dws_beam_abi.cpp", "dws_abi.cpp"]
 
 COMMON_FLAGS = [
     f"--offload-arch={ARCH}",

@@ -749,6 +749,159 @@ dws_status dws_pages_copy(void* d_pool, long long n_pages, long long page_bytes,
                           long long layer_stride, const int* d_src, const int* d_dst, long long n,
                           const long long* d_count, hipStream_t stream);
 
+/* ---- keys and values in pages ------------------------------------------------
+ *
+ * What fills the pages of a dws_page_cache with one layer's keys and values, and
+ * what reads them. Token t of row r lies at place t % page_tokens of page
+ * d_table[r * max_pages + t / page_tokens]; a row's tokens are numbered from 0 to
+ * d_lengths[r] - 1.
+ */
+
+/* A pool of pages: element d of head h of the token at place s of page p is at
+ * p * page_stride + s * token_stride + h * head_stride + d (strides in elements,
+ * not negative, at most 2^40). */
+typedef struct dws_page_pool {
+    void* data;
+    long long page_stride, token_stride, head_stride;
+} dws_page_pool;
+
+/* One layer's keys and values, and where rows have them. dtype: DWS_FLOAT32,
+ * DWS_FLOAT16 or DWS_BFLOAT16. d_table and d_lengths are read only. At most 2^24
+ * pages, 2^31 - 1 rows, entries a row and tokens a page or row, 65,535 heads,
+ * dimensions of 256. */
+typedef struct dws_kv_cache {
+    dws_page_pool keys, values;         /* dim: dim_k, dim_v */
+    const int* d_table;
+    const int* d_lengths;
+    long long n_pages, n_rows, max_pages, page_tokens;
+    int heads, dim_k, dim_v, dtype;
+} dws_kv_cache;
+
+/* The tokens of a call: `tokens` rows of its arrays hold n sequences one after
+ * another, sequence i the rows d_offsets[i] .. d_offsets[i+1] - 1 (DEVICE, n + 1
+ * int64, not decreasing; NULL: tokens / n each). They are the last tokens of cache
+ * row d_rows[i] (DEVICE, n int32; NULL: row i): with T of them, row d_rows[i]'s
+ * tokens d_lengths - T .. d_lengths - 1. Whatever the arrays hold, nothing outside
+ * the operands is touched. */
+typedef struct dws_page_seqs {
+    long long tokens, n;
+    const long long* d_offsets;
+    const int* d_rows;
+} dws_page_seqs;
+
+/* Arguments of dws_pages_append; set unused members to 0. */
+typedef struct dws_pages_append_args {
+    dws_kv_cache cache;
+    dws_page_seqs seqs;
+    const int* d_granted;       /* n, or NULL: sequences with 0 are left out (as dws_pages_grow gives it) */
+    const int* d_positions;     /* tokens, or NULL: what angles go by instead of the place in the row */
+    const float* d_freqs;       /* pairs: the angle between neighbouring positions, in radians */
+    int pairs;                  /* dimensions that are turned, halved; 0: none */
+    int adjacent;               /* 0: dimensions j and j + pairs are a pair; else 2 j and 2 j + 1 */
+    int heads_q;                /* 0: no queries */
+    int zero_rest;              /* != 0: rows of q_out whose token is left out become 0 */
+    dws_rows k, v;              /* (tokens, cache.heads, dim) */
+    dws_rows q, q_out;          /* (tokens, heads_q, dim_k); q_out may be q */
+} dws_pages_append_args;
+
+/*
+ * Writes the tokens' keys and values into the pages, after dws_pages_grow made
+ * room. Each pair (a, b) of the first 2 * pairs dimensions of keys and queries
+ * becomes (a cos x - b sin x, a sin x + b cos x), x = position * d_freqs[pair], in
+ * fp32, rounded once; x is reduced in fp64, so far positions lose nothing.
+ * Left out are sequences with a row outside the table, 0 in d_granted or a row that
+ * an earlier sequence of the call names (searched for, work that grows with the
+ * square of n), sequences with more tokens than their row or a row longer than
+ * max_pages pages. A token whose page is outside the pool is not written; its query
+ * is. Two rows with one page in common must not both write to it. Errors, checked
+ * before any HIP call: a NULL structure or required pointer, sizes, strides or types
+ * out of range, an output that names an element twice, heads_q above 0 without q and
+ * q_out, pairs beyond dim_k / 2, tokens not a multiple of n without d_offsets give
+ * DWS_ERR_INVALID_ARG; sizes beyond the limits DWS_ERR_UNSUPPORTED; a pointer not
+ * aligned to its element DWS_ERR_MISALIGNED; outputs that meet another operand
+ * DWS_ERR_OVERLAP (parts of one array side by side do not meet). Asynchronous,
+ * allocates nothing, may be captured.
+ */
+dws_status dws_pages_append(const dws_pages_append_args* args, hipStream_t stream);
+
+/* Arguments of dws_pages_attention; set unused members to 0. */
+typedef struct dws_pages_attention_args {
+    dws_kv_cache cache;
+    dws_page_seqs seqs;
+    int heads_q;                /* a multiple of cache.heads: query head h uses head h / (heads_q / cache.heads) */
+    float scale;                /* finite */
+    /* Sequences that begin alike: group g is sequences d_groups[g] .. d_groups[g+1] - 1 (DEVICE, n_groups + 1 int64, not
+     * decreasing), and the first d_shared[g] (DEVICE, n_groups int32) tokens of their rows are in the same pages, which
+     * are read once for all of them. Both NULL and n_groups 0 without groups. */
+    long long n_groups;
+    const long long* d_groups;
+    const int* d_shared;
+    int zero_rest;              /* != 0: rows of out (and d_lse: -infinity) before the first and behind the last sequence are set */
+    dws_rows q, out;            /* (tokens, heads_q, dim_k), (tokens, heads_q, dim_v) */
+    float* d_lse;               /* (tokens, heads_q), contiguous: natural logarithm of the sum of the exponentials; NULL: not wanted */
+    void* d_workspace;          /* DEVICE, 256-byte aligned */
+    size_t workspace_bytes;
+} dws_pages_attention_args;
+
+/* Bytes of workspace that dws_pages_attention needs with these sizes (host only, no HIP call; pointers and strides
+ * are not read). It holds nothing between calls, and calls that may run at the same time, replays of captured graphs among
+ * them, need one each. */
+dws_status dws_pages_attention_workspace(const dws_pages_attention_args* args, size_t* bytes);
+
+/*
+ * Attention of each token's queries with the keys and values of its row up to its own place, the call's own tokens
+ * (dws_pages_append first) included: out = sum p_t v_t with p the softmax of scale q . k_t over them. For one token a
+ * sequence, a few, or whole prompts behind what is there. A query that sees nothing (a row outside the table, a sequence
+ * with more tokens than its row, a row longer than max_pages pages, pages outside the pool) gives 0, and -infinity in d_lse. Scores, their statistics and
+ * all sums are fp32; with 16-bit inputs the probabilities are rounded to dtype for their product with the values. What is
+ * behind a row's end is not read, whatever the pages hold there. Values that are not finite reach the queries that see
+ * them, and no others. d_shared must say the truth: the shared tokens are read from the pages of the group's first
+ * sequence. Results do not depend on scheduling. Errors as dws_pages_append, and too small a workspace:
+ * DWS_ERR_INVALID_ARG. Asynchronous, allocates nothing, may be captured.
+ */
+dws_status dws_pages_attention(const dws_pages_attention_args* args, hipStream_t stream);
+
+/* ---- beam search --------------------------------------------------------------- */
+
+/* Arguments of dws_beam_select; set unused members to 0. All pointers DEVICE. */
+typedef struct dws_beam_args {
+    const void* d_logits;               /* (batch, beams, vocab) of dtype (DWS_FLOAT32, DWS_FLOAT16, DWS_BFLOAT16) */
+    long long batch, beams, vocab;      /* at most 64 beams, batch * beams and vocab below 2^31 */
+    long long batch_stride, beam_stride;    /* in elements, not negative, at most 2^40 */
+    int dtype;
+    int k;                              /* continuations of a request: 1 .. 64, at most beams * vocab */
+    const float* d_scores;              /* (batch, beams) */
+    const unsigned char* d_finished;    /* (batch, beams), or NULL: beams that go on with end_token alone */
+    long long end_token;                /* 0 .. vocab - 1 where d_finished is given */
+    const int* d_rows;                  /* (batch, beams), or NULL; needs k == beams */
+    float* d_out_scores;                /* (batch, k) */
+    int* d_parents;                     /* (batch, k): 0 .. beams - 1 */
+    int* d_tokens;                      /* (batch, k) */
+    int* d_out_rows;                    /* (batch, beams); this and the next two where d_rows is given */
+    int* d_src;                         /* (batch * beams) */
+    int* d_dst;
+    void* d_workspace;                  /* 256-byte aligned */
+    size_t workspace_bytes;
+} dws_beam_args;
+
+/* Bytes of workspace for dws_beam_select (host only); as dws_pages_attention_workspace. */
+dws_status dws_beam_select_workspace(const dws_beam_args* args, size_t* bytes);
+
+/*
+ * For each request the k pairs (beam, token) with the largest d_scores[beam] + log softmax(logits[beam])[token], in
+ * descending order, the lowest beam and then the lowest token first among equal ones. A beam's tokens are ordered by their
+ * logits, beams against each other in fp64, so neighbours at the border are told apart. A finished beam has one
+ * continuation, end_token at its own score, and -infinity for every other token. A beam whose score is not finite, or
+ * whose logits hold a NaN, +infinity or nothing above -infinity, has -infinity for all of them.
+ *
+ * With d_rows (the cache rows, or state slots, of the beams) continuation c gets row d_out_rows[c]: the first one of a
+ * beam keeps its row, further ones take the rows of beams without any, in order, and are to be copied there: from
+ * d_src[c] to d_dst[c], -1 where nothing is. No row is both source and destination. For states: dws_pages_copy (d_src,
+ * d_dst). For rows of pages: dws_pages_free (d_dst), dws_pages_fork (d_src, d_dst), dws_pages_copy of what that lists.
+ * Errors: as dws_pages_append. Asynchronous, allocates nothing, may be captured.
+ */
+dws_status dws_beam_select(const dws_beam_args* args, hipStream_t stream);
+
 /* Human-readable name of a status code (static string, never NULL). */
 const char* dws_status_string(dws_status status);
 
