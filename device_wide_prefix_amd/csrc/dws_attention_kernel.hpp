@@ -9,12 +9,12 @@
 // operand of O^T = V^T P^T, whose columns are again queries: rescaling is a product
 // with the lane's own factor.
 //
-// Each wave brings 32 tokens of keys and values into its part of the LDS, the next
-// ones on their way meanwhile in registers. Tiles of up to 32 queries are memory bound
-// (2 queries' products for each byte): there the waves work on their own tokens and
-// are joined at the end of the part. Larger ones are bound by the matrix products and
-// the softmax beside them: there each wave has 32 queries of its own and goes through
-// the tokens of all waves.
+// Tiles of up to 32 queries are memory bound (2 operations a query for each byte of
+// keys): their waves work on 32 tokens each and are joined at the end. Larger ones are
+// bound by the matrix products and the softmax beside them: each wave brings 16 tokens,
+// and goes with its own 32 queries (of 128 in all) through the 64 of all waves, or (of 64)
+// through half of them. Keys go by way of the LDS, then values, the ones of the next
+// piece on their way in registers while the others are multiplied.
 //
 // Fragments (32 x 32 tiles, h = lane / 32):
 //   operand  lane holds row (or column) lane % 32, contraction indices 8 h .. 8 h + 7 of
@@ -24,7 +24,7 @@
 // step are the rows above, and the transposing LDS reads bring V's in the same order.
 #pragma once
 
-#include "dws_cache_device.hpp"
+#include "dws_attention_work.hpp"
 
 namespace dws {
 namespace {
@@ -71,19 +71,26 @@ struct Attention {
     static constexpr int NCH = D / CH;                  // chunks of a row
     static constexpr int ROW = D * (int)sizeof(T);      // bytes of a row
     static constexpr int TILE = kKvTokens * ROW;        // bytes of 32 rows
+    static constexpr int RESULT = kAttnRows * D * 4;    // of a wave's results
     static constexpr int N = kKvTokens * NCH / 64;      // chunks of a tile in a lane
     static constexpr int STEP = 64 / NCH;               // rows that 64 lanes hold at a time
     static constexpr int BLOCKS = D / 32;
     static constexpr int THREADS = 64 * NW;
-    // Whether the next tiles wait in registers (8 N): not where they do not fit beside the
-    // queries' and the results', nor where rows are read element by element.
+    // Whether a piece waits in registers: not where 4 N of them do not fit, nor where rows
+    // are read element by element.
     static constexpr bool kAhead = WHOLE && N <= 16;
     static constexpr int kBatch = WHOLE ? 8 : 1;
+    // Whether a small tile's keys and values both do.
+    static constexpr bool kBoth = kAhead && D * sizeof(T) <= 256;
+    static constexpr int SUB = NW / 2;                  // tiles of 32 tokens that all waves go through at a time
 
     struct Lds {
-        char kv[NW][2 * TILE];          // keys, values; then results
+        // a wave's keys, then its values; or all waves' keys, and their values; then results
+        alignas(16) char kv[NW * (TILE > RESULT ? TILE : RESULT)];
+        AttnSeg segs[kAttnSegs + 1];
         int64_t at[NW][2][kKvTokens];   // where a token's keys and values are, -1: nowhere
-        uint32_t there[NW];             // which tokens of a tile are
+        uint32_t there[NW];             // which of a wave's tokens are there
+        int wild[2];                    // rows to compute again, of this tile and the next
         float m[kAttnRows * NW], l[kAttnRows * NW];
     };
 
@@ -100,10 +107,15 @@ struct Attention {
 
     const AttentionParams& p;
     Lds& s;
-    const int lane, wave, half, col;
-    int kv_head, tile_number;
+    int lane, half, col;
+    const int wave;
+    int kv_head, sets;                  // sets: of 32 queries, 1, 2 or 4
+    AttnSeg seg;
     AttnTile a;
-    int stop;                           // tokens of the part end here
+    bool group;
+    int turn;                           // which of Lds.wild
+    int64_t table;
+    int stop;                           // tokens of the stretch end here
     Chunk<T> q[NCH / 2];
     int position;                       // of the lane's query
     int least;                          // smallest of the wave's queries
@@ -111,13 +123,10 @@ struct Attention {
     f32x16_t o[BLOCKS];
     float m, l;
 
-    struct Ahead {
-        u32x4_t k[kAhead ? N : 1], v[kAhead ? N : 1];
-        uint32_t there;
-    };
+    uint32_t there;                     // which of the wave's tokens are
 
     __device__ __forceinline__ Attention(const AttentionParams& p, Lds& s)
-        : p(p), s(s), lane(threadIdx.x & 63), wave(__builtin_amdgcn_readfirstlane(threadIdx.x >> 6)), half(lane >> 5), col(lane & 31)
+        : p(p), s(s), lane(threadIdx.x & 63), half(lane >> 5), col(lane & 31), wave(__builtin_amdgcn_readfirstlane(threadIdx.x >> 6))
     {
     }
 
@@ -126,22 +135,37 @@ struct Attention {
         const int64_t at = a.row + r;
         if (at < (int64_t)1 << 31) {
             const uint32_t t = (uint32_t)at / (uint32_t)p.share;
-            *token = a.token + t;
+            *token = seg.begin + t;
             *head = kv_head * p.share + (int)((uint32_t)at - t * (uint32_t)p.share);
         } else {
-            *token = a.token + at / p.share;
+            *token = seg.begin + at / p.share;
             *head = kv_head * p.share + (int)(at % p.share);
         }
     }
 
-    __device__ __forceinline__ void load_queries(bool wide)
+    // Where a query of a group's tile stands in its own row; -1: nowhere.
+    __device__ __forceinline__ int position_in_group(const AttnSeg* segs, int64_t token) const
     {
-        const int r = (wide ? wave * kAttnRows : 0) + col;
+        int64_t lo = 0, hi = p.c.n - 1;
+        while (lo < hi) {
+            const int64_t mid = (lo + hi + 1) / 2;
+            if (segs[p.n_groups + mid].begin <= token)
+                lo = mid;
+            else
+                hi = mid - 1;
+        }
+        const AttnSeg& x = segs[p.n_groups + lo];
+        return x.length > 0 ? x.length - x.count + (int)(token - x.begin) : -1;
+    }
+    __device__ __forceinline__ void load_queries(const AttnSeg* segs)
+    {
+        const int r = (wave & (sets - 1)) * kAttnRows + col;
         const bool in = r < a.rows;
         int64_t token = 0;
         int head = 0;
         if (in) row_place(r, &token, &head);
-        position = !in ? INT32_MAX : (a.group ? p.positions[token] : a.position + (int)(token - a.token));
+        position = INT32_MAX;
+        if (in) position = group ? position_in_group(segs, token) : seg.length - seg.count + (int)(token - seg.begin);
         least = position;
 #pragma unroll
         for (int d = 16; d > 0; d >>= 1) {
@@ -150,10 +174,9 @@ struct Attention {
         }
         least = __builtin_amdgcn_readfirstlane(least);
         // the scale's sign goes to the queries, so that the largest product has the largest score
-        const float sign = p.scale > 0.f ? 1.f : (p.scale < 0.f ? -1.f : 0.f);
-        const double wide_c = p.scale == 0.f ? 1.0 : fabs((double)p.scale) * 1.4426950408889634;
-        c = (float)wide_c;
-        c_rest = (float)(wide_c - (double)c);
+        const float sign = p.sign;
+        c = p.log2_scale;
+        c_rest = p.log2_rest;
         const T* from = static_cast<const T*>(p.q.data) + token * p.q.ts + head * p.q.hs;
 #pragma unroll
         for (int i = 0; i < NCH / 2; ++i) {
@@ -173,12 +196,12 @@ struct Attention {
         }
     }
 
-    // The page of the token that the lane looks up (lanes 32 and on look up nothing).
-    __device__ __forceinline__ int page_of(int first) const
+    // The page of the token that the lane looks up, of `tokens`.
+    __device__ __forceinline__ int page_of(int first, int tokens) const
     {
         const int t = first + lane;
-        if (lane >= kKvTokens || (uint32_t)t >= (uint32_t)stop) return -1;
-        return p.c.table[a.table + (uint32_t)t / (uint32_t)p.c.page_tokens];
+        if (lane >= tokens || (uint32_t)t >= (uint32_t)stop) return -1;
+        return p.c.table[table + (uint32_t)t / (uint32_t)p.c.page_tokens];
     }
     // Finds the tokens of a tile, and returns which are there. (The others are read from
     // the pool's beginning, and become 0 before they are used.)
@@ -217,61 +240,47 @@ struct Attention {
         for (int j = 0; j < CH; ++j) y[j] = row && d + j < dim ? y[j] : (T)0.f;
         return __builtin_bit_cast(u32x4_t, y);
     }
-    __device__ __forceinline__ u32x4_t load_key(int i) const
+    // Row i * STEP + lane / NCH of 16 or 32 that start at row `base` of the tile (a
+    // multiple of 16); what depends on the lane alone stands apart.
+    template <bool VALUES>
+    __device__ __forceinline__ u32x4_t load(int i) const
     {
-        return load_chunk(p.c.keys.data, s.at[wave][0][i * STEP + lane / NCH], p.c.dim_k);
+        const int64_t at = s.at[wave][VALUES][i * STEP + lane / NCH];
+        return VALUES ? load_chunk(p.c.values.data, at, p.c.dim_v) : load_chunk(p.c.keys.data, at, p.c.dim_k);
     }
-    __device__ __forceinline__ u32x4_t load_value(int i) const
+    template <bool VALUES>
+    __device__ __forceinline__ void put_chunk(LdsBytes to, int i, u32x4_t x)
     {
-        return load_chunk(p.c.values.data, s.at[wave][1][i * STEP + lane / NCH], p.c.dim_v);
-    }
-    // Row i * STEP + lane / NCH; what depends on the lane alone stands apart.
-    __device__ __forceinline__ void put_key(int i, u32x4_t x)
-    {
-        const int r = lane / NCH, c = (lane % NCH) ^ key_swizzle(r);
         static_assert(STEP * SPAN == 1 || (16 % STEP == 0 && (STEP % SPAN == 0 || SPAN == 1)), "rows' bits stand apart");
-        *(InLds<u32x4_t>)(tile(wave) + r * ROW + ((c ^ key_swizzle(i * STEP)) << 4) + i * STEP * ROW) = x;
+        const int r = lane / NCH;
+        const int c = (lane % NCH) ^ (VALUES ? value_swizzle(r) : key_swizzle(r));
+        *(InLds<u32x4_t>)(to + r * ROW + ((c ^ (VALUES ? value_swizzle(i * STEP) : key_swizzle(i * STEP))) << 4) + i * STEP * ROW) = x;
     }
-    __device__ __forceinline__ void put_value(int i, u32x4_t x)
+    // Keys (values) of the wave's tokens, whose places are known, to registers and then to
+    // the LDS; 0 for what is not there.
+    template <bool VALUES, int COUNT>
+    __device__ __forceinline__ void fetch(u32x4_t (&next)[kAhead ? N : 1]) const
     {
-        const int r = lane / NCH, c = (lane % NCH) ^ value_swizzle(r);
-        *(InLds<u32x4_t>)(tile(wave) + r * ROW + ((c ^ value_swizzle(i * STEP)) << 4) + TILE + i * STEP * ROW) = x;
-    }
-    __device__ __forceinline__ LdsBytes tile(int w) const { return (LdsBytes)&s.kv[0][0] + w * (2 * TILE); }
-    __device__ __forceinline__ void fetch(Ahead* x, int first, int page)
-    {
-        x->there = places(first, page);
         if constexpr (kAhead) {
 #pragma unroll
-            for (int i = 0; i < N; ++i) x->k[i] = load_key(i);
-#pragma unroll
-            for (int i = 0; i < N; ++i) x->v[i] = load_value(i);
+            for (int i = 0; i < COUNT; ++i) next[i] = load<VALUES>(i);
         }
     }
-    __device__ __forceinline__ void put(Ahead& x)
+    template <bool VALUES, int COUNT>
+    __device__ __forceinline__ void put(LdsBytes to, u32x4_t (&next)[kAhead ? N : 1])
     {
-        const bool rest = x.there != 0xffffffffu || p.c.dim_k != D || p.c.dim_v != D;
+        const int dim = VALUES ? p.c.dim_v : p.c.dim_k;
         if constexpr (kAhead) {
-            if (rest) {
+            if (there != (uint32_t)((1ull << (COUNT * STEP)) - 1) || dim != D) {
 #pragma unroll
-                for (int i = 0; i < N; ++i) {
-                    x.k[i] = only_there(i, x.k[i], x.there, p.c.dim_k);
-                    x.v[i] = only_there(i, x.v[i], x.there, p.c.dim_v);
-                }
+                for (int i = 0; i < COUNT; ++i) next[i] = only_there(i, next[i], there, dim);
             }
 #pragma unroll
-            for (int i = 0; i < N; ++i) put_key(i, x.k[i]);
-#pragma unroll
-            for (int i = 0; i < N; ++i) put_value(i, x.v[i]);
+            for (int i = 0; i < COUNT; ++i) put_chunk<VALUES>(to, i, next[i]);
         } else {
 #pragma unroll kBatch
-            for (int i = 0; i < N; ++i) {
-                const u32x4_t k = load_key(i), v = load_value(i);
-                put_key(i, only_there(i, k, x.there, p.c.dim_k));
-                put_value(i, only_there(i, v, x.there, p.c.dim_v));
-            }
+            for (int i = 0; i < COUNT; ++i) put_chunk<VALUES>(to, i, only_there(i, load<VALUES>(i), there, dim));
         }
-        if (lane == 0) s.there[wave] = x.there;
     }
 
     // Eight (four) values of V's column (dimension) 32 block + col, of the tokens that
@@ -298,31 +307,54 @@ struct Attention {
     }
     static __device__ __forceinline__ bool finite(T x) { return __builtin_fabsf((float)x) < __builtin_inff(); }
 
-    // The wave's queries and the 32 tokens from `first` on, which wave w brought.
-    __device__ __forceinline__ void step(int w, int first)
+    // Products of a tile's 32 keys and the wave's queries.
+    __device__ __forceinline__ f32x16_t scores(LdsBytes keys) const
     {
-        const LdsBytes keys = tile(w), values = keys + TILE;
-        const uint32_t there = s.there[w];
-        f32x16_t x = {};
         const int swizzle = half ^ key_swizzle(col);
+        f32x16_t x = {};
 #pragma unroll
-        for (int i = 0; i < NCH / 2; ++i)
-            x = mma(*(InLds<Chunk<T>>)(keys + col * ROW + (((2 * i) ^ swizzle) << 4)), q[i], x);
-        const bool masked = there != 0xffffffffu || (int64_t)first + kKvTokens - 1 > least;
-        if (masked) {
+        for (int i = 0; i < NCH / 2; ++i) x = mma(*(InLds<Chunk<T>>)(keys + col * ROW + (((2 * i) ^ swizzle) << 4)), q[i], x);
+        return x;
+    }
+    // Whether there are tokens among the 32 from `first` on that not every query sees.
+    __device__ __forceinline__ bool masked(uint32_t there, int first) const
+    {
+        return there != 0xffffffffu || (int64_t)first + kKvTokens - 1 > least;
+    }
+    // A value that is not finite, of a token that not every query sees: 0 times it is not
+    // 0. Such a tile's rows are computed again, one by one, where the parts are joined.
+    __device__ __forceinline__ void note_wild(LdsBytes values)
+    {
+        bool bad = false;
+#pragma unroll 1
+        for (int i = 0; i < NCH / 2; ++i) {
+            const Chunk<T> v = *(InLds<Chunk<T>>)(values + col * ROW + ((2 * i + half) << 4));
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                const int t = 8 * (i / 4) + 4 * half + i % 4;
-                const bool sees = (there >> t & 1) && first + t <= position;
-                x[i] = sees ? x[i] : -__builtin_inff();
-            }
+            for (int j = 0; j < CH; ++j) bad |= !finite(v[j]);
+        }
+        if (__ballot(bad)) s.wild[turn] = 1;
+    }
+
+    // Scores of 32 tokens, of which the bits in `here` are there: -infinity for those that
+    // the lane's query does not see; returns the largest.
+    __device__ __forceinline__ float only_seen(f32x16_t& x, uint32_t here, int first) const
+    {
+        if (masked(here, first)) {
+            const int past = position - first;      // the last token that the query sees
+            const uint32_t sees = (here & (past < 0 ? 0u : 0xffffffffu >> (past > 31 ? 0 : 31 - past))) >> (4 * half);
+#pragma unroll
+            for (int e = 0; e < 16; ++e) x[e] = sees >> (8 * (e / 4) + e % 4) & 1 ? x[e] : -__builtin_inff();
         }
         float top = x[0];
 #pragma unroll
-        for (int i = 1; i < 16; ++i) top = fmaxf(top, x[i]);
+        for (int e = 1; e < 16; ++e) top = fmaxf(top, x[e]);
+        return top;
+    }
+    // The maximum follows once a score is 2^8 times above it: until then sums grow by
+    // that, which fp32 and fp16 hold, and the results need no rescaling.
+    __device__ __forceinline__ void follow(float top)
+    {
         top = max_halves(top) * c;
-        // The maximum follows once a score is 2^8 times above it: until then sums grow
-        // by that, which fp32 and fp16 hold, and the results need no rescaling.
         if (__ballot(top > m + 8.f)) {
             const float now = fmaxf(m, top);
             const float by = now == m ? 1.f : __builtin_amdgcn_exp2f(m - now);
@@ -331,41 +363,145 @@ struct Attention {
             for (int b = 0; b < BLOCKS; ++b) o[b] *= by;
             m = now;
         }
+    }
+    static constexpr int STEPS = 16 / CH;       // steps of the second product
+    struct Weights {
+        Chunk<T> p[STEPS];
+    };
+    __device__ __forceinline__ Weights weights(const f32x16_t& x)
+    {
+        Weights w;
         const float base = m == -__builtin_inff() ? 0.f : m;
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            float y = __builtin_fmaf(x[i], c, -base);
-            if constexpr (sizeof(T) == 4)
-                if (c_rest != 0.f && x[i] != -__builtin_inff()) y = __builtin_fmaf(x[i], c_rest, y);
-            x[i] = __builtin_amdgcn_exp2f(y);
-        }
         float sum = 0.f;
 #pragma unroll
-        for (int i = 0; i < 16; ++i) sum += x[i];
-        l += sum;
-
-        constexpr int STEPS = 16 / CH;          // steps of the second product
-        Chunk<T> pr[STEPS];
-#pragma unroll
-        for (int u = 0; u < STEPS; ++u)
-#pragma unroll
-            for (int j = 0; j < CH; ++j) pr[u][j] = (T)x[u * CH + j];
-        if (masked) {
-            // A value that is not finite, of a token that not every query sees: 0 times it is
-            // not 0. Such a tile's rows are computed again, one by one, where the parts are joined.
-            bool bad = false;
-#pragma unroll 1
-            for (int i = 0; i < NCH / 2; ++i) {
-                const Chunk<T> v = *(InLds<Chunk<T>>)(values + col * ROW + ((2 * i + half) << 4));
-#pragma unroll
-                for (int j = 0; j < CH; ++j) bad |= !finite(v[j]);
-            }
-            if (__ballot(bad)) p.wild[tile_number] = 1;
+        for (int e = 0; e < 16; ++e) {
+            float y = __builtin_fmaf(x[e], c, -base);
+            if constexpr (sizeof(T) == 4)
+                if (x[e] != -__builtin_inff()) y = __builtin_fmaf(x[e], c_rest, y);
+            y = __builtin_amdgcn_exp2f(y);
+            sum += y;
+            w.p[e / CH][e % CH] = (T)y;
         }
+        l += sum;
+        return w;
+    }
+    __device__ __forceinline__ void accumulate(LdsBytes values, const Weights& w)
+    {
 #pragma unroll
         for (int b = 0; b < BLOCKS; ++b)
 #pragma unroll
-            for (int u = 0; u < STEPS; ++u) o[b] = mma(value_fragment(values, b, u), pr[u], o[b]);
+            for (int u = 0; u < STEPS; ++u) o[b] = mma(value_fragment(values, b, u), w.p[u], o[b]);
+    }
+    // Addresses are worked out anew for each piece: kept, they push results out of the registers.
+    __device__ __forceinline__ void forget_addresses()
+    {
+        asm volatile("" : "+v"(lane));
+        half = lane >> 5;
+        col = lane & 31;
+    }
+
+    // Tokens t .. end - 1 for up to 32 queries: 32 a wave.
+    __device__ __forceinline__ void pieces_apart(int t, int end, int page)
+    {
+        constexpr int TOKENS = kKvTokens * NW;
+        const LdsBytes mine = (LdsBytes)&s.kv[0] + wave * TILE;
+        t += wave * kKvTokens;
+        if (t >= end) return;
+        // (without kBoth one set of registers serves both in turn)
+        u32x4_t next[kAhead ? N : 1], also[kBoth ? N : 1];
+        u32x4_t(&v)[kAhead ? N : 1] = value_registers(next, also);
+        uint32_t after = places(t, page);
+        fetch<false, N>(next);
+        if (kBoth) fetch<true, N>(v);
+        page = page_of(t + TOKENS, kKvTokens);
+        for (; t < end; t += TOKENS) {
+            forget_addresses();
+            there = after;
+            wave_sync();
+            put<false, N>(mine, next);
+            wave_sync();
+            const bool more = t + TOKENS < end;
+            if (!kBoth) fetch<true, N>(v);
+            if (kBoth && more) {
+                after = places(t + TOKENS, page);
+                fetch<false, N>(next);
+            }
+            f32x16_t x = scores(mine);
+            follow(only_seen(x, there, t));
+            const Weights w = weights(x);
+            wave_sync();
+            put<true, N>(mine, v);
+            wave_sync();
+            if (more) {
+                if (kBoth) {
+                    fetch<true, N>(v);
+                } else {
+                    after = places(t + TOKENS, page);
+                    fetch<false, N>(next);
+                }
+                page = page_of(t + 2 * TOKENS, kKvTokens);
+            }
+            if (masked(there, t)) note_wild(mine);
+            accumulate(mine, w);
+        }
+    }
+    static __device__ __forceinline__ auto value_registers(u32x4_t (&next)[kAhead ? N : 1], u32x4_t (&also)[kBoth ? N : 1])
+        -> u32x4_t (&)[kAhead ? N : 1]
+    {
+        if constexpr (kBoth)
+            return also;
+        else
+            return next;
+    }
+    // The same for more queries: the waves go through each other's tokens.
+    __device__ __forceinline__ void pieces_together(int t, int end, int page)
+    {
+        constexpr int TOKENS = 16 * NW, HALF = N / 2;
+        const LdsBytes keys = (LdsBytes)&s.kv[0], values = keys + SUB * TILE;
+        const int mine = wave * 16 * ROW;
+        const int subs = sets == NW ? SUB : 1, first_sub = sets == NW ? 0 : wave / sets;
+        uint32_t after = places(t + wave * 16, page);
+        u32x4_t next[kAhead ? N : 1];
+        fetch<false, HALF>(next);
+        page = page_of(t + wave * 16 + TOKENS, 16);
+        for (; t < end; t += TOKENS) {
+            forget_addresses();
+            there = after;
+            put<false, HALF>(keys + mine, next);
+            if (lane == 0) s.there[wave] = there;
+            fetch<true, HALF>(next);
+            __syncthreads();
+            f32x16_t x[SUB];
+            uint32_t here[SUB];
+            float top = -__builtin_inff();
+#pragma unroll
+            for (int r = 0; r < SUB; ++r) {
+                if (r > 0 && r >= subs) continue;
+                const int sub = first_sub + r;
+                x[r] = scores(keys + sub * TILE);
+                here[r] = __builtin_amdgcn_readfirstlane(s.there[2 * sub] | s.there[2 * sub + 1] << 16);
+                top = fmaxf(top, only_seen(x[r], here[r], t + sub * kKvTokens));
+            }
+            follow(top);
+            Weights w[SUB];
+#pragma unroll
+            for (int r = 0; r < SUB; ++r)
+                if (r == 0 || r < subs) w[r] = weights(x[r]);
+            put<true, HALF>(values + mine, next);
+            if (t + TOKENS < end) {
+                after = places(t + wave * 16 + TOKENS, page);
+                fetch<false, HALF>(next);
+                page = page_of(t + wave * 16 + 2 * TOKENS, 16);
+            }
+            __syncthreads();
+#pragma unroll
+            for (int r = 0; r < SUB; ++r) {
+                if (r > 0 && r >= subs) continue;
+                const int sub = first_sub + r;
+                if (masked(here[r], t + sub * kKvTokens)) note_wild(values + sub * TILE);
+                accumulate(values + sub * TILE, w[r]);
+            }
+        }
     }
 
     __device__ __forceinline__ void store(int64_t at, f32x4_t x, int d)
@@ -384,82 +520,77 @@ struct Attention {
         }
     }
 
-    __device__ __forceinline__ void run(int part)
+    // Pieces first_step .. last_step - 1 of the tile's keys. `part`: where partial results go.
+    __device__ __forceinline__ void run(const AttnSeg* segs, int first_step, int last_step, bool whole, int64_t part)
     {
-        const bool wide = a.rows > kAttnRows;
-        const int per = (a.steps + a.parts - 1) / a.parts;
-        constexpr int TOKENS = kKvTokens * NW;
-        const int first_step = part * per, last_step = first_step + per < a.steps ? first_step + per : a.steps;
+        sets = a.rows <= kAttnRows ? 1 : (a.rows <= 2 * kAttnRows || NW == 2 ? 2 : NW);
         stop = a.end;
-        int t = a.begin + first_step * TOKENS + wave * kKvTokens;
-        load_queries(wide);
+        table = seg.row * p.c.max_pages;
+        constexpr int PIECE = kKvTokens * NW;
+        const int t = a.begin + first_step * PIECE;
+        // (64 bits: the last piece may reach beyond 2^31)
+        const int64_t behind = (int64_t)a.begin + (int64_t)last_step * PIECE;
+        stop = behind < stop ? (int)behind : stop;
+        // the first pages are looked up while the queries come
+        const int mine = sets == 1 ? kKvTokens : 16, page = page_of(t + wave * mine, mine);
+        load_queries(segs);
         m = -__builtin_inff();
         l = 0.f;
 #pragma unroll
         for (int b = 0; b < BLOCKS; ++b) o[b] = f32x16_t{};
-        Ahead x;
-        int page = -1;
-        if (first_step < last_step) {
-            fetch(&x, t, page_of(t));
-            page = page_of(t + TOKENS);
-        }
-        for (int i = first_step; i < last_step; ++i, t += TOKENS) {
-            put(x);
-            if (i + 1 < last_step) {
-                fetch(&x, t + TOKENS, page);
-                page = page_of(t + 2 * TOKENS);
-            }
-            if (wide) __syncthreads();
-            wave_sync();
-            const int last = wide ? NW : wave + 1;
-#pragma unroll 1
-            for (int w = wide ? 0 : wave; w < last; ++w) step(w, t + (w - wave) * kKvTokens);
-            if (wide) __syncthreads();
-            wave_sync();
+        if (t < stop) {
+            if (sets == 1)
+                pieces_apart(t, stop, page);
+            else
+                pieces_together(t, stop, page);
         }
         l = sum_halves(l);
-
-        // Results by way of the LDS (a wave's own part of it), so that rows are written whole.
-        float* mine = reinterpret_cast<float*>(s.kv[wave]);
-#pragma unroll
-        for (int b = 0; b < BLOCKS; ++b)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int quad = 8 * b + 2 * j + half;
-                *reinterpret_cast<f32x4_t*>(mine + col * D + ((quad ^ (col & 15)) << 2)) =
-                    f32x4_t{o[b][4 * j], o[b][4 * j + 1], o[b][4 * j + 2], o[b][4 * j + 3]};
-            }
         if (half == 0) {
             s.m[wave * kAttnRows + col] = m;
             s.l[wave * kAttnRows + col] = l;
         }
-        __syncthreads();
+
+        float* to = nullptr;
+        float2* to_stat = nullptr;
+        if (!whole) {
+            to = p.part + part * p.tile_rows * D;
+            to_stat = p.part_stat + part * p.tile_rows;
+        } else if (seg.apart >= 0) {
+            const int64_t row = kv_head * p.max_apart + seg.apart + a.row;
+            to = p.apart + row * D;
+            to_stat = p.apart_stat + row;
+        }
+        // Results by way of the LDS (a wave's own part of it), so that rows are written whole.
         constexpr int QUADS = D / 4;
+        __syncthreads();            // the other waves are done with keys and values
+        const InLds<float> mine_out = (InLds<float>)((LdsBytes)&s.kv[0] + wave * RESULT);
+#pragma unroll
+        for (int b = 0; b < BLOCKS; ++b)
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                *(InLds<f32x4_t>)(mine_out + col * D + (((8 * b + 2 * j + half) ^ (col & 15)) << 2)) =
+                    f32x4_t{o[b][4 * j], o[b][4 * j + 1], o[b][4 * j + 2], o[b][4 * j + 3]};
+        if (threadIdx.x == 0) s.wild[turn ^ 1] = 0;
+        __syncthreads();
         for (int i = threadIdx.x; i < a.rows * QUADS; i += THREADS) {
-            const int r = i / QUADS, quad = i % QUADS;
-            const int place = (r % kAttnRows) * D + ((quad ^ (r & 15)) << 2);
+            const int r = i / QUADS, quad = i % QUADS, in = r % kAttnRows;
+            const int place = in * D + ((quad ^ (in & 15)) << 2);
             f32x4_t sum = {0.f, 0.f, 0.f, 0.f};
             float most = -__builtin_inff(), total = 0.f;
-            if (wide) {
-                most = s.m[r];
-                total = s.l[r];
-                sum = *reinterpret_cast<const f32x4_t*>(reinterpret_cast<const float*>(s.kv[r / kAttnRows]) + place);
-            } else {
-#pragma unroll
-                for (int w = 0; w < NW; ++w) most = fmaxf(most, s.l[w * kAttnRows + r] == 0.f ? most : s.m[w * kAttnRows + r]);
-#pragma unroll
-                for (int w = 0; w < NW; ++w) {
-                    const float lw = s.l[w * kAttnRows + r], mw = s.m[w * kAttnRows + r];
-                    if (lw == 0.f) continue;
-                    const float by = mw == most ? 1.f : __builtin_amdgcn_exp2f(mw - most);
-                    sum += *reinterpret_cast<const f32x4_t*>(reinterpret_cast<const float*>(s.kv[w]) + place) * by;
-                    total += lw * by;
-                }
+            // the waves that have the row's queries
+            for (int w = r / kAttnRows; w < NW; w += sets)
+                if (s.l[w * kAttnRows + in] != 0.f) most = fmaxf(most, s.m[w * kAttnRows + in]);
+            for (int w = r / kAttnRows; w < NW; w += sets) {
+                const float lw = s.l[w * kAttnRows + in], mw = s.m[w * kAttnRows + in];
+                if (lw == 0.f) continue;
+                const float by = mw == most ? 1.f : __builtin_amdgcn_exp2f(mw - most);
+                sum += *(InLds<f32x4_t>)((InLds<float>)((LdsBytes)&s.kv[0] + w * RESULT) + place) * by;
+                total += lw * by;
             }
-            if (a.slot >= 0) {
-                const int64_t row = (int64_t)kv_head * p.max_rows + a.slot + (int64_t)part * a.rows + r;
-                *reinterpret_cast<f32x4_t*>(p.partial + row * D + 4 * quad) = sum;
-                if (quad == 0) p.stat[row] = make_float2(most, total);
+            if (to != nullptr) {
+                *reinterpret_cast<f32x4_t*>(to + (int64_t)r * D + 4 * quad) = sum;
+                // (a sum below 0: rows to compute again)
+                if (quad == 0) to_stat[r] = make_float2(most, s.wild[turn] ? -1.f : total);
             } else {
                 int64_t token;
                 int head;
@@ -474,38 +605,90 @@ struct Attention {
     }
 };
 
-// An entry of the plan, the same for all lanes.
 template <class X>
-__device__ __forceinline__ X uniform_load(const X* from)
+__device__ __forceinline__ X uniform(X x)
 {
     static_assert(sizeof(X) % 4 == 0, "whole words");
-    X x;
     uint32_t w[sizeof(X) / 4];
+    __builtin_memcpy(w, &x, sizeof(X));
 #pragma unroll
-    for (size_t i = 0; i < sizeof(X) / 4; ++i)
-        w[i] = __builtin_amdgcn_readfirstlane(reinterpret_cast<const uint32_t*>(from)[i]);
+    for (size_t i = 0; i < sizeof(X) / 4; ++i) w[i] = __builtin_amdgcn_readfirstlane(w[i]);
     __builtin_memcpy(&x, w, sizeof(X));
     return x;
 }
 
-// Waves a SIMD that the LDS allows.
-constexpr int attn_occupancy(int bytes) { return bytes <= 80 * 1024 ? 2 : 1; }
+// Waves a SIMD: queries, results, scores and the next keys take D sizeof(T) / 4 times 1/2
+// and 1 registers, 16 to 32, and as many as the queries.
+constexpr int attn_occupancy(int dim, int size) { return dim * size <= 128 ? 3 : (dim * size <= 256 ? 2 : 1); }
 
 template <class T, int D, int NW, bool WHOLE>
-__global__ __launch_bounds__(64 * NW, attn_occupancy(sizeof(typename Attention<T, D, NW, WHOLE>::Lds))) void k_attention(
+__global__ __launch_bounds__(64 * NW, attn_occupancy(D, sizeof(T))) void k_attention(
     AttentionParams p)
 {
     __shared__ typename Attention<T, D, NW, WHOLE>::Lds lds;
     Attention<T, D, NW, WHOLE> w(p, lds);
-    const int all = __builtin_amdgcn_readfirstlane(p.head->items) * p.c.heads;
-    for (int x = blockIdx.x; x < all; x += gridDim.x) {
-        const AttnItem item = uniform_load(p.item + x / p.c.heads);
-        w.kv_head = x % p.c.heads;
-        if (item.part < 0) continue;
-        w.tile_number = item.tile;
-        w.a = uniform_load(p.tile + item.tile);
-        w.run(item.part);
-        __syncthreads();
+    const AttnWork work(p);
+    const int all = (int)(p.n_groups + p.c.n);
+    if (threadIdx.x < 2) lds.wild[threadIdx.x] = 0;
+    if (p.own_plan) lay_out<64 * NW>(p, lds.segs, reinterpret_cast<AttnSums*>(lds.kv));
+    const AttnSeg* segs = p.own_plan ? lds.segs : p.segs;
+    __syncthreads();
+    const AttnSeg last = p.own_plan ? lds.segs[all] : p.segs[all];
+    const uint32_t line = __builtin_amdgcn_readfirstlane(last.cost), whole_line = line * (uint32_t)p.c.heads;
+    // (costs that sum up beyond 2^31 are of offsets that make no sense)
+    const bool sane = line <= INT32_MAX / (uint32_t)p.c.heads;
+    if (blockIdx.x == 0 && threadIdx.x == 0) *p.tiles = sane ? last.tile : 0;
+    const uint32_t stretch = __builtin_amdgcn_readfirstlane(work.stretch(whole_line));
+    // neighbours in the line, which may read the same keys, on the same XCD (every eighth workgroup)
+    const uint32_t x = p.workgroups % 8 == 0 ? blockIdx.x % 8 * (p.workgroups / 8) + blockIdx.x / 8 : blockIdx.x;
+    if (!sane || (uint64_t)x * stretch >= whole_line) return;
+    uint32_t at = x * stretch;
+    const uint32_t end = whole_line - at < stretch ? whole_line : at + stretch;
+    w.turn = 0;
+    while (at < end) {
+        const uint32_t head = __builtin_amdgcn_readfirstlane(at / line), off = at - head * line;
+        const int i = __builtin_amdgcn_readfirstlane(p.own_plan ? seg_at_cost(lds.segs, all, off, threadIdx.x & 63)
+                                                                : seg_at_cost(p.segs, all, off, threadIdx.x & 63));
+        w.group = i < p.n_groups;
+        w.seg = uniform(p.own_plan ? lds.segs[i] : p.segs[i]);
+        w.kv_head = (int)head;
+        const AttnShape shape = work.shape(w.seg, w.group);
+        const int j = __builtin_amdgcn_readfirstlane(work.tile_at(shape, off - w.seg.cost));
+        w.a = uniform(work.tile(w.seg, j, w.group));
+        const uint32_t before = __builtin_amdgcn_readfirstlane(work.cost(shape, j));
+        const uint32_t cost = __builtin_amdgcn_readfirstlane(work.cost(shape, j + 1)) - before;
+        const uint32_t x0 = off - w.seg.cost - before, x1 = x0 + (end - at < cost - x0 ? end - at : cost - x0);
+        const int s0 = __builtin_amdgcn_readfirstlane(work.step_at(shape, x0, cost, w.a.steps));
+        const int s1 = __builtin_amdgcn_readfirstlane(work.step_at(shape, x1, cost, w.a.steps));
+        const bool whole = x0 == 0 && x1 == cost, left_out = w.seg.row == -2;
+        const int number = w.seg.tile + j;
+        AttnDone* done = p.done + ((int64_t)number * p.c.heads + w.kv_head);
+        const bool notes = threadIdx.x == 64 * NW - 1 && x0 == 0 && number < p.max_tiles;
+        if (notes) {
+            AttnDone d{};
+            d.first = whole ? -1 : (int)x;
+            d.last = (int)((at + (cost - 1)) / stretch);
+            d.kind = w.group || left_out ? 2 : (w.seg.apart >= 0 ? 1 : 0);
+            d.rows = left_out ? 0 : w.a.rows;
+            d.row = w.a.row;
+            d.slot = w.seg.apart + w.a.row;
+            d.begin = w.seg.begin;
+            d.position = w.seg.length - w.seg.count;
+            d.table = w.seg.row;
+            if (d.kind == 1) {
+                const AttnSeg& g = segs[w.seg.group];
+                d.group_row = (int64_t)(w.seg.begin - g.begin) * p.share + w.a.row;
+                d.group_tile = g.tile;
+            }
+            *done = d;
+        }
+        if (!left_out) {
+            w.run(segs, s0, s1, whole, 2 * (int64_t)x + (x0 > 0 ? 0 : 1));
+            if (notes && whole && lds.wild[w.turn]) done->first = -2;
+            w.turn ^= 1;
+            __syncthreads();
+        }
+        at += cost - x0;
     }
 }
 
@@ -513,8 +696,7 @@ template <class T, int D>
 hipError_t launch_dim(const AttentionParams& p, hipStream_t stream)
 {
     constexpr int NW = attn_waves(sizeof(T) == 4 ? DWS_FLOAT32 : DWS_BFLOAT16, D);
-    const int64_t most = p.max_items * p.c.heads;
-    const unsigned grid = (unsigned)(most < kAttnTarget ? most : kAttnTarget);
+    const unsigned grid = (unsigned)p.workgroups;
     if (p.whole_kv)
         k_attention<T, D, NW, true><<<grid, 64 * NW, 0, stream>>>(p);
     else

@@ -1,0 +1,614 @@
+// Attention over cached keys and values: the kernel.
+//
+//   out = sum_t p_t v_t / sum_t p_t,  p_t = 2^(c q . k_t - m),  c = scale log2(e)
+//
+// in one pass over the tokens t, with m a running maximum. A wave holds 32 queries
+// (rows (token, head) that share a key head) in registers and takes 32 tokens at a
+// time: S^T = K Q^T leaves a query's scores in one lane and the lane 32 beside it, so
+// that the softmax needs one exchange between lanes, and P^T is, as it lies, the
+// operand of O^T = V^T P^T, whose columns are again queries: rescaling is a product
+// with the lane's own factor.
+//
+// Each wave brings 32 tokens of keys and values into its part of the LDS, the next
+// ones on their way meanwhile in registers. Tiles of up to 32 queries are memory bound
+// (2 operations a query for each byte of keys): there the waves work on their own tokens
+// and are joined at the end. Larger ones are bound by the matrix products and the softmax
+// beside them: of 64 queries each wave has half and goes through half of the tokens, of
+// 128 it has a quarter and goes through those of all waves.
+//
+// Fragments (32 x 32 tiles, h = lane / 32):
+//   operand  lane holds row (or column) lane % 32, contraction indices 8 h .. 8 h + 7 of
+//            16 (16 bits), or h of 2 (fp32, where a chunk of four takes four products)
+//   result   lane holds column lane % 32, rows 8 (i / 4) + 4 h + i % 4, i = 0 .. 15
+// A contraction may run in any order that both operands share: P's eight elements of a
+// step are the rows above, and the transposing LDS reads bring V's in the same order.
+#pragma once
+
+#include "dws_attention_work.hpp"
+
+namespace dws {
+namespace {
+
+typedef float f32x4_t __attribute__((ext_vector_type(4)));
+typedef float f32x16_t __attribute__((ext_vector_type(16)));
+typedef short s16x4_t __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) char* LdsBytes;      // 32-bit addresses, so that offsets fold into the accesses
+template <class X>
+using InLds = __attribute__((address_space(3))) X*;
+template <class T>
+using Chunk = T __attribute__((ext_vector_type(16 / sizeof(T))));
+
+__device__ __forceinline__ f32x16_t mma(Chunk<bf16_t> a, Chunk<bf16_t> b, f32x16_t c)
+{
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
+}
+__device__ __forceinline__ f32x16_t mma(Chunk<f16_t> a, Chunk<f16_t> b, f32x16_t c)
+{
+    return __builtin_amdgcn_mfma_f32_32x32x16_f16(a, b, c, 0, 0, 0);
+}
+__device__ __forceinline__ f32x16_t mma(Chunk<float> a, Chunk<float> b, f32x16_t c)
+{
+#pragma unroll
+    for (int j = 0; j < 4; ++j) c = __builtin_amdgcn_mfma_f32_32x32x2f32(a[j], b[j], c, 0, 0, 0);
+    return c;
+}
+
+// The larger (the sum) of a lane's value and that of the lane 32 beside it.
+__device__ __forceinline__ float max_halves(float x)
+{
+    const auto r = __builtin_amdgcn_permlane32_swap(__builtin_bit_cast(uint32_t, x), __builtin_bit_cast(uint32_t, x), false, false);
+    return fmaxf(__builtin_bit_cast(float, (uint32_t)r[0]), __builtin_bit_cast(float, (uint32_t)r[1]));
+}
+__device__ __forceinline__ float sum_halves(float x)
+{
+    const auto r = __builtin_amdgcn_permlane32_swap(__builtin_bit_cast(uint32_t, x), __builtin_bit_cast(uint32_t, x), false, false);
+    return __builtin_bit_cast(float, (uint32_t)r[0]) + __builtin_bit_cast(float, (uint32_t)r[1]);
+}
+
+template <class T, int D, int NW, bool WHOLE>
+struct Attention {
+    static constexpr int CH = 16 / sizeof(T);           // elements of a chunk
+    static constexpr int NCH = D / CH;                  // chunks of a row
+    static constexpr int ROW = D * (int)sizeof(T);      // bytes of a row
+    static constexpr int TILE = kKvTokens * ROW;        // bytes of 32 rows
+    static constexpr int N = kKvTokens * NCH / 64;      // chunks of a tile in a lane
+    static constexpr int STEP = 64 / NCH;               // rows that 64 lanes hold at a time
+    static constexpr int BLOCKS = D / 32;
+    static constexpr int THREADS = 64 * NW;
+    struct Lds {
+        char kv[NW][2 * TILE];          // keys, values; then results
+        AttnSeg segs[kAttnSegs + 1];
+        int64_t at[NW][2][kKvTokens];   // where a token's keys and values are, -1: nowhere
+        uint32_t there[NW];             // which tokens of a tile are
+        int wild;                       // rows to compute again
+        float m[kAttnRows * NW], l[kAttnRows * NW];
+    };
+
+    // Chunks of a row are permuted so that reads of one column by 16 rows (keys), and
+    // of four rows by 16 columns (values), go to different banks.
+    static constexpr int SPAN = NCH < 16 ? 16 / NCH : 1;        // rows of 256 bytes
+    static constexpr int MASK = (NCH < 16 ? NCH : 16) - 1;
+    static __device__ __forceinline__ int key_swizzle(int row) { return (row / SPAN) & MASK; }
+    static __device__ __forceinline__ int value_swizzle(int row)
+    {
+        if constexpr (sizeof(T) == 4) return ((row >> 2) & 1) << 3;
+        return ((row / SPAN) << 2) & MASK & 12;
+    }
+
+    const AttentionParams& p;
+    Lds& s;
+    int lane, half, col;
+    const int wave;
+    int kv_head, share_rows;            // share_rows: sets of 32 queries, 1, 2 or 4
+    AttnSeg seg;
+    AttnTile a;
+    bool group;
+    int64_t table;
+    int stop;                           // tokens of the stretch end here
+    Chunk<T> q[NCH / 2];
+    int position;                       // of the lane's query
+    int least;                          // smallest of the wave's queries
+    float c, c_rest;                    // scale log2(e), and what fp32 loses of it
+    f32x16_t o[BLOCKS];
+    float m, l;
+
+    u32x4_t next[N];                    // keys or values on their way to the LDS
+    uint32_t there;                     // which of the wave's tokens are
+
+    __device__ __forceinline__ Attention(const AttentionParams& p, Lds& s)
+        : p(p), s(s), lane(threadIdx.x & 63), half(lane >> 5), col(lane & 31), wave(__builtin_amdgcn_readfirstlane(threadIdx.x >> 6))
+    {
+    }
+
+    __device__ __forceinline__ void row_place(int64_t r, int64_t* token, int* head) const
+    {
+        const int64_t at = a.row + r;
+        if (at < (int64_t)1 << 31) {
+            const uint32_t t = (uint32_t)at / (uint32_t)p.share;
+            *token = seg.begin + t;
+            *head = kv_head * p.share + (int)((uint32_t)at - t * (uint32_t)p.share);
+        } else {
+            *token = seg.begin + at / p.share;
+            *head = kv_head * p.share + (int)(at % p.share);
+        }
+    }
+
+    // Where a query of a group's tile stands in its own row; -1: nowhere.
+    __device__ __forceinline__ int position_in_group(const AttnSeg* segs, int64_t token) const
+    {
+        int64_t lo = 0, hi = p.c.n - 1;
+        while (lo < hi) {
+            const int64_t mid = (lo + hi + 1) / 2;
+            if (segs[p.n_groups + mid].begin <= token)
+                lo = mid;
+            else
+                hi = mid - 1;
+        }
+        const AttnSeg& x = segs[p.n_groups + lo];
+        return x.length > 0 ? x.length - x.count + (int)(token - x.begin) : -1;
+    }
+    __device__ __forceinline__ void load_queries(const AttnSeg* segs)
+    {
+        const int r = (wave & (share_rows - 1)) * kAttnRows + col;
+        const bool in = r < a.rows;
+        int64_t token = 0;
+        int head = 0;
+        if (in) row_place(r, &token, &head);
+        position = INT32_MAX;
+        if (in) position = group ? position_in_group(segs, token) : seg.length - seg.count + (int)(token - seg.begin);
+        least = position;
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) {
+            const int y = __shfl_xor(least, d, 64);
+            least = y < least ? y : least;
+        }
+        least = __builtin_amdgcn_readfirstlane(least);
+        // the scale's sign goes to the queries, so that the largest product has the largest score
+        const float sign = p.scale > 0.f ? 1.f : (p.scale < 0.f ? -1.f : 0.f);
+        const double wide_c = p.scale == 0.f ? 1.0 : fabs((double)p.scale) * 1.4426950408889634;
+        c = (float)wide_c;
+        c_rest = (float)(wide_c - (double)c);
+        const T* from = static_cast<const T*>(p.q.data) + token * p.q.ts + head * p.q.hs;
+#pragma unroll
+        for (int i = 0; i < NCH / 2; ++i) {
+            const int d = (2 * i + half) * CH;
+            Chunk<T> x;
+            if (p.whole_q) {
+                x = in && d < p.c.dim_k ? *reinterpret_cast<const Chunk<T>*>(from + d) : Chunk<T>{};
+            } else {
+#pragma unroll
+                for (int j = 0; j < CH; ++j) x[j] = in && d + j < p.c.dim_k ? from[d + j] : (T)0.f;
+            }
+            if (sign != 1.f) {
+#pragma unroll
+                for (int j = 0; j < CH; ++j) x[j] = sign == 0.f ? (T)0.f : -x[j];
+            }
+            q[i] = x;
+        }
+    }
+
+    // The page of the token that the lane looks up (lanes 32 and on look up nothing).
+    __device__ __forceinline__ int page_of(int first) const
+    {
+        const int t = first + lane;
+        if (lane >= kKvTokens || (uint32_t)t >= (uint32_t)stop) return -1;
+        return p.c.table[table + (uint32_t)t / (uint32_t)p.c.page_tokens];
+    }
+    // Finds the tokens of a tile, and returns which are there. (The others are read from
+    // the pool's beginning, and become 0 before they are used.)
+    __device__ __forceinline__ uint32_t places(int first, int page)
+    {
+        const uint32_t t = (uint32_t)(first + lane), place = t % (uint32_t)p.c.page_tokens;
+        const bool there = page >= 0 && page < p.c.n_pages;
+        if (lane < kKvTokens) {
+            s.at[wave][0][lane] = there ? page * p.c.keys.ps + place * p.c.keys.ts + kv_head * p.c.keys.hs : 0;
+            s.at[wave][1][lane] = there ? page * p.c.values.ps + place * p.c.values.ts + kv_head * p.c.values.hs : 0;
+        }
+        wave_sync();
+        return (uint32_t)__ballot(there);
+    }
+    __device__ __forceinline__ u32x4_t load_chunk(const void* data, int64_t at, int dim) const
+    {
+        const int d = (lane % NCH) * CH;
+        const T* from = static_cast<const T*>(data) + at;
+        if constexpr (WHOLE) {
+            return *reinterpret_cast<const u32x4_t*>(from + (d < dim ? d : 0));
+        } else {
+            Chunk<T> x;
+#pragma unroll
+            for (int j = 0; j < CH; ++j) x[j] = from[d + j < dim ? d + j : 0];
+            return __builtin_bit_cast(u32x4_t, x);
+        }
+    }
+    // The chunk with 0 where the row or the dimension is not there.
+    __device__ __forceinline__ u32x4_t only_there(int i, u32x4_t x, uint32_t there, int dim) const
+    {
+        const int d = (lane % NCH) * CH;
+        const bool row = (there >> (i * STEP + lane / NCH)) & 1;
+        if constexpr (WHOLE) return row && d < dim ? x : u32x4_t{};
+        Chunk<T> y = __builtin_bit_cast(Chunk<T>, x);
+#pragma unroll
+        for (int j = 0; j < CH; ++j) y[j] = row && d + j < dim ? y[j] : (T)0.f;
+        return __builtin_bit_cast(u32x4_t, y);
+    }
+    __device__ __forceinline__ u32x4_t load_key(int i) const
+    {
+        return load_chunk(p.c.keys.data, s.at[wave][0][i * STEP + lane / NCH], p.c.dim_k);
+    }
+    __device__ __forceinline__ u32x4_t load_value(int i) const
+    {
+        return load_chunk(p.c.values.data, s.at[wave][1][i * STEP + lane / NCH], p.c.dim_v);
+    }
+    // Row i * STEP + lane / NCH; what depends on the lane alone stands apart.
+    __device__ __forceinline__ void put_key(int i, u32x4_t x)
+    {
+        const int r = lane / NCH, c = (lane % NCH) ^ key_swizzle(r);
+        static_assert(STEP * SPAN == 1 || (16 % STEP == 0 && (STEP % SPAN == 0 || SPAN == 1)), "rows' bits stand apart");
+        *(InLds<u32x4_t>)(tile_of(wave) + r * ROW + ((c ^ key_swizzle(i * STEP)) << 4) + i * STEP * ROW) = x;
+    }
+    __device__ __forceinline__ void put_value(int i, u32x4_t x)
+    {
+        const int r = lane / NCH, c = (lane % NCH) ^ value_swizzle(r);
+        *(InLds<u32x4_t>)(tile_of(wave) + r * ROW + ((c ^ value_swizzle(i * STEP)) << 4) + TILE + i * STEP * ROW) = x;
+    }
+    __device__ __forceinline__ LdsBytes tile_of(int w) const { return (LdsBytes)&s.kv[0][0] + w * (2 * TILE); }
+    // Keys (values) of the wave's tokens, whose places are known, to registers and then to
+    // its part of the LDS; 0 for what is not there. Rows that are no whole chunks are read
+    // element by element, in no time ahead.
+    template <bool VALUES>
+    __device__ __forceinline__ void fetch()
+    {
+        if constexpr (WHOLE) {
+#pragma unroll
+            for (int i = 0; i < N; ++i) next[i] = VALUES ? load_value(i) : load_key(i);
+        }
+    }
+    template <bool VALUES>
+    __device__ __forceinline__ void put()
+    {
+        const int dim = VALUES ? p.c.dim_v : p.c.dim_k;
+        if constexpr (WHOLE) {
+            if (there != 0xffffffffu || dim != D) {
+#pragma unroll
+                for (int i = 0; i < N; ++i) next[i] = only_there(i, next[i], there, dim);
+            }
+#pragma unroll
+            for (int i = 0; i < N; ++i) VALUES ? put_value(i, next[i]) : put_key(i, next[i]);
+        } else {
+#pragma unroll 1
+            for (int i = 0; i < N; ++i) {
+                const u32x4_t x = only_there(i, VALUES ? load_value(i) : load_key(i), there, dim);
+                VALUES ? put_value(i, x) : put_key(i, x);
+            }
+        }
+    }
+
+    // Eight (four) values of V's column (dimension) 32 block + col, of the tokens that
+    // step u's eight (four) elements of P belong to.
+    __device__ __forceinline__ Chunk<T> value_fragment(LdsBytes values, int block, int u) const
+    {
+        if constexpr (sizeof(T) == 2) {
+            const int r = (lane >> 2) & 3;      // the row that the lane points at, of four
+            const int low = 2 * ((lane >> 4) & 1) + ((lane >> 1) & 1);
+            const LdsBytes at = values + (4 * half + r) * ROW + 8 * (lane & 1) + (((4 * block) ^ (low ^ value_swizzle(r))) << 4) + 16 * u * ROW;
+            const s16x4_t lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((InLds<s16x4_t>)at);
+            const s16x4_t hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((InLds<s16x4_t>)(at + 8 * ROW));
+            return __builtin_bit_cast(Chunk<T>, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+        } else {
+            Chunk<T> x;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) x[j] = value_at(values, 8 * u + 4 * half + j, 32 * block + col);
+            return x;
+        }
+    }
+    static __device__ __forceinline__ T value_at(LdsBytes values, int row, int d)
+    {
+        return *(InLds<T>)(values + row * ROW + (((d / CH) ^ value_swizzle(row)) << 4) + (d % CH) * sizeof(T));
+    }
+    static __device__ __forceinline__ bool finite(T x) { return __builtin_fabsf((float)x) < __builtin_inff(); }
+
+    // The wave's queries and the 32 tokens that wave w brought: products, largest ones.
+    __device__ __forceinline__ f32x16_t scores(int w) const
+    {
+        const LdsBytes keys = tile_of(w);
+        const int swizzle = half ^ key_swizzle(col);
+        f32x16_t x = {};
+#pragma unroll
+        for (int i = 0; i < NCH / 2; ++i) x = mma(*(InLds<Chunk<T>>)(keys + col * ROW + (((2 * i) ^ swizzle) << 4)), q[i], x);
+        return x;
+    }
+    // Whether there are tokens among the 32 from `first` on that not every query sees.
+    __device__ __forceinline__ bool masked(uint32_t there, int first) const
+    {
+        return there != 0xffffffffu || (int64_t)first + kKvTokens - 1 > least;
+    }
+    // A value that is not finite, of a token that not every query sees: 0 times it is not
+    // 0. Such a tile's rows are computed again, one by one, where the parts are joined.
+    __device__ __forceinline__ void note_wild(LdsBytes values)
+    {
+        bool bad = false;
+#pragma unroll 1
+        for (int i = 0; i < NCH / 2; ++i) {
+            const Chunk<T> v = *(InLds<Chunk<T>>)(values + col * ROW + ((2 * i + half) << 4));
+#pragma unroll
+            for (int j = 0; j < CH; ++j) bad |= !finite(v[j]);
+        }
+        if (__ballot(bad)) s.wild = 1;
+    }
+
+    // The loop over pieces with R sets of 32 queries, each of which R waves' tokens go by.
+    // One set of registers brings the keys while values are multiplied, and the values while
+    // scores are.
+    template <int R>
+    __device__ __forceinline__ void pieces(int t, int count)
+    {
+        constexpr int TOKENS = kKvTokens * NW;
+        constexpr int STEPS = 16 / CH;          // steps of the second product
+        auto meet = [] {
+            if constexpr (R > 1)
+                __syncthreads();
+            else
+                wave_sync();
+        };
+        const int first_wave = wave / R * R;
+        uint32_t after = 0;
+        int page = -1;
+        if (count > 0) {
+            after = places(t, page_of(t));
+            fetch<false>();
+            page = page_of(t + TOKENS);
+        }
+        for (int i = 0; i < count; ++i, t += TOKENS) {
+            // addresses are worked out anew for each piece: kept, they push results out of the registers
+            asm volatile("" : "+v"(lane));
+            half = lane >> 5;
+            col = lane & 31;
+            there = after;
+            put<false>();
+            if (lane == 0) s.there[wave] = there;
+            fetch<true>();
+            meet();
+            f32x16_t x[R];
+            uint32_t here[R];
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                x[r] = scores(first_wave + r);
+                here[r] = __builtin_amdgcn_readfirstlane(s.there[first_wave + r]);
+            }
+            const int first = t + (first_wave - wave) * kKvTokens;
+            float top = -__builtin_inff();
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                if (masked(here[r], first + r * kKvTokens)) {
+                    const int past = position - (first + r * kKvTokens);        // the last token that the query sees
+                    const uint32_t sees = (here[r] & (past < 0 ? 0u : 0xffffffffu >> (past > 31 ? 0 : 31 - past))) >> (4 * half);
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) x[r][e] = sees >> (8 * (e / 4) + e % 4) & 1 ? x[r][e] : -__builtin_inff();
+                }
+#pragma unroll
+                for (int e = 0; e < 16; ++e) top = fmaxf(top, x[r][e]);
+            }
+            top = max_halves(top) * c;
+            // The maximum follows once a score is 2^8 times above it: until then sums grow
+            // by that, which fp32 and fp16 hold, and the results need no rescaling.
+            if (__ballot(top > m + 8.f)) {
+                const float now = fmaxf(m, top);
+                const float by = now == m ? 1.f : __builtin_amdgcn_exp2f(m - now);
+                l *= by;
+#pragma unroll
+                for (int b = 0; b < BLOCKS; ++b) o[b] *= by;
+                m = now;
+            }
+            const float base = m == -__builtin_inff() ? 0.f : m;
+            Chunk<T> pr[R][STEPS];
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                float sum = 0.f;
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                    float y = __builtin_fmaf(x[r][e], c, -base);
+                    if constexpr (sizeof(T) == 4)
+                        if (x[r][e] != -__builtin_inff()) y = __builtin_fmaf(x[r][e], c_rest, y);
+                    y = __builtin_amdgcn_exp2f(y);
+                    sum += y;
+                    pr[r][e / CH][e % CH] = (T)y;
+                }
+                l += sum;
+            }
+            put<true>();
+            if (i + 1 < count) {
+                after = places(t + TOKENS, page);
+                fetch<false>();
+                page = page_of(t + 2 * TOKENS);
+            }
+            meet();
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                const LdsBytes values = tile_of(first_wave + r) + TILE;
+                if (masked(here[r], first + r * kKvTokens)) note_wild(values);
+#pragma unroll
+                for (int b = 0; b < BLOCKS; ++b)
+#pragma unroll
+                    for (int u = 0; u < STEPS; ++u) o[b] = mma(value_fragment(values, b, u), pr[r][u], o[b]);
+            }
+        }
+        if constexpr (R > 1) __syncthreads();       // results go where others' values may still be read
+    }
+
+    __device__ __forceinline__ void store(int64_t at, f32x4_t x, int d)
+    {
+        T* to = static_cast<T*>(p.out.data) + at + d;
+        if (p.whole_out) {
+            typedef T Four __attribute__((ext_vector_type(4)));
+            Four y;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) y[j] = (T)x[j];
+            if (d < p.c.dim_v) *reinterpret_cast<Four*>(to) = y;
+        } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (d + j < p.c.dim_v) to[j] = (T)x[j];
+        }
+    }
+
+    // Pieces first_step .. last_step - 1 of the tile's keys. `part`: where partial results go.
+    __device__ __forceinline__ void run(const AttnSeg* segs, int first_step, int last_step, int tile, int64_t part)
+    {
+        share_rows = a.rows <= kAttnRows ? 1 : (a.rows <= 2 * kAttnRows || NW == 2 ? 2 : NW);
+        stop = a.end;
+        table = seg.row * p.c.max_pages;
+        load_queries(segs);
+        m = -__builtin_inff();
+        l = 0.f;
+#pragma unroll
+        for (int b = 0; b < BLOCKS; ++b) o[b] = f32x16_t{};
+        const int t = a.begin + first_step * kKvTokens * NW + wave * kKvTokens, count = last_step - first_step;
+        if (share_rows == 1)
+            pieces<1>(t, count);
+        else if (share_rows == 2)
+            pieces<2>(t, count);
+        else
+            {}
+        l = sum_halves(l);
+
+        // Results by way of the LDS (a wave's own part of it), so that rows are written whole.
+        float* mine = reinterpret_cast<float*>(s.kv[wave]);
+#pragma unroll
+        for (int b = 0; b < BLOCKS; ++b)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int quad = 8 * b + 2 * j + half;
+                *reinterpret_cast<f32x4_t*>(mine + col * D + ((quad ^ (col & 15)) << 2)) =
+                    f32x4_t{o[b][4 * j], o[b][4 * j + 1], o[b][4 * j + 2], o[b][4 * j + 3]};
+            }
+        if (half == 0) {
+            s.m[wave * kAttnRows + col] = m;
+            s.l[wave * kAttnRows + col] = l;
+        }
+        __syncthreads();
+        const bool whole = first_step == 0 && last_step >= a.steps;
+        float* to = nullptr;
+        float2* to_stat = nullptr;
+        if (!whole) {
+            to = p.part + part * p.tile_rows * D;
+            to_stat = p.part_stat + part * p.tile_rows;
+        } else if (seg.apart >= 0) {
+            const int64_t row = kv_head * p.max_apart + seg.apart + a.row;
+            to = p.apart + row * D;
+            to_stat = p.apart_stat + row;
+        }
+        if (threadIdx.x == 0) {
+            *(whole ? p.wild + (int64_t)tile * p.c.heads + kv_head : p.wild_part + part) = s.wild != 0;
+            s.wild = 0;
+        }
+        constexpr int QUADS = D / 4;
+        for (int i = threadIdx.x; i < a.rows * QUADS; i += THREADS) {
+            const int r = i / QUADS, quad = i % QUADS, in = r % kAttnRows;
+            const int place = in * D + ((quad ^ (in & 15)) << 2);
+            f32x4_t sum = {0.f, 0.f, 0.f, 0.f};
+            float most = -__builtin_inff(), total = 0.f;
+            // the waves that have the row's queries
+            for (int w = r / kAttnRows; w < NW; w += share_rows)
+                if (s.l[w * kAttnRows + in] != 0.f) most = fmaxf(most, s.m[w * kAttnRows + in]);
+            for (int w = r / kAttnRows; w < NW; w += share_rows) {
+                const float lw = s.l[w * kAttnRows + in], mw = s.m[w * kAttnRows + in];
+                if (lw == 0.f) continue;
+                const float by = mw == most ? 1.f : __builtin_amdgcn_exp2f(mw - most);
+                sum += *(InLds<f32x4_t>)((InLds<float>)tile_of(w) + place) * by;
+                total += lw * by;
+            }
+            if (to != nullptr) {
+                *reinterpret_cast<f32x4_t*>(to + (int64_t)r * D + 4 * quad) = sum;
+                if (quad == 0) to_stat[r] = make_float2(most, total);
+            } else {
+                int64_t token;
+                int head;
+                row_place(r, &token, &head);
+                const float by = total == 0.f ? 0.f : 1.f / total;
+                store(token * p.out.ts + head * p.out.hs, total == 0.f ? f32x4_t{0.f, 0.f, 0.f, 0.f} : sum * by, 4 * quad);
+                if (quad == 0 && p.lse != nullptr)
+                    p.lse[token * p.heads_q + head] =
+                        total == 0.f ? -__builtin_inff() : (most + __builtin_log2f(total)) * 0.693147180559945f;
+            }
+        }
+    }
+};
+
+template <class X>
+__device__ __forceinline__ X uniform(X x)
+{
+    static_assert(sizeof(X) % 4 == 0, "whole words");
+    uint32_t w[sizeof(X) / 4];
+    __builtin_memcpy(w, &x, sizeof(X));
+#pragma unroll
+    for (size_t i = 0; i < sizeof(X) / 4; ++i) w[i] = __builtin_amdgcn_readfirstlane(w[i]);
+    __builtin_memcpy(&x, w, sizeof(X));
+    return x;
+}
+
+// Waves a SIMD that the LDS allows.
+constexpr int attn_occupancy(int bytes) { return bytes <= 80 * 1024 ? 2 : 1; }
+
+template <class T, int D, int NW, bool WHOLE>
+__global__ __launch_bounds__(64 * NW, attn_occupancy(sizeof(typename Attention<T, D, NW, WHOLE>::Lds))) void k_attention(
+    AttentionParams p)
+{
+    __shared__ typename Attention<T, D, NW, WHOLE>::Lds lds;
+    Attention<T, D, NW, WHOLE> w(p, lds);
+    const AttnWork work(p);
+    const int64_t all = p.n_groups + p.c.n;
+    const AttnSeg* segs = p.segs;
+    if (threadIdx.x == 0) lds.wild = 0;
+    __syncthreads();
+    if (p.own_plan) {
+        lay_out<64 * NW>(p, lds.segs, reinterpret_cast<int64_t*>(lds.kv[0]));
+        segs = lds.segs;
+        if (blockIdx.x == 0)
+            for (int i = threadIdx.x; i <= all; i += 64 * NW) p.segs[i] = lds.segs[i];
+    }
+    const int64_t line = uniform(segs[all].cost), stretch = uniform(work.stretch(line * p.c.heads));
+    // neighbours in the line, which may read the same keys, on the same XCD (every eighth workgroup)
+    const int64_t x = p.workgroups % 8 == 0 ? blockIdx.x % 8 * (p.workgroups / 8) + blockIdx.x / 8 : blockIdx.x;
+    int64_t at = x * stretch;
+    const int64_t end = at + stretch < line * p.c.heads ? at + stretch : line * p.c.heads;
+    while (at < end) {
+        const int64_t head = line <= UINT32_MAX && at <= UINT32_MAX ? (uint32_t)at / (uint32_t)line : at / line, off = at - head * line;
+        const int64_t i = uniform(seg_at_cost(segs, all, off));
+        w.group = i < p.n_groups;
+        w.seg = uniform(segs[i]);
+        w.kv_head = (int)head;
+        const AttnShape shape = work.shape(w.seg, w.group);
+        const int j = uniform(AttnWork::tile_at(shape, off - w.seg.cost));
+        w.a = uniform(work.tile(w.seg, j, w.group));
+        const int64_t before = AttnWork::cost(shape, j), cost = AttnWork::cost(shape, j + 1) - before;
+        const int64_t x0 = off - w.seg.cost - before, x1 = x0 + (end - at) < cost ? x0 + (end - at) : cost;
+        const int s0 = uniform(AttnWork::step_at(x0, cost, w.a.steps)), s1 = uniform(AttnWork::step_at(x1, cost, w.a.steps));
+        if (w.seg.row != -2 && (s1 > s0 || (w.a.steps == 0 && x0 == 0))) {
+            w.run(segs, s0, s1, w.seg.tile + j, 2 * x + (s0 > 0 ? 0 : 1));
+            __syncthreads();
+        }
+        at += uniform(cost - x0);
+    }
+}
+
+template <class T, int D>
+hipError_t launch_dim(const AttentionParams& p, hipStream_t stream)
+{
+    constexpr int NW = attn_waves(sizeof(T) == 4 ? DWS_FLOAT32 : DWS_BFLOAT16, D);
+    const unsigned grid = (unsigned)p.workgroups;
+    if (p.whole_kv)
+        k_attention<T, D, NW, true><<<grid, 64 * NW, 0, stream>>>(p);
+    else
+        k_attention<T, D, NW, false><<<grid, 64 * NW, 0, stream>>>(p);
+    return hipGetLastError();
+}
+template <class T>
+hipError_t launch_type(const AttentionParams& p, hipStream_t stream)
+{
+    if (p.padded == 64) return launch_dim<T, 64>(p, stream);
+    if (p.padded == 128) return launch_dim<T, 128>(p, stream);
+    return launch_dim<T, 256>(p, stream);
+}
+
+}  // namespace
+}  // namespace dws

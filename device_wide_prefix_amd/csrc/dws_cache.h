@@ -28,7 +28,8 @@ struct KvView {
     int n_pages, page_tokens;
     int heads, dim_k, dim_v;
     int64_t tokens, n;
-    const int64_t* offsets;     // n + 1, or null: tokens / n each
+    const int64_t* offsets;     // n + 1, or null: `each` tokens a sequence
+    int64_t each;
     const int* rows;            // n, or null: row i
 };
 
@@ -56,53 +57,65 @@ constexpr int attn_padded_dim(int dim_k, int dim_v)
 // workgroups of them up to 128 dimensions of 16 bits.
 constexpr int attn_waves(int dtype, int padded) { return dtype == DWS_FLOAT32 && padded == 256 ? 2 : 4; }
 
-// Workgroups that the keys are shared out to, two a compute unit.
-constexpr int kAttnTarget = 512;
+// Workgroups that the work is shared out to at most, two a compute unit.
+constexpr int kAttnGroups = 512;
+// The time of a piece of kKvTokens tokens a wave for tiles of up to 32, 64 and 128
+// queries, of a tile beside its pieces, and the least for a workgroup of its own.
+constexpr uint32_t kCostNarrow = 4, kCostMiddle = 5, kCostWide = 8, kCostTile = 4, kCostLeast = 8;
+// Segments that a workgroup lays out for itself.
+constexpr int kAttnSegs = 256;
 
-// A tile of queries that belong together: rows (token, head of the key head) of one
-// sequence or of one group.
-struct AttnTile {
-    int64_t token;          // first token of the sequence (of the group)
-    int64_t row;            // the tile's first row behind it
-    int64_t table;          // first table entry of the cache row
-    int64_t slot;           // first row of its partial results; -1: written as it is
-    int64_t other_row;      // where a sequence's shared tokens are computed apart: the tile's first row in its group,
-    int other;              // and the group's first tile; else -1
+// A segment of the work: a group's shared tokens for the queries of all its
+// sequences, or a sequence's other tokens (all without a group). Its queries, rows
+// (token, head of the key head), are cut into tiles.
+struct AttnSeg {
+    uint32_t cost;          // of the segments before it
+    int begin, count;       // tokens of the call
+    int row;                // of the cache; -1: none
+    int from, length;       // its keys: tokens of that row
+    int group;              // a sequence: its group if that shares tokens, else -1; a group: its first sequence
+    int tile;               // number of its first tile
+    int apart;              // where its tiles are always joined with others: first row of their results; else -1
+};
+
+// How a tile was computed, for the joining.
+struct AttnDone {
+    int first, last;        // workgroups that have a part of it; first < 0: one has it all, -2: and its rows are to be computed again
+    int kind;               // 0: as it is, 1: together with its group's tiles, 2: a group's own, or left out
     int rows;
-    int begin, end;         // its keys: tokens of the cache row
-    int position;           // of `token`; a group's are in AttentionParams.positions
-    int group;              // 1: the shared tokens of a group
-    int steps, parts;       // pieces of kKvTokens tokens a wave, and the workgroups they are shared out to
-};
-struct AttnHead {
-    int tiles, items;
-};
-struct AttnItem {
-    int tile, part;
+    int64_t row;            // first row of the sequence
+    int64_t slot;           // kind 1 and 2: first row of the results that one workgroup has
+    int64_t group_row;      // kind 1: the tile's first row in the group,
+    int group_tile;         // and the group's first tile
+    int begin;              // first token of the sequence, its place in the row, and the cache row
+    int position, table;
 };
 
 struct AttentionParams {
     KvView c;
     int heads_q, share;         // share: query heads of a key head
     float scale;
+    float log2_scale, log2_rest, sign;      // |scale| log2(e), what fp32 loses of it, and the sign
     int64_t n_groups;
     const int64_t* groups;
     const int* shared;
     int zero_rest, whole_q, whole_kv, whole_out;
     HeadRows q, out;
     float* lse;
-    int dtype, padded, waves;
+    int dtype, padded;
+    int shift;                  // log2 of the queries of a whole tile, and of the tokens of a piece
+    int cost_shift;             // of costs, so that all of them together stay below 2^31
+    int workgroups, tile_rows;  // tile_rows: of a tile at most
+    int own_plan;               // every workgroup lays the segments out for itself
     // plan and partial results, in the workspace
-    int64_t max_tiles, max_items, max_rows;
-    AttnHead* head;
-    int* seg;                   // [n_groups + n + 1] first tile of each group, then of each sequence
-    int* from;                  // [n_groups] tokens that are computed once for the group
-    int* positions;             // [tokens], with groups
-    AttnTile* tile;             // [max_tiles]
-    AttnItem* item;             // [max_items]
-    int* wild;                  // [max_tiles] 1: rows to compute again one by one
-    float* partial;             // [heads][max_rows][padded] sums
-    float2* stat;               // [heads][max_rows] largest score (log2) and sum of the exponentials
+    int64_t max_tiles, max_apart;
+    AttnSeg* segs;              // [n_groups + n + 1], where not every workgroup has them
+    AttnDone* done;             // [max_tiles][heads]
+    int* tiles;                 // their number
+    float* apart;               // [heads][max_apart][padded] sums,
+    float2* apart_stat;         // [heads][max_apart] largest score (log2) and sum of the exponentials
+    float* part;                // [workgroups][2][tile_rows][padded]
+    float2* part_stat;          // [workgroups][2][tile_rows]
 };
 hipError_t launch_attention(const AttentionParams& p, hipStream_t stream);
 hipError_t launch_attention_bf16(const AttentionParams& p, hipStream_t stream);

@@ -93,6 +93,7 @@ dws_status check_view(Arrays* arrays, const dws_kv_cache& c, const dws_page_seqs
     v->tokens = s.tokens;
     v->n = s.n;
     v->offsets = reinterpret_cast<const int64_t*>(s.d_offsets);
+    v->each = s.n > 0 ? s.tokens / s.n : 0;
     v->rows = s.d_rows;
     return st;
 }
@@ -142,50 +143,53 @@ dws_status append_entry(const dws_pages_append_args* a, hipStream_t stream)
 // ---- attention ---------------------------------------------------------------
 
 struct Plan {
-    int padded, waves;
-    int64_t tiles, items, rows;
-    size_t head, seg, from, positions, tile, item, wild, partial, stat, bytes;
+    int padded, waves, tile_rows, workgroups, cost_shift;
+    int64_t tiles, apart;
+    size_t segs, done, tiles_at, apart_sum, apart_stat, part_sum, part_stat, bytes;
 };
 // Sizes of the workspace's arrays; the caller's sizes have passed
-// check_attention_sizes. A sequence's (a group's) rows fill whole tiles but for the
-// last one. A tile in more than one part has parts that are, but for the last one,
-// at least as large as shares all work out to kAttnTarget workgroups, so a head's
-// such parts are fewer than twice kAttnTarget / heads. Beside them, partial results
-// are of groups and their sequences, which are apart only while a group's rows fill
-// less than half a tile a sequence.
+// check_attention_sizes. Each workgroup has an equal share of the work, so at most its
+// first and its last tile are parts. Results that are always joined are those of
+// groups and their sequences, which are apart only while a group's rows fill less than
+// half a tile a sequence.
 dws_status plan_of(const dws_pages_attention_args* a, Plan* z)
 {
     const dws_kv_cache& c = a->cache;
     const int64_t share = a->heads_q / c.heads, n = a->seqs.n, groups = a->n_groups;
     z->padded = attn_padded_dim(c.dim_k, c.dim_v);
     z->waves = attn_waves(c.dtype, z->padded);
-    const int64_t tile_rows = kAttnRows * z->waves, parts = (kAttnTarget + c.heads - 1) / c.heads;
+    const int64_t full = kAttnRows * z->waves;
     const __int128 rows = (__int128)a->seqs.tokens * share;
-    __int128 tiles = rows / tile_rows + n;
-    if (groups > 0) tiles += rows / tile_rows + groups;
-    if ((tiles + parts) * c.heads > kMaxCount / 2) return DWS_ERR_UNSUPPORTED;
+    __int128 tiles = rows / full + n;
+    if (groups > 0) tiles += rows / full + groups;
+    if (tiles * c.heads > kMaxCount / 2 || n + groups > kMaxCount / 2) return DWS_ERR_UNSUPPORTED;
     z->tiles = (int64_t)tiles;
-    z->items = z->tiles + parts;
     __int128 apart = 0;
-    if (groups > 0) apart = 2 * (rows < (__int128)n * (tile_rows / 2) ? rows : (__int128)n * (tile_rows / 2));
-    const __int128 all = apart + (__int128)tile_rows * 2 * parts;
-    if (all > kMaxCount || all * c.heads * (z->padded + 2) * 4 > kMaxArrayBytes) return DWS_ERR_UNSUPPORTED;
-    z->rows = (int64_t)all;
+    if (groups > 0) apart = 2 * (rows < (__int128)n * (full / 2) ? rows : (__int128)n * (full / 2));
+    if (apart > kMaxCount || apart * c.heads * (z->padded + 2) * 4 > kMaxArrayBytes) return DWS_ERR_UNSUPPORTED;
+    z->apart = (int64_t)apart;
+    z->tile_rows = (int)(rows < full ? (rows < 1 ? 1 : rows) : full);
+    // no row is longer than its pages
+    const __int128 most = (__int128)c.max_pages * c.page_tokens, step = kKvTokens * z->waves;
+    const int64_t tile_cost = kCostTile + (int64_t)kCostWide * (int64_t)((most < kMaxCount ? most : kMaxCount) / step + 1);
+    const __int128 cost = tiles * c.heads * tile_cost;
+    z->workgroups = cost < (__int128)kAttnGroups * kCostLeast ? (int)(cost / kCostLeast) + 1 : kAttnGroups;
+    z->cost_shift = 0;
+    while (tiles * c.heads * (1 + (tile_cost >> z->cost_shift)) > kMaxCount) ++z->cost_shift;
     size_t at = 0;
     auto take = [&](size_t bytes) {
         const size_t was = at;
         at += (bytes + 255) / 256 * 256;
         return was;
     };
-    z->head = take(sizeof(AttnHead));
-    z->seg = take((size_t)(groups + n + 1) * 4);
-    z->from = take((size_t)groups * 4);
-    z->positions = take(groups > 0 ? (size_t)a->seqs.tokens * 4 : 0);
-    z->tile = take((size_t)z->tiles * sizeof(AttnTile));
-    z->item = take((size_t)z->items * sizeof(AttnItem));
-    z->wild = take((size_t)z->tiles * 4);
-    z->partial = take((size_t)z->rows * c.heads * z->padded * 4);
-    z->stat = take((size_t)z->rows * c.heads * 8);
+    const size_t part = (size_t)z->workgroups * 2 * (size_t)z->tile_rows, always = (size_t)z->apart * c.heads;
+    z->segs = take((size_t)(groups + n + 1) * sizeof(AttnSeg));
+    z->done = take((size_t)z->tiles * c.heads * sizeof(AttnDone));
+    z->tiles_at = take(4);
+    z->apart_sum = take(always * z->padded * 4);
+    z->apart_stat = take(always * 8);
+    z->part_sum = take(part * z->padded * 4);
+    z->part_stat = take(part * 8);
     z->bytes = at;
     return DWS_OK;
 }
@@ -242,19 +246,25 @@ dws_status attention_entry(const dws_pages_attention_args* a, hipStream_t stream
     p.lse = a->d_lse;
     p.dtype = c.dtype;
     p.padded = z.padded;
-    p.waves = z.waves;
+    p.shift = z.waves == 4 ? 7 : 6;
+    p.workgroups = z.workgroups;
+    p.cost_shift = z.cost_shift;
+    // 0 leaves the queries out, so that any factor will do
+    const double by = a->scale == 0.f ? 1.0 : std::fabs((double)a->scale) * 1.4426950408889634;
+    p.log2_scale = (float)by;
+    p.log2_rest = (float)(by - (double)p.log2_scale);
+    p.sign = a->scale > 0.f ? 1.f : (a->scale < 0.f ? -1.f : 0.f);
+    p.tile_rows = z.tile_rows;
+    p.own_plan = a->seqs.n + a->n_groups <= kAttnSegs;
     p.max_tiles = z.tiles;
-    p.max_items = z.items;
-    p.max_rows = z.rows;
-    p.head = part<AttnHead>(a->d_workspace, z.head);
-    p.seg = part<int>(a->d_workspace, z.seg);
-    p.from = part<int>(a->d_workspace, z.from);
-    p.positions = part<int>(a->d_workspace, z.positions);
-    p.tile = part<AttnTile>(a->d_workspace, z.tile);
-    p.item = part<AttnItem>(a->d_workspace, z.item);
-    p.wild = part<int>(a->d_workspace, z.wild);
-    p.partial = part<float>(a->d_workspace, z.partial);
-    p.stat = part<float2>(a->d_workspace, z.stat);
+    p.max_apart = z.apart;
+    p.segs = part<AttnSeg>(a->d_workspace, z.segs);
+    p.done = part<AttnDone>(a->d_workspace, z.done);
+    p.tiles = part<int>(a->d_workspace, z.tiles_at);
+    p.apart = part<float>(a->d_workspace, z.apart_sum);
+    p.apart_stat = part<float2>(a->d_workspace, z.apart_stat);
+    p.part = part<float>(a->d_workspace, z.part_sum);
+    p.part_stat = part<float2>(a->d_workspace, z.part_stat);
     return status_of(launch_attention(p, stream));
 }
 

@@ -22,7 +22,7 @@ __device__ __forceinline__ void wave_sync()
 
 __device__ __forceinline__ int64_t seq_begin(const KvView& c, int64_t i)
 {
-    return c.offsets != nullptr ? c.offsets[i] : i * (c.tokens / c.n);
+    return c.offsets != nullptr ? c.offsets[i] : i * c.each;
 }
 
 // The sequence that holds token t, -1 if none does, and its first token and
@@ -33,7 +33,7 @@ __device__ __forceinline__ int64_t seq_of(const KvView& c, int64_t t, int64_t* f
     if (c.n == 0) return -1;
     int64_t i;
     if (c.offsets == nullptr) {
-        i = t / (c.tokens / c.n);
+        i = t / c.each;
     } else {
         int64_t lo = 0, hi = c.n - 1;
         while (hi > lo) {

@@ -852,7 +852,8 @@ dws_status dws_pages_attention_workspace(const dws_pages_attention_args* args, s
  * Attention of each token's queries with the keys and values of its row up to its own place, the call's own tokens
  * (dws_pages_append first) included: out = sum p_t v_t with p the softmax of scale q . k_t over them. For one token a
  * sequence, a few, or whole prompts behind what is there. A query that sees nothing (a row outside the table, a sequence
- * with more tokens than its row, a row longer than max_pages pages, pages outside the pool) gives 0, and -infinity in d_lse. Scores, their statistics and
+ * with more tokens than its row, a row longer than max_pages pages or 2^31 - 4097
+ * tokens, pages outside the pool) gives 0, and -infinity in d_lse. Scores, their statistics and
  * all sums are fp32; with 16-bit inputs the probabilities are rounded to dtype for their product with the values. What is
  * behind a row's end is not read, whatever the pages hold there. Values that are not finite reach the queries that see
  * them, and no others. d_shared must say the truth: the shared tokens are read from the pages of the group's first
