@@ -24,6 +24,8 @@
 // step are the rows above, and the transposing LDS reads bring V's in the same order.
 #pragma once
 
+#include <type_traits>
+
 #include "dws_attention_work.hpp"
 
 namespace dws {
@@ -65,8 +67,9 @@ __device__ __forceinline__ float sum_halves(float x)
     return __builtin_bit_cast(float, (uint32_t)r[0]) + __builtin_bit_cast(float, (uint32_t)r[1]);
 }
 
-template <class T, int D, int NW, bool WHOLE>
+template <class T, int D, int NW, int ACCESS>
 struct Attention {
+    static constexpr bool WHOLE = ACCESS != kElements;
     static constexpr int CH = 16 / sizeof(T);           // elements of a chunk
     static constexpr int NCH = D / CH;                  // chunks of a row
     static constexpr int ROW = D * (int)sizeof(T);      // bytes of a row
@@ -88,7 +91,8 @@ struct Attention {
         // a wave's keys, then its values; or all waves' keys, and their values; then results
         alignas(16) char kv[NW * (TILE > RESULT ? TILE : RESULT)];
         AttnSeg segs[kAttnSegs + 1];
-        int64_t at[NW][2][kKvTokens];   // where a token's keys and values are, -1: nowhere
+        // where a token's keys and values are: elements, or 16 bytes of 32-bit numbers
+        std::conditional_t<ACCESS == kNear, uint32_t, int64_t> at[NW][2][kKvTokens];
         uint32_t there[NW];             // which of a wave's tokens are there
         int wild[2];                    // rows to compute again, of this tile and the next
         float m[kAttnRows * NW], l[kAttnRows * NW];
@@ -115,6 +119,7 @@ struct Attention {
     bool group;
     int turn;                           // which of Lds.wild
     int64_t table;
+    const T *keys_of_head, *values_of_head;
     int stop;                           // tokens of the stretch end here
     Chunk<T> q[NCH / 2];
     int position;                       // of the lane's query
@@ -196,36 +201,55 @@ struct Attention {
         }
     }
 
+    __device__ __forceinline__ uint32_t page_number(uint32_t t) const
+    {
+        return p.c.page_magic == 0 ? t : __umulhi(t, p.c.page_magic) >> p.c.page_shift;
+    }
     // The page of the token that the lane looks up, of `tokens`.
     __device__ __forceinline__ int page_of(int first, int tokens) const
     {
         const int t = first + lane;
         if (lane >= tokens || (uint32_t)t >= (uint32_t)stop) return -1;
-        return p.c.table[table + (uint32_t)t / (uint32_t)p.c.page_tokens];
+        return (p.c.table + table)[page_number((uint32_t)t)];
     }
     // Finds the tokens of a tile, and returns which are there. (The others are read from
     // the pool's beginning, and become 0 before they are used.)
     __device__ __forceinline__ uint32_t places(int first, int page)
     {
-        const uint32_t t = (uint32_t)(first + lane), place = t % (uint32_t)p.c.page_tokens;
-        const bool there = page >= 0 && page < p.c.n_pages;
+        const uint32_t t = (uint32_t)(first + lane), place = t - page_number(t) * (uint32_t)p.c.page_tokens;
+        const bool there = (uint32_t)page < (uint32_t)p.c.n_pages;
         if (lane < kKvTokens) {
-            s.at[wave][0][lane] = there ? page * p.c.keys.ps + place * p.c.keys.ts + kv_head * p.c.keys.hs : 0;
-            s.at[wave][1][lane] = there ? page * p.c.values.ps + place * p.c.values.ts + kv_head * p.c.values.hs : 0;
+            if constexpr (ACCESS == kNear) {
+                s.at[wave][0][lane] = there ? (uint32_t)page * p.key_ps + place * p.key_ts : 0;
+                s.at[wave][1][lane] = there ? (uint32_t)page * p.value_ps + place * p.value_ts : 0;
+            } else {
+                s.at[wave][0][lane] = there ? page * p.c.keys.ps + place * p.c.keys.ts : 0;
+                s.at[wave][1][lane] = there ? page * p.c.values.ps + place * p.c.values.ts : 0;
+            }
         }
         wave_sync();
         return (uint32_t)__ballot(there);
     }
-    __device__ __forceinline__ u32x4_t load_chunk(const void* data, int64_t at, int dim) const
+    using Place = std::conditional_t<ACCESS == kNear, uint32_t, int64_t>;
+    template <bool VALUES>
+    __device__ __forceinline__ Place place_of(int i) const
     {
-        const int d = (lane % NCH) * CH;
-        const T* from = static_cast<const T*>(data) + at;
-        if constexpr (WHOLE) {
-            return *reinterpret_cast<const u32x4_t*>(from + (d < dim ? d : 0));
+        return s.at[wave][VALUES][i * STEP + lane / NCH];
+    }
+    template <bool VALUES>
+    __device__ __forceinline__ u32x4_t load(Place at) const
+    {
+        const int dim = VALUES ? p.c.dim_v : p.c.dim_k, d = (lane % NCH) * CH;
+        const T* from = VALUES ? values_of_head : keys_of_head;
+        if constexpr (ACCESS == kNear) {
+            // (chunks behind the last dimension are read from the first one)
+            return *reinterpret_cast<const u32x4_t*>(reinterpret_cast<const char*>(from + (d < dim ? d : 0)) + ((uint64_t)at << 4));
+        } else if constexpr (WHOLE) {
+            return *reinterpret_cast<const u32x4_t*>(from + at + (d < dim ? d : 0));
         } else {
             Chunk<T> x;
 #pragma unroll
-            for (int j = 0; j < CH; ++j) x[j] = from[d + j < dim ? d + j : 0];
+            for (int j = 0; j < CH; ++j) x[j] = from[at + (d + j < dim ? d + j : 0)];
             return __builtin_bit_cast(u32x4_t, x);
         }
     }
@@ -240,14 +264,7 @@ struct Attention {
         for (int j = 0; j < CH; ++j) y[j] = row && d + j < dim ? y[j] : (T)0.f;
         return __builtin_bit_cast(u32x4_t, y);
     }
-    // Row i * STEP + lane / NCH of 16 or 32 that start at row `base` of the tile (a
-    // multiple of 16); what depends on the lane alone stands apart.
-    template <bool VALUES>
-    __device__ __forceinline__ u32x4_t load(int i) const
-    {
-        const int64_t at = s.at[wave][VALUES][i * STEP + lane / NCH];
-        return VALUES ? load_chunk(p.c.values.data, at, p.c.dim_v) : load_chunk(p.c.keys.data, at, p.c.dim_k);
-    }
+    // Row i * STEP + lane / NCH; what depends on the lane alone stands apart.
     template <bool VALUES>
     __device__ __forceinline__ void put_chunk(LdsBytes to, int i, u32x4_t x)
     {
@@ -262,8 +279,12 @@ struct Attention {
     __device__ __forceinline__ void fetch(u32x4_t (&next)[kAhead ? N : 1]) const
     {
         if constexpr (kAhead) {
+            Place at[COUNT];
 #pragma unroll
-            for (int i = 0; i < COUNT; ++i) next[i] = load<VALUES>(i);
+            for (int i = 0; i < COUNT; ++i) at[i] = place_of<VALUES>(i);
+            __builtin_amdgcn_sched_barrier(0);          // all places before the first load
+#pragma unroll
+            for (int i = 0; i < COUNT; ++i) next[i] = load<VALUES>(at[i]);
         }
     }
     template <bool VALUES, int COUNT>
@@ -279,7 +300,7 @@ struct Attention {
             for (int i = 0; i < COUNT; ++i) put_chunk<VALUES>(to, i, next[i]);
         } else {
 #pragma unroll kBatch
-            for (int i = 0; i < COUNT; ++i) put_chunk<VALUES>(to, i, only_there(i, load<VALUES>(i), there, dim));
+            for (int i = 0; i < COUNT; ++i) put_chunk<VALUES>(to, i, only_there(i, load<VALUES>(place_of<VALUES>(i)), there, dim));
         }
     }
 
@@ -307,14 +328,64 @@ struct Attention {
     }
     static __device__ __forceinline__ bool finite(T x) { return __builtin_fabsf((float)x) < __builtin_inff(); }
 
-    // Products of a tile's 32 keys and the wave's queries.
+    // Operands are read from the LDS before their products begin, and those of a second
+    // tile among the products of the first: left to itself, the compiler waits for each
+    // before its product.
+    static constexpr bool kAmong = D * sizeof(T) <= 256;       // registers for two tiles
+    struct Operands {
+        Chunk<T> x[NCH / 2];
+    };
+    static __device__ __forceinline__ void reads_before_products()
+    {
+        if constexpr (kAmong) __builtin_amdgcn_sched_barrier(0);
+    }
+    template <int COUNT, int READS>
+    static __device__ __forceinline__ void reads_among_products()
+    {
+#pragma unroll
+        for (int i = 0; i < COUNT; ++i) {
+            __builtin_amdgcn_sched_group_barrier(0x100, READS, 0);                              // LDS reads
+            __builtin_amdgcn_sched_group_barrier(0x008, sizeof(T) == 2 ? 1 : CH, 0);            // matrix products
+        }
+    }
+    __device__ __forceinline__ Chunk<T> key_fragment(LdsBytes keys, int i) const
+    {
+        return *(InLds<Chunk<T>>)(keys + col * ROW + (((2 * i) ^ (half ^ key_swizzle(col))) << 4));
+    }
+    // Products of a tile's 32 keys and the wave's queries; of two.
     __device__ __forceinline__ f32x16_t scores(LdsBytes keys) const
     {
-        const int swizzle = half ^ key_swizzle(col);
+        Operands k;
+#pragma unroll
+        for (int i = 0; i < NCH / 2; ++i) k.x[i] = key_fragment(keys, i);
+        reads_before_products();
         f32x16_t x = {};
 #pragma unroll
-        for (int i = 0; i < NCH / 2; ++i) x = mma(*(InLds<Chunk<T>>)(keys + col * ROW + (((2 * i) ^ swizzle) << 4)), q[i], x);
+        for (int i = 0; i < NCH / 2; ++i) x = mma(k.x[i], q[i], x);
         return x;
+    }
+    __device__ __forceinline__ void scores(LdsBytes keys, f32x16_t (&x)[1]) const { x[0] = scores(keys); }
+    __device__ __forceinline__ void scores(LdsBytes keys, f32x16_t (&x)[2]) const
+    {
+        if constexpr (!kAmong) {
+            x[0] = scores(keys);
+            x[1] = scores(keys + TILE);
+            return;
+        }
+        Operands k[2];
+#pragma unroll
+        for (int i = 0; i < NCH / 2; ++i) k[0].x[i] = key_fragment(keys, i);
+        reads_before_products();
+        x[0] = x[1] = f32x16_t{};
+#pragma unroll
+        for (int i = 0; i < NCH / 2; ++i) {
+            k[1].x[i] = key_fragment(keys + TILE, i);
+            x[0] = mma(k[0].x[i], q[i], x[0]);
+        }
+        reads_among_products<NCH / 2, 1>();
+        reads_before_products();
+#pragma unroll
+        for (int i = 0; i < NCH / 2; ++i) x[1] = mma(k[1].x[i], q[i], x[1]);
     }
     // Whether there are tokens among the 32 from `first` on that not every query sees.
     __device__ __forceinline__ bool masked(uint32_t there, int first) const
@@ -385,12 +456,41 @@ struct Attention {
         l += sum;
         return w;
     }
+    // Products of a tile's 32 values and the weights, added to the results; of two tiles.
+    static constexpr int FRAGMENTS = BLOCKS * STEPS;
+    struct Values {
+        Chunk<T> x[FRAGMENTS];
+    };
     __device__ __forceinline__ void accumulate(LdsBytes values, const Weights& w)
     {
+        Values v;
 #pragma unroll
-        for (int b = 0; b < BLOCKS; ++b)
+        for (int i = 0; i < FRAGMENTS; ++i) v.x[i] = value_fragment(values, i / STEPS, i % STEPS);
+        reads_before_products();
 #pragma unroll
-            for (int u = 0; u < STEPS; ++u) o[b] = mma(value_fragment(values, b, u), w.p[u], o[b]);
+        for (int i = 0; i < FRAGMENTS; ++i) o[i / STEPS] = mma(v.x[i], w.p[i % STEPS], o[i / STEPS]);
+    }
+    __device__ __forceinline__ void accumulate(LdsBytes values, const Weights (&w)[1]) { accumulate(values, w[0]); }
+    __device__ __forceinline__ void accumulate(LdsBytes values, const Weights (&w)[2])
+    {
+        if constexpr (!kAmong) {
+            accumulate(values, w[0]);
+            accumulate(values + TILE, w[1]);
+            return;
+        }
+        Values v[2];
+#pragma unroll
+        for (int i = 0; i < FRAGMENTS; ++i) v[0].x[i] = value_fragment(values, i / STEPS, i % STEPS);
+        reads_before_products();
+#pragma unroll
+        for (int i = 0; i < FRAGMENTS; ++i) {
+            v[1].x[i] = value_fragment(values + TILE, i / STEPS, i % STEPS);
+            o[i / STEPS] = mma(v[0].x[i], w[0].p[i % STEPS], o[i / STEPS]);
+        }
+        reads_among_products<FRAGMENTS, sizeof(T) == 2 ? 2 : CH>();
+        reads_before_products();
+#pragma unroll
+        for (int i = 0; i < FRAGMENTS; ++i) o[i / STEPS] = mma(v[1].x[i], w[1].p[i % STEPS], o[i / STEPS]);
     }
     // Addresses are worked out anew for each piece: kept, they push results out of the registers.
     __device__ __forceinline__ void forget_addresses()
@@ -453,13 +553,14 @@ struct Attention {
         else
             return next;
     }
-    // The same for more queries: the waves go through each other's tokens.
+    // The same for more queries: the waves go through each other's tokens, SUBS tiles of them each.
+    template <int SUBS>
     __device__ __forceinline__ void pieces_together(int t, int end, int page)
     {
         constexpr int TOKENS = 16 * NW, HALF = N / 2;
         const LdsBytes keys = (LdsBytes)&s.kv[0], values = keys + SUB * TILE;
         const int mine = wave * 16 * ROW;
-        const int subs = sets == NW ? SUB : 1, first_sub = sets == NW ? 0 : wave / sets;
+        const int first_sub = SUBS == SUB ? 0 : wave / 2;
         uint32_t after = places(t + wave * 16, page);
         u32x4_t next[kAhead ? N : 1];
         fetch<false, HALF>(next);
@@ -471,22 +572,20 @@ struct Attention {
             if (lane == 0) s.there[wave] = there;
             fetch<true, HALF>(next);
             __syncthreads();
-            f32x16_t x[SUB];
-            uint32_t here[SUB];
+            // tiles of which a token is not there, in 32 bits
+            uint32_t here[SUBS];
+#pragma unroll
+            for (int r = 0; r < SUBS; ++r)
+                here[r] = __builtin_amdgcn_readfirstlane(s.there[2 * (first_sub + r)] | s.there[2 * (first_sub + r) + 1] << 16);
+            f32x16_t x[SUBS];
+            Weights w[SUBS];
+            scores(keys + first_sub * TILE, x);
             float top = -__builtin_inff();
 #pragma unroll
-            for (int r = 0; r < SUB; ++r) {
-                if (r > 0 && r >= subs) continue;
-                const int sub = first_sub + r;
-                x[r] = scores(keys + sub * TILE);
-                here[r] = __builtin_amdgcn_readfirstlane(s.there[2 * sub] | s.there[2 * sub + 1] << 16);
-                top = fmaxf(top, only_seen(x[r], here[r], t + sub * kKvTokens));
-            }
+            for (int r = 0; r < SUBS; ++r) top = fmaxf(top, only_seen(x[r], here[r], t + (first_sub + r) * kKvTokens));
             follow(top);
-            Weights w[SUB];
 #pragma unroll
-            for (int r = 0; r < SUB; ++r)
-                if (r == 0 || r < subs) w[r] = weights(x[r]);
+            for (int r = 0; r < SUBS; ++r) w[r] = weights(x[r]);
             put<true, HALF>(values + mine, next);
             if (t + TOKENS < end) {
                 after = places(t + wave * 16 + TOKENS, page);
@@ -495,12 +594,9 @@ struct Attention {
             }
             __syncthreads();
 #pragma unroll
-            for (int r = 0; r < SUB; ++r) {
-                if (r > 0 && r >= subs) continue;
-                const int sub = first_sub + r;
-                if (masked(here[r], t + sub * kKvTokens)) note_wild(values + sub * TILE);
-                accumulate(values + sub * TILE, w[r]);
-            }
+            for (int r = 0; r < SUBS; ++r)
+                if (masked(here[r], t + (first_sub + r) * kKvTokens)) note_wild(values + (first_sub + r) * TILE);
+            accumulate(values + first_sub * TILE, w);
         }
     }
 
@@ -526,6 +622,8 @@ struct Attention {
         sets = a.rows <= kAttnRows ? 1 : (a.rows <= 2 * kAttnRows || NW == 2 ? 2 : NW);
         stop = a.end;
         table = seg.row * p.c.max_pages;
+        keys_of_head = static_cast<const T*>(p.c.keys.data) + kv_head * p.c.keys.hs;
+        values_of_head = static_cast<const T*>(p.c.values.data) + kv_head * p.c.values.hs;
         constexpr int PIECE = kKvTokens * NW;
         const int t = a.begin + first_step * PIECE;
         // (64 bits: the last piece may reach beyond 2^31)
@@ -541,8 +639,10 @@ struct Attention {
         if (t < stop) {
             if (sets == 1)
                 pieces_apart(t, stop, page);
-            else
-                pieces_together(t, stop, page);
+            else if (sets == NW)
+                pieces_together<SUB>(t, stop, page);
+            else if constexpr (NW > 2)
+                pieces_together<1>(t, stop, page);
         }
         l = sum_halves(l);
         if (half == 0) {
@@ -621,12 +721,12 @@ __device__ __forceinline__ X uniform(X x)
 // and 1 registers, 16 to 32, and as many as the queries.
 constexpr int attn_occupancy(int dim, int size) { return dim * size <= 128 ? 3 : (dim * size <= 256 ? 2 : 1); }
 
-template <class T, int D, int NW, bool WHOLE>
+template <class T, int D, int NW, int ACCESS>
 __global__ __launch_bounds__(64 * NW, attn_occupancy(D, sizeof(T))) void k_attention(
     AttentionParams p)
 {
-    __shared__ typename Attention<T, D, NW, WHOLE>::Lds lds;
-    Attention<T, D, NW, WHOLE> w(p, lds);
+    __shared__ typename Attention<T, D, NW, ACCESS>::Lds lds;
+    Attention<T, D, NW, ACCESS> w(p, lds);
     const AttnWork work(p);
     const int all = (int)(p.n_groups + p.c.n);
     if (threadIdx.x < 2) lds.wild[threadIdx.x] = 0;
@@ -697,10 +797,12 @@ hipError_t launch_dim(const AttentionParams& p, hipStream_t stream)
 {
     constexpr int NW = attn_waves(sizeof(T) == 4 ? DWS_FLOAT32 : DWS_BFLOAT16, D);
     const unsigned grid = (unsigned)p.workgroups;
-    if (p.whole_kv)
-        k_attention<T, D, NW, true><<<grid, 64 * NW, 0, stream>>>(p);
+    if (p.kv_access == kNear)
+        k_attention<T, D, NW, kNear><<<grid, 64 * NW, 0, stream>>>(p);
+    else if (p.kv_access == kFar)
+        k_attention<T, D, NW, kFar><<<grid, 64 * NW, 0, stream>>>(p);
     else
-        k_attention<T, D, NW, false><<<grid, 64 * NW, 0, stream>>>(p);
+        k_attention<T, D, NW, kElements><<<grid, 64 * NW, 0, stream>>>(p);
     return hipGetLastError();
 }
 template <class T>

@@ -26,6 +26,7 @@ struct KvView {
     const int* lengths;
     int64_t n_rows, max_pages;
     int n_pages, page_tokens;
+    uint32_t page_magic, page_shift;    // t / page_tokens = (t * magic >> 32) >> shift for t < 2^31; magic 0: t
     int heads, dim_k, dim_v;
     int64_t tokens, n;
     const int64_t* offsets;     // n + 1, or null: `each` tokens a sequence
@@ -91,6 +92,10 @@ struct AttnDone {
     int position, table;
 };
 
+// Rows that are not made of whole, aligned 16 bytes; rows that are; and those in pools
+// whose places, in 16 bytes, are 32-bit numbers.
+enum AttnAccess { kElements, kFar, kNear };
+
 struct AttentionParams {
     KvView c;
     int heads_q, share;         // share: query heads of a key head
@@ -99,7 +104,9 @@ struct AttentionParams {
     int64_t n_groups;
     const int64_t* groups;
     const int* shared;
-    int zero_rest, whole_q, whole_kv, whole_out;
+    int zero_rest, whole_q, whole_out;
+    int kv_access;              // how keys and values are read (AttnAccess)
+    uint32_t key_ps, key_ts, value_ps, value_ts;    // kNear: strides in 16 bytes
     HeadRows q, out;
     float* lse;
     int dtype, padded;

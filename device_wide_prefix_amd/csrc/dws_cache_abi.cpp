@@ -87,6 +87,12 @@ dws_status check_view(Arrays* arrays, const dws_kv_cache& c, const dws_page_seqs
     v->max_pages = c.max_pages;
     v->n_pages = (int)c.n_pages;
     v->page_tokens = (int)c.page_tokens;
+    // 31-bit numbers divided by page_tokens: with 2^l the power of two at or above it,
+    // ceil(2^(31 + l) / page_tokens) is exact enough and below 2^32
+    int l = 0;
+    while (((int64_t)1 << l) < c.page_tokens) ++l;
+    v->page_magic = l == 0 ? 0 : (uint32_t)((((unsigned __int128)1 << (31 + l)) + c.page_tokens - 1) / c.page_tokens);
+    v->page_shift = l == 0 ? 0 : (uint32_t)(l - 1);
     v->heads = c.heads;
     v->dim_k = c.dim_k;
     v->dim_v = c.dim_v;
@@ -240,8 +246,19 @@ dws_status attention_entry(const dws_pages_attention_args* a, hipStream_t stream
     p.zero_rest = a->zero_rest != 0;
     const int64_t e = (int64_t)size_of(c.dtype);
     p.whole_q = whole(a->q.data, e, 16, c.dim_k, a->q.token_stride, a->q.head_stride);
-    p.whole_kv = whole(c.keys.data, e, 16, c.dim_k, c.keys.page_stride, c.keys.token_stride, c.keys.head_stride) &&
-                 whole(c.values.data, e, 16, c.dim_v, c.values.page_stride, c.values.token_stride, c.values.head_stride);
+    const bool whole_kv = whole(c.keys.data, e, 16, c.dim_k, c.keys.page_stride, c.keys.token_stride, c.keys.head_stride) &&
+                          whole(c.values.data, e, 16, c.dim_v, c.values.page_stride, c.values.token_stride, c.values.head_stride);
+    // (arrays.r[0] and [1] are the keys and the values)
+    const bool near = arrays.r[0].end - arrays.r[0].begin <= (uintptr_t)1 << 36 && arrays.r[1].end - arrays.r[1].begin <= (uintptr_t)1 << 36;
+    p.kv_access = !whole_kv ? kElements : (near ? kNear : kFar);
+    if (p.kv_access == kNear) {
+        // a stride that nothing is apart by may be any
+        auto units = [&](int64_t stride, int64_t count) { return count > 1 ? (uint32_t)(stride * e / 16) : 0u; };
+        p.key_ps = units(c.keys.page_stride, c.n_pages);
+        p.key_ts = units(c.keys.token_stride, c.page_tokens);
+        p.value_ps = units(c.values.page_stride, c.n_pages);
+        p.value_ts = units(c.values.token_stride, c.page_tokens);
+    }
     p.whole_out = whole(a->out.data, e, 4 * e, c.dim_v, a->out.token_stride, a->out.head_stride);
     p.lse = a->d_lse;
     p.dtype = c.dtype;
