@@ -496,6 +496,7 @@ struct Attention {
     __device__ __forceinline__ void forget_addresses()
     {
         asm volatile("" : "+v"(lane));
+        lane &= 63;         // (not negative, for divisions)
         half = lane >> 5;
         col = lane & 31;
     }
@@ -566,6 +567,12 @@ struct Attention {
         fetch<false, HALF>(next);
         page = page_of(t + wave * 16 + TOKENS, 16);
         for (; t < end; t += TOKENS) {
+            // Of the two workgroups on a compute unit the older one goes first, and would be done
+            // long before the other: they take turns (attend_prompts: 670 to 629 us).
+            if (((t / TOKENS) ^ (blockIdx.x / 256)) & 1)
+                __builtin_amdgcn_s_setprio(1);
+            else
+                __builtin_amdgcn_s_setprio(0);
             forget_addresses();
             there = after;
             put<false, HALF>(keys + mine, next);
@@ -573,13 +580,13 @@ struct Attention {
             fetch<true, HALF>(next);
             __syncthreads();
             // tiles of which a token is not there, in 32 bits
+            f32x16_t x[SUBS];
+            Weights w[SUBS];
+            scores(keys + first_sub * TILE, x);
             uint32_t here[SUBS];
 #pragma unroll
             for (int r = 0; r < SUBS; ++r)
                 here[r] = __builtin_amdgcn_readfirstlane(s.there[2 * (first_sub + r)] | s.there[2 * (first_sub + r) + 1] << 16);
-            f32x16_t x[SUBS];
-            Weights w[SUBS];
-            scores(keys + first_sub * TILE, x);
             float top = -__builtin_inff();
 #pragma unroll
             for (int r = 0; r < SUBS; ++r) top = fmaxf(top, only_seen(x[r], here[r], t + (first_sub + r) * kKvTokens));
@@ -598,6 +605,7 @@ struct Attention {
                 if (masked(here[r], t + (first_sub + r) * kKvTokens)) note_wild(values + (first_sub + r) * TILE);
             accumulate(values + first_sub * TILE, w);
         }
+        __builtin_amdgcn_s_setprio(0);
     }
 
     __device__ __forceinline__ void store(int64_t at, f32x4_t x, int d)

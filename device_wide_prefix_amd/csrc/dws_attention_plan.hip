@@ -32,6 +32,31 @@ __device__ __forceinline__ float load_as_float(const void* from, int64_t at, int
     return (float)static_cast<const f16_t*>(from)[at];
 }
 
+// Four dimensions from d on, which are whole units where whole_out says so.
+template <class T, class V>
+__device__ __forceinline__ void store_four_as(const AttentionParams& p, int64_t at, int d, V x)
+{
+    typedef T Four __attribute__((ext_vector_type(4)));
+    T* to = static_cast<T*>(p.out.data) + at + d;
+    if (p.whole_out) {
+        if (d < p.c.dim_v) *reinterpret_cast<Four*>(to) = __builtin_convertvector(x, Four);
+    } else {
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            if (d + k < p.c.dim_v) to[k] = (T)x[k];
+    }
+}
+template <class V>
+__device__ __forceinline__ void store_four(const AttentionParams& p, int64_t at, int d, V x)
+{
+    if (p.dtype == DWS_FLOAT32)
+        store_four_as<float>(p, at, d, x);
+    else if (p.dtype == DWS_BFLOAT16)
+        store_four_as<bf16_t>(p, at, d, x);
+    else
+        store_four_as<f16_t>(p, at, d, x);
+}
+
 // One row of queries by the whole workgroup, 512 tokens at a time, each token's score
 // by a thread and each dimension's sum by a thread: only what the row sees is touched,
 // so that values which are not finite stay with those that see them.
@@ -145,7 +170,8 @@ __global__ __launch_bounds__(kJoinThreads) void k_attention_join(AttentionParams
                     float2 y[8];
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
-                        const int k = k0 + i * ways < n ? k0 + i * ways : k0;
+                        const int k = k0 + i * ways;
+                        if (k >= n) break;
                         const int64_t at = (2 * (int64_t)(t.first + k) + (k == 0 ? 1 : 0)) * p.tile_rows + row;
                         y[i] = p.part_stat[at];
                         o[i] = *reinterpret_cast<const f32x4*>(p.part + at * p.padded + 4 * q);
@@ -182,9 +208,7 @@ __global__ __launch_bounds__(kJoinThreads) void k_attention_join(AttentionParams
             const int64_t behind = a.row + r, token = a.begin + behind / p.share;
             const int head = h * p.share + (int)(behind % p.share);
             const float by = l == 0.f ? 0.f : 1.f / l;
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-                if (4 * q + k < p.c.dim_v) store_out(p, token * p.out.ts + head * p.out.hs + 4 * q + k, l == 0.f ? 0.f : sum[k] * by);
+            store_four(p, token * p.out.ts + head * p.out.hs, 4 * q, l == 0.f ? f32x4{0.f, 0.f, 0.f, 0.f} : sum * by);
             if (q == 0 && p.lse != nullptr)
                 p.lse[token * p.heads_q + head] = l == 0.f ? -__builtin_inff() : (m + __builtin_log2f(l)) * 0.693147180559945f;
         }
