@@ -1034,17 +1034,18 @@ _ATTENTION = struct.Struct("@" + _KV + "ifqPPi" + 2 * "Pqq" + "PPQ")
 _BEAM = struct.Struct("@PqqqqqiiPPq" + 8 * "P" + "Q")
 
 
-def _pool(t, what, pages, page_tokens, heads, dtype, device):
-    """dws_page_pool of t (pages, page_tokens, heads, dim) and its dim."""
-    try:
-        ok = t.dim() == 4 and t.dtype == dtype and t.device == device and t.shape[:3] == (pages, page_tokens, heads) and \
-            (t.stride(3) == 1 or t.shape[3] <= 1)
-    except AttributeError:
-        ok = False
-    if not ok:
-        raise ValueError(f"{what} must have shape {(pages, page_tokens, heads)} + (dim,), dtype {dtype} and a contiguous "
-                         f"last dimension, and be on {device}")
-    return (t.data_ptr(), *t.stride()[:3]), t.shape[3]
+_workspaces = {}        # bytes by a call's sizes: asking again takes as long as a kernel's launch
+
+
+def _workspace_bytes(query, key, make):
+    need = _workspaces.get(key)
+    if need is None:
+        out = ctypes.c_size_t(0)
+        _check(getattr(load_library(), query)(make(), ctypes.byref(out)), query)
+        if len(_workspaces) >= 4096:
+            _workspaces.clear()
+        need = _workspaces[key] = out.value
+    return need
 
 
 def _kv_args(keys, values, table, lengths, tokens, rows, offsets):
@@ -1053,20 +1054,25 @@ def _kv_args(keys, values, table, lengths, tokens, rows, offsets):
     if keys.dim() != 4:
         raise ValueError("keys and values must be (pages, page_tokens, heads, dim)")
     device, dtype = keys.device, keys.dtype
-    code = _float_code(dtype, "keys")
-    shape = keys.shape[:3]
-    k, dim_k = _pool(keys, "keys", *shape, dtype, device)
-    v, dim_v = _pool(values, "values", *shape, dtype, device)
+    code = _float_codes.get(dtype) or _float_code(dtype, "keys")
+    pages, page_tokens, heads, dim_k = keys.shape
+    k, v, dim_v = keys.stride(), (), -1
+    try:
+        if values.dtype == dtype and values.device == device:
+            *same, dim_v = values.shape
+            v = values.stride() if same == [pages, page_tokens, heads] else ()
+    except AttributeError:
+        pass
+    if k[3] != 1 and dim_k > 1 or not v or v[3] != 1 and dim_v > 1:
+        raise ValueError(f"keys and values must have shape {(pages, page_tokens, heads)} + (dim,), dtype {dtype} and a "
+                         f"contiguous last dimension, and be on {device}")
     int32 = _int32()
     try:
-        ok = table.dtype == int32 and table.dim() == 2 and table.device == device and table.is_contiguous()
-    except AttributeError:
-        ok = False
-    if not ok:
-        raise ValueError(f"table must be a contiguous int32 tensor (rows, pages) on {device}")
-    n_rows, max_pages = table.shape
+        n_rows, max_pages = table.shape if table.dtype == int32 and table.device == device and table.is_contiguous() else ()
+    except (AttributeError, ValueError):
+        raise ValueError(f"table must be a contiguous int32 tensor (rows, pages) on {device}") from None
     held = _device_ints(lengths, "lengths", int32, n_rows, device)
-    at = of = None
+    at = of = 0
     n = n_rows
     if offsets is not None:
         of = _device_ints(offsets, "offsets", _int64(), None, device)
@@ -1076,12 +1082,12 @@ def _kv_args(keys, values, table, lengths, tokens, rows, offsets):
     if rows is not None:
         at = _device_ints(rows, "rows", int32, n if offsets is not None else None, device)
         n = rows.shape[0]
-    if rows is None and n > n_rows:
+    elif n > n_rows:
         raise ValueError(f"{n} sequences, but the table has {n_rows} rows")
     if offsets is None and (tokens % n if n else tokens):
         raise ValueError(f"{tokens} tokens cannot be shared out to {n} sequences")
-    return (*k, *v, table.data_ptr(), held, shape[0], n_rows, max_pages, shape[1], shape[2], dim_k, dim_v, code,
-            tokens, n, of or 0, at or 0), device, n
+    return (keys.data_ptr(), k[0], k[1], k[2], values.data_ptr(), v[0], v[1], v[2], table.data_ptr(), held, pages, n_rows,
+            max_pages, page_tokens, heads, dim_k, dim_v, code, tokens, n, of, at), device, n
 
 
 def pages_append(keys, values, table, lengths, k, v, rows=None, offsets=None, granted=None, positions=None, freqs=None,
@@ -1102,9 +1108,10 @@ def pages_append(keys, values, table, lengths, k, v, rows=None, offsets=None, gr
     import torch
     _records_no_graph("pages_append", keys, values, k, v, q, q_out)
     _gpu_tensor(k, "k")
-    tokens = k.shape[0] if k.dim() == 3 else -1
+    shape = k.shape
+    tokens = shape[0] if len(shape) == 3 else -1
     a, device, n = _kv_args(keys, values, table, lengths, max(tokens, 0), rows, offsets)
-    dtype, heads, dim_k, dim_v = keys.dtype, keys.shape[2], keys.shape[3], values.shape[3]
+    dtype, heads, dim_k, dim_v = keys.dtype, a[14], a[15], a[16]
     kr, vr = _rows(k, "k", (tokens, heads, dim_k), dtype, device), _rows(v, "v", (tokens, heads, dim_v), dtype, device)
     ok = 0 if granted is None else _device_ints(granted, "granted", torch.int32, n, device)
     at = 0 if positions is None else _device_ints(positions, "positions", torch.int32, tokens, device)
@@ -1121,13 +1128,17 @@ def pages_append(keys, values, table, lengths, k, v, rows=None, offsets=None, gr
             _gpu_tensor(q, "q")
             if q.dim() != 3:
                 raise ValueError("q must be (tokens, heads_q, dim_k)")
-            heads_q = q.shape[1]
+            shape = q.shape
+            heads_q = shape[1]
             qr = _rows(q, "q", (tokens, heads_q, dim_k), dtype, device)
             if q_out is None:
-                q_out, zero = torch.empty(q.shape, dtype=dtype, device=device), 1
-            to = _rows(q_out, "q_out", q.shape, dtype, device)
+                q_out, zero = torch.empty(shape, dtype=dtype, device=device), 1
+                to = q_out.data_ptr(), heads_q * dim_k, dim_k
+            else:
+                to = _rows(q_out, "q_out", shape, dtype, device)
         _check(load_library().dws_pages_append(
-            _APPEND.pack(*a, ok, at, by, pairs, bool(adjacent), heads_q, zero, *kr, *vr, *qr, *to), s), "dws_pages_append")
+            _APPEND.pack(*a, ok, at, by, pairs, bool(adjacent), heads_q, zero, *kr, *vr, *qr, *to), s),
+            "dws_pages_append")
     return q_out
 
 
@@ -1147,11 +1158,11 @@ def pages_attention(q, keys, values, table, lengths, rows=None, offsets=None, gr
     _gpu_tensor(q, "q")
     if q.dim() != 3:
         raise ValueError("q must be (tokens, heads_q, dim_k)")
-    tokens, heads_q = q.shape[:2]
+    tokens, heads_q, _ = q.shape
     a, device, n = _kv_args(keys, values, table, lengths, tokens, rows, offsets)
-    dtype, dim_k, dim_v = keys.dtype, keys.shape[3], values.shape[3]
-    if heads_q < 1 or heads_q % keys.shape[2]:
-        raise ValueError(f"{heads_q} query heads are no multiple of {keys.shape[2]}")
+    dtype, heads, dim_k, dim_v = keys.dtype, a[14], a[15], a[16]
+    if heads_q < 1 or heads_q % heads:
+        raise ValueError(f"{heads_q} query heads are no multiple of {heads}")
     qr = _rows(q, "q", (tokens, heads_q, dim_k), dtype, device)
     n_groups = gp = sh = 0
     if (groups is None) != (shared is None):
@@ -1160,24 +1171,28 @@ def pages_attention(q, keys, values, table, lengths, rows=None, offsets=None, gr
         gp, n_groups = _device_ints(groups, "groups", torch.int64, None, device), groups.shape[0] - 1
         sh = _device_ints(shared, "shared", torch.int32, n_groups, device)
     with _on_stream(q, stream) as s:
-        zero = 0
+        zero, shape = 0, (tokens, heads_q, dim_v)
         if out is None:
-            out, zero = torch.empty((tokens, heads_q, dim_v), dtype=dtype, device=device), int(offsets is not None)
-        elif lse is True and offsets is not None:
-            lse = torch.full((tokens, heads_q), float("-inf"), dtype=torch.float32, device=device)
-        to = _rows(out, "out", (tokens, heads_q, dim_v), dtype, device)
-        if lse is True:
-            lse = torch.empty((tokens, heads_q), dtype=torch.float32, device=device)
-        if lse is not None and not (isinstance(lse, torch.Tensor) and lse.dtype == torch.float32 and lse.device == device and
-                                    lse.shape == (tokens, heads_q) and lse.is_contiguous()):
-            raise ValueError(f"lse must be a contiguous float32 tensor {(tokens, heads_q)} on {device}")
-        to_lse = 0 if lse is None else lse.data_ptr()
+            out, zero = torch.empty(shape, dtype=dtype, device=device), int(offsets is not None)
+            to = out.data_ptr(), heads_q * dim_v, dim_v
+        else:
+            if lse is True and offsets is not None:
+                lse = torch.full((tokens, heads_q), float("-inf"), dtype=torch.float32, device=device)
+            to = _rows(out, "out", shape, dtype, device)
+        to_lse = 0
+        if lse is not None:
+            if lse is True:
+                lse = torch.empty((tokens, heads_q), dtype=torch.float32, device=device)
+            if not (isinstance(lse, torch.Tensor) and lse.dtype == torch.float32 and lse.device == device and
+                    lse.shape == (tokens, heads_q) and lse.is_contiguous()):
+                raise ValueError(f"lse must be a contiguous float32 tensor {(tokens, heads_q)} on {device}")
+            to_lse = lse.data_ptr()
         rest = (heads_q, dim_k ** -0.5 if scale is None else float(scale), n_groups, gp, sh, zero, *qr, *to, to_lse)
-        need, lib = ctypes.c_size_t(0), load_library()
-        _check(lib.dws_pages_attention_workspace(_ATTENTION.pack(*a, *rest, 0, 0), ctypes.byref(need)),
-               "dws_pages_attention_workspace")
-        work = torch.empty(need.value, dtype=torch.uint8, device=device)
-        _check(lib.dws_pages_attention(_ATTENTION.pack(*a, *rest, work.data_ptr(), need.value), s), "dws_pages_attention")
+        need = _workspace_bytes("dws_pages_attention_workspace", (heads_q, n_groups, *a[10:20]),
+                                lambda: _ATTENTION.pack(*a, *rest, 0, 0))
+        work = torch.empty(need, dtype=torch.uint8, device=device)
+        _check(load_library().dws_pages_attention(_ATTENTION.pack(*a, *rest, work.data_ptr(), need), s),
+               "dws_pages_attention")
         del work
     return out if lse is None else (out, lse)
 
@@ -1204,32 +1219,39 @@ def beam_select(logits, scores, k=None, finished=None, end_token=0, rows=None, s
     batch, beams, vocab = logits.shape
     k = beams if k is None else int(k)
 
-    def plain(t, what, *dtypes):
-        if not (isinstance(t, torch.Tensor) and t.dtype in dtypes and t.shape == (batch, beams) and t.device == device and
-                t.is_contiguous()):
-            raise ValueError(f"{what} must be a contiguous {dtypes[0]} tensor {(batch, beams)} on {device}")
-        return t.data_ptr()
+    shape, int32 = (batch, beams), torch.int32
+
+    def plain(t, what, dtype, other=None):
+        try:
+            if t.shape == shape and (t.dtype == dtype or t.dtype == other) and t.device == device and t.is_contiguous():
+                return t.data_ptr()
+        except AttributeError:
+            pass
+        raise ValueError(f"{what} must be a contiguous {dtype} tensor {shape} on {device}")
 
     of = plain(scores, "scores", torch.float32)
     over = 0 if finished is None else plain(finished, "finished", torch.bool, torch.uint8)
-    at = 0 if rows is None else plain(rows, "rows", torch.int32)
+    at = 0 if rows is None else plain(rows, "rows", int32)
     if rows is not None and k != beams:
         raise ValueError("rows can be followed only with as many continuations as beams")
     with _on_stream(logits, stream) as s:
-        best = torch.empty((batch, k), dtype=torch.float32, device=device)
-        parents, tokens = torch.empty((2, batch, k), dtype=torch.int32, device=device).unbind(0)
-        moves = (0, 0, 0)
+        best = torch.empty_like(scores) if k == beams else torch.empty((batch, k), dtype=torch.float32, device=device)
+        parents = torch.empty_like(best, dtype=int32)
+        tokens = torch.empty_like(parents)
+        new = src = dst = None
         if rows is not None:
-            new, src, dst = torch.empty((3, batch * beams), dtype=torch.int32, device=device).unbind(0)
-            moves = new.data_ptr(), src.data_ptr(), dst.data_ptr()
-        a = (logits.data_ptr(), batch, beams, vocab, logits.stride(0), logits.stride(1), code, k, of, over, int(end_token), at,
-             best.data_ptr(), parents.data_ptr(), tokens.data_ptr(), *moves)
-        need, lib = ctypes.c_size_t(0), load_library()
-        _check(lib.dws_beam_select_workspace(_BEAM.pack(*a, 0, 0), ctypes.byref(need)), "dws_beam_select_workspace")
-        work = torch.empty(need.value, dtype=torch.uint8, device=device)
-        _check(lib.dws_beam_select(_BEAM.pack(*a, work.data_ptr(), need.value), s), "dws_beam_select")
+            new = torch.empty_like(parents)
+            src = torch.empty(batch * beams, dtype=int32, device=device)
+            dst = torch.empty_like(src)
+            at = at, best.data_ptr(), parents.data_ptr(), tokens.data_ptr(), new.data_ptr(), src.data_ptr(), dst.data_ptr()
+        else:
+            at = 0, best.data_ptr(), parents.data_ptr(), tokens.data_ptr(), 0, 0, 0
+        a = (logits.data_ptr(), batch, beams, vocab, *logits.stride()[:2], code, k, of, over, int(end_token), *at)
+        need = _workspace_bytes("dws_beam_select_workspace", a[1:8], lambda: _BEAM.pack(*a, 0, 0))
+        work = torch.empty(need, dtype=torch.uint8, device=device)
+        _check(load_library().dws_beam_select(_BEAM.pack(*a, work.data_ptr(), need), s), "dws_beam_select")
         del work
-    return (best, parents, tokens) if rows is None else (best, parents, tokens, new.view(batch, beams), src, dst)
+    return (best, parents, tokens) if rows is None else (best, parents, tokens, new, src, dst)
 
 
 def device_memory_info() -> dict:
