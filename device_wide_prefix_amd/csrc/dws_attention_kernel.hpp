@@ -86,6 +86,9 @@ struct Attention {
     // Whether a small tile's keys and values both do.
     static constexpr bool kBoth = kAhead && D * sizeof(T) <= 256;
     static constexpr int SUB = NW / 2;                  // tiles of 32 tokens that all waves go through at a time
+    // Whether the pieces of larger tiles go from memory to the LDS by themselves: two fit there.
+    static constexpr bool kStream = ACCESS == kNear && sizeof(T) == 2 && D <= 128;
+    static_assert(!kStream || 4 * SUB * TILE <= NW * RESULT, "two pieces of keys and values");
 
     struct Lds {
         // a wave's keys, then its values; or all waves' keys, and their values; then results
@@ -93,7 +96,7 @@ struct Attention {
         AttnSeg segs[kAttnSegs + 1];
         // where a token's keys and values are: elements, or 16 bytes of 32-bit numbers
         std::conditional_t<ACCESS == kNear, uint32_t, int64_t> at[NW][2][kKvTokens];
-        uint32_t there[NW];             // which of a wave's tokens are there
+        uint32_t there[2][NW];          // which of a wave's tokens are there, of a piece and the next
         int wild[2];                    // rows to compute again, of this tile and the next
         float m[kAttnRows * NW], l[kAttnRows * NW];
     };
@@ -576,7 +579,7 @@ struct Attention {
             forget_addresses();
             there = after;
             put<false, HALF>(keys + mine, next);
-            if (lane == 0) s.there[wave] = there;
+            if (lane == 0) s.there[0][wave] = there;
             fetch<true, HALF>(next);
             __syncthreads();
             // tiles of which a token is not there, in 32 bits
@@ -586,7 +589,7 @@ struct Attention {
             uint32_t here[SUBS];
 #pragma unroll
             for (int r = 0; r < SUBS; ++r)
-                here[r] = __builtin_amdgcn_readfirstlane(s.there[2 * (first_sub + r)] | s.there[2 * (first_sub + r) + 1] << 16);
+                here[r] = __builtin_amdgcn_readfirstlane(s.there[0][2 * (first_sub + r)] | s.there[0][2 * (first_sub + r) + 1] << 16);
             float top = -__builtin_inff();
 #pragma unroll
             for (int r = 0; r < SUBS; ++r) top = fmaxf(top, only_seen(x[r], here[r], t + (first_sub + r) * kKvTokens));
@@ -606,6 +609,108 @@ struct Attention {
             accumulate(values + first_sub * TILE, w);
         }
         __builtin_amdgcn_s_setprio(0);
+    }
+    // Keys (values) of the wave's 16 tokens, whose places are known, from memory to the LDS, 64
+    // lanes' chunks one behind the other, without a register between; each lane brings the chunk
+    // that belongs into its place. In assembly, since of the compiler's own such loads every
+    // read of the LDS would wait for all; `landed` does.
+    template <bool VALUES>
+    __device__ __forceinline__ uint32_t chunk_of(int i) const
+    {
+        const int r = lane / NCH;
+        return (uint32_t)(lane % NCH) ^ (uint32_t)(VALUES ? value_swizzle(r) ^ value_swizzle(i * STEP) : key_swizzle(r) ^ key_swizzle(i * STEP));
+    }
+    template <bool VALUES>
+    __device__ __forceinline__ void stream(LdsBytes to) const
+    {
+        const uint32_t chunks = (uint32_t)(VALUES ? p.c.dim_v : p.c.dim_k) / CH;
+        const char* head = reinterpret_cast<const char*>(VALUES ? values_of_head : keys_of_head);
+        Place at[N / 2];
+#pragma unroll
+        for (int i = 0; i < N / 2; ++i) at[i] = place_of<VALUES>(i);
+        __builtin_amdgcn_sched_barrier(0);          // all places before the first load
+#pragma unroll
+        for (int i = 0; i < N / 2; ++i) {
+            const uint32_t c = chunk_of<VALUES>(i);
+            asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off"
+                         :
+                         : "v"(head + ((uint64_t)(at[i] + (c < chunks ? c : 0)) << 4)), "s"((uint32_t)(uintptr_t)(to + i * STEP * ROW))
+                         : "memory");
+        }
+    }
+    __device__ __forceinline__ void stream_piece(LdsBytes keys) const
+    {
+        stream<false>(keys);
+        stream<true>(keys + SUB * TILE);
+    }
+    // What has been streamed is there, and 0 where a token's values or a dimension are not.
+    __device__ __forceinline__ void landed(LdsBytes keys) const
+    {
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        if (there == 0xffffu && p.c.dim_k == D && p.c.dim_v == D) return;
+#pragma unroll
+        for (int i = 0; i < N / 2; ++i) {
+            const InLds<u32x4_t> at = (InLds<u32x4_t>)(keys + i * STEP * ROW + lane * 16);
+            if ((int)chunk_of<false>(i) * CH >= p.c.dim_k) *at = u32x4_t{};
+            if (!(there >> (i * STEP + lane / NCH) & 1) || (int)chunk_of<true>(i) * CH >= p.c.dim_v) at[SUB * TILE / 16] = u32x4_t{};
+        }
+    }
+    // pieces_together with the next piece's keys and values on their way to the other half of the LDS.
+    template <int SUBS>
+    __device__ __forceinline__ void pieces_streamed(int t, int end, int page)
+    {
+        constexpr int TOKENS = 16 * NW, PIECE = 2 * SUB * TILE;
+        const LdsBytes kv = (LdsBytes)&s.kv[0];
+        const int mine = wave * 16 * ROW, first_sub = SUBS == SUB ? 0 : wave / 2;
+        uint32_t after = places(t + wave * 16, page);
+        stream_piece(kv + mine);
+        page = page_of(t + wave * 16 + TOKENS, 16);
+        for (int turn = 0; t < end; t += TOKENS, turn ^= 1) {
+            // Of the two workgroups on a compute unit the older one goes first, and would be done
+            // long before the other: they take turns.
+            if ((turn ^ (blockIdx.x / 256)) & 1)
+                __builtin_amdgcn_s_setprio(1);
+            else
+                __builtin_amdgcn_s_setprio(0);
+            forget_addresses();
+            there = after;
+            const LdsBytes keys = kv + turn * PIECE, values = keys + SUB * TILE;
+            landed(keys + mine);
+            if (lane == 0) s.there[turn][wave] = there;
+            __syncthreads();            // and the other half has been read
+            if (t + TOKENS < end) {
+                after = places(t + wave * 16 + TOKENS, page);
+                stream_piece(kv + (turn ^ 1) * PIECE + mine);
+                page = page_of(t + wave * 16 + 2 * TOKENS, 16);
+            }
+            // tiles of which a token is not there, in 32 bits
+            f32x16_t x[SUBS];
+            Weights w[SUBS];
+            scores(keys + first_sub * TILE, x);
+            uint32_t here[SUBS];
+#pragma unroll
+            for (int r = 0; r < SUBS; ++r)
+                here[r] = __builtin_amdgcn_readfirstlane(s.there[turn][2 * (first_sub + r)] | s.there[turn][2 * (first_sub + r) + 1] << 16);
+            float top = -__builtin_inff();
+#pragma unroll
+            for (int r = 0; r < SUBS; ++r) top = fmaxf(top, only_seen(x[r], here[r], t + (first_sub + r) * kKvTokens));
+            follow(top);
+#pragma unroll
+            for (int r = 0; r < SUBS; ++r) w[r] = weights(x[r]);
+#pragma unroll
+            for (int r = 0; r < SUBS; ++r)
+                if (masked(here[r], t + (first_sub + r) * kKvTokens)) note_wild(values + (first_sub + r) * TILE);
+            accumulate(values + first_sub * TILE, w);
+        }
+        __builtin_amdgcn_s_setprio(0);
+    }
+    template <int SUBS>
+    __device__ __forceinline__ void pieces(int t, int end, int page)
+    {
+        if constexpr (kStream)
+            pieces_streamed<SUBS>(t, end, page);
+        else
+            pieces_together<SUBS>(t, end, page);
     }
 
     __device__ __forceinline__ void store(int64_t at, f32x4_t x, int d)
@@ -627,6 +732,12 @@ struct Attention {
     // Pieces first_step .. last_step - 1 of the tile's keys. `part`: where partial results go.
     __device__ __forceinline__ void run(const AttnSeg* segs, int first_step, int last_step, bool whole, int64_t part)
     {
+        if (!whole && first_step >= last_step) {
+            // a stretch that ends before the tile's first piece
+            for (int r = threadIdx.x; r < a.rows; r += THREADS) p.part_stat[part * p.tile_rows + r] = make_float2(-__builtin_inff(), 0.f);
+            if (threadIdx.x == 0) s.wild[turn ^ 1] = 0;
+            return;
+        }
         sets = a.rows <= kAttnRows ? 1 : (a.rows <= 2 * kAttnRows || NW == 2 ? 2 : NW);
         stop = a.end;
         table = seg.row * p.c.max_pages;
@@ -648,9 +759,9 @@ struct Attention {
             if (sets == 1)
                 pieces_apart(t, stop, page);
             else if (sets == NW)
-                pieces_together<SUB>(t, stop, page);
+                pieces<SUB>(t, stop, page);
             else if constexpr (NW > 2)
-                pieces_together<1>(t, stop, page);
+                pieces<1>(t, stop, page);
         }
         l = sum_halves(l);
         if (half == 0) {

@@ -62,7 +62,7 @@ constexpr int attn_waves(int dtype, int padded) { return dtype == DWS_FLOAT32 &&
 constexpr int kAttnGroups = 512;
 // The time of a piece of kKvTokens tokens a wave for tiles of up to 32, 64 and 128
 // queries, of a tile beside its pieces, and the least for a workgroup of its own.
-constexpr uint32_t kCostNarrow = 4, kCostMiddle = 5, kCostWide = 8, kCostTile = 4, kCostLeast = 8;
+constexpr uint32_t kCostNarrow = 4, kCostMiddle = 5, kCostWide = 8, kCostTile = 12, kCostLeast = 8;
 // Segments that a workgroup lays out for itself.
 constexpr int kAttnSegs = 256;
 
