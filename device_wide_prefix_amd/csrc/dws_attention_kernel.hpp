@@ -678,15 +678,15 @@ struct Attention {
             landed(keys + mine);
             if (lane == 0) s.there[turn][wave] = there;
             __syncthreads();            // and the other half has been read
+            // tiles of which a token is not there, in 32 bits
+            f32x16_t x[SUBS];
+            Weights w[SUBS];
+            scores(keys + first_sub * TILE, x);
             if (t + TOKENS < end) {
                 after = places(t + wave * 16 + TOKENS, page);
                 stream_piece(kv + (turn ^ 1) * PIECE + mine);
                 page = page_of(t + wave * 16 + 2 * TOKENS, 16);
             }
-            // tiles of which a token is not there, in 32 bits
-            f32x16_t x[SUBS];
-            Weights w[SUBS];
-            scores(keys + first_sub * TILE, x);
             uint32_t here[SUBS];
 #pragma unroll
             for (int r = 0; r < SUBS; ++r)

@@ -6,8 +6,9 @@ namespace dws {
 namespace {
 
 constexpr int kPlanThreads = 1024;
-constexpr int kJoinThreads = 512;
-constexpr int kJoinRows = 32;          // of a tile, for a workgroup
+constexpr int kJoinThreads = 256;      // (at least one a dimension)
+constexpr int kJoinRows = 64;          // of a tile, for a workgroup: 32 to 128 take as long
+static_assert(kJoinThreads >= 256, "row_again has a thread for each dimension");
 
 __global__ __launch_bounds__(kPlanThreads) void k_attention_plan(AttentionParams p)
 {
@@ -57,7 +58,7 @@ __device__ __forceinline__ void store_four(const AttentionParams& p, int64_t at,
         store_four_as<f16_t>(p, at, d, x);
 }
 
-// One row of queries by the whole workgroup, 512 tokens at a time, each token's score
+// One row of queries by the whole workgroup, 256 tokens at a time, each token's score
 // by a thread and each dimension's sum by a thread: only what the row sees is touched,
 // so that values which are not finite stay with those that see them.
 struct Again {
