@@ -93,12 +93,45 @@ struct Arrays {
         }
         return false;
     }
+    // Whether runs of two arrays with the same strides and counts meet, b beginning d
+    // bytes behind a: in the dimensions from the widest one on, `order`, each wider than
+    // all behind it, only the two places next to d can be as near as that.
+    static bool meet(__int128 d, const Strided& a, const Strided& b, const int* order, int n)
+    {
+        if (n == 3) return d < a.run && -d < b.run;
+        const __int128 s = a.stride[order[n]], c = a.count[order[n]];
+        if (c <= 1) return meet(d, a, b, order, n + 1);
+        __int128 k = d / s;
+        if (k * s > d) --k;
+        for (int i = 0; i < 2; ++i, ++k)
+            if (k > -c && k < c && meet(d - k * s, a, b, order, n + 1)) return true;
+        return false;
+    }
+    static bool interleaved(const One& a, const One& b)
+    {
+        Strided widest = a.shape;
+        widest.run = a.shape.run > b.shape.run ? a.shape.run : b.shape.run;
+        if (!widest.distinct()) return false;
+        for (int i = 0; i < 3; ++i)
+            if (a.shape.count[i] != b.shape.count[i] || (a.shape.count[i] > 1 && (a.shape.stride[i] != b.shape.stride[i] || a.shape.stride[i] <= 0)))
+                return false;
+        int order[3] = {0, 1, 2};
+        for (int i = 0; i < 2; ++i)
+            for (int j = 0; j < 2 - i; ++j)
+                if (a.shape.stride[order[j]] < a.shape.stride[order[j + 1]]) {
+                    const int t = order[j];
+                    order[j] = order[j + 1];
+                    order[j + 1] = t;
+                }
+        const __int128 d = (__int128)b.begin - (__int128)a.begin;
+        return !meet(d, a.shape, b.shape, order, 0);
+    }
     bool overlap() const
     {
         for (int i = 0; i < n; ++i)
             for (int j = 0; j < i; ++j)
                 if ((r[i].written || r[j].written) && r[i].begin < r[j].end && r[j].begin < r[i].end &&
-                    !beside(r[i], r[j]) && !beside(r[j], r[i]))
+                    !beside(r[i], r[j]) && !beside(r[j], r[i]) && !interleaved(r[i], r[j]))
                     return true;
         return false;
     }

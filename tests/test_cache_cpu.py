@@ -133,6 +133,26 @@ def test_parts_of_one_pool_do_not_overlap(lib):
         assert status(lib, append_args(**pools(0))) == OVERLAP, keys
 
 
+def test_pools_that_lie_in_one_another(lib):
+    """Equal strides of any size, none a multiple of another: refused exactly where an element is in both, told element by
+    element. (A call without tokens that is not refused ends well, and launches nothing.)"""
+    for page, token, head, dim in ((5000, 301, 150, 70), (1203, 600, 75, 37), (700, 40, 20, 10), (80, 20, 641, 9)):
+        pages, page_tokens, heads = 3, 2, 2
+
+        def elements(at):
+            return {at + i * page + j * token + k * head + d for i in range(pages) for j in range(page_tokens) for k in range(heads)
+                    for d in range(dim)}
+
+        keys = elements(0)
+        for shift in list(range(-2 * head, 2 * head)) + [page - 3, page + 1, token + dim, -page + dim, -token - dim]:
+            a = append_args(**{"seqs.tokens": 0, "heads_q": 0, "cache.n_pages": pages, "cache.page_tokens": page_tokens,
+                               "cache.heads": heads, "cache.dim_k": dim, "cache.dim_v": dim, "pairs": 0,
+                               "cache.keys": dws.PagePool(room(21), page, token, head),
+                               "cache.values": dws.PagePool(room(21) + 2 * shift, page, token, head)})
+            want = OVERLAP if keys & elements(shift) else dws.OK
+            assert status(lib, a) == want, (page, token, head, dim, shift)
+
+
 def test_refusals_of_attention(lib):
     assert lib.dws_pages_attention(None, None) == BAD
     need = ctypes.c_size_t(0)

@@ -262,6 +262,22 @@ def test_groups(gpu, share, members, tokens, new, dtype):
     check_attention(c, rows, counts, 2 * share, groups=[1, 1, members + 1, members + 1], shared=[5, tokens, 9])
 
 
+@pytest.mark.parametrize("dtype", [BF16, FP16, FP32])
+@pytest.mark.parametrize("dims", [(128, 128), (96, 96), (40, 128), (128, 24), (64, 64), (8, 56), (256, 72)])
+def test_tiles_of_many_queries(gpu, dims, dtype):
+    """36, 80 and 160 rows of queries a key head, pages that are not there, and NaN where the pool begins."""
+    note(f"attention many queries {dims} {dtype}")
+    c = Cache(21, [61, 40, 230], dtype, 2, *dims, 16, "heads", device="cuda")
+    c.table[c.table == 0] = -1
+    c.table[2, 5] = -1
+    c.table[2, 9] = c.keys.shape[0]
+    c.keys[0] = c.values[0] = math.nan
+    check_attention(c, [0, 1, 2], [20, 9, 40], 8)
+    # the tile's end is that of the cache, and of a page
+    c = Cache(22, [64, 128, 192], dtype, 1, *dims, 16, "tokens", device="cuda")
+    check_attention(c, [2, 0, 1], [33, 64, 17], 4)
+
+
 def test_groups_with_odd_places(gpu):
     """Fewer shared tokens than whole pages, more than the rows have, none; empty places first and last in a group."""
     note("attention groups, odd places")
@@ -450,6 +466,51 @@ def test_pool_beyond_32_bits(gpu):
     kk, vv = (x.transpose(0, 1).double() for x in (k, v))
     want = torch.cat([wide_reference(q[:, 2 * h: 2 * h + 2].transpose(0, 1), kk[h: h + 1], vv[h: h + 1], dim ** -0.5) for h in range(kv)])
     assert (out.double() - want.transpose(0, 1)).norm() / want.norm() <= torch.finfo(BF16).eps
+
+
+@pytest.mark.parametrize("new", [1, 30])
+def test_pages_far_apart(gpu, new):
+    """Three pages 33 GiB apart, keys and values beside each other in their rows."""
+    note(f"attention pages far apart {new}")
+    page, kv, dk, dv, n = 16, 2, 64, 96, 43
+    step = 33 * 2 ** 30 // 2
+    pool = torch.empty(2 * step + page * kv * (dk + dv), dtype=BF16, device="cuda")
+    pool = pool.as_strided((3, page, kv, dk + dv), (step, kv * (dk + dv), dk + dv, 1))
+    pool.fill_(math.nan)
+    keys, values = pool.split([dk, dv], dim=3)
+    table, lengths = ints([[2, 0, 1]]), ints([n])
+    gen = torch.Generator().manual_seed(17)
+    k, v = (torch.randn(n, kv, d, generator=gen).to(BF16).cuda() for d in (dk, dv))
+    q = torch.randn(new, 4 * kv, dk, generator=gen).to(BF16).cuda()
+    dws.pages_append(keys, values, table, lengths, k, v)
+    out = dws.pages_attention(q, keys, values, table, lengths, offsets=ints([0, new], torch.int64))
+    kk, vv = (x.transpose(0, 1) for x in (k, v))
+    want = torch.cat([wide_reference(q[:, 4 * h: 4 * h + 4].transpose(0, 1), kk[h: h + 1], vv[h: h + 1], dk ** -0.5) for h in range(kv)])
+    assert (out.double() - want.transpose(0, 1)).norm() / want.norm() <= torch.finfo(BF16).eps
+
+
+def test_tables_for_very_long_rows(gpu):
+    """Tables that could hold 2^31 tokens a row: what a row may cost is counted in larger units, and rounded."""
+    note("attention, tables for very long rows")
+    page, kv, dim = 1024, 2, 64
+    lens = [1, 70, 5000, 1024, 30011, 2, 900, 4096] * 3
+    gen = torch.Generator().manual_seed(18)
+    need = [-(-n // page) for n in lens]
+    keys, values = (torch.randn(sum(need), page, kv, dim, generator=gen).to(BF16).cuda() for _ in range(2))
+    table = torch.full((len(lens), 2 ** 21 - 1), -1, dtype=torch.int32)
+    order, at = torch.randperm(sum(need), generator=gen).int(), 0
+    for r, x in enumerate(need):
+        table[r, :x] = order[at: at + x]
+        at += x
+    new = [min(n, (1, 40, 3)[r % 3]) for r, n in enumerate(lens)]
+    offsets = torch.tensor([0] + new).cumsum(0)
+    q = torch.randn(int(offsets[-1]), 8, dim, generator=gen).to(BF16).cuda()
+    out = dws.pages_attention(q, keys, values, table.cuda(), ints(lens), offsets=offsets.cuda())
+    for r, n in enumerate(lens):
+        pages, b, e = table[r, : need[r]].long().cuda(), int(offsets[r]), int(offsets[r + 1])
+        k, v = (x[pages].reshape(-1, kv, dim)[:n].transpose(0, 1) for x in (keys, values))
+        want = torch.cat([wide_reference(q[b:e, 4 * h: 4 * h + 4].transpose(0, 1), k[h: h + 1], v[h: h + 1], dim ** -0.5) for h in range(kv)])
+        assert (out[b:e].double() - want.transpose(0, 1)).norm() / want.norm() <= torch.finfo(BF16).eps, (r, n)
 
 
 def test_same_bits_every_time(gpu):
