@@ -672,7 +672,6 @@ struct Attention {
                 __builtin_amdgcn_s_setprio(1);
             else
                 __builtin_amdgcn_s_setprio(0);
-            forget_addresses();
             there = after;
             const LdsBytes keys = kv + turn * PIECE, values = keys + SUB * TILE;
             landed(keys + mine);
