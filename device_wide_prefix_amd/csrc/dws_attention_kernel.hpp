@@ -13,8 +13,17 @@
 // keys): their waves work on 32 tokens each and are joined at the end. Larger ones are
 // bound by the matrix products and the softmax beside them: each wave brings 16 tokens,
 // and goes with its own 32 queries (of 128 in all) through the 64 of all waves, or (of 64)
-// through half of them. Keys go by way of the LDS, then values, the ones of the next
-// piece on their way in registers while the others are multiplied.
+// through half of them. The next piece's keys and values are on their way meanwhile: to the
+// other half of the LDS by themselves, or in registers where two pieces do not fit there or
+// rows are not whole units of 16 bytes.
+//
+// Measured, with the joining, a call: 96 sequences of 1 to 16,000 tokens, 8 heads of 128, 4
+// queries each, bf16: 157 us, 4.7 TB/s of keys and values. 3 prompts of 900 to 2,000 tokens
+// behind 4,097: 567 us, 790 TFLOP/s, where a large matrix product reaches 1,335. There each
+// SIMD's vector instructions take 53% of the time (scores to weights: 4 of 32 bits for each,
+// 4 times that for the exponential) and its matrix products 36%: two waves hide what one
+// waits for, and hardly overlap the two. Tiles of 256 queries would halve the reads of the
+// LDS (26% of the time), but leave one wave a SIMD.
 //
 // Fragments (32 x 32 tiles, h = lane / 32):
 //   operand  lane holds row (or column) lane % 32, contraction indices 8 h .. 8 h + 7 of
@@ -79,10 +88,9 @@ struct Attention {
     static constexpr int STEP = 64 / NCH;               // rows that 64 lanes hold at a time
     static constexpr int BLOCKS = D / 32;
     static constexpr int THREADS = 64 * NW;
-    // Whether a piece waits in registers: not where 4 N of them do not fit, nor where rows
-    // are read element by element.
-    static constexpr bool kAhead = WHOLE && N <= 16;
-    static constexpr int kBatch = WHOLE ? 8 : 1;
+    // Whether a piece waits in registers: not where 4 N of them do not fit.
+    static constexpr bool kAhead = N <= 16 && (WHOLE || ROW <= 256);
+    static constexpr int kBatch = N > 16 ? 16 : 8;      // loads at a time where it does not
     // Whether a small tile's keys and values both do.
     static constexpr bool kBoth = kAhead && D * sizeof(T) <= 256;
     static constexpr int SUB = NW / 2;                  // tiles of 32 tokens that all waves go through at a time
@@ -239,6 +247,14 @@ struct Attention {
     {
         return s.at[wave][VALUES][i * STEP + lane / NCH];
     }
+    // 128 bits moved down by 0 to 127.
+    static __device__ __forceinline__ u32x4_t shifted(u32x4_t x, int by)
+    {
+        const uint64_t lo = (uint64_t)x[1] << 32 | x[0], hi = (uint64_t)x[3] << 32 | x[2];
+        const uint64_t up = hi >> (by & 63);
+        const uint64_t a = by < 64 ? lo >> (by & 63) | hi << 1 << (63 - (by & 63)) : up, b = by < 64 ? up : 0;
+        return u32x4_t{(uint32_t)a, (uint32_t)(a >> 32), (uint32_t)b, (uint32_t)(b >> 32)};
+    }
     template <bool VALUES>
     __device__ __forceinline__ u32x4_t load(Place at) const
     {
@@ -250,6 +266,13 @@ struct Attention {
         } else if constexpr (WHOLE) {
             return *reinterpret_cast<const u32x4_t*>(from + at + (d < dim ? d : 0));
         } else {
+            // rows at any address, 16 bytes at a time too; the last ones end with the row (`only_there`
+            // moves them to the front)
+            if (dim >= CH) {
+                u32x4_t x;
+                __builtin_memcpy(&x, from + at + (d + CH <= dim ? d : dim - CH), 16);
+                return x;
+            }
             Chunk<T> x;
 #pragma unroll
             for (int j = 0; j < CH; ++j) x[j] = from[at + (d + j < dim ? d + j : 0)];
@@ -262,7 +285,8 @@ struct Attention {
         const int d = (lane % NCH) * CH;
         const bool row = (there >> (i * STEP + lane / NCH)) & 1;
         if constexpr (WHOLE) return row && d < dim ? x : u32x4_t{};
-        Chunk<T> y = __builtin_bit_cast(Chunk<T>, x);
+        const int behind = d + CH - dim;        // elements of the chunk
+        Chunk<T> y = __builtin_bit_cast(Chunk<T>, dim >= CH && behind > 0 && behind < CH ? shifted(x, 8 * (int)sizeof(T) * behind) : x);
 #pragma unroll
         for (int j = 0; j < CH; ++j) y[j] = row && d + j < dim ? y[j] : (T)0.f;
         return __builtin_bit_cast(u32x4_t, y);
@@ -571,7 +595,7 @@ struct Attention {
         page = page_of(t + wave * 16 + TOKENS, 16);
         for (; t < end; t += TOKENS) {
             // Of the two workgroups on a compute unit the older one goes first, and would be done
-            // long before the other: they take turns (attend_prompts: 670 to 629 us).
+            // long before the other: they take turns.
             if (((t / TOKENS) ^ (blockIdx.x / 256)) & 1)
                 __builtin_amdgcn_s_setprio(1);
             else
@@ -667,7 +691,7 @@ struct Attention {
         page = page_of(t + wave * 16 + TOKENS, 16);
         for (int turn = 0; t < end; t += TOKENS, turn ^= 1) {
             // Of the two workgroups on a compute unit the older one goes first, and would be done
-            // long before the other: they take turns.
+            // long before the other: they take turns (2% of the prompts above).
             if ((turn ^ (blockIdx.x / 256)) & 1)
                 __builtin_amdgcn_s_setprio(1);
             else

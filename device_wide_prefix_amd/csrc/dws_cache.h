@@ -58,8 +58,13 @@ constexpr int attn_padded_dim(int dim_k, int dim_v)
 // workgroups of them up to 128 dimensions of 16 bits.
 constexpr int attn_waves(int dtype, int padded) { return dtype == DWS_FLOAT32 && padded == 256 ? 2 : 4; }
 
-// Workgroups that the work is shared out to at most, two a compute unit.
-constexpr int kAttnGroups = 512;
+// Workgroups that the work is shared out to at most, as many as are there at a time: two
+// a compute unit, one where its four waves have all registers (23 sequences of 64 heads of
+// 256 dimensions: 73 us, with 512 of them 96).
+constexpr int attn_groups(int dtype, int padded)
+{
+    return padded * (dtype == DWS_FLOAT32 ? 4 : 2) > 256 && attn_waves(dtype, padded) == 4 ? 256 : 512;
+}
 // The time of a piece of kKvTokens tokens a wave for tiles of up to 32, 64 and 128
 // queries, of a tile beside its pieces, and the least for a workgroup of its own.
 constexpr uint32_t kCostNarrow = 4, kCostMiddle = 5, kCostWide = 8, kCostTile = 12, kCostLeast = 8;

@@ -179,7 +179,8 @@ dws_status plan_of(const dws_pages_attention_args* a, Plan* z)
     const __int128 most = (__int128)c.max_pages * c.page_tokens, step = kKvTokens * z->waves;
     const int64_t tile_cost = kCostTile + (int64_t)kCostWide * (int64_t)((most < kMaxCount ? most : kMaxCount) / step + 1);
     const __int128 cost = tiles * c.heads * tile_cost;
-    z->workgroups = cost < (__int128)kAttnGroups * kCostLeast ? (int)(cost / kCostLeast) + 1 : kAttnGroups;
+    const int groups_at_once = attn_groups(c.dtype, z->padded);
+    z->workgroups = cost < (__int128)groups_at_once * kCostLeast ? (int)(cost / kCostLeast) + 1 : groups_at_once;
     z->cost_shift = 0;
     while (tiles * c.heads * (1 + (tile_cost >> z->cost_shift)) > kMaxCount) ++z->cost_shift;
     size_t at = 0;

@@ -853,7 +853,7 @@ dws_status dws_pages_attention_workspace(const dws_pages_attention_args* args, s
  * (dws_pages_append first) included: out = sum p_t v_t with p the softmax of scale q . k_t over them. For one token a
  * sequence, a few, or whole prompts behind what is there. A query that sees nothing (a row outside the table, a sequence
  * with more tokens than its row, a row longer than max_pages pages or 2^31 - 4097
- * tokens, pages outside the pool) gives 0, and -infinity in d_lse. Scores, their statistics and
+ * tokens, pages outside the pool) gives 0, and -infinity in d_lse; so does one all of whose scores are -infinity. Scores, their statistics and
  * all sums are fp32; with 16-bit inputs the probabilities are rounded to dtype for their product with the values. What is
  * behind a row's end is not read, whatever the pages hold there. Values that are not finite reach the queries that see
  * them, and no others. d_shared must say the truth: the shared tokens are read from the pages of the group's first
@@ -891,9 +891,10 @@ dws_status dws_beam_select_workspace(const dws_beam_args* args, size_t* bytes);
 /*
  * For each request the k pairs (beam, token) with the largest d_scores[beam] + log softmax(logits[beam])[token], in
  * descending order, the lowest beam and then the lowest token first among equal ones. A beam's tokens are ordered by their
- * logits, beams against each other in fp64, so neighbours at the border are told apart. A finished beam has one
- * continuation, end_token at its own score, and -infinity for every other token. A beam whose score is not finite, or
- * whose logits hold a NaN, +infinity or nothing above -infinity, has -infinity for all of them.
+ * logits, so neighbours at the border are told apart; beams against each other in fp64, where scores that differ by less
+ * than 2^-40 of themselves are equal. A finished beam has one continuation, end_token at its own score, and -infinity for
+ * every other token. A beam whose score is not finite, or whose logits hold a NaN, +infinity or nothing above -infinity,
+ * has -infinity for all of them.
  *
  * With d_rows (the cache rows, or state slots, of the beams) continuation c gets row d_out_rows[c]: the first one of a
  * beam keeps its row, further ones take the rows of beams without any, in order, and are to be copied there: from
