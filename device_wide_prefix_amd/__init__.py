@@ -19,6 +19,9 @@ fallback; if the library is not built, importing the binding's functions raises.
     pages_free(refs, table, lengths, rows, page_tokens) -> freed
     pages_compact(refs, table)             -> (count, remap, src, dst, moves)
     pages_copy(pool, src, dst, count=None, page_dim=0) -> pool
+    pages_append(keys, values, table, lengths, k, v, ..., q=None) -> q turned, or None (pools updated)
+    pages_attention(q, keys, values, table, lengths, ...) -> out or (out, lse)
+    beam_select(logits, scores, k=None, ..., rows=None) -> (scores, parents, tokens[, rows, src, dst])
     delta_rule(q, k, v, g, beta, ...)      -> out or (out, final_state)
     delta_rule_backward(d_out, q, ...)     -> (dq, dk, dv, dg, dbeta, d_initial_state)
     delta_rule_step(q, k, v, g, beta, state, slots=None, ...) -> out (state updated)
