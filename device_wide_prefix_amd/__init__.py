@@ -752,10 +752,8 @@ def _delta_args(q, k, v, g, beta, offsets, n_seqs, scale):
 def _records_no_graph(name, *tensors):
     """Refuses tensors whose gradients the result would silently lack."""
     import torch
-    if not torch.is_grad_enabled():
-        return
     for t in tensors:
-        if getattr(t, "requires_grad", False):
+        if getattr(t, "requires_grad", False) and torch.is_grad_enabled():
             raise RuntimeError(f"{name} records no graph: call it with detached tensors or under torch.no_grad(), as the "
                                "forward and backward of a torch.autograd.Function are; delta_rule_backward gives "
                                "delta_rule's gradients")
@@ -1053,12 +1051,14 @@ def _workspace_bytes(query, key, make):
 
 def _kv_args(keys, values, table, lengths, tokens, rows, offsets):
     """The values of dws_kv_cache and dws_page_seqs; checks shapes, types and devices. Returns (values, device, n)."""
+    import torch
     _gpu_tensor(keys, "keys")
-    if keys.dim() != 4:
-        raise ValueError("keys and values must be (pages, page_tokens, heads, dim)")
-    device, dtype = keys.device, keys.dtype
+    try:
+        pages, page_tokens, heads, dim_k = keys.shape
+    except ValueError:
+        raise ValueError("keys and values must be (pages, page_tokens, heads, dim)") from None
+    device, dtype, int32 = keys.device, keys.dtype, torch.int32
     code = _float_codes.get(dtype) or _float_code(dtype, "keys")
-    pages, page_tokens, heads, dim_k = keys.shape
     k, v, dim_v = keys.stride(), (), -1
     try:
         if values.dtype == dtype and values.device == device:
@@ -1069,7 +1069,6 @@ def _kv_args(keys, values, table, lengths, tokens, rows, offsets):
     if k[3] != 1 and dim_k > 1 or not v or v[3] != 1 and dim_v > 1:
         raise ValueError(f"keys and values must have shape {(pages, page_tokens, heads)} + (dim,), dtype {dtype} and a "
                          f"contiguous last dimension, and be on {device}")
-    int32 = _int32()
     try:
         n_rows, max_pages = table.shape if table.dtype == int32 and table.device == device and table.is_contiguous() else ()
     except (AttributeError, ValueError):
@@ -1078,7 +1077,7 @@ def _kv_args(keys, values, table, lengths, tokens, rows, offsets):
     at = of = 0
     n = n_rows
     if offsets is not None:
-        of = _device_ints(offsets, "offsets", _int64(), None, device)
+        of = _device_ints(offsets, "offsets", torch.int64, None, device)
         n = offsets.shape[0] - 1
         if n < 0:
             raise ValueError("offsets holds one more than there are sequences")
@@ -1110,10 +1109,12 @@ def pages_append(keys, values, table, lengths, k, v, rows=None, offsets=None, gr
     tensor, 0 where the token is left out). Returns q_out, or None without q."""
     import torch
     _records_no_graph("pages_append", keys, values, k, v, q, q_out)
-    _gpu_tensor(k, "k")
-    shape = k.shape
-    tokens = shape[0] if len(shape) == 3 else -1
-    a, device, n = _kv_args(keys, values, table, lengths, max(tokens, 0), rows, offsets)
+    try:
+        tokens, _, _ = k.shape
+    except (AttributeError, ValueError):
+        _gpu_tensor(k, "k")
+        raise ValueError(f"k must be (tokens, heads, dim), got {tuple(k.shape)}") from None
+    a, device, n = _kv_args(keys, values, table, lengths, tokens, rows, offsets)
     dtype, heads, dim_k, dim_v = keys.dtype, a[14], a[15], a[16]
     kr, vr = _rows(k, "k", (tokens, heads, dim_k), dtype, device), _rows(v, "v", (tokens, heads, dim_v), dtype, device)
     ok = 0 if granted is None else _device_ints(granted, "granted", torch.int32, n, device)
@@ -1128,11 +1129,11 @@ def pages_append(keys, values, table, lengths, k, v, rows=None, offsets=None, gr
     with _on_stream(keys, stream) as s:
         heads_q, zero, qr, to = 0, 0, (0, 0, 0), (0, 0, 0)
         if q is not None:
-            _gpu_tensor(q, "q")
-            if q.dim() != 3:
-                raise ValueError("q must be (tokens, heads_q, dim_k)")
-            shape = q.shape
-            heads_q = shape[1]
+            try:
+                shape = _, heads_q, _ = q.shape
+            except (AttributeError, ValueError):
+                _gpu_tensor(q, "q")
+                raise ValueError("q must be (tokens, heads_q, dim_k)") from None
             qr = _rows(q, "q", (tokens, heads_q, dim_k), dtype, device)
             if q_out is None:
                 q_out, zero = torch.empty(shape, dtype=dtype, device=device), 1
@@ -1158,10 +1159,11 @@ def pages_attention(q, keys, values, table, lengths, rows=None, offsets=None, gr
     Returns out, or (out, lse)."""
     import torch
     _records_no_graph("pages_attention", q, keys, values, out, lse if lse is not True else None)
-    _gpu_tensor(q, "q")
-    if q.dim() != 3:
-        raise ValueError("q must be (tokens, heads_q, dim_k)")
-    tokens, heads_q, _ = q.shape
+    try:
+        tokens, heads_q, _ = q.shape
+    except (AttributeError, ValueError):
+        _gpu_tensor(q, "q")
+        raise ValueError("q must be (tokens, heads_q, dim_k)") from None
     a, device, n = _kv_args(keys, values, table, lengths, tokens, rows, offsets)
     dtype, heads, dim_k, dim_v = keys.dtype, a[14], a[15], a[16]
     if heads_q < 1 or heads_q % heads:

@@ -269,9 +269,9 @@ struct Attention {
             // rows at any address, 16 bytes at a time too; the last ones end with the row (`only_there`
             // moves them to the front)
             if (dim >= CH) {
-                u32x4_t x;
-                __builtin_memcpy(&x, from + at + (d + CH <= dim ? d : dim - CH), 16);
-                return x;
+                // (as memory that is global: loads that might be of the LDS too may not be at any address)
+                typedef u32x4_t Loose __attribute__((aligned(2)));
+                return *(const __attribute__((address_space(1))) Loose*)(from + at + (d + CH <= dim ? d : dim - CH));
             }
             Chunk<T> x;
 #pragma unroll

@@ -170,8 +170,10 @@ __device__ __forceinline__ AttnSeg sequence(const AttentionParams& p, int64_t i)
 
 // Lays out the segments, n_groups + n and one that ends them, with all threads of a
 // workgroup; `segs` in LDS or global memory. Ends with a barrier.
+// (Inlined always: called, it would have the parameters in scratch memory, and every
+// access by their pointers would be one that might be of the LDS.)
 template <int THREADS>
-__device__ void lay_out(const AttentionParams& p, AttnSeg* segs, AttnSums* scratch)
+__device__ __forceinline__ void lay_out(const AttentionParams& p, AttnSeg* segs, AttnSums* scratch)
 {
     const AttnWork work(p);
     const int tid = threadIdx.x;

@@ -19,6 +19,7 @@ namespace {
 typedef __bf16 bf16_t;
 typedef _Float16 f16_t;
 typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
+typedef u32x4_t Loose __attribute__((aligned(2)));      // at any address that elements have
 
 constexpr int kEach = kBeamBlock / 64;      // logits of a lane's chunk
 constexpr double kLog2eD = 1.4426950408889634074;
@@ -122,7 +123,7 @@ struct Stretch {
     __device__ __forceinline__ void load(const T* from)
     {
 #pragma unroll
-        for (int i = 0; i < LOADS; ++i) __builtin_memcpy(&raw[i], from + i * VEC, 16);
+        for (int i = 0; i < LOADS; ++i) raw[i] = *(const __attribute__((address_space(1))) Loose*)(from + i * VEC);
     }
     // The first `count` of them; -infinity for the others.
     __device__ __forceinline__ void load(const T* from, int count)
