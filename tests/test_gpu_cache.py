@@ -264,7 +264,7 @@ def test_groups(gpu, share, members, tokens, new, dtype):
 
 @pytest.mark.parametrize("dtype", [BF16, FP16, FP32])
 @pytest.mark.parametrize("dims", [(128, 128), (96, 96), (40, 128), (128, 24), (64, 64), (8, 56), (256, 72), (33, 65), (117, 117), (5, 3),
-                                  (142, 64), (170, 170)])
+                                  (142, 64), (170, 170), (256, 256), (136, 248)])
 def test_tiles_of_many_queries(gpu, dims, dtype):
     """36, 80 and 160 rows of queries a key head, pages that are not there, and NaN where the pool begins."""
     note(f"attention many queries {dims} {dtype}")
