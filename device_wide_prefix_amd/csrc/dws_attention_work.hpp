@@ -178,10 +178,10 @@ __device__ __forceinline__ void lay_out(const AttentionParams& p, AttnSeg* segs,
     const AttnWork work(p);
     const int tid = threadIdx.x;
     const int64_t n = p.c.n, groups = p.n_groups, all = groups + n;
-    // what the first segment of a sequence needs is on its way while the groups are looked at
+    // the sequences are looked up by the first waves, while the last ones look at the groups
     AttnSeg mine{};
     if (tid >= groups && tid < all) mine = sequence(p, tid - groups);
-    for (int64_t g = tid; g < groups; g += THREADS) {
+    for (int64_t g = THREADS - 1 - tid; g < groups; g += THREADS) {
         const int64_t s0 = clamped(p.groups[g], n), s1 = clamped(p.groups[g + 1], n);
         AttnSeg s{};
         s.row = s.apart = -1;
