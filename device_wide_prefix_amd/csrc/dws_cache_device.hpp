@@ -27,7 +27,8 @@ __device__ __forceinline__ int64_t seq_begin(const KvView& c, int64_t i)
 
 // The sequence that holds token t, -1 if none does, and its first token and
 // length. Every lane of the wave calls it with the same t; 64 candidates a round,
-// since a round is one trip to memory.
+// since a round is one trip to memory. (A sequence that begins before row 0 holds
+// none: with 0 <= first <= t < end no difference of the three leaves 64 bits.)
 __device__ __forceinline__ int64_t seq_of(const KvView& c, int64_t t, int64_t* first, int64_t* count, int lane)
 {
     if (c.n == 0) return -1;
@@ -46,9 +47,10 @@ __device__ __forceinline__ int64_t seq_of(const KvView& c, int64_t t, int64_t* f
         i = lo;
     }
     const int64_t b = seq_begin(c, i), e = seq_begin(c, i + 1);
+    if (b < 0 || b > t || e <= t) return -1;
     *first = b;
     *count = e - b;
-    return b <= t && t < e ? i : -1;
+    return i;
 }
 
 }  // namespace dws

@@ -811,8 +811,8 @@ typedef struct dws_pages_append_args {
  * fp32, rounded once; x is reduced in fp64, so far positions lose nothing.
  * Left out are sequences with a row outside the table, 0 in d_granted or a row that
  * an earlier sequence of the call names (searched for, work that grows with the
- * square of n), sequences with more tokens than their row or a row longer than
- * max_pages pages. A token whose page is outside the pool is not written; its query
+ * square of n), sequences that begin before row 0 of the call or have more tokens than
+ * their row, or a row longer than max_pages pages. A token whose page is outside the pool is not written; its query
  * is. Two rows with one page in common must not both write to it. Errors, checked
  * before any HIP call: a NULL structure or required pointer, sizes, strides or types
  * out of range, an output that names an element twice, heads_q above 0 without q and

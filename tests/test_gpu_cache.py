@@ -177,6 +177,28 @@ def test_append_many_sequences(gpu):
     assert torch.equal(keys.cpu(), want) and torch.equal(values.cpu(), -want)
 
 
+@pytest.mark.parametrize("begin,end", [(-(2**62), 2**62), (-(2**63), 5), (-(2**63), 40), (-(2**63), 2**63 - 1), (-1, 2**63 - 1), (-3, 40)])
+def test_append_offsets_before_the_first_row(gpu, begin, end):
+    """A sequence that says it begins before the call's first token is left out, however far: its length is no 64-bit number, and
+    places reckoned with it would lie before the row, or in other rows and pages."""
+    note(f"append, offsets {begin} {end}")
+    c = Cache(23, [40, 0, 7, 64], BF16, 2, 64, 64, 16, device="cuda")
+    gen = torch.Generator().manual_seed(6)
+    k, v = (torch.randn(44, 2, 64, generator=gen).to(BF16).cuda() for _ in range(2))
+    q = torch.randn(44, 4, 64, generator=gen).to(BF16).cuda()
+    bits = [x.clone().view(torch.int16) for x in (c.keys, c.values)]
+    for row in range(4):
+        got = dws.pages_append(*c.args(), k, v, rows=ints([row]), offsets=ints([begin, end], torch.int64), q=q, freqs=freqs_of(32))
+        assert (got == 0).all()
+        assert torch.equal(c.keys.view(torch.int16), bits[0]) and torch.equal(c.values.view(torch.int16), bits[1])
+    # the sequences beside it are written
+    before = c.keys.clone(), c.values.clone()
+    offsets = [begin, 2, 5]
+    got = dws.pages_append(*c.args(), k, v, rows=ints([0, 2]), offsets=ints(offsets, torch.int64), q=q, freqs=freqs_of(32))
+    check_append(c, [0, 2], [0, 2, 5], k, v, q, freqs_of(32), False, before, got, skip=(0,))
+    assert (got[5:] == 0).all()
+
+
 # ---- attention ----------------------------------------------------------------
 
 def run_attention(c, rows, new, heads, scale=None, groups=None, shared=None, seed=0, q=None, lse=True, **more):
