@@ -43,6 +43,9 @@ struct AppendParams {
     int whole;                  // every run is made of whole, aligned 16-byte units
     HeadRows k, v, q, q_out;
 };
+// Tokens of a call at most: workgroups of four waves, a token each, and fewer than 2^32
+// threads in a launch.
+constexpr int64_t kMaxAppendTokens = (((int64_t)1 << 32) - 1) / 256 * 4;
 hipError_t launch_pages_append(const AppendParams& p, int dtype, hipStream_t stream);
 
 // ---- attention ---------------------------------------------------------------

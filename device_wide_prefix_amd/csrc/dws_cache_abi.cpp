@@ -110,6 +110,7 @@ dws_status append_entry(const dws_pages_append_args* a, hipStream_t stream)
     const dws_kv_cache& c = a->cache;
     dws_status st = check_sizes(c, a->seqs, a->heads_q);
     if (st != DWS_OK) return st;
+    if (a->seqs.tokens > kMaxAppendTokens) return DWS_ERR_UNSUPPORTED;
     if (a->pairs < 0 || a->pairs > c.dim_k / 2) return DWS_ERR_INVALID_ARG;
     AppendParams p{};
     Arrays arrays;

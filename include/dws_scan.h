@@ -812,9 +812,10 @@ typedef struct dws_pages_append_args {
  * Left out are sequences with a row outside the table, 0 in d_granted or a row that
  * an earlier sequence of the call names (searched for, work that grows with the
  * square of n), sequences that begin before row 0 of the call or have more tokens than
- * their row, or a row longer than max_pages pages. A token whose page is outside the pool is not written; its query
- * is. Two rows with one page in common must not both write to it. Errors, checked
- * before any HIP call: a NULL structure or required pointer, sizes, strides or types
+ * their row, or a row longer than max_pages pages. A token whose page is outside the
+ * pool is not written; its query is. Two rows with one page in common must not both
+ * write to it. At most 67,108,860 tokens a call, a launch's. Errors, checked before any
+ * HIP call: a NULL structure or required pointer, sizes, strides or types
  * out of range, an output that names an element twice, heads_q above 0 without q and
  * q_out, pairs beyond dim_k / 2, tokens not a multiple of n without d_offsets give
  * DWS_ERR_INVALID_ARG; sizes beyond the limits DWS_ERR_UNSUPPORTED; a pointer not

@@ -119,6 +119,16 @@ def test_refusals_of_append(lib):
     assert status(lib, append_args(**{"seqs.tokens": 0, "k.data": None, "v.data": None, "q.data": None, "q_out.data": None})) == dws.OK
 
 
+def test_append_refuses_more_tokens_than_a_launch_has(lib):
+    """A wave of 64 threads a token, four to a workgroup, and at most 2^32 - 1 threads: refused before any HIP call."""
+    far = {"cache.n_rows": 1, "cache.max_pages": 1 << 24, "cache.n_pages": 1 << 24, "cache.page_tokens": 128, "heads_q": 0, "pairs": 0,
+           "cache.heads": 1, "cache.dim_k": 1, "cache.dim_v": 1, "cache.keys": dws.PagePool(1 << 40, 128, 1, 1),
+           "cache.values": dws.PagePool(1 << 41, 128, 1, 1), "k": dws.Rows(1 << 42, 1, 1), "v": dws.Rows(1 << 43, 1, 1),
+           "d_granted": None, "d_positions": None}
+    for tokens in (4 * ((2**32 - 1) // 256) + 1, 1 << 26, 1 << 28, (1 << 31) - 1):
+        assert status(lib, append_args(**{**far, "seqs.tokens": tokens})) == UNSUPPORTED, tokens
+
+
 def test_parts_of_one_pool_do_not_overlap(lib):
     """Keys beside values in every page, in every token's row, and with heads outside."""
     empty = {"seqs.tokens": 0, "cache.dim_v": 64}

@@ -177,6 +177,19 @@ def test_append_many_sequences(gpu):
     assert torch.equal(keys.cpu(), want) and torch.equal(values.cpu(), -want)
 
 
+def test_append_as_many_tokens_as_a_launch_has(gpu):
+    note("append, the most tokens")
+    tokens, page = 4 * ((2**32 - 1) // 256), 64
+    pages = -(-tokens // page)
+    k = torch.arange(tokens, dtype=torch.int32, device="cuda").to(torch.int16).view(FP16).view(tokens, 1, 1)
+    v = k.view(torch.int16).bitwise_not().view(FP16)
+    keys, values = (torch.zeros(pages, page, 1, 1, dtype=FP16, device="cuda") for _ in range(2))
+    table = torch.arange(pages - 1, -1, -1, dtype=torch.int32, device="cuda")[None].contiguous()
+    dws.pages_append(keys, values, table, ints([tokens]), k, v)
+    for pool, x in ((keys, k), (values, v)):
+        assert torch.equal(pool.view(torch.int16).flip(0).reshape(-1)[:tokens], x.view(torch.int16).reshape(-1))
+
+
 @pytest.mark.parametrize("begin,end", [(-(2**62), 2**62), (-(2**63), 5), (-(2**63), 40), (-(2**63), 2**63 - 1), (-1, 2**63 - 1), (-3, 40)])
 def test_append_offsets_before_the_first_row(gpu, begin, end):
     """A sequence that says it begins before the call's first token is left out, however far: its length is no 64-bit number, and
