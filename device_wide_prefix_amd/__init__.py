@@ -1210,7 +1210,8 @@ def beam_select(logits, scores, k=None, finished=None, end_token=0, rows=None, s
     (dws_beam_select).
 
     logits: (batch, beams, vocab), float32, float16 or bfloat16, any strides with a contiguous last dimension; scores:
-    float32 (batch, beams). finished: bool or uint8 (batch, beams), beams that go on with end_token alone, at their score.
+    float32 (batch, beams). finished: bool or uint8 (batch, beams), beams that go on with end_token alone, at their score,
+    whatever their logits hold.
     Returns (scores (batch, k) float32, parents (batch, k) int32, tokens (batch, k) int32).
     With rows (int32 (batch, beams): cache rows or state slots of the beams; needs k == beams) also (rows, src, dst): the
     continuations' rows, and which to copy where (batch * beams each, -1: none). States follow with

@@ -361,7 +361,8 @@ __global__ __launch_bounds__(64 * kJoinWaves) void k_beam_join(BeamParams p)
 #pragma unroll
         for (int d = 32; d > 0; d >>= 1) sum += __shfl_xor(sum, d, 64);
         const double norm = (double)top + log2(sum) / kLog2eD;
-        const bool alive = __builtin_fabs(norm) < __builtin_inf() && __builtin_fabsf(score) < __builtin_inff();
+        // (a finished beam goes on by its score, whatever its logits are)
+        const bool alive = __builtin_fabsf(score) < __builtin_inff() && (!open || __builtin_fabs(norm) < __builtin_inf());
         uint64_t x = 0;
         int64_t t = lane;
         if (alive && open) {

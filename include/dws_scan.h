@@ -895,8 +895,8 @@ dws_status dws_beam_select_workspace(const dws_beam_args* args, size_t* bytes);
  * descending order, the lowest beam and then the lowest token first among equal ones. A beam's tokens are ordered by their
  * logits, so neighbours at the border are told apart; beams against each other in fp64, where scores that differ by less
  * than 2^-40 of themselves are equal. A finished beam has one continuation, end_token at its own score, and -infinity for
- * every other token. A beam whose score is not finite, or whose logits hold a NaN, +infinity or nothing above -infinity,
- * has -infinity for all of them.
+ * every other token, whatever its logits hold. Any other beam whose logits hold a NaN, +infinity or nothing above
+ * -infinity has -infinity for all tokens, and so has a beam, finished or not, whose score is not finite.
  *
  * With d_rows (the cache rows, or state slots, of the beams) continuation c gets row d_out_rows[c]: the first one of a
  * beam keeps its row, further ones take the rows of beams without any, in order, and are to be copied there: from

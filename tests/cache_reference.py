@@ -135,11 +135,12 @@ def select(logits, scores, k, finished=None, end_token=0):
         for w in range(logits.shape[1]):
             x, s = logits[b, w].double(), float(scores[b, w])
             norm = float(torch.logsumexp(x, 0))
+            if finished is not None and finished[b, w]:
+                # (its logits are not looked at)
+                x, norm = torch.full((vocab,), -math.inf, dtype=torch.float64), 0.0
+                x[end_token] = 0.0
             alive = math.isfinite(s) and math.isfinite(norm)
-            if alive and finished is not None and finished[b, w]:
-                x = torch.full((vocab,), -math.inf, dtype=torch.float64)
-                x[end_token] = norm
-            elif not alive:
+            if not alive:
                 x = torch.full((vocab,), -math.inf, dtype=torch.float64)
             order = torch.sort(x, descending=True, stable=True).indices[:k].tolist()
             best += [(-(s + (float(x[t]) - norm)) if alive else math.inf, w, place, t) for place, t in enumerate(order)]

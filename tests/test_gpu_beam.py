@@ -101,6 +101,37 @@ def test_masked_logits(gpu, dtype):
     check(logits, scores, 4, rows=torch.arange(36, dtype=torch.int32).view(9, 4))
 
 
+@pytest.mark.parametrize("dtype", [BF16, FP16, FP32])
+@pytest.mark.parametrize("bad", [math.nan, -math.inf, math.inf])
+def test_finished_beams_whatever_their_logits_hold(gpu, bad, dtype):
+    """A finished beam goes on with the end token at its own score, its logits computed or not: one value of them that is not
+    finite, or all; first, in the middle and last among the beams."""
+    note(f"beam finished, logits {bad} {dtype}")
+    for vocab in (5, 700, 9001):
+        logits, scores, gen = made(9, 6, 4, vocab, dtype)
+        over = torch.zeros(6, 4, dtype=torch.bool)
+        for b in range(3):
+            for at, w in ((slice(vocab // 3, vocab // 3 + 1), b), (slice(None), 3 - b)):
+                logits[b, w, at] = bad
+                over[b, w] = True
+        logits[3:5] = bad                           # all of a request's beams have ended
+        over[3:5] = True
+        scores[5, 2], over[5, 2] = -math.inf, True  # one that has no score
+        end = vocab - 2
+        for k in (2, 4, 5):
+            value, parents, tokens = (x.cpu() for x in dws.beam_select(logits.cuda(), scores.cuda(), k=k, finished=over.cuda(), end_token=end))
+            for b in range(6):
+                best = sorted((-float(scores[b, w]), w) for w in range(4) if over[b, w] and scores[b, w].isfinite())
+                got = [(-s, w) for s, w, t in zip(value[b].tolist(), parents[b].tolist(), tokens[b].tolist()) if over[b, w] and s > -math.inf]
+                assert all(tokens[b, i] == end for i in range(k) if over[b, parents[b, i]] and value[b, i] > -math.inf)
+                assert got == best[: len(got)]
+                if over[b].all():
+                    assert len(got) == min(k, 4) and (value[b, 4:] == -math.inf).all()
+                # what is left out is below what was chosen
+                assert all(-x <= float(value[b, -1]) for x, _ in best[len(got):])
+        check(logits, scores, 4, over, end, rows=torch.randperm(24, generator=gen).int().view(6, 4))
+
+
 def test_far_apart(gpu):
     """Logits and scores of any size; the largest far above the others."""
     note("beam far apart")
