@@ -433,6 +433,19 @@ struct Attention {
         if (__ballot(bad)) s.wild[turn] = 1;
     }
 
+    // Results of 16-bit weights that are not finite where their sum is: an infinity among the values that the
+    // queries see becomes NaN where a part of its weight is 0 or below it. Such a tile's rows are computed
+    // again, too.
+    __device__ __forceinline__ void note_wild_results()
+    {
+        float most = 0.f;
+#pragma unroll
+        for (int b = 0; b < BLOCKS; ++b)
+#pragma unroll
+            for (int e = 0; e < 16; ++e) most = __builtin_fmaf(0.f, o[b][e], most);       // 0, or NaN
+        if (__ballot(most != 0.f && __builtin_fabsf(l) < __builtin_inff())) s.wild[turn] = 1;
+    }
+
     // Scores of 32 tokens, of which the bits in `here` are there: -infinity for those that
     // the lane's query does not see; returns the largest.
     __device__ __forceinline__ float only_seen(f32x16_t& x, uint32_t here, int first) const
@@ -811,6 +824,7 @@ struct Attention {
                 pieces<1>(t, stop, page);
         }
         l = sum_halves(l);
+        if constexpr (sizeof(T) == 2) note_wild_results();
         if (half == 0) {
             s.m[wave * kAttnRows + col] = m;
             s.l[wave * kAttnRows + col] = l;

@@ -364,6 +364,30 @@ def test_values_that_are_not_finite(gpu, dtype):
         assert ((out - want).abs() <= bound)[fine].all()
 
 
+@pytest.mark.parametrize("dtype", [BF16, FP16, FP32])
+@pytest.mark.parametrize("new,heads,groups", [([1, 1, 1, 1], 4, None), ([1, 1, 1, 1], 4, 96), ([4, 1, 3, 2], 8, None), ([9, 4, 1, 9], 8, None),
+                                              ([60, 40, 70, 33], 4, None), ([40, 2, 1, 33], 16, 96), ([1, 1, 1, 1], 64, 96)])
+@pytest.mark.parametrize("dims", [(64, 64), (128, 96), (33, 17), (160, 200)])
+def test_infinities_among_the_values(gpu, new, heads, groups, dims, dtype):
+    """Values that are not finite in the middle of rows, where every query sees them: infinities stay infinities of their sign,
+    both signs in one dimension give NaN, and other dimensions nothing of it."""
+    note(f"attention infinities {new} {heads} {groups} {dims} {dtype}")
+    shared = [(0, 4, groups)] if groups else None
+    more = {"groups": [0, 4], "shared": [groups]} if groups else {}
+    for row, tokens in ((0, 40), (3, 165)):
+        c = Cache(24, [300, 261, 200, 333], dtype, 2, *dims, 16, shared=shared, device="cuda")
+
+        def at(t):
+            return c.values[int(c.table[row, t // 16]), t % 16]
+
+        at(tokens)[0, 3] = math.inf
+        at(tokens)[1, 5] = -math.inf
+        at(tokens + 1)[1, 6] = math.inf
+        at(tokens + 20)[1, 6] = -math.inf
+        at(tokens + 50)[0, 11] = math.nan
+        check_attention(c, [0, 1, 2, 3], new, heads, **more)
+
+
 @pytest.mark.parametrize("scale", [0.0, -0.3, 1e-30, 3.0])
 def test_scales(gpu, scale):
     note(f"attention scale {scale}")
