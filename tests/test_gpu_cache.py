@@ -507,6 +507,58 @@ def test_long_rows(gpu, dtype, dim, new, length):
     assert off <= (2 * torch.finfo(dtype).eps / 2 if dtype != FP32 else 64 * 2.0 ** -24), off
 
 
+@pytest.mark.parametrize("dtype", [BF16, FP16, FP32])
+@pytest.mark.parametrize("below", [11.0, 14.0, 16.3, 17.7, 20.0])
+@pytest.mark.parametrize("new,heads", [(1, 2), (3, 8), (1, 48), (40, 3)])
+def test_one_token_far_above_many(gpu, new, heads, below, dtype):
+    """A token that outweighs each of 100,000 others by e^below, which together still weigh what counts: first, in the middle and
+    last, in tiles of up to 32 queries and of more. What a weight loses to its type's range is a loss in one direction. As many
+    rows (with the same pages) as workgroups, so that each row's maximum goes along with all of it."""
+    note(f"attention one above many {new} {heads} {below} {dtype}")
+    n, rows, dim, page = 100001, 530, 64, 64
+    gen = torch.Generator(device="cuda").manual_seed(25)
+    pages = -(-n // page)
+    table = torch.randperm(pages, generator=gen, device="cuda").int().expand(rows, pages).contiguous()
+    values = (0.5 + torch.rand(pages, page, 1, dim, generator=gen, device="cuda")).to(dtype)
+    q = torch.zeros(rows * new, heads, dim, device="cuda", dtype=dtype)
+    q[..., 0] = 1
+    offsets = torch.arange(0, rows * new + 1, new, device="cuda")
+    for place in (0, n // 2, n - new):
+        keys = torch.zeros(pages, page, 1, dim, device="cuda", dtype=dtype)
+        at = table[0, place // page].long(), place % page
+        keys[at][0, 0] = below
+        kept = values[at].clone()
+        values[at] = 0.0625
+        out, lse = dws.pages_attention(q, keys, values, table, ints([n] * rows), offsets=offsets, scale=1.0, lse=True)
+        k, v = (x[table[0].long()].reshape(-1, dim)[:n].double() for x in (keys, values))
+        values[at] = kept
+        for j in {0, new - 1}:
+            seen = n - new + 1 + j
+            x = k[:seen, 0]
+            w = torch.softmax(x, 0)
+            want = w @ v[:seen]
+            largest = torch.full((1,), float(x.max()), dtype=torch.float64)
+            # (fp32 products add two tokens a step, not 16: n / 2 steps of a sum)
+            bound = attention_bound(want[None].cpu(), want[None].cpu(), largest, 8 * n if dtype == FP32 else n, 1, dtype)[0].cuda()
+            off = (out.view(rows, new, heads, dim)[:, j].double() - want).abs()
+            assert (off <= bound).all(), f"off by up to {(off / bound).max():.3g} of the bound"
+            exact = float(torch.logsumexp(x, 0))
+            assert (lse.view(rows, new, heads)[:, j].double() - exact).abs().max() <= (n / 8 + 64 + 9 * below + 4 * exact) * 2.0 ** -24
+
+
+def test_far_apart_scores_in_fp16(gpu):
+    """Scores that rise and fall by hundreds along the row, with the range of fp16."""
+    note("attention far apart scores, fp16")
+    for tokens, heads in ((4, 2), (4, 24), (60, 2)):
+        c = Cache(10, [700, 700], FP16, 1, 64, 64, 16, device="cuda")
+        for r, sign in ((0, 1), (1, -1)):
+            for t in range(700):
+                c.keys[int(c.table[r, t // 16]), t % 16] = sign * (t - 350) / 8
+        for scale in (0.25, 0.01):
+            q = torch.full((2 * tokens, heads, 64), 0.5, dtype=FP16, device="cuda")
+            check_attention(c, [0, 1], [tokens, tokens], heads, q=q, scale=scale)
+
+
 def test_pool_beyond_32_bits(gpu):
     """Pages more than 2^32 bytes and 2^31 elements from the pool's beginning, written and read."""
     note("attention beyond 32 bits")
