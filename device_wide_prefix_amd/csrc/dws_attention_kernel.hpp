@@ -19,7 +19,8 @@
 //
 // Measured, with the joining, a call: 96 sequences of 1 to 16,000 tokens, 8 heads of 128, 4
 // queries each, bf16: 157 us, 4.7 TB/s of keys and values. 3 prompts of 900 to 2,000 tokens
-// behind 4,097: 567 us, 790 TFLOP/s, where a large matrix product reaches 1,335. There each
+// behind 4,097: 740 us, 603 TFLOP/s, where a large matrix product reaches 1,335; with weights
+// in one part, where a caller asks for that, 587. There (in one part) each
 // SIMD's vector instructions take 53% of the time (scores to weights: 4 of 32 bits for each,
 // 4 times that for the exponential) and its matrix products 36%: two waves hide what one
 // waits for, and hardly overlap the two. Tiles of 256 queries would halve the reads of the
@@ -76,7 +77,8 @@ __device__ __forceinline__ float sum_halves(float x)
     return __builtin_bit_cast(float, (uint32_t)r[0]) + __builtin_bit_cast(float, (uint32_t)r[1]);
 }
 
-template <class T, int D, int NW, int ACCESS>
+// PARTS: of the weights in tiles of more than 32 queries.
+template <class T, int D, int NW, int ACCESS, int PARTS>
 struct Attention {
     static constexpr bool WHOLE = ACCESS != kElements;
     static constexpr int CH = 16 / sizeof(T);           // elements of a chunk
@@ -366,13 +368,13 @@ struct Attention {
     {
         if constexpr (kAmong) __builtin_amdgcn_sched_barrier(0);
     }
-    template <int COUNT, int READS>
+    template <int COUNT, int READS, int PRODUCTS = 1>
     static __device__ __forceinline__ void reads_among_products()
     {
 #pragma unroll
         for (int i = 0; i < COUNT; ++i) {
             __builtin_amdgcn_sched_group_barrier(0x100, READS, 0);                              // LDS reads
-            __builtin_amdgcn_sched_group_barrier(0x008, sizeof(T) == 2 ? 1 : CH, 0);            // matrix products
+            __builtin_amdgcn_sched_group_barrier(0x008, PRODUCTS * (sizeof(T) == 2 ? 1 : CH), 0);            // matrix products
         }
     }
     __device__ __forceinline__ Chunk<T> key_fragment(LdsBytes keys, int i) const
@@ -482,11 +484,13 @@ struct Attention {
         }
     }
     static constexpr int STEPS = 16 / CH;       // steps of the second product
+    static constexpr int kSmallParts = sizeof(T) == 2 ? 2 : 1;
     struct Weights {
         Chunk<T> p[STEPS];
     };
-    // `rest`: what rounding to 16 bits leaves of them.
-    __device__ __forceinline__ Weights weights(const f32x16_t& x, Weights* rest = nullptr)
+    // `rest`: what rounding to 16 bits leaves of them, if they are wanted in two parts.
+    template <int COUNT>
+    __device__ __forceinline__ Weights weights(const f32x16_t& x, Weights& rest)
     {
         Weights w;
         const float base = m == -__builtin_inff() ? 0.f : m - kHeadroom;
@@ -499,7 +503,7 @@ struct Attention {
             y = __builtin_amdgcn_exp2f(y);
             sum += y;
             w.p[e / CH][e % CH] = (T)y;
-            if (rest != nullptr) rest->p[e / CH][e % CH] = (T)(y - (float)w.p[e / CH][e % CH]);
+            if constexpr (COUNT == 2) rest.p[e / CH][e % CH] = (T)(y - (float)w.p[e / CH][e % CH]);
         }
         l += sum;
         return w;
@@ -509,15 +513,13 @@ struct Attention {
     struct Values {
         Chunk<T> x[FRAGMENTS];
     };
-    __device__ __forceinline__ void accumulate(LdsBytes values, const Weights& w)
+    template <int COUNT>
+    __device__ __forceinline__ void add_product(int i, const Values& v, const Weights& w, const Weights& rest)
     {
-        Values v;
-#pragma unroll
-        for (int i = 0; i < FRAGMENTS; ++i) v.x[i] = value_fragment(values, i / STEPS, i % STEPS);
-        reads_before_products();
-#pragma unroll
-        for (int i = 0; i < FRAGMENTS; ++i) o[i / STEPS] = mma(v.x[i], w.p[i % STEPS], o[i / STEPS]);
+        o[i / STEPS] = mma(v.x[i], w.p[i % STEPS], o[i / STEPS]);
+        if constexpr (COUNT == 2) o[i / STEPS] = mma(v.x[i], rest.p[i % STEPS], o[i / STEPS]);
     }
+    template <int COUNT>
     __device__ __forceinline__ void accumulate(LdsBytes values, const Weights& w, const Weights& rest)
     {
         Values v;
@@ -525,17 +527,19 @@ struct Attention {
         for (int i = 0; i < FRAGMENTS; ++i) v.x[i] = value_fragment(values, i / STEPS, i % STEPS);
         reads_before_products();
 #pragma unroll
-        for (int i = 0; i < FRAGMENTS; ++i) {
-            o[i / STEPS] = mma(v.x[i], w.p[i % STEPS], o[i / STEPS]);
-            o[i / STEPS] = mma(v.x[i], rest.p[i % STEPS], o[i / STEPS]);
-        }
+        for (int i = 0; i < FRAGMENTS; ++i) add_product<COUNT>(i, v, w, rest);
     }
-    __device__ __forceinline__ void accumulate(LdsBytes values, const Weights (&w)[1]) { accumulate(values, w[0]); }
-    __device__ __forceinline__ void accumulate(LdsBytes values, const Weights (&w)[2])
+    template <int COUNT>
+    __device__ __forceinline__ void accumulate(LdsBytes values, const Weights (&w)[1], const Weights (&rest)[1])
+    {
+        accumulate<COUNT>(values, w[0], rest[0]);
+    }
+    template <int COUNT>
+    __device__ __forceinline__ void accumulate(LdsBytes values, const Weights (&w)[2], const Weights (&rest)[2])
     {
         if constexpr (!kAmong) {
-            accumulate(values, w[0]);
-            accumulate(values + TILE, w[1]);
+            accumulate<COUNT>(values, w[0], rest[0]);
+            accumulate<COUNT>(values + TILE, w[1], rest[1]);
             return;
         }
         Values v[2];
@@ -545,12 +549,12 @@ struct Attention {
 #pragma unroll
         for (int i = 0; i < FRAGMENTS; ++i) {
             v[1].x[i] = value_fragment(values + TILE, i / STEPS, i % STEPS);
-            o[i / STEPS] = mma(v[0].x[i], w[0].p[i % STEPS], o[i / STEPS]);
+            add_product<COUNT>(i, v[0], w[0], rest[0]);
         }
-        reads_among_products<FRAGMENTS, sizeof(T) == 2 ? 2 : CH>();
+        reads_among_products<FRAGMENTS, sizeof(T) == 2 ? 2 : CH, COUNT>();
         reads_before_products();
 #pragma unroll
-        for (int i = 0; i < FRAGMENTS; ++i) o[i / STEPS] = mma(v[1].x[i], w[1].p[i % STEPS], o[i / STEPS]);
+        for (int i = 0; i < FRAGMENTS; ++i) add_product<COUNT>(i, v[1], w[1], rest[1]);
     }
     // Addresses are worked out anew for each piece: kept, they push results out of the registers.
     __device__ __forceinline__ void forget_addresses()
@@ -589,14 +593,10 @@ struct Attention {
             }
             f32x16_t x = scores(mine);
             follow(only_seen(x, there, t));
-            // In two parts the weights leave no error beside the result's own rounding (0.0017 of bf16
-            // results instead of 0.0020), for half a percent of 96 sequences of 1 to 16,000 tokens; in
-            // larger tiles it would be half as many matrix products again.
+            // In two parts 16-bit weights leave no error beside the result's own rounding (0.0017 of bf16
+            // results instead of 0.0020), here for half a percent of 96 sequences of 1 to 16,000 tokens.
             Weights w, rest;
-            if constexpr (sizeof(T) == 2)
-                w = weights(x, &rest);
-            else
-                w = weights(x);
+            w = weights<kSmallParts>(x, rest);
             wave_sync();
             put<true, N>(mine, v);
             wave_sync();
@@ -610,10 +610,7 @@ struct Attention {
                 page = page_of(t + 2 * TOKENS, kKvTokens);
             }
             if (masked(there, t)) note_wild(mine);
-            if constexpr (sizeof(T) == 2)
-                accumulate(mine, w, rest);
-            else
-                accumulate(mine, w);
+            accumulate<kSmallParts>(mine, w, rest);
         }
     }
     static __device__ __forceinline__ auto value_registers(u32x4_t (&next)[kAhead ? N : 1], u32x4_t (&also)[kBoth ? N : 1])
@@ -651,7 +648,7 @@ struct Attention {
             __syncthreads();
             // tiles of which a token is not there, in 32 bits
             f32x16_t x[SUBS];
-            Weights w[SUBS];
+            Weights w[SUBS], rest[SUBS];
             scores(keys + first_sub * TILE, x);
             uint32_t here[SUBS];
 #pragma unroll
@@ -662,7 +659,7 @@ struct Attention {
             for (int r = 0; r < SUBS; ++r) top = fmaxf(top, only_seen(x[r], here[r], t + (first_sub + r) * kKvTokens));
             follow(top);
 #pragma unroll
-            for (int r = 0; r < SUBS; ++r) w[r] = weights(x[r]);
+            for (int r = 0; r < SUBS; ++r) w[r] = weights<PARTS>(x[r], rest[r]);
             put<true, HALF>(values + mine, next);
             if (t + TOKENS < end) {
                 after = places(t + wave * 16 + TOKENS, page);
@@ -673,7 +670,7 @@ struct Attention {
 #pragma unroll
             for (int r = 0; r < SUBS; ++r)
                 if (masked(here[r], t + (first_sub + r) * kKvTokens)) note_wild(values + (first_sub + r) * TILE);
-            accumulate(values + first_sub * TILE, w);
+            accumulate<PARTS>(values + first_sub * TILE, w, rest);
         }
         __builtin_amdgcn_s_setprio(0);
     }
@@ -746,7 +743,7 @@ struct Attention {
             __syncthreads();            // and the other half has been read
             // tiles of which a token is not there, in 32 bits
             f32x16_t x[SUBS];
-            Weights w[SUBS];
+            Weights w[SUBS], rest[SUBS];
             scores(keys + first_sub * TILE, x);
             if (t + TOKENS < end) {
                 after = places(t + wave * 16 + TOKENS, page);
@@ -762,11 +759,11 @@ struct Attention {
             for (int r = 0; r < SUBS; ++r) top = fmaxf(top, only_seen(x[r], here[r], t + (first_sub + r) * kKvTokens));
             follow(top);
 #pragma unroll
-            for (int r = 0; r < SUBS; ++r) w[r] = weights(x[r]);
+            for (int r = 0; r < SUBS; ++r) w[r] = weights<PARTS>(x[r], rest[r]);
 #pragma unroll
             for (int r = 0; r < SUBS; ++r)
                 if (masked(here[r], t + (first_sub + r) * kKvTokens)) note_wild(values + (first_sub + r) * TILE);
-            accumulate(values + first_sub * TILE, w);
+            accumulate<PARTS>(values + first_sub * TILE, w, rest);
         }
         __builtin_amdgcn_s_setprio(0);
     }
@@ -907,12 +904,12 @@ __device__ __forceinline__ X uniform(X x)
 // and 1 registers, 16 to 32, and as many as the queries.
 constexpr int attn_occupancy(int dim, int size) { return dim * size <= 128 ? 3 : (dim * size <= 256 ? 2 : 1); }
 
-template <class T, int D, int NW, int ACCESS>
+template <class T, int D, int NW, int ACCESS, int PARTS>
 __global__ __launch_bounds__(64 * NW, attn_occupancy(D, sizeof(T))) void k_attention(
     AttentionParams p)
 {
-    __shared__ typename Attention<T, D, NW, ACCESS>::Lds lds;
-    Attention<T, D, NW, ACCESS> w(p, lds);
+    __shared__ typename Attention<T, D, NW, ACCESS, PARTS>::Lds lds;
+    Attention<T, D, NW, ACCESS, PARTS> w(p, lds);
     const AttnWork work(p);
     const int all = (int)(p.n_groups + p.c.n);
     if (threadIdx.x < 2) lds.wild[threadIdx.x] = 0;
@@ -978,18 +975,25 @@ __global__ __launch_bounds__(64 * NW, attn_occupancy(D, sizeof(T))) void k_atten
     }
 }
 
-template <class T, int D>
-hipError_t launch_dim(const AttentionParams& p, hipStream_t stream)
+template <class T, int D, int PARTS>
+hipError_t launch_parts(const AttentionParams& p, hipStream_t stream)
 {
     constexpr int NW = attn_waves(sizeof(T) == 4 ? DWS_FLOAT32 : DWS_BFLOAT16, D);
     const unsigned grid = (unsigned)p.workgroups;
     if (p.kv_access == kNear)
-        k_attention<T, D, NW, kNear><<<grid, 64 * NW, 0, stream>>>(p);
+        k_attention<T, D, NW, kNear, PARTS><<<grid, 64 * NW, 0, stream>>>(p);
     else if (p.kv_access == kFar)
-        k_attention<T, D, NW, kFar><<<grid, 64 * NW, 0, stream>>>(p);
+        k_attention<T, D, NW, kFar, PARTS><<<grid, 64 * NW, 0, stream>>>(p);
     else
-        k_attention<T, D, NW, kElements><<<grid, 64 * NW, 0, stream>>>(p);
+        k_attention<T, D, NW, kElements, PARTS><<<grid, 64 * NW, 0, stream>>>(p);
     return hipGetLastError();
+}
+template <class T, int D>
+hipError_t launch_dim(const AttentionParams& p, hipStream_t stream)
+{
+    if constexpr (sizeof(T) == 2)
+        if (!p.one_part) return launch_parts<T, D, 2>(p, stream);
+    return launch_parts<T, D, 1>(p, stream);
 }
 template <class T>
 hipError_t launch_type(const AttentionParams& p, hipStream_t stream)

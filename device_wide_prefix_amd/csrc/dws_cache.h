@@ -113,6 +113,7 @@ struct AttentionParams {
     const int64_t* groups;
     const int* shared;
     int zero_rest, whole_q, whole_out;
+    int one_part;               // 16-bit weights of tiles of more than 32 queries rounded once
     int kv_access;              // how keys and values are read (AttnAccess)
     uint32_t key_ps, key_ts, value_ps, value_ts;    // kNear: strides in 16 bytes
     HeadRows q, out;

@@ -222,7 +222,7 @@ dws_status attention_entry(const dws_pages_attention_args* a, hipStream_t stream
     dws_status st = check_attention_sizes(a);
     if (st != DWS_OK) return st;
     const dws_kv_cache& c = a->cache;
-    if (!std::isfinite(a->scale)) return DWS_ERR_INVALID_ARG;
+    if (!std::isfinite(a->scale) || (a->options & ~DWS_ATTENTION_ONE_PART) != 0) return DWS_ERR_INVALID_ARG;
     const int64_t tokens = a->seqs.tokens;
     AttentionParams p{};
     Arrays arrays;
@@ -246,6 +246,7 @@ dws_status attention_entry(const dws_pages_attention_args* a, hipStream_t stream
     p.groups = reinterpret_cast<const int64_t*>(a->d_groups);
     p.shared = a->d_shared;
     p.zero_rest = a->zero_rest != 0;
+    p.one_part = (a->options & DWS_ATTENTION_ONE_PART) != 0;
     const int64_t e = (int64_t)size_of(c.dtype);
     p.whole_q = whole(a->q.data, e, 16, c.dim_k, a->q.token_stride, a->q.head_stride);
     const bool whole_kv = whole(c.keys.data, e, 16, c.dim_k, c.keys.page_stride, c.keys.token_stride, c.keys.head_stride) &&

@@ -825,6 +825,13 @@ typedef struct dws_pages_append_args {
  */
 dws_status dws_pages_append(const dws_pages_append_args* args, hipStream_t stream);
 
+/* dws_pages_attention_args.options */
+enum {
+    /* 16-bit probabilities rounded once, not in two parts, for their product with the values where more than 32 queries
+     * share keys: results with 1.35 times the error of their own rounding, and a fifth less time for long prompts. */
+    DWS_ATTENTION_ONE_PART = 1
+};
+
 /* Arguments of dws_pages_attention; set unused members to 0. */
 typedef struct dws_pages_attention_args {
     dws_kv_cache cache;
@@ -838,6 +845,7 @@ typedef struct dws_pages_attention_args {
     const long long* d_groups;
     const int* d_shared;
     int zero_rest;              /* != 0: rows of out (and d_lse: -infinity) before the first and behind the last sequence are set */
+    int options;                /* DWS_ATTENTION_..., or 0 */
     dws_rows q, out;            /* (tokens, heads_q, dim_k), (tokens, heads_q, dim_v) */
     float* d_lse;               /* (tokens, heads_q), contiguous: natural logarithm of the sum of the exponentials; NULL: not wanted */
     void* d_workspace;          /* DEVICE, 256-byte aligned */
@@ -855,9 +863,9 @@ dws_status dws_pages_attention_workspace(const dws_pages_attention_args* args, s
  * sequence, a few, or whole prompts behind what is there. A query that sees nothing (a row outside the table, a sequence
  * with more tokens than its row, a row longer than max_pages pages or 2^31 - 4097
  * tokens, pages outside the pool) gives 0, and -infinity in d_lse; so does one all of whose scores are -infinity. Scores, their statistics and
- * all sums are fp32; with 16-bit inputs the probabilities are rounded to dtype for their product with the values, in two
- * parts (which loses nothing of the result's precision) where up to 32 queries share a key head, in one otherwise; fp16 ones
- * below 2^-36 of the row's largest may count as 0 there. What is
+ * all sums are fp32; with 16-bit inputs the probabilities are rounded to dtype in two parts for their product with the
+ * values, which loses nothing of the result's precision (but for options; fp16 ones below 2^-36 of the row's largest may
+ * count as 0 there). What is
  * behind a row's end is not read, whatever the pages hold there. Values that are not finite reach the queries that see
  * them, and no others. d_shared must say the truth: the shared tokens are read from the pages of the group's first
  * sequence. Results do not depend on scheduling. Errors as dws_pages_append, and too small a workspace:

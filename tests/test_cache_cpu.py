@@ -188,6 +188,14 @@ def test_refusals_of_attention(lib):
     assert status(lib, attention_args(**{**work, **none})) == dws.OK
 
 
+def test_options_of_attention(lib):
+    need = ctypes.c_size_t(0)
+    assert lib.dws_pages_attention_workspace(ctypes.byref(attention_args()), ctypes.byref(need)) == dws.OK
+    none = {"seqs.tokens": 0, "q.data": None, "out.data": None, "d_lse": None, "d_workspace": room(20), "workspace_bytes": need.value}
+    for options, want in ((0, dws.OK), (dws.ATTENTION_ONE_PART, dws.OK), (2, BAD), (3, BAD), (-1, BAD), (1 << 30, BAD)):
+        assert status(lib, attention_args(**none, options=options)) == want, options
+
+
 def test_workspace_of_attention_does_not_grow_with_prompts_alone(lib):
     def bytes_of(**changes):
         need = ctypes.c_size_t(0)

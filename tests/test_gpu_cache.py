@@ -314,6 +314,43 @@ def test_tiles_of_many_queries(gpu, dims, dtype):
     check_attention(c, [2, 0, 1], [33, 64, 17], 4)
 
 
+def check_own_rounding(c, rows, new, heads, **more):
+    """Nothing but the result's own rounding: half a step of it. Weights in two parts of h = eps / 2 keep h^2 of themselves; the
+    rest is fp32's, as attention_bound has it for that type."""
+    q, offsets, scale, (out, _) = run_attention(c, rows, new, heads, **more)
+    want, _, spread, largest = attention(q, *c.args(), rows, offsets, scale)
+    half = torch.finfo(c.dtype).eps / 2
+    bound = attention_bound(want, spread, largest, max(c.lens), c.dk, FP32) + half * (1 + half) * want.abs() + half ** 2 * spread
+    off = (out.double().cpu() - want).abs()
+    assert (off <= bound).all(), f"off by up to {(off / bound).max():.3g} of the bound"
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP16])
+@pytest.mark.parametrize("dims", [(128, 128), (64, 64), (96, 80), (33, 65), (160, 200), (256, 256)])
+def test_weights_lose_nothing(gpu, dims, dtype):
+    """Tiles of up to 32, 64 and 128 queries, of tokens and of sequences that share their first ones."""
+    note(f"attention, weights in two parts {dims} {dtype}")
+    c = Cache(26, [150, 230, 90, 400], dtype, 2, *dims, 16, shared=[(0, 2, 96)], device="cuda")
+    for new, heads in (([1, 1, 1, 1], 4), ([3, 1, 2, 4], 8), ([5, 9, 7, 8], 14), ([70, 30, 64, 20], 4)):
+        check_own_rounding(c, [0, 1, 2, 3], new, heads)
+    check_own_rounding(c, [0, 1, 2, 3], [1, 1, 1, 1], 60, groups=[0, 2], shared=[96])
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP16, FP32])
+@pytest.mark.parametrize("dims", [(128, 128), (64, 64), (33, 65), (160, 200)])
+def test_weights_in_one_part_where_asked_for(gpu, dims, dtype):
+    """Rounded once in tiles of more than 32 queries, and nothing else: the others, and fp32, have the same bits."""
+    note(f"attention, weights in one part {dims} {dtype}")
+    c = Cache(27, [150, 230, 90, 400], dtype, 2, *dims, 16, shared=[(0, 2, 96)], device="cuda")
+    c.values[int(c.table[1, 2]), 3, 0, 5] = math.inf
+    for new, heads, more in (([1, 1, 1, 1], 4, {}), ([5, 9, 7, 8], 14, {}), ([70, 30, 64, 20], 4, {}),
+                             ([1, 1, 1, 1], 60, {"groups": [0, 2], "shared": [96]})):
+        one = check_attention(c, [0, 1, 2, 3], new, heads, one_part=True, **more)
+        two = check_attention(c, [0, 1, 2, 3], new, heads, **more)
+        same = torch.equal(one.nan_to_num(nan=7.0), two.nan_to_num(nan=7.0))
+        assert same == (dtype == FP32 or max(new) * heads // 2 <= 32 and not more)
+
+
 def test_groups_with_odd_places(gpu):
     """Fewer shared tokens than whole pages, more than the rows have, none; empty places first and last in a group."""
     note("attention groups, odd places")
