@@ -1155,7 +1155,8 @@ def pages_attention(q, keys, values, table, lengths, rows=None, offsets=None, gr
     and shared (int32 GPU tensor): the first shared[g] tokens of sequences groups[g] .. groups[g + 1] - 1 are in the same
     pages, as pages_fork leaves them, and are read once for all of these. scale: dim_k^-0.5 by default. Queries that see
     nothing give 0. Rows of ``out`` in no sequence stay as they were, and are 0 in a new one. lse: None, True for a new
-    float32 (tokens, heads_q) tensor of the logarithms of the exponentials' sums, or one to write. one_part: 16-bit
+    float32 (tokens, heads_q) tensor of the logarithms of the exponentials' sums, or one to write; its rows in no sequence
+    stay as they were, and are -infinity in a new one. one_part: 16-bit
     probabilities rounded once for their product with the values where more than 32 queries share keys: 1.35 times the
     error, a fifth less time for long prompts.
     Returns out, or (out, lse)."""
@@ -1180,7 +1181,9 @@ def pages_attention(q, keys, values, table, lengths, rows=None, offsets=None, gr
     with _on_stream(q, stream) as s:
         zero, shape = 0, (tokens, heads_q, dim_v)
         if out is None:
-            out, zero = torch.empty(shape, dtype=dtype, device=device), int(offsets is not None)
+            # (dws_pages_attention sets the rest of both results, or of none: a given lse keeps its own)
+            kept = offsets is not None and lse is not None and lse is not True
+            out, zero = (torch.zeros if kept else torch.empty)(shape, dtype=dtype, device=device), int(offsets is not None and not kept)
             to = out.data_ptr(), heads_q * dim_v, dim_v
         else:
             if lse is True and offsets is not None:

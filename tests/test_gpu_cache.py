@@ -479,6 +479,24 @@ def test_rest_of_the_rows(gpu):
     assert dws.pages_attention(q[:0], *c.args()).shape == (0, 4, 64)
 
 
+def test_rest_of_given_and_new_results(gpu):
+    """Rows in no sequence stay as they were in a given tensor, and are set in a new one, whichever of the two results is which."""
+    note("attention, rest of given and new results")
+    c = Cache(28, [90, 130], FP32, 2, 64, 64, 16, device="cuda")
+    q = torch.randn(12, 4, 64, device="cuda")
+    offsets = ints([3, 5, 9], torch.int64)
+    want, want_lse = dws.pages_attention(q, *c.args(), offsets=offsets, lse=True)
+    rest = [0, 1, 2, 9, 10, 11]
+    for new_out in (False, True):
+        for new_lse in (False, True):
+            out, lse = (torch.full_like(x, 5) for x in (want, want_lse))
+            got, got_lse = dws.pages_attention(q, *c.args(), offsets=offsets, out=None if new_out else out, lse=True if new_lse else lse)
+            assert (got is out) != new_out and (got_lse is lse) != new_lse
+            assert torch.equal(got[3:9], want[3:9]) and torch.equal(got_lse[3:9], want_lse[3:9])
+            assert (got[rest] == (0 if new_out else 5)).all(), (new_out, new_lse)
+            assert (got_lse[rest] == (-math.inf if new_lse else 5)).all(), (new_out, new_lse)
+
+
 def test_offsets_that_are_wrong(gpu):
     """Offsets, groups and lengths that make no sense: nothing outside the arrays is touched, and the right sequences of
     another call are as before."""
