@@ -161,7 +161,8 @@ struct Attention {
         }
     }
 
-    // Where a query of a group's tile stands in its own row; -1: nowhere.
+    // Where a query of a group's tile stands in its own row. Of a sequence without a row: behind
+    // everything, so that no piece has places that it alone must not see; the joining leaves it out.
     __device__ __forceinline__ int position_in_group(const AttnSeg* segs, int64_t token) const
     {
         int64_t lo = 0, hi = p.c.n - 1;
@@ -173,7 +174,7 @@ struct Attention {
                 hi = mid - 1;
         }
         const AttnSeg& x = segs[p.n_groups + lo];
-        return x.length > 0 ? x.length - x.count + (int)(token - x.begin) : -1;
+        return x.length > 0 ? x.length - x.count + (int)(token - x.begin) : INT32_MAX;
     }
     __device__ __forceinline__ void load_queries(const AttnSeg* segs)
     {

@@ -185,7 +185,7 @@ __global__ __launch_bounds__(kJoinThreads) void k_attention_join(AttentionParams
                     }
                 }
             };
-            if (r < end) {
+            if (r < end && a.table >= 0) {
                 // the group's tile with the row is on its way while the own parts are added
                 AttnDone g{};
                 int in = 0;

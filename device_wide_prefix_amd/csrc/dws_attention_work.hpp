@@ -187,12 +187,16 @@ __device__ __forceinline__ void lay_out(const AttentionParams& p, AttnSeg* segs,
         s.row = s.apart = -1;
         s.group = (int)s0;
         if (s1 - s0 > 1) {
-            const AttnSeg lead = sequence(p, s0);
-            const int64_t end = clamped(seq_begin(p.c, s1), p.c.tokens), count = end - lead.begin;
+            // the first one that has a row
+            AttnSeg lead = sequence(p, s0);
+#pragma unroll 1
+            for (int64_t i = s0 + 1; i < s1 && lead.length == 0; ++i) lead = sequence(p, i);
+            const int64_t begin = clamped(seq_begin(p.c, s0), p.c.tokens), end = clamped(seq_begin(p.c, s1), p.c.tokens);
+            const int64_t count = end - begin;
             const int shared = p.shared[g] < lead.length ? p.shared[g] : lead.length;
             // larger tiles are full with the rows of one sequence
             if (count > 0 && shared > 0 && count * p.share < (s1 - s0) * (work.tile_rows() / 2)) {
-                s.begin = lead.begin;
+                s.begin = (int)begin;
                 s.count = (int)count;
                 s.row = lead.row;
                 s.length = shared;

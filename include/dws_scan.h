@@ -868,7 +868,7 @@ dws_status dws_pages_attention_workspace(const dws_pages_attention_args* args, s
  * count as 0 there). What is
  * behind a row's end is not read, whatever the pages hold there. Values that are not finite reach the queries that see
  * them, and no others. d_shared must say the truth: the shared tokens are read from the pages of the group's first
- * sequence. Results do not depend on scheduling. Errors as dws_pages_append, and too small a workspace:
+ * sequence that has a row. Results do not depend on scheduling. Errors as dws_pages_append, and too small a workspace:
  * DWS_ERR_INVALID_ARG. Asynchronous, allocates nothing, may be captured.
  */
 dws_status dws_pages_attention(const dws_pages_attention_args* args, hipStream_t stream);

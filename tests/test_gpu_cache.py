@@ -366,6 +366,34 @@ def test_groups_with_odd_places(gpu):
     check_attention(c, list(range(6)), [2, 1, 0, 3, 1, 1], 4, groups=[0, 6], shared=[192])
 
 
+@pytest.mark.parametrize("members,empty", [(6, []), (6, [0]), (6, [3]), (6, [5]), (6, [0, 1, 2, 4]), (6, [0, 1, 2, 3, 4]), (40, list(range(33))),
+                                           (40, list(range(0, 40, 2))), (300, list(range(270)))])
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+def test_groups_share_whatever_places_are_empty(gpu, members, empty, dtype):
+    """The shared tokens are read through the first sequence that has a row, for all of a group: here no other row's table has them."""
+    note(f"attention groups, empty places {members} {len(empty)} {dtype}")
+    c = Cache(29, [96 + 1 + 7 * (r % 9) for r in range(members)], dtype, 2, 64, 64, 16, shared=[(0, members, 96)], device="cuda")
+    rows = [-1 if r in empty else r for r in range(members)]
+    for odd in (False, True):       # among the shared values, too
+        if odd:
+            c.values[int(c.table[0, 3]), 5, 1, 7] = math.inf
+        for heads, new in ((4, [1] * members), (16, [1 + r % 2 for r in range(members)])):
+            q, offsets, scale, got = run_attention(c, rows, new, heads, groups=[0, members], shared=[96])
+            want, _, spread, largest = attention(q, *c.args(), rows, offsets, scale)
+            off = (got[0].double().cpu() - want).abs()
+            fine = want.isfinite()
+            assert torch.equal(got[0].double().cpu()[~fine], want[~fine])
+            assert (off <= attention_bound(want, spread, largest, 200, 64, dtype))[fine].all()
+            if odd:                 # (rows that are computed again read their own tables)
+                continue
+            table, live = c.table.clone(), [r for r in range(members) if r not in empty]
+            for r in live[1:]:
+                table[r, :6] = -1
+            again = dws.pages_attention(q, c.keys, c.values, table, c.lengths, rows=ints(rows), offsets=ints(offsets, torch.int64), scale=scale,
+                                        groups=ints([0, members], torch.int64), shared=ints([96]), lse=True)
+            assert torch.equal(again[0], got[0]) and torch.equal(again[1], got[1])
+
+
 @pytest.mark.parametrize("dtype", [BF16, FP32])
 def test_rows_that_see_nothing(gpu, dtype):
     note(f"attention empty rows {dtype}")
