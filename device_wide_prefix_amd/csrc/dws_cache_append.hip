@@ -12,14 +12,18 @@ namespace {
 
 constexpr int kMaxPairs = 128;
 
-// cos and sin of position * freq. The turns are reduced in fp64 (a product of a
-// 31-bit and a 24-bit number; 2^-53 of it is all that is lost), the rest of the
-// rounding to fp32 enters through the first order, so that both are as good as fp32
-// holds them, however far the position.
+// cos and sin of position * freq. A product of a 31-bit and a 24-bit number has up to 55
+// bits, and 2^-53 of far positions' angles is several units of fp32: so the angle and
+// 1 / (2 pi) are two fp64 numbers each, and the whole turns go before anything is rounded.
+// The rest of the rounding to fp32 enters through the first order, so that both are as good
+// as fp32 holds them, however far the position.
 __device__ __forceinline__ float2 turn_of(int position, float freq)
 {
-    const double turns = (double)position * (double)freq * 0.15915494309189533577;      // 1 / (2 pi)
-    const double half = 2.0 * (turns - rint(turns));                                     // half turns, -1 .. 1
+    constexpr double kTurn = 0.15915494309189535, kTurnRest = -9.839338337591243e-18;    // 1 / (2 pi)
+    const double angle = (double)position * (double)freq;
+    const double angle_rest = __builtin_fma((double)position, (double)freq, -angle);
+    const double turns = __builtin_fma(angle, kTurn, -rint(angle * kTurn));
+    const double half = 2.0 * (turns + __builtin_fma(angle, kTurnRest, angle_rest * kTurn));     // half turns, -1 .. 1
     const float x = (float)half;
     const float rest = (float)(half - (double)x) * 3.14159265358979f;
     float s, c;

@@ -808,7 +808,7 @@ typedef struct dws_pages_append_args {
  * Writes the tokens' keys and values into the pages, after dws_pages_grow made
  * room. Each pair (a, b) of the first 2 * pairs dimensions of keys and queries
  * becomes (a cos x - b sin x, a sin x + b cos x), x = position * d_freqs[pair], in
- * fp32, rounded once; x is reduced in fp64, so far positions lose nothing.
+ * fp32, rounded once; x is reduced in two fp64 numbers, so far positions lose nothing.
  * Left out are sequences with a row outside the table, 0 in d_granted or a row that
  * an earlier sequence of the call names (searched for, work that grows with the
  * square of n), sequences that begin before row 0 of the call or have more tokens than

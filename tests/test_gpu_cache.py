@@ -1,6 +1,7 @@
 """Cached keys and values on the GPU: what is written, and attention over it, against 64 bits."""
 import math
 import random
+from fractions import Fraction
 
 import pytest
 import torch
@@ -131,6 +132,37 @@ def test_append_evenly_and_positions(gpu):
     before = c.keys.clone(), c.values.clone()
     got = dws.pages_append(*c.args(), k, v, freqs=freqs_of(32), positions=ints(positions), q=q)
     check_append(c, [0, 1, 2], [0, 2, 4, 6], k, v, q, freqs_of(32), False, before, got, positions)
+
+
+PI = Fraction("3.14159265358979323846264338327950288419716939937510582097494459230781640628620899")
+
+
+def test_angles_of_far_positions(gpu):
+    """Cosine and sine of position * frequency, in whole numbers until the angle is below pi: one unit of fp32 each, as near the
+    beginning, one for the correction and two for the function that gives them."""
+    note("append, far positions")
+    gen = torch.Generator().manual_seed(7)
+    positions = [1, 1000003, 2**24 + 1, 999999937, 1 << 30, 2**31 - 1, 2**31 - 2, 2147483629, -(2**31), -1999999973, 1234567891, -5]
+    n, pairs = len(positions), 128
+    freqs = (0.5 + torch.rand(pairs, generator=gen) * 0.5)
+    freqs[:40] *= 4.0 ** -torch.arange(40) % 1 + 0.001
+    freqs[0], freqs[1], freqs[2] = 1.0, 6.2831855, 1e-7
+    c = Cache(30, [n], FP32, 1, 256, 4, 16, device="cuda")
+    k, v, q = (torch.zeros(n, 1, d, device="cuda") for d in (256, 4, 256))
+    k[..., :pairs] = 1          # (cos, sin)
+    q[..., pairs:] = 1          # (-sin, cos)
+    got = dws.pages_append(*c.args(), k, v, freqs=freqs.cuda(), positions=ints(positions), q=q).double().cpu()
+    keys = torch.stack([c.keys[int(c.table[0, 0]), t] for t in range(n)]).double().cpu()
+    for t, p in enumerate(positions):
+        want = []
+        for f in freqs.tolist():
+            x = p * Fraction(f)
+            x = float(x - round(x / (2 * PI)) * 2 * PI)
+            want.append((math.cos(x), math.sin(x)))
+        cos, sin = torch.tensor(want, dtype=torch.float64).T
+        for a, b in ((keys[t, 0, :pairs], cos), (keys[t, 0, pairs:], sin), (got[t, 0, :pairs], -sin), (got[t, 0, pairs:], cos)):
+            off = (a - b).abs().max()
+            assert off <= 4 * 2.0 ** -24, f"position {p}: {off * 2 ** 24:.3g} units"
 
 
 def test_append_leaves_out(gpu):
