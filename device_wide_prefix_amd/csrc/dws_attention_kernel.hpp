@@ -34,6 +34,8 @@
 // step are the rows above, and the transposing LDS reads bring V's in the same order.
 #pragma once
 
+#include <stddef.h>
+
 #include <type_traits>
 
 #include "dws_attention_work.hpp"
@@ -110,6 +112,9 @@ struct Attention {
         int wild[2];                    // rows to compute again, of this tile and the next
         float m[kAttnRows * NW], l[kAttnRows * NW];
     };
+
+    // (m0 has 16 bits for the place in the LDS, where this is the kernel's only variable)
+    static_assert(!kStream || (offsetof(Lds, kv) == 0 && sizeof(Lds::kv) <= 1 << 16), "streamed within the first 64 KB");
 
     // Chunks of a row are permuted so that reads of one column by 16 rows (keys), and
     // of four rows by 16 columns (values), go to different banks.
@@ -700,7 +705,7 @@ struct Attention {
             asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off"
                          :
                          : "v"(head + ((uint64_t)(at[i] + (c < chunks ? c : 0)) << 4)), "s"((uint32_t)(uintptr_t)(to + i * STEP * ROW))
-                         : "memory");
+                         : "m0", "memory");
         }
     }
     __device__ __forceinline__ void stream_piece(LdsBytes keys) const
