@@ -5,6 +5,7 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <cfloat>
 #include <cmath>
 #include <new>
 
@@ -222,7 +223,9 @@ dws_status attention_entry(const dws_pages_attention_args* a, hipStream_t stream
     dws_status st = check_attention_sizes(a);
     if (st != DWS_OK) return st;
     const dws_kv_cache& c = a->cache;
-    if (!std::isfinite(a->scale) || (a->options & ~DWS_ATTENTION_ONE_PART) != 0) return DWS_ERR_INVALID_ARG;
+    // 0 leaves the queries out, so that any factor will do
+    const double by = a->scale == 0.f ? 1.0 : std::fabs((double)a->scale) * 1.4426950408889634;
+    if (!(by <= (double)FLT_MAX) || (a->options & ~DWS_ATTENTION_ONE_PART) != 0) return DWS_ERR_INVALID_ARG;
     const int64_t tokens = a->seqs.tokens;
     AttentionParams p{};
     Arrays arrays;
@@ -269,8 +272,6 @@ dws_status attention_entry(const dws_pages_attention_args* a, hipStream_t stream
     p.shift = z.waves == 4 ? 7 : 6;
     p.workgroups = z.workgroups;
     p.cost_shift = z.cost_shift;
-    // 0 leaves the queries out, so that any factor will do
-    const double by = a->scale == 0.f ? 1.0 : std::fabs((double)a->scale) * 1.4426950408889634;
     p.log2_scale = (float)by;
     p.log2_rest = (float)(by - (double)p.log2_scale);
     p.sign = a->scale > 0.f ? 1.f : (a->scale < 0.f ? -1.f : 0.f);

@@ -837,7 +837,7 @@ typedef struct dws_pages_attention_args {
     dws_kv_cache cache;
     dws_page_seqs seqs;
     int heads_q;                /* a multiple of cache.heads: query head h uses head h / (heads_q / cache.heads) */
-    float scale;                /* finite */
+    float scale;                /* finite, as scale log2(e) */
     /* Sequences that begin alike: group g is sequences d_groups[g] .. d_groups[g+1] - 1 (DEVICE, n_groups + 1 int64, not
      * decreasing), and the first d_shared[g] (DEVICE, n_groups int32) tokens of their rows are in the same pages, which
      * are read once for all of them. Both NULL and n_groups 0 without groups. */

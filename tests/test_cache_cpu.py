@@ -188,6 +188,15 @@ def test_refusals_of_attention(lib):
     assert status(lib, attention_args(**{**work, **none})) == dws.OK
 
 
+def test_scales_of_attention(lib):
+    """scale log2(e) has to be a number, too: a score of 0 would be NaN with an infinite one."""
+    need = ctypes.c_size_t(0)
+    assert lib.dws_pages_attention_workspace(ctypes.byref(attention_args()), ctypes.byref(need)) == dws.OK
+    none = {"seqs.tokens": 0, "q.data": None, "out.data": None, "d_lse": None, "d_workspace": room(20), "workspace_bytes": need.value}
+    for scale, want in ((0.0, dws.OK), (2.3e38, dws.OK), (-2.3e38, dws.OK), (1e-45, dws.OK), (2.4e38, BAD), (-3.4e38, BAD), (NAN, BAD), (-INF, BAD)):
+        assert status(lib, attention_args(**none, scale=scale)) == want, scale
+
+
 def test_options_of_attention(lib):
     need = ctypes.c_size_t(0)
     assert lib.dws_pages_attention_workspace(ctypes.byref(attention_args()), ctypes.byref(need)) == dws.OK
