@@ -187,10 +187,10 @@ __device__ __forceinline__ void lay_out(const AttentionParams& p, AttnSeg* segs,
         s.row = s.apart = -1;
         s.group = (int)s0;
         if (s1 - s0 > 1) {
-            // the first one that has a row
+            // the first one that has a row (the last one of a group shares with none)
             AttnSeg lead = sequence(p, s0);
 #pragma unroll 1
-            for (int64_t i = s0 + 1; i < s1 && lead.length == 0; ++i) lead = sequence(p, i);
+            for (int64_t i = s0 + 1; i < s1 - 1 && lead.length == 0; ++i) lead = sequence(p, i);
             const int64_t begin = clamped(seq_begin(p.c, s0), p.c.tokens), end = clamped(seq_begin(p.c, s1), p.c.tokens);
             const int64_t count = end - begin;
             const int shared = p.shared[g] < lead.length ? p.shared[g] : lead.length;
