@@ -1157,7 +1157,7 @@ def pages_attention(q, keys, values, table, lengths, rows=None, offsets=None, gr
     nothing give 0. Rows of ``out`` in no sequence stay as they were, and are 0 in a new one. lse: None, True for a new
     float32 (tokens, heads_q) tensor of the logarithms of the exponentials' sums, or one to write; its rows in no sequence
     stay as they were, and are -infinity in a new one. one_part: 16-bit
-    probabilities rounded once for their product with the values where more than 32 queries share keys: 1.35 times the
+    probabilities rounded once for their product with the values where more than 32 queries share keys: 1.4 times the
     error, a fifth less time for long prompts.
     Returns out, or (out, lse)."""
     import torch

@@ -194,7 +194,8 @@ __device__ __forceinline__ void lay_out(const AttentionParams& p, AttnSeg* segs,
             const int64_t begin = clamped(seq_begin(p.c, s0), p.c.tokens), end = clamped(seq_begin(p.c, s1), p.c.tokens);
             const int64_t count = end - begin;
             const int shared = p.shared[g] < lead.length ? p.shared[g] : lead.length;
-            // larger tiles are full with the rows of one sequence
+            // (from half a tile of rows a sequence on, all read the shared tokens for themselves: their
+            // own tiles are half full at least)
             if (count > 0 && shared > 0 && count * p.share < (s1 - s0) * (work.tile_rows() / 2)) {
                 s.begin = (int)begin;
                 s.count = (int)count;

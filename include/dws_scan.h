@@ -828,7 +828,7 @@ dws_status dws_pages_append(const dws_pages_append_args* args, hipStream_t strea
 /* dws_pages_attention_args.options */
 enum {
     /* 16-bit probabilities rounded once, not in two parts, for their product with the values where more than 32 queries
-     * share keys: results with 1.35 times the error of their own rounding, and a fifth less time for long prompts. */
+     * share keys: results with 1.4 times the error of their own rounding, and a fifth less time for long prompts. */
     DWS_ATTENTION_ONE_PART = 1
 };
 
@@ -840,7 +840,8 @@ typedef struct dws_pages_attention_args {
     float scale;                /* finite, as scale log2(e) */
     /* Sequences that begin alike: group g is sequences d_groups[g] .. d_groups[g+1] - 1 (DEVICE, n_groups + 1 int64, not
      * decreasing), and the first d_shared[g] (DEVICE, n_groups int32) tokens of their rows are in the same pages, which
-     * are read once for all of them. Both NULL and n_groups 0 without groups. */
+     * are read once for all of them while these have fewer than 64 queries a key head each, on average (32: fp32 above
+     * 128 dimensions). Both NULL and n_groups 0 without groups. */
     long long n_groups;
     const long long* d_groups;
     const int* d_shared;
@@ -860,16 +861,16 @@ dws_status dws_pages_attention_workspace(const dws_pages_attention_args* args, s
 /*
  * Attention of each token's queries with the keys and values of its row up to its own place, the call's own tokens
  * (dws_pages_append first) included: out = sum p_t v_t with p the softmax of scale q . k_t over them. For one token a
- * sequence, a few, or whole prompts behind what is there. A query that sees nothing (a row outside the table, a sequence
- * with more tokens than its row, a row longer than max_pages pages or 2^31 - 4097
- * tokens, pages outside the pool) gives 0, and -infinity in d_lse; so does one all of whose scores are -infinity. Scores, their statistics and
+ * sequence, a few, or whole prompts behind what is there. A query that sees nothing (a row outside the table, a
+ * sequence with more tokens than its row, a row longer than max_pages pages or 2^31 - 4097 tokens, pages outside the
+ * pool) gives 0, and -infinity in d_lse; so does one all of whose scores are -infinity. Scores, their statistics and
  * all sums are fp32; with 16-bit inputs the probabilities are rounded to dtype in two parts for their product with the
- * values, which loses nothing of the result's precision (but for options; fp16 ones below 2^-36 of the row's largest may
- * count as 0 there). What is
- * behind a row's end is not read, whatever the pages hold there. Values that are not finite reach the queries that see
- * them, and no others. d_shared must say the truth: the shared tokens are read from the pages of the group's first
- * sequence that has a row. Results do not depend on scheduling. Errors as dws_pages_append, and too small a workspace:
- * DWS_ERR_INVALID_ARG. Asynchronous, allocates nothing, may be captured.
+ * values, which loses nothing of the result's precision (but for options; fp16 ones below 2^-36 of the row's largest
+ * may count as 0 there). What is behind a row's end is not read, whatever the pages hold there. Values that are not
+ * finite reach the queries that see them, and no others. d_shared must say the truth: the shared tokens are read from
+ * the pages of the group's first sequence that has a row. Results do not depend on scheduling. Errors as
+ * dws_pages_append, and too small a workspace or unknown options: DWS_ERR_INVALID_ARG. Asynchronous, allocates nothing,
+ * may be captured.
  */
 dws_status dws_pages_attention(const dws_pages_attention_args* args, hipStream_t stream);
 
