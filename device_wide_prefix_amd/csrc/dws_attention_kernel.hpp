@@ -441,19 +441,6 @@ struct Attention {
         if (__ballot(bad)) s.wild[turn] = 1;
     }
 
-    // Results of 16-bit weights that are not finite where their sum is: an infinity among the values that the
-    // queries see becomes NaN where a part of its weight is 0 or below it. Such a tile's rows are computed
-    // again, too.
-    __device__ __forceinline__ void note_wild_results()
-    {
-        float most = 0.f;
-#pragma unroll
-        for (int b = 0; b < BLOCKS; ++b)
-#pragma unroll
-            for (int e = 0; e < 16; ++e) most = __builtin_fmaf(0.f, o[b][e], most);       // 0, or NaN
-        if (__ballot(most != 0.f && __builtin_fabsf(l) < __builtin_inff())) s.wild[turn] = 1;
-    }
-
     // Scores of 32 tokens, of which the bits in `here` are there: -infinity for those that
     // the lane's query does not see; returns the largest.
     __device__ __forceinline__ float only_seen(f32x16_t& x, uint32_t here, int first) const
@@ -494,22 +481,52 @@ struct Attention {
     struct Weights {
         Chunk<T> p[STEPS];
     };
-    // `rest`: what rounding to 16 bits leaves of them, if they are wanted in two parts.
+    // Two weights in 16 bits, less than they are, and what that leaves of them in `rest`. Both
+    // parts are above 0 where the weight is, so that a value that is infinite stays so: rounded to the
+    // nearest, the second part is 0 or below it for every other weight, and the sum of the products NaN.
+    static __device__ __forceinline__ uint32_t parted(float x, float y, float (&rest)[2])
+    {
+        if constexpr (kNarrow) {
+            typedef uint16_t Pair __attribute__((ext_vector_type(2)));
+            typedef f16_t Halves __attribute__((ext_vector_type(2)));
+            const Pair down = __builtin_elementwise_sub_sat(__builtin_bit_cast(Pair, __builtin_amdgcn_cvt_pkrtz(x, y)), Pair{1, 1});
+            const Halves w = __builtin_bit_cast(Halves, down);
+            rest[0] = x - (float)w[0];
+            rest[1] = y - (float)w[1];
+            return __builtin_bit_cast(uint32_t, down);
+        } else {
+            // (the 2^-20 added are a 2^11th of the result's rounding)
+            const uint32_t a = __builtin_bit_cast(uint32_t, x), b = __builtin_bit_cast(uint32_t, y);
+            rest[0] = __builtin_fmaf(x, 1.f + 0x1p-20f, -__builtin_bit_cast(float, a & 0xffff0000u));
+            rest[1] = __builtin_fmaf(y, 1.f + 0x1p-20f, -__builtin_bit_cast(float, b & 0xffff0000u));
+            return __builtin_amdgcn_perm(b, a, 0x07060302);         // the upper halves
+        }
+    }
+    // `rest`: the second part, if they are wanted in two.
     template <int COUNT>
     __device__ __forceinline__ Weights weights(const f32x16_t& x, Weights& rest)
     {
         Weights w;
         const float base = m == -__builtin_inff() ? 0.f : m - kHeadroom;
-        float sum = 0.f;
+        float y[16], sum = 0.f;
 #pragma unroll
         for (int e = 0; e < 16; ++e) {
-            float y = __builtin_fmaf(x[e], c, -base);
+            y[e] = __builtin_fmaf(x[e], c, -base);
             if constexpr (sizeof(T) == 4)
-                if (x[e] != -__builtin_inff()) y = __builtin_fmaf(x[e], c_rest, y);
-            y = __builtin_amdgcn_exp2f(y);
-            sum += y;
-            w.p[e / CH][e % CH] = (T)y;
-            if constexpr (COUNT == 2) rest.p[e / CH][e % CH] = (T)(y - (float)w.p[e / CH][e % CH]);
+                if (x[e] != -__builtin_inff()) y[e] = __builtin_fmaf(x[e], c_rest, y[e]);
+            y[e] = __builtin_amdgcn_exp2f(y[e]);
+            sum += y[e];
+            if constexpr (COUNT == 1) {
+                w.p[e / CH][e % CH] = (T)y[e];
+            } else if (e % 2) {
+                typedef T Pair __attribute__((ext_vector_type(2)));
+                float left[2];
+                const Pair both = __builtin_bit_cast(Pair, parted(y[e - 1], y[e], left));
+                w.p[e / CH][e % CH - 1] = both[0];
+                w.p[e / CH][e % CH] = both[1];
+                rest.p[e / CH][e % CH - 1] = (T)left[0];
+                rest.p[e / CH][e % CH] = (T)left[1];
+            }
         }
         l += sum;
         return w;
@@ -834,7 +851,6 @@ struct Attention {
                 pieces<1>(t, stop, page);
         }
         l = sum_halves(l);
-        if constexpr (sizeof(T) == 2) note_wild_results();
         if (half == 0) {
             s.m[wave * kAttnRows + col] = m - kHeadroom;       // what the sums go by
             s.l[wave * kAttnRows + col] = l;

@@ -865,7 +865,7 @@ dws_status dws_pages_attention_workspace(const dws_pages_attention_args* args, s
  * sequence with more tokens than its row, a row longer than max_pages pages or 2^31 - 4097 tokens, pages outside the
  * pool) gives 0, and -infinity in d_lse; so does one all of whose scores are -infinity. Scores, their statistics and
  * all sums are fp32; with 16-bit inputs the probabilities are rounded to dtype in two parts for their product with the
- * values, which loses nothing of the result's precision (but for options; fp16 ones below 2^-36 of the row's largest
+ * values, which loses nothing of the result's precision (but for options; fp16 ones below 2^-34 of the row's largest
  * may count as 0 there). What is behind a row's end is not read, whatever the pages hold there. Values that are not
  * finite reach the queries that see them, and no others. d_shared must say the truth: the shared tokens are read from
  * the pages of the group's first sequence that has a row. Results do not depend on scheduling. Errors as

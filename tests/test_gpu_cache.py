@@ -347,12 +347,13 @@ def test_tiles_of_many_queries(gpu, dims, dtype):
 
 
 def check_own_rounding(c, rows, new, heads, **more):
-    """Nothing but the result's own rounding: half a step of it. Weights in two parts of h = eps / 2 keep h^2 of themselves; the
-    rest is fp32's, as attention_bound has it for that type."""
+    """Nothing but the result's own rounding: half a step of it, h = eps / 2. The first part of a weight is less than it is by up to
+    two steps, 4 h of it; rounding that costs 4 h^2 of the weight, and 2^-20 of it may be added. The rest is fp32's, as
+    attention_bound has it for that type."""
     q, offsets, scale, (out, _) = run_attention(c, rows, new, heads, **more)
     want, _, spread, largest = attention(q, *c.args(), rows, offsets, scale)
     half = torch.finfo(c.dtype).eps / 2
-    bound = attention_bound(want, spread, largest, max(c.lens), c.dk, FP32) + half * (1 + half) * want.abs() + half ** 2 * spread
+    bound = attention_bound(want, spread, largest, max(c.lens), c.dk, FP32) + half * (1 + half) * want.abs() + (4 * half ** 2 + 2.0 ** -20) * spread
     off = (out.double().cpu() - want).abs()
     assert (off <= bound).all(), f"off by up to {(off / bound).max():.3g} of the bound"
 
@@ -483,6 +484,26 @@ def test_infinities_among_the_values(gpu, new, heads, groups, dims, dtype):
         at(tokens + 20)[1, 6] = -math.inf
         at(tokens + 50)[0, 11] = math.nan
         check_attention(c, [0, 1, 2, 3], new, heads, **more)
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP16, FP32])
+@pytest.mark.parametrize("new,heads", [(1, 4), (9, 7), (40, 4), (70, 3)])
+def test_infinities_of_any_weight(gpu, new, heads, dtype):
+    """Infinite values of tokens whose weights are whole powers of two, from the largest to 2^-30 of it, which 16 bits hold
+    exactly and in one part."""
+    note(f"attention, infinities of any weight {new} {heads} {dtype}")
+    c = Cache(31, [333, 200, 400], dtype, 1, 64, 64, 16, device="cuda")
+    c.keys[c.keys.isfinite()] = 0
+    q = torch.zeros(3 * new, heads, 64, dtype=dtype, device="cuda")
+    q[..., 0] = 1
+    for row in range(3):
+        for i, (below, at) in enumerate(((0, 37), (1, 33), (5, 64), (10, 70), (14, 71), (20, 90), (24, 95), (27, 96), (30, 100))):
+            page, place = int(c.table[row, at // 16]), at % 16
+            c.keys[page, place, 0, 0] = -below
+            c.values[page, place, 0, 2 * i] = math.inf
+            c.values[page, place, 0, 2 * i + 1] = -math.inf
+    for more in ({}, {"one_part": True}) if dtype == BF16 else ({},):
+        check_attention(c, [0, 1, 2], [new] * 3, heads, q=q, scale=math.log(2.0), **more)
 
 
 @pytest.mark.parametrize("scale", [0.0, -0.3, 1e-30, 3.0])
