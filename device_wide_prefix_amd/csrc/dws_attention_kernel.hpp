@@ -18,13 +18,13 @@
 // rows are not whole units of 16 bytes.
 //
 // Measured, with the joining, a call: 96 sequences of 1 to 16,000 tokens, 8 heads of 128, 4
-// queries each, bf16: 160 us, 4.6 TB/s of keys and values. 3 prompts of 900 to 2,000 tokens
-// behind 4,097: 740 to 780 us by the machine, 570 to 600 TFLOP/s without the weights' second
-// part, where a large matrix product reaches 1,308. Each SIMD's vector instructions take 53%
-// of the time (scores to weights: 6 of 32 bits for each, 4 times one for the exponential)
-// and its matrix products 44%: two waves hide what one waits for, and hardly overlap the two.
-// Tiles of 256 queries would halve the reads of the LDS (21% of the time), but leave one wave
-// a SIMD. With weights in one part, where a caller asks for that, 587 to 624 us.
+// queries each, bf16: 156 us, 4.7 TB/s of keys and values. 3 prompts of 900 to 2,000 tokens
+// behind 4,097: 731 us, 610 TFLOP/s without the weights' second part, where a large matrix
+// product reaches 1,274 in the same session. Each SIMD's vector instructions take 52% of the
+// time (scores to weights: 5 of 32 bits for each, 4 times one for the exponential) and its
+// matrix products 48%: two waves hide what one waits for, and hardly overlap the two. Tiles
+// of 256 queries would halve the reads of the LDS (23% of the time), but leave one wave a
+// SIMD. With weights in one part, where a caller asks for that, 583 us.
 //
 // Fragments (32 x 32 tiles, h = lane / 32):
 //   operand  lane holds row (or column) lane % 32, contraction indices 8 h .. 8 h + 7 of
