@@ -1153,7 +1153,8 @@ def pages_attention(q, keys, values, table, lengths, rows=None, offsets=None, gr
     q: (tokens, heads_q, dim_k); keys, values, table, lengths, rows and offsets as pages_append, whose tokens these are, one
     a sequence or as many as a prompt has; heads_q is a multiple of the cache's heads. groups (int64 GPU tensor, groups + 1)
     and shared (int32 GPU tensor): the first shared[g] tokens of sequences groups[g] .. groups[g + 1] - 1 are in the same
-    pages, as pages_fork leaves them, and are read once for all of these. scale: dim_k^-0.5 by default. Queries that see
+    pages, as pages_fork leaves them, and are read once for all of these (while they have fewer than 64 queries a key head each, on
+    average; through the first one that has a row). scale: dim_k^-0.5 by default. Queries that see
     nothing give 0. Rows of ``out`` in no sequence stay as they were, and are 0 in a new one. lse: None, True for a new
     float32 (tokens, heads_q) tensor of the logarithms of the exponentials' sums, or one to write; its rows in no sequence
     stay as they were, and are -infinity in a new one. one_part: 16-bit
